@@ -25,6 +25,9 @@ from ._binding import (  # noqa: F401
     w8a8_block_fp8_matmul_splitk_noalloc, W8A8_NOALLOC_SCRATCH_BYTES,
     w8a8_quantize_fp8_per_token_group, W8A8_IN_BF16, W8A8_IN_FP16, W8A8_IN_FP32,
     w8a8_block_fp8_grouped_matmul_masked, w8a8_block_fp8_grouped_matmul_contiguous,
+    w8a8_block_fp8_grouped_matmul_ragged, W8A8_RAGGED_MAX_EXPERTS,
+    w8a8_int8_matmul, w8a8_int8_workspace_size, W8A8_INT8_MAX_K, w8a8_quantize_int8_per_token,
+    w8a8_sandwich_norm, W8A8_NORM_SAME, W8A8_NORM_FP8, W8A8_NORM_INT8, W8A8_NORM_MAX_D,
     w8a8_launch_floor_kernel, w8a8_block_fp8_quant_matmul,
     w8a8_block_fp8_quant_matmul_workspace_size,
     w8a8_get_device_status, w8a8_last_error, w8a8_options, w8a8_shutdown, w8a8_status_string,
@@ -173,3 +176,147 @@ def quant_matmul(X, B, b_s, out_dtype="bf16", out=None, stream=None, **opts):
     check(w8a8_block_fp8_quant_matmul(X, xk, B, b_s, out, M, N, K, 128, 128, code, stream,
                                       options(**opts) if opts else None))
     return out
+
+
+def grouped_matmul_ragged(A, a_s, B, b_s, offsets, out_dtype="bf16", out=None, stream=None,
+                          **opts):
+    """Grouped matmul, ragged layout, on CUDA tensors: A [M, K], a_s [M, ceil(K/128)],
+    B [E, N, K], b_s [E, ceil(N/128), ceil(K/128)], offsets int32 [E + 1] (expert e's
+    rows are offsets[e] .. offsets[e+1]-1; read on the device).  Returns C [M, N];
+    rows of no expert are left as they are in ``out`` (unspecified without it)."""
+    M, K = A.shape
+    E, N = B.shape[0], B.shape[1]
+    code = out_code(out_dtype)
+    if out is None:
+        out = _out_tensor((M, N), code, A.device)
+    for t in (A, a_s, B, b_s, out, offsets):
+        if not t.is_contiguous():
+            raise W8A8Error(W8A8_ERR_UNSUPPORTED, "tensors must be contiguous row-major")
+    _want(a_s, (M, (K + 127) // 128), "a_s")
+    _want(b_s, (E, (N + 127) // 128, (K + 127) // 128), "b_s")
+    _want(offsets, (E + 1,), "offsets")
+    _want(out, (M, N), "out")
+    if B.shape[2] != K:
+        raise W8A8Error(W8A8_ERR_INVALID_ARG, f"B has {B.shape[2]} columns, A {K}")
+    check(w8a8_block_fp8_grouped_matmul_ragged(A, a_s, B, b_s, out, offsets, M, E, N, K, 128, 128,
+                                               code, stream, options(**opts) if opts else None))
+    return out
+
+
+def _want(t, shape, name):
+    if t.shape != shape:
+        raise W8A8Error(W8A8_ERR_INVALID_ARG, f"{name} has shape {tuple(t.shape)}, want {shape}")
+
+
+def _rows(t):
+    """Row stride of a 2-D tensor whose rows are contiguous."""
+    if t.dim() != 2 or (t.size(1) > 1 and t.stride(1) != 1):
+        raise W8A8Error(W8A8_ERR_UNSUPPORTED, "each row must be contiguous (unit stride)")
+    return t.stride(0) if t.size(0) > 1 else t.size(1)
+
+
+def _in_code(dtype):
+    import torch
+    code = {torch.bfloat16: W8A8_IN_BF16, torch.float16: W8A8_IN_FP16,
+            torch.float32: W8A8_IN_FP32}.get(dtype)
+    if code is None:
+        raise W8A8Error(W8A8_ERR_INVALID_ARG, f"unsupported input dtype {dtype}")
+    return code
+
+
+def int8_matmul(A, a_s, B, b_s, out_dtype="bf16", out=None, stream=None, **opts):
+    """C[m,n] = a_s[m] b_s[n] sum_k A[m,k] B[n,k] on CUDA tensors: A int8 [M, K], a_s
+    float32 [M], B int8 [N, K], b_s float32 [N]; the sum is exact.  A, B and ``out``
+    need unit stride along their last dimension only.  Keyword options map to
+    w8a8_options fields.  Raises W8A8Error on a non-zero status."""
+    import torch
+    M, K = A.shape
+    N = B.shape[0]
+    code = out_code(out_dtype)
+    if A.dtype != torch.int8 or B.dtype != torch.int8:
+        raise W8A8Error(W8A8_ERR_INVALID_ARG, f"A and B must be int8, not {A.dtype}, {B.dtype}")
+    if out is None:
+        out = _out_tensor((M, N), code, A.device)
+    _want(B, (N, K), "B")
+    _want(a_s, (M,), "a_s")
+    _want(b_s, (N,), "b_s")
+    _want(out, (M, N), "out")
+    if not a_s.is_contiguous() or not b_s.is_contiguous():
+        raise W8A8Error(W8A8_ERR_UNSUPPORTED, "scales must be contiguous")
+    check(w8a8_int8_matmul(A, _rows(A), a_s, B, _rows(B), b_s, out, _rows(out), M, N, K, code,
+                           stream, options(**opts) if opts else None))
+    return out
+
+
+def quantize_int8_per_token(X, A=None, a_s=None, stream=None):
+    """Per-token INT8 quantisation of a CUDA tensor X [M, K] (bf16, fp16 or fp32, unit
+    stride along K): returns (A int8 [M, K], a_s float32 [M]), the INT8 matmul's
+    activation operand.  ``A`` / ``a_s`` may be preallocated."""
+    import torch
+    M, K = X.shape
+    code = _in_code(X.dtype)
+    if A is None:
+        A = torch.empty((M, K), dtype=torch.int8, device=X.device)
+    if a_s is None:
+        a_s = torch.empty(M, dtype=torch.float32, device=X.device)
+    _want(A, (M, K), "A")
+    _want(a_s, (M,), "a_s")
+    if not a_s.is_contiguous():
+        raise W8A8Error(W8A8_ERR_UNSUPPORTED, "scales must be contiguous")
+    check(w8a8_quantize_int8_per_token(X, code, _rows(X), A, _rows(A), a_s, M, K, stream))
+    return A, a_s
+
+
+_NORM_KINDS = {"same": W8A8_NORM_SAME, "fp8": W8A8_NORM_FP8, "int8": W8A8_NORM_INT8}
+
+
+def sandwich_norm(h, x, w_post=None, w_pre=None, gate=None, gate_rows=None, res_scale=1.0,
+                  eps=1e-6, out="same", x_out=None, y_out=None, scales_out=None, stream=None):
+    """The norms around a block, fused with its gate and residual, on CUDA tensors:
+
+        u = h / rms(h) * w_post;  r = res_scale * x + gate * u;  y = r / rms(r) * w_pre
+
+    h, x [M, D]; w_post, w_pre [D] (None: no norm); gate [R, D], row m // gate_rows for
+    token m (default: R equal runs of tokens), or [D] for all, or None.  Returns (r, y),
+    r in x's type; with out="fp8" (E4M3 codes and one scale per 128 columns) or "int8"
+    (one scale per row) (r, codes, scales).  x_out may be x itself.  Raises W8A8Error
+    on a non-zero status."""
+    import torch
+    M, D = h.shape
+    hk, kind = _in_code(h.dtype), _NORM_KINDS[out]
+    if x_out is None:
+        x_out = torch.empty((M, D), dtype=x.dtype, device=x.device)
+    if y_out is None:
+        y_out = torch.empty((M, D), device=h.device,
+                            dtype=(h.dtype, torch.uint8, torch.int8)[kind])
+    if kind != W8A8_NORM_SAME:
+        shape = (M, (D + 127) // 128) if kind == W8A8_NORM_FP8 else (M,)
+        if scales_out is None:
+            scales_out = torch.empty(shape, dtype=torch.float32, device=h.device)
+        _want(scales_out, shape, "scales_out")
+        if not scales_out.is_contiguous():
+            raise W8A8Error(W8A8_ERR_UNSUPPORTED, "scales must be contiguous")
+    _want(x, (M, D), "x")
+    _want(x_out, (M, D), "x_out")
+    _want(y_out, (M, D), "y_out")
+    if x_out.dtype != x.dtype:
+        raise W8A8Error(W8A8_ERR_INVALID_ARG, "x_out must have x's dtype")
+    R = 1
+    if gate is not None:
+        R = gate.shape[0] if gate.dim() == 2 else 1
+        if gate_rows is None:
+            gate_rows = max(1, -(-M // max(R, 1)))
+        if gate.shape[-1] != D or gate_rows < 1 or R < -(-M // gate_rows):
+            raise W8A8Error(W8A8_ERR_INVALID_ARG,
+                            f"gate of {tuple(gate.shape)} for {M} rows of {D}, {gate_rows} to a gate")
+    for t, shape in ((w_post, (D,)), (w_pre, (D,)), (gate, None)):
+        if t is None:
+            continue
+        if shape is not None:
+            _want(t, shape, "weight")
+        if t.dtype != h.dtype or not t.is_contiguous():
+            raise W8A8Error(W8A8_ERR_UNSUPPORTED, "weights and gate must be contiguous, of h's dtype")
+    check(w8a8_sandwich_norm(h, hk, _rows(h), x, _in_code(x.dtype), _rows(x), w_post, gate,
+                             gate_rows or 1, w_pre, res_scale, eps, x_out, _rows(x_out), y_out,
+                             scales_out, kind, _rows(y_out), M, D, stream))
+    return (x_out, y_out) if kind == W8A8_NORM_SAME else (x_out, y_out, scales_out)

@@ -38,6 +38,11 @@ EXPORTED = (
     "w8a8_block_fp8_matmul_splitk_noalloc",
     "w8a8_block_fp8_grouped_matmul_masked",
     "w8a8_block_fp8_grouped_matmul_contiguous",
+    "w8a8_block_fp8_grouped_matmul_ragged",
+    "w8a8_int8_matmul",
+    "w8a8_int8_workspace_size",
+    "w8a8_quantize_int8_per_token",
+    "w8a8_sandwich_norm",
     "w8a8_quantize_fp8_per_token_group",
     "w8a8_launch_floor_kernel",
     "w8a8_block_fp8_quant_matmul",
@@ -126,6 +131,16 @@ def load_library():
     lib.w8a8_block_fp8_grouped_matmul_contiguous.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64,
                                                              i64, i64, i32, i32, i32, vp, opt_p]
     lib.w8a8_block_fp8_grouped_matmul_contiguous.restype = ctypes.c_int
+    lib.w8a8_block_fp8_grouped_matmul_ragged.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64,
+                                                         i64, i32, i32, i32, vp, opt_p]
+    lib.w8a8_int8_matmul.argtypes = [vp, i64, vp, vp, i64, vp, vp, i64, i64, i64, i64, i32, vp,
+                                     opt_p]
+    lib.w8a8_int8_workspace_size.argtypes = [i64, i64, i64, opt_p]
+    lib.w8a8_int8_workspace_size.restype = sz
+    lib.w8a8_quantize_int8_per_token.argtypes = [vp, i32, i64, vp, i64, vp, i64, i64, vp]
+    f32 = ctypes.c_float
+    lib.w8a8_sandwich_norm.argtypes = [vp, i32, i64, vp, i32, i64, vp, vp, i64, vp, f32, f32, vp,
+                                       i64, vp, vp, i32, i64, i64, i64, vp]
     lib.w8a8_block_fp8_quant_matmul.argtypes = [vp, i32, vp, vp, vp, i64, i64, i64, i32, i32, i32,
                                                 vp, opt_p]
     lib.w8a8_block_fp8_quant_matmul.restype = ctypes.c_int
@@ -154,7 +169,9 @@ def load_library():
     lib.w8a8_shutdown.argtypes = []
     lib.w8a8_shutdown.restype = None
     for name in ("w8a8_block_fp8_matmul", "w8a8_block_fp8_matmul_ex", "w8a8_block_fp8_matmul_host",
-                 "w8a8_block_fp8_plan", "w8a8_get_device_status", "w8a8_abi_version"):
+                 "w8a8_block_fp8_plan", "w8a8_get_device_status", "w8a8_abi_version",
+                 "w8a8_block_fp8_grouped_matmul_ragged", "w8a8_int8_matmul",
+                 "w8a8_quantize_int8_per_token", "w8a8_sandwich_norm"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -252,6 +269,45 @@ def w8a8_block_fp8_quant_matmul(X, x_dtype, B, b_s, C, M, N, K, block_n=128, blo
     return load_library().w8a8_block_fp8_quant_matmul(
         _ptr(X), x_dtype, _ptr(B), _ptr(b_s), _ptr(C), M, N, K, block_n, block_k, out_dtype,
         _stream(stream), _opts(opts))
+
+
+def w8a8_block_fp8_grouped_matmul_ragged(A, a_s, B, b_s, C, offsets, M, E, N, K,
+                                         block_n=128, block_k=128, out_dtype=W8A8_OUT_BF16,
+                                         stream=None, opts=None) -> int:
+    return load_library().w8a8_block_fp8_grouped_matmul_ragged(
+        _ptr(A), _ptr(a_s), _ptr(B), _ptr(b_s), _ptr(C), _ptr(offsets), M, E, N, K,
+        block_n, block_k, out_dtype, _stream(stream), _opts(opts))
+
+
+W8A8_RAGGED_MAX_EXPERTS = 1024
+W8A8_INT8_MAX_K = 131071
+W8A8_NORM_MAX_D = 57344
+W8A8_NORM_SAME, W8A8_NORM_FP8, W8A8_NORM_INT8 = 0, 1, 2
+
+
+def w8a8_int8_matmul(A, lda, a_s, B, ldb, b_s, C, ldc, M, N, K, out_dtype=W8A8_OUT_BF16,
+                     stream=None, opts=None) -> int:
+    return load_library().w8a8_int8_matmul(_ptr(A), lda, _ptr(a_s), _ptr(B), ldb, _ptr(b_s),
+                                           _ptr(C), ldc, M, N, K, out_dtype, _stream(stream),
+                                           _opts(opts))
+
+
+def w8a8_int8_workspace_size(M, N, K, opts=None) -> int:
+    return load_library().w8a8_int8_workspace_size(M, N, K, _opts(opts))
+
+
+def w8a8_quantize_int8_per_token(X, x_dtype, ld_x, A, ld_a, a_s, M, K, stream=None) -> int:
+    return load_library().w8a8_quantize_int8_per_token(_ptr(X), x_dtype, ld_x, _ptr(A), ld_a,
+                                                       _ptr(a_s), M, K, _stream(stream))
+
+
+def w8a8_sandwich_norm(h, h_dtype, ld_h, x, x_dtype, ld_x, w_post, gate, gate_rows, w_pre,
+                       res_scale, eps, x_out, ld_xo, y, scales, y_kind, ld_y, M, D,
+                       stream=None) -> int:
+    return load_library().w8a8_sandwich_norm(
+        _ptr(h), h_dtype, ld_h, _ptr(x), x_dtype, ld_x, _ptr(w_post), _ptr(gate), gate_rows,
+        _ptr(w_pre), res_scale, eps, _ptr(x_out), ld_xo, _ptr(y), _ptr(scales), y_kind, ld_y, M, D,
+        _stream(stream))
 
 
 def w8a8_launch_floor_kernel(pdl=1, stream=None) -> int:

@@ -653,10 +653,11 @@ w8a8_status acquire_workspace(const w8a8_options *o, int dev, cudaStream_t strea
 }
 
 // Grouped (MoE) calls: which layout, the device array of per-expert counts
-// (masked) or per-row expert ids (contiguous), and the number of experts.  In
+// (masked), per-row expert ids (contiguous) or offsets (ragged), and the number
+// of experts.  In
 // the masked layout M is the rows of one expert's slab.
 struct Grouping {
-    enum Mode { NONE, MASKED, CONTIGUOUS } mode = NONE;
+    enum Mode { NONE, MASKED, CONTIGUOUS, RAGGED } mode = NONE;
     const int32_t *ids = nullptr;
     int64_t experts = 0;
 };
@@ -741,6 +742,205 @@ w8a8_status run_generic(const void *A, const float *a_s, const void *B, const fl
     return W8A8_OK;
 }
 
+// INT8 matmul: bytes of fp16 operands that one launch's rows of A may take in
+// the workspace (longer problems run in several), and the workspace itself: the
+// counter block that every workspace starts with, the widened A rows, B.
+constexpr int64_t kInt8ChunkBytes = 512ll << 20;
+
+struct Int8Plan {
+    int64_t Kp, chunk;           // padded K; rows of A per launch (a multiple of 256, or M)
+    size_t a_bytes, b_bytes;
+    size_t workspace() const { return kCounterBytes + a_bytes + b_bytes; }
+};
+
+Int8Plan int8_plan(int64_t M, int64_t N, int64_t K)
+{
+    Int8Plan pl;
+    pl.Kp = std::max<int64_t>(cdiv(K, 64), 1) * 64;
+    pl.chunk = std::max<int64_t>(kInt8ChunkBytes / (pl.Kp * 2) / 256, 1) * 256;
+    pl.chunk = std::min(pl.chunk, M);
+    auto up = [](int64_t x) { return static_cast<size_t>((x + 255) / 256 * 256); };
+    pl.a_bytes = up(pl.chunk * pl.Kp * 2);
+    pl.b_bytes = up(N * pl.Kp * 2);
+    return pl;
+}
+
+w8a8_status check_int8(int64_t M, int64_t N, int64_t K, const w8a8_options *o)
+{
+    if (M < 0 || N < 0 || K < 0)
+        return fail(W8A8_ERR_INVALID_ARG, "negative size (M=%lld N=%lld K=%lld)", (long long)M,
+                    (long long)N, (long long)K);
+    w8a8_status st;
+    if ((st = check_options(o)) != W8A8_OK)
+        return st;
+    const int v = o ? o->variant : W8A8_VARIANT_AUTO;
+    if (v != W8A8_VARIANT_AUTO && v != W8A8_VARIANT_TILED && v != W8A8_VARIANT_TILED_PAIR)
+        return fail(W8A8_ERR_UNSUPPORTED, "the INT8 matmul takes variant AUTO, TILED or TILED_PAIR");
+    if (K > W8A8_INT8_MAX_K)
+        return fail(W8A8_ERR_UNSUPPORTED, "K=%lld: sums of more than %d products may leave 32 bits",
+                    (long long)K, W8A8_INT8_MAX_K);
+    if (M > (1ll << 31) - 512 || N > (1ll << 31) - 512 ||
+        cdiv(M, 128) * cdiv(N, 128) > (1ll << 31) - 1)
+        return fail(W8A8_ERR_UNSUPPORTED, "sizes must be below 2^31");
+    return W8A8_OK;
+}
+
+w8a8_status run_int8(const void *A, int64_t lda, const float *a_s, const void *B, int64_t ldb,
+                     const float *b_s, void *C, int64_t ldc, int64_t M, int64_t N, int64_t K,
+                     int out, cudaStream_t stream, const w8a8_options *o)
+{
+    g_last_error[0] = '\0';
+    w8a8_status st;
+    w8a8_options env_opts;
+    if ((st = with_env(o, false, &env_opts, &o)) != W8A8_OK || (st = check_int8(M, N, K, o)) != W8A8_OK)
+        return st;
+    if (out < W8A8_OUT_BF16 || out > W8A8_OUT_FP32)
+        return fail(W8A8_ERR_INVALID_ARG, "unknown out_dtype %d", out);
+    lda = lda ? lda : K;
+    ldb = ldb ? ldb : K;
+    ldc = ldc ? ldc : N;
+    if (lda < K || ldb < K || ldc < N)
+        return fail(W8A8_ERR_INVALID_ARG, "a row stride is shorter than its row");
+    if (M == 0 || N == 0)
+        return W8A8_OK;
+    const int eb = out == W8A8_OUT_FP32 ? 4 : 2;
+    if (!a_s || !b_s || !C || (K > 0 && (!A || !B)))
+        return fail(W8A8_ERR_INVALID_ARG, "null pointer argument");
+    if (!aligned(C, eb) || !aligned(a_s, 4) || !aligned(b_s, 4))
+        return fail(W8A8_ERR_UNSUPPORTED,
+                    "C must be aligned to its element size and a_s, b_s to 4 bytes");
+    int dev;
+    DeviceInfo info;
+    if ((st = current_device(&dev, &info)) != W8A8_OK)
+        return st;
+    const Int8Plan pl = int8_plan(M, N, K);
+    void *ws = nullptr;
+    if ((st = acquire_workspace(o, dev, stream, pl.workspace(), &ws)) != W8A8_OK)
+        return st;
+    uint8_t *A16 = static_cast<uint8_t *>(ws) + kCounterBytes, *B16 = A16 + pl.a_bytes;
+    auto fits = [&](int a) {
+        return aligned(A, a) && aligned(B, a) && lda % a == 0 && ldb % a == 0;
+    };
+    const int access = fits(16) ? 16 : fits(4) ? 4 : 1;
+    const int v = o ? o->variant : W8A8_VARIANT_AUTO;
+    for (int64_t r0 = 0; r0 < M; r0 += pl.chunk) {
+        const int64_t rows = std::min(pl.chunk, M - r0);
+        Int8WidenParams w = {};
+        w.A = static_cast<const uint8_t *>(A) + r0 * lda;
+        w.B = static_cast<const uint8_t *>(B);
+        w.A16 = A16;
+        w.B16 = B16;
+        w.rows_a = rows;
+        w.rows_b = r0 == 0 ? N : 0;
+        w.lda = lda;
+        w.ldb = ldb;
+        w.K = static_cast<int>(K);
+        w.Kp = static_cast<int>(pl.Kp);
+        w.status = info.status;
+        const int64_t units = (w.rows_a + w.rows_b) * (pl.Kp / 16);
+        cudaError_t e = launch_int8_widen(
+            w, access, static_cast<int>(std::min<int64_t>(cdiv(units, 256), 8 * info.sm_count)), stream);
+        if (e != cudaSuccess)
+            return cuda_fail(e, "kernel launch (widening)");
+
+        Int8Params p = {};
+        p.a_s = a_s + r0;
+        p.b_s = b_s;
+        p.C = static_cast<uint8_t *>(C) + r0 * ldc * eb;
+        p.M = static_cast<int>(rows);
+        p.N = static_cast<int>(N);
+        p.steps = static_cast<int>(pl.Kp / 64);
+        p.ldc = ldc;
+        p.out_kind = out;
+        p.status = info.status;
+        p.wait_limit = (o && o->wait_limit_cycles) ? o->wait_limit_cycles : kDefaultWaitLimit;
+        p.debug_skip_tma = (o && o->debug_skip_load > 0) ? o->debug_skip_load - 1 : -1;
+        if (W8A8_DEBUG_BOUNDS && o && o->debug_bad_index && p.debug_skip_tma < 0)
+            p.debug_skip_tma = kDebugBadFirstLoad;
+        const int64_t pair_tiles = cdiv(rows, 256) * cdiv(N, 256);
+        const bool pair = v == W8A8_VARIANT_TILED_PAIR ||
+                          (v == W8A8_VARIANT_AUTO && pair_tiles * 2 >= info.sm_count / 2);
+        const int tm = pair ? 256 : 128;
+        p.num_m_tiles = static_cast<int>(cdiv(rows, tm));
+        p.num_n_tiles = static_cast<int>(cdiv(N, tm));
+        p.num_tiles = p.num_m_tiles * p.num_n_tiles;
+        int64_t ctas = info.sm_count;
+        if (pair) {
+            const int pairs = int8_max_pairs();
+            if (pairs <= 0)
+                return fail(W8A8_ERR_CUDA, "no CTA pair of the INT8 kernel fits on this device");
+            ctas = 2 * pairs;
+        }
+        if (o && o->grid_limit)
+            ctas = std::min<int64_t>(ctas, std::max(o->grid_limit, pair ? 2 : 1));
+        ctas = std::min<int64_t>(ctas, static_cast<int64_t>(p.num_tiles) * (pair ? 2 : 1));
+        LaunchCfg cfg = {};
+        cfg.grid = static_cast<int>(pair ? ctas / 2 * 2 : ctas);
+        cfg.stream = stream;
+        CUtensorMap mA, mB, mC = {};
+        p.tma_store = aligned(p.C, 16) && N * eb % 16 == 0 && ldc * eb % 16 == 0;
+        if ((st = encode_u8_map(&mA, A16, rows, 2 * pl.Kp, 128)) != W8A8_OK ||
+            (st = encode_u8_map(&mB, B16, N, 2 * pl.Kp, 128)) != W8A8_OK ||
+            (p.tma_store &&
+             (st = encode_out_map(&mC, p.C, rows, N, out, out == W8A8_OUT_FP32 ? 16 : 32, 32,
+                                  CU_TENSOR_MAP_SWIZZLE_64B, 0, ldc)) != W8A8_OK))
+            return st;
+        e = launch_int8_mma(mA, mB, mC, p, pair, cfg);
+        if (e != cudaSuccess)
+            return cuda_fail(e, "kernel launch");
+    }
+    return W8A8_OK;
+}
+
+// The ragged layout on its own kernel, arguments checked by run().
+w8a8_status run_ragged(const void *A, const float *a_s, const void *B, const float *b_s, void *C,
+                       int64_t M, int64_t N, int64_t K, int out, cudaStream_t stream,
+                       const w8a8_options *o, const Grouping &gr, const DeviceInfo &info)
+{
+    // Row tiles that the routing can make at most; the host does not know it.
+    const int64_t tiles = std::min<int64_t>(gr.experts, M) + M / 128;
+    int bn = o ? o->block_n_tile : 0;
+    if (bn == 192)
+        return fail(W8A8_ERR_UNSUPPORTED, "the ragged layout takes block_n_tile 128 or 256");
+    if (!bn)
+        bn = tiles * cdiv(N, 256) >= 2 * info.sm_count ? 256 : 128;
+    const int64_t items = tiles * cdiv(N, bn);
+    int64_t grid = std::min<int64_t>(items, info.sm_count);
+    if (o && o->grid_limit)
+        grid = std::min<int64_t>(grid, o->grid_limit);
+    w8a8_status st;
+    CUtensorMap mA, mB, mC;
+    if ((st = encode_u8_map(&mA, A, M, K, 32)) != W8A8_OK ||
+        (st = encode_u8_map(&mB, B, N, K, bn, gr.experts)) != W8A8_OK ||
+        (st = encode_out_map(&mC, C, M, N, out, out == W8A8_OUT_FP32 ? 16 : 32, 32,
+                             CU_TENSOR_MAP_SWIZZLE_64B)) != W8A8_OK)
+        return st;
+    RaggedParams p = {};
+    p.a_s = a_s;
+    p.b_s = b_s;
+    p.C = C;
+    p.offsets = gr.ids;
+    p.M = static_cast<int>(M);
+    p.N = static_cast<int>(N);
+    p.K = static_cast<int>(K);
+    p.G = static_cast<int>(cdiv(K, 128));
+    p.NB = static_cast<int>(cdiv(N, 128));
+    p.experts = static_cast<int>(gr.experts);
+    p.num_n_tiles = static_cast<int>(cdiv(N, bn));
+    p.out_kind = out;
+    p.debug_skip_tma = (o && o->debug_skip_load > 0) ? o->debug_skip_load - 1 : -1;
+    if (W8A8_DEBUG_BOUNDS && o && o->debug_bad_index && p.debug_skip_tma < 0)
+        p.debug_skip_tma = kDebugBadFirstLoad;
+    p.status = info.status;
+    p.wait_limit = (o && o->wait_limit_cycles) ? o->wait_limit_cycles : kDefaultWaitLimit;
+    LaunchCfg cfg = {};
+    cfg.grid = static_cast<int>(grid);
+    cfg.pdl = o ? o->pdl : 0;
+    cfg.stream = stream;
+    const cudaError_t e = launch_ragged(mA, mB, mC, p, bn, cfg);
+    return e == cudaSuccess ? W8A8_OK : cuda_fail(e, "kernel launch");
+}
+
 w8a8_status run(const void *A, const float *a_s, const void *B, const float *b_s, void *C,
                 int64_t M, int64_t N, int64_t K, int block_n, int block_k, int out,
                 cudaStream_t stream, const w8a8_options *o, const Grouping &gr = Grouping(),
@@ -809,10 +1009,13 @@ w8a8_status run(const void *A, const float *a_s, const void *B, const float *b_s
         a_s = b_s;
     }
     const bool masked = gr.mode == Grouping::MASKED, contiguous = gr.mode == Grouping::CONTIGUOUS;
+    const bool ragged = gr.mode == Grouping::RAGGED;
     if (gr.mode != Grouping::NONE) {
         if (gr.experts < 0)
             return fail(W8A8_ERR_INVALID_ARG, "negative number of experts");
-        if (gr.experts * std::max<int64_t>(M, 1) > (1ll << 31) - 1 || gr.experts > 65535)
+        if (ragged ? gr.experts > kRaggedMaxExperts ||
+                         (cdiv(M, 128) + gr.experts) * cdiv(N, 128) > (1ll << 31) - 1
+                   : gr.experts * std::max<int64_t>(M, 1) > (1ll << 31) - 1 || gr.experts > 65535)
             return fail(W8A8_ERR_UNSUPPORTED, "%lld experts of %lld rows: too many",
                         static_cast<long long>(gr.experts), static_cast<long long>(M));
         const int v = o ? o->variant : W8A8_VARIANT_AUTO;
@@ -820,9 +1023,10 @@ w8a8_status run(const void *A, const float *a_s, const void *B, const float *b_s
             v != W8A8_VARIANT_SPLITK_CLUSTER)
             return fail(W8A8_ERR_UNSUPPORTED, "the masked layout runs the swap-AB kernel "
                                               "(variant AUTO, SWAPAB or SPLITK_CLUSTER)");
-        if (contiguous && v != W8A8_VARIANT_AUTO && v != W8A8_VARIANT_TILED)
-            return fail(W8A8_ERR_UNSUPPORTED, "the contiguous layout runs the tiled kernel "
-                                              "(variant AUTO or TILED)");
+        if ((contiguous || ragged) && v != W8A8_VARIANT_AUTO && v != W8A8_VARIANT_TILED)
+            return fail(W8A8_ERR_UNSUPPORTED, "the %s layout runs the tiled kernel "
+                                              "(variant AUTO or TILED)",
+                        ragged ? "ragged" : "contiguous");
         if (gr.experts == 0 && masked)
             return W8A8_OK;
     }
@@ -836,11 +1040,15 @@ w8a8_status run(const void *A, const float *a_s, const void *B, const float *b_s
         return fail(W8A8_ERR_UNSUPPORTED, "A, B and C must be 16-byte aligned");
     if (!aligned(a_s, 4) || !aligned(b_s, 4))
         return fail(W8A8_ERR_UNSUPPORTED, "a_s and b_s must be 4-byte aligned");
+    if (ragged && !aligned(gr.ids, 4))
+        return fail(W8A8_ERR_UNSUPPORTED, "offsets must be 4-byte aligned");
 
     int dev;
     DeviceInfo info;
     if ((st = current_device(&dev, &info)) != W8A8_OK)
         return st;
+    if (ragged)
+        return run_ragged(A, a_s, B, b_s, C, M, N, K, out, stream, o, gr, info);
     Plan pl;
     w8a8_options forced = {};
     if (o)
@@ -1286,6 +1494,39 @@ w8a8_status w8a8_block_fp8_grouped_matmul_contiguous(const void *A_dev, const fl
     gr.experts = E;
     return run(A_dev, a_s_dev, B_dev, b_s_dev, C_dev, M, N, K, block_n, block_k, out_dtype,
                reinterpret_cast<cudaStream_t>(stream), opts, gr);
+}
+
+w8a8_status w8a8_block_fp8_grouped_matmul_ragged(const void *A_dev, const float *a_s_dev,
+                                                 const void *B_dev, const float *b_s_dev,
+                                                 void *C_dev, const int32_t *offsets_dev,
+                                                 int64_t M, int64_t E, int64_t N, int64_t K,
+                                                 int block_n, int block_k,
+                                                 w8a8_out_dtype out_dtype, w8a8_stream_t stream,
+                                                 const w8a8_options *opts)
+{
+    Grouping gr;
+    gr.mode = Grouping::RAGGED;
+    gr.ids = offsets_dev;
+    gr.experts = E;
+    return run(A_dev, a_s_dev, B_dev, b_s_dev, C_dev, M, N, K, block_n, block_k, out_dtype,
+               reinterpret_cast<cudaStream_t>(stream), opts, gr);
+}
+
+w8a8_status w8a8_int8_matmul(const void *A_dev, int64_t lda, const float *a_s_dev,
+                             const void *B_dev, int64_t ldb, const float *b_s_dev, void *C_dev,
+                             int64_t ldc, int64_t M, int64_t N, int64_t K,
+                             w8a8_out_dtype out_dtype, w8a8_stream_t stream,
+                             const w8a8_options *opts)
+{
+    return run_int8(A_dev, lda, a_s_dev, B_dev, ldb, b_s_dev, C_dev, ldc, M, N, K, out_dtype,
+                    reinterpret_cast<cudaStream_t>(stream), opts);
+}
+
+size_t w8a8_int8_workspace_size(int64_t M, int64_t N, int64_t K, const w8a8_options *opts)
+{
+    if (check_int8(M, N, K, opts) != W8A8_OK || M == 0 || N == 0)
+        return 0;
+    return int8_plan(M, N, K).workspace();
 }
 
 size_t w8a8_block_fp8_host_staging_size(int64_t M, int64_t N, int64_t K, w8a8_out_dtype out)

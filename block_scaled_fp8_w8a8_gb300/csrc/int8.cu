@@ -1,0 +1,536 @@
+// INT8 matmul with one scale per token and per output channel on sm_103a:
+//
+//   C[m,n] = cast( a_s[m] * b_s[n] * sum_k A[m,k] B[n,k] )
+//
+// The sum is over whole numbers and exact (32 bits); it is converted to fp32
+// once and multiplied by the two scales in fp32.
+//
+// This part's INT8 tensor rate is a small fraction of its fp16 rate, and the
+// tcgen05 kinds of sm_103a have no INT8 form.  But every INT8 value is an fp16
+// value, a product of two is at most 2^14, and a sum of up to 512 of them stays
+// within 2^23, which the MMA's fp32 accumulator holds without rounding.  So the
+// operands are widened to fp16, multiplied with tcgen05.mma kind::f16, and
+// every 512 columns of K the accumulator is added to 32-bit integer registers:
+// the INT8 product at the fp16 tensor rate, to the bit.
+//
+// Two launches: k_int8_widen writes both operands as fp16 into the workspace
+// (rows padded with zeros to whole 64-column steps, so that any size, stride
+// and alignment of the INT8 operands is as good as another), k_int8_mma
+// multiplies them.
+#include <algorithm>
+
+#include "epilogue.cuh"
+#include "kernels.cuh"
+#include "ptx.cuh"
+
+namespace w8a8 {
+
+namespace {
+
+// A stage holds 64 columns of K (one 128-byte fp16 row); an accumulator takes
+// the products of this many stages: 512 columns.
+constexpr int kChunkSteps = 8;
+
+// ------------------------------------------------------------------ widening
+
+// Four INT8 values of a word as fp16 pairs, exactly: byte b (offset by 128) in
+// the low mantissa bits of 1024 is 1024 + b + 128; the constant goes off again.
+__device__ __forceinline__ uint2 widen4(uint32_t w)
+{
+    const uint32_t u = w ^ 0x80808080u;
+    const uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140);
+    const uint32_t hi = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 off = __floats2half2_rn(1152.f, 1152.f);
+    const __half2 a = __hsub2(*reinterpret_cast<const __half2 *>(&lo), off);
+    const __half2 b = __hsub2(*reinterpret_cast<const __half2 *>(&hi), off);
+    return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+}
+
+// 16 INT8 values at columns c .. c+15 of a row (zeros past K).  ACCESS: bytes
+// per load that the operand's address and stride allow (16, 4 or 1).
+template <int ACCESS>
+__device__ __forceinline__ uint4 load16(const uint8_t *row, int c, int K)
+{
+    if (ACCESS == 16 && c + 16 <= K)
+        return __ldg(reinterpret_cast<const uint4 *>(row + c));
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int k = c + 4 * i;
+        if (ACCESS >= 4 && k + 4 <= K) {
+            w[i] = __ldg(reinterpret_cast<const uint32_t *>(row + k));
+        } else {
+            w[i] = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (k + j < K)
+                    w[i] |= static_cast<uint32_t>(__ldg(row + k + j)) << (8 * j);
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+constexpr int kWidenThreads = 256;
+
+// Both operands in one launch: units of 16 columns, A's first.
+template <int ACCESS>
+__global__ void __launch_bounds__(kWidenThreads) k_int8_widen(const Int8WidenParams p)
+{
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const long long per_row = p.Kp / 16;
+    const long long units_a = p.rows_a * per_row, units = units_a + p.rows_b * per_row;
+    const long long stride = static_cast<long long>(gridDim.x) * kWidenThreads;
+    for (long long u = static_cast<long long>(blockIdx.x) * kWidenThreads + threadIdx.x; u < units;
+         u += stride) {
+        const bool b = u >= units_a;
+        const long long v = b ? u - units_a : u;
+        const long long r = v / per_row;
+        const int c = static_cast<int>(v - r * per_row) * 16;
+        const uint8_t *row = b ? p.B + r * p.ldb : p.A + r * p.lda;
+        if (!in_bounds(r < (b ? p.rows_b : p.rows_a) && c < p.Kp, p.status, SITE_BOUNDS_WORKSPACE))
+            continue;
+        const uint4 w = load16<ACCESS>(row, c, p.K);
+        const uint2 h0 = widen4(w.x), h1 = widen4(w.y), h2 = widen4(w.z), h3 = widen4(w.w);
+        uint4 *dst = reinterpret_cast<uint4 *>((b ? p.B16 : p.A16) + (r * p.Kp + c) * 2);
+        dst[0] = make_uint4(h0.x, h0.y, h1.x, h1.y);
+        dst[1] = make_uint4(h2.x, h2.y, h3.x, h3.y);
+    }
+}
+
+// ------------------------------------------------------------------ product
+
+template <bool PAIR, int BN, int STAGES, int CPW, int EB> struct Int8Layout {
+    static constexpr int kTileM = PAIR ? 256 : 128;
+    static constexpr int kPromoWG = BN / CPW;
+    static constexpr int kThreads = 128 + 128 * kPromoWG;
+    static constexpr uint32_t kABytes = 128u * 128u;                             // this CTA's rows of A
+    static constexpr uint32_t kBBytes = static_cast<uint32_t>(PAIR ? BN / 2 : BN) * 128u;
+    static constexpr int kBufs = 512 / BN;
+    static constexpr uint32_t kTmemCols = 512;
+    static constexpr size_t kStageBytes = STAGES * (kABytes + kBBytes);
+    static constexpr size_t kEpiBytes = 4 * kPromoWG * 2048 * EB;
+    static constexpr size_t kScaleBytes = 4 * kPromoWG * CPW * 4;                // b_s, per warp
+    static constexpr int kRegsLow = 56, kRegsHigh = 224;
+    static_assert(kThreads == 384 && 128 * kRegsLow + 256 * kRegsHigh <= 384 * 168,
+                  "register split exceeds the launch's registers");
+    // full, pair_full, empty per stage; tfull, tempty per buffer; drain
+    static constexpr int kBars = 3 * STAGES + 2 * kBufs + 1;
+    static constexpr size_t kSmem = 1024 + kStageBytes + kEpiBytes + kScaleBytes + kBars * 8 + 16;
+    static_assert(kSmem <= 232448, "shared memory per CTA");
+};
+
+constexpr int kRaster = 8;           // M tiles per raster group
+
+__device__ __forceinline__ void int8_tile_coords(int t, int num_m, int num_n, int &mb, int &nb)
+{
+    const int per_group = kRaster * num_n;
+    const int gid = t / per_group;
+    const int first_m = gid * kRaster;
+    const int gm = min(num_m - first_m, kRaster);
+    const int r = t - gid * per_group;
+    mb = first_m + r % gm;
+    nb = r / gm;
+}
+
+// One persistent CTA (PAIR: one CTA pair, sharing 256 x BN tiles through
+// cta_group::2 MMAs) per SM (SM pair).  Roles, barriers and the pair's protocol
+// are those of the FP8 kernels (gemm_tiled.cu, gemm_pair.cu) without their
+// per-group scales: warp 0 TMA producer, warp 1 MMA issuer (the odd CTA's:
+// forwarder of its landed stages), warps 4.. integer promotion and epilogue.
+template <bool PAIR, int BN, int STAGES, int CPW, int EB>
+__global__ void __launch_bounds__(Int8Layout<PAIR, BN, STAGES, CPW, EB>::kThreads, 1)
+    k_int8_mma(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+               const __grid_constant__ CUtensorMap tmC, const Int8Params p)
+{
+    using L = Int8Layout<PAIR, BN, STAGES, CPW, EB>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t sB = smem_addr(smem);
+    const uint32_t sA = sB + STAGES * L::kBBytes;
+    const uint32_t sEpi = sB + static_cast<uint32_t>(L::kStageBytes);
+    float *scales = reinterpret_cast<float *>(smem + L::kStageBytes + L::kEpiBytes);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kStageBytes + L::kEpiBytes +
+                                                  L::kScaleBytes);
+    const uint32_t bar0 = smem_addr(bars);
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto pfull_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };
+    auto tfull_bar = [&](int b) { return bar0 + 8u * (3 * STAGES + b); };
+    auto tempty_bar = [&](int b) { return bar0 + 8u * (3 * STAGES + L::kBufs + b); };
+    const uint32_t drain_bar = bar0 + 8u * (3 * STAGES + 2 * L::kBufs);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + L::kBars);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const uint32_t warp = warp_index(), lane = lane_index();
+    const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+    const int first_tile = static_cast<int>(PAIR ? blockIdx.x >> 1 : blockIdx.x);
+    const int tile_stride = static_cast<int>(PAIR ? gridDim.x >> 1 : gridDim.x);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(pfull_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        for (int b = 0; b < L::kBufs; ++b) {
+            mbar_init(tfull_bar(b), 1);
+            mbar_init(tempty_bar(b), (PAIR ? 2 : 1) * 4 * L::kPromoWG);
+        }
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        mbar_fence_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_map(&tmA);
+        tma_prefetch_map(&tmB);
+        tma_prefetch_map(&tmC);
+    }
+    if (warp == 1) {
+        if constexpr (PAIR) {
+            tmem_alloc_pair(smem_addr(tmem_slot), L::kTmemCols);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(smem_addr(tmem_slot), L::kTmemCols);
+            tmem_relinquish();
+        }
+    }
+    tc_fence_before_sync();
+    if constexpr (PAIR)
+        cluster_sync();      // barriers of both CTAs initialised, TMEM allocated in both
+    else
+        __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_slot;
+    const WaitGuard guard{abort_flag, p.status, p.wait_limit};
+
+    grid_launch_dependents();
+    grid_dependency_wait();
+
+    // A role that gives up also raises the peer's abort flag.
+    auto abort_peer = [&]() {
+        if constexpr (PAIR) {
+            const uint32_t peer_flag =
+                cluster_map(smem_addr(const_cast<int *>(abort_flag)), rank ^ 1u);
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_flag), "r"(1u) : "memory");
+        }
+    };
+
+    if (warp < 4) {
+        regs_dealloc<L::kRegsLow>();
+        if (warp == 0 && lane == 0) {
+            // ---------------------------------------------------------- TMA producer
+            int stage = 0;
+            uint32_t phase = 0;
+            long long issued = 0;
+            bool ok = true;
+            for (int t = first_tile; ok && t < p.num_tiles; t += tile_stride) {
+                int mb, nb;
+                int8_tile_coords(t, p.num_m_tiles, p.num_n_tiles, mb, nb);
+                const int arow0 = mb * L::kTileM + 128 * static_cast<int>(rank);
+                const int brow = nb * BN + (PAIR ? (BN / 2) * static_cast<int>(rank) : 0);
+                for (int g = 0; g < p.steps; ++g) {
+                    if (!wait_bounded(empty_bar(stage), phase ^ 1u, guard, SITE_TILED_PRODUCER)) {
+                        ok = false;
+                        break;
+                    }
+                    const int arow = arow0 + ((W8A8_DEBUG_BOUNDS && issued == 0 &&
+                                               p.debug_skip_tma == kDebugBadFirstLoad)
+                                                  ? (1 << 28)
+                                                  : 0);
+                    const bool in =
+                        in_bounds(arow < p.num_m_tiles * L::kTileM, p.status, SITE_BOUNDS_A) &&
+                        in_bounds(brow < p.num_n_tiles * BN, p.status, SITE_BOUNDS_B);
+                    if (issued != p.debug_skip_tma && in) {
+                        mbar_arrive_expect_tx(full_bar(stage), L::kABytes + L::kBBytes);
+                        tma_load_2d(sA + stage * L::kABytes, &tmA, full_bar(stage), g * 128, arow);
+                        tma_load_2d(sB + stage * L::kBBytes, &tmB, full_bar(stage), g * 128, brow);
+                    }
+                    ++issued;
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            const int next_stage = stage;
+            const uint32_t next_phase = phase;
+            if (ok) {
+                // Tail: every stage released by the MMA, so that no commit
+                // arrives on this CTA after it has left.
+                for (int s = 0; s < STAGES && ok; ++s) {
+                    ok = wait_bounded(empty_bar(stage), phase ^ 1u, guard, SITE_TILED_PRODUCER);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (!ok) {
+                abort_peer();
+                // Drain this CTA's own loads (the last issue into each stage).
+                for (int s = 0; s < STAGES; ++s) {
+                    const bool this_round = s < next_stage;
+                    if (!this_round && issued < STAGES && s >= issued)
+                        continue;
+                    wait_drain(full_bar(s), this_round ? next_phase : (next_phase ^ 1u), p.status,
+                               p.wait_limit, (SITE_DRAIN << 8) | 4u);
+                }
+            }
+        } else if (warp == 1 && lane == 0 && rank == 0) {
+            // ---------------------------------------------------------- MMA issuer
+            constexpr uint32_t idesc = idesc_f16_f32(L::kTileM, BN);
+            int stage = 0;
+            uint32_t phase = 0;
+            uint32_t it = 0;                 // accumulator uses
+            bool ok = true;
+            for (int t = first_tile; ok && t < p.num_tiles; t += tile_stride) {
+                for (int g = 0; g < p.steps; ++g) {
+                    const uint32_t buf = it % L::kBufs;
+                    const int in_chunk = g % kChunkSteps;
+                    if ((in_chunk == 0 && !wait_bounded(tempty_bar(buf), ((it / L::kBufs) & 1u) ^ 1u,
+                                                        guard, SITE_TILED_MMA_TMEM)) ||
+                        !wait_bounded(full_bar(stage), phase, guard, SITE_TILED_MMA_FULL) ||
+                        (PAIR && !wait_bounded(pfull_bar(stage), phase, guard, SITE_PAIR_PEER))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const uint32_t d = tmem_base + buf * BN;
+                    const uint64_t ad = sw128_kmajor_desc(sA + stage * L::kABytes);
+                    const uint64_t bd = sw128_kmajor_desc(sB + stage * L::kBBytes);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_f16<PAIR>(d, ad + 2u * kk, bd + 2u * kk, idesc,
+                                      (in_chunk > 0 || kk > 0) ? 1u : 0u);
+                    const bool last = in_chunk == kChunkSteps - 1 || g == p.steps - 1;
+                    if constexpr (PAIR) {
+                        mma_commit_pair_mc(empty_bar(stage), 3);
+                        if (last)
+                            mma_commit_pair_mc(tfull_bar(buf), 3);
+                    } else {
+                        mma_commit(empty_bar(stage));
+                        if (last)
+                            mma_commit(tfull_bar(buf));
+                    }
+                    if (last)
+                        ++it;
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (!ok)
+                abort_peer();
+            // Every MMA has finished reading shared memory and writing TMEM
+            // before the CTA (pair) can pass its final barrier.
+            if constexpr (PAIR)
+                mma_commit_pair_mc(drain_bar, 1);
+            else
+                mma_commit(drain_bar);
+            wait_drain(drain_bar, 0, p.status, p.wait_limit, (SITE_DRAIN << 8) | 4u);
+        } else if (PAIR && warp == 1 && lane == 0) {
+            // ---------------------------------------------------------- forwarder (rank 1)
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int t = first_tile; ok && t < p.num_tiles; t += tile_stride) {
+                for (int g = 0; g < p.steps; ++g) {
+                    if (!wait_bounded(full_bar(stage), phase, guard, SITE_PAIR_PEER)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_remote(cluster_map(pfull_bar(stage), 0));
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (!ok)
+                abort_peer();
+        }
+        __syncwarp();
+    } else {
+        // -------------------------------------------------------------- promotion + epilogue
+        regs_alloc<L::kRegsHigh>();
+        const int h = static_cast<int>(warp / 4) - 1;
+        const uint32_t q = warp & 3u;
+        const uint32_t epi_buf = sEpi + (warp - 4u) * 2048u * EB;
+        float *my_bs = scales + (warp - 4u) * CPW;
+        const bool fp32 = p.out_kind == OUT_FP32, bf = p.out_kind == OUT_BF16;
+        uint32_t it = 0;
+        bool ok = true;
+        for (int t = first_tile; t < p.num_tiles; t += tile_stride) {
+            int mb, nb;
+            int8_tile_coords(t, p.num_m_tiles, p.num_n_tiles, mb, nb);
+            const int col0 = nb * BN + h * CPW;
+            const int y = mb * L::kTileM + 128 * static_cast<int>(rank) + static_cast<int>(q * 32);
+            const int rows = min(32, p.M - y);
+            // This warp's column scales, and the lane's row scale.
+            __syncwarp();
+            for (int c = static_cast<int>(lane); c < CPW; c += 32)
+                my_bs[c] = col0 + c < p.N ? __ldg(p.b_s + col0 + c) : 0.f;
+            const float as = static_cast<int>(lane) < rows ? __ldg(p.a_s + y + lane) : 0.f;
+            __syncwarp();
+            int acc[CPW];
+#pragma unroll
+            for (int j = 0; j < CPW; ++j)
+                acc[j] = 0;
+            for (int g = 0; g < p.steps; g += kChunkSteps) {
+                const uint32_t buf = it % L::kBufs;
+                ok = __all_sync(0xffffffffu, wait_bounded(tfull_bar(buf), (it / L::kBufs) & 1u,
+                                                          guard, SITE_TILED_PROMOTE));
+                if (!ok)
+                    break;
+                tc_fence_after_sync();
+                const uint32_t taddr = tmem_base + ((q * 32u) << 16) + buf * BN + h * CPW;
+#pragma unroll
+                for (int c = 0; c < CPW / 32; ++c) {
+                    float v[32];
+                    tmem_load_32cols(taddr + 32u * c, v);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        acc[32 * c + j] += __float2int_rn(v[j]);
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (PAIR)
+                        mbar_arrive_remote(cluster_map(tempty_bar(buf), 0));
+                    else
+                        mbar_arrive(tempty_bar(buf));
+                }
+                ++it;
+            }
+            if (!ok)
+                break;
+            if (rows > 0 && col0 < p.N &&
+                in_bounds(y + rows <= p.M && y >= 0, p.status, SITE_BOUNDS_C)) {
+                auto pack = [&](int k, int j) {
+                    if (fp32) {
+                        const int c = (16 * k + 4 * j) % CPW;
+                        const float4 s = *reinterpret_cast<const float4 *>(my_bs + c);
+                        return make_uint4(__float_as_uint(__int2float_rn(acc[c]) * as * s.x),
+                                          __float_as_uint(__int2float_rn(acc[c + 1]) * as * s.y),
+                                          __float_as_uint(__int2float_rn(acc[c + 2]) * as * s.z),
+                                          __float_as_uint(__int2float_rn(acc[c + 3]) * as * s.w));
+                    }
+                    const int c = (32 * k + 8 * j) % CPW;
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 s = *reinterpret_cast<const float2 *>(my_bs + c + 2 * i);
+                        const float lo = __int2float_rn(acc[c + 2 * i]) * as * s.x;
+                        const float hi = __int2float_rn(acc[c + 2 * i + 1]) * as * s.y;
+                        w[i] = bf ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
+                    }
+                    return make_uint4(w[0], w[1], w[2], w[3]);
+                };
+                store_warp_rows<CPW, EB>(pack, &tmC, epi_buf, lane, col0, y, p.N, fp32, p.tma_store,
+                                         false, rows, p.C, p.ldc);
+            }
+        }
+        if (!ok && lane == 0)
+            abort_peer();
+        if (lane == 0)
+            tma_store_wait_read();
+    }
+
+    tc_fence_before_sync();
+    if constexpr (PAIR)
+        cluster_sync();
+    else
+        __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        if constexpr (PAIR)
+            tmem_dealloc_pair(tmem_base, L::kTmemCols);
+        else
+            tmem_dealloc(tmem_base, L::kTmemCols);
+    }
+}
+
+template <bool PAIR, int BN, int STAGES, int CPW, int EB>
+cudaError_t launch_mma(const CUtensorMap &tmA, const CUtensorMap &tmB, const CUtensorMap &tmC,
+                       const Int8Params &p, const LaunchCfg &cfg, int *clusters)
+{
+    using L = Int8Layout<PAIR, BN, STAGES, CPW, EB>;
+    auto kernel = k_int8_mma<PAIR, BN, STAGES, CPW, EB>;
+    static volatile int smem_set[kMaxDeviceFlags] = {};
+    cudaError_t e = ensure_smem_limit(kernel, smem_set);
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(clusters ? 2 : cfg.grid, 1, 1);
+    lc.blockDim = dim3(L::kThreads, 1, 1);
+    lc.dynamicSmemBytes = L::kSmem;
+    lc.stream = cfg.stream;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (PAIR) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = 2;
+        attr[n].val.clusterDim.y = 1;
+        attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    lc.attrs = attr;
+    if (clusters) {
+        lc.numAttrs = n;
+        return cudaOccupancyMaxActiveClusters(clusters, kernel, &lc);
+    }
+    // Behind the widening launch it always overlaps that one's tail: it waits
+    // for it before its first access.
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    lc.numAttrs = n + 1;
+    return cudaLaunchKernelEx(&lc, kernel, tmA, tmB, tmC, p);
+}
+
+}  // namespace
+
+cudaError_t launch_int8_widen(const Int8WidenParams &p, int access, int grid, cudaStream_t stream)
+{
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(grid, 1, 1);
+    lc.blockDim = dim3(kWidenThreads, 1, 1);
+    lc.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelEx(&lc, access == 16  ? k_int8_widen<16>
+                                   : access == 4 ? k_int8_widen<4>
+                                                 : k_int8_widen<1>,
+                              p);
+}
+
+cudaError_t launch_int8_mma(const CUtensorMap &tmA, const CUtensorMap &tmB, const CUtensorMap &tmC,
+                            const Int8Params &p, int pair, const LaunchCfg &cfg)
+{
+    return pair ? launch_mma<true, 256, 6, 128, 1>(tmA, tmB, tmC, p, cfg, nullptr)
+                : launch_mma<false, 128, 6, 64, 1>(tmA, tmB, tmC, p, cfg, nullptr);
+}
+
+int int8_max_pairs()
+{
+    static volatile int cached[kMaxDeviceFlags] = {};
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDeviceFlags)
+        return -1;
+    if (cached[dev] > 0)
+        return cached[dev];
+    const CUtensorMap none = {};
+    if (launch_mma<true, 256, 6, 128, 1>(none, none, none, Int8Params{}, LaunchCfg{}, &n) !=
+            cudaSuccess ||
+        n <= 0)
+        return -1;
+    cached[dev] = n;
+    return n;
+}
+
+}  // namespace w8a8

@@ -186,6 +186,58 @@ struct GenericParams {
 };
 cudaError_t launch_generic(const GenericParams &p, const LaunchCfg &cfg);
 
+// Ragged grouped matmul: rows of A sorted by expert, expert e's rows at
+// offsets[e] .. offsets[e+1]-1 (read on the device).
+constexpr int kRaggedMaxExperts = 1024;
+struct RaggedParams {
+    const float *a_s;      // [M, G]
+    const float *b_s;      // [experts, NB, G]
+    void *C;               // [M, N]
+    const int *offsets;    // [experts + 1]
+    int M, N, K, G, NB;
+    int experts;
+    int num_n_tiles;       // column tiles of BN
+    int out_kind;
+    int debug_skip_tma;    // test hook: >= 0 makes the producer skip that many-th load
+    unsigned *status;
+    unsigned long long wait_limit;
+};
+// tmA: boxes of 32 rows; tmB: 3-D [experts, N, K], boxes of bn rows; tmC as for
+// launch_tiled.  bn: 128 or 256.
+cudaError_t launch_ragged(const CUtensorMap &tmA, const CUtensorMap &tmB, const CUtensorMap &tmC,
+                          const RaggedParams &p, int bn, const LaunchCfg &cfg);
+
+// INT8 matmul.  Widening: rows_a rows of A and rows_b of B (INT8, K columns) to
+// fp16 rows of Kp columns (a multiple of 64; zeros past K).
+struct Int8WidenParams {
+    const uint8_t *A, *B;
+    uint8_t *A16, *B16;        // [rows, Kp] fp16
+    long long rows_a, rows_b, lda, ldb;
+    int K, Kp;
+    unsigned *status;
+};
+// access: 16, 4 or 1 bytes per load, as the operands' addresses and strides allow.
+cudaError_t launch_int8_widen(const Int8WidenParams &p, int access, int grid, cudaStream_t stream);
+struct Int8Params {
+    const float *a_s;          // [M]
+    const float *b_s;          // [N]
+    void *C;                   // [M, ldc]
+    int M, N;
+    int steps;                 // 64-column steps of K
+    long long ldc;
+    int num_m_tiles, num_n_tiles, num_tiles;
+    int out_kind;
+    int tma_store;             // C, its rows and N allow 16-byte rows (tmC is valid)
+    int debug_skip_tma;
+    unsigned *status;
+    unsigned long long wait_limit;
+};
+// tmA, tmB: the fp16 operands as rows of 2 Kp bytes, boxes of 128 bytes by 128
+// rows.  pair: CTA pairs on 256 x 256 tiles (cfg.grid CTAs, even), else 128 x 128.
+cudaError_t launch_int8_mma(const CUtensorMap &tmA, const CUtensorMap &tmB, const CUtensorMap &tmC,
+                            const Int8Params &p, int pair, const LaunchCfg &cfg);
+int int8_max_pairs();          // CTA pairs that can be resident at once; < 0 on error
+
 // Shared memory bytes each kernel configuration needs (0 = unsupported configuration).
 size_t tiled_smem_bytes(int bn, int stages);
 // x_esize: fused activation quantisation's input element size (0: not fused).

@@ -1,0 +1,607 @@
+// The norms around a transformer block, fused with its gate and its residual,
+// and the per-token INT8 quantiser: the kernels that make the 8-bit operands
+// of the matmuls from whole rows.
+//
+// Sandwich norm, for each row m (all arithmetic in fp32, one rounding per output):
+//   u = h[m] / sqrt(mean(h[m]^2) + eps) * w_post      (w_post null: u = h[m])
+//   r = res_scale * x[m] + gate[m / gate_rows] * u    (gate null: 1)
+//   y = r / sqrt(mean(r^2) + eps) * w_pre             (w_pre null: y = r)
+// x_out = r in x's type; y in h's type, or quantised as the matmuls take it:
+// E4M3 codes with one scale per 128 columns, or INT8 codes with one per row.
+// y is computed from the fp32 r, not from the rounded x_out.
+//
+// INT8 quantiser: a_s[m] = max_k |X[m,k]| / 127 (fp32 quotient; 1 where it is
+// 0), A[m,k] = round_half_even(X[m,k] / a_s[m]) (fp32 quotient), in -127..127.
+//
+// HBM-bound: every input is read once and every output written once.  A row
+// is held in registers by the threads of one CTA (or one warp, for short
+// rows) between its two reductions; rows too long for that are held in shared
+// memory.
+#include <algorithm>
+#include <cstdio>
+
+#include "../../include/w8a8_block_fp8.h"
+#include "kernels.cuh"
+#include "ptx.cuh"
+#include "quant_math.cuh"
+
+namespace w8a8 {
+w8a8_status record_error(w8a8_status st, const char *message);
+
+namespace {
+
+constexpr int kPer = 16;                 // elements of a row that a thread holds in registers
+constexpr int kMaxThreads = 1024;
+constexpr int kRegRow = kPer * kMaxThreads;
+
+template <int KIND> struct Elem;
+template <> struct Elem<W8A8_IN_BF16> {
+    using T = __nv_bfloat16;
+    static __device__ __forceinline__ float load(const T *p) { return __bfloat162float(*p); }
+    static __device__ __forceinline__ void store(T *p, float v) { *p = __float2bfloat16_rn(v); }
+};
+template <> struct Elem<W8A8_IN_FP16> {
+    using T = __half;
+    static __device__ __forceinline__ float load(const T *p) { return __half2float(*p); }
+    static __device__ __forceinline__ void store(T *p, float v) { *p = __float2half_rn(v); }
+};
+template <> struct Elem<W8A8_IN_FP32> {
+    using T = float;
+    static __device__ __forceinline__ float load(const T *p) { return *p; }
+    static __device__ __forceinline__ void store(T *p, float v) { *p = v; }
+};
+
+// VEC (8 or 1) consecutive elements at element index `i` of a row.  Eight are
+// one or two 16-byte accesses; the row starts on a 16-byte boundary then.
+template <int KIND, int VEC>
+__device__ __forceinline__ void load_vec(const void *row, int i, float (&v)[VEC])
+{
+    using E = Elem<KIND>;
+    const typename E::T *p = static_cast<const typename E::T *>(row) + i;
+    if constexpr (VEC == 1) {
+        v[0] = E::load(p);
+    } else if constexpr (KIND == W8A8_IN_FP32) {
+        const float4 a = reinterpret_cast<const float4 *>(p)[0];
+        const float4 b = reinterpret_cast<const float4 *>(p)[1];
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+        const uint4 a = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = quant::element<KIND>(w, j);
+    }
+}
+
+template <int KIND, int VEC>
+__device__ __forceinline__ void store_vec(void *row, int i, const float (&v)[VEC])
+{
+    using E = Elem<KIND>;
+    typename E::T *p = static_cast<typename E::T *>(row) + i;
+    if constexpr (VEC == 1) {
+        E::store(p, v[0]);
+    } else if constexpr (KIND == W8A8_IN_FP32) {
+        reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        uint4 a;
+        if constexpr (KIND == W8A8_IN_BF16)
+            a = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                           pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+        else
+            a = make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]),
+                           pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7]));
+        *reinterpret_cast<uint4 *>(p) = a;
+    }
+}
+
+// Sum (or maximum) of v over the threads of one row: the CTA, or a warp where
+// the CTA's warps each have a row of their own.  Every thread gets the result;
+// the order of the additions is fixed.  `part` is used once per launch.
+struct Add {
+    static __device__ __forceinline__ float op(float a, float b) { return a + b; }
+};
+struct Max {
+    static __device__ __forceinline__ float op(float a, float b) { return fmaxf(a, b); }
+};
+template <typename Op>
+__device__ __forceinline__ float row_reduce(float v, float *part, bool warp_rows)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        v = Op::op(v, __shfl_xor_sync(0xffffffffu, v, o));
+    if (warp_rows)
+        return v;
+    const int warps = static_cast<int>(blockDim.x) >> 5;
+    if ((threadIdx.x & 31) == 0)
+        part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    const int l = static_cast<int>(threadIdx.x & 31);
+    v = part[l < warps ? l : 0];          // every warp reduces the partials alike
+    if (l >= warps)
+        v = 0.f;                          // neutral: the maxima are of magnitudes
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        v = Op::op(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+// x / s for a pair, correctly rounded (see quant_math.cuh for the fast form's range).
+__device__ __forceinline__ float2 div_pair(float a, float b, float s, bool fast, uint64_t ns2,
+                                           uint64_t y2)
+{
+    float2 q;
+    if (fast) {
+        unpack2f(quant::div_by_scale2(pack2f(a, b), ns2, y2), q.x, q.y);
+    } else {
+        q.x = __fdiv_rn(a, s);
+        q.y = __fdiv_rn(b, s);
+    }
+    return q;
+}
+
+// A row's scale for INT8 codes from its absolute maximum.
+__device__ __forceinline__ float int8_scale(float amax)
+{
+    const float s = __fdiv_rn(amax, 127.f);
+    return s == 0.f ? 1.f : s;            // an all-zero row, or a maximum that underflows
+}
+
+__device__ __forceinline__ uint32_t int8_code(float q)
+{
+    // |q| <= 127 (1 + 2^-23) but where a subnormal scale lost precision
+    return static_cast<uint32_t>(max(-127, min(127, __float2int_rn(q)))) & 0xffu;
+}
+
+template <int VEC>
+__device__ __forceinline__ void store_int8(uint8_t *p, const float (&v)[VEC], float s)
+{
+    const bool fast = s >= 0x1p-64f && s <= 0x1p64f;
+    const float y = __frcp_rn(s);
+    const uint64_t ns2 = pack2f(-s, -s), y2 = pack2f(y, y);
+    if constexpr (VEC == 1) {
+        *p = static_cast<uint8_t>(int8_code(div_pair(v[0], v[0], s, fast, ns2, y2).x));
+    } else {
+        uint32_t w[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float2 a = div_pair(v[4 * j], v[4 * j + 1], s, fast, ns2, y2);
+            const float2 b = div_pair(v[4 * j + 2], v[4 * j + 3], s, fast, ns2, y2);
+            w[j] = int8_code(a.x) | int8_code(a.y) << 8 | int8_code(b.x) << 16 | int8_code(b.y) << 24;
+        }
+        *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    }
+}
+
+struct NormParams {
+    const void *h, *x, *w_post, *gate, *w_pre;
+    void *x_out, *y;
+    float *scales;
+    long long M;
+    int D;
+    long long ld_h, ld_x, ld_xo, ld_y;     // elements per row
+    long long gate_rows;
+    float res_scale, eps;
+    int y_kind;                            // w8a8_norm_out
+    int row_threads;                       // 32: a warp per row, else the CTA
+    unsigned *status;
+};
+
+// One row per CTA (per warp where row_threads is 32).  HELD: the row stays in
+// the threads' registers; otherwise in dynamic shared memory (D floats).
+template <int HK, int XK, int VEC, bool HELD>
+__global__ void __launch_bounds__(kMaxThreads) k_sandwich_norm(const NormParams p)
+{
+    extern __shared__ float held[];
+    __shared__ float part[3][32];
+    constexpr int kN = HELD ? kPer / VEC : 1;
+    constexpr int kHB = HK == W8A8_IN_FP32 ? 4 : 2, kXB = XK == W8A8_IN_FP32 ? 4 : 2;
+    grid_launch_dependents();
+    grid_dependency_wait();          // the inputs come from the work before this launch
+    const bool warp_rows = p.row_threads == 32;
+    const int T = warp_rows ? 32 : static_cast<int>(blockDim.x);
+    const int tid = warp_rows ? static_cast<int>(lane_index()) : static_cast<int>(threadIdx.x);
+    const long long m = warp_rows
+                            ? static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + warp_index()
+                            : static_cast<long long>(blockIdx.x);
+    if (m >= p.M || !in_bounds(m >= 0 && p.D > 0, p.status, SITE_BOUNDS_A))
+        return;                      // whole warps (or the CTA): nothing waits for them
+    const int D = p.D;
+    const uint8_t *hrow = static_cast<const uint8_t *>(p.h) + m * p.ld_h * kHB;
+    const uint8_t *xrow = static_cast<const uint8_t *>(p.x) + m * p.ld_x * kXB;
+    uint8_t *orow = static_cast<uint8_t *>(p.x_out) + m * p.ld_xo * kXB;
+    const uint8_t *grow =
+        p.gate ? static_cast<const uint8_t *>(p.gate) + (m / p.gate_rows) * D * kHB : nullptr;
+    const int steps = HELD ? kN : (D + T * VEC - 1) / (T * VEC);
+
+    float v[kN][VEC], xv[kN][VEC];
+    // Chunk i of this thread: VEC elements from (i T + tid) VEC; D % VEC == 0.
+    auto at = [&](int i) { return (i * T + tid) * VEC; };
+
+    // (the unrolled form of every pass indexes registers; the other walks the row)
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < (HELD ? kN : steps); ++i) {
+        const int e = at(i);
+        float(&w)[VEC] = v[HELD ? i : 0];
+        if (e < D) {
+            load_vec<HK, VEC>(hrow, e, w);
+            if (HELD)
+                load_vec<XK, VEC>(xrow, e, xv[HELD ? i : 0]);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                ss = fmaf(w[j], w[j], ss);
+                if (!HELD)
+                    held[e + j] = w[j];
+            }
+        }
+    }
+    float inv = 1.f;
+    if (p.w_post)
+        inv = rsqrtf(row_reduce<Add>(ss, part[0], warp_rows) / static_cast<float>(D) + p.eps);
+
+    ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < (HELD ? kN : steps); ++i) {
+        const int e = at(i);
+        float(&w)[VEC] = v[HELD ? i : 0];
+        float(&xw)[VEC] = xv[HELD ? i : 0];
+        if (e < D) {
+            float wp[VEC], g[VEC];
+            if (p.w_post)
+                load_vec<HK, VEC>(p.w_post, e, wp);
+            if (grow)
+                load_vec<HK, VEC>(grow, e, g);
+            if (!HELD)
+                load_vec<XK, VEC>(xrow, e, xw);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                float u = HELD ? w[j] : held[e + j];
+                if (p.w_post)
+                    u = u * inv * wp[j];
+                if (grow)
+                    u *= g[j];
+                const float r = fmaf(p.res_scale, xw[j], u);
+                ss = fmaf(r, r, ss);
+                w[j] = r;
+                if (!HELD)
+                    held[e + j] = r;
+            }
+            if (p.x_out)
+                store_vec<XK, VEC>(orow, e, w);
+        }
+    }
+    inv = 1.f;
+    if (p.w_pre)
+        inv = rsqrtf(row_reduce<Add>(ss, part[1], warp_rows) / static_cast<float>(D) + p.eps);
+
+    // y, and its absolute maximum where one scale covers the row
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < (HELD ? kN : steps); ++i) {
+        const int e = at(i);
+        float(&w)[VEC] = v[HELD ? i : 0];
+        const bool in = e < D;
+        if (in) {
+            float wp[VEC];
+            if (p.w_pre)
+                load_vec<HK, VEC>(p.w_pre, e, wp);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                float y = HELD ? w[j] : held[e + j];
+                if (p.w_pre)
+                    y = y * inv * wp[j];
+                w[j] = y;
+                amax = fmaxf(amax, fabsf(y));
+                if (!HELD && p.y_kind == W8A8_NORM_INT8)
+                    held[e + j] = y;
+            }
+        }
+        if (p.y_kind == W8A8_NORM_SAME) {
+            if (in)
+                store_vec<HK, VEC>(static_cast<uint8_t *>(p.y) + m * p.ld_y * kHB, e, w);
+        } else if (VEC == 8 && p.y_kind == W8A8_NORM_FP8) {
+            // Sixteen neighbouring lanes hold one 128-column group (T is a
+            // multiple of 16, so a group never straddles two steps).
+            const int warp_first = at(i) - static_cast<int>(lane_index()) * VEC;
+            if (warp_first < D) {            // the same for the whole warp
+                if (!in)
+                    amax = 0.f;
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1)
+                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                const float s = quant::group_scale(amax);
+                if (in) {
+                    const bool fast = s >= 0x1p-64f && s <= 0x1p64f;
+                    const float rc = __frcp_rn(s);
+                    const uint64_t ns2 = pack2f(-s, -s), y2 = pack2f(rc, rc);
+                    uint32_t raw[8], c[2];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        raw[j] = __float_as_uint(w[VEC == 8 ? j : 0]);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        c[j] = fast ? quant::encode4<W8A8_IN_FP32, true>(raw, j, s, ns2, y2)
+                                    : quant::encode4<W8A8_IN_FP32, false>(raw, j, s, ns2, y2);
+                    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.y) + m * p.ld_y + e) =
+                        make_uint2(c[0], c[1]);
+                    if ((lane_index() & 15) == 0)
+                        p.scales[m * ((D + 127) / 128) + e / 128] = s;
+                }
+            }
+            amax = 0.f;
+        }
+    }
+    if (p.y_kind == W8A8_NORM_INT8) {
+        const float s = int8_scale(row_reduce<Max>(amax, part[2], warp_rows));
+        uint8_t *row = static_cast<uint8_t *>(p.y) + m * p.ld_y;
+#pragma unroll
+        for (int i = 0; i < (HELD ? kN : steps); ++i) {
+            const int e = at(i);
+            if (e < D) {
+                float w[VEC];
+#pragma unroll
+                for (int j = 0; j < VEC; ++j)
+                    w[j] = HELD ? v[HELD ? i : 0][j] : held[e + j];
+                store_int8<VEC>(row + e, w, s);
+            }
+        }
+        if (tid == 0)
+            p.scales[m] = s;
+    }
+}
+
+struct QuantParams {
+    const void *X;
+    uint8_t *A;
+    float *a_s;
+    long long M;
+    int K;
+    long long ld_x, ld_a;
+    int row_threads;
+    unsigned *status;
+};
+
+// HELD: the row stays in registers; otherwise it is read twice.
+template <int KIND, int VEC, bool HELD>
+__global__ void __launch_bounds__(kMaxThreads) k_quant_int8(const QuantParams p)
+{
+    __shared__ float part[32];
+    constexpr int kN = HELD ? kPer / VEC : 1;
+    constexpr int kB = KIND == W8A8_IN_FP32 ? 4 : 2;
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const bool warp_rows = p.row_threads == 32;
+    const int T = warp_rows ? 32 : static_cast<int>(blockDim.x);
+    const int tid = warp_rows ? static_cast<int>(lane_index()) : static_cast<int>(threadIdx.x);
+    const long long m = warp_rows
+                            ? static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + warp_index()
+                            : static_cast<long long>(blockIdx.x);
+    if (m >= p.M || !in_bounds(m >= 0 && p.K > 0, p.status, SITE_BOUNDS_A))
+        return;
+    const uint8_t *row = static_cast<const uint8_t *>(p.X) + m * p.ld_x * kB;
+    const int steps = HELD ? kN : (p.K + T * VEC - 1) / (T * VEC);
+    float v[kN][VEC];
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < (HELD ? kN : steps); ++i) {
+        const int e = (i * T + tid) * VEC;
+        if (e < p.K) {
+            load_vec<KIND, VEC>(row, e, v[HELD ? i : 0]);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j)
+                amax = fmaxf(amax, fabsf(v[HELD ? i : 0][j]));
+        }
+    }
+    const float s = int8_scale(row_reduce<Max>(amax, part, warp_rows));
+#pragma unroll
+    for (int i = 0; i < (HELD ? kN : steps); ++i) {
+        const int e = (i * T + tid) * VEC;
+        if (e < p.K) {
+            if (!HELD)
+                load_vec<KIND, VEC>(row, e, v[0]);
+            store_int8<VEC>(p.A + m * p.ld_a + e, v[HELD ? i : 0], s);
+        }
+    }
+    if (tid == 0)
+        p.a_s[m] = s;
+}
+
+// Threads of a row's CTA: enough for kPer elements each, whole warps.
+int row_threads(long long n)
+{
+    const long long t = (n + kPer - 1) / kPer;
+    return static_cast<int>(std::min<long long>(kMaxThreads, (t + 31) / 32 * 32));
+}
+
+w8a8_status cuda_error(const char *what, cudaError_t e)
+{
+    char msg[256];
+    snprintf(msg, sizeof(msg), "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
+    return record_error(W8A8_ERR_CUDA, msg);
+}
+
+template <typename Params>
+cudaError_t launch_rows(void (*kernel)(Params), const Params &p, long long rows, int T, size_t smem,
+                        cudaStream_t stream)
+{
+    const int per_cta = T == 32 ? 4 : 1;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(static_cast<unsigned>((rows + per_cta - 1) / per_cta), 1, 1);
+    lc.blockDim = dim3(T == 32 ? 128 : T, 1, 1);
+    lc.dynamicSmemBytes = smem;
+    lc.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelEx(&lc, kernel, p);
+}
+
+bool on(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+template <int HK, int XK, int VEC>
+cudaError_t launch_norm(NormParams p, cudaStream_t stream)
+{
+    if (p.D <= kRegRow) {
+        p.row_threads = row_threads(p.D);
+        return launch_rows(k_sandwich_norm<HK, XK, VEC, true>, p, p.M, p.row_threads, 0, stream);
+    }
+    static volatile int smem_set[kMaxDeviceFlags] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev < 0 || dev >= kMaxDeviceFlags))
+        e = cudaErrorInvalidDevice;
+    if (e == cudaSuccess && !smem_set[dev]) {
+        e = cudaFuncSetAttribute(k_sandwich_norm<HK, XK, VEC, false>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, W8A8_NORM_MAX_D * 4);
+        smem_set[dev] = e == cudaSuccess;
+    }
+    if (e != cudaSuccess)
+        return e;
+    p.row_threads = kMaxThreads;
+    return launch_rows(k_sandwich_norm<HK, XK, VEC, false>, p, p.M, kMaxThreads,
+                       static_cast<size_t>(p.D) * 4, stream);
+}
+
+template <int HK, int XK> cudaError_t launch_norm(const NormParams &p, bool vec, cudaStream_t stream)
+{
+    return vec ? launch_norm<HK, XK, 8>(p, stream) : launch_norm<HK, XK, 1>(p, stream);
+}
+
+template <int KIND> cudaError_t launch_quant(QuantParams p, bool vec, cudaStream_t stream)
+{
+    const bool held = p.K <= kRegRow;
+    p.row_threads = row_threads(p.K);
+    void (*kernel)(QuantParams) =
+        vec ? (held ? k_quant_int8<KIND, 8, true> : k_quant_int8<KIND, 8, false>)
+            : (held ? k_quant_int8<KIND, 1, true> : k_quant_int8<KIND, 1, false>);
+    return launch_rows(kernel, p, p.M, p.row_threads, 0, stream);
+}
+
+}  // namespace
+}  // namespace w8a8
+
+extern "C" w8a8_status w8a8_sandwich_norm(const void *h_dev, w8a8_in_dtype h_dtype, int64_t ld_h,
+                                          const void *x_dev, w8a8_in_dtype x_dtype, int64_t ld_x,
+                                          const void *w_post_dev, const void *gate_dev,
+                                          int64_t gate_rows, const void *w_pre_dev,
+                                          float res_scale, float eps, void *x_out_dev,
+                                          int64_t ld_xo, void *y_dev, float *scales_dev,
+                                          w8a8_norm_out y_kind, int64_t ld_y, int64_t M, int64_t D,
+                                          w8a8_stream_t stream)
+{
+    using namespace w8a8;
+    if (M < 0 || D < 0)
+        return record_error(W8A8_ERR_INVALID_ARG, "negative size");
+    if (h_dtype < W8A8_IN_BF16 || h_dtype > W8A8_IN_FP32 || x_dtype < W8A8_IN_BF16 ||
+        x_dtype > W8A8_IN_FP32)
+        return record_error(W8A8_ERR_INVALID_ARG, "unknown input dtype");
+    if (y_kind < W8A8_NORM_SAME || y_kind > W8A8_NORM_INT8)
+        return record_error(W8A8_ERR_INVALID_ARG, "unknown form of y");
+    if (x_dtype != h_dtype && x_dtype != W8A8_IN_FP32)
+        return record_error(W8A8_ERR_UNSUPPORTED, "x must have h's type or fp32");
+    if (gate_dev && gate_rows < 1)
+        return record_error(W8A8_ERR_INVALID_ARG, "gate_rows must be positive");
+    ld_h = ld_h ? ld_h : D;
+    ld_x = ld_x ? ld_x : D;
+    ld_xo = ld_xo ? ld_xo : D;
+    ld_y = ld_y ? ld_y : D;
+    if (ld_h < D || ld_x < D || ld_xo < D || ld_y < D)
+        return record_error(W8A8_ERR_INVALID_ARG, "a row stride is shorter than its row");
+    if (M == 0 || D == 0)
+        return W8A8_OK;
+    if (!h_dev || !x_dev || !y_dev || (y_kind != W8A8_NORM_SAME && !scales_dev))
+        return record_error(W8A8_ERR_INVALID_ARG, "null pointer argument");
+    if (M > (1ll << 31) - 1 || D > W8A8_NORM_MAX_D)
+        return record_error(W8A8_ERR_UNSUPPORTED, "M of 2^31 or more, or D above W8A8_NORM_MAX_D");
+    const int hb = h_dtype == W8A8_IN_FP32 ? 4 : 2, xb = x_dtype == W8A8_IN_FP32 ? 4 : 2;
+    const int yb = y_kind == W8A8_NORM_SAME ? hb : 1;
+    if (!on(h_dev, hb) || !on(w_post_dev, hb) || !on(gate_dev, hb) || !on(w_pre_dev, hb) ||
+        !on(x_dev, xb) || !on(x_out_dev, xb) || !on(y_dev, yb) || !on(scales_dev, 4))
+        return record_error(W8A8_ERR_UNSUPPORTED, "a pointer is not aligned to its element size");
+    // Eight elements at a time where every row of every tensor allows it
+    // (y's eight INT8 or E4M3 codes are one 8-byte store), else one.
+    const bool vec = D % 8 == 0 && on(h_dev, 16) && on(x_dev, 16) && on(w_post_dev, 16) &&
+                     on(gate_dev, 16) && on(w_pre_dev, 16) && on(x_out_dev, 16) &&
+                     on(y_dev, yb == 1 ? 8 : 16) && ld_h * hb % 16 == 0 && ld_x * xb % 16 == 0 &&
+                     (!x_out_dev || ld_xo * xb % 16 == 0) && ld_y * yb % (yb == 1 ? 8 : 16) == 0;
+    if (y_kind == W8A8_NORM_FP8 && (!vec || D < 16 || D % 16 != 0))
+        return record_error(W8A8_ERR_UNSUPPORTED, "FP8 codes need D to be a multiple of 16, rows of h, x "
+                                                  "and x_out on 16-byte boundaries and of y on 8-byte ones");
+    NormParams p = {};
+    p.h = h_dev;
+    p.x = x_dev;
+    p.w_post = w_post_dev;
+    p.gate = gate_dev;
+    p.w_pre = w_pre_dev;
+    p.x_out = x_out_dev;
+    p.y = y_dev;
+    p.scales = scales_dev;
+    p.M = M;
+    p.D = static_cast<int>(D);
+    p.ld_h = ld_h;
+    p.ld_x = ld_x;
+    p.ld_xo = ld_xo;
+    p.ld_y = ld_y;
+    p.gate_rows = gate_rows;
+    p.res_scale = res_scale;
+    p.eps = eps;
+    p.y_kind = y_kind;
+    if (W8A8_DEBUG_BOUNDS && status_word_address(&p.status) != cudaSuccess)
+        p.status = nullptr;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (h_dtype == W8A8_IN_FP32)
+        e = launch_norm<W8A8_IN_FP32, W8A8_IN_FP32>(p, vec, s);
+    else if (h_dtype == W8A8_IN_BF16)
+        e = x_dtype == W8A8_IN_FP32 ? launch_norm<W8A8_IN_BF16, W8A8_IN_FP32>(p, vec, s)
+                                    : launch_norm<W8A8_IN_BF16, W8A8_IN_BF16>(p, vec, s);
+    else
+        e = x_dtype == W8A8_IN_FP32 ? launch_norm<W8A8_IN_FP16, W8A8_IN_FP32>(p, vec, s)
+                                    : launch_norm<W8A8_IN_FP16, W8A8_IN_FP16>(p, vec, s);
+    return e == cudaSuccess ? W8A8_OK : cuda_error("kernel launch", e);
+}
+
+extern "C" w8a8_status w8a8_quantize_int8_per_token(const void *X_dev, w8a8_in_dtype x_dtype,
+                                                    int64_t ld_x, void *A_dev, int64_t ld_a,
+                                                    float *a_s_dev, int64_t M, int64_t K,
+                                                    w8a8_stream_t stream)
+{
+    using namespace w8a8;
+    if (M < 0 || K < 0)
+        return record_error(W8A8_ERR_INVALID_ARG, "negative size");
+    if (x_dtype < W8A8_IN_BF16 || x_dtype > W8A8_IN_FP32)
+        return record_error(W8A8_ERR_INVALID_ARG, "unknown input dtype");
+    ld_x = ld_x ? ld_x : K;
+    ld_a = ld_a ? ld_a : K;
+    if (ld_x < K || ld_a < K)
+        return record_error(W8A8_ERR_INVALID_ARG, "a row stride is shorter than its row");
+    if (M == 0 || K == 0)
+        return W8A8_OK;
+    if (!X_dev || !A_dev || !a_s_dev)
+        return record_error(W8A8_ERR_INVALID_ARG, "null pointer argument");
+    if (M > (1ll << 31) - 1 || K > (1ll << 30))
+        return record_error(W8A8_ERR_UNSUPPORTED, "M of 2^31 or more, or K above 2^30");
+    const int xb = x_dtype == W8A8_IN_FP32 ? 4 : 2;
+    if (!on(X_dev, xb) || !on(a_s_dev, 4))
+        return record_error(W8A8_ERR_UNSUPPORTED, "a pointer is not aligned to its element size");
+    const bool vec = K % 8 == 0 && on(X_dev, 16) && on(A_dev, 8) && ld_x * xb % 16 == 0 && ld_a % 8 == 0;
+    QuantParams p = {};
+    p.X = X_dev;
+    p.A = static_cast<uint8_t *>(A_dev);
+    p.a_s = a_s_dev;
+    p.M = M;
+    p.K = static_cast<int>(K);
+    p.ld_x = ld_x;
+    p.ld_a = ld_a;
+    if (W8A8_DEBUG_BOUNDS && status_word_address(&p.status) != cudaSuccess)
+        p.status = nullptr;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = x_dtype == W8A8_IN_BF16   ? launch_quant<W8A8_IN_BF16>(p, vec, s)
+                          : x_dtype == W8A8_IN_FP16 ? launch_quant<W8A8_IN_FP16>(p, vec, s)
+                                                    : launch_quant<W8A8_IN_FP32>(p, vec, s);
+    return e == cudaSuccess ? W8A8_OK : cuda_error("kernel launch", e);
+}

@@ -406,6 +406,8 @@ size_t w8a8_block_fp8_quant_matmul_workspace_size(int64_t M, int64_t N, int64_t 
  *   rows of C are unspecified.  Ids outside [-1, E) give unspecified results
  *   but never an out-of-bounds access.  opts: variant AUTO or TILED.
  *
+ * (A third layout, ragged, has its own declaration below.)
+ *
  * Shape rules are those of the plain call (K % 16, N % 8 or 4, alignment),
  * plus E * rows < 2^31 and E <= 65535 (masked: E x token tiles <= 65535).
  * E == 0 (masked) or max_m == 0 or M == 0 is a no-op.  Errors as for
@@ -426,6 +428,114 @@ w8a8_status w8a8_block_fp8_grouped_matmul_contiguous(const void *A_dev, const fl
                                                      w8a8_out_dtype out_dtype,
                                                      w8a8_stream_t stream,
                                                      const w8a8_options *opts);
+
+/*
+ * Ragged layout: as the contiguous one, with no padding between the experts.
+ *   A_dev [M, K], a_s_dev [M, ceil(K/128)], C_dev [M, N]: the rows of expert 0,
+ *   then those of expert 1, ...; B_dev [E, N, K], b_s_dev [E, ceil(N/128), ceil(K/128)];
+ *   offsets_dev int32 [E + 1], 4-byte aligned: expert e has the rows
+ *   offsets[e] .. offsets[e+1]-1 (none where the two are equal).
+ * Like the other layouts' routing, the offsets are read on the device after the
+ * earlier work on the stream.  Rows before offsets[0] and from offsets[E] on
+ * belong to no expert: their rows of C are left as they are.  Offsets that
+ * decrease or leave [0, M] give unspecified results but never an out-of-bounds
+ * access.  E <= W8A8_RAGGED_MAX_EXPERTS; M == 0 is a no-op, E == 0 with rows is
+ * W8A8_ERR_INVALID_ARG; other shape rules as for the plain tensor-core call.
+ * One kernel for every routing, from one row to full prefill; no workspace.
+ * opts: variant AUTO or TILED; block_n_tile 128 or 256, grid_limit, pdl,
+ * wait_limit_cycles and the test hooks apply.
+ */
+#define W8A8_RAGGED_MAX_EXPERTS 1024
+w8a8_status w8a8_block_fp8_grouped_matmul_ragged(const void *A_dev, const float *a_s_dev,
+                                                 const void *B_dev, const float *b_s_dev,
+                                                 void *C_dev, const int32_t *offsets_dev,
+                                                 int64_t M, int64_t E, int64_t N, int64_t K,
+                                                 int block_n, int block_k,
+                                                 w8a8_out_dtype out_dtype, w8a8_stream_t stream,
+                                                 const w8a8_options *opts);
+
+/*
+ * INT8 matmul with one scale per token and per output channel:
+ *
+ *   C[m,n] = cast_out( a_s[m] * b_s[n] * sum_k A[m,k] * B[n,k] )
+ *
+ *   A_dev   INT8 [M, lda], the first K of each row used; a_s_dev fp32 [M]
+ *   B_dev   INT8 [N, ldb], the first K of each row used; b_s_dev fp32 [N]
+ *   C_dev   [M, ldc] of out_dtype, the first N written
+ * A stride of 0 means the dense value.  Any M, N >= 0 and 0 <= K <=
+ * W8A8_INT8_MAX_K, any strides and alignments (C to its element size, scales to
+ * 4 bytes); M == 0 or N == 0 is a no-op, K == 0 gives zeros.  The sum is exact
+ * over the whole INT8 range; it is converted to fp32, multiplied by a_s, then by
+ * b_s, and cast (each rounded to nearest even).
+ * Workspace: w8a8_int8_workspace_size() bytes from opts->workspace_dev, or the
+ * library's for this stream, under the rules of the split-K workspace.
+ * opts: variant AUTO, TILED (128 x 128 tiles) or TILED_PAIR (CTA pairs, 256 x
+ * 256); grid_limit, wait_limit_cycles, workspace and the test hooks apply.  The
+ * launches of a call wait on the device for the work before them on the stream,
+ * whatever opts->pdl says.
+ */
+#define W8A8_INT8_MAX_K 131071
+w8a8_status w8a8_int8_matmul(const void *A_dev, int64_t lda, const float *a_s_dev,
+                             const void *B_dev, int64_t ldb, const float *b_s_dev, void *C_dev,
+                             int64_t ldc, int64_t M, int64_t N, int64_t K,
+                             w8a8_out_dtype out_dtype, w8a8_stream_t stream,
+                             const w8a8_options *opts);
+
+/* Device scratch (bytes) that w8a8_int8_matmul takes for this problem (0 for none,
+ * or bad sizes). */
+size_t w8a8_int8_workspace_size(int64_t M, int64_t N, int64_t K, const w8a8_options *opts);
+
+/*
+ * Per-token INT8 quantiser, which makes the INT8 matmul's A and a_s:
+ *
+ *   a_s[m] = max_k |X[m,k]| / 127   (fp32 quotient; 1 where it is 0)
+ *   A[m,k] = X[m,k] / a_s[m]        (fp32 quotient) rounded to the nearest whole
+ *                                   number, ties to even; -127..127
+ *
+ *   X_dev [M, ld_x] of x_dtype, A_dev INT8 [M, ld_a]; strides in elements, 0 =
+ *   dense (K); any K up to 2^30 and alignments (X to its element size).  M == 0
+ *   or K == 0 is a no-op.  X must not overlap A, and must be finite: a row with a
+ *   NaN or an infinity gets unspecified codes and scale.
+ */
+w8a8_status w8a8_quantize_int8_per_token(const void *X_dev, w8a8_in_dtype x_dtype, int64_t ld_x,
+                                         void *A_dev, int64_t ld_a, float *a_s_dev, int64_t M,
+                                         int64_t K, w8a8_stream_t stream);
+
+/*
+ * Sandwich norm: what stands between two blocks of a transformer that has norms
+ * before and after each block -- the norm of the finished block's output h, its
+ * gate, the residual sum, and the norm before the next block -- in one pass:
+ *
+ *   u = h / sqrt(mean(h^2) + eps) * w_post         (w_post NULL: u = h)
+ *   r = res_scale * x + gate[m / gate_rows] * u    (gate NULL: r = res_scale * x + u)
+ *   y = r / sqrt(mean(r^2) + eps) * w_pre          (w_pre NULL: y = r)
+ *
+ * for each of M rows of D columns, in fp32, with one rounding per output (y is
+ * made from the fp32 r).
+ *   h_dev [M, ld_h] of h_dtype; x_dev [M, ld_x] of x_dtype (h's type or fp32);
+ *   w_post, w_pre [D] and gate [ceil(M / gate_rows), D] dense, of h_dtype (a gate
+ *   for all tokens: gate_rows >= M; for each: 1; for sequences: their length).
+ *   x_out_dev [M, ld_xo] of x_dtype: r; may be x_dev (with its stride) or NULL.
+ *   y_dev [M, ld_y] by y_kind:
+ *     W8A8_NORM_SAME  y in h_dtype; may be h_dev (with its stride)
+ *     W8A8_NORM_FP8   E4M3 codes, scales_dev [M, ceil(D/128)]: y quantised as
+ *                     w8a8_quantize_fp8_per_token_group does (D % 16 == 0, rows on
+ *                     16-byte boundaries, y's on 8-byte ones)
+ *     W8A8_NORM_INT8  INT8 codes, scales_dev [M]: as w8a8_quantize_int8_per_token
+ * Strides in elements, 0 = dense (D).  D <= W8A8_NORM_MAX_D.  M == 0 or D == 0 is a
+ * no-op.  Other overlaps of inputs and outputs are not allowed.  NaN and infinity
+ * pass into r and y; with 8-bit codes they leave their row's codes and scales
+ * unspecified.  h^2 and r^2 are summed in fp32: they overflow for magnitudes
+ * near 1e19.
+ */
+typedef enum { W8A8_NORM_SAME = 0, W8A8_NORM_FP8 = 1, W8A8_NORM_INT8 = 2 } w8a8_norm_out;
+#define W8A8_NORM_MAX_D 57344
+w8a8_status w8a8_sandwich_norm(const void *h_dev, w8a8_in_dtype h_dtype, int64_t ld_h,
+                               const void *x_dev, w8a8_in_dtype x_dtype, int64_t ld_x,
+                               const void *w_post_dev, const void *gate_dev, int64_t gate_rows,
+                               const void *w_pre_dev, float res_scale, float eps, void *x_out_dev,
+                               int64_t ld_xo, void *y_dev, float *scales_dev, w8a8_norm_out y_kind,
+                               int64_t ld_y, int64_t M, int64_t D, w8a8_stream_t stream);
 
 /*
  * Per-token-group FP8 quantiser: makes the matmul's activation operand A and

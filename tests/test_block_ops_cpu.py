@@ -1,0 +1,115 @@
+"""Refusals of the ragged, INT8 and norm entry points: every one comes before any
+CUDA call, so they are checked without a GPU, by status and message."""
+import pytest
+import torch
+
+import block_scaled_fp8_w8a8_gb300 as w8
+from block_scaled_fp8_w8a8_gb300 import build
+
+OK, ARG, UNS = w8.W8A8_OK, w8.W8A8_ERR_INVALID_ARG, w8.W8A8_ERR_UNSUPPORTED
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    build.build()
+    return w8.load_library()
+
+
+def ragged(M=8, E=2, N=128, K=256, out=0, bn=128, bk=128, opts=None, **ptr):
+    p = dict(A=256, a_s=256, B=256, b_s=256, C=256, off=256)
+    p.update(ptr)
+    return w8.w8a8_block_fp8_grouped_matmul_ragged(p["A"], p["a_s"], p["B"], p["b_s"], p["C"], p["off"], M, E, N, K,
+                                                   bn, bk, out, 0, opts)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(M=-1), ARG), (dict(N=-8), ARG), (dict(E=-1), ARG), (dict(E=0), ARG), (dict(out=3), ARG),
+    (dict(A=0), ARG), (dict(off=0), ARG), (dict(C=0), ARG), (dict(M=0), OK), (dict(bn=64), UNS), (dict(K=250), UNS),
+    (dict(K=8), UNS), (dict(N=132), UNS), (dict(N=130, out=2), UNS), (dict(A=264), UNS), (dict(off=258), UNS),
+    (dict(E=w8.W8A8_RAGGED_MAX_EXPERTS + 1), UNS), (dict(M=1 << 31), UNS), (dict(M=(1 << 31) - 1, N=1 << 20), UNS),
+    (dict(opts=w8.options(variant=w8.W8A8_VARIANT_SWAPAB)), UNS),
+    (dict(opts=w8.options(variant=99)), ARG), (dict(opts=w8.options(wait_limit_cycles=5)), ARG),
+])
+def test_ragged(kw, status):
+    assert ragged(**kw) == status
+    assert (w8.w8a8_last_error() != "") == (status != OK)
+
+
+def int8(M=4, N=8, K=16, out=0, lda=0, ldb=0, ldc=0, opts=None, **ptr):
+    p = dict(A=256, a_s=256, B=256, b_s=256, C=256)
+    p.update(ptr)
+    return w8.w8a8_int8_matmul(p["A"], lda, p["a_s"], p["B"], ldb, p["b_s"], p["C"], ldc, M, N, K, out, 0, opts)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(M=-1), ARG), (dict(N=-1), ARG), (dict(K=-1), ARG), (dict(out=-1), ARG), (dict(lda=15), ARG),
+    (dict(ldb=1), ARG), (dict(ldc=7), ARG), (dict(A=0), ARG), (dict(b_s=0), ARG), (dict(C=0), ARG), (dict(M=0), OK),
+    (dict(N=0, C=0), OK), (dict(K=w8.W8A8_INT8_MAX_K + 1), UNS), (dict(C=257), UNS), (dict(C=258, out=2), UNS),
+    (dict(a_s=258), UNS), (dict(M=1 << 31), UNS), (dict(opts=w8.options(variant=w8.W8A8_VARIANT_SPLITK)), UNS),
+    (dict(opts=w8.options(stages=9)), ARG),
+])
+def test_int8(kw, status):
+    assert int8(**kw) == status
+
+
+def test_int8_workspace_size():
+    size = w8.w8a8_int8_workspace_size
+    assert size(-1, 8, 8) == 0 and size(0, 8, 8) == 0 and size(4, 8, w8.W8A8_INT8_MAX_K + 1) == 0
+    # large problems are cut: the workspace does not grow with M without end
+    assert size(1 << 20, 4096, 4096) == size(1 << 22, 4096, 4096) < 1 << 30
+
+
+def quant(M=4, K=16, kind=0, ld_x=0, ld_a=0, X=256, A=256, s=256):
+    return w8.w8a8_quantize_int8_per_token(X, kind, ld_x, A, ld_a, s, M, K, 0)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(M=-1), ARG), (dict(K=-1), ARG), (dict(kind=3), ARG), (dict(ld_x=15), ARG), (dict(ld_a=3), ARG),
+    (dict(X=0), ARG), (dict(s=0), ARG), (dict(M=0), OK), (dict(K=0), OK), (dict(X=257), UNS), (dict(s=258), UNS),
+    (dict(X=258, kind=2), UNS), (dict(K=(1 << 30) + 1), UNS), (dict(M=1 << 31), UNS),
+])
+def test_quantiser(kw, status):
+    assert quant(**kw) == status
+
+
+def norm(M=4, D=32, hk=0, xk=0, ld_h=0, ld_x=0, gate=0, gate_rows=1, ld_xo=0, kind=0, ld_y=0, **ptr):
+    p = dict(h=256, x=256, w_post=256, w_pre=256, x_out=256, y=256, s=256)
+    p.update(ptr)
+    return w8.w8a8_sandwich_norm(p["h"], hk, ld_h, p["x"], xk, ld_x, p["w_post"], gate, gate_rows, p["w_pre"], 1.0,
+                                 1e-6, p["x_out"], ld_xo, p["y"], p["s"], kind, ld_y, M, D, 0)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(M=-1), ARG), (dict(D=-1), ARG), (dict(hk=3), ARG), (dict(xk=-1), ARG), (dict(kind=3), ARG),
+    (dict(gate=256, gate_rows=0), ARG), (dict(ld_h=31), ARG), (dict(ld_y=1), ARG), (dict(h=0), ARG), (dict(y=0), ARG),
+    (dict(kind=1, s=0), ARG), (dict(M=0), OK), (dict(D=0), OK), (dict(hk=0, xk=1), UNS), (dict(hk=2, xk=0), UNS),
+    (dict(D=w8.W8A8_NORM_MAX_D + 1), UNS), (dict(M=1 << 31), UNS), (dict(h=257), UNS), (dict(s=258, kind=2), UNS),
+    (dict(kind=1, D=24), UNS), (dict(kind=1, h=258), UNS), (dict(kind=1, ld_x=33), UNS),
+])
+def test_norm(kw, status):
+    assert norm(**kw) == status
+
+
+def test_python_wrappers_refuse_shapes_and_types():
+    e8 = lambda *s: torch.zeros(s, dtype=torch.int8)  # noqa: E731
+    f = torch.zeros
+    for call in (
+        lambda: w8.int8_matmul(e8(4, 16).float(), f(4), e8(8, 16), f(8)),
+        lambda: w8.int8_matmul(e8(4, 16), f(5), e8(8, 16), f(8)),
+        lambda: w8.int8_matmul(e8(4, 16), f(4), e8(8, 17), f(8)),
+        lambda: w8.int8_matmul(e8(16, 4).t(), f(4), e8(8, 16), f(8)),
+        lambda: w8.int8_matmul(e8(4, 16), f(4), e8(8, 16), f(8), out=f(4, 9)),
+        lambda: w8.quantize_int8_per_token(e8(4, 16)),
+        lambda: w8.quantize_int8_per_token(f(4, 16), A=e8(4, 15)),
+        lambda: w8.grouped_matmul_ragged(e8(4, 128), f(4, 1), e8(2, 8, 128), f(2, 1, 1), torch.zeros(2, dtype=torch.int32)),
+        lambda: w8.grouped_matmul_ragged(e8(4, 128), f(4, 2), e8(2, 8, 128), f(2, 1, 1), torch.zeros(3, dtype=torch.int32)),
+        lambda: w8.grouped_matmul_ragged(e8(4, 128), f(4, 1), e8(2, 8, 64), f(2, 1, 1), torch.zeros(3, dtype=torch.int32)),
+        lambda: w8.sandwich_norm(f(4, 8), f(4, 9)),
+        lambda: w8.sandwich_norm(f(4, 8), f(4, 8), w_post=f(9)),
+        lambda: w8.sandwich_norm(f(4, 8), f(4, 8), w_pre=f(8).half()),
+        lambda: w8.sandwich_norm(f(4, 8), f(4, 8), gate=f(1, 8), gate_rows=2),
+        lambda: w8.sandwich_norm(f(4, 8), f(4, 8), x_out=f(4, 8).half()),
+        lambda: w8.sandwich_norm(f(8, 4).t(), f(4, 8)),
+    ):
+        with pytest.raises(w8.W8A8Error):
+            call()

@@ -1,0 +1,195 @@
+"""GPU: the INT8 matmul and its per-token quantiser.
+
+The sum of the products is a whole number and exact, and what follows is three
+fp32 roundings in a fixed order, so the matmul's results are compared bit for
+bit: fp32(sum) * a_s * b_s, then the cast.  The quantiser's quotients are
+correctly rounded fp32 ones: its codes and scales are compared bit for bit too."""
+import numpy as np
+import pytest
+import torch
+
+import block_scaled_fp8_w8a8_gb300 as w8
+
+pytestmark = pytest.mark.gpu
+
+OUT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+
+
+def make(M, N, K, seed, lo=-128, hi=127):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    codes = lambda *s: torch.randint(lo, hi + 1, s, generator=g, device="cuda", dtype=torch.int8)  # noqa: E731
+    rnd = lambda n: 1e-3 * (0.1 + torch.rand(n, generator=g, device="cuda"))  # noqa: E731
+    return codes(M, K), rnd(M), codes(N, K), rnd(N)
+
+
+def reference(A, a_s, B, b_s, out):
+    """Sums in fp64 (whole numbers below 2^53: exact), then the fp32 steps."""
+    s = (A.double() @ B.double().t()).float()
+    return (s * a_s[:, None] * b_s).to(OUT[out])
+
+
+def assert_same(got, want, what=""):
+    bad = (got != want).sum().item()
+    assert bad == 0, f"{what}: {bad} of {want.numel()} differ"
+
+
+SIZES = [(1, 1, 1), (1, 128, 64), (3, 64, 16), (7, 130, 100), (16, 512, 256), (33, 1537, 1000), (64, 256, 4096),
+         (100, 96, 513), (128, 128, 512), (129, 257, 1040), (257, 1000, 777), (300, 520, 2048), (1025, 768, 320),
+         (2048, 1536, 1024)]
+
+
+@pytest.mark.parametrize("M,N,K", SIZES)
+@pytest.mark.parametrize("out", ["bf16", "fp16", "fp32"])
+def test_parity(M, N, K, out):
+    x = make(M, N, K, seed=M + N + K)
+    C = w8.int8_matmul(*x, out)
+    torch.cuda.synchronize()
+    assert w8.w8a8_get_device_status()[0] == w8.W8A8_OK
+    assert_same(C, reference(*x, out), f"{M} {N} {K} {out}")
+
+
+@pytest.mark.parametrize("variant", [w8.W8A8_VARIANT_TILED, w8.W8A8_VARIANT_TILED_PAIR])
+@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (40, 70, 65), (300, 520, 1100), (513, 768, 2048)])
+def test_forced_kernels(M, N, K, variant):
+    x = make(M, N, K, seed=3)
+    for grid in (0, 4):
+        C = w8.int8_matmul(*x, "fp32", variant=variant, grid_limit=grid)
+        assert_same(C, reference(*x, "fp32"), f"{variant} {grid}")
+
+
+@pytest.mark.parametrize("K", [512, 513, 4096, 20000, w8.W8A8_INT8_MAX_K])
+@pytest.mark.parametrize("M", [2, 40, 130])
+def test_largest_sums_are_exact(M, K):
+    """Every product 2^14, the most any can be: the accumulators and their
+    running total reach their limits; one operand off by one shows a lost unit."""
+    A = torch.full((M, K), -128, dtype=torch.int8, device="cuda")
+    B = torch.full((136, K), -128, dtype=torch.int8, device="cuda")
+    A[1, K // 2], B[5, K - 1] = 127, -127
+    one = lambda n: torch.ones(n, device="cuda")  # noqa: E731
+    s = (A.double() @ B.double().t())
+    C = w8.int8_matmul(A, one(M), B, one(136), "fp32")
+    assert_same(C, s.float())
+    for variant in (w8.W8A8_VARIANT_TILED, w8.W8A8_VARIANT_TILED_PAIR):
+        assert_same(w8.int8_matmul(A, one(M), B, one(136), "fp32", variant=variant), s.float())
+
+
+def test_every_unit_of_a_large_sum_counts():
+    """Sums around 2^23 whose last units differ, read through scales of one."""
+    K = 1024
+    A = torch.full((64, K), 127, dtype=torch.int8, device="cuda")
+    B = torch.full((128, K), 64, dtype=torch.int8, device="cuda")
+    B[:, 0] = torch.arange(128, device="cuda", dtype=torch.int8)
+    A[:, 0] = torch.arange(64, device="cuda", dtype=torch.int8) - 32
+    one = lambda n: torch.ones(n, device="cuda")  # noqa: E731
+    assert_same(w8.int8_matmul(A, one(64), B, one(128), "fp32"), (A.double() @ B.double().t()).float())
+
+
+def test_strided_and_misaligned_operands_and_memory_around_c():
+    for off, pad in ((0, 16), (4, 4), (1, 3), (0, 0)):
+        M, N, K = 37, 83, 200
+        a = torch.randint(-128, 128, (off + (M + 1) * (K + pad),), device="cuda", dtype=torch.int8)
+        b = torch.randint(-128, 128, (off + (N + 1) * (K + pad),), device="cuda", dtype=torch.int8)
+        A = a[off:off + M * (K + pad)].view(M, K + pad)[:, :K]
+        B = b[off:off + N * (K + pad)].view(N, K + pad)[:, :K]
+        a_s, b_s = torch.rand(M + 1, device="cuda")[1:], torch.rand(N + 1, device="cuda")[1:]
+        for out in ("bf16", "fp32"):
+            buf = torch.full(((M + 2) * (N + pad) + 64,), 7.0, dtype=OUT[out], device="cuda")
+            C = buf[off:off + M * (N + pad)].view(M, N + pad)[:, :N]
+            w8.int8_matmul(A, a_s, B, b_s, out, out=C)
+            assert_same(C, reference(A, a_s, B, b_s, out))
+            C.fill_(7.0)
+            assert (buf == 7).all()
+
+
+def test_no_columns_gives_zeros_and_no_rows_nothing():
+    z = lambda *s: torch.zeros(s, dtype=torch.int8, device="cuda")  # noqa: E731
+    C = w8.int8_matmul(z(3, 0), torch.ones(3, device="cuda"), z(5, 0), torch.ones(5, device="cuda"), "fp32",
+                       out=torch.full((3, 5), 9.0, device="cuda"))
+    assert (C == 0).all()
+    assert w8.int8_matmul(z(0, 8), torch.ones(0, device="cuda"), z(5, 8), torch.ones(5, device="cuda")).shape == (0, 5)
+
+
+def test_callers_workspace_and_capture():
+    x = make(200, 300, 700, seed=4)
+    need = w8.w8a8_int8_workspace_size(200, 300, 700)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    C = torch.zeros(200, 300, dtype=torch.bfloat16, device="cuda")
+    opts = dict(workspace_dev=ws.data_ptr(), workspace_bytes=need)
+    w8.int8_matmul(*x, out=C, stream=s, **opts)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        w8.int8_matmul(*x, out=C, stream=s, **opts)
+    x[0].copy_(make(200, 300, 700, seed=5)[0])
+    g.replay()
+    torch.cuda.synchronize()
+    assert_same(C, reference(*x, "bf16"))
+    with pytest.raises(w8.W8A8Error) as e:
+        w8.int8_matmul(*x, workspace_dev=ws.data_ptr(), workspace_bytes=need - 256)
+    assert e.value.status == w8.W8A8_ERR_WORKSPACE
+
+
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right():
+    x = make(300, 520, 1100, seed=6)
+    for variant in (w8.W8A8_VARIANT_TILED, w8.W8A8_VARIANT_TILED_PAIR):
+        w8.int8_matmul(*x, variant=variant, debug_skip_load=5, wait_limit_cycles=2_000_000)
+        assert w8.w8a8_get_device_status()[0] == w8.W8A8_ERR_DEVICE_TIMEOUT
+        assert_same(w8.int8_matmul(*x, variant=variant), reference(*x, "bf16"))
+        assert w8.w8a8_get_device_status()[0] == w8.W8A8_OK
+
+
+def quant_reference(X):
+    x = X.float().cpu().numpy()
+    s = (np.abs(x).max(1) / np.float32(127)).astype(np.float32)
+    s[s == 0] = 1
+    q = np.clip(np.rint(x / s[:, None]), -127, 127).astype(np.int8)
+    return q, s
+
+
+@pytest.mark.parametrize("M,K", [(1, 1), (3, 7), (5, 64), (33, 512), (9, 513), (17, 1000), (65, 4096), (2, 16384),
+                                 (2, 16392), (3, 20001)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_quantiser(M, K, dtype):
+    g = torch.Generator(device="cuda").manual_seed(M * K)
+    X = torch.randn((M, K), generator=g, device="cuda")
+    X[:, K // 2] *= 40
+    X[0] = 0 if M > 1 else X[0]
+    X = X.to(OUT[dtype])
+    q, s = w8.quantize_int8_per_token(X)
+    want_q, want_s = quant_reference(X)
+    assert np.array_equal(s.cpu().numpy().view(np.uint32), want_s.view(np.uint32))
+    assert np.array_equal(q.cpu().numpy(), want_q)
+
+
+def test_quantiser_extremes_and_strides():
+    """Rows of tiny, huge and tied values; rows of a wider buffer."""
+    X = torch.zeros(6, 264, device="cuda")
+    X[0] = 1e-44
+    X[1, :3] = torch.tensor([3e38, -3e38, 1e38])
+    X[2] = torch.arange(264, device="cuda") - 127.5                 # quotients in halves
+    X[3, 5] = 1e-45
+    X[4] = torch.arange(264, device="cuda") * 2.0 ** -130
+    wide = torch.randn(6, 300, device="cuda")
+    wide[:, 8:272] = X
+    for src in (X, wide[:, 8:272], wide[:, 7:271]):
+        out = torch.full((6, 280), 9, dtype=torch.int8, device="cuda")
+        q, s = w8.quantize_int8_per_token(src, A=out[:, 3:267])
+        want_q, want_s = quant_reference(src)
+        assert np.array_equal(s.cpu().numpy(), want_s)
+        assert np.array_equal(q.cpu().numpy(), want_q)
+        assert (out[:, :3] == 9).all() and (out[:, 267:] == 9).all()
+
+
+def test_from_activations():
+    """Quantise and multiply, back to back on a side stream."""
+    X = torch.randn(77, 1000, device="cuda", dtype=torch.bfloat16)
+    _, _, B, b_s = make(1, 400, 1000, seed=7)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    A, a_s = w8.quantize_int8_per_token(X, stream=s)
+    C = w8.int8_matmul(A, a_s, B, b_s, "fp16", stream=s)
+    s.synchronize()
+    q, sc = quant_reference(X)
+    assert_same(C, reference(torch.from_numpy(q).cuda(), torch.from_numpy(sc).cuda(), B, b_s, "fp16"))
