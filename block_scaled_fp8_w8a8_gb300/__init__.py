@@ -178,6 +178,42 @@ def quant_matmul(X, B, b_s, out_dtype="bf16", out=None, stream=None, **opts):
     return out
 
 
+def _want(t, shape, name):
+    if t.shape != shape:
+        raise W8A8Error(W8A8_ERR_INVALID_ARG,
+                        f"{name} has shape {tuple(t.shape)}, want {tuple(shape)}")
+
+
+def _dense(t, name):
+    if not t.is_contiguous():
+        raise W8A8Error(W8A8_ERR_UNSUPPORTED, f"{name} must be contiguous")
+
+
+def _rows(t):
+    """Row stride of a 2-D tensor whose rows are contiguous, 0 for a dense one."""
+    if t.is_contiguous():
+        return 0
+    if t.size(1) > 1 and t.stride(1) != 1:
+        raise W8A8Error(W8A8_ERR_UNSUPPORTED, "each row must be contiguous (unit stride)")
+    if t.size(0) > 1 and t.stride(0) < t.size(1):
+        raise W8A8Error(W8A8_ERR_UNSUPPORTED, "rows must not overlap")
+    return t.stride(0) if t.size(0) > 1 else 0
+
+
+def _in_code(dtype):
+    import torch
+    if not _IN_CODES:
+        _IN_CODES.update({torch.bfloat16: W8A8_IN_BF16, torch.float16: W8A8_IN_FP16,
+                          torch.float32: W8A8_IN_FP32})
+    code = _IN_CODES.get(dtype)
+    if code is None:
+        raise W8A8Error(W8A8_ERR_INVALID_ARG, f"unsupported input dtype {dtype}")
+    return code
+
+
+_IN_CODES = {}
+
+
 def grouped_matmul_ragged(A, a_s, B, b_s, offsets, out_dtype="bf16", out=None, stream=None,
                           **opts):
     """Grouped matmul, ragged layout, on CUDA tensors: A [M, K], a_s [M, ceil(K/128)],
@@ -185,43 +221,24 @@ def grouped_matmul_ragged(A, a_s, B, b_s, offsets, out_dtype="bf16", out=None, s
     rows are offsets[e] .. offsets[e+1]-1; read on the device).  Returns C [M, N];
     rows of no expert are left as they are in ``out`` (unspecified without it)."""
     M, K = A.shape
-    E, N = B.shape[0], B.shape[1]
+    E, N, Kb = B.shape
     code = out_code(out_dtype)
+    G = (K + 127) // 128
+    if Kb != K:
+        raise W8A8Error(W8A8_ERR_INVALID_ARG, f"B has {Kb} columns, A {K}")
+    _want(a_s, (M, G), "a_s")
+    _want(b_s, (E, (N + 127) // 128, G), "b_s")
+    _want(offsets, (E + 1,), "offsets")
     if out is None:
         out = _out_tensor((M, N), code, A.device)
-    for t in (A, a_s, B, b_s, out, offsets):
-        if not t.is_contiguous():
-            raise W8A8Error(W8A8_ERR_UNSUPPORTED, "tensors must be contiguous row-major")
-    _want(a_s, (M, (K + 127) // 128), "a_s")
-    _want(b_s, (E, (N + 127) // 128, (K + 127) // 128), "b_s")
-    _want(offsets, (E + 1,), "offsets")
-    _want(out, (M, N), "out")
-    if B.shape[2] != K:
-        raise W8A8Error(W8A8_ERR_INVALID_ARG, f"B has {B.shape[2]} columns, A {K}")
+    else:
+        _want(out, (M, N), "out")
+    if not (A.is_contiguous() and a_s.is_contiguous() and B.is_contiguous() and
+            b_s.is_contiguous() and out.is_contiguous() and offsets.is_contiguous()):
+        raise W8A8Error(W8A8_ERR_UNSUPPORTED, "tensors must be contiguous row-major")
     check(w8a8_block_fp8_grouped_matmul_ragged(A, a_s, B, b_s, out, offsets, M, E, N, K, 128, 128,
                                                code, stream, options(**opts) if opts else None))
     return out
-
-
-def _want(t, shape, name):
-    if t.shape != shape:
-        raise W8A8Error(W8A8_ERR_INVALID_ARG, f"{name} has shape {tuple(t.shape)}, want {shape}")
-
-
-def _rows(t):
-    """Row stride of a 2-D tensor whose rows are contiguous."""
-    if t.dim() != 2 or (t.size(1) > 1 and t.stride(1) != 1):
-        raise W8A8Error(W8A8_ERR_UNSUPPORTED, "each row must be contiguous (unit stride)")
-    return t.stride(0) if t.size(0) > 1 else t.size(1)
-
-
-def _in_code(dtype):
-    import torch
-    code = {torch.bfloat16: W8A8_IN_BF16, torch.float16: W8A8_IN_FP16,
-            torch.float32: W8A8_IN_FP32}.get(dtype)
-    if code is None:
-        raise W8A8Error(W8A8_ERR_INVALID_ARG, f"unsupported input dtype {dtype}")
-    return code
 
 
 def int8_matmul(A, a_s, B, b_s, out_dtype="bf16", out=None, stream=None, **opts):
@@ -233,16 +250,17 @@ def int8_matmul(A, a_s, B, b_s, out_dtype="bf16", out=None, stream=None, **opts)
     M, K = A.shape
     N = B.shape[0]
     code = out_code(out_dtype)
-    if A.dtype != torch.int8 or B.dtype != torch.int8:
+    if A.dtype is not torch.int8 or B.dtype is not torch.int8:
         raise W8A8Error(W8A8_ERR_INVALID_ARG, f"A and B must be int8, not {A.dtype}, {B.dtype}")
-    if out is None:
-        out = _out_tensor((M, N), code, A.device)
     _want(B, (N, K), "B")
     _want(a_s, (M,), "a_s")
     _want(b_s, (N,), "b_s")
-    _want(out, (M, N), "out")
-    if not a_s.is_contiguous() or not b_s.is_contiguous():
-        raise W8A8Error(W8A8_ERR_UNSUPPORTED, "scales must be contiguous")
+    if out is None:
+        out = _out_tensor((M, N), code, A.device)
+    else:
+        _want(out, (M, N), "out")
+    _dense(a_s, "a_s")
+    _dense(b_s, "b_s")
     check(w8a8_int8_matmul(A, _rows(A), a_s, B, _rows(B), b_s, out, _rows(out), M, N, K, code,
                            stream, options(**opts) if opts else None))
     return out
@@ -253,16 +271,18 @@ def quantize_int8_per_token(X, A=None, a_s=None, stream=None):
     stride along K): returns (A int8 [M, K], a_s float32 [M]), the INT8 matmul's
     activation operand.  ``A`` / ``a_s`` may be preallocated."""
     import torch
-    M, K = X.shape
+    shape = X.shape
+    M, K = shape
     code = _in_code(X.dtype)
     if A is None:
-        A = torch.empty((M, K), dtype=torch.int8, device=X.device)
+        A = torch.empty(shape, dtype=torch.int8, device=X.device)
+    else:
+        _want(A, shape, "A")
     if a_s is None:
         a_s = torch.empty(M, dtype=torch.float32, device=X.device)
-    _want(A, (M, K), "A")
-    _want(a_s, (M,), "a_s")
-    if not a_s.is_contiguous():
-        raise W8A8Error(W8A8_ERR_UNSUPPORTED, "scales must be contiguous")
+    else:
+        _want(a_s, (M,), "a_s")
+        _dense(a_s, "a_s")
     check(w8a8_quantize_int8_per_token(X, code, _rows(X), A, _rows(A), a_s, M, K, stream))
     return A, a_s
 
@@ -282,26 +302,30 @@ def sandwich_norm(h, x, w_post=None, w_pre=None, gate=None, gate_rows=None, res_
     (one scale per row) (r, codes, scales).  x_out may be x itself.  Raises W8A8Error
     on a non-zero status."""
     import torch
-    M, D = h.shape
-    hk, kind = _in_code(h.dtype), _NORM_KINDS[out]
+    shape = h.shape
+    M, D = shape
+    dtype = h.dtype
+    hk, kind = _in_code(dtype), _NORM_KINDS[out]
+    _want(x, shape, "x")
     if x_out is None:
-        x_out = torch.empty((M, D), dtype=x.dtype, device=x.device)
+        x_out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    else:
+        _want(x_out, shape, "x_out")
+        if x_out.dtype is not x.dtype:
+            raise W8A8Error(W8A8_ERR_INVALID_ARG, "x_out must have x's dtype")
     if y_out is None:
-        y_out = torch.empty((M, D), device=h.device,
-                            dtype=(h.dtype, torch.uint8, torch.int8)[kind])
+        y_out = torch.empty(shape, device=h.device, dtype=(dtype, torch.uint8, torch.int8)[kind])
+    else:
+        _want(y_out, shape, "y_out")
+        if kind == W8A8_NORM_SAME and y_out.dtype is not dtype or y_out.element_size() != 1 and kind:
+            raise W8A8Error(W8A8_ERR_INVALID_ARG, f"y_out of {y_out.dtype} for out={out!r}")
     if kind != W8A8_NORM_SAME:
-        shape = (M, (D + 127) // 128) if kind == W8A8_NORM_FP8 else (M,)
+        s_shape = (M, (D + 127) // 128) if kind == W8A8_NORM_FP8 else (M,)
         if scales_out is None:
-            scales_out = torch.empty(shape, dtype=torch.float32, device=h.device)
-        _want(scales_out, shape, "scales_out")
-        if not scales_out.is_contiguous():
-            raise W8A8Error(W8A8_ERR_UNSUPPORTED, "scales must be contiguous")
-    _want(x, (M, D), "x")
-    _want(x_out, (M, D), "x_out")
-    _want(y_out, (M, D), "y_out")
-    if x_out.dtype != x.dtype:
-        raise W8A8Error(W8A8_ERR_INVALID_ARG, "x_out must have x's dtype")
-    R = 1
+            scales_out = torch.empty(s_shape, dtype=torch.float32, device=h.device)
+        else:
+            _want(scales_out, s_shape, "scales_out")
+            _dense(scales_out, "scales_out")
     if gate is not None:
         R = gate.shape[0] if gate.dim() == 2 else 1
         if gate_rows is None:
@@ -309,13 +333,13 @@ def sandwich_norm(h, x, w_post=None, w_pre=None, gate=None, gate_rows=None, res_
         if gate.shape[-1] != D or gate_rows < 1 or R < -(-M // gate_rows):
             raise W8A8Error(W8A8_ERR_INVALID_ARG,
                             f"gate of {tuple(gate.shape)} for {M} rows of {D}, {gate_rows} to a gate")
-    for t, shape in ((w_post, (D,)), (w_pre, (D,)), (gate, None)):
-        if t is None:
-            continue
-        if shape is not None:
-            _want(t, shape, "weight")
-        if t.dtype != h.dtype or not t.is_contiguous():
-            raise W8A8Error(W8A8_ERR_UNSUPPORTED, "weights and gate must be contiguous, of h's dtype")
+    for t in (w_post, w_pre, gate):
+        if t is not None:
+            if t.dtype is not dtype or not t.is_contiguous():
+                raise W8A8Error(W8A8_ERR_UNSUPPORTED,
+                                "weights and gate must be contiguous, of h's dtype")
+            if t is not gate:
+                _want(t, (D,), "a norm's weight")
     check(w8a8_sandwich_norm(h, hk, _rows(h), x, _in_code(x.dtype), _rows(x), w_post, gate,
                              gate_rows or 1, w_pre, res_scale, eps, x_out, _rows(x_out), y_out,
                              scales_out, kind, _rows(y_out), M, D, stream))

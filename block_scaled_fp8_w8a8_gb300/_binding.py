@@ -182,19 +182,34 @@ def _ptr(x):
         return None
     if isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
-        return x.data_ptr()
+    get = getattr(x, "data_ptr", None)
+    if get is not None:
+        return get()
     if isinstance(x, ctypes.c_void_p):
         return x.value
     raise TypeError(f"cannot pass {type(x).__name__} as a pointer")
 
 
-def _stream(s):
-    if s is None:
+_current = None   # the current device's current stream, as a raw handle
+
+
+def _current_stream():
+    global _current
+    if _current is None:
         import torch
         if not torch.cuda.is_available():
             return 0   # the legacy default stream; the library reports the missing device
-        return torch.cuda.current_stream().cuda_stream
+        torch.cuda.current_stream()    # initialises CUDA
+        raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        # torch.cuda.current_stream().cuda_stream without the Stream object (0.2
+        # instead of 2.9 us a call, a quarter of a small kernel's launch)
+        _current = lambda: raw(device())  # noqa: E731
+    return _current()
+
+
+def _stream(s):
+    if s is None:
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream

@@ -1349,6 +1349,22 @@ int64_t host_chunk_rows(int64_t M, int64_t N, int64_t K, size_t ob, const w8a8_o
 namespace w8a8 {
 // Lets other translation units of the library report an error through
 // w8a8_last_error(); returns `st`.
+int device_view(DeviceView *out)
+{
+    w8a8_options scratch;
+    const w8a8_options *o = nullptr;
+    int dev;
+    DeviceInfo info;
+    w8a8_status st;
+    if ((st = with_env(nullptr, false, &scratch, &o)) != W8A8_OK ||
+        (st = current_device(&dev, &info)) != W8A8_OK)
+        return st;
+    out->sm_count = info.sm_count;
+    out->status = info.status;
+    out->wait_limit = o ? o->wait_limit_cycles : kDefaultWaitLimit;
+    return W8A8_OK;
+}
+
 w8a8_status record_error(w8a8_status st, const char *message)
 {
     return fail(st, "%s", message);

@@ -31,6 +31,7 @@ enum WaitSite : uint32_t {
     SITE_SMALL_WEIGHTS = 11,
     SITE_SWAP_QUANT = 12,
     SITE_PAIR_PEER = 13,   // CTA-pair kernel: waiting for the other CTA's stage
+    SITE_NORM_ROWS = 14,   // norm: a ring stage's rows
     // Access sites of the debug-bounds build's checks (status W8A8_ERR_DEVICE_BOUNDS).
     SITE_BOUNDS_A = 20,          // a TMA box or a load of A (or X) that starts outside it
     SITE_BOUNDS_B = 21,          // the same for B
@@ -290,5 +291,14 @@ cudaError_t ensure_smem_limit(Kernel kernel, volatile int *flags)
 
 // Device address of the per-device status word (for the current device).
 cudaError_t status_word_address(unsigned **out);
+
+// The current device's SM count, status word and the default bound of device
+// waits (cached); W8A8_OK or an error with its message recorded.
+struct DeviceView {
+    int sm_count;
+    unsigned *status;
+    unsigned long long wait_limit;
+};
+int device_view(DeviceView *out);      // a w8a8_status
 
 }  // namespace w8a8

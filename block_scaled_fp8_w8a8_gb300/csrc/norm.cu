@@ -188,6 +188,34 @@ struct NormParams {
     unsigned *status;
 };
 
+// The E4M3 codes of eight columns e .. e+7 of row m and their group's scale.
+// Sixteen neighbouring lanes hold one 128-column group; every lane of the warp
+// calls it (`in`: the columns exist).
+__device__ __forceinline__ void store_fp8(const NormParams &p, long long m, int e, bool in,
+                                          const float (&v)[8], float amax)
+{
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const float s = quant::group_scale(amax);
+    if (!in)
+        return;
+    const bool fast = s >= 0x1p-64f && s <= 0x1p64f;
+    const float rc = __frcp_rn(s);
+    const uint64_t ns2 = pack2f(-s, -s), y2 = pack2f(rc, rc);
+    uint32_t raw[8], c[2];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        raw[j] = __float_as_uint(v[j]);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        c[j] = fast ? quant::encode4<W8A8_IN_FP32, true>(raw, j, s, ns2, y2)
+                    : quant::encode4<W8A8_IN_FP32, false>(raw, j, s, ns2, y2);
+    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.y) + m * p.ld_y + e) = make_uint2(c[0], c[1]);
+    if ((lane_index() & 15) == 0)
+        p.scales[m * ((p.D + 127) / 128) + e / 128] = s;
+}
+
 // One row per CTA (per warp where row_threads is 32).  HELD: the row stays in
 // the threads' registers; otherwise in dynamic shared memory (D floats).
 template <int HK, int XK, int VEC, bool HELD>
@@ -302,33 +330,13 @@ __global__ void __launch_bounds__(kMaxThreads) k_sandwich_norm(const NormParams 
             if (in)
                 store_vec<HK, VEC>(static_cast<uint8_t *>(p.y) + m * p.ld_y * kHB, e, w);
         } else if (VEC == 8 && p.y_kind == W8A8_NORM_FP8) {
-            // Sixteen neighbouring lanes hold one 128-column group (T is a
-            // multiple of 16, so a group never straddles two steps).
             const int warp_first = at(i) - static_cast<int>(lane_index()) * VEC;
             if (warp_first < D) {            // the same for the whole warp
-                if (!in)
-                    amax = 0.f;
+                float w8[8];
 #pragma unroll
-                for (int o = 8; o > 0; o >>= 1)
-                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                const float s = quant::group_scale(amax);
-                if (in) {
-                    const bool fast = s >= 0x1p-64f && s <= 0x1p64f;
-                    const float rc = __frcp_rn(s);
-                    const uint64_t ns2 = pack2f(-s, -s), y2 = pack2f(rc, rc);
-                    uint32_t raw[8], c[2];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        raw[j] = __float_as_uint(w[VEC == 8 ? j : 0]);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        c[j] = fast ? quant::encode4<W8A8_IN_FP32, true>(raw, j, s, ns2, y2)
-                                    : quant::encode4<W8A8_IN_FP32, false>(raw, j, s, ns2, y2);
-                    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.y) + m * p.ld_y + e) =
-                        make_uint2(c[0], c[1]);
-                    if ((lane_index() & 15) == 0)
-                        p.scales[m * ((D + 127) / 128) + e / 128] = s;
-                }
+                for (int j = 0; j < 8; ++j)
+                    w8[j] = w[VEC == 8 ? j : 0];
+                store_fp8(p, m, e, in, w8, in ? amax : 0.f);
             }
             amax = 0.f;
         }
@@ -350,6 +358,184 @@ __global__ void __launch_bounds__(kMaxThreads) k_sandwich_norm(const NormParams 
         if (tid == 0)
             p.scales[m] = s;
     }
+}
+
+// ------------------------------------------------------------------ many rows
+
+// The same for many rows of at most 8192 columns, as a stream: persistent CTAs
+// walk the rows, each thread on the same eight columns of every row, so that
+// the norms' weights stay in its registers (the gate too, while its row lasts).
+// The rows of h and x come through a ring of shared-memory stages filled by
+// bulk copies, so that the loads of the next rows are in flight through a row's
+// two reductions.
+constexpr int kRingMaxStages = 4;
+
+struct RingParams {
+    NormParams n;
+    int stages;
+    uint32_t h_bytes, x_bytes;             // of one row
+    unsigned long long wait_limit;
+};
+
+template <int HK> __device__ __forceinline__ void raw_load(const void *row, int e, uint32_t (&w)[HK == W8A8_IN_FP32 ? 8 : 4])
+{
+    const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(row) +
+                                                     e * (HK == W8A8_IN_FP32 ? 4 : 2));
+#pragma unroll
+    for (int i = 0; i < (HK == W8A8_IN_FP32 ? 2 : 1); ++i) {
+        const uint4 a = __ldg(p + i);
+        w[4 * i] = a.x, w[4 * i + 1] = a.y, w[4 * i + 2] = a.z, w[4 * i + 3] = a.w;
+    }
+}
+
+template <int KIND>
+__device__ __forceinline__ void load_shared8(uint32_t addr, float (&v)[8])
+{
+    constexpr int kW = KIND == W8A8_IN_FP32 ? 8 : 4;
+    uint32_t w[kW];
+#pragma unroll
+    for (int i = 0; i < kW / 4; ++i)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
+                     : "r"(addr + 16u * i));
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        v[j] = quant::element<KIND>(w, j);
+}
+
+template <int HK, int XK>
+__global__ void __launch_bounds__(kMaxThreads, 1) k_sandwich_ring(const RingParams rp)
+{
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ float part[2][3][32];
+    __shared__ __align__(8) uint64_t bars[kRingMaxStages];
+    __shared__ int abort_word;
+    constexpr int kHB = HK == W8A8_IN_FP32 ? 4 : 2, kXB = XK == W8A8_IN_FP32 ? 4 : 2;
+    constexpr int kHW = HK == W8A8_IN_FP32 ? 8 : 4;
+    const NormParams &p = rp.n;
+    volatile int *abort_flag = &abort_word;
+    const int tid = static_cast<int>(threadIdx.x), e = 8 * tid, D = p.D;
+    const bool in = e < D;
+    const uint32_t ring0 = smem_addr(ring), bar0 = smem_addr(bars);
+    const uint32_t stage_bytes = rp.h_bytes + rp.x_bytes;
+    if (tid == 0) {
+        for (int s = 0; s < rp.stages; ++s)
+            mbar_init(bar0 + 8u * s, 1);
+        abort_word = 0;
+        mbar_fence_init();
+    }
+    __syncthreads();
+    const WaitGuard guard{abort_flag, p.status, rp.wait_limit};
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const long long first = blockIdx.x, stride = gridDim.x;
+    // (thread 0; after a timeout nothing more is copied)
+    uint32_t filled = 0, last_phase = 0;   // stages filled at all, and their last fills' parities
+    auto fill = [&](long long m, int s) {
+        if (*abort_flag || !in_bounds(m >= 0 && m < p.M, p.status, SITE_BOUNDS_A))
+            return;
+        last_phase = filled >> s & 1u ? last_phase ^ (1u << s) : last_phase;
+        filled |= 1u << s;
+        const uint32_t bar = bar0 + 8u * s, dst = ring0 + s * stage_bytes;
+        mbar_arrive_expect_tx(bar, stage_bytes);
+        bulk_load(dst, static_cast<const uint8_t *>(p.h) + m * p.ld_h * kHB, rp.h_bytes, bar);
+        bulk_load(dst + rp.h_bytes, static_cast<const uint8_t *>(p.x) + m * p.ld_x * kXB, rp.x_bytes,
+                  bar);
+    };
+    if (tid == 0)
+        for (int s = 0; s < rp.stages && first + s * stride < p.M; ++s)
+            fill(first + s * stride, s);
+
+    uint32_t wpost[kHW] = {}, wpre[kHW] = {}, wg[kHW] = {};
+    if (in) {
+        if (p.w_post)
+            raw_load<HK>(p.w_post, e, wpost);
+        if (p.w_pre)
+            raw_load<HK>(p.w_pre, e, wpre);
+    }
+    long long gate_now = -1;
+    int stage = 0, odd = 0;
+    uint32_t phase = 0;
+    for (long long m = first; m < p.M; m += stride, odd ^= 1) {
+        const long long g = p.gate ? m / p.gate_rows : -1;
+        if (g != gate_now && in)
+            raw_load<HK>(static_cast<const uint8_t *>(p.gate) + g * D * kHB, e, wg);
+        gate_now = g;
+        // A wait that runs out leaves garbage in the row, an entry in the
+        // status word and the abort flag, which ends every later wait at once.
+        wait_bounded(bar0 + 8u * stage, phase, guard, SITE_NORM_ROWS);
+        const uint32_t src = ring0 + stage * stage_bytes;
+        float v[8] = {}, x[8];
+        float ss = 0.f, inv = 1.f;
+        if (in) {
+            load_shared8<HK>(src + e * kHB, v);
+            load_shared8<XK>(src + rp.h_bytes + e * kXB, x);
+        }
+        if (p.w_post) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                ss = fmaf(v[j], v[j], ss);
+            inv = rsqrtf(row_reduce<Add>(ss, part[odd][0], false) / static_cast<float>(D) + p.eps);
+        }
+        ss = 0.f;
+        if (in) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float u = v[j];
+                if (p.w_post)
+                    u = u * inv * quant::element<HK>(wpost, j);
+                if (p.gate)
+                    u *= quant::element<HK>(wg, j);
+                v[j] = fmaf(p.res_scale, x[j], u);
+                ss = fmaf(v[j], v[j], ss);
+            }
+        }
+        inv = 1.f;
+        if (p.w_pre)
+            inv = rsqrtf(row_reduce<Add>(ss, part[odd][1], false) / static_cast<float>(D) + p.eps);
+        else
+            __syncthreads();
+        // Every thread has read its part of the stage: refill it.
+        if (tid == 0 && m + rp.stages * stride < p.M)
+            fill(m + rp.stages * stride, stage);
+        if (++stage == rp.stages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+        if (in && p.x_out)
+            store_vec<XK, 8>(static_cast<uint8_t *>(p.x_out) + m * p.ld_xo * kXB, e, v);
+        float amax = 0.f;
+        if (p.w_pre) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = v[j] * inv * quant::element<HK>(wpre, j);
+        }
+        if (p.y_kind == W8A8_NORM_SAME) {
+            if (in)
+                store_vec<HK, 8>(static_cast<uint8_t *>(p.y) + m * p.ld_y * kHB, e, v);
+            continue;
+        }
+        if (in) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                amax = fmaxf(amax, fabsf(v[j]));
+        }
+        if (p.y_kind == W8A8_NORM_FP8) {
+            store_fp8(p, m, e, in, v, amax);
+        } else {
+            const float s = int8_scale(row_reduce<Max>(amax, part[odd][2], false));
+            if (in)
+                store_int8<8>(static_cast<uint8_t *>(p.y) + m * p.ld_y + e, v, s);
+            if (tid == 0)
+                p.scales[m] = s;
+        }
+    }
+    // After a timeout the copies still in flight land before the CTA leaves.
+    if (tid == 0 && *abort_flag)
+        for (int s = 0; s < rp.stages; ++s)
+            if (filled >> s & 1u)
+                wait_drain(bar0 + 8u * s, last_phase >> s & 1u, p.status, rp.wait_limit,
+                           (SITE_DRAIN << 8) | 4u);
 }
 
 struct QuantParams {
@@ -466,8 +652,53 @@ cudaError_t launch_norm(NormParams p, cudaStream_t stream)
                        static_cast<size_t>(p.D) * 4, stream);
 }
 
-template <int HK, int XK> cudaError_t launch_norm(const NormParams &p, bool vec, cudaStream_t stream)
+// Long rows in number: the ring.  Threads of a CTA take eight columns each; as
+// many CTAs per SM as make about 1024 threads, and stages that fill the SM's
+// shared memory between them.
+template <int HK, int XK>
+cudaError_t launch_ring(const NormParams &p, const DeviceView &dev, cudaStream_t stream)
 {
+    const int T = (p.D / 8 + 31) / 32 * 32;
+    const int per_sm = std::max(1, std::min(8, 1024 / T));
+    RingParams r = {};
+    r.n = p;
+    r.h_bytes = static_cast<uint32_t>(p.D) * (HK == W8A8_IN_FP32 ? 4 : 2);
+    r.x_bytes = static_cast<uint32_t>(p.D) * (XK == W8A8_IN_FP32 ? 4 : 2);
+    r.wait_limit = dev.wait_limit;
+    const size_t stage = r.h_bytes + r.x_bytes, room = 220u * 1024u / per_sm - 2048u;
+    r.stages = static_cast<int>(std::min<size_t>(kRingMaxStages, room / stage));
+    static volatile int smem_set[kMaxDeviceFlags] = {};
+    int id = 0;
+    cudaError_t e = cudaGetDevice(&id);
+    if (e == cudaSuccess && !smem_set[id]) {
+        e = cudaFuncSetAttribute(k_sandwich_ring<HK, XK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 220 * 1024);
+        smem_set[id] = e == cudaSuccess;
+    }
+    if (e != cudaSuccess)
+        return e;
+    const long long ctas = std::min<long long>(p.M, static_cast<long long>(per_sm) * dev.sm_count);
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+    lc.blockDim = dim3(T, 1, 1);
+    lc.dynamicSmemBytes = r.stages * stage;
+    lc.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelEx(&lc, k_sandwich_ring<HK, XK>, r);
+}
+
+template <int HK, int XK>
+cudaError_t launch_norm(const NormParams &p, bool vec, const DeviceView &dev, cudaStream_t stream)
+{
+    // The ring where each of its CTAs gets several rows, and rows are long
+    // enough to be worth a CTA of at least four warps.
+    if (vec && p.D >= 1024 && p.D <= 8 * kMaxThreads &&
+        p.M >= 2ll * dev.sm_count * std::max(1, 1024 / (p.D / 8)))
+        return launch_ring<HK, XK>(p, dev, stream);
     return vec ? launch_norm<HK, XK, 8>(p, stream) : launch_norm<HK, XK, 1>(p, stream);
 }
 
@@ -550,18 +781,20 @@ extern "C" w8a8_status w8a8_sandwich_norm(const void *h_dev, w8a8_in_dtype h_dty
     p.res_scale = res_scale;
     p.eps = eps;
     p.y_kind = y_kind;
-    if (W8A8_DEBUG_BOUNDS && status_word_address(&p.status) != cudaSuccess)
-        p.status = nullptr;
+    DeviceView dev;
+    if (const int st = device_view(&dev); st != W8A8_OK)
+        return static_cast<w8a8_status>(st);
+    p.status = dev.status;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (h_dtype == W8A8_IN_FP32)
-        e = launch_norm<W8A8_IN_FP32, W8A8_IN_FP32>(p, vec, s);
+        e = launch_norm<W8A8_IN_FP32, W8A8_IN_FP32>(p, vec, dev, s);
     else if (h_dtype == W8A8_IN_BF16)
-        e = x_dtype == W8A8_IN_FP32 ? launch_norm<W8A8_IN_BF16, W8A8_IN_FP32>(p, vec, s)
-                                    : launch_norm<W8A8_IN_BF16, W8A8_IN_BF16>(p, vec, s);
+        e = x_dtype == W8A8_IN_FP32 ? launch_norm<W8A8_IN_BF16, W8A8_IN_FP32>(p, vec, dev, s)
+                                    : launch_norm<W8A8_IN_BF16, W8A8_IN_BF16>(p, vec, dev, s);
     else
-        e = x_dtype == W8A8_IN_FP32 ? launch_norm<W8A8_IN_FP16, W8A8_IN_FP32>(p, vec, s)
-                                    : launch_norm<W8A8_IN_FP16, W8A8_IN_FP16>(p, vec, s);
+        e = x_dtype == W8A8_IN_FP32 ? launch_norm<W8A8_IN_FP16, W8A8_IN_FP32>(p, vec, dev, s)
+                                    : launch_norm<W8A8_IN_FP16, W8A8_IN_FP16>(p, vec, dev, s);
     return e == cudaSuccess ? W8A8_OK : cuda_error("kernel launch", e);
 }
 

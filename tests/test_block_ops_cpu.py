@@ -110,6 +110,10 @@ def test_python_wrappers_refuse_shapes_and_types():
         lambda: w8.sandwich_norm(f(4, 8), f(4, 8), gate=f(1, 8), gate_rows=2),
         lambda: w8.sandwich_norm(f(4, 8), f(4, 8), x_out=f(4, 8).half()),
         lambda: w8.sandwich_norm(f(8, 4).t(), f(4, 8)),
+        lambda: w8.sandwich_norm(f(1, 8).expand(4, 8), f(4, 8)),
+        lambda: w8.sandwich_norm(f(4, 8), f(4, 8), y_out=torch.zeros(4, 8, dtype=torch.int8)),
+        lambda: w8.sandwich_norm(f(4, 16), f(4, 16), out="fp8", y_out=f(4, 16)),
+        lambda: w8.int8_matmul(e8(1, 16).expand(4, 16), f(4), e8(8, 16), f(8)),
     ):
         with pytest.raises(w8.W8A8Error):
             call()

@@ -174,6 +174,36 @@ def test_many_rows_on_a_side_stream_and_in_a_graph():
     check(k, r, y)
 
 
+@pytest.mark.parametrize("M,D", [(2500, 1024), (1000, 2056), (701, 4096), (333, 8192), (5000, 1032)])
+@pytest.mark.parametrize("dtype,resid", [("bf16", "bf16"), ("fp16", "fp32"), ("fp32", "fp32")])
+def test_many_long_rows(M, D, dtype, resid):
+    """Enough rows for the persistent kernel; its codes are those of few rows at a time."""
+    for gate_rows, drop in ((M, ()), (100, ()), (1, ("w_post",)), (0, ("w_post", "w_pre")), (0, ("w_pre",))):
+        k = make(M, D, dtype, resid, gate_rows)
+        for n in drop:
+            k[n] = None
+        r, y = w8.sandwich_norm(**k, eps=EPS)
+        check(k, r, y, f"{gate_rows} {drop}")
+    k = make(M, D, dtype, resid)
+    for out in ("fp8", "int8") if D % 16 == 0 else ("int8",):
+        r, q, s = w8.sandwich_norm(**k, eps=EPS, out=out)
+        for lo in (0, M // 2, M - 8):
+            few = dict(k, h=k["h"][lo:lo + 8], x=k["x"][lo:lo + 8])
+            r1, q1, s1 = w8.sandwich_norm(**few, eps=EPS, out=out)
+            assert_near(r[lo:lo + 8], r1.double(), reference(**few)[2] + r1.double().abs() * HALF_ULP[r1.dtype], out)
+            scale = s1 if out == "fp8" else s1[:, None]
+            got = s[lo:lo + 8] if out == "fp8" else s[lo:lo + 8, None]
+            assert ((got - scale).abs() <= 2.0 ** -16 * scale).all()
+            view = torch.float8_e4m3fn if out == "fp8" else torch.int8
+            a, b = q[lo:lo + 8].view(view).float(), q1.view(view).float()
+            # a code may differ by one step where y lies at the edge of two
+            step = torch.maximum(b.abs() / 8, torch.full_like(b, 2.0 ** -9)) if out == "fp8" else 1.0
+            assert ((a - b).abs() <= step).all() and (a != b).float().mean() < 1e-3
+    x = k["x"].clone()
+    w8.sandwich_norm(**dict(k, x=x), eps=EPS, x_out=x)
+    assert torch.equal(x, w8.sandwich_norm(**k, eps=EPS)[0])
+
+
 def test_empty():
     for M, D in ((0, 64), (3, 0)):
         r, y = w8.sandwich_norm(torch.empty(M, D, device="cuda"), torch.empty(M, D, device="cuda"))
