@@ -191,8 +191,8 @@ struct NormParams {
 // The E4M3 codes of eight columns e .. e+7 of row m and their group's scale.
 // Sixteen neighbouring lanes hold one 128-column group; every lane of the warp
 // calls it (`in`: the columns exist).
-__device__ __forceinline__ void store_fp8(const NormParams &p, long long m, int e, bool in,
-                                          const float (&v)[8], float amax)
+__device__ __forceinline__ void store_fp8(const NormParams &p, long long m, uint8_t *row, int e,
+                                          bool in, const float (&v)[8], float amax)
 {
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1)
@@ -211,7 +211,7 @@ __device__ __forceinline__ void store_fp8(const NormParams &p, long long m, int 
     for (int j = 0; j < 2; ++j)
         c[j] = fast ? quant::encode4<W8A8_IN_FP32, true>(raw, j, s, ns2, y2)
                     : quant::encode4<W8A8_IN_FP32, false>(raw, j, s, ns2, y2);
-    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.y) + m * p.ld_y + e) = make_uint2(c[0], c[1]);
+    *reinterpret_cast<uint2 *>(row + e) = make_uint2(c[0], c[1]);
     if ((lane_index() & 15) == 0)
         p.scales[m * ((p.D + 127) / 128) + e / 128] = s;
 }
@@ -336,7 +336,8 @@ __global__ void __launch_bounds__(kMaxThreads) k_sandwich_norm(const NormParams 
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     w8[j] = w[VEC == 8 ? j : 0];
-                store_fp8(p, m, e, in, w8, in ? amax : 0.f);
+                store_fp8(p, m, static_cast<uint8_t *>(p.y) + m * p.ld_y, e, in, w8,
+                          in ? amax : 0.f);
             }
             amax = 0.f;
         }
@@ -363,61 +364,159 @@ __global__ void __launch_bounds__(kMaxThreads) k_sandwich_norm(const NormParams 
 // ------------------------------------------------------------------ many rows
 
 // The same for many rows of at most 8192 columns, as a stream: persistent CTAs
-// walk the rows, each thread on the same eight columns of every row, so that
-// the norms' weights stay in its registers (the gate too, while its row lasts).
-// The rows of h and x come through a ring of shared-memory stages filled by
-// bulk copies, so that the loads of the next rows are in flight through a row's
-// two reductions.
+// walk the rows, each thread on the same two chunks of eight columns of every
+// row, so that the norms' weights stay in its registers in fp32 (the post-norm's
+// times the gate, while the gate's row lasts).  The rows of h and x come through
+// a ring of shared-memory stages filled by bulk copies, so that the next rows'
+// loads are in flight through a row's two reductions.
 constexpr int kRingMaxStages = 4;
+constexpr int kRingThreads = 512;
 
 struct RingParams {
     NormParams n;
     int stages;
     uint32_t h_bytes, x_bytes;             // of one row
+    float inv_d;                           // 1 / D
+    long long gate_step, gate_rest;        // gridDim.x / gate_rows and the remainder
     unsigned long long wait_limit;
 };
 
-template <int HK> __device__ __forceinline__ void raw_load(const void *row, int e, uint32_t (&w)[HK == W8A8_IN_FP32 ? 8 : 4])
-{
-    const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(row) +
-                                                     e * (HK == W8A8_IN_FP32 ? 4 : 2));
-#pragma unroll
-    for (int i = 0; i < (HK == W8A8_IN_FP32 ? 2 : 1); ++i) {
-        const uint4 a = __ldg(p + i);
-        w[4 * i] = a.x, w[4 * i + 1] = a.y, w[4 * i + 2] = a.z, w[4 * i + 3] = a.w;
-    }
-}
-
+// Eight elements as four fp32 pairs, from shared or global memory.
 template <int KIND>
-__device__ __forceinline__ void load_shared8(uint32_t addr, float (&v)[8])
+__device__ __forceinline__ void pairs_of(const uint32_t (&w)[KIND == W8A8_IN_FP32 ? 8 : 4],
+                                         uint64_t *v)
 {
-    constexpr int kW = KIND == W8A8_IN_FP32 ? 8 : 4;
-    uint32_t w[kW];
 #pragma unroll
-    for (int i = 0; i < kW / 4; ++i)
+    for (int j = 0; j < 4; ++j)
+        v[j] = pack2f(quant::element<KIND>(w, 2 * j), quant::element<KIND>(w, 2 * j + 1));
+}
+template <int KIND> __device__ __forceinline__ void shared_pairs(uint32_t addr, uint64_t *v)
+{
+    uint32_t w[KIND == W8A8_IN_FP32 ? 8 : 4];
+#pragma unroll
+    for (int i = 0; i < (KIND == W8A8_IN_FP32 ? 2 : 1); ++i)
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
                      : "r"(addr + 16u * i));
+    pairs_of<KIND>(w, v);
+}
+template <int KIND> __device__ __forceinline__ void global_pairs(const void *row, int e, uint64_t *v)
+{
+    uint32_t w[KIND == W8A8_IN_FP32 ? 8 : 4];
+    const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(row) +
+                                                     e * (KIND == W8A8_IN_FP32 ? 4 : 2));
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        v[j] = quant::element<KIND>(w, j);
+    for (int i = 0; i < (KIND == W8A8_IN_FP32 ? 2 : 1); ++i) {
+        const uint4 a = __ldg(p + i);
+        w[4 * i] = a.x, w[4 * i + 1] = a.y, w[4 * i + 2] = a.z, w[4 * i + 3] = a.w;
+    }
+    pairs_of<KIND>(w, v);
 }
 
-template <int HK, int XK>
-__global__ void __launch_bounds__(kMaxThreads, 1) k_sandwich_ring(const RingParams rp)
+template <int KIND> __device__ __forceinline__ void store_pairs(uint8_t *row, int e, const uint64_t *v)
+{
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        unpack2f(v[j], f[2 * j], f[2 * j + 1]);
+    store_vec<KIND, 8>(row, e, f);
+}
+
+// Sum over the CTA of at most THREADS threads, the same bits for every thread:
+// warps by shuffles, then every thread adds the warps' partials in order (zeros
+// past the last warp).
+template <int THREADS> __device__ __forceinline__ float cta_sum(float v, float *part)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane_index() == 0)
+        part[warp_index()] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < THREADS / 128; ++i) {
+        const float4 f = reinterpret_cast<const float4 *>(part)[i];
+        v += (f.x + f.y) + (f.z + f.w);
+    }
+    return v;
+}
+
+// The scales amax / 448 of two groups (1 where the quotient is 0), correctly
+// rounded: Markstein's corrections on the constant's reciprocal (see
+// quant_math.cuh) within the range where they hold, the division elsewhere.
+__device__ __forceinline__ uint64_t group_scales2(float a0, float a1)
+{
+    const bool fast = fminf(a0, a1) >= 0x1p-64f && fmaxf(a0, a1) <= 0x1p64f;
+    if (!fast)
+        return pack2f(quant::group_scale(a0), quant::group_scale(a1));
+    const float y = 1.f / 448.f;               // rounded to nearest by the compiler
+    return quant::div_by_scale2(pack2f(a0, a1), pack2f(-448.f, -448.f), pack2f(y, y));
+}
+
+// E4M3 codes of a thread's two chunks of eight columns (values as fp32 pairs)
+// and their groups' scales; sixteen neighbouring lanes hold a group of each.
+__device__ __forceinline__ void store_fp8_chunks(const NormParams &p, float *scale_row, uint8_t *row,
+                                                 int e0, int e1, bool in0, bool in1,
+                                                 const uint64_t (&v)[8])
+{
+    float am[2] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        float a, b;
+        unpack2f(v[j], a, b);
+        am[j / 4] = fmaxf(am[j / 4], fmaxf(fabsf(a), fabsf(b)));
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+        am[0] = fmaxf(am[0], __shfl_xor_sync(0xffffffffu, am[0], o));
+        am[1] = fmaxf(am[1], __shfl_xor_sync(0xffffffffu, am[1], o));
+    }
+    float s[2];
+    unpack2f(group_scales2(am[0], am[1]), s[0], s[1]);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        if (!(c ? in1 : in0))
+            continue;
+        const int e = c ? e1 : e0;
+        const bool fast = s[c] >= 0x1p-64f && s[c] <= 0x1p64f;
+        const float rc = __frcp_rn(s[c]);
+        const uint64_t ns2 = pack2f(-s[c], -s[c]), y2 = pack2f(rc, rc);
+        uint32_t raw[8], q[2];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            raw[2 * j] = static_cast<uint32_t>(v[4 * c + j]);
+            raw[2 * j + 1] = static_cast<uint32_t>(v[4 * c + j] >> 32);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            q[j] = fast ? quant::encode4<W8A8_IN_FP32, true>(raw, j, s[c], ns2, y2)
+                        : quant::encode4<W8A8_IN_FP32, false>(raw, j, s[c], ns2, y2);
+        *reinterpret_cast<uint2 *>(row + e) = make_uint2(q[0], q[1]);
+        if ((lane_index() & 15) == 0)
+            scale_row[e >> 7] = s[c];
+    }
+}
+
+// FULL: the threads' chunks cover the row exactly (D = 16 x the CTA's threads).
+template <int HK, int XK, int THREADS, int PER_SM, bool FULL>
+__global__ void __launch_bounds__(THREADS, PER_SM) k_sandwich_ring(const RingParams rp)
 {
     extern __shared__ __align__(128) uint8_t ring[];
-    __shared__ float part[2][3][32];
+    __shared__ __align__(16) float part[2][2][16];
+    __shared__ float part_max[2][32];
     __shared__ __align__(8) uint64_t bars[kRingMaxStages];
     __shared__ int abort_word;
     constexpr int kHB = HK == W8A8_IN_FP32 ? 4 : 2, kXB = XK == W8A8_IN_FP32 ? 4 : 2;
-    constexpr int kHW = HK == W8A8_IN_FP32 ? 8 : 4;
     const NormParams &p = rp.n;
     volatile int *abort_flag = &abort_word;
-    const int tid = static_cast<int>(threadIdx.x), e = 8 * tid, D = p.D;
-    const bool in = e < D;
+    const int tid = static_cast<int>(threadIdx.x), T = static_cast<int>(blockDim.x), D = p.D;
+    const int e0 = 8 * tid, e1 = e0 + 8 * T;          // the thread's two chunks
+    const bool in0 = FULL || e0 < D, in1 = FULL || e1 < D;
     const uint32_t ring0 = smem_addr(ring), bar0 = smem_addr(bars);
     const uint32_t stage_bytes = rp.h_bytes + rp.x_bytes;
+    if (tid < 64)
+        part[tid >> 5][(tid >> 4) & 1][tid & 15] = 0.f;
     if (tid == 0) {
         for (int s = 0; s < rp.stages; ++s)
             mbar_init(bar0 + 8u * s, 1);
@@ -446,55 +545,98 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_sandwich_ring(const RingPara
         for (int s = 0; s < rp.stages && first + s * stride < p.M; ++s)
             fill(first + s * stride, s);
 
-    uint32_t wpost[kHW] = {}, wpre[kHW] = {}, wg[kHW] = {};
-    if (in) {
-        if (p.w_post)
-            raw_load<HK>(p.w_post, e, wpost);
-        if (p.w_pre)
-            raw_load<HK>(p.w_pre, e, wpre);
+    const uint64_t one2 = pack2f(1.f, 1.f), scale2 = pack2f(p.res_scale, p.res_scale);
+    uint64_t wpost[8], wpre[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        wpost[j] = wpre[j] = one2;
+    if (p.w_pre) {
+        if (in0)
+            global_pairs<HK>(p.w_pre, e0, wpre);
+        if (in1)
+            global_pairs<HK>(p.w_pre, e1, wpre + 4);
     }
-    long long gate_now = -1;
+    // w_post times the gate's row
+    auto load_post = [&](long long g) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int e = c ? e1 : e0;
+            if (e < D) {
+                if (p.w_post)
+                    global_pairs<HK>(p.w_post, e, wpost + 4 * c);
+                if (p.gate) {
+                    uint64_t w[4];
+                    global_pairs<HK>(static_cast<const uint8_t *>(p.gate) + g * D * kHB, e, w);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        wpost[4 * c + j] = p.w_post ? mul2_rn(wpost[4 * c + j], w[j]) : w[j];
+                }
+            }
+        }
+    };
+    long long g = 0, g_rest = 0;
+    if (p.gate) {
+        g = first / p.gate_rows;
+        g_rest = first - g * p.gate_rows;
+    }
+    load_post(g);
+
+    uint8_t *orow = static_cast<uint8_t *>(p.x_out) + first * p.ld_xo * kXB;
+    const int yb = p.y_kind == W8A8_NORM_SAME ? kHB : 1;
+    uint8_t *yrow = static_cast<uint8_t *>(p.y) + first * p.ld_y * yb;
+    const long long o_step = stride * p.ld_xo * kXB, y_step = stride * p.ld_y * yb;
+    const int per_row = p.y_kind == W8A8_NORM_FP8 ? (D + 127) / 128 : 1;      // scales
+    float *srow = p.scales + first * per_row;
+    const long long s_step = stride * per_row;
     int stage = 0, odd = 0;
     uint32_t phase = 0;
-    for (long long m = first; m < p.M; m += stride, odd ^= 1) {
-        const long long g = p.gate ? m / p.gate_rows : -1;
-        if (g != gate_now && in)
-            raw_load<HK>(static_cast<const uint8_t *>(p.gate) + g * D * kHB, e, wg);
-        gate_now = g;
+    for (long long m = first; m < p.M; m += stride, odd ^= 1, orow += o_step, yrow += y_step,
+                   srow += s_step) {
         // A wait that runs out leaves garbage in the row, an entry in the
         // status word and the abort flag, which ends every later wait at once.
         wait_bounded(bar0 + 8u * stage, phase, guard, SITE_NORM_ROWS);
         const uint32_t src = ring0 + stage * stage_bytes;
-        float v[8] = {}, x[8];
-        float ss = 0.f, inv = 1.f;
-        if (in) {
-            load_shared8<HK>(src + e * kHB, v);
-            load_shared8<XK>(src + rp.h_bytes + e * kXB, x);
+        uint64_t v[8], ss2 = 0;
+        if (!FULL) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = 0;
         }
+        if (in0)
+            shared_pairs<HK>(src + e0 * kHB, v);
+        if (in1)
+            shared_pairs<HK>(src + e1 * kHB, v + 4);
+        float inv = 1.f, a, b;
         if (p.w_post) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                ss = fmaf(v[j], v[j], ss);
-            inv = rsqrtf(row_reduce<Add>(ss, part[odd][0], false) / static_cast<float>(D) + p.eps);
+                fma2(ss2, v[j], v[j]);
+            unpack2f(ss2, a, b);
+            inv = rsqrtf(fmaf(cta_sum<THREADS>(a + b, part[odd][0]), rp.inv_d, p.eps));
         }
-        ss = 0.f;
-        if (in) {
+        ss2 = 0;
+        const uint64_t inv2 = pack2f(inv, inv);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float u = v[j];
-                if (p.w_post)
-                    u = u * inv * quant::element<HK>(wpost, j);
-                if (p.gate)
-                    u *= quant::element<HK>(wg, j);
-                v[j] = fmaf(p.res_scale, x[j], u);
-                ss = fmaf(v[j], v[j], ss);
+        for (int c = 0; c < 2; ++c) {
+            uint64_t x[4];
+            if (!FULL)
+                x[0] = x[1] = x[2] = x[3] = 0;
+            if (c ? in1 : in0)
+                shared_pairs<XK>(src + rp.h_bytes + (c ? e1 : e0) * kXB, x);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint64_t &w = v[4 * c + j];
+                w = fma2_rn(scale2, x[j], mul2_rn(mul2_rn(w, inv2), wpost[4 * c + j]));
+                fma2(ss2, w, w);
             }
         }
         inv = 1.f;
-        if (p.w_pre)
-            inv = rsqrtf(row_reduce<Add>(ss, part[odd][1], false) / static_cast<float>(D) + p.eps);
-        else
+        if (p.w_pre) {
+            unpack2f(ss2, a, b);
+            inv = rsqrtf(fmaf(cta_sum<THREADS>(a + b, part[odd][1]), rp.inv_d, p.eps));
+        } else {
             __syncthreads();
+        }
         // Every thread has read its part of the stage: refill it.
         if (tid == 0 && m + rp.stages * stride < p.M)
             fill(m + rp.stages * stride, stage);
@@ -502,32 +644,50 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_sandwich_ring(const RingPara
             stage = 0;
             phase ^= 1u;
         }
-        if (in && p.x_out)
-            store_vec<XK, 8>(static_cast<uint8_t *>(p.x_out) + m * p.ld_xo * kXB, e, v);
-        float amax = 0.f;
+        if (p.x_out) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                if (c ? in1 : in0)
+                    store_pairs<XK>(orow, c ? e1 : e0, v + 4 * c);
+        }
         if (p.w_pre) {
+            const uint64_t pre2 = pack2f(inv, inv);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                v[j] = v[j] * inv * quant::element<HK>(wpre, j);
+                v[j] = mul2_rn(mul2_rn(v[j], pre2), wpre[j]);
         }
         if (p.y_kind == W8A8_NORM_SAME) {
-            if (in)
-                store_vec<HK, 8>(static_cast<uint8_t *>(p.y) + m * p.ld_y * kHB, e, v);
-            continue;
-        }
-        if (in) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                amax = fmaxf(amax, fabsf(v[j]));
-        }
-        if (p.y_kind == W8A8_NORM_FP8) {
-            store_fp8(p, m, e, in, v, amax);
+            for (int c = 0; c < 2; ++c)
+                if (c ? in1 : in0)
+                    store_pairs<HK>(yrow, c ? e1 : e0, v + 4 * c);
+        } else if (p.y_kind == W8A8_NORM_FP8) {
+            store_fp8_chunks(p, srow, yrow, e0, e1, in0, in1, v);
         } else {
-            const float s = int8_scale(row_reduce<Max>(amax, part[odd][2], false));
-            if (in)
-                store_int8<8>(static_cast<uint8_t *>(p.y) + m * p.ld_y + e, v, s);
+            float amax = 0.f, f[16];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                unpack2f(v[j], f[2 * j], f[2 * j + 1]);
+                amax = fmaxf(amax, fmaxf(fabsf(f[2 * j]), fabsf(f[2 * j + 1])));
+            }
+            const float s = int8_scale(row_reduce<Max>(amax, part_max[odd], false));
+            if (in0)
+                store_int8<8>(yrow + e0, reinterpret_cast<const float(&)[8]>(f[0]), s);
+            if (in1)
+                store_int8<8>(yrow + e1, reinterpret_cast<const float(&)[8]>(f[8]), s);
             if (tid == 0)
-                p.scales[m] = s;
+                *srow = s;
+        }
+        if (p.gate) {
+            const long long was = g;
+            g += rp.gate_step;
+            g_rest += rp.gate_rest;
+            if (g_rest >= p.gate_rows) {
+                g_rest -= p.gate_rows;
+                ++g;
+            }
+            if (g != was && m + stride < p.M)
+                load_post(g);
         }
     }
     // After a timeout the copies still in flight land before the CTA leaves.
@@ -652,32 +812,34 @@ cudaError_t launch_norm(NormParams p, cudaStream_t stream)
                        static_cast<size_t>(p.D) * 4, stream);
 }
 
-// Long rows in number: the ring.  Threads of a CTA take eight columns each; as
-// many CTAs per SM as make about 1024 threads, and stages that fill the SM's
-// shared memory between them.
-template <int HK, int XK>
-cudaError_t launch_ring(const NormParams &p, const DeviceView &dev, cudaStream_t stream)
+// Long rows in number: the ring.  Threads of a CTA take 16 columns each; as many
+// CTAs per SM as their registers allow (three of 256 threads: 80 registers
+// each), and stages that fill the SM's shared memory between them.
+template <int HK, int XK, int THREADS, int PER_SM, bool FULL>
+cudaError_t launch_ring_t(RingParams &r, const DeviceView &dev, cudaStream_t stream)
 {
-    const int T = (p.D / 8 + 31) / 32 * 32;
-    const int per_sm = std::max(1, std::min(8, 1024 / T));
-    RingParams r = {};
-    r.n = p;
-    r.h_bytes = static_cast<uint32_t>(p.D) * (HK == W8A8_IN_FP32 ? 4 : 2);
-    r.x_bytes = static_cast<uint32_t>(p.D) * (XK == W8A8_IN_FP32 ? 4 : 2);
-    r.wait_limit = dev.wait_limit;
-    const size_t stage = r.h_bytes + r.x_bytes, room = 220u * 1024u / per_sm - 2048u;
+    constexpr int kRoom = 220 * 1024;
+    auto kernel = k_sandwich_ring<HK, XK, THREADS, PER_SM, FULL>;
+    const int T = row_threads(r.n.D);
+    const int per_sm = std::max(1, PER_SM * THREADS / T);
+    r.h_bytes = static_cast<uint32_t>(r.n.D) * (HK == W8A8_IN_FP32 ? 4 : 2);
+    r.x_bytes = static_cast<uint32_t>(r.n.D) * (XK == W8A8_IN_FP32 ? 4 : 2);
+    const size_t stage = r.h_bytes + r.x_bytes, room = kRoom / per_sm - 2048;
     r.stages = static_cast<int>(std::min<size_t>(kRingMaxStages, room / stage));
     static volatile int smem_set[kMaxDeviceFlags] = {};
     int id = 0;
     cudaError_t e = cudaGetDevice(&id);
     if (e == cudaSuccess && !smem_set[id]) {
-        e = cudaFuncSetAttribute(k_sandwich_ring<HK, XK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 220 * 1024);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRoom);
         smem_set[id] = e == cudaSuccess;
     }
     if (e != cudaSuccess)
         return e;
-    const long long ctas = std::min<long long>(p.M, static_cast<long long>(per_sm) * dev.sm_count);
+    const long long ctas = std::min<long long>(r.n.M, static_cast<long long>(per_sm) * dev.sm_count);
+    if (r.n.gate) {
+        r.gate_step = ctas / r.n.gate_rows;
+        r.gate_rest = ctas % r.n.gate_rows;
+    }
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
     lc.blockDim = dim3(T, 1, 1);
@@ -688,17 +850,27 @@ cudaError_t launch_ring(const NormParams &p, const DeviceView &dev, cudaStream_t
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = attr;
     lc.numAttrs = 1;
-    return cudaLaunchKernelEx(&lc, k_sandwich_ring<HK, XK>, r);
+    return cudaLaunchKernelEx(&lc, kernel, r);
 }
 
 template <int HK, int XK>
 cudaError_t launch_norm(const NormParams &p, bool vec, const DeviceView &dev, cudaStream_t stream)
 {
     // The ring where each of its CTAs gets several rows, and rows are long
-    // enough to be worth a CTA of at least four warps.
-    if (vec && p.D >= 1024 && p.D <= 8 * kMaxThreads &&
-        p.M >= 2ll * dev.sm_count * std::max(1, 1024 / (p.D / 8)))
-        return launch_ring<HK, XK>(p, dev, stream);
+    // enough to be worth a CTA of at least two warps.
+    if (vec && p.D >= 1024 && p.D <= 16 * kRingThreads &&
+        p.M >= 2ll * dev.sm_count * std::max(1, 768 * 16 / p.D)) {
+        RingParams r = {};
+        r.n = p;
+        r.inv_d = 1.f / static_cast<float>(p.D);
+        r.wait_limit = dev.wait_limit;
+        const bool full = p.D % 512 == 0;      // whole warps of 16 columns a thread
+        if (p.D <= 16 * 256)
+            return full ? launch_ring_t<HK, XK, 256, 3, true>(r, dev, stream)
+                        : launch_ring_t<HK, XK, 256, 3, false>(r, dev, stream);
+        return full ? launch_ring_t<HK, XK, kRingThreads, 1, true>(r, dev, stream)
+                    : launch_ring_t<HK, XK, kRingThreads, 1, false>(r, dev, stream);
+    }
     return vec ? launch_norm<HK, XK, 8>(p, stream) : launch_norm<HK, XK, 1>(p, stream);
 }
 

@@ -621,6 +621,13 @@ __device__ __forceinline__ uint64_t fma2_rn(uint64_t a, uint64_t b, uint64_t c)
     return d;
 }
 
+__device__ __forceinline__ uint64_t mul2_rn(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 // ------------------------------------------------------------------ cp.async (4-byte gathers)
 
 // Copy 4 bytes global -> shared; src_bytes = 0 writes zeros and reads nothing.
