@@ -127,20 +127,6 @@ __device__ __forceinline__ float row_reduce(float v, float *part, bool warp_rows
     return v;
 }
 
-// x / s for a pair, correctly rounded (see quant_math.cuh for the fast form's range).
-__device__ __forceinline__ float2 div_pair(float a, float b, float s, bool fast, uint64_t ns2,
-                                           uint64_t y2)
-{
-    float2 q;
-    if (fast) {
-        unpack2f(quant::div_by_scale2(pack2f(a, b), ns2, y2), q.x, q.y);
-    } else {
-        q.x = __fdiv_rn(a, s);
-        q.y = __fdiv_rn(b, s);
-    }
-    return q;
-}
-
 // A row's scale for INT8 codes from its absolute maximum.
 __device__ __forceinline__ float int8_scale(float amax)
 {
@@ -154,6 +140,26 @@ __device__ __forceinline__ uint32_t int8_code(float q)
     return static_cast<uint32_t>(max(-127, min(127, __float2int_rn(q)))) & 0xffu;
 }
 
+// Four codes of two quotient pairs.  FAST (a normal scale): |q| < 127.5, and
+// adding 3 * 2^22 rounds a quotient half-to-even to its units, which are then
+// the sum's low byte.
+template <bool FAST>
+__device__ __forceinline__ uint32_t int8_codes4(float a, float b, float c, float d, float s,
+                                                uint64_t ns2, uint64_t y2)
+{
+    if constexpr (FAST) {
+        const uint64_t one = pack2f(1.f, 1.f), magic = pack2f(12582912.f, 12582912.f);
+        const uint64_t p = fma2_rn(quant::div_by_scale2(pack2f(a, b), ns2, y2), one, magic);
+        const uint64_t q = fma2_rn(quant::div_by_scale2(pack2f(c, d), ns2, y2), one, magic);
+        return __byte_perm(__byte_perm(static_cast<uint32_t>(p), static_cast<uint32_t>(p >> 32), 0x0040),
+                           __byte_perm(static_cast<uint32_t>(q), static_cast<uint32_t>(q >> 32), 0x0040),
+                           0x5410);
+    } else {
+        return int8_code(__fdiv_rn(a, s)) | int8_code(__fdiv_rn(b, s)) << 8 |
+               int8_code(__fdiv_rn(c, s)) << 16 | int8_code(__fdiv_rn(d, s)) << 24;
+    }
+}
+
 template <int VEC>
 __device__ __forceinline__ void store_int8(uint8_t *p, const float (&v)[VEC], float s)
 {
@@ -161,16 +167,22 @@ __device__ __forceinline__ void store_int8(uint8_t *p, const float (&v)[VEC], fl
     const float y = __frcp_rn(s);
     const uint64_t ns2 = pack2f(-s, -s), y2 = pack2f(y, y);
     if constexpr (VEC == 1) {
-        *p = static_cast<uint8_t>(int8_code(div_pair(v[0], v[0], s, fast, ns2, y2).x));
+        *p = static_cast<uint8_t>(fast ? int8_codes4<true>(v[0], 0.f, 0.f, 0.f, s, ns2, y2)
+                                       : int8_codes4<false>(v[0], 0.f, 0.f, 0.f, s, ns2, y2));
     } else {
-        uint32_t w[2];
+        uint32_t w[VEC / 4];
+        if (fast) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float2 a = div_pair(v[4 * j], v[4 * j + 1], s, fast, ns2, y2);
-            const float2 b = div_pair(v[4 * j + 2], v[4 * j + 3], s, fast, ns2, y2);
-            w[j] = int8_code(a.x) | int8_code(a.y) << 8 | int8_code(b.x) << 16 | int8_code(b.y) << 24;
+            for (int j = 0; j < VEC; j += 4)
+                w[j / 4] = int8_codes4<true>(v[j], v[j + 1], v[j + 2], v[j + 3], s, ns2, y2);
+        } else {
+#pragma unroll
+            for (int j = 0; j < VEC; j += 4)
+                w[j / 4] = int8_codes4<false>(v[j], v[j + 1], v[j + 2], v[j + 3], s, ns2, y2);
         }
-        *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+#pragma unroll
+        for (int j = 0; j < VEC / 8; ++j)
+            reinterpret_cast<uint2 *>(p)[j] = make_uint2(w[2 * j], w[2 * j + 1]);
     }
 }
 
@@ -364,8 +376,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_sandwich_norm(const NormParams 
 // ------------------------------------------------------------------ many rows
 
 // The same for many rows of at most 8192 columns, as a stream: persistent CTAs
-// walk the rows, each thread on the same two chunks of eight columns of every
-// row, so that the norms' weights stay in its registers in fp32 (the post-norm's
+// walk the rows, each thread on the same 16 columns of every row, so that the norms' weights stay in its registers in fp32 (the post-norm's
 // times the gate, while the gate's row lasts).  The rows of h and x come through
 // a ring of shared-memory stages filled by bulk copies, so that the next rows'
 // loads are in flight through a row's two reductions.
@@ -413,13 +424,39 @@ template <int KIND> __device__ __forceinline__ void global_pairs(const void *row
     pairs_of<KIND>(w, v);
 }
 
-template <int KIND> __device__ __forceinline__ void store_pairs(uint8_t *row, int e, const uint64_t *v)
+// A thread's 16 columns from e.  WIDE: all exist and the row lies on 32-byte
+// boundaries; whole 32-byte sectors leave in one store each (two 16-byte stores
+// to a sector cost the L2 two requests: 37 against 31 us for 4864 x 4096).
+template <int KIND, bool WIDE>
+__device__ __forceinline__ void store_pairs(uint8_t *row, int e, bool in0, bool in1,
+                                            const uint64_t (&v)[8])
 {
-    float f[8];
+    float f[16];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 8; ++j)
         unpack2f(v[j], f[2 * j], f[2 * j + 1]);
-    store_vec<KIND, 8>(row, e, f);
+    if constexpr (!WIDE) {
+        if (in0)
+            store_vec<KIND, 8>(row, e, reinterpret_cast<const float(&)[8]>(f[0]));
+        if (in1)
+            store_vec<KIND, 8>(row, e + 8, reinterpret_cast<const float(&)[8]>(f[8]));
+    } else if constexpr (KIND == W8A8_IN_FP32) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                w[j] = __float_as_uint(f[8 * h + j]);
+            st_global_v8(row + 4 * e + 32 * h, w);
+        }
+    } else {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            w[j] = KIND == W8A8_IN_BF16 ? pack_bf16x2(f[2 * j], f[2 * j + 1])
+                                        : pack_f16x2(f[2 * j], f[2 * j + 1]);
+        st_global_v8(row + 2 * e, w);
+    }
 }
 
 // Sum over the CTA of at most THREADS threads, the same bits for every thread:
@@ -442,63 +479,36 @@ template <int THREADS> __device__ __forceinline__ float cta_sum(float v, float *
     return v;
 }
 
-// The scales amax / 448 of two groups (1 where the quotient is 0), correctly
-// rounded: Markstein's corrections on the constant's reciprocal (see
-// quant_math.cuh) within the range where they hold, the division elsewhere.
-__device__ __forceinline__ uint64_t group_scales2(float a0, float a1)
+// E4M3 codes of a thread's 16 columns (values as fp32 pairs) and their group's
+// scale; eight neighbouring lanes hold a group.
+__device__ __forceinline__ void store_fp8_16(float *scale_row, uint8_t *row, int e, bool in0,
+                                             bool in1, const uint64_t (&v)[8])
 {
-    const bool fast = fminf(a0, a1) >= 0x1p-64f && fmaxf(a0, a1) <= 0x1p64f;
-    if (!fast)
-        return pack2f(quant::group_scale(a0), quant::group_scale(a1));
-    const float y = 1.f / 448.f;               // rounded to nearest by the compiler
-    return quant::div_by_scale2(pack2f(a0, a1), pack2f(-448.f, -448.f), pack2f(y, y));
-}
-
-// E4M3 codes of a thread's two chunks of eight columns (values as fp32 pairs)
-// and their groups' scales; sixteen neighbouring lanes hold a group of each.
-__device__ __forceinline__ void store_fp8_chunks(const NormParams &p, float *scale_row, uint8_t *row,
-                                                 int e0, int e1, bool in0, bool in1,
-                                                 const uint64_t (&v)[8])
-{
-    float am[2] = {0.f, 0.f};
+    uint32_t raw[16];
+    float amax = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         float a, b;
         unpack2f(v[j], a, b);
-        am[j / 4] = fmaxf(am[j / 4], fmaxf(fabsf(a), fabsf(b)));
+        raw[2 * j] = __float_as_uint(a);
+        raw[2 * j + 1] = __float_as_uint(b);
+        amax = fmaxf(amax, fmaxf(fabsf(a), fabsf(b)));
     }
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {
-        am[0] = fmaxf(am[0], __shfl_xor_sync(0xffffffffu, am[0], o));
-        am[1] = fmaxf(am[1], __shfl_xor_sync(0xffffffffu, am[1], o));
-    }
-    float s[2];
-    unpack2f(group_scales2(am[0], am[1]), s[0], s[1]);
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        if (!(c ? in1 : in0))
-            continue;
-        const int e = c ? e1 : e0;
-        const bool fast = s[c] >= 0x1p-64f && s[c] <= 0x1p64f;
-        const float rc = __frcp_rn(s[c]);
-        const uint64_t ns2 = pack2f(-s[c], -s[c]), y2 = pack2f(rc, rc);
-        uint32_t raw[8], q[2];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            raw[2 * j] = static_cast<uint32_t>(v[4 * c + j]);
-            raw[2 * j + 1] = static_cast<uint32_t>(v[4 * c + j] >> 32);
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            q[j] = fast ? quant::encode4<W8A8_IN_FP32, true>(raw, j, s[c], ns2, y2)
-                        : quant::encode4<W8A8_IN_FP32, false>(raw, j, s[c], ns2, y2);
-        *reinterpret_cast<uint2 *>(row + e) = make_uint2(q[0], q[1]);
-        if ((lane_index() & 15) == 0)
-            scale_row[e >> 7] = s[c];
-    }
+    for (int o = 4; o > 0; o >>= 1)
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const float s = quant::group_scale(amax);
+    const uint4 q = quant::encode16<W8A8_IN_FP32>(raw, s);
+    if (in0)
+        *reinterpret_cast<uint2 *>(row + e) = make_uint2(q.x, q.y);
+    if (in1)
+        *reinterpret_cast<uint2 *>(row + e + 8) = make_uint2(q.z, q.w);
+    if (in0 && (lane_index() & 7) == 0)
+        scale_row[e >> 7] = s;
 }
 
-// FULL: the threads' chunks cover the row exactly (D = 16 x the CTA's threads).
+// FULL: the threads' columns cover the row exactly (D = 16 x the CTA's threads)
+// and the outputs' rows lie on 32-byte boundaries.
 template <int HK, int XK, int THREADS, int PER_SM, bool FULL>
 __global__ void __launch_bounds__(THREADS, PER_SM) k_sandwich_ring(const RingParams rp)
 {
@@ -510,8 +520,8 @@ __global__ void __launch_bounds__(THREADS, PER_SM) k_sandwich_ring(const RingPar
     constexpr int kHB = HK == W8A8_IN_FP32 ? 4 : 2, kXB = XK == W8A8_IN_FP32 ? 4 : 2;
     const NormParams &p = rp.n;
     volatile int *abort_flag = &abort_word;
-    const int tid = static_cast<int>(threadIdx.x), T = static_cast<int>(blockDim.x), D = p.D;
-    const int e0 = 8 * tid, e1 = e0 + 8 * T;          // the thread's two chunks
+    const int tid = static_cast<int>(threadIdx.x), D = p.D;
+    const int e0 = 16 * tid, e1 = e0 + 8;             // the thread's two chunks
     const bool in0 = FULL || e0 < D, in1 = FULL || e1 < D;
     const uint32_t ring0 = smem_addr(ring), bar0 = smem_addr(bars);
     const uint32_t stage_bytes = rp.h_bytes + rp.x_bytes;
@@ -644,12 +654,8 @@ __global__ void __launch_bounds__(THREADS, PER_SM) k_sandwich_ring(const RingPar
             stage = 0;
             phase ^= 1u;
         }
-        if (p.x_out) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-                if (c ? in1 : in0)
-                    store_pairs<XK>(orow, c ? e1 : e0, v + 4 * c);
-        }
+        if (p.x_out)
+            store_pairs<XK, FULL>(orow, e0, in0, in1, v);
         if (p.w_pre) {
             const uint64_t pre2 = pack2f(inv, inv);
 #pragma unroll
@@ -657,12 +663,9 @@ __global__ void __launch_bounds__(THREADS, PER_SM) k_sandwich_ring(const RingPar
                 v[j] = mul2_rn(mul2_rn(v[j], pre2), wpre[j]);
         }
         if (p.y_kind == W8A8_NORM_SAME) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-                if (c ? in1 : in0)
-                    store_pairs<HK>(yrow, c ? e1 : e0, v + 4 * c);
+            store_pairs<HK, FULL>(yrow, e0, in0, in1, v);
         } else if (p.y_kind == W8A8_NORM_FP8) {
-            store_fp8_chunks(p, srow, yrow, e0, e1, in0, in1, v);
+            store_fp8_16(srow, yrow, e0, in0, in1, v);
         } else {
             float amax = 0.f, f[16];
 #pragma unroll
@@ -671,10 +674,10 @@ __global__ void __launch_bounds__(THREADS, PER_SM) k_sandwich_ring(const RingPar
                 amax = fmaxf(amax, fmaxf(fabsf(f[2 * j]), fabsf(f[2 * j + 1])));
             }
             const float s = int8_scale(row_reduce<Max>(amax, part_max[odd], false));
-            if (in0)
-                store_int8<8>(yrow + e0, reinterpret_cast<const float(&)[8]>(f[0]), s);
             if (in1)
-                store_int8<8>(yrow + e1, reinterpret_cast<const float(&)[8]>(f[8]), s);
+                store_int8<16>(yrow + e0, f, s);
+            else if (in0)
+                store_int8<8>(yrow + e0, reinterpret_cast<const float(&)[8]>(f[0]), s);
             if (tid == 0)
                 *srow = s;
         }
@@ -864,7 +867,10 @@ cudaError_t launch_norm(const NormParams &p, bool vec, const DeviceView &dev, cu
         r.n = p;
         r.inv_d = 1.f / static_cast<float>(p.D);
         r.wait_limit = dev.wait_limit;
-        const bool full = p.D % 512 == 0;      // whole warps of 16 columns a thread
+        // whole warps of 16 columns a thread, 32-byte rows out
+        constexpr int kHB = HK == W8A8_IN_FP32 ? 4 : 2, kXB = XK == W8A8_IN_FP32 ? 4 : 2;
+        const bool full = p.D % 512 == 0 && on(p.x_out, 32) && p.ld_xo * kXB % 32 == 0 &&
+                          (p.y_kind != W8A8_NORM_SAME || (on(p.y, 32) && p.ld_y * kHB % 32 == 0));
         if (p.D <= 16 * 256)
             return full ? launch_ring_t<HK, XK, 256, 3, true>(r, dev, stream)
                         : launch_ring_t<HK, XK, 256, 3, false>(r, dev, stream);

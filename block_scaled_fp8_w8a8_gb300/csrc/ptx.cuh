@@ -646,6 +646,14 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar)
 
 // ------------------------------------------------------------------ output conversion
 
+// 32-byte store to a 32-byte aligned global address.
+__device__ __forceinline__ void st_global_v8(void *p, const uint32_t (&w)[8])
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
 {
     __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
