@@ -556,15 +556,29 @@ __global__ void __launch_bounds__(THREADS, PER_SM) k_sandwich_ring(const RingPar
             fill(first + s * stride, s);
 
     const uint64_t one2 = pack2f(1.f, 1.f), scale2 = pack2f(p.res_scale, p.res_scale);
-    uint64_t wpost[8], wpre[8];
+    uint64_t wpost[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-        wpost[j] = wpre[j] = one2;
+        wpost[j] = one2;
+    // The pre-norm's weights of this thread's columns wait in shared memory
+    // (16 more registers a thread would cost the third CTA per SM), four
+    // 16-byte words a thread, neighbouring threads' side by side.
+    const uint32_t pre0 = ring0 + rp.stages * stage_bytes + 16u * tid;
+    const uint32_t pre_step = 16u * blockDim.x;
     if (p.w_pre) {
+        uint64_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            w[j] = one2;
         if (in0)
-            global_pairs<HK>(p.w_pre, e0, wpre);
+            global_pairs<HK>(p.w_pre, e0, w);
         if (in1)
-            global_pairs<HK>(p.w_pre, e1, wpre + 4);
+            global_pairs<HK>(p.w_pre, e1, w + 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(pre0 + j * pre_step),
+                         "l"(w[2 * j]), "l"(w[2 * j + 1])
+                         : "memory");
     }
     // w_post times the gate's row
     auto load_post = [&](long long g) {
@@ -659,8 +673,14 @@ __global__ void __launch_bounds__(THREADS, PER_SM) k_sandwich_ring(const RingPar
         if (p.w_pre) {
             const uint64_t pre2 = pack2f(inv, inv);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[j] = mul2_rn(mul2_rn(v[j], pre2), wpre[j]);
+            for (int j = 0; j < 4; ++j) {
+                uint64_t a2, b2;
+                asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
+                             : "=l"(a2), "=l"(b2)
+                             : "r"(pre0 + j * pre_step));
+                v[2 * j] = mul2_rn(mul2_rn(v[2 * j], pre2), a2);
+                v[2 * j + 1] = mul2_rn(mul2_rn(v[2 * j + 1], pre2), b2);
+            }
         }
         if (p.y_kind == W8A8_NORM_SAME) {
             store_pairs<HK, FULL>(yrow, e0, in0, in1, v);
@@ -827,7 +847,8 @@ cudaError_t launch_ring_t(RingParams &r, const DeviceView &dev, cudaStream_t str
     const int per_sm = std::max(1, PER_SM * THREADS / T);
     r.h_bytes = static_cast<uint32_t>(r.n.D) * (HK == W8A8_IN_FP32 ? 4 : 2);
     r.x_bytes = static_cast<uint32_t>(r.n.D) * (XK == W8A8_IN_FP32 ? 4 : 2);
-    const size_t stage = r.h_bytes + r.x_bytes, room = kRoom / per_sm - 2048;
+    const size_t stage = r.h_bytes + r.x_bytes, weights = r.n.w_pre ? 64 * T : 0;
+    const size_t room = kRoom / per_sm - 2048 - weights;
     r.stages = static_cast<int>(std::min<size_t>(kRingMaxStages, room / stage));
     static volatile int smem_set[kMaxDeviceFlags] = {};
     int id = 0;
@@ -846,7 +867,7 @@ cudaError_t launch_ring_t(RingParams &r, const DeviceView &dev, cudaStream_t str
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
     lc.blockDim = dim3(T, 1, 1);
-    lc.dynamicSmemBytes = r.stages * stage;
+    lc.dynamicSmemBytes = r.stages * stage + weights;
     lc.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
