@@ -746,6 +746,14 @@ w8a8_status run_generic(const void *A, const float *a_s, const void *B, const fl
 // the workspace (longer problems run in several), and the workspace itself: the
 // counter block that every workspace starts with, the widened A rows, B.
 constexpr int64_t kInt8ChunkBytes = 512ll << 20;
+// Up to this many tokens AUTO takes the kernel that widens in registers.
+constexpr int64_t kInt8SmallM = 64;
+
+bool int8_small(int64_t M, const w8a8_options *o)
+{
+    const int v = o ? o->variant : W8A8_VARIANT_AUTO;
+    return v == W8A8_VARIANT_SMALLM || (v == W8A8_VARIANT_AUTO && M <= kInt8SmallM);
+}
 
 struct Int8Plan {
     int64_t Kp, chunk;           // padded K; rows of A per launch (a multiple of 256, or M)
@@ -774,8 +782,12 @@ w8a8_status check_int8(int64_t M, int64_t N, int64_t K, const w8a8_options *o)
     if ((st = check_options(o)) != W8A8_OK)
         return st;
     const int v = o ? o->variant : W8A8_VARIANT_AUTO;
-    if (v != W8A8_VARIANT_AUTO && v != W8A8_VARIANT_TILED && v != W8A8_VARIANT_TILED_PAIR)
-        return fail(W8A8_ERR_UNSUPPORTED, "the INT8 matmul takes variant AUTO, TILED or TILED_PAIR");
+    if (v != W8A8_VARIANT_AUTO && v != W8A8_VARIANT_TILED && v != W8A8_VARIANT_TILED_PAIR &&
+        v != W8A8_VARIANT_SMALLM)
+        return fail(W8A8_ERR_UNSUPPORTED,
+                    "the INT8 matmul takes variant AUTO, SMALLM, TILED or TILED_PAIR");
+    if (v == W8A8_VARIANT_SMALLM && M > (1 << 20))
+        return fail(W8A8_ERR_UNSUPPORTED, "M=%lld is too large for the small-M variant", (long long)M);
     if (K > W8A8_INT8_MAX_K)
         return fail(W8A8_ERR_UNSUPPORTED, "K=%lld: sums of more than %d products may leave 32 bits",
                     (long long)K, W8A8_INT8_MAX_K);
@@ -813,15 +825,33 @@ w8a8_status run_int8(const void *A, int64_t lda, const float *a_s, const void *B
     DeviceInfo info;
     if ((st = current_device(&dev, &info)) != W8A8_OK)
         return st;
+    auto fits = [&](int a) {
+        return aligned(A, a) && aligned(B, a) && lda % a == 0 && ldb % a == 0;
+    };
+    const int access = fits(16) ? 16 : fits(4) ? 4 : 1;
+    if (int8_small(M, o)) {
+        Int8SmallParams p = {};
+        p.A = static_cast<const uint8_t *>(A);
+        p.B = static_cast<const uint8_t *>(B);
+        p.a_s = a_s;
+        p.b_s = b_s;
+        p.C = C;
+        p.M = static_cast<int>(M);
+        p.N = static_cast<int>(N);
+        p.K = static_cast<int>(K);
+        p.lda = lda;
+        p.ldb = ldb;
+        p.ldc = ldc;
+        p.out_kind = out;
+        p.status = info.status;
+        const cudaError_t e = launch_int8_small(p, access, info.sm_count, stream);
+        return e == cudaSuccess ? W8A8_OK : cuda_fail(e, "kernel launch");
+    }
     const Int8Plan pl = int8_plan(M, N, K);
     void *ws = nullptr;
     if ((st = acquire_workspace(o, dev, stream, pl.workspace(), &ws)) != W8A8_OK)
         return st;
     uint8_t *A16 = static_cast<uint8_t *>(ws) + kCounterBytes, *B16 = A16 + pl.a_bytes;
-    auto fits = [&](int a) {
-        return aligned(A, a) && aligned(B, a) && lda % a == 0 && ldb % a == 0;
-    };
-    const int access = fits(16) ? 16 : fits(4) ? 4 : 1;
     const int v = o ? o->variant : W8A8_VARIANT_AUTO;
     for (int64_t r0 = 0; r0 < M; r0 += pl.chunk) {
         const int64_t rows = std::min(pl.chunk, M - r0);
@@ -1540,7 +1570,7 @@ w8a8_status w8a8_int8_matmul(const void *A_dev, int64_t lda, const float *a_s_de
 
 size_t w8a8_int8_workspace_size(int64_t M, int64_t N, int64_t K, const w8a8_options *opts)
 {
-    if (check_int8(M, N, K, opts) != W8A8_OK || M == 0 || N == 0)
+    if (check_int8(M, N, K, opts) != W8A8_OK || M == 0 || N == 0 || int8_small(M, opts))
         return 0;
     return int8_plan(M, N, K).workspace();
 }

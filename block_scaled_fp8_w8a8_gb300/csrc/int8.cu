@@ -98,6 +98,206 @@ __global__ void __launch_bounds__(kWidenThreads) k_int8_widen(const Int8WidenPar
     }
 }
 
+// ------------------------------------------------------------------ few tokens
+
+// Up to 64 tokens: the weights' bytes bound the time, and each is widened in
+// registers right after its load (writing them as fp16 first would triple
+// their traffic).  A warp multiplies 16 MT weight rows (the MMA's M side) with 8
+// NT tokens on mma.sync fp16 tiles, whose operands a thread builds from plain
+// 16-byte loads: the MMA sums over k in any order, so thread t of a quad takes
+// bytes 16 t .. 16 t + 15 of every 64-byte run, for weights and tokens alike,
+// and word j of them is its share of the run's j-th MMA.  (tcgen05 would want
+// both operands in shared memory: at the HBM rate the widened weights' way
+// through it takes more than its bandwidth.)
+// The warps of a CTA, and the CTAs of a cluster, split K; whole sums meet in
+// shared memory, where the order of integer additions does not matter.
+constexpr int kSmallWarps = 8;
+
+__device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                            uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+                 "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t word_of(const uint4 &v, int j)
+{
+    return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
+}
+
+// UN: 64-column steps whose loads are issued together.
+template <int NT, int MT, int UN, int ACCESS>
+__global__ void __launch_bounds__(32 * kSmallWarps) k_int8_small(const Int8SmallParams p)
+{
+    constexpr int kRows = 16 * MT, kTokens = 8 * NT;
+    __shared__ int sums[kRows * kTokens];            // [token][row]
+    const int lane = static_cast<int>(lane_index()), warp = static_cast<int>(warp_index());
+    const int g = lane >> 2, t = lane & 3;
+    for (int i = static_cast<int>(threadIdx.x); i < kRows * kTokens; i += 32 * kSmallWarps)
+        sums[i] = 0;
+    __syncthreads();
+    grid_launch_dependents();
+    grid_dependency_wait();
+
+    const int n0 = static_cast<int>(blockIdx.x) * kRows, m0 = static_cast<int>(blockIdx.z) * kTokens;
+    // This warp's steps: the cluster's CTAs and their warps take equal shares.
+    const int steps = (p.K + 63) / 64, shares = static_cast<int>(gridDim.y) * kSmallWarps;
+    const int share = static_cast<int>(blockIdx.y) * kSmallWarps + warp;
+    const int first = static_cast<int>(static_cast<long long>(steps) * share / shares);
+    const int last = static_cast<int>(static_cast<long long>(steps) * (share + 1) / shares);
+    // Rows past the ends repeat the last one; their sums are not stored.
+    const uint8_t *wrow[2 * MT], *xrow[NT];
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i)
+        wrow[i] = p.B + static_cast<long long>(min(n0 + 8 * i + g, p.N - 1)) * p.ldb;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+        xrow[i] = p.A + static_cast<long long>(min(m0 + 8 * i + g, p.M - 1)) * p.lda;
+
+    float acc[MT][NT][4];
+    auto clear = [&]() {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    acc[i][j][k] = 0.f;
+    };
+    // An accumulator's element: weight row g (+ 8), tokens 2 t and 2 t + 1.
+    auto flush = [&]() {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    atomicAdd(sums + (8 * j + 2 * t + (k & 1)) * kRows + 16 * i + g + 8 * (k >> 1),
+                              __float2int_rn(acc[i][j][k]));
+    };
+    clear();
+    int since = 0;                                   // steps in the accumulators: at most 8
+    for (int s = first; s < last; s += UN) {
+        uint4 w[UN][2 * MT], x[UN][NT];
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            const int c = (s + u) * 64 + 16 * t;
+            const bool in = s + u < last && c < p.K;
+#pragma unroll
+            for (int i = 0; i < 2 * MT; ++i)
+                w[u][i] = in ? load16<ACCESS>(wrow[i], c, p.K) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+                x[u][i] = in ? load16<ACCESS>(xrow[i], c, p.K) : make_uint4(0, 0, 0, 0);
+        }
+        if (since + UN > kChunkSteps) {
+            flush();
+            clear();
+            since = 0;
+        }
+        since += UN;
+#pragma unroll
+        for (int u = 0; u < UN; ++u)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t a[MT][4];
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    const uint2 lo = widen4(word_of(w[u][2 * i], j));
+                    const uint2 hi = widen4(word_of(w[u][2 * i + 1], j));
+                    a[i][0] = lo.x;
+                    a[i][1] = hi.x;
+                    a[i][2] = lo.y;
+                    a[i][3] = hi.y;
+                }
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const uint2 b = widen4(word_of(x[u][i], j));
+#pragma unroll
+                    for (int k = 0; k < MT; ++k)
+                        mma_16x8x16(acc[k][i], a[k], b.x, b.y);
+                }
+            }
+    }
+    flush();
+
+    // The CTAs of a cluster hold partial sums of the same tile: each finishes
+    // its share of it, reading the others' through distributed shared memory.
+    const int S = static_cast<int>(gridDim.y);
+    uint32_t rank = 0;
+    if (S > 1) {
+        rank = cluster_ctarank();
+        cluster_sync();
+    } else {
+        __syncthreads();
+    }
+    constexpr int kAll = kRows * kTokens;
+    const int hi = kAll * (static_cast<int>(rank) + 1) / S;
+    for (int i = kAll * static_cast<int>(rank) / S + static_cast<int>(threadIdx.x); i < hi;
+         i += 32 * kSmallWarps) {
+        const int m = m0 + i / kRows, n = n0 + i % kRows;
+        if (m >= p.M || n >= p.N)
+            continue;
+        int sum = 0;
+        if (S == 1) {
+            sum = sums[i];
+        } else {
+            for (int r = 0; r < S; ++r) {
+                int v;
+                asm volatile("ld.shared::cluster.s32 %0, [%1];"
+                             : "=r"(v)
+                             : "r"(cluster_map(smem_addr(sums + i), static_cast<uint32_t>(r)))
+                             : "memory");
+                sum += v;
+            }
+        }
+        const float v = __int2float_rn(sum) * __ldg(p.a_s + m) * __ldg(p.b_s + n);
+        if (!in_bounds(m >= 0 && n >= 0, p.status, SITE_BOUNDS_C))
+            continue;
+        const long long at = m * p.ldc + n;
+        if (p.out_kind == OUT_FP32)
+            static_cast<float *>(p.C)[at] = v;
+        else if (p.out_kind == OUT_BF16)
+            static_cast<__nv_bfloat16 *>(p.C)[at] = __float2bfloat16_rn(v);
+        else
+            static_cast<__half *>(p.C)[at] = __float2half_rn(v);
+    }
+    if (S > 1)
+        cluster_sync();              // no CTA leaves while another reads its sums
+}
+
+template <int NT, int MT, int UN>
+cudaError_t launch_small_t(const Int8SmallParams &p, int access, int sm_count, cudaStream_t stream)
+{
+    auto kernel = access == 16  ? k_int8_small<NT, MT, UN, 16>
+                  : access == 4 ? k_int8_small<NT, MT, UN, 4>
+                                : k_int8_small<NT, MT, UN, 1>;
+    const int tiles_n = (p.N + 16 * MT - 1) / (16 * MT), tiles_m = (p.M + 8 * NT - 1) / (8 * NT);
+    // Split K over a cluster while that keeps the GPU within about two CTAs per
+    // SM and leaves every warp a step.
+    const long long tiles = static_cast<long long>(tiles_n) * tiles_m;
+    const int steps = (p.K + 63) / 64;
+    int splits = 1;
+    while (splits < 8 && tiles * splits * 2 <= 2ll * sm_count && steps >= 2 * splits * kSmallWarps)
+        splits *= 2;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(tiles_n, splits, tiles_m);
+    lc.blockDim = dim3(32 * kSmallWarps, 1, 1);
+    lc.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1;
+    attr[1].val.clusterDim.y = static_cast<unsigned>(splits);
+    attr[1].val.clusterDim.z = 1;
+    lc.attrs = attr;
+    lc.numAttrs = splits > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&lc, kernel, p);
+}
+
 // ------------------------------------------------------------------ product
 
 template <bool PAIR, int BN, int STAGES, int CPW, int EB> struct Int8Layout {
@@ -491,6 +691,17 @@ cudaError_t launch_mma(const CUtensorMap &tmA, const CUtensorMap &tmB, const CUt
 }
 
 }  // namespace
+
+cudaError_t launch_int8_small(const Int8SmallParams &p, int access, int sm_count, cudaStream_t stream)
+{
+    if (p.M <= 8)
+        return launch_small_t<1, 1, 4>(p, access, sm_count, stream);
+    if (p.M <= 16)
+        return launch_small_t<2, 1, 4>(p, access, sm_count, stream);
+    if (p.M <= 32)
+        return launch_small_t<4, 2, 2>(p, access, sm_count, stream);
+    return launch_small_t<8, 2, 1>(p, access, sm_count, stream);
+}
 
 cudaError_t launch_int8_widen(const Int8WidenParams &p, int access, int grid, cudaStream_t stream)
 {

@@ -219,6 +219,17 @@ struct Int8WidenParams {
 };
 // access: 16, 4 or 1 bytes per load, as the operands' addresses and strides allow.
 cudaError_t launch_int8_widen(const Int8WidenParams &p, int access, int grid, cudaStream_t stream);
+// Few tokens: one launch on the INT8 operands themselves, no workspace.
+struct Int8SmallParams {
+    const uint8_t *A, *B;
+    const float *a_s, *b_s;
+    void *C;
+    int M, N, K;
+    long long lda, ldb, ldc;
+    int out_kind;
+    unsigned *status;
+};
+cudaError_t launch_int8_small(const Int8SmallParams &p, int access, int sm_count, cudaStream_t stream);
 struct Int8Params {
     const float *a_s;          // [M]
     const float *b_s;          // [N]

@@ -467,10 +467,11 @@ w8a8_status w8a8_block_fp8_grouped_matmul_ragged(const void *A_dev, const float 
  * 4 bytes); M == 0 or N == 0 is a no-op, K == 0 gives zeros.  The sum is exact
  * over the whole INT8 range; it is converted to fp32, multiplied by a_s, then by
  * b_s, and cast (each rounded to nearest even).
- * Workspace: w8a8_int8_workspace_size() bytes from opts->workspace_dev, or the
- * library's for this stream, under the rules of the split-K workspace.
- * opts: variant AUTO, TILED (128 x 128 tiles) or TILED_PAIR (CTA pairs, 256 x
- * 256); grid_limit, wait_limit_cycles, workspace and the test hooks apply.  The
+ * Workspace (none for few tokens): w8a8_int8_workspace_size() bytes from
+ * opts->workspace_dev, or the library's for this stream, under the rules of the
+ * split-K workspace.
+ * opts: variant AUTO, SMALLM (few tokens, no workspace), TILED (128 x 128 tiles) or
+ * TILED_PAIR (CTA pairs, 256 x 256), all with the same bits; grid_limit, wait_limit_cycles, workspace and the test hooks apply.  The
  * launches of a call wait on the device for the work before them on the stream,
  * whatever opts->pdl says.
  */

@@ -48,8 +48,11 @@ def test_parity(M, N, K, out):
     assert_same(C, reference(*x, out), f"{M} {N} {K} {out}")
 
 
-@pytest.mark.parametrize("variant", [w8.W8A8_VARIANT_TILED, w8.W8A8_VARIANT_TILED_PAIR])
-@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (40, 70, 65), (300, 520, 1100), (513, 768, 2048)])
+VARIANTS = [w8.W8A8_VARIANT_SMALLM, w8.W8A8_VARIANT_TILED, w8.W8A8_VARIANT_TILED_PAIR]
+
+
+@pytest.mark.parametrize("variant", VARIANTS)
+@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 48, 8192), (9, 40, 5000), (20, 100, 2048), (130, 70, 64), (40, 70, 65), (300, 520, 1100), (513, 768, 2048)])
 def test_forced_kernels(M, N, K, variant):
     x = make(M, N, K, seed=3)
     for grid in (0, 4):
@@ -69,7 +72,7 @@ def test_largest_sums_are_exact(M, K):
     s = (A.double() @ B.double().t())
     C = w8.int8_matmul(A, one(M), B, one(136), "fp32")
     assert_same(C, s.float())
-    for variant in (w8.W8A8_VARIANT_TILED, w8.W8A8_VARIANT_TILED_PAIR):
+    for variant in VARIANTS:
         assert_same(w8.int8_matmul(A, one(M), B, one(136), "fp32", variant=variant), s.float())
 
 
@@ -86,7 +89,7 @@ def test_every_unit_of_a_large_sum_counts():
 
 def test_strided_and_misaligned_operands_and_memory_around_c():
     for off, pad in ((0, 16), (4, 4), (1, 3), (0, 0)):
-        M, N, K = 37, 83, 200
+        M, N, K = (37, 83, 200) if off != 4 else (91, 83, 200)
         a = torch.randint(-128, 128, (off + (M + 1) * (K + pad),), device="cuda", dtype=torch.int8)
         b = torch.randint(-128, 128, (off + (N + 1) * (K + pad),), device="cuda", dtype=torch.int8)
         A = a[off:off + M * (K + pad)].view(M, K + pad)[:, :K]
