@@ -190,7 +190,7 @@ def _ptr(x):
     raise TypeError(f"cannot pass {type(x).__name__} as a pointer")
 
 
-_current = None   # the current device's current stream, as a raw handle
+_current = None   # torch's functions for the current stream's raw handle and the device
 
 
 def _current_stream():
@@ -200,11 +200,11 @@ def _current_stream():
         if not torch.cuda.is_available():
             return 0   # the legacy default stream; the library reports the missing device
         torch.cuda.current_stream()    # initialises CUDA
-        raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
         # torch.cuda.current_stream().cuda_stream without the Stream object (0.2
-        # instead of 2.9 us a call, a quarter of a small kernel's launch)
-        _current = lambda: raw(device())  # noqa: E731
-    return _current()
+        # instead of 2.9 us a call, more than a small kernel's launch)
+        _current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    raw, device = _current
+    return raw(device())
 
 
 def _stream(s):
