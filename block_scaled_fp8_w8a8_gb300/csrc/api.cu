@@ -749,6 +749,19 @@ constexpr int64_t kInt8ChunkBytes = 512ll << 20;
 // Up to this many tokens AUTO takes the kernel that widens in registers.
 constexpr int64_t kInt8SmallM = 64;
 
+// ... and up to this many, where K allows it, the one that widens on the way to
+// shared memory.
+constexpr int64_t kInt8MidM = 1024;
+
+bool int8_mid(int64_t M, int64_t N, int64_t K, const w8a8_options *o, int sm_count, int *tile,
+              int *splits)
+{
+    const int v = o ? o->variant : W8A8_VARIANT_AUTO;
+    return (v == W8A8_VARIANT_SWAPAB || (v == W8A8_VARIANT_AUTO && M <= kInt8MidM)) &&
+           int8_mid_plan(static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), sm_count, tile,
+                         splits);
+}
+
 bool int8_small(int64_t M, const w8a8_options *o)
 {
     const int v = o ? o->variant : W8A8_VARIANT_AUTO;
@@ -783,9 +796,9 @@ w8a8_status check_int8(int64_t M, int64_t N, int64_t K, const w8a8_options *o)
         return st;
     const int v = o ? o->variant : W8A8_VARIANT_AUTO;
     if (v != W8A8_VARIANT_AUTO && v != W8A8_VARIANT_TILED && v != W8A8_VARIANT_TILED_PAIR &&
-        v != W8A8_VARIANT_SMALLM)
+        v != W8A8_VARIANT_SMALLM && v != W8A8_VARIANT_SWAPAB)
         return fail(W8A8_ERR_UNSUPPORTED,
-                    "the INT8 matmul takes variant AUTO, SMALLM, TILED or TILED_PAIR");
+                    "the INT8 matmul takes variant AUTO, SMALLM, SWAPAB, TILED or TILED_PAIR");
     if (v == W8A8_VARIANT_SMALLM && M > (1 << 20))
         return fail(W8A8_ERR_UNSUPPORTED, "M=%lld is too large for the small-M variant", (long long)M);
     if (K > W8A8_INT8_MAX_K)
@@ -847,6 +860,34 @@ w8a8_status run_int8(const void *A, int64_t lda, const float *a_s, const void *B
         const cudaError_t e = launch_int8_small(p, access, info.sm_count, stream);
         return e == cudaSuccess ? W8A8_OK : cuda_fail(e, "kernel launch");
     }
+    const unsigned long long limit =
+        (o && o->wait_limit_cycles) ? o->wait_limit_cycles : kDefaultWaitLimit;
+    int tile = 0, splits = 0;
+    if (int8_mid(M, N, K, o, info.sm_count, &tile, &splits)) {
+        Int8MidParams p = {};
+        p.A = static_cast<const uint8_t *>(A);
+        p.B = static_cast<const uint8_t *>(B);
+        p.a_s = a_s;
+        p.b_s = b_s;
+        p.C = C;
+        p.M = static_cast<int>(M);
+        p.N = static_cast<int>(N);
+        p.K = static_cast<int>(K);
+        p.lda = lda;
+        p.ldb = ldb;
+        p.ldc = ldc;
+        p.tile_tokens = tile;
+        p.out_kind = out;
+        p.wide = aligned(C, 4 * eb) && ldc % 4 == 0;
+        p.debug_skip = (o && o->debug_skip_load > 0) ? o->debug_skip_load - 1 : -1;
+        p.status = info.status;
+        p.wait_limit = limit;
+        const cudaError_t e = launch_int8_mid(p, access, splits, stream);
+        return e == cudaSuccess ? W8A8_OK : cuda_fail(e, "kernel launch");
+    }
+    if (o && o->variant == W8A8_VARIANT_SWAPAB)
+        return fail(W8A8_ERR_UNSUPPORTED, "M=%lld, K=%lld: too long for the SWAPAB form's tensor memory",
+                    (long long)M, (long long)K);
     const Int8Plan pl = int8_plan(M, N, K);
     void *ws = nullptr;
     if ((st = acquire_workspace(o, dev, stream, pl.workspace(), &ws)) != W8A8_OK)
@@ -883,7 +924,7 @@ w8a8_status run_int8(const void *A, int64_t lda, const float *a_s, const void *B
         p.ldc = ldc;
         p.out_kind = out;
         p.status = info.status;
-        p.wait_limit = (o && o->wait_limit_cycles) ? o->wait_limit_cycles : kDefaultWaitLimit;
+        p.wait_limit = limit;
         p.debug_skip_tma = (o && o->debug_skip_load > 0) ? o->debug_skip_load - 1 : -1;
         if (W8A8_DEBUG_BOUNDS && o && o->debug_bad_index && p.debug_skip_tma < 0)
             p.debug_skip_tma = kDebugBadFirstLoad;
@@ -1570,7 +1611,8 @@ w8a8_status w8a8_int8_matmul(const void *A_dev, int64_t lda, const float *a_s_de
 
 size_t w8a8_int8_workspace_size(int64_t M, int64_t N, int64_t K, const w8a8_options *opts)
 {
-    if (check_int8(M, N, K, opts) != W8A8_OK || M == 0 || N == 0 || int8_small(M, opts))
+    if (check_int8(M, N, K, opts) != W8A8_OK || M == 0 || N == 0 || int8_small(M, opts) ||
+        (opts && opts->variant == W8A8_VARIANT_SWAPAB))
         return 0;
     return int8_plan(M, N, K).workspace();
 }

@@ -298,6 +298,288 @@ cudaError_t launch_small_t(const Int8SmallParams &p, int access, int sm_count, c
     return cudaLaunchKernelEx(&lc, kernel, p);
 }
 
+// ------------------------------------------------------------------ some hundred tokens
+
+// Between those and the sizes that repay widening in a launch of its own: the
+// operands are widened on their way to shared memory.  One CTA owns 128 weight
+// rows (the MMA's M side), up to 256 tokens (its N side) and a share of K; its
+// eight warps load INT8 runs of 16 columns, two steps ahead, widen them and
+// store them in the 128-byte-swizzled layout that the MMA reads; a ninth
+// issues the MMAs.  Each 512 columns of K go to a tensor memory buffer of their
+// own, so nothing is promoted before the end: the buffers' whole numbers are
+// added up then, and the cluster's CTAs, which split K, add theirs through
+// distributed shared memory.
+// Bound by shared memory: a step's 24 KB (of 128 + 64 rows) to 48 KB (128 + 256)
+// are written once and read once by the MMA.
+constexpr int kMidWarps = 8;
+constexpr int kMidStages = 4;
+
+struct MidBars {
+    uint64_t full[kMidStages], empty[kMidStages], done;
+    uint32_t tmem;
+    int abort_word;
+};
+
+template <int CH, int ACCESS>
+__global__ void __launch_bounds__(32 * kMidWarps + 32, 1) k_int8_mid(const Int8MidParams p)
+{
+    // CH: 16-column runs per thread and step, the most (rows of both operands) / 64
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    __shared__ MidBars bars;
+    const uint32_t sW = smem_addr(smem);
+    const int Nt = p.tile_tokens;                      // a multiple of 16, at most 256
+    const uint32_t w_bytes = 128u * 128u, stage_bytes = w_bytes + static_cast<uint32_t>(Nt) * 128u;
+    const uint32_t full0 = smem_addr(bars.full), empty0 = smem_addr(bars.empty);
+    const uint32_t done = smem_addr(&bars.done);
+    volatile int *abort_flag = &bars.abort_word;
+    const int tid = static_cast<int>(threadIdx.x);
+    const uint32_t warp = warp_index(), lane = lane_index();
+    const int buf_cols = (Nt + 31) / 32 * 32;          // columns of a tensor memory buffer
+
+    if (tid == 0) {
+        for (int s = 0; s < kMidStages; ++s) {
+            mbar_init(full0 + 8u * s, kMidWarps);
+            mbar_init(empty0 + 8u * s, 1);
+        }
+        mbar_init(done, 1);
+        bars.abort_word = 0;
+        mbar_fence_init();
+    }
+    if (warp == kMidWarps) {
+        tmem_alloc(smem_addr(&bars.tmem), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = bars.tmem;
+    const WaitGuard guard{abort_flag, p.status, p.wait_limit};
+    grid_launch_dependents();
+    grid_dependency_wait();
+
+    const int n0 = static_cast<int>(blockIdx.x) * 128, m0 = static_cast<int>(blockIdx.z) * Nt;
+    const int S = static_cast<int>(gridDim.y);
+    const int all = (p.K + 63) / 64;
+    const int first = static_cast<int>(static_cast<long long>(all) * blockIdx.y / S);
+    const int steps = static_cast<int>(static_cast<long long>(all) * (blockIdx.y + 1) / S) - first;
+
+    if (warp < kMidWarps) {
+        // ------------------------------------------------------------ widening
+        // Run i of this thread: row (tid + 256 i) / 4 of the stage (weights, then
+        // tokens), 16 columns from 16 (tid % 4).  Rows past the ends repeat the
+        // last one: their results are not stored.
+        const int c0 = 16 * (tid & 3);
+        const uint8_t *src[CH];
+        uint32_t dst[CH];
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int r = (tid + 256 * i) >> 2;
+            src[i] = r < 128 ? p.B + static_cast<long long>(min(n0 + r, p.N - 1)) * p.ldb
+                             : p.A + static_cast<long long>(min(m0 + r - 128, p.M - 1)) * p.lda;
+            dst[i] = sW + static_cast<uint32_t>(r) * 128u;       // tokens follow the weights
+        }
+        const uint32_t sw = static_cast<uint32_t>((tid >> 2) & 7);      // row % 8, the same for all i
+        const uint32_t p0 = 16u * ((2u * (tid & 3)) ^ sw), p1 = 16u * ((2u * (tid & 3) + 1u) ^ sw);
+        const int runs = (4 * (128 + Nt) - tid + 255) / 256;            // of the CH, those that exist
+        auto load = [&](uint4(&x)[CH], int s) {
+            const int c = (first + s) * 64 + c0;
+#pragma unroll
+            for (int i = 0; i < CH; ++i)
+                x[i] = (i < runs && s < steps && c < p.K) ? load16<ACCESS>(src[i], c, p.K)
+                                                          : make_uint4(0, 0, 0, 0);
+        };
+        auto put = [&](const uint4(&x)[CH], int s) {
+            const int stage = s % kMidStages;
+            const uint32_t parity = static_cast<uint32_t>(s / kMidStages) & 1u;
+            if (!__all_sync(0xffffffffu, wait_bounded(empty0 + 8u * stage, parity ^ 1u, guard,
+                                                      SITE_TILED_PRODUCER)))
+                return false;
+            const uint32_t off = static_cast<uint32_t>(stage) * stage_bytes;
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                if (i < runs) {
+                    const uint2 a = widen4(x[i].x), b = widen4(x[i].y), c = widen4(x[i].z),
+                                d = widen4(x[i].w);
+                    st_shared_v4(dst[i] + off + p0, a.x, a.y, b.x, b.y);
+                    st_shared_v4(dst[i] + off + p1, c.x, c.y, d.x, d.y);
+                }
+            }
+            fence_async_smem();              // the codes are read by the tensor cores
+            __syncwarp();
+            if (lane == 0 && s != p.debug_skip)
+                mbar_arrive(full0 + 8u * stage);
+            return true;
+        };
+        uint4 xa[CH], xb[CH];
+        load(xa, 0);
+        load(xb, 1);
+        for (int s = 0; s < steps; s += 2) {
+            if (!put(xa, s))
+                break;
+            load(xa, s + 2);
+            if (s + 1 < steps && !put(xb, s + 1))
+                break;
+            load(xb, s + 3);
+        }
+    } else if (lane == 0) {
+        // ------------------------------------------------------------ MMA issuer
+        const uint32_t idesc = idesc_f16_f32(128, static_cast<uint32_t>(Nt));
+        for (int s = 0; s < steps; ++s) {
+            const int stage = s % kMidStages;
+            if (!wait_bounded(full0 + 8u * stage, static_cast<uint32_t>(s / kMidStages) & 1u, guard,
+                              SITE_TILED_MMA_FULL))
+                break;
+            tc_fence_after_sync();
+            const uint32_t d = tmem_base + static_cast<uint32_t>(s / kChunkSteps * buf_cols);
+            const uint64_t ad = sw128_kmajor_desc(sW + stage * stage_bytes);
+            const uint64_t bd = sw128_kmajor_desc(sW + stage * stage_bytes + w_bytes);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                mma_f16<false>(d, ad + 2u * kk, bd + 2u * kk, idesc,
+                               (s % kChunkSteps > 0 || kk > 0) ? 1u : 0u);
+            mma_commit(empty0 + 8u * stage);
+        }
+        mma_commit(done);
+    }
+    __syncwarp();
+    // All MMAs have read shared memory and written tensor memory (after a
+    // timeout too, whose garbage the status word reports).
+    wait_drain(done, 0, p.status, p.wait_limit, (SITE_DRAIN << 8) | 4u);
+    tc_fence_after_sync();
+    __syncthreads();                   // every warp is past its stores into the stages
+
+    // ---------------------------------------------------------------- the sums, [token][weight row]
+    int *sums = reinterpret_cast<int *>(smem);
+    const int bufs = (steps + kChunkSteps - 1) / kChunkSteps;
+    if (warp < kMidWarps) {
+        const uint32_t q = warp & 3u;
+        const int row = static_cast<int>(q * 32 + lane);
+        for (int c = 32 * static_cast<int>(warp >> 2); c < Nt; c += 64) {
+            int sum[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                sum[j] = 0;
+            for (int b = 0; b < bufs; ++b) {
+                float v[32];
+                tmem_load_32cols(tmem_base + ((q * 32u) << 16) + static_cast<uint32_t>(b * buf_cols + c), v);
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    sum[j] += __float2int_rn(v[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (c + j < Nt)
+                    sums[(c + j) * 128 + row] = sum[j];
+        }
+    }
+    uint32_t rank = 0;
+    if (S > 1) {
+        rank = cluster_ctarank();
+        cluster_sync();
+    } else {
+        __syncthreads();
+    }
+    // Each CTA of the cluster finishes its share of the tokens: 32 threads to a
+    // token's row, four columns each.
+    const int tokens = min(Nt, p.M - m0);
+    const int t0 = tokens * static_cast<int>(rank) / S, t1 = tokens * (static_cast<int>(rank) + 1) / S;
+    const int n = n0 + 4 * static_cast<int>(lane);
+    if (warp < kMidWarps && n < p.N) {
+        float bs[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            bs[j] = n + j < p.N ? __ldg(p.b_s + n + j) : 0.f;
+        for (int tk = t0 + static_cast<int>(warp); tk < t1; tk += kMidWarps) {
+            int s[4] = {0, 0, 0, 0};
+            const uint32_t at = smem_addr(sums + tk * 128 + 4 * static_cast<int>(lane));
+            for (int r = 0; r < S; ++r) {
+                int v[4];
+                const uint32_t from = S > 1 ? cluster_map(at, static_cast<uint32_t>(r)) : at;
+                asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                             : "r"(from)
+                             : "memory");
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    s[j] += v[j];
+            }
+            const int m = m0 + tk;
+            const float as = __ldg(p.a_s + m);
+            float f[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                f[j] = __int2float_rn(s[j]) * as * bs[j];
+            if (!in_bounds(m < p.M && n < p.N, p.status, SITE_BOUNDS_C))
+                continue;
+            const long long o = static_cast<long long>(m) * p.ldc + n;
+            if (p.out_kind == OUT_FP32) {
+                float *c = static_cast<float *>(p.C) + o;
+                if (p.wide && n + 4 <= p.N)
+                    *reinterpret_cast<float4 *>(c) = make_float4(f[0], f[1], f[2], f[3]);
+                else
+                    for (int j = 0; j < 4 && n + j < p.N; ++j)
+                        c[j] = f[j];
+            } else {
+                uint16_t *c = static_cast<uint16_t *>(p.C) + o;
+                const bool bf = p.out_kind == OUT_BF16;
+                const uint32_t lo = bf ? pack_bf16x2(f[0], f[1]) : pack_f16x2(f[0], f[1]);
+                const uint32_t hi = bf ? pack_bf16x2(f[2], f[3]) : pack_f16x2(f[2], f[3]);
+                if (p.wide && n + 4 <= p.N)
+                    *reinterpret_cast<uint2 *>(c) = make_uint2(lo, hi);
+                else
+                    for (int j = 0; j < 4 && n + j < p.N; ++j)
+                        c[j] = static_cast<uint16_t>((j < 2 ? lo : hi) >> (16 * (j & 1)));
+            }
+        }
+    }
+    tc_fence_before_sync();
+    if (S > 1)
+        cluster_sync();                // no CTA leaves while another reads its sums
+    else
+        __syncthreads();
+    if (warp == kMidWarps) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem_base, 512);
+    }
+}
+
+template <int CH>
+cudaError_t launch_mid_t(const Int8MidParams &p, int access, int splits, cudaStream_t stream)
+{
+    auto kernel = access == 16 ? k_int8_mid<CH, 16> : access == 4 ? k_int8_mid<CH, 4> : k_int8_mid<CH, 1>;
+    const size_t smem = 1024 + kMidStages * (128 * 128 + static_cast<size_t>(p.tile_tokens) * 128);
+    static volatile int smem_set[3][kMaxDeviceFlags] = {};
+    const int a = access == 16 ? 0 : access == 4 ? 1 : 2;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev < 0 || dev >= kMaxDeviceFlags))
+        e = cudaErrorInvalidDevice;
+    if (e == cudaSuccess && !smem_set[a][dev]) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 1024 + kMidStages * (128 + 256) * 128);
+        smem_set[a][dev] = e == cudaSuccess;
+    }
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3((p.N + 127) / 128, splits, (p.M + p.tile_tokens - 1) / p.tile_tokens);
+    lc.blockDim = dim3(32 * kMidWarps + 32, 1, 1);
+    lc.dynamicSmemBytes = smem;
+    lc.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1;
+    attr[1].val.clusterDim.y = static_cast<unsigned>(splits);
+    attr[1].val.clusterDim.z = 1;
+    lc.attrs = attr;
+    lc.numAttrs = splits > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&lc, kernel, p);
+}
+
 // ------------------------------------------------------------------ product
 
 template <bool PAIR, int BN, int STAGES, int CPW, int EB> struct Int8Layout {
@@ -701,6 +983,39 @@ cudaError_t launch_int8_small(const Int8SmallParams &p, int access, int sm_count
     if (p.M <= 32)
         return launch_small_t<4, 2, 2>(p, access, sm_count, stream);
     return launch_small_t<8, 2, 1>(p, access, sm_count, stream);
+}
+
+bool int8_mid_plan(int M, int N, int K, int sm_count, int *tile_tokens, int *splits)
+{
+    const int steps = (K + 63) / 64, blocks = (N + 127) / 128;
+    // Token tiles of equal size, as few as 256 tokens allow; more of them while
+    // the GPU would otherwise stand half empty with K split as far as it goes
+    // (two steps a CTA, clusters of 8).
+    const int most = std::max(1, std::min(8, steps / 2));
+    int tiles = (M + 255) / 256;
+    while (static_cast<long long>(blocks) * tiles * most * 2 <= sm_count && M / (tiles + 1) >= 64)
+        ++tiles;
+    const int nt = ((M + tiles - 1) / tiles + 15) / 16 * 16;
+    tiles = (M + nt - 1) / nt;
+    // The 512 columns of tensor memory hold 512 / nt buffers of 8 steps.
+    const int room = 512 / ((nt + 31) / 32 * 32) * kChunkSteps;
+    int s = 1;
+    while (s < 8 && ((steps + s - 1) / s > room ||
+                     (static_cast<long long>(blocks) * tiles * s * 2 <= sm_count && s * 2 <= most)))
+        s *= 2;
+    if ((steps + s - 1) / s > room || tiles > 65535)
+        return false;
+    *tile_tokens = nt;
+    *splits = s;
+    return true;
+}
+
+cudaError_t launch_int8_mid(const Int8MidParams &p, int access, int splits, cudaStream_t stream)
+{
+    const int ch = (4 * (128 + p.tile_tokens) + 255) / 256;
+    return ch <= 3 ? launch_mid_t<3>(p, access, splits, stream)
+                   : ch <= 4 ? launch_mid_t<4>(p, access, splits, stream)
+                             : launch_mid_t<6>(p, access, splits, stream);
 }
 
 cudaError_t launch_int8_widen(const Int8WidenParams &p, int access, int grid, cudaStream_t stream)

@@ -230,6 +230,23 @@ struct Int8SmallParams {
     unsigned *status;
 };
 cudaError_t launch_int8_small(const Int8SmallParams &p, int access, int sm_count, cudaStream_t stream);
+// Some hundred tokens: one launch, operands widened on the way to shared memory.
+struct Int8MidParams {
+    const uint8_t *A, *B;
+    const float *a_s, *b_s;
+    void *C;
+    int M, N, K;
+    long long lda, ldb, ldc;
+    int tile_tokens;           // multiple of 16, at most 256
+    int out_kind;
+    int wide;                  // four neighbouring elements of C can be stored at once
+    int debug_skip;            // test hook: >= 0 withholds that step's arrival
+    unsigned *status;
+    unsigned long long wait_limit;
+};
+// Token tile and cluster size for a problem; false where K is too long for them.
+bool int8_mid_plan(int M, int N, int K, int sm_count, int *tile_tokens, int *splits);
+cudaError_t launch_int8_mid(const Int8MidParams &p, int access, int splits, cudaStream_t stream);
 struct Int8Params {
     const float *a_s;          // [M]
     const float *b_s;          // [N]

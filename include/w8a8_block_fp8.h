@@ -470,8 +470,10 @@ w8a8_status w8a8_block_fp8_grouped_matmul_ragged(const void *A_dev, const float 
  * Workspace (none for few tokens): w8a8_int8_workspace_size() bytes from
  * opts->workspace_dev, or the library's for this stream, under the rules of the
  * split-K workspace.
- * opts: variant AUTO, SMALLM (few tokens, no workspace), TILED (128 x 128 tiles) or
- * TILED_PAIR (CTA pairs, 256 x 256), all with the same bits; grid_limit, wait_limit_cycles, workspace and the test hooks apply.  The
+ * opts: variant AUTO, SMALLM (few tokens), SWAPAB (some hundred; K within 4096 to
+ * 32768 by the token tile, else W8A8_ERR_UNSUPPORTED), TILED (128 x 128 tiles) or
+ * TILED_PAIR (CTA pairs, 256 x 256), all with the same bits, the first two without
+ * workspace; grid_limit, wait_limit_cycles, workspace and the test hooks apply.  The
  * launches of a call wait on the device for the work before them on the stream,
  * whatever opts->pdl says.
  */
@@ -482,8 +484,8 @@ w8a8_status w8a8_int8_matmul(const void *A_dev, int64_t lda, const float *a_s_de
                              w8a8_out_dtype out_dtype, w8a8_stream_t stream,
                              const w8a8_options *opts);
 
-/* Device scratch (bytes) that w8a8_int8_matmul takes for this problem (0 for none,
- * or bad sizes). */
+/* Device scratch (bytes) that w8a8_int8_matmul takes for this problem at most (0 for
+ * none, or bad sizes). */
 size_t w8a8_int8_workspace_size(int64_t M, int64_t N, int64_t K, const w8a8_options *opts);
 
 /*
