@@ -839,9 +839,9 @@ w8a8_status run_int8(const void *A, int64_t lda, const float *a_s, const void *B
     if ((st = current_device(&dev, &info)) != W8A8_OK)
         return st;
     auto fits = [&](int a) {
-        return aligned(A, a) && aligned(B, a) && lda % a == 0 && ldb % a == 0;
+        return aligned(A, a) && aligned(B, a) && lda % a == 0 && ldb % a == 0 && K % a == 0;
     };
-    const int access = fits(16) ? 16 : fits(4) ? 4 : 1;
+    const int access = fits(16) ? 16 : fits(8) ? 8 : fits(4) ? 4 : 1;
     if (int8_small(M, o)) {
         Int8SmallParams p = {};
         p.A = static_cast<const uint8_t *>(A);

@@ -47,18 +47,25 @@ __device__ __forceinline__ uint2 widen4(uint32_t w)
 }
 
 // 16 INT8 values at columns c .. c+15 of a row (zeros past K).  ACCESS: bytes
-// per load that the operand's address and stride allow (16, 4 or 1).
+// per load (16, 8 or 4 where the operands' addresses, strides and K are
+// multiples of it, so that no load straddles the row's end; else 1).
 template <int ACCESS>
 __device__ __forceinline__ uint4 load16(const uint8_t *row, int c, int K)
 {
-    if (ACCESS == 16 && c + 16 <= K)
-        return __ldg(reinterpret_cast<const uint4 *>(row + c));
+    if constexpr (ACCESS == 16)
+        return c < K ? __ldg(reinterpret_cast<const uint4 *>(row + c)) : make_uint4(0, 0, 0, 0);
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int k = c + 4 * i;
-        if (ACCESS >= 4 && k + 4 <= K) {
-            w[i] = __ldg(reinterpret_cast<const uint32_t *>(row + k));
+        if constexpr (ACCESS == 8) {
+            if (i & 1)
+                continue;
+            const uint2 v = k < K ? __ldg(reinterpret_cast<const uint2 *>(row + k)) : make_uint2(0, 0);
+            w[i] = v.x;
+            w[i + 1] = v.y;
+        } else if constexpr (ACCESS == 4) {
+            w[i] = k < K ? __ldg(reinterpret_cast<const uint32_t *>(row + k)) : 0u;
         } else {
             w[i] = 0;
 #pragma unroll
@@ -129,7 +136,7 @@ __device__ __forceinline__ uint32_t word_of(const uint4 &v, int j)
 
 // UN: 64-column steps whose loads are issued together.
 template <int NT, int MT, int UN, int ACCESS>
-__global__ void __launch_bounds__(32 * kSmallWarps) k_int8_small(const Int8SmallParams p)
+__global__ void __launch_bounds__(32 * kSmallWarps, NT <= 4 ? 2 : 1) k_int8_small(const Int8SmallParams p)
 {
     constexpr int kRows = 16 * MT, kTokens = 8 * NT;
     __shared__ int sums[kRows * kTokens];            // [token][row]
@@ -184,13 +191,13 @@ __global__ void __launch_bounds__(32 * kSmallWarps) k_int8_small(const Int8Small
 #pragma unroll
         for (int u = 0; u < UN; ++u) {
             const int c = (s + u) * 64 + 16 * t;
-            const bool in = s + u < last && c < p.K;
+            const int end = s + u < last ? p.K : 0;          // nothing past this warp's steps
 #pragma unroll
             for (int i = 0; i < 2 * MT; ++i)
-                w[u][i] = in ? load16<ACCESS>(wrow[i], c, p.K) : make_uint4(0, 0, 0, 0);
+                w[u][i] = load16<ACCESS>(wrow[i], c, end);
 #pragma unroll
             for (int i = 0; i < NT; ++i)
-                x[u][i] = in ? load16<ACCESS>(xrow[i], c, p.K) : make_uint4(0, 0, 0, 0);
+                x[u][i] = load16<ACCESS>(xrow[i], c, end);
         }
         if (since + UN > kChunkSteps) {
             flush();
@@ -272,6 +279,7 @@ template <int NT, int MT, int UN>
 cudaError_t launch_small_t(const Int8SmallParams &p, int access, int sm_count, cudaStream_t stream)
 {
     auto kernel = access == 16  ? k_int8_small<NT, MT, UN, 16>
+                  : access == 8 ? k_int8_small<NT, MT, UN, 8>
                   : access == 4 ? k_int8_small<NT, MT, UN, 4>
                                 : k_int8_small<NT, MT, UN, 1>;
     const int tiles_n = (p.N + 16 * MT - 1) / (16 * MT), tiles_m = (p.M + 8 * NT - 1) / (8 * NT);
@@ -303,7 +311,7 @@ cudaError_t launch_small_t(const Int8SmallParams &p, int access, int sm_count, c
 // Between those and the sizes that repay widening in a launch of its own: the
 // operands are widened on their way to shared memory.  One CTA owns 128 weight
 // rows (the MMA's M side), up to 256 tokens (its N side) and a share of K; its
-// eight warps load INT8 runs of 16 columns, two steps ahead, widen them and
+// eight warps load INT8 runs of 16 columns, several steps ahead, widen them and
 // store them in the 128-byte-swizzled layout that the MMA reads; a ninth
 // issues the MMAs.  Each 512 columns of K go to a tensor memory buffer of their
 // own, so nothing is promoted before the end: the buffers' whole numbers are
@@ -311,7 +319,9 @@ cudaError_t launch_small_t(const Int8SmallParams &p, int access, int sm_count, c
 // distributed shared memory.
 // Bound by shared memory: a step's 24 KB (of 128 + 64 rows) to 48 KB (128 + 256)
 // are written once and read once by the MMA.
-constexpr int kMidWarps = 8;
+constexpr int kMidGroup = 8;
+constexpr int kMidGroups = 2;
+constexpr int kMidWarps = kMidGroup * kMidGroups;
 constexpr int kMidStages = 4;
 
 struct MidBars {
@@ -320,10 +330,11 @@ struct MidBars {
     int abort_word;
 };
 
-template <int CH, int ACCESS>
+// CH: 16-column runs per thread and step, (rows of both operands) / 64 rounded
+// up; AHEAD: steps whose loads are in flight.
+template <int CH, int AHEAD, int ACCESS>
 __global__ void __launch_bounds__(32 * kMidWarps + 32, 1) k_int8_mid(const Int8MidParams p)
 {
-    // CH: 16-column runs per thread and step, the most (rows of both operands) / 64
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -340,7 +351,7 @@ __global__ void __launch_bounds__(32 * kMidWarps + 32, 1) k_int8_mid(const Int8M
 
     if (tid == 0) {
         for (int s = 0; s < kMidStages; ++s) {
-            mbar_init(full0 + 8u * s, kMidWarps);
+            mbar_init(full0 + 8u * s, kMidGroup);
             mbar_init(empty0 + 8u * s, 1);
         }
         mbar_init(done, 1);
@@ -367,28 +378,28 @@ __global__ void __launch_bounds__(32 * kMidWarps + 32, 1) k_int8_mid(const Int8M
 
     if (warp < kMidWarps) {
         // ------------------------------------------------------------ widening
-        // Run i of this thread: row (tid + 256 i) / 4 of the stage (weights, then
-        // tokens), 16 columns from 16 (tid % 4).  Rows past the ends repeat the
+        // Run i of the group's thread gt: row (gt + 256 i) / 4 of the stage (weights,
+        // then tokens), 16 columns from 16 (gt % 4).  Rows past the ends repeat the
         // last one: their results are not stored.
-        const int c0 = 16 * (tid & 3);
+        const int gt = tid % (32 * kMidGroup), group = tid / (32 * kMidGroup);
+        const int c0 = 16 * (gt & 3);
         const uint8_t *src[CH];
         uint32_t dst[CH];
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const int r = (tid + 256 * i) >> 2;
+            const int r = (gt + 256 * i) >> 2;
             src[i] = r < 128 ? p.B + static_cast<long long>(min(n0 + r, p.N - 1)) * p.ldb
                              : p.A + static_cast<long long>(min(m0 + r - 128, p.M - 1)) * p.lda;
             dst[i] = sW + static_cast<uint32_t>(r) * 128u;       // tokens follow the weights
         }
-        const uint32_t sw = static_cast<uint32_t>((tid >> 2) & 7);      // row % 8, the same for all i
-        const uint32_t p0 = 16u * ((2u * (tid & 3)) ^ sw), p1 = 16u * ((2u * (tid & 3) + 1u) ^ sw);
-        const int runs = (4 * (128 + Nt) - tid + 255) / 256;            // of the CH, those that exist
+        const uint32_t sw = static_cast<uint32_t>((gt >> 2) & 7);       // row % 8, the same for all i
+        const uint32_t p0 = 16u * ((2u * (gt & 3)) ^ sw), p1 = 16u * ((2u * (gt & 3) + 1u) ^ sw);
+        const int runs = (4 * (128 + Nt) - gt + 255) / 256;             // of the CH, those that exist
         auto load = [&](uint4(&x)[CH], int s) {
-            const int c = (first + s) * 64 + c0;
+            const int c = (first + s) * 64 + c0, end = s < steps ? p.K : 0;
 #pragma unroll
             for (int i = 0; i < CH; ++i)
-                x[i] = (i < runs && s < steps && c < p.K) ? load16<ACCESS>(src[i], c, p.K)
-                                                          : make_uint4(0, 0, 0, 0);
+                x[i] = load16<ACCESS>(src[i], c, i < runs ? end : 0);
         };
         auto put = [&](const uint4(&x)[CH], int s) {
             const int stage = s % kMidStages;
@@ -412,16 +423,18 @@ __global__ void __launch_bounds__(32 * kMidWarps + 32, 1) k_int8_mid(const Int8M
                 mbar_arrive(full0 + 8u * stage);
             return true;
         };
-        uint4 xa[CH], xb[CH];
-        load(xa, 0);
-        load(xb, 1);
-        for (int s = 0; s < steps; s += 2) {
-            if (!put(xa, s))
-                break;
-            load(xa, s + 2);
-            if (s + 1 < steps && !put(xb, s + 1))
-                break;
-            load(xb, s + 3);
+        uint4 x[AHEAD][CH];
+#pragma unroll
+        for (int d = 0; d < AHEAD; ++d)
+            load(x[d], group + kMidGroups * d);
+        bool ok = true;
+        for (int s = group; ok && s < steps; s += kMidGroups * AHEAD) {
+#pragma unroll
+            for (int d = 0; d < AHEAD; ++d) {
+                const int at = s + kMidGroups * d;
+                ok = ok && (at >= steps || put(x[d], at));
+                load(x[d], at + kMidGroups * AHEAD);
+            }
         }
     } else if (lane == 0) {
         // ------------------------------------------------------------ MMA issuer
@@ -456,7 +469,7 @@ __global__ void __launch_bounds__(32 * kMidWarps + 32, 1) k_int8_mid(const Int8M
     if (warp < kMidWarps) {
         const uint32_t q = warp & 3u;
         const int row = static_cast<int>(q * 32 + lane);
-        for (int c = 32 * static_cast<int>(warp >> 2); c < Nt; c += 64) {
+        for (int c = 32 * static_cast<int>(warp >> 2); c < Nt; c += 8 * kMidWarps) {
             int sum[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j)
@@ -491,22 +504,30 @@ __global__ void __launch_bounds__(32 * kMidWarps + 32, 1) k_int8_mid(const Int8M
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             bs[j] = n + j < p.N ? __ldg(p.b_s + n + j) : 0.f;
-        for (int tk = t0 + static_cast<int>(warp); tk < t1; tk += kMidWarps) {
-            int s[4] = {0, 0, 0, 0};
-            const uint32_t at = smem_addr(sums + tk * 128 + 4 * static_cast<int>(lane));
-            for (int r = 0; r < S; ++r) {
-                int v[4];
-                const uint32_t from = S > 1 ? cluster_map(at, static_cast<uint32_t>(r)) : at;
-                asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                             : "r"(from)
-                             : "memory");
+        uint32_t base[8];                       // the cluster's tiles
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    s[j] += v[j];
-            }
+        for (int r = 0; r < 8; ++r) {
+            const uint32_t own = smem_addr(sums + 4 * static_cast<int>(lane));
+            base[r] = S > 1 ? cluster_map(own, static_cast<uint32_t>(min(r, S - 1))) : own;
+        }
+        for (int tk = t0 + static_cast<int>(warp); tk < t1; tk += kMidWarps) {
             const int m = m0 + tk;
             const float as = __ldg(p.a_s + m);
+            int v[8][4], s[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int r = 0; r < 8; ++r)         // every load before the first addition
+                if (r < S)
+                    asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(v[r][0]), "=r"(v[r][1]), "=r"(v[r][2]), "=r"(v[r][3])
+                                 : "r"(base[r] + 512u * tk)
+                                 : "memory");
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (r < S) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        s[j] += v[r][j];
+                }
             float f[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -545,13 +566,16 @@ __global__ void __launch_bounds__(32 * kMidWarps + 32, 1) k_int8_mid(const Int8M
     }
 }
 
-template <int CH>
+template <int CH, int AHEAD>
 cudaError_t launch_mid_t(const Int8MidParams &p, int access, int splits, cudaStream_t stream)
 {
-    auto kernel = access == 16 ? k_int8_mid<CH, 16> : access == 4 ? k_int8_mid<CH, 4> : k_int8_mid<CH, 1>;
+    auto kernel = access == 16  ? k_int8_mid<CH, AHEAD, 16>
+                  : access == 8 ? k_int8_mid<CH, AHEAD, 8>
+                  : access == 4 ? k_int8_mid<CH, AHEAD, 4>
+                                : k_int8_mid<CH, AHEAD, 1>;
     const size_t smem = 1024 + kMidStages * (128 * 128 + static_cast<size_t>(p.tile_tokens) * 128);
-    static volatile int smem_set[3][kMaxDeviceFlags] = {};
-    const int a = access == 16 ? 0 : access == 4 ? 1 : 2;
+    static volatile int smem_set[4][kMaxDeviceFlags] = {};
+    const int a = access == 16 ? 0 : access == 8 ? 1 : access == 4 ? 2 : 3;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && (dev < 0 || dev >= kMaxDeviceFlags))
@@ -1013,9 +1037,9 @@ bool int8_mid_plan(int M, int N, int K, int sm_count, int *tile_tokens, int *spl
 cudaError_t launch_int8_mid(const Int8MidParams &p, int access, int splits, cudaStream_t stream)
 {
     const int ch = (4 * (128 + p.tile_tokens) + 255) / 256;
-    return ch <= 3 ? launch_mid_t<3>(p, access, splits, stream)
-                   : ch <= 4 ? launch_mid_t<4>(p, access, splits, stream)
-                             : launch_mid_t<6>(p, access, splits, stream);
+    return ch <= 3 ? launch_mid_t<3, 3>(p, access, splits, stream)
+                   : ch <= 4 ? launch_mid_t<4, 2>(p, access, splits, stream)
+                             : launch_mid_t<6, 2>(p, access, splits, stream);
 }
 
 cudaError_t launch_int8_widen(const Int8WidenParams &p, int access, int grid, cudaStream_t stream)
@@ -1030,6 +1054,7 @@ cudaError_t launch_int8_widen(const Int8WidenParams &p, int access, int grid, cu
     lc.attrs = attr;
     lc.numAttrs = 1;
     return cudaLaunchKernelEx(&lc, access == 16  ? k_int8_widen<16>
+                                   : access == 8 ? k_int8_widen<8>
                                    : access == 4 ? k_int8_widen<4>
                                                  : k_int8_widen<1>,
                               p);

@@ -217,7 +217,7 @@ struct Int8WidenParams {
     int K, Kp;
     unsigned *status;
 };
-// access: 16, 4 or 1 bytes per load, as the operands' addresses and strides allow.
+// access: 16, 8, 4 or 1 bytes per load, as the operands' addresses, strides and K allow.
 cudaError_t launch_int8_widen(const Int8WidenParams &p, int access, int grid, cudaStream_t stream);
 // Few tokens: one launch on the INT8 operands themselves, no workspace.
 struct Int8SmallParams {
