@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(32 * kMidWarps + 32, 1) k_int8_mid(const Int8M
     const uint32_t done = smem_addr(&bars.done);
     volatile int *abort_flag = &bars.abort_word;
     const int tid = static_cast<int>(threadIdx.x);
-    const uint32_t warp = warp_index(), lane = lane_index();
+    const uint32_t warp = warp_uniform(warp_index()), lane = lane_index();
     const int buf_cols = (Nt + 31) / 32 * 32;          // columns of a tensor memory buffer
 
     if (tid == 0) {
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(32 * kMidWarps + 32, 1) k_int8_mid(const Int8M
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    const uint32_t tmem_base = bars.tmem;
+    const uint32_t tmem_base = warp_uniform(bars.tmem);
     const WaitGuard guard{abort_flag, p.status, p.wait_limit};
     grid_launch_dependents();
     grid_dependency_wait();
@@ -436,13 +436,14 @@ __global__ void __launch_bounds__(32 * kMidWarps + 32, 1) k_int8_mid(const Int8M
                 load(x[d], at + kMidGroups * AHEAD);
             }
         }
-    } else if (lane == 0) {
+    } else {
         // ------------------------------------------------------------ MMA issuer
         const uint32_t idesc = idesc_f16_f32(128, static_cast<uint32_t>(Nt));
         for (int s = 0; s < steps; ++s) {
             const int stage = s % kMidStages;
-            if (!wait_bounded(full0 + 8u * stage, static_cast<uint32_t>(s / kMidStages) & 1u, guard,
-                              SITE_TILED_MMA_FULL))
+            if (!__all_sync(0xffffffffu,
+                            wait_bounded(full0 + 8u * stage, static_cast<uint32_t>(s / kMidStages) & 1u,
+                                         guard, SITE_TILED_MMA_FULL)))
                 break;
             tc_fence_after_sync();
             const uint32_t d = tmem_base + static_cast<uint32_t>(s / kChunkSteps * buf_cols);
@@ -450,11 +451,11 @@ __global__ void __launch_bounds__(32 * kMidWarps + 32, 1) k_int8_mid(const Int8M
             const uint64_t bd = sw128_kmajor_desc(sW + stage * stage_bytes + w_bytes);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-                mma_f16<false>(d, ad + 2u * kk, bd + 2u * kk, idesc,
-                               (s % kChunkSteps > 0 || kk > 0) ? 1u : 0u);
-            mma_commit(empty0 + 8u * stage);
+                mma_f16_elect<false>(d, ad + 2u * kk, bd + 2u * kk, idesc,
+                                     (s % kChunkSteps > 0 || kk > 0) ? 1u : 0u);
+            mma_commit_elect<false>(empty0 + 8u * stage);
         }
-        mma_commit(done);
+        mma_commit_elect<false>(done);
     }
     __syncwarp();
     // All MMAs have read shared memory and written tensor memory (after a
@@ -669,7 +670,7 @@ __global__ void __launch_bounds__(Int8Layout<PAIR, BN, STAGES, CPW, EB>::kThread
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + L::kBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
-    const uint32_t warp = warp_index(), lane = lane_index();
+    const uint32_t warp = warp_uniform(warp_index()), lane = lane_index();
     const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
     const int first_tile = static_cast<int>(PAIR ? blockIdx.x >> 1 : blockIdx.x);
     const int tile_stride = static_cast<int>(PAIR ? gridDim.x >> 1 : gridDim.x);
@@ -708,7 +709,7 @@ __global__ void __launch_bounds__(Int8Layout<PAIR, BN, STAGES, CPW, EB>::kThread
     else
         __syncthreads();
     tc_fence_after_sync();
-    const uint32_t tmem_base = *tmem_slot;
+    const uint32_t tmem_base = warp_uniform(*tmem_slot);
     const WaitGuard guard{abort_flag, p.status, p.wait_limit};
 
     grid_launch_dependents();
@@ -784,7 +785,7 @@ __global__ void __launch_bounds__(Int8Layout<PAIR, BN, STAGES, CPW, EB>::kThread
                                p.wait_limit, (SITE_DRAIN << 8) | 4u);
                 }
             }
-        } else if (warp == 1 && lane == 0 && rank == 0) {
+        } else if (warp == 1 && rank == 0) {
             // ---------------------------------------------------------- MMA issuer
             constexpr uint32_t idesc = idesc_f16_f32(L::kTileM, BN);
             int stage = 0;
@@ -795,47 +796,40 @@ __global__ void __launch_bounds__(Int8Layout<PAIR, BN, STAGES, CPW, EB>::kThread
                 for (int g = 0; g < p.steps; ++g) {
                     const uint32_t buf = it % L::kBufs;
                     const int in_chunk = g % kChunkSteps;
-                    if ((in_chunk == 0 && !wait_bounded(tempty_bar(buf), ((it / L::kBufs) & 1u) ^ 1u,
-                                                        guard, SITE_TILED_MMA_TMEM)) ||
-                        !wait_bounded(full_bar(stage), phase, guard, SITE_TILED_MMA_FULL) ||
-                        (PAIR && !wait_bounded(pfull_bar(stage), phase, guard, SITE_PAIR_PEER))) {
-                        ok = false;
+                    ok = __all_sync(
+                        0xffffffffu,
+                        (in_chunk > 0 || wait_bounded(tempty_bar(buf), ((it / L::kBufs) & 1u) ^ 1u,
+                                                      guard, SITE_TILED_MMA_TMEM)) &&
+                            wait_bounded(full_bar(stage), phase, guard, SITE_TILED_MMA_FULL) &&
+                            (!PAIR ||
+                             wait_bounded(pfull_bar(stage), phase, guard, SITE_PAIR_PEER)));
+                    if (!ok)
                         break;
-                    }
                     tc_fence_after_sync();
                     const uint32_t d = tmem_base + buf * BN;
                     const uint64_t ad = sw128_kmajor_desc(sA + stage * L::kABytes);
                     const uint64_t bd = sw128_kmajor_desc(sB + stage * L::kBBytes);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_f16<PAIR>(d, ad + 2u * kk, bd + 2u * kk, idesc,
-                                      (in_chunk > 0 || kk > 0) ? 1u : 0u);
+                        mma_f16_elect<PAIR>(d, ad + 2u * kk, bd + 2u * kk, idesc,
+                                            (in_chunk > 0 || kk > 0) ? 1u : 0u);
                     const bool last = in_chunk == kChunkSteps - 1 || g == p.steps - 1;
-                    if constexpr (PAIR) {
-                        mma_commit_pair_mc(empty_bar(stage), 3);
-                        if (last)
-                            mma_commit_pair_mc(tfull_bar(buf), 3);
-                    } else {
-                        mma_commit(empty_bar(stage));
-                        if (last)
-                            mma_commit(tfull_bar(buf));
-                    }
-                    if (last)
+                    mma_commit_elect<PAIR>(empty_bar(stage));
+                    if (last) {
+                        mma_commit_elect<PAIR>(tfull_bar(buf));
                         ++it;
+                    }
                     if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
             }
-            if (!ok)
+            if (!ok && lane == 0)
                 abort_peer();
             // Every MMA has finished reading shared memory and writing TMEM
             // before the CTA (pair) can pass its final barrier.
-            if constexpr (PAIR)
-                mma_commit_pair_mc(drain_bar, 1);
-            else
-                mma_commit(drain_bar);
+            mma_commit_elect<PAIR>(drain_bar, 1);
             wait_drain(drain_bar, 0, p.status, p.wait_limit, (SITE_DRAIN << 8) | 4u);
         } else if (PAIR && warp == 1 && lane == 0) {
             // ---------------------------------------------------------- forwarder (rank 1)

@@ -19,6 +19,9 @@ __device__ __forceinline__ uint32_t smem_addr(const void *p)
 
 __device__ __forceinline__ uint32_t warp_index() { return threadIdx.x >> 5; }
 __device__ __forceinline__ uint32_t lane_index() { return threadIdx.x & 31u; }
+// A value that is the same in every lane, in a form the compiler knows to be so
+// (see mma_f16_elect).
+__device__ __forceinline__ uint32_t warp_uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // Programmatic dependent launch: wait for the previous grid's memory, and let
 // the next grid start its prologue.  Both are no-ops without the launch attribute.
@@ -479,28 +482,56 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr)
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-// As mma_e4m3 (mma_e4m3_pair with PAIR) with fp16 operands: kind::f16, K = 16
-// per instruction, fp32 D.  The instruction descriptor's fields lie where
-// kind::f8f6f4 has them, fp16 being operand format 0.
+// kind::f16 with fp16 operands and fp32 D, K = 16 per instruction.  The
+// instruction descriptor's fields lie where kind::f8f6f4 has them, fp16 being
+// operand format 0.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t m, uint32_t n)
 {
     return (1u << 4) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
+
+// The issue of MMAs and commits by one elected lane of a converged warp, the
+// same lane every time.  A loop that a whole warp walks keeps its addresses and
+// descriptors in uniform registers, which is where the tcgen05 instructions
+// take them from; issued from a branch that only lane 0 takes, four MMAs and a
+// commit cost about 400 cycles.
 template <bool PAIR>
-__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                        uint32_t idesc, uint32_t accumulate)
+__device__ __forceinline__ void mma_f16_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t accumulate)
 {
     if constexpr (PAIR)
-        asm volatile("{\n\t.reg .pred p;\n\t"
+        asm volatile("{\n\t.reg .pred p, q;\n\t"
+                     "elect.sync _|q, 0xffffffff;\n\t"
                      "setp.ne.b32 p, %4, 0;\n\t"
-                     "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+                     "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
                      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
                      : "memory");
     else
-        asm volatile("{\n\t.reg .pred p;\n\t"
+        asm volatile("{\n\t.reg .pred p, q;\n\t"
+                     "elect.sync _|q, 0xffffffff;\n\t"
                      "setp.ne.b32 p, %4, 0;\n\t"
-                     "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+                     "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
                      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+                     : "memory");
+}
+
+// As mma_commit (mma_commit_pair_mc to the CTAs of cta_mask with PAIR), by the
+// lane that issued the MMAs.
+template <bool PAIR>
+__device__ __forceinline__ void mma_commit_elect(uint32_t bar, uint16_t cta_mask = 3)
+{
+    if constexpr (PAIR)
+        asm volatile("{\n\t.reg .pred q;\n\t"
+                     "elect.sync _|q, 0xffffffff;\n\t"
+                     "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::"
+                     "cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+                     "h"(cta_mask)
+                     : "memory");
+    else
+        asm volatile("{\n\t.reg .pred q;\n\t"
+                     "elect.sync _|q, 0xffffffff;\n\t"
+                     "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                     "\n\t}" ::"r"(bar)
                      : "memory");
 }
 
