@@ -777,7 +777,7 @@ struct Int8Plan {
 Int8Plan int8_plan(int64_t M, int64_t N, int64_t K)
 {
     Int8Plan pl;
-    pl.Kp = std::max<int64_t>(cdiv(K, 64), 1) * 64;
+    pl.Kp = std::max<int64_t>(cdiv(K, 128), 1) * 128;
     pl.chunk = std::max<int64_t>(kInt8ChunkBytes / (pl.Kp * 2) / 256, 1) * 256;
     pl.chunk = std::min(pl.chunk, M);
     auto up = [](int64_t x) { return static_cast<size_t>((x + 255) / 256 * 256); };
@@ -920,7 +920,7 @@ w8a8_status run_int8(const void *A, int64_t lda, const float *a_s, const void *B
         p.C = static_cast<uint8_t *>(C) + r0 * ldc * eb;
         p.M = static_cast<int>(rows);
         p.N = static_cast<int>(N);
-        p.steps = static_cast<int>(pl.Kp / 64);
+        p.steps = static_cast<int>(pl.Kp / 128);
         p.ldc = ldc;
         p.out_kind = out;
         p.status = info.status;

@@ -14,7 +14,7 @@
 // the INT8 product at the fp16 tensor rate, to the bit.
 //
 // Two launches: k_int8_widen writes both operands as fp16 into the workspace
-// (rows padded with zeros to whole 64-column steps, so that any size, stride
+// (rows padded with zeros to whole 128-column stages, so that any size, stride
 // and alignment of the INT8 operands is as good as another), k_int8_mma
 // multiplies them.
 #include <algorithm>
@@ -27,9 +27,10 @@ namespace w8a8 {
 
 namespace {
 
-// A stage holds 64 columns of K (one 128-byte fp16 row); an accumulator takes
-// the products of this many stages: 512 columns.
+// An accumulator takes the products of 512 columns: this many steps of 64 (one
+// 128-byte fp16 row each), or stages of 128.
 constexpr int kChunkSteps = 8;
+constexpr int kChunkStages = 4;
 
 // ------------------------------------------------------------------ widening
 
@@ -611,8 +612,12 @@ template <bool PAIR, int BN, int STAGES, int CPW, int EB> struct Int8Layout {
     static constexpr int kTileM = PAIR ? 256 : 128;
     static constexpr int kPromoWG = BN / CPW;
     static constexpr int kThreads = 128 + 128 * kPromoWG;
-    static constexpr uint32_t kABytes = 128u * 128u;                             // this CTA's rows of A
-    static constexpr uint32_t kBBytes = static_cast<uint32_t>(PAIR ? BN / 2 : BN) * 128u;
+    // A stage: 128 columns of K, as two 64-column halves of this CTA's rows of A
+    // (128) and of B.  (One wait and one commit for eight MMAs: the issuing warp
+    // takes longer over four with theirs than the tensor core.)
+    static constexpr uint32_t kAHalf = 128u * 128u;
+    static constexpr uint32_t kBHalf = static_cast<uint32_t>(PAIR ? BN / 2 : BN) * 128u;
+    static constexpr uint32_t kABytes = 2 * kAHalf, kBBytes = 2 * kBHalf;
     static constexpr int kBufs = 512 / BN;
     static constexpr uint32_t kTmemCols = 512;
     static constexpr size_t kStageBytes = STAGES * (kABytes + kBBytes);
@@ -751,8 +756,13 @@ __global__ void __launch_bounds__(Int8Layout<PAIR, BN, STAGES, CPW, EB>::kThread
                         in_bounds(brow < p.num_n_tiles * BN, p.status, SITE_BOUNDS_B);
                     if (issued != p.debug_skip_tma && in) {
                         mbar_arrive_expect_tx(full_bar(stage), L::kABytes + L::kBBytes);
-                        tma_load_2d(sA + stage * L::kABytes, &tmA, full_bar(stage), g * 128, arow);
-                        tma_load_2d(sB + stage * L::kBBytes, &tmB, full_bar(stage), g * 128, brow);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            tma_load_2d(sA + stage * L::kABytes + h * L::kAHalf, &tmA, full_bar(stage),
+                                        g * 256 + 128 * h, arow);
+                            tma_load_2d(sB + stage * L::kBBytes + h * L::kBHalf, &tmB, full_bar(stage),
+                                        g * 256 + 128 * h, brow);
+                        }
                     }
                     ++issued;
                     if (++stage == STAGES) {
@@ -795,7 +805,7 @@ __global__ void __launch_bounds__(Int8Layout<PAIR, BN, STAGES, CPW, EB>::kThread
             for (int t = first_tile; ok && t < p.num_tiles; t += tile_stride) {
                 for (int g = 0; g < p.steps; ++g) {
                     const uint32_t buf = it % L::kBufs;
-                    const int in_chunk = g % kChunkSteps;
+                    const int in_chunk = g % kChunkStages;
                     ok = __all_sync(
                         0xffffffffu,
                         (in_chunk > 0 || wait_bounded(tempty_bar(buf), ((it / L::kBufs) & 1u) ^ 1u,
@@ -810,10 +820,11 @@ __global__ void __launch_bounds__(Int8Layout<PAIR, BN, STAGES, CPW, EB>::kThread
                     const uint64_t ad = sw128_kmajor_desc(sA + stage * L::kABytes);
                     const uint64_t bd = sw128_kmajor_desc(sB + stage * L::kBBytes);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_f16_elect<PAIR>(d, ad + 2u * kk, bd + 2u * kk, idesc,
+                    for (int kk = 0; kk < 8; ++kk)
+                        mma_f16_elect<PAIR>(d, ad + 2u * (kk % 4) + (kk / 4) * (L::kAHalf >> 4),
+                                            bd + 2u * (kk % 4) + (kk / 4) * (L::kBHalf >> 4), idesc,
                                             (in_chunk > 0 || kk > 0) ? 1u : 0u);
-                    const bool last = in_chunk == kChunkSteps - 1 || g == p.steps - 1;
+                    const bool last = in_chunk == kChunkStages - 1 || g == p.steps - 1;
                     mma_commit_elect<PAIR>(empty_bar(stage));
                     if (last) {
                         mma_commit_elect<PAIR>(tfull_bar(buf));
@@ -879,7 +890,7 @@ __global__ void __launch_bounds__(Int8Layout<PAIR, BN, STAGES, CPW, EB>::kThread
 #pragma unroll
             for (int j = 0; j < CPW; ++j)
                 acc[j] = 0;
-            for (int g = 0; g < p.steps; g += kChunkSteps) {
+            for (int g = 0; g < p.steps; g += kChunkStages) {
                 const uint32_t buf = it % L::kBufs;
                 ok = __all_sync(0xffffffffu, wait_bounded(tfull_bar(buf), (it / L::kBufs) & 1u,
                                                           guard, SITE_TILED_PROMOTE));
@@ -1057,8 +1068,8 @@ cudaError_t launch_int8_widen(const Int8WidenParams &p, int access, int grid, cu
 cudaError_t launch_int8_mma(const CUtensorMap &tmA, const CUtensorMap &tmB, const CUtensorMap &tmC,
                             const Int8Params &p, int pair, const LaunchCfg &cfg)
 {
-    return pair ? launch_mma<true, 256, 6, 128, 1>(tmA, tmB, tmC, p, cfg, nullptr)
-                : launch_mma<false, 128, 6, 64, 1>(tmA, tmB, tmC, p, cfg, nullptr);
+    return pair ? launch_mma<true, 256, 3, 128, 1>(tmA, tmB, tmC, p, cfg, nullptr)
+                : launch_mma<false, 128, 3, 64, 1>(tmA, tmB, tmC, p, cfg, nullptr);
 }
 
 int int8_max_pairs()
@@ -1070,7 +1081,7 @@ int int8_max_pairs()
     if (cached[dev] > 0)
         return cached[dev];
     const CUtensorMap none = {};
-    if (launch_mma<true, 256, 6, 128, 1>(none, none, none, Int8Params{}, LaunchCfg{}, &n) !=
+    if (launch_mma<true, 256, 3, 128, 1>(none, none, none, Int8Params{}, LaunchCfg{}, &n) !=
             cudaSuccess ||
         n <= 0)
         return -1;

@@ -209,7 +209,7 @@ cudaError_t launch_ragged(const CUtensorMap &tmA, const CUtensorMap &tmB, const 
                           const RaggedParams &p, int bn, const LaunchCfg &cfg);
 
 // INT8 matmul.  Widening: rows_a rows of A and rows_b of B (INT8, K columns) to
-// fp16 rows of Kp columns (a multiple of 64; zeros past K).
+// fp16 rows of Kp columns (a multiple of 128; zeros past K).
 struct Int8WidenParams {
     const uint8_t *A, *B;
     uint8_t *A16, *B16;        // [rows, Kp] fp16
@@ -252,7 +252,7 @@ struct Int8Params {
     const float *b_s;          // [N]
     void *C;                   // [M, ldc]
     int M, N;
-    int steps;                 // 64-column steps of K
+    int steps;                 // 128-column stages of K
     long long ldc;
     int num_m_tiles, num_n_tiles, num_tiles;
     int out_kind;
