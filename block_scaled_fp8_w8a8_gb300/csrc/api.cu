@@ -980,8 +980,9 @@ w8a8_status run_ragged(const void *A, const float *a_s, const void *B, const flo
     if (o && o->grid_limit)
         grid = std::min<int64_t>(grid, o->grid_limit);
     w8a8_status st;
-    CUtensorMap mA, mB, mC;
+    CUtensorMap mA, mTile, mB, mC;
     if ((st = encode_u8_map(&mA, A, M, K, 32)) != W8A8_OK ||
+        (st = encode_u8_map(&mTile, A, M, K, 128)) != W8A8_OK ||
         (st = encode_u8_map(&mB, B, N, K, bn, gr.experts)) != W8A8_OK ||
         (st = encode_out_map(&mC, C, M, N, out, out == W8A8_OUT_FP32 ? 16 : 32, 32,
                              CU_TENSOR_MAP_SWIZZLE_64B)) != W8A8_OK)
@@ -1006,9 +1007,8 @@ w8a8_status run_ragged(const void *A, const float *a_s, const void *B, const flo
     p.wait_limit = (o && o->wait_limit_cycles) ? o->wait_limit_cycles : kDefaultWaitLimit;
     LaunchCfg cfg = {};
     cfg.grid = static_cast<int>(grid);
-    cfg.pdl = o ? o->pdl : 0;
     cfg.stream = stream;
-    const cudaError_t e = launch_ragged(mA, mB, mC, p, bn, cfg);
+    const cudaError_t e = launch_ragged(mA, mTile, mB, mC, p, bn, cfg);
     return e == cudaSuccess ? W8A8_OK : cuda_fail(e, "kernel launch");
 }
 

@@ -440,12 +440,17 @@ __global__ void __launch_bounds__(32 * kMidWarps + 32, 1) k_int8_mid(const Int8M
     } else {
         // ------------------------------------------------------------ MMA issuer
         const uint32_t idesc = idesc_f16_f32(128, static_cast<uint32_t>(Nt));
+        bool ready = false;
         for (int s = 0; s < steps; ++s) {
             const int stage = s % kMidStages;
             if (!__all_sync(0xffffffffu,
-                            wait_bounded(full0 + 8u * stage, static_cast<uint32_t>(s / kMidStages) & 1u,
-                                         guard, SITE_TILED_MMA_FULL)))
+                            ready || wait_bounded(full0 + 8u * stage,
+                                                  static_cast<uint32_t>(s / kMidStages) & 1u, guard,
+                                                  SITE_TILED_MMA_FULL)))
                 break;
+            // the next step's probe answers while this one's MMAs are issued
+            ready = mbar_test_wait(full0 + 8u * ((s + 1) % kMidStages),
+                                   static_cast<uint32_t>((s + 1) / kMidStages) & 1u);
             tc_fence_after_sync();
             const uint32_t d = tmem_base + static_cast<uint32_t>(s / kChunkSteps * buf_cols);
             const uint64_t ad = sw128_kmajor_desc(sW + stage * stage_bytes);
@@ -626,8 +631,8 @@ template <bool PAIR, int BN, int STAGES, int CPW, int EB> struct Int8Layout {
     static constexpr int kRegsLow = 56, kRegsHigh = 224;
     static_assert(kThreads == 384 && 128 * kRegsLow + 256 * kRegsHigh <= 384 * 168,
                   "register split exceeds the launch's registers");
-    // full, pair_full, empty per stage; tfull, tempty per buffer; drain
-    static constexpr int kBars = 3 * STAGES + 2 * kBufs + 1;
+    // full, empty per stage; tfull, tempty per buffer; drain
+    static constexpr int kBars = 2 * STAGES + 2 * kBufs + 1;
     static constexpr size_t kSmem = 1024 + kStageBytes + kEpiBytes + kScaleBytes + kBars * 8 + 16;
     static_assert(kSmem <= 232448, "shared memory per CTA");
 };
@@ -667,11 +672,10 @@ __global__ void __launch_bounds__(Int8Layout<PAIR, BN, STAGES, CPW, EB>::kThread
                                                   L::kScaleBytes);
     const uint32_t bar0 = smem_addr(bars);
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
-    auto pfull_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
-    auto empty_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };
-    auto tfull_bar = [&](int b) { return bar0 + 8u * (3 * STAGES + b); };
-    auto tempty_bar = [&](int b) { return bar0 + 8u * (3 * STAGES + L::kBufs + b); };
-    const uint32_t drain_bar = bar0 + 8u * (3 * STAGES + 2 * L::kBufs);
+    auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+    auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };
+    auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + L::kBufs + b); };
+    const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 2 * L::kBufs);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + L::kBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -682,8 +686,8 @@ __global__ void __launch_bounds__(Int8Layout<PAIR, BN, STAGES, CPW, EB>::kThread
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(full_bar(s), 1);
-            mbar_init(pfull_bar(s), 1);
+            // rank 0 of a pair also counts its peer's landed stage
+            mbar_init(full_bar(s), PAIR && rank == 0 ? 2 : 1);
             mbar_init(empty_bar(s), 1);
         }
         for (int b = 0; b < L::kBufs; ++b) {
@@ -801,7 +805,7 @@ __global__ void __launch_bounds__(Int8Layout<PAIR, BN, STAGES, CPW, EB>::kThread
             int stage = 0;
             uint32_t phase = 0;
             uint32_t it = 0;                 // accumulator uses
-            bool ok = true;
+            bool ok = true, ready = false;
             for (int t = first_tile; ok && t < p.num_tiles; t += tile_stride) {
                 for (int g = 0; g < p.steps; ++g) {
                     const uint32_t buf = it % L::kBufs;
@@ -810,11 +814,13 @@ __global__ void __launch_bounds__(Int8Layout<PAIR, BN, STAGES, CPW, EB>::kThread
                         0xffffffffu,
                         (in_chunk > 0 || wait_bounded(tempty_bar(buf), ((it / L::kBufs) & 1u) ^ 1u,
                                                       guard, SITE_TILED_MMA_TMEM)) &&
-                            wait_bounded(full_bar(stage), phase, guard, SITE_TILED_MMA_FULL) &&
-                            (!PAIR ||
-                             wait_bounded(pfull_bar(stage), phase, guard, SITE_PAIR_PEER)));
+                            (ready || wait_bounded(full_bar(stage), phase, guard,
+                                                   SITE_TILED_MMA_FULL)));
                     if (!ok)
                         break;
+                    // the next stage's probe answers while this one's MMAs are issued
+                    ready = mbar_test_wait(full_bar(stage + 1 < STAGES ? stage + 1 : 0),
+                                           stage + 1 < STAGES ? phase : phase ^ 1u);
                     tc_fence_after_sync();
                     const uint32_t d = tmem_base + buf * BN;
                     const uint64_t ad = sw128_kmajor_desc(sA + stage * L::kABytes);
@@ -853,7 +859,7 @@ __global__ void __launch_bounds__(Int8Layout<PAIR, BN, STAGES, CPW, EB>::kThread
                         ok = false;
                         break;
                     }
-                    mbar_arrive_remote(cluster_map(pfull_bar(stage), 0));
+                    mbar_arrive_remote(cluster_map(full_bar(stage), 0));
                     if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1u;
@@ -867,10 +873,11 @@ __global__ void __launch_bounds__(Int8Layout<PAIR, BN, STAGES, CPW, EB>::kThread
     } else {
         // -------------------------------------------------------------- promotion + epilogue
         regs_alloc<L::kRegsHigh>();
-        const int h = static_cast<int>(warp / 4) - 1;
-        const uint32_t q = warp & 3u;
-        const uint32_t epi_buf = sEpi + (warp - 4u) * 2048u * EB;
-        float *my_bs = scales + (warp - 4u) * CPW;
+        const uint32_t w = warp_index();       // (not the uniform copy: it costs spills here)
+        const int h = static_cast<int>(w / 4) - 1;
+        const uint32_t q = w & 3u;
+        const uint32_t epi_buf = sEpi + (w - 4u) * 2048u * EB;
+        float *my_bs = scales + (w - 4u) * CPW;
         const bool fp32 = p.out_kind == OUT_FP32, bf = p.out_kind == OUT_BF16;
         uint32_t it = 0;
         bool ok = true;

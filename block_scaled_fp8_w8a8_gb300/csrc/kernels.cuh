@@ -203,10 +203,10 @@ struct RaggedParams {
     unsigned *status;
     unsigned long long wait_limit;
 };
-// tmA: boxes of 32 rows; tmB: 3-D [experts, N, K], boxes of bn rows; tmC as for
-// launch_tiled.  bn: 128 or 256.
-cudaError_t launch_ragged(const CUtensorMap &tmA, const CUtensorMap &tmB, const CUtensorMap &tmC,
-                          const RaggedParams &p, int bn, const LaunchCfg &cfg);
+// tmA, tmTile: A in boxes of 32 and of 128 rows; tmB: 3-D [experts, N, K], boxes of
+// bn rows; tmC as for launch_tiled.  bn: 128 or 256.
+cudaError_t launch_ragged(const CUtensorMap &tmA, const CUtensorMap &tmTile, const CUtensorMap &tmB,
+                          const CUtensorMap &tmC, const RaggedParams &p, int bn, const LaunchCfg &cfg);
 
 // INT8 matmul.  Widening: rows_a rows of A and rows_b of B (INT8, K columns) to
 // fp16 rows of Kp columns (a multiple of 128; zeros past K).

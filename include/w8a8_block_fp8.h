@@ -441,8 +441,10 @@ w8a8_status w8a8_block_fp8_grouped_matmul_contiguous(const void *A_dev, const fl
  * decrease or leave [0, M] give unspecified results but never an out-of-bounds
  * access.  E <= W8A8_RAGGED_MAX_EXPERTS; M == 0 is a no-op, E == 0 with rows is
  * W8A8_ERR_INVALID_ARG; other shape rules as for the plain tensor-core call.
- * One kernel for every routing, from one row to full prefill; no workspace.
- * opts: variant AUTO or TILED; block_n_tile 128 or 256, grid_limit, pdl,
+ * One kernel for every routing, from one row to full prefill; no workspace.  Its
+ * launch may overlap the end of the work before it on the stream, which it waits
+ * for on the device, whatever opts->pdl says.
+ * opts: variant AUTO or TILED; block_n_tile 128 or 256, grid_limit,
  * wait_limit_cycles and the test hooks apply.
  */
 #define W8A8_RAGGED_MAX_EXPERTS 1024
