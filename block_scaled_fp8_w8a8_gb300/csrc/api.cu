@@ -746,26 +746,35 @@ w8a8_status run_generic(const void *A, const float *a_s, const void *B, const fl
 // the workspace (longer problems run in several), and the workspace itself: the
 // counter block that every workspace starts with, the widened A rows, B.
 constexpr int64_t kInt8ChunkBytes = 512ll << 20;
-// Up to this many tokens AUTO takes the kernel that widens in registers.
-constexpr int64_t kInt8SmallM = 64;
+// Up to this many tokens AUTO takes the kernel that widens in registers (N = K =
+// 4096: 6.9 against 10.1 us at M = 16, 10.3 against 11.2 at M = 32, 21 against 12.5
+// at M = 48, for it and for the one that widens on the way to shared memory).
+constexpr int64_t kInt8SmallM = 32;
 
-// ... and up to this many, where K allows it, the one that widens on the way to
-// shared memory.
-constexpr int64_t kInt8MidM = 1024;
-
-bool int8_mid(int64_t M, int64_t N, int64_t K, const w8a8_options *o, int sm_count, int *tile,
-              int *splits)
+// The kernel of an INT8 call: by the caller's variant, else by M and, above
+// kInt8SmallM, by the kernels' estimated times (N = K = 4096: SWAPAB 12 / 22 / 42
+// us and TILED 28 / 30 / 30 us at M = 64 / 256 / 512, TILED_PAIR 40 and TILED 46 us
+// at M = 1024).  tile and splits are SWAPAB's.
+int int8_variant(int64_t M, int64_t N, int64_t K, const w8a8_options *o, int sm_count, int *tile,
+                 int *splits)
 {
+    *tile = o ? o->m_tile : 0;
+    *splits = o ? o->split_k : 0;
     const int v = o ? o->variant : W8A8_VARIANT_AUTO;
-    return (v == W8A8_VARIANT_SWAPAB || (v == W8A8_VARIANT_AUTO && M <= kInt8MidM)) &&
-           int8_mid_plan(static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), sm_count, tile,
-                         splits);
-}
-
-bool int8_small(int64_t M, const w8a8_options *o)
-{
-    const int v = o ? o->variant : W8A8_VARIANT_AUTO;
-    return v == W8A8_VARIANT_SMALLM || (v == W8A8_VARIANT_AUTO && M <= kInt8SmallM);
+    if (v != W8A8_VARIANT_AUTO && v != W8A8_VARIANT_SWAPAB)
+        return v;
+    if (v == W8A8_VARIANT_AUTO && M <= kInt8SmallM)
+        return W8A8_VARIANT_SMALLM;
+    const int m = static_cast<int>(M), n = static_cast<int>(N), k = static_cast<int>(K);
+    const float tiled = int8_tiled_cost(m, n, k, sm_count, 0), pair = int8_tiled_cost(m, n, k, sm_count, 1);
+    // (more than some thousand tokens never pay here: the plan is not searched)
+    const float mid = v == W8A8_VARIANT_SWAPAB || M <= 4096 ? int8_mid_plan(m, n, k, sm_count, tile, splits)
+                                                            : -1.f;
+    if (v == W8A8_VARIANT_SWAPAB)
+        return mid < 0.f ? W8A8_VARIANT_AUTO : v;       // AUTO: K is too long for it
+    if (mid >= 0.f && mid <= std::min(tiled, pair))
+        return W8A8_VARIANT_SWAPAB;
+    return pair < tiled ? W8A8_VARIANT_TILED_PAIR : W8A8_VARIANT_TILED;
 }
 
 struct Int8Plan {
@@ -801,6 +810,8 @@ w8a8_status check_int8(int64_t M, int64_t N, int64_t K, const w8a8_options *o)
                     "the INT8 matmul takes variant AUTO, SMALLM, SWAPAB, TILED or TILED_PAIR");
     if (v == W8A8_VARIANT_SMALLM && M > (1 << 20))
         return fail(W8A8_ERR_UNSUPPORTED, "M=%lld is too large for the small-M variant", (long long)M);
+    if (o && o->split_k > 8)
+        return fail(W8A8_ERR_UNSUPPORTED, "the INT8 matmul splits K over at most 8 CTAs");
     if (K > W8A8_INT8_MAX_K)
         return fail(W8A8_ERR_UNSUPPORTED, "K=%lld: sums of more than %d products may leave 32 bits",
                     (long long)K, W8A8_INT8_MAX_K);
@@ -842,7 +853,12 @@ w8a8_status run_int8(const void *A, int64_t lda, const float *a_s, const void *B
         return aligned(A, a) && aligned(B, a) && lda % a == 0 && ldb % a == 0 && K % a == 0;
     };
     const int access = fits(16) ? 16 : fits(8) ? 8 : fits(4) ? 4 : 1;
-    if (int8_small(M, o)) {
+    int tile = 0, splits = 0;
+    const int v = int8_variant(M, N, K, o, info.sm_count, &tile, &splits);
+    if (v == W8A8_VARIANT_AUTO)
+        return fail(W8A8_ERR_UNSUPPORTED, "M=%lld, K=%lld: too long for the SWAPAB form's tensor memory",
+                    (long long)M, (long long)K);
+    if (v == W8A8_VARIANT_SMALLM) {
         Int8SmallParams p = {};
         p.A = static_cast<const uint8_t *>(A);
         p.B = static_cast<const uint8_t *>(B);
@@ -862,8 +878,7 @@ w8a8_status run_int8(const void *A, int64_t lda, const float *a_s, const void *B
     }
     const unsigned long long limit =
         (o && o->wait_limit_cycles) ? o->wait_limit_cycles : kDefaultWaitLimit;
-    int tile = 0, splits = 0;
-    if (int8_mid(M, N, K, o, info.sm_count, &tile, &splits)) {
+    if (v == W8A8_VARIANT_SWAPAB) {
         Int8MidParams p = {};
         p.A = static_cast<const uint8_t *>(A);
         p.B = static_cast<const uint8_t *>(B);
@@ -885,15 +900,11 @@ w8a8_status run_int8(const void *A, int64_t lda, const float *a_s, const void *B
         const cudaError_t e = launch_int8_mid(p, access, splits, stream);
         return e == cudaSuccess ? W8A8_OK : cuda_fail(e, "kernel launch");
     }
-    if (o && o->variant == W8A8_VARIANT_SWAPAB)
-        return fail(W8A8_ERR_UNSUPPORTED, "M=%lld, K=%lld: too long for the SWAPAB form's tensor memory",
-                    (long long)M, (long long)K);
     const Int8Plan pl = int8_plan(M, N, K);
     void *ws = nullptr;
     if ((st = acquire_workspace(o, dev, stream, pl.workspace(), &ws)) != W8A8_OK)
         return st;
     uint8_t *A16 = static_cast<uint8_t *>(ws) + kCounterBytes, *B16 = A16 + pl.a_bytes;
-    const int v = o ? o->variant : W8A8_VARIANT_AUTO;
     for (int64_t r0 = 0; r0 < M; r0 += pl.chunk) {
         const int64_t rows = std::min(pl.chunk, M - r0);
         Int8WidenParams w = {};
@@ -928,9 +939,7 @@ w8a8_status run_int8(const void *A, int64_t lda, const float *a_s, const void *B
         p.debug_skip_tma = (o && o->debug_skip_load > 0) ? o->debug_skip_load - 1 : -1;
         if (W8A8_DEBUG_BOUNDS && o && o->debug_bad_index && p.debug_skip_tma < 0)
             p.debug_skip_tma = kDebugBadFirstLoad;
-        const int64_t pair_tiles = cdiv(rows, 256) * cdiv(N, 256);
-        const bool pair = v == W8A8_VARIANT_TILED_PAIR ||
-                          (v == W8A8_VARIANT_AUTO && pair_tiles * 2 >= info.sm_count / 2);
+        const bool pair = v == W8A8_VARIANT_TILED_PAIR;
         const int tm = pair ? 256 : 128;
         p.num_m_tiles = static_cast<int>(cdiv(rows, tm));
         p.num_n_tiles = static_cast<int>(cdiv(N, tm));
@@ -1611,8 +1620,9 @@ w8a8_status w8a8_int8_matmul(const void *A_dev, int64_t lda, const float *a_s_de
 
 size_t w8a8_int8_workspace_size(int64_t M, int64_t N, int64_t K, const w8a8_options *opts)
 {
-    if (check_int8(M, N, K, opts) != W8A8_OK || M == 0 || N == 0 || int8_small(M, opts) ||
-        (opts && opts->variant == W8A8_VARIANT_SWAPAB))
+    const int v = opts ? opts->variant : W8A8_VARIANT_AUTO;
+    if (check_int8(M, N, K, opts) != W8A8_OK || M == 0 || N == 0 || v == W8A8_VARIANT_SMALLM ||
+        v == W8A8_VARIANT_SWAPAB || (v == W8A8_VARIANT_AUTO && M <= kInt8SmallM))
         return 0;
     return int8_plan(M, N, K).workspace();
 }

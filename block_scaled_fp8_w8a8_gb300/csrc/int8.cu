@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kWidenThreads) k_int8_widen(const Int8WidenPar
 
 // ------------------------------------------------------------------ few tokens
 
-// Up to 64 tokens: the weights' bytes bound the time, and each is widened in
+// Up to 32 tokens: the weights' bytes bound the time, and each is widened in
 // registers right after its load (writing them as fp16 first would triple
 // their traffic).  A warp multiplies 16 MT weight rows (the MMA's M side) with 8
 // NT tokens on mma.sync fp16 tiles, whose operands a thread builds from plain
@@ -137,7 +137,7 @@ __device__ __forceinline__ uint32_t word_of(const uint4 &v, int j)
 
 // UN: 64-column steps whose loads are issued together.
 template <int NT, int MT, int UN, int ACCESS>
-__global__ void __launch_bounds__(32 * kSmallWarps, NT <= 4 ? 2 : 1) k_int8_small(const Int8SmallParams p)
+__global__ void __launch_bounds__(32 * kSmallWarps, 2) k_int8_small(const Int8SmallParams p)
 {
     constexpr int kRows = 16 * MT, kTokens = 8 * NT;
     __shared__ int sums[kRows * kTokens];            // [token][row]
@@ -324,6 +324,7 @@ constexpr int kMidGroup = 8;
 constexpr int kMidGroups = 2;
 constexpr int kMidWarps = kMidGroup * kMidGroups;
 constexpr int kMidStages = 4;
+constexpr int kMidSmem = 1024 + kMidStages * (128 + 256) * 128;     // the most: 256 tokens
 
 struct MidBars {
     uint64_t full[kMidStages], empty[kMidStages], done;
@@ -588,8 +589,7 @@ cudaError_t launch_mid_t(const Int8MidParams &p, int access, int splits, cudaStr
     if (e == cudaSuccess && (dev < 0 || dev >= kMaxDeviceFlags))
         e = cudaErrorInvalidDevice;
     if (e == cudaSuccess && !smem_set[a][dev]) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 1024 + kMidStages * (128 + 256) * 128);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMidSmem);
         smem_set[a][dev] = e == cudaSuccess;
     }
     if (e != cudaSuccess)
@@ -1016,34 +1016,96 @@ cudaError_t launch_int8_small(const Int8SmallParams &p, int access, int sm_count
         return launch_small_t<1, 1, 4>(p, access, sm_count, stream);
     if (p.M <= 16)
         return launch_small_t<2, 1, 4>(p, access, sm_count, stream);
-    if (p.M <= 32)
-        return launch_small_t<4, 2, 2>(p, access, sm_count, stream);
-    return launch_small_t<8, 2, 1>(p, access, sm_count, stream);
+    return launch_small_t<4, 2, 2>(p, access, sm_count, stream);
 }
 
-bool int8_mid_plan(int M, int N, int K, int sm_count, int *tile_tokens, int *splits)
+namespace {
+
+// CTAs of k_int8_mid that run at once when they come in clusters of s (1, 2, 4, 8):
+// one to an SM, and clusters do not cross the GPU's processing clusters, so that
+// those of 8 leave some SMs idle.
+int mid_at_once(int s, int sm_count)
+{
+    static volatile int cached[kMaxDeviceFlags][9] = {};
+    int dev = 0, n = 0;
+    if (s == 1 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDeviceFlags)
+        return sm_count;
+    if (cached[dev][s])
+        return cached[dev][s];
+    auto kernel = k_int8_mid<6, 2, 16>;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(1, s, 1);
+    lc.blockDim = dim3(32 * kMidWarps + 32, 1, 1);
+    lc.dynamicSmemBytes = kMidSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = static_cast<unsigned>(s);
+    attr[0].val.clusterDim.z = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMidSmem) !=
+            cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &lc) != cudaSuccess || n <= 0) {
+        cudaGetLastError();
+        n = std::max(1, sm_count / s / 2);
+    }
+    cached[dev][s] = n * s;
+    return n * s;
+}
+
+// Estimated microseconds of k_int8_mid with token tiles of nt and K split by s:
+// per wave of CTAs a fixed part, its steps, and adding up and storing the tile.
+// (Fitted on a GB300 for N x K from 512 x 512 to 8192 x 4096 and M from 48 to 1024;
+// a step's 740 to 1330 cycles are the MMA issue for few tokens and the shared
+// memory's bandwidth for many.)
+float mid_cost(int blocks, int tiles, int nt, int s, int steps, int sm_count)
+{
+    const int at_once = mid_at_once(s, sm_count);
+    const float waves = static_cast<float>((blocks * static_cast<long long>(tiles) * s + at_once - 1) / at_once);
+    const float cycles = 5500.f + static_cast<float>((steps + s - 1) / s) * (700.f + 2.45f * nt) +
+                         (s > 1 ? 50.f : 30.f) * nt;
+    return 1.f + waves * cycles / 1900.f;
+}
+
+}  // namespace
+
+float int8_mid_plan(int M, int N, int K, int sm_count, int *tile_tokens, int *splits)
 {
     const int steps = (K + 63) / 64, blocks = (N + 127) / 128;
-    // Token tiles of equal size, as few as 256 tokens allow; more of them while
-    // the GPU would otherwise stand half empty with K split as far as it goes
-    // (two steps a CTA, clusters of 8).
-    const int most = std::max(1, std::min(8, steps / 2));
-    int tiles = (M + 255) / 256;
-    while (static_cast<long long>(blocks) * tiles * most * 2 <= sm_count && M / (tiles + 1) >= 64)
-        ++tiles;
-    const int nt = ((M + tiles - 1) / tiles + 15) / 16 * 16;
-    tiles = (M + nt - 1) / nt;
-    // The 512 columns of tensor memory hold 512 / nt buffers of 8 steps.
-    const int room = 512 / ((nt + 31) / 32 * 32) * kChunkSteps;
-    int s = 1;
-    while (s < 8 && ((steps + s - 1) / s > room ||
-                     (static_cast<long long>(blocks) * tiles * s * 2 <= sm_count && s * 2 <= most)))
-        s *= 2;
-    if ((steps + s - 1) / s > room || tiles > 65535)
-        return false;
-    *tile_tokens = nt;
-    *splits = s;
-    return true;
+    const int fixed_nt = *tile_tokens, fixed_s = *splits;
+    float best = -1.f;
+    const int fewest = fixed_nt ? (M + fixed_nt - 1) / fixed_nt : (M + 255) / 256;
+    const int most = fixed_nt ? fewest : std::min(fewest + 7, (M + 15) / 16);
+    for (int tiles = fewest; tiles <= most; ++tiles) {
+        const int nt = fixed_nt ? fixed_nt : ((M + tiles - 1) / tiles + 15) / 16 * 16;
+        // The 512 columns of tensor memory hold 512 / nt buffers of 8 steps.
+        const int room = 512 / ((nt + 31) / 32 * 32) * kChunkSteps;
+        for (int s = fixed_s ? fixed_s : 1; s <= (fixed_s ? fixed_s : 8); s *= 2) {
+            if ((steps + s - 1) / s > room || (!fixed_s && s > 1 && s > steps) || tiles > 65535)
+                continue;
+            const float c = mid_cost(blocks, (M + nt - 1) / nt, nt, s, steps, sm_count);
+            if (best < 0.f || c < best) {
+                best = c;
+                *tile_tokens = nt;
+                *splits = s;
+            }
+        }
+    }
+    return best;
+}
+
+// The same for widening in a launch of its own and multiplying 128 x 128 tiles or
+// a CTA pair's 256 x 256: both launches, 5 bytes of traffic a widened element
+// (most of it in L2), and per wave a tile's stages of 128 columns and its stores.
+float int8_tiled_cost(int M, int N, int K, int sm_count, int pair)
+{
+    const long long tile = pair ? 256 : 128, at_once = pair ? sm_count / 2 : sm_count;
+    const long long tiles = (M + tile - 1) / tile * ((N + tile - 1) / tile);
+    const float stages = static_cast<float>((K + 127) / 128);
+    return 5.f + (static_cast<float>(M) + static_cast<float>(N)) * static_cast<float>(K) * 5.f / 11e6f +
+           static_cast<float>((tiles + at_once - 1) / at_once) *
+               (pair ? 3.f + 0.68f * stages : 0.4f + 0.52f * stages);
 }
 
 cudaError_t launch_int8_mid(const Int8MidParams &p, int access, int splits, cudaStream_t stream)

@@ -244,8 +244,9 @@ struct Int8MidParams {
     unsigned *status;
     unsigned long long wait_limit;
 };
-// Token tile and cluster size for a problem; false where K is too long for them.
-bool int8_mid_plan(int M, int N, int K, int sm_count, int *tile_tokens, int *splits);
+// Token tile and cluster size for a problem, where not set, and the estimated
+// microseconds; < 0 where K is too long for them.
+float int8_mid_plan(int M, int N, int K, int sm_count, int *tile_tokens, int *splits);
 cudaError_t launch_int8_mid(const Int8MidParams &p, int access, int splits, cudaStream_t stream);
 struct Int8Params {
     const float *a_s;          // [M]
@@ -265,6 +266,7 @@ struct Int8Params {
 // rows.  pair: CTA pairs on 256 x 256 tiles (cfg.grid CTAs, even), else 128 x 128.
 cudaError_t launch_int8_mma(const CUtensorMap &tmA, const CUtensorMap &tmB, const CUtensorMap &tmC,
                             const Int8Params &p, int pair, const LaunchCfg &cfg);
+float int8_tiled_cost(int M, int N, int K, int sm_count, int pair);   // estimated microseconds
 int int8_max_pairs();          // CTA pairs that can be resident at once; < 0 on error
 
 // Shared memory bytes each kernel configuration needs (0 = unsupported configuration).
