@@ -18,7 +18,7 @@ from ._binding import (  # noqa: F401
     W8A8_OUT_FP16, W8A8_OUT_FP32, W8A8_VARIANT_AUTO, W8A8_VARIANT_TILED, W8A8_VARIANT_SWAPAB,
     W8A8_VARIANT_SPLITK, W8A8_VARIANT_SPLITK_CLUSTER, W8A8_VARIANT_SMALLM, W8A8_VARIANT_TILED_PAIR,
     W8A8_VARIANT_GENERIC, w8a8_block_fp8_matmul_strided,
-    _stream, check, library_path, load_library,
+    _opts_address, _stream, check, library_path, load_library,
     w8a8_abi_version, w8a8_debug_bounds_build, w8a8_env_config, debug_bounds_requested,
     w8a8_block_fp8_host_staging_size, w8a8_block_fp8_matmul, w8a8_block_fp8_matmul_ex,
     w8a8_block_fp8_matmul_host, w8a8_block_fp8_plan, w8a8_block_fp8_workspace_size,
@@ -243,10 +243,10 @@ def grouped_matmul_ragged(A, a_s, B, b_s, offsets, out_dtype="bf16", out=None, s
     if not (A.is_contiguous() and a_s.is_contiguous() and B.is_contiguous() and
             b_s.is_contiguous() and out.is_contiguous() and offsets.is_contiguous()):
         raise W8A8Error(W8A8_ERR_UNSUPPORTED, "tensors must be contiguous row-major")
+    o = options(**opts) if opts else None
     st = load_library().w8a8_block_fp8_grouped_matmul_ragged(
         A.data_ptr(), a_s.data_ptr(), B.data_ptr(), b_s.data_ptr(), out.data_ptr(),
-        offsets.data_ptr(), M, E, N, K, 128, 128, code, _stream(stream),
-        options(**opts) if opts else None)
+        offsets.data_ptr(), M, E, N, K, 128, 128, code, _stream(stream), _opts_address(o))
     if st:
         check(st)
     return out
@@ -273,10 +273,10 @@ def int8_matmul(A, a_s, B, b_s, out_dtype="bf16", out=None, stream=None, **opts)
         _want(out, (M, N), "out")
     if not (a_s.is_contiguous() and b_s.is_contiguous()):
         raise W8A8Error(W8A8_ERR_UNSUPPORTED, "scales must be contiguous")
+    o = options(**opts) if opts else None
     st = load_library().w8a8_int8_matmul(
         A.data_ptr(), _rows(A), a_s.data_ptr(), B.data_ptr(), _rows(B), b_s.data_ptr(),
-        out.data_ptr(), _rows(out), M, N, K, code, _stream(stream),
-        options(**opts) if opts else None)
+        out.data_ptr(), _rows(out), M, N, K, code, _stream(stream), _opts_address(o))
     if st:
         check(st)
     return out

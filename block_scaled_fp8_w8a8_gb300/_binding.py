@@ -9,6 +9,8 @@ fallback: without it every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 from . import build as _build
@@ -102,6 +104,25 @@ def library_path() -> str:
     return _build.lib_path(debug_bounds_requested())
 
 
+# The functions that pycall.c has entries for, in bind()'s order.
+_PYCALL = ("w8a8_sandwich_norm", "w8a8_block_fp8_grouped_matmul_ragged", "w8a8_int8_matmul",
+           "w8a8_quantize_int8_per_token")
+
+
+def _bind_pycall(lib):
+    """Give those functions of the loaded library their entries from the extension
+    module where it has been built; they take the same arguments."""
+    path = _build.pycall_path()
+    if not os.path.exists(path):
+        return
+    loader = importlib.machinery.ExtensionFileLoader("_w8a8_pycall", path)
+    mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_w8a8_pycall", loader))
+    loader.exec_module(mod)
+    mod.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _PYCALL))
+    for n in _PYCALL:
+        setattr(lib, n, getattr(mod, n))
+
+
 def load_library():
     """Load the built shared library (raises if it has not been built)."""
     global _lib
@@ -131,10 +152,10 @@ def load_library():
     lib.w8a8_block_fp8_grouped_matmul_contiguous.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64,
                                                              i64, i64, i32, i32, i32, vp, opt_p]
     lib.w8a8_block_fp8_grouped_matmul_contiguous.restype = ctypes.c_int
+    # (the options of these two by address: see _bind_pycall)
     lib.w8a8_block_fp8_grouped_matmul_ragged.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64,
-                                                         i64, i32, i32, i32, vp, opt_p]
-    lib.w8a8_int8_matmul.argtypes = [vp, i64, vp, vp, i64, vp, vp, i64, i64, i64, i64, i32, vp,
-                                     opt_p]
+                                                         i64, i32, i32, i32, vp, vp]
+    lib.w8a8_int8_matmul.argtypes = [vp, i64, vp, vp, i64, vp, vp, i64, i64, i64, i64, i32, vp, vp]
     lib.w8a8_int8_workspace_size.argtypes = [i64, i64, i64, opt_p]
     lib.w8a8_int8_workspace_size.restype = sz
     lib.w8a8_quantize_int8_per_token.argtypes = [vp, i32, i64, vp, i64, vp, i64, i64, vp]
@@ -173,6 +194,7 @@ def load_library():
                  "w8a8_block_fp8_grouped_matmul_ragged", "w8a8_int8_matmul",
                  "w8a8_quantize_int8_per_token", "w8a8_sandwich_norm"):
         getattr(lib, name).restype = ctypes.c_int
+    _bind_pycall(lib)
     _lib = lib
     return lib
 
@@ -217,6 +239,11 @@ def _stream(s):
 
 def _opts(o):
     return ctypes.byref(o) if o is not None else None
+
+
+def _opts_address(o):
+    """Address of the caller's options, which stay alive through the call."""
+    return ctypes.addressof(o) if o is not None else None
 
 
 def w8a8_block_fp8_matmul(A, a_s, B, b_s, C, M, N, K, block_n=128, block_k=128,
@@ -291,7 +318,7 @@ def w8a8_block_fp8_grouped_matmul_ragged(A, a_s, B, b_s, C, offsets, M, E, N, K,
                                          stream=None, opts=None) -> int:
     return load_library().w8a8_block_fp8_grouped_matmul_ragged(
         _ptr(A), _ptr(a_s), _ptr(B), _ptr(b_s), _ptr(C), _ptr(offsets), M, E, N, K,
-        block_n, block_k, out_dtype, _stream(stream), _opts(opts))
+        block_n, block_k, out_dtype, _stream(stream), _opts_address(opts))
 
 
 W8A8_RAGGED_MAX_EXPERTS = 1024
@@ -304,7 +331,7 @@ def w8a8_int8_matmul(A, lda, a_s, B, ldb, b_s, C, ldc, M, N, K, out_dtype=W8A8_O
                      stream=None, opts=None) -> int:
     return load_library().w8a8_int8_matmul(_ptr(A), lda, _ptr(a_s), _ptr(B), ldb, _ptr(b_s),
                                            _ptr(C), ldc, M, N, K, out_dtype, _stream(stream),
-                                           _opts(opts))
+                                           _opts_address(opts))
 
 
 def w8a8_int8_workspace_size(M, N, K, opts=None) -> int:

@@ -10,6 +10,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 SRC = os.path.join(HERE, "csrc")
@@ -55,11 +56,36 @@ def _stale(obj: str, src: str) -> bool:
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
 
 
+def pycall_path() -> str:
+    """The extension module with the small kernels' Python entries (see pycall.c)."""
+    return os.path.join(OUT, "_w8a8_pycall" + sysconfig.get_config_var("EXT_SUFFIX"))
+
+
+def build_pycall(force: bool = False) -> str | None:
+    """Compile pycall.c for this interpreter; None where Python's headers are missing
+    (the binding then makes the same calls through ctypes)."""
+    src, lib = os.path.join(SRC, "pycall.c"), pycall_path()
+    include = sysconfig.get_paths()["include"]
+    cc = shutil.which(os.environ.get("CC", "gcc"))
+    if cc is None or not os.path.exists(os.path.join(include, "Python.h")):
+        return None
+    if force or not os.path.exists(lib) or os.path.getmtime(src) > os.path.getmtime(lib):
+        os.makedirs(OUT, exist_ok=True)
+        tmp = lib + ".tmp"
+        r = subprocess.run([cc, "-O2", "-shared", "-fPIC", "-I", include, src, "-o", tmp],
+                           capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{cc} failed for pycall.c:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, lib)
+    return lib
+
+
 def build(force: bool = False, verbose: bool = False, debug_bounds: bool = False) -> str:
     """Compile and link the library; debug_bounds=True builds the debug-bounds
     library (its own objects and .so) instead of the release one."""
     out = OUT_DEBUG if debug_bounds else OUT
     os.makedirs(out, exist_ok=True)
+    build_pycall(force)
     cc = nvcc()
 
     def compile_unit(u):
