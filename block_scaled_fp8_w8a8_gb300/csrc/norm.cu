@@ -229,9 +229,13 @@ __device__ __forceinline__ void store_fp8(const NormParams &p, long long m, uint
 }
 
 // One row per CTA (per warp where row_threads is 32).  HELD: the row stays in
-// the threads' registers; otherwise in dynamic shared memory (D floats).
-template <int HK, int XK, int VEC, bool HELD>
-__global__ void __launch_bounds__(kMaxThreads) k_sandwich_norm(const NormParams p)
+// the threads' registers; otherwise in dynamic shared memory (D floats).  EARLY:
+// at most kEarlyThreads, whose registers also hold the weights and the gate,
+// loaded along with the row.
+constexpr int kEarlyThreads = 512;
+template <int HK, int XK, int VEC, bool HELD, bool EARLY>
+__global__ void __launch_bounds__(EARLY ? kEarlyThreads : kMaxThreads)
+    k_sandwich_norm(const NormParams p)
 {
     extern __shared__ float held[];
     __shared__ float part[3][32];
@@ -255,7 +259,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_sandwich_norm(const NormParams 
         p.gate ? static_cast<const uint8_t *>(p.gate) + (m / p.gate_rows) * D * kHB : nullptr;
     const int steps = HELD ? kN : (D + T * VEC - 1) / (T * VEC);
 
-    float v[kN][VEC], xv[kN][VEC];
+    float v[kN][VEC], xv[kN][VEC], early[EARLY ? 3 : 1][kN][VEC];
     // Chunk i of this thread: VEC elements from (i T + tid) VEC; D % VEC == 0.
     auto at = [&](int i) { return (i * T + tid) * VEC; };
 
@@ -265,10 +269,26 @@ __global__ void __launch_bounds__(kMaxThreads) k_sandwich_norm(const NormParams 
     for (int i = 0; i < (HELD ? kN : steps); ++i) {
         const int e = at(i);
         float(&w)[VEC] = v[HELD ? i : 0];
-        if (e < D) {
+        if (HELD && e < D) {
             load_vec<HK, VEC>(hrow, e, w);
-            if (HELD)
-                load_vec<XK, VEC>(xrow, e, xv[HELD ? i : 0]);
+            load_vec<XK, VEC>(xrow, e, xv[HELD ? i : 0]);
+            if constexpr (EARLY) {
+                if (p.w_post)
+                    load_vec<HK, VEC>(p.w_post, e, early[0][i]);
+                if (grow)
+                    load_vec<HK, VEC>(grow, e, early[1][i]);
+                if (p.w_pre)
+                    load_vec<HK, VEC>(p.w_pre, e, early[2][i]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < (HELD ? kN : steps); ++i) {
+        const int e = at(i);
+        float(&w)[VEC] = v[HELD ? i : 0];
+        if (e < D) {
+            if (!HELD)
+                load_vec<HK, VEC>(hrow, e, w);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
                 ss = fmaf(w[j], w[j], ss);
@@ -288,10 +308,12 @@ __global__ void __launch_bounds__(kMaxThreads) k_sandwich_norm(const NormParams 
         float(&w)[VEC] = v[HELD ? i : 0];
         float(&xw)[VEC] = xv[HELD ? i : 0];
         if (e < D) {
-            float wp[VEC], g[VEC];
-            if (p.w_post)
+            float wp_[VEC], g_[VEC];
+            float(&wp)[VEC] = EARLY ? early[0][HELD ? i : 0] : wp_;
+            float(&g)[VEC] = EARLY ? early[EARLY ? 1 : 0][HELD ? i : 0] : g_;
+            if (!EARLY && p.w_post)
                 load_vec<HK, VEC>(p.w_post, e, wp);
-            if (grow)
+            if (!EARLY && grow)
                 load_vec<HK, VEC>(grow, e, g);
             if (!HELD)
                 load_vec<XK, VEC>(xrow, e, xw);
@@ -324,8 +346,9 @@ __global__ void __launch_bounds__(kMaxThreads) k_sandwich_norm(const NormParams 
         float(&w)[VEC] = v[HELD ? i : 0];
         const bool in = e < D;
         if (in) {
-            float wp[VEC];
-            if (p.w_pre)
+            float wp_[VEC];
+            float(&wp)[VEC] = EARLY ? early[EARLY ? 2 : 0][HELD ? i : 0] : wp_;
+            if (!EARLY && p.w_pre)
                 load_vec<HK, VEC>(p.w_pre, e, wp);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
@@ -388,8 +411,28 @@ struct RingParams {
     int stages;
     uint32_t h_bytes, x_bytes;             // of one row
     float inv_d;                           // 1 / D
-    long long gate_step, gate_rest;        // gridDim.x / gate_rows and the remainder
     unsigned long long wait_limit;
+};
+
+// A persistent CTA's rows.  Round robin, so that the CTAs read one neighbourhood
+// of memory at a time (16384 rows of 3943: 120 against 140 us for a run of rows
+// each); but neighbours where the gate's row changes among them, as it then
+// changes seldom.  (g_rest counts rows since the gate's last change: with one row
+// of the gate for all it never reaches gate_rows.)
+struct RowWalk {
+    int first, step, last;             // M < 2^31, and so is every m + step
+    __device__ explicit RowWalk(const NormParams &p)
+    {
+        if (p.gate && p.gate_rows < p.M) {
+            first = static_cast<int>(p.M * blockIdx.x / gridDim.x);
+            step = 1;
+            last = static_cast<int>(p.M * (blockIdx.x + 1) / gridDim.x);
+        } else {
+            first = static_cast<int>(blockIdx.x);
+            step = static_cast<int>(gridDim.x);
+            last = static_cast<int>(p.M);
+        }
+    }
 };
 
 // Eight elements as four fp32 pairs, from shared or global memory.
@@ -472,7 +515,7 @@ template <int THREADS> __device__ __forceinline__ float cta_sum(float v, float *
     __syncthreads();
     v = 0.f;
 #pragma unroll
-    for (int i = 0; i < THREADS / 128; ++i) {
+    for (int i = 0; i < (THREADS + 127) / 128; ++i) {
         const float4 f = reinterpret_cast<const float4 *>(part)[i];
         v += (f.x + f.y) + (f.z + f.w);
     }
@@ -525,8 +568,8 @@ __global__ void __launch_bounds__(THREADS, PER_SM) k_sandwich_ring(const RingPar
     const bool in0 = FULL || e0 < D, in1 = FULL || e1 < D;
     const uint32_t ring0 = smem_addr(ring), bar0 = smem_addr(bars);
     const uint32_t stage_bytes = rp.h_bytes + rp.x_bytes;
-    if (tid < 64)
-        part[tid >> 5][(tid >> 4) & 1][tid & 15] = 0.f;
+    for (int i = tid; i < 64; i += static_cast<int>(blockDim.x))
+        (&part[0][0][0])[i] = 0.f;
     if (tid == 0) {
         for (int s = 0; s < rp.stages; ++s)
             mbar_init(bar0 + 8u * s, 1);
@@ -537,7 +580,8 @@ __global__ void __launch_bounds__(THREADS, PER_SM) k_sandwich_ring(const RingPar
     const WaitGuard guard{abort_flag, p.status, rp.wait_limit};
     grid_launch_dependents();
     grid_dependency_wait();
-    const long long first = blockIdx.x, stride = gridDim.x;
+    const RowWalk walk(p);
+    const int first = walk.first, step = walk.step, last = walk.last;
     // (thread 0; after a timeout nothing more is copied)
     uint32_t filled = 0, last_phase = 0;   // stages filled at all, and their last fills' parities
     auto fill = [&](long long m, int s) {
@@ -552,8 +596,8 @@ __global__ void __launch_bounds__(THREADS, PER_SM) k_sandwich_ring(const RingPar
                   bar);
     };
     if (tid == 0)
-        for (int s = 0; s < rp.stages && first + s * stride < p.M; ++s)
-            fill(first + s * stride, s);
+        for (int s = 0; s < rp.stages && first + s * step < last; ++s)
+            fill(first + s * step, s);
 
     const uint64_t one2 = pack2f(1.f, 1.f), scale2 = pack2f(p.res_scale, p.res_scale);
     uint64_t wpost[8];
@@ -598,23 +642,22 @@ __global__ void __launch_bounds__(THREADS, PER_SM) k_sandwich_ring(const RingPar
             }
         }
     };
-    long long g = 0, g_rest = 0;
+    int g = 0, g_rest = 0;             // the gate's row, and rows since it began
     if (p.gate) {
-        g = first / p.gate_rows;
-        g_rest = first - g * p.gate_rows;
+        g = static_cast<int>(first / p.gate_rows);
+        g_rest = static_cast<int>(first - g * p.gate_rows);
     }
     load_post(g);
 
-    uint8_t *orow = static_cast<uint8_t *>(p.x_out) + first * p.ld_xo * kXB;
+    uint8_t *orow = static_cast<uint8_t *>(p.x_out) + static_cast<long long>(first) * p.ld_xo * kXB;
     const int yb = p.y_kind == W8A8_NORM_SAME ? kHB : 1;
-    uint8_t *yrow = static_cast<uint8_t *>(p.y) + first * p.ld_y * yb;
-    const long long o_step = stride * p.ld_xo * kXB, y_step = stride * p.ld_y * yb;
     const int per_row = p.y_kind == W8A8_NORM_FP8 ? (D + 127) / 128 : 1;      // scales
-    float *srow = p.scales + first * per_row;
-    const long long s_step = stride * per_row;
+    uint8_t *yrow = static_cast<uint8_t *>(p.y) + static_cast<long long>(first) * p.ld_y * yb;
+    const long long o_step = step * p.ld_xo * kXB, y_step = step * p.ld_y * yb, s_step = static_cast<long long>(step) * per_row;
+    float *srow = p.scales + static_cast<long long>(first) * per_row;
     int stage = 0, odd = 0;
     uint32_t phase = 0;
-    for (long long m = first; m < p.M; m += stride, odd ^= 1, orow += o_step, yrow += y_step,
+    for (int m = first; m < last; m += step, odd ^= 1, orow += o_step, yrow += y_step,
                    srow += s_step) {
         // A wait that runs out leaves garbage in the row, an entry in the
         // status word and the abort flag, which ends every later wait at once.
@@ -662,8 +705,8 @@ __global__ void __launch_bounds__(THREADS, PER_SM) k_sandwich_ring(const RingPar
             __syncthreads();
         }
         // Every thread has read its part of the stage: refill it.
-        if (tid == 0 && m + rp.stages * stride < p.M)
-            fill(m + rp.stages * stride, stage);
+        if (tid == 0 && m + rp.stages * step < last)
+            fill(m + rp.stages * step, stage);
         if (++stage == rp.stages) {
             stage = 0;
             phase ^= 1u;
@@ -701,16 +744,9 @@ __global__ void __launch_bounds__(THREADS, PER_SM) k_sandwich_ring(const RingPar
             if (tid == 0)
                 *srow = s;
         }
-        if (p.gate) {
-            const long long was = g;
-            g += rp.gate_step;
-            g_rest += rp.gate_rest;
-            if (g_rest >= p.gate_rows) {
-                g_rest -= p.gate_rows;
-                ++g;
-            }
-            if (g != was && m + stride < p.M)
-                load_post(g);
+        if (p.gate && ++g_rest == p.gate_rows && m + step < last) {
+            g_rest = 0;
+            load_post(++g);
         }
     }
     // After a timeout the copies still in flight land before the CTA leaves.
@@ -719,6 +755,240 @@ __global__ void __launch_bounds__(THREADS, PER_SM) k_sandwich_ring(const RingPar
             if (filled >> s & 1u)
                 wait_drain(bar0 + 8u * s, last_phase >> s & 1u, p.status, rp.wait_limit,
                            (SITE_DRAIN << 8) | 4u);
+}
+
+// ------------------------------------------------------------------ rows of any width
+
+// Many rows of a width that leaves them off 16-byte boundaries (so not for FP8
+// codes).  All tensors are dense, so row m starts at
+// element m D of each; a thread takes 16 elements from an element index that is
+// a multiple of 8, which every tensor loads and stores in whole 16-byte words
+// (the words at a row's two ends hold elements of its neighbours: masked on the
+// way in, stored one by one on the way out).  Column 16 t + k of a norm's
+// weights lies at [k][t] in shared memory, so that a row shifted by s of 8
+// elements reads them without bank conflicts.  The next row's words wait in
+// registers while this one's reductions run.
+struct FlatParams {
+    NormParams n;
+    float inv_d;
+};
+
+template <int KIND> struct Raw16 {
+    static constexpr int kWords = KIND == W8A8_IN_FP32 ? 16 : 8;
+    uint32_t w[kWords];
+    // 16 elements at element index f, those before `total`
+    __device__ __forceinline__ void load(const void *base, long long f, long long total)
+    {
+        constexpr int kB = KIND == W8A8_IN_FP32 ? 4 : 2;
+        const uint8_t *p = static_cast<const uint8_t *>(base) + f * kB;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            uint32_t *d = w + c * (kWords / 2);
+            if (f + 8 * c + 8 <= total) {
+                const uint4 *q = reinterpret_cast<const uint4 *>(p + 8 * c * kB);
+#pragma unroll
+                for (int i = 0; i < kWords / 8; ++i) {
+                    const uint4 v = q[i];
+                    d[4 * i] = v.x, d[4 * i + 1] = v.y, d[4 * i + 2] = v.z, d[4 * i + 3] = v.w;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kWords / 2; ++i)
+                    d[i] = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (f + 8 * c + j >= total)
+                        continue;
+                    if constexpr (KIND == W8A8_IN_FP32)
+                        d[j] = reinterpret_cast<const uint32_t *>(p)[8 * c + j];
+                    else
+                        d[j / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(p)[8 * c + j])
+                                    << (16 * (j & 1));
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ float operator[](int j) const { return quant::element<KIND>(w, j); }
+};
+
+// The elements of v that lie in columns 0 .. D-1, v's first one being column c0.
+template <int KIND>
+__device__ __forceinline__ void store_flat(uint8_t *row, int c0, int D, const float (&v)[16])
+{
+    constexpr int kB = KIND == W8A8_IN_FP32 ? 4 : 2;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const int at = c0 + 8 * c;
+        if (at >= 0 && at + 8 <= D) {
+            store_vec<KIND, 8>(row + static_cast<long long>(at) * kB, 0,
+                               reinterpret_cast<const float(&)[8]>(v[8 * c]));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (at + j >= 0 && at + j < D)
+                    Elem<KIND>::store(reinterpret_cast<typename Elem<KIND>::T *>(row) + at + j,
+                                      v[8 * c + j]);
+        }
+    }
+}
+
+template <int HK, int XK, int THREADS, int PER_SM>
+__global__ void __launch_bounds__(THREADS, PER_SM) k_sandwich_flat(const FlatParams fp)
+{
+    // post [16][kPitch], pre [16][kPitch]; the pitch keeps the columns of a
+    // coalesced load, 16 words of a row apart, in different banks
+    extern __shared__ float weights[];
+    constexpr int kPitch = THREADS + 2;
+    __shared__ __align__(16) float part[2][2][THREADS < 128 ? 4 : THREADS / 32];
+    __shared__ float part_max[2][32];
+    constexpr int kHB = HK == W8A8_IN_FP32 ? 4 : 2, kXB = XK == W8A8_IN_FP32 ? 4 : 2;
+    const NormParams &p = fp.n;
+    const int tid = static_cast<int>(threadIdx.x), D = p.D;
+    const long long total = p.M * D;
+    const RowWalk walk(p);
+    const int first = walk.first, step = walk.step, last = walk.last;
+    for (int i = tid; i < static_cast<int>(sizeof(part) / 4); i += static_cast<int>(blockDim.x))
+        (&part[0][0][0])[i] = 0.f;
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const bool has_post = p.w_post || p.gate;
+    using HE = Elem<HK>;
+    Raw16<HK> hn;
+    Raw16<XK> xn;
+    auto fetch = [&](long long row) {
+        const long long f = (row * D & ~7ll) + 16 * tid;
+        if (f < (row + 1) * D && in_bounds(row < p.M, p.status, SITE_BOUNDS_A)) {
+            hn.load(p.h, f, total);
+            xn.load(p.x, f, total);
+        }
+    };
+    fetch(first);
+    // Columns tid + i blockDim.x of a vector for eight i from h, 0 past D: every load
+    // before any use.
+    auto columns = [&](const void *w, int h, float (&v)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int c = tid + (h + i) * static_cast<int>(blockDim.x);
+            v[i] = c < D ? HE::load(static_cast<const typename HE::T *>(w) + c) : 0.f;
+        }
+    };
+    auto put = [&](float *dst, int h, const float (&v)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int c = tid + (h + i) * static_cast<int>(blockDim.x);
+            dst[(c & 15) * kPitch + (c >> 4)] = v[i];
+        }
+    };
+    auto load_post = [&](long long g) {
+        for (int h = 0; h < 16; h += 8) {
+            float w[8], u[8];
+            if (p.gate)
+                columns(static_cast<const typename HE::T *>(p.gate) + g * D, h, u);
+            if (p.w_post)
+                columns(p.w_post, h, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                w[i] = !p.gate ? w[i] : p.w_post ? w[i] * u[i] : u[i];
+            put(weights, h, w);
+        }
+    };
+    int g = 0, g_rest = 0;             // the gate's row, and rows since it began
+    if (p.gate) {
+        g = static_cast<int>(first / p.gate_rows);
+        g_rest = static_cast<int>(first - g * p.gate_rows);
+    }
+    if (has_post)
+        load_post(g);
+    if (p.w_pre)
+        for (int h = 0; h < 16; h += 8) {
+            float w[8];
+            columns(p.w_pre, h, w);
+            put(weights + 16 * kPitch, h, w);
+        }
+    __syncthreads();
+
+    const uint32_t w0 = smem_addr(weights) + 4u * tid;
+    int odd = 0;
+    for (int m = first; m < last; m += step, odd ^= 1) {
+        const long long m0 = static_cast<long long>(m) * D;        // the row's first element
+        const int s = static_cast<int>(m0 & 7);
+        const int c0 = 16 * tid - s;                   // column of v[0]
+        const bool any = c0 < D, all = c0 >= 0 && c0 + 16 <= D;
+        float v[16], x[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const bool in = all || (any && c0 + j >= 0 && c0 + j < D);
+            v[j] = in ? hn[j] : 0.f;
+            x[j] = in ? xn[j] : 0.f;
+        }
+        if (m + step < last)
+            fetch(m + step);
+        // weight of v[j]: [j - s][tid], or [j - s + 16][tid - 1]
+        const uint32_t wa = w0 - 4u * s * kPitch;
+        auto weight = [&](int j, int pre) {
+            const uint32_t at = (j < 8 && j < s ? wa + 4u * (16 * kPitch - 1) : wa) +
+                                4u * (j + 16 * pre) * kPitch;
+            float w;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(w) : "r"(at));
+            return w;
+        };
+        float ss = 0.f, inv = 1.f;
+        if (p.w_post) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                ss = fmaf(v[j], v[j], ss);
+            inv = rsqrtf(fmaf(cta_sum<THREADS>(ss, part[odd][0]), fp.inv_d, p.eps));
+        }
+        ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            float u = v[j];
+            if (has_post)
+                u = u * inv * ((j < 8 && j < s && tid == 0) ? 0.f : weight(j, 0));
+            v[j] = fmaf(p.res_scale, x[j], u);
+            ss = fmaf(v[j], v[j], ss);
+        }
+        if (p.x_out && any)
+            store_flat<XK>(static_cast<uint8_t *>(p.x_out) + m0 * kXB, c0, D, v);
+        if (p.w_pre) {
+            inv = rsqrtf(fmaf(cta_sum<THREADS>(ss, part[odd][1]), fp.inv_d, p.eps));
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                v[j] = v[j] * inv * ((j < 8 && j < s && tid == 0) ? 0.f : weight(j, 1));
+        }
+        if (p.y_kind == W8A8_NORM_SAME) {
+            if (any)
+                store_flat<HK>(static_cast<uint8_t *>(p.y) + m0 * kHB, c0, D, v);
+        } else {
+            float amax = 0.f;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                amax = fmaxf(amax, fabsf(v[j]));
+            const float sc = int8_scale(row_reduce<Max>(amax, part_max[odd], false));
+            uint8_t *row = static_cast<uint8_t *>(p.y) + m0;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int at = c0 + 8 * c;
+                if (at >= 0 && at + 8 <= D) {
+                    store_int8<8>(row + at, reinterpret_cast<const float(&)[8]>(v[8 * c]), sc);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (at + j >= 0 && at + j < D)
+                            store_int8<1>(row + at + j, reinterpret_cast<const float(&)[1]>(v[8 * c + j]),
+                                          sc);
+                }
+            }
+            if (tid == 0)
+                p.scales[m] = sc;
+        }
+        if (p.gate && ++g_rest == p.gate_rows && m + step < last) {
+            g_rest = 0;
+            __syncthreads();                       // this row's weights have been read
+            load_post(++g);
+            __syncthreads();
+        }
+    }
 }
 
 struct QuantParams {
@@ -816,7 +1086,9 @@ cudaError_t launch_norm(NormParams p, cudaStream_t stream)
 {
     if (p.D <= kRegRow) {
         p.row_threads = row_threads(p.D);
-        return launch_rows(k_sandwich_norm<HK, XK, VEC, true>, p, p.M, p.row_threads, 0, stream);
+        return launch_rows(p.row_threads <= kEarlyThreads ? k_sandwich_norm<HK, XK, VEC, true, true>
+                                                          : k_sandwich_norm<HK, XK, VEC, true, false>,
+                           p, p.M, p.row_threads, 0, stream);
     }
     static volatile int smem_set[kMaxDeviceFlags] = {};
     int dev = 0;
@@ -824,14 +1096,14 @@ cudaError_t launch_norm(NormParams p, cudaStream_t stream)
     if (e == cudaSuccess && (dev < 0 || dev >= kMaxDeviceFlags))
         e = cudaErrorInvalidDevice;
     if (e == cudaSuccess && !smem_set[dev]) {
-        e = cudaFuncSetAttribute(k_sandwich_norm<HK, XK, VEC, false>,
+        e = cudaFuncSetAttribute(k_sandwich_norm<HK, XK, VEC, false, false>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, W8A8_NORM_MAX_D * 4);
         smem_set[dev] = e == cudaSuccess;
     }
     if (e != cudaSuccess)
         return e;
     p.row_threads = kMaxThreads;
-    return launch_rows(k_sandwich_norm<HK, XK, VEC, false>, p, p.M, kMaxThreads,
+    return launch_rows(k_sandwich_norm<HK, XK, VEC, false, false>, p, p.M, kMaxThreads,
                        static_cast<size_t>(p.D) * 4, stream);
 }
 
@@ -844,7 +1116,7 @@ cudaError_t launch_ring_t(RingParams &r, const DeviceView &dev, cudaStream_t str
     constexpr int kRoom = 220 * 1024;
     auto kernel = k_sandwich_ring<HK, XK, THREADS, PER_SM, FULL>;
     const int T = row_threads(r.n.D);
-    const int per_sm = std::max(1, PER_SM * THREADS / T);
+    const int per_sm = std::min(24, std::max(1, PER_SM * THREADS / T));
     r.h_bytes = static_cast<uint32_t>(r.n.D) * (HK == W8A8_IN_FP32 ? 4 : 2);
     r.x_bytes = static_cast<uint32_t>(r.n.D) * (XK == W8A8_IN_FP32 ? 4 : 2);
     const size_t stage = r.h_bytes + r.x_bytes, weights = r.n.w_pre ? 64 * T : 0;
@@ -860,10 +1132,6 @@ cudaError_t launch_ring_t(RingParams &r, const DeviceView &dev, cudaStream_t str
     if (e != cudaSuccess)
         return e;
     const long long ctas = std::min<long long>(r.n.M, static_cast<long long>(per_sm) * dev.sm_count);
-    if (r.n.gate) {
-        r.gate_step = ctas / r.n.gate_rows;
-        r.gate_rest = ctas % r.n.gate_rows;
-    }
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
     lc.blockDim = dim3(T, 1, 1);
@@ -877,13 +1145,63 @@ cudaError_t launch_ring_t(RingParams &r, const DeviceView &dev, cudaStream_t str
     return cudaLaunchKernelEx(&lc, kernel, r);
 }
 
+template <int HK, int XK, int THREADS, int PER_SM>
+cudaError_t launch_flat_t(const NormParams &p, const DeviceView &dev, cudaStream_t stream)
+{
+    auto kernel = k_sandwich_flat<HK, XK, THREADS, PER_SM>;
+    constexpr int kWeights = 2 * 16 * (THREADS + 2) * 4;
+    static volatile int smem_set[kMaxDeviceFlags] = {};
+    int id = 0;
+    cudaError_t e = cudaGetDevice(&id);
+    if (e == cudaSuccess && !smem_set[id]) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWeights);
+        smem_set[id] = e == cudaSuccess;
+    }
+    if (e != cudaSuccess)
+        return e;
+    const int T = row_threads(p.D + 7);     // a row's shift takes up to seven elements more
+    FlatParams f = {};
+    f.n = p;
+    f.inv_d = 1.f / static_cast<float>(p.D);
+    const int per_sm = PER_SM * THREADS / T;
+    const long long ctas = std::min<long long>(p.M, static_cast<long long>(per_sm) * dev.sm_count);
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+    lc.blockDim = dim3(T, 1, 1);
+    lc.dynamicSmemBytes = kWeights;
+    lc.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelEx(&lc, kernel, f);
+}
+
 template <int HK, int XK>
 cudaError_t launch_norm(const NormParams &p, bool vec, const DeviceView &dev, cudaStream_t stream)
 {
+    // Rows off 16-byte boundaries: the flat kernel where the tensors are dense,
+    // its CTAs get rows enough, and single elements would make narrow accesses
+    // (16384 rows in bf16, flat against direct: of 3943 122 / 577 us, of 513 44 / 84,
+    // of 251 50 / 30; 4096 rows of 513 15.1 / 15.4, 2000 10.6 / 8.5; fp32: 4096 rows
+    // of 7001 98 / 131, of 3943 65 / 60).
+    const int span = p.D + 7;
+    const bool wide = HK == W8A8_IN_FP32 ? p.D > 4096 : p.D >= 1000 || (p.D >= 512 && p.M >= 4096);
+    if (!vec && wide && span <= kRegRow && p.M >= 2 * dev.sm_count && p.ld_h == p.D &&
+        p.ld_x == p.D && p.ld_xo == p.D && p.ld_y == p.D && on(p.h, 16) && on(p.x, 16) &&
+        on(p.x_out, 16) && on(p.y, p.y_kind == W8A8_NORM_SAME ? 16 : 8)) {
+        if (span <= 16 * 256)
+            return launch_flat_t<HK, XK, 256, 3>(p, dev, stream);
+        if (span <= 16 * 512)
+            return launch_flat_t<HK, XK, 512, 1>(p, dev, stream);
+        return launch_flat_t<HK, XK, 1024, 1>(p, dev, stream);
+    }
     // The ring where each of its CTAs gets several rows, and rows are long
-    // enough to be worth a CTA of at least two warps.
-    if (vec && p.D >= 1024 && p.D <= 16 * kRingThreads &&
-        p.M >= 2ll * dev.sm_count * std::max(1, 768 * 16 / p.D)) {
+    // enough to be worth a CTA (16384 rows of 768 to FP8: 26 against 33 us; of 512
+    // 19.5 against 18.9, of 256 14 against 10).
+    if (vec && p.D >= 640 && p.D <= 16 * kRingThreads &&
+        p.M >= 2ll * dev.sm_count * std::min(24, std::max(1, 768 * 16 / p.D))) {
         RingParams r = {};
         r.n = p;
         r.inv_d = 1.f / static_cast<float>(p.D);

@@ -174,7 +174,8 @@ def test_many_rows_on_a_side_stream_and_in_a_graph():
     check(k, r, y)
 
 
-@pytest.mark.parametrize("M,D", [(2500, 1024), (1000, 2056), (701, 4096), (333, 8192), (5000, 1032)])
+@pytest.mark.parametrize("M,D", [(2500, 1024), (1000, 2056), (701, 4096), (333, 8192), (5000, 1032), (8000, 640), (400, 1537), (305, 3943),
+                                 (310, 6001), (304, 12003), (333, 4095), (4100, 517)])
 @pytest.mark.parametrize("dtype,resid", [("bf16", "bf16"), ("fp16", "fp32"), ("fp32", "fp32")])
 def test_many_long_rows(M, D, dtype, resid):
     """Enough rows for the persistent kernel; its codes are those of few rows at a time."""
