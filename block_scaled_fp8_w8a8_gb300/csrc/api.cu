@@ -752,8 +752,8 @@ constexpr int64_t kInt8ChunkBytes = 512ll << 20;
 constexpr int64_t kInt8SmallM = 32;
 
 // The kernel of an INT8 call: by the caller's variant, else by M and, above
-// kInt8SmallM, by the kernels' estimated times (N = K = 4096: SWAPAB 12 / 22 / 42
-// us and TILED 28 / 30 / 30 us at M = 64 / 256 / 512, TILED_PAIR 40 and TILED 46 us
+// kInt8SmallM, by the kernels' estimated times (N = K = 4096: SWAPAB 12 / 22 / 43
+// us and TILED 25 / 25 / 26 us at M = 64 / 256 / 512, TILED_PAIR 35 and TILED 40 us
 // at M = 1024).  tile and splits are SWAPAB's.
 int int8_variant(int64_t M, int64_t N, int64_t K, const w8a8_options *o, int sm_count, int *tile,
                  int *splits)

@@ -79,31 +79,57 @@ __device__ __forceinline__ uint4 load16(const uint8_t *row, int c, int K)
 }
 
 constexpr int kWidenThreads = 256;
+constexpr int kWidenUnroll = 4;
 
-// Both operands in one launch: units of 16 columns, A's first.
+// rows x Kp fp16 from INT8 rows: units of 16 columns, dealt round robin to the
+// grid's threads, kWidenUnroll loads of a thread in flight.
+template <int ACCESS>
+__device__ __forceinline__ void widen_rows(const uint8_t *src, long long ld, uint8_t *dst,
+                                           long long rows, int K, int Kp, unsigned *status)
+{
+    const unsigned per_row = static_cast<unsigned>(Kp) / 16;
+    const unsigned stride = gridDim.x * kWidenThreads;       // units; a row is at most 2^13 of them
+    const unsigned step_r = stride / per_row, step_c = stride - step_r * per_row;
+    const unsigned at = blockIdx.x * kWidenThreads + threadIdx.x;
+    long long r = at / per_row;
+    unsigned c = at % per_row;
+    while (r < rows) {
+        uint4 w[kWidenUnroll];
+        uint8_t *to[kWidenUnroll];
+#pragma unroll
+        for (int i = 0; i < kWidenUnroll; ++i) {
+            to[i] = nullptr;
+            if (r < rows && in_bounds(c < per_row, status, SITE_BOUNDS_WORKSPACE)) {
+                w[i] = load16<ACCESS>(src + r * ld, static_cast<int>(16 * c), K);
+                to[i] = dst + (r * Kp + 16 * c) * 2;
+            }
+            r += step_r;
+            c += step_c;
+            if (c >= per_row) {
+                c -= per_row;
+                ++r;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kWidenUnroll; ++i) {
+            if (!to[i])
+                continue;
+            const uint2 h0 = widen4(w[i].x), h1 = widen4(w[i].y), h2 = widen4(w[i].z),
+                        h3 = widen4(w[i].w);
+            const uint32_t out[8] = {h0.x, h0.y, h1.x, h1.y, h2.x, h2.y, h3.x, h3.y};
+            st_global_v8(to[i], out);            // 32 bytes on a 32-byte boundary
+        }
+    }
+}
+
+// Both operands in one launch.
 template <int ACCESS>
 __global__ void __launch_bounds__(kWidenThreads) k_int8_widen(const Int8WidenParams p)
 {
     grid_launch_dependents();
     grid_dependency_wait();
-    const long long per_row = p.Kp / 16;
-    const long long units_a = p.rows_a * per_row, units = units_a + p.rows_b * per_row;
-    const long long stride = static_cast<long long>(gridDim.x) * kWidenThreads;
-    for (long long u = static_cast<long long>(blockIdx.x) * kWidenThreads + threadIdx.x; u < units;
-         u += stride) {
-        const bool b = u >= units_a;
-        const long long v = b ? u - units_a : u;
-        const long long r = v / per_row;
-        const int c = static_cast<int>(v - r * per_row) * 16;
-        const uint8_t *row = b ? p.B + r * p.ldb : p.A + r * p.lda;
-        if (!in_bounds(r < (b ? p.rows_b : p.rows_a) && c < p.Kp, p.status, SITE_BOUNDS_WORKSPACE))
-            continue;
-        const uint4 w = load16<ACCESS>(row, c, p.K);
-        const uint2 h0 = widen4(w.x), h1 = widen4(w.y), h2 = widen4(w.z), h3 = widen4(w.w);
-        uint4 *dst = reinterpret_cast<uint4 *>((b ? p.B16 : p.A16) + (r * p.Kp + c) * 2);
-        dst[0] = make_uint4(h0.x, h0.y, h1.x, h1.y);
-        dst[1] = make_uint4(h2.x, h2.y, h3.x, h3.y);
-    }
+    widen_rows<ACCESS>(p.A, p.lda, p.A16, p.rows_a, p.K, p.Kp, p.status);
+    widen_rows<ACCESS>(p.B, p.ldb, p.B16, p.rows_b, p.K, p.Kp, p.status);
 }
 
 // ------------------------------------------------------------------ few tokens
@@ -1096,16 +1122,16 @@ float int8_mid_plan(int M, int N, int K, int sm_count, int *tile_tokens, int *sp
 }
 
 // The same for widening in a launch of its own and multiplying 128 x 128 tiles or
-// a CTA pair's 256 x 256: both launches, 5 bytes of traffic a widened element
-// (most of it in L2), and per wave a tile's stages of 128 columns and its stores.
+// a CTA pair's 256 x 256: both launches, the widened elements (mostly in L2), and
+// per wave a tile's stages of 128 columns and its stores.
 float int8_tiled_cost(int M, int N, int K, int sm_count, int pair)
 {
     const long long tile = pair ? 256 : 128, at_once = pair ? sm_count / 2 : sm_count;
     const long long tiles = (M + tile - 1) / tile * ((N + tile - 1) / tile);
     const float stages = static_cast<float>((K + 127) / 128);
-    return 5.f + (static_cast<float>(M) + static_cast<float>(N)) * static_cast<float>(K) * 5.f / 11e6f +
+    return 6.f + (static_cast<float>(M) + static_cast<float>(N)) * static_cast<float>(K) / 5.2e6f +
            static_cast<float>((tiles + at_once - 1) / at_once) *
-               (pair ? 3.f + 0.68f * stages : 0.4f + 0.52f * stages);
+               (pair ? 3.f + 0.64f * stages : 0.4f + 0.46f * stages);
 }
 
 cudaError_t launch_int8_mid(const Int8MidParams &p, int access, int splits, cudaStream_t stream)

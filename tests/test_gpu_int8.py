@@ -157,7 +157,7 @@ def quant_reference(X):
 
 
 @pytest.mark.parametrize("M,K", [(1, 1), (3, 7), (5, 64), (33, 512), (9, 513), (17, 1000), (65, 4096), (2, 16384),
-                                 (2, 16392), (3, 20001)])
+                                 (2, 16392), (3, 20001), (8000, 640), (1300, 4096), (1300, 4104), (700, 8192)])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 def test_quantiser(M, K, dtype):
     g = torch.Generator(device="cuda").manual_seed(M * K)
