@@ -12,6 +12,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -982,8 +983,20 @@ w8a8_status run_ragged(const void *A, const float *a_s, const void *B, const flo
     int bn = o ? o->block_n_tile : 0;
     if (bn == 192)
         return fail(W8A8_ERR_UNSUPPORTED, "the ragged layout takes block_n_tile 128 or 256");
-    if (!bn)
-        bn = tiles * cdiv(N, 256) >= 2 * info.sm_count ? 256 : 128;
+    if (!bn) {
+        // The estimated cycles of either width: waves of items, each its K groups
+        // and its stores (a group of 128 x 128 / 128 x 256 takes some 700 / 1130
+        // cycles, or what its weights take to arrive).  Measured, 128 / 256: 5 rows
+        // of 45 experts, 712 x 1264, 7.8 / 9.9 us; 792 rows of 28, 656 x 784, 10.6 / 9.1;
+        // 2876 rows of 10, 952 x 2368, 19.8 / 16.1; 16384 rows of 64, 4096 x 4096, 397 / 325.
+        const double spread = gr.experts * (1.0 - std::exp(-static_cast<double>(M) / gr.experts));
+        const int64_t likely = static_cast<int64_t>(spread) + M / 128 + 1;
+        const int64_t G = cdiv(K, 128);
+        auto cycles = [&](int64_t width, int64_t group, int64_t store) {
+            return cdiv(likely * cdiv(N, width), info.sm_count) * (G * group + store);
+        };
+        bn = cycles(128, 700, 1500) <= cycles(256, 1130, 2500) ? 128 : 256;
+    }
     const int64_t items = tiles * cdiv(N, bn);
     int64_t grid = std::min<int64_t>(items, info.sm_count);
     if (o && o->grid_limit)
