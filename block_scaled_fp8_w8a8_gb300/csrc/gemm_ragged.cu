@@ -18,6 +18,10 @@
 //    per 32 KB of weights the MMA takes about a fifth of the SM's share of the
 //    HBM time.  The ring runs across items, so the stream of weights does not
 //    pause between experts.
+// Where even that leaves most SMs without an item (a few rows of a few experts),
+// the CTAs of a cluster share one: each takes a range of its K groups, leaves its
+// fp32 partial rows in shared memory, and they are added in rank order through
+// distributed shared memory.
 //
 // Roles per CTA, promotion and scale ring are those of the tiled kernel (see
 // gemm_tiled.cu): warp 0 TMA producer, warps 1 and 3 MMA issuers, warp 2 scale
@@ -85,13 +89,29 @@ __device__ __forceinline__ int block_prefix(int v, int neutral, volatile int *wa
 
 // The items of one CTA: blockIdx.x, blockIdx.x + gridDim.x, ... over (row
 // tile, column tile), column tiles innermost, so that the CTAs running at one
-// time share row tiles of A and an expert's weights in L2.
-struct RaggedWalk {
+// time share row tiles of A and an expert's weights in L2.  SPLIT: the one item
+// of this CTA's cluster, of which it takes the K groups g0 .. g1-1.
+template <bool SPLIT> __device__ __forceinline__ int first_item(const RaggedParams &p)
+{
+    return static_cast<int>(SPLIT ? blockIdx.x / p.split : blockIdx.x);
+}
+template <bool SPLIT>
+__device__ __forceinline__ void group_range(const RaggedParams &p, int &g0, int &g1)
+{
+    g0 = 0;
+    g1 = p.G;
+    if (SPLIT) {
+        const int r = static_cast<int>(blockIdx.x % p.split);
+        g0 = p.G * r / p.split;
+        g1 = p.G * (r + 1) / p.split;
+    }
+}
+template <bool SPLIT> struct RaggedWalk {
     const int *row0, *tile0;      // [experts + 1] first row and first tile of each expert
     int item, items, num_n, experts;
     int e, m0, rows, nb;          // the current item: expert, first row, valid rows, column tile
     __device__ RaggedWalk(const RaggedParams &p, const int *r, const int *t)
-        : row0(r), tile0(t), item(static_cast<int>(blockIdx.x)), items(t[p.experts] * p.num_n_tiles),
+        : row0(r), tile0(t), item(first_item<SPLIT>(p)), items(t[p.experts] * p.num_n_tiles),
           num_n(p.num_n_tiles), experts(p.experts)
     {
     }
@@ -112,18 +132,24 @@ struct RaggedWalk {
         e = lo;
         m0 = row0[lo] + (mt - tile0[lo]) * 128;
         rows = min(128, row0[lo + 1] - m0);
-        item += static_cast<int>(gridDim.x);
+        item = SPLIT ? items : item + static_cast<int>(gridDim.x);
         return true;
     }
 };
 
-template <int BN, int STAGES, int CPW, int EB>
+// A partial tile in shared memory: rows of 128 floats, padded so that neighbouring
+// rows start in different banks.
+constexpr int kPartialPitch = 132;
+
+template <int BN, int STAGES, int CPW, int EB, bool SPLIT>
 __global__ void __launch_bounds__(RaggedLayout<BN, STAGES, CPW, EB>::kThreads, 1)
     k_ragged(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmTile,
              const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmC,
              const RaggedParams p)
 {
     using L = RaggedLayout<BN, STAGES, CPW, EB>;
+    static_assert(!SPLIT || (BN == 128 && 128 * kPartialPitch * 4 <= L::kStageBytes),
+                  "the partial tile takes the stages' place");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -229,6 +255,9 @@ __global__ void __launch_bounds__(RaggedLayout<BN, STAGES, CPW, EB>::kThreads, 1
         __syncthreads();
     }
 
+    int g0, g1;
+    group_range<SPLIT>(p, g0, g1);
+
     if (warp < 4) {
         regs_dealloc<L::kRegsLow>();
         if (warp == 0 && lane == 0) {
@@ -237,7 +266,7 @@ __global__ void __launch_bounds__(RaggedLayout<BN, STAGES, CPW, EB>::kThreads, 1
             uint32_t phase = 0;
             long long issued = 0;
             bool ok = true;
-            RaggedWalk w(p, row0, tile0);
+            RaggedWalk<SPLIT> w(p, row0, tile0);
             while (ok && w.next()) {
                 // All 128 rows at once, or the boxes of 32 that hold valid ones (an
                 // issue takes the producer some hundred cycles: with four boxes for
@@ -247,7 +276,7 @@ __global__ void __launch_bounds__(RaggedLayout<BN, STAGES, CPW, EB>::kThreads, 1
                 const CUtensorMap *const map_a = whole ? &tmTile : &tmA;
                 const int loads = whole ? 1 : (w.rows + kBoxRows - 1) / kBoxRows;
                 const uint32_t a_bytes = (whole ? 128 : loads * kBoxRows) * 128u;
-                for (int g = 0; g < p.G; ++g) {
+                for (int g = g0; g < g1; ++g) {
                     if (!wait_bounded(empty_bar(stage), phase ^ 1u, guard, SITE_TILED_PRODUCER)) {
                         ok = false;
                         break;
@@ -307,9 +336,9 @@ __global__ void __launch_bounds__(RaggedLayout<BN, STAGES, CPW, EB>::kThreads, 1
             uint32_t it = 0;
             bool ok = true;
             const int items = tile0[p.experts] * p.num_n_tiles;
-            for (int item = static_cast<int>(blockIdx.x); ok && item < items;
-                 item += static_cast<int>(gridDim.x)) {
-                for (int g = 0; g < p.G; ++g) {
+            for (int item = first_item<SPLIT>(p); ok && item < items;
+                 item = SPLIT ? items : item + static_cast<int>(gridDim.x)) {
+                for (int g = g0; g < g1; ++g) {
                     if (it % L::kIssuers == me) {
                         const uint32_t buf = it % L::kBufs;
                         const uint32_t bphase = (it / L::kBufs) & 1u;
@@ -347,10 +376,10 @@ __global__ void __launch_bounds__(RaggedLayout<BN, STAGES, CPW, EB>::kThreads, 1
             int slot = 0;
             uint32_t sphase = 0;
             bool ok = true;
-            RaggedWalk w(p, row0, tile0);
+            RaggedWalk<SPLIT> w(p, row0, tile0);
             while (ok && w.next()) {
                 const size_t b_row0 = static_cast<size_t>(w.e) * p.NB;
-                for (int g = 0; g < p.G; ++g) {
+                for (int g = g0; g < g1; ++g) {
                     ok = __all_sync(0xffffffffu, wait_bounded(sempty_bar(slot), sphase ^ 1u, guard,
                                                               SITE_TILED_SCALES));
                     if (!ok)
@@ -381,6 +410,10 @@ __global__ void __launch_bounds__(RaggedLayout<BN, STAGES, CPW, EB>::kThreads, 1
             asm volatile("cp.async.wait_all;" ::: "memory");
         }
         __syncwarp();
+        if (SPLIT) {
+            cluster_sync();       // the partial rows are in shared memory
+            cluster_sync();       // and have been read
+        }
     } else {
         // -------------------------------------------------------------- promotion + epilogue
         regs_alloc<L::kRegsHigh>();
@@ -392,7 +425,7 @@ __global__ void __launch_bounds__(RaggedLayout<BN, STAGES, CPW, EB>::kThreads, 1
         uint32_t it = 0;
         int slot = 0;
         uint32_t sphase = 0;
-        RaggedWalk w(p, row0, tile0);
+        RaggedWalk<SPLIT> w(p, row0, tile0);
         while (w.next()) {
             const int col0 = w.nb * BN + h * CPW;
             const int mine = min(32, w.rows - static_cast<int>(q * 32));   // rows of this warp
@@ -402,7 +435,7 @@ __global__ void __launch_bounds__(RaggedLayout<BN, STAGES, CPW, EB>::kThreads, 1
             for (int j = 0; j < L::kPairs; ++j)
                 acc[j] = 0ull;
             bool ok = true;
-            for (int g = 0; g < p.G; ++g) {
+            for (int g = g0; g < g1; ++g) {
                 const uint32_t buf = it % L::kBufs;
                 const uint32_t bphase = (it / L::kBufs) & 1u;
                 ok = __all_sync(0xffffffffu,
@@ -437,7 +470,19 @@ __global__ void __launch_bounds__(RaggedLayout<BN, STAGES, CPW, EB>::kThreads, 1
             if (!ok)
                 break;
             const int y = w.m0 + static_cast<int>(q * 32);
-            if (!idle && in_bounds(y >= 0 && y + mine <= p.M, p.status, SITE_BOUNDS_C)) {
+            if (SPLIT) {
+                // Every group's MMA has completed (its partial was read), so the
+                // stages are free.
+                float4 *part = reinterpret_cast<float4 *>(smem) + row * (kPartialPitch / 4) + h * (CPW / 4);
+#pragma unroll
+                for (int j = 0; j < CPW / 4; ++j) {
+                    float4 v;
+                    unpack2f(acc[2 * j], v.x, v.y);
+                    unpack2f(acc[2 * j + 1], v.z, v.w);
+                    if (!idle)
+                        part[j] = v;
+                }
+            } else if (!idle && in_bounds(y >= 0 && y + mine <= p.M, p.status, SITE_BOUNDS_C)) {
                 auto pack = [&](int k, int j) {
                     if (fp32) {
                         const uint64_t a = acc[8 * k + 2 * j], b = acc[8 * k + 2 * j + 1];
@@ -457,6 +502,44 @@ __global__ void __launch_bounds__(RaggedLayout<BN, STAGES, CPW, EB>::kThreads, 1
         }
         if (lane == 0)
             tma_store_wait_read();
+        if (SPLIT) {
+            cluster_sync();
+            // Each CTA finishes its share of the tile's rows: 32 threads to a row,
+            // four columns each.
+            RaggedWalk<SPLIT> last(p, row0, tile0);
+            const int S = p.split, rank = static_cast<int>(blockIdx.x % p.split);
+            if (last.next()) {
+                const int n = last.nb * BN + 4 * static_cast<int>(lane);
+                const uint32_t at = smem_addr(smem) + 16u * lane;
+                const int r1 = last.rows * (rank + 1) / S;
+                for (int r = last.rows * rank / S + static_cast<int>(warp) - 4; r < r1 && n < p.N; r += 8) {
+                    float4 v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)          // every load before the first addition
+                        if (i < S)
+                            v[i] = ld_cluster_f4(cluster_map(at + 4u * kPartialPitch * r,
+                                                             static_cast<uint32_t>(i)));
+#pragma unroll
+                    for (int i = 1; i < 8; ++i)
+                        if (i < S) {
+                            v[0].x += v[i].x;
+                            v[0].y += v[i].y;
+                            v[0].z += v[i].z;
+                            v[0].w += v[i].w;
+                        }
+                    const size_t to = static_cast<size_t>(last.m0 + r) * p.N + n;
+                    if (!in_bounds(last.m0 + r < p.M && n + 4 <= p.N, p.status, SITE_BOUNDS_C))
+                        continue;
+                    if (fp32)
+                        *reinterpret_cast<float4 *>(static_cast<float *>(p.C) + to) = v[0];
+                    else
+                        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.C) + to) =
+                            bf ? make_uint2(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[0].z, v[0].w))
+                               : make_uint2(pack_f16x2(v[0].x, v[0].y), pack_f16x2(v[0].z, v[0].w));
+                }
+            }
+            cluster_sync();
+        }
     }
 
     tc_fence_before_sync();
@@ -467,37 +550,65 @@ __global__ void __launch_bounds__(RaggedLayout<BN, STAGES, CPW, EB>::kThreads, 1
     }
 }
 
-template <int BN, int STAGES, int CPW, int EB>
+template <int BN, int STAGES, int CPW, int EB, bool SPLIT>
 cudaError_t launch_ragged_t(const CUtensorMap &tmA, const CUtensorMap &tmTile,
                             const CUtensorMap &tmB, const CUtensorMap &tmC, const RaggedParams &p,
-                            const LaunchCfg &cfg)
+                            const LaunchCfg &cfg, int *clusters = nullptr)
 {
     using L = RaggedLayout<BN, STAGES, CPW, EB>;
-    auto kernel = k_ragged<BN, STAGES, CPW, EB>;
+    auto kernel = k_ragged<BN, STAGES, CPW, EB, SPLIT>;
     static volatile int smem_set[kMaxDeviceFlags] = {};
     cudaError_t e = ensure_smem_limit(kernel, smem_set);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(cfg.grid, 1, 1);
+    lc.gridDim = dim3(clusters ? p.split : cfg.grid, 1, 1);
     lc.blockDim = dim3(L::kThreads, 1, 1);
     lc.dynamicSmemBytes = L::kSmem;
     lc.stream = cfg.stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
+    // the kernel waits for the work before it ahead of its first access
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[0].val.programmaticStreamSerializationAllowed = clusters ? 0 : 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(SPLIT ? p.split : 1);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     lc.attrs = attr;
-    lc.numAttrs = 1;      // the kernel waits for the work before it ahead of its first access
+    lc.numAttrs = SPLIT ? 2 : 1;
+    if (clusters)
+        return cudaOccupancyMaxActiveClusters(clusters, kernel, &lc);
     return cudaLaunchKernelEx(&lc, kernel, tmA, tmTile, tmB, tmC, p);
 }
 
 }  // namespace
 
+int ragged_clusters(int split)
+{
+    static volatile int cached[kMaxDeviceFlags][9] = {};
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDeviceFlags)
+        return 0;
+    if (cached[dev][split])
+        return cached[dev][split];
+    const CUtensorMap none = {};
+    RaggedParams p = {};
+    p.split = split;
+    if (launch_ragged_t<128, 6, 64, 1, true>(none, none, none, none, p, LaunchCfg{}, &n) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    cached[dev][split] = n;
+    return n;
+}
+
 cudaError_t launch_ragged(const CUtensorMap &tmA, const CUtensorMap &tmTile, const CUtensorMap &tmB,
                           const CUtensorMap &tmC, const RaggedParams &p, int bn, const LaunchCfg &cfg)
 {
-    return bn == 256 ? launch_ragged_t<256, 4, 128, 1>(tmA, tmTile, tmB, tmC, p, cfg)
-                     : launch_ragged_t<128, 6, 64, 1>(tmA, tmTile, tmB, tmC, p, cfg);
+    if (p.split > 1)
+        return launch_ragged_t<128, 6, 64, 1, true>(tmA, tmTile, tmB, tmC, p, cfg);
+    return bn == 256 ? launch_ragged_t<256, 4, 128, 1, false>(tmA, tmTile, tmB, tmC, p, cfg)
+                     : launch_ragged_t<128, 6, 64, 1, false>(tmA, tmTile, tmB, tmC, p, cfg);
 }
 
 }  // namespace w8a8

@@ -198,11 +198,15 @@ struct RaggedParams {
     int M, N, K, G, NB;
     int experts;
     int num_n_tiles;       // column tiles of BN
+    int split;             // CTAs of a cluster that share an item's K groups (1: none), at
+                           // most G; then bn is 128 and the grid holds split CTAs for
+                           // every item there can be
     int out_kind;
     int debug_skip_tma;    // test hook: >= 0 makes the producer skip that many-th load
     unsigned *status;
     unsigned long long wait_limit;
 };
+int ragged_clusters(int split);        // clusters of `split` CTAs that run at once
 // tmA, tmTile: A in boxes of 32 and of 128 rows; tmB: 3-D [experts, N, K], boxes of
 // bn rows; tmC as for launch_tiled.  bn: 128 or 256.
 cudaError_t launch_ragged(const CUtensorMap &tmA, const CUtensorMap &tmTile, const CUtensorMap &tmB,

@@ -444,8 +444,10 @@ w8a8_status w8a8_block_fp8_grouped_matmul_contiguous(const void *A_dev, const fl
  * One kernel for every routing, from one row to full prefill; no workspace.  Its
  * launch may overlap the end of the work before it on the stream, which it waits
  * for on the device, whatever opts->pdl says.
- * opts: variant AUTO or TILED; block_n_tile 128 or 256, grid_limit,
- * wait_limit_cycles and the test hooks apply.
+ * opts: variant AUTO or TILED; block_n_tile 128 or 256, grid_limit, split_k (0 =
+ * choose; 1 = none; 2, 4 or 8 CTAs of a cluster share an item's K groups, where every
+ * item finds a cluster, else W8A8_ERR_UNSUPPORTED; the partial sums are added in a
+ * fixed order), wait_limit_cycles and the test hooks apply.
  */
 #define W8A8_RAGGED_MAX_EXPERTS 1024
 w8a8_status w8a8_block_fp8_grouped_matmul_ragged(const void *A_dev, const float *a_s_dev,

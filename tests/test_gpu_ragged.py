@@ -69,6 +69,11 @@ CASES = [
     ([1000, 0, 1, 2000], 1536, 640, dict(block_n_tile=256)),
     ([64, 65], 1024, 4096, dict(grid_limit=3)),
     ([5] * 1024, 128, 128, {}),
+    ([5, 0, 3], 256, 1024, dict(split_k=8)),
+    ([130, 2], 128, 640, dict(split_k=4)),
+    ([33] * 3, 264, 4096, dict(split_k=2)),
+    ([1, 0, 0, 0, 1], 360, 3552, {}),
+    ([7], 1000, 272, {}),
 ]
 
 
@@ -86,7 +91,7 @@ def test_equals_the_plain_matmul_per_expert():
     """Every expert's rows carry the bits of a plain call on them alone."""
     counts = [70, 0, 129, 3]
     x = make(counts, 256, 512, seed=2)
-    C = w8.grouped_matmul_ragged(*x, "fp32")
+    C = w8.grouped_matmul_ragged(*x, "fp32", split_k=1)
     lo = 0
     for e, n in enumerate(counts):
         if n:
@@ -168,7 +173,9 @@ def test_pdl_behind_the_quantiser_and_the_same_bits_every_time():
 
 def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right():
     x = make([50, 60], 256, 1024, seed=10)
-    w8.grouped_matmul_ragged(*x, debug_skip_load=3, wait_limit_cycles=2_000_000)
+    w8.grouped_matmul_ragged(*x, debug_skip_load=3, split_k=1, wait_limit_cycles=2_000_000)
+    assert w8.w8a8_get_device_status()[0] == w8.W8A8_ERR_DEVICE_TIMEOUT
+    w8.grouped_matmul_ragged(*x, debug_skip_load=1, wait_limit_cycles=2_000_000)
     assert w8.w8a8_get_device_status()[0] == w8.W8A8_ERR_DEVICE_TIMEOUT
     C = w8.grouped_matmul_ragged(*x)
     torch.cuda.synchronize()
