@@ -76,7 +76,7 @@ def run_all(seed=1):
     rn = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
     i8 = lambda *s: torch.randint(-128, 128, s, generator=g, device="cuda", dtype=torch.int8)  # noqa: E731
     out = {}
-    A, B = (rn(230, 400) * 90).to(torch.float8_e4m3fn), (rn(5, 264, 400) * 90).to(torch.float8_e4m3fn)
+    A, B = ((rn(*s) * 90).clamp_(-448, 448).to(torch.float8_e4m3fn) for s in ((230, 400), (5, 264, 400)))
     off = torch.tensor([3, 40, 40, 173, 200, 229], dtype=torch.int32, device="cuda")
     for bn in (128, 256):
         C = torch.zeros(230, 264, device="cuda")
@@ -136,8 +136,7 @@ def test_debug_bounds_build(tmp_path):
     assert res["status"][0] == w8.W8A8_OK, hex(res["status"][1])
     want = run_all()
     for k, v in want.items():
-        assert torch.equal(res["out"][k].nan_to_num() if v.is_floating_point() else res["out"][k],
-                           v.nan_to_num() if v.is_floating_point() else v), k
+        assert torch.equal(res["out"][k], v), k
     for bad, after in res["bad"]:
         assert bad[0] == w8.W8A8_ERR_DEVICE_BOUNDS and (bad[1] >> 8) & 0xFF == 20, hex(bad[1])
         assert after[0] == w8.W8A8_OK
