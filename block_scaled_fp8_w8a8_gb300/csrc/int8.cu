@@ -145,7 +145,11 @@ __global__ void __launch_bounds__(kWidenThreads) k_int8_widen(const Int8WidenPar
 // through it takes more than its bandwidth.)
 // The warps of a CTA, and the CTAs of a cluster, split K; whole sums meet in
 // shared memory, where the order of integer additions does not matter.
-constexpr int kSmallWarps = 8;
+// Bound by the latency of a launch and of the loads: two batches of loads a
+// thread, 32 KB a CTA, stay in flight.  One token by 4096 x 4096: 4.2 us (4.0
+// TB/s; with a single batch 5.4), by 8192 x 16384: 28.7 us (4.7 TB/s).
+// Batches of 4 steps give 4.6 and 26.4 us.
+constexpr int kSmallWarps = 8, kSmallCtas = 2;       // CTAs per SM
 
 __device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                             uint32_t b1)
@@ -161,21 +165,24 @@ __device__ __forceinline__ uint32_t word_of(const uint4 &v, int j)
     return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
 }
 
-// UN: 64-column steps whose loads are issued together.
+// UN: 64-column steps whose loads are issued together; two such batches are held.
 template <int NT, int MT, int UN, int ACCESS>
-__global__ void __launch_bounds__(32 * kSmallWarps, 2) k_int8_small(const Int8SmallParams p)
+__global__ void __launch_bounds__(32 * kSmallWarps, kSmallCtas) k_int8_small(const Int8SmallParams p)
 {
     constexpr int kRows = 16 * MT, kTokens = 8 * NT;
-    __shared__ int sums[kRows * kTokens];            // [token][row]
+    // [token][row], of two tiles in turn; with 4 words of padding a warp's
+    // additions fall into different banks
+    constexpr int kPitch = kRows + 4, kSums = kPitch * kTokens;
+    __shared__ int sums2[2][kSums];
     const int lane = static_cast<int>(lane_index()), warp = static_cast<int>(warp_index());
     const int g = lane >> 2, t = lane & 3;
-    for (int i = static_cast<int>(threadIdx.x); i < kRows * kTokens; i += 32 * kSmallWarps)
-        sums[i] = 0;
+    for (int i = static_cast<int>(threadIdx.x); i < 2 * kSums; i += 32 * kSmallWarps)
+        sums2[0][i] = 0;
     __syncthreads();
     grid_launch_dependents();
     grid_dependency_wait();
 
-    const int n0 = static_cast<int>(blockIdx.x) * kRows, m0 = static_cast<int>(blockIdx.z) * kTokens;
+    const int m0 = static_cast<int>(blockIdx.z) * kTokens;
     // This warp's steps: the cluster's CTAs and their warps take equal shares.
     const int steps = (p.K + 63) / 64, shares = static_cast<int>(gridDim.y) * kSmallWarps;
     const int share = static_cast<int>(blockIdx.y) * kSmallWarps + warp;
@@ -183,9 +190,11 @@ __global__ void __launch_bounds__(32 * kSmallWarps, 2) k_int8_small(const Int8Sm
     const int last = static_cast<int>(static_cast<long long>(steps) * (share + 1) / shares);
     // Rows past the ends repeat the last one; their sums are not stored.
     const uint8_t *wrow[2 * MT], *xrow[NT];
+    auto rows_from = [&](int n0) {
 #pragma unroll
-    for (int i = 0; i < 2 * MT; ++i)
-        wrow[i] = p.B + static_cast<long long>(min(n0 + 8 * i + g, p.N - 1)) * p.ldb;
+        for (int i = 0; i < 2 * MT; ++i)
+            wrow[i] = p.B + static_cast<long long>(min(n0 + 8 * i + g, p.N - 1)) * p.ldb;
+    };
 #pragma unroll
     for (int i = 0; i < NT; ++i)
         xrow[i] = p.A + static_cast<long long>(min(m0 + 8 * i + g, p.M - 1)) * p.lda;
@@ -201,33 +210,36 @@ __global__ void __launch_bounds__(32 * kSmallWarps, 2) k_int8_small(const Int8Sm
                     acc[i][j][k] = 0.f;
     };
     // An accumulator's element: weight row g (+ 8), tokens 2 t and 2 t + 1.
-    auto flush = [&]() {
+    auto flush = [&](int *sums) {
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    atomicAdd(sums + (8 * j + 2 * t + (k & 1)) * kRows + 16 * i + g + 8 * (k >> 1),
+                    atomicAdd(sums + (8 * j + 2 * t + (k & 1)) * kPitch + 16 * i + g + 8 * (k >> 1),
                               __float2int_rn(acc[i][j][k]));
     };
-    clear();
-    int since = 0;                                   // steps in the accumulators: at most 8
-    for (int s = first; s < last; s += UN) {
+    struct Batch {
         uint4 w[UN][2 * MT], x[UN][NT];
+    };
+    auto load = [&](Batch &q, int s) {
 #pragma unroll
         for (int u = 0; u < UN; ++u) {
             const int c = (s + u) * 64 + 16 * t;
             const int end = s + u < last ? p.K : 0;          // nothing past this warp's steps
 #pragma unroll
             for (int i = 0; i < 2 * MT; ++i)
-                w[u][i] = load16<ACCESS>(wrow[i], c, end);
+                q.w[u][i] = load16<ACCESS>(wrow[i], c, end);
 #pragma unroll
             for (int i = 0; i < NT; ++i)
-                x[u][i] = load16<ACCESS>(xrow[i], c, end);
+                q.x[u][i] = load16<ACCESS>(xrow[i], c, end);
         }
+    };
+    int since = 0;                                   // steps in the accumulators: at most 8
+    auto multiply = [&](const Batch &q, int *sums) {
         if (since + UN > kChunkSteps) {
-            flush();
+            flush(sums);
             clear();
             since = 0;
         }
@@ -239,8 +251,8 @@ __global__ void __launch_bounds__(32 * kSmallWarps, 2) k_int8_small(const Int8Sm
                 uint32_t a[MT][4];
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
-                    const uint2 lo = widen4(word_of(w[u][2 * i], j));
-                    const uint2 hi = widen4(word_of(w[u][2 * i + 1], j));
+                    const uint2 lo = widen4(word_of(q.w[u][2 * i], j));
+                    const uint2 hi = widen4(word_of(q.w[u][2 * i + 1], j));
                     a[i][0] = lo.x;
                     a[i][1] = hi.x;
                     a[i][2] = lo.y;
@@ -248,55 +260,83 @@ __global__ void __launch_bounds__(32 * kSmallWarps, 2) k_int8_small(const Int8Sm
                 }
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
-                    const uint2 b = widen4(word_of(x[u][i], j));
+                    const uint2 b = widen4(word_of(q.x[u][i], j));
 #pragma unroll
                     for (int k = 0; k < MT; ++k)
                         mma_16x8x16(acc[k][i], a[k], b.x, b.y);
                 }
             }
-    }
-    flush();
-
-    // The CTAs of a cluster hold partial sums of the same tile: each finishes
-    // its share of it, reading the others' through distributed shared memory.
+    };
+    // The CTA's tiles.  Two batches in turn: one's loads are in flight while the
+    // other is multiplied, and the next tile's first while a tile is finished.
     const int S = static_cast<int>(gridDim.y);
-    uint32_t rank = 0;
-    if (S > 1) {
-        rank = cluster_ctarank();
-        cluster_sync();
-    } else {
-        __syncthreads();
-    }
-    constexpr int kAll = kRows * kTokens;
-    const int hi = kAll * (static_cast<int>(rank) + 1) / S;
-    for (int i = kAll * static_cast<int>(rank) / S + static_cast<int>(threadIdx.x); i < hi;
-         i += 32 * kSmallWarps) {
-        const int m = m0 + i / kRows, n = n0 + i % kRows;
-        if (m >= p.M || n >= p.N)
-            continue;
-        int sum = 0;
-        if (S == 1) {
-            sum = sums[i];
-        } else {
-            for (int r = 0; r < S; ++r) {
-                int v;
-                asm volatile("ld.shared::cluster.s32 %0, [%1];"
-                             : "=r"(v)
-                             : "r"(cluster_map(smem_addr(sums + i), static_cast<uint32_t>(r)))
-                             : "memory");
-                sum += v;
-            }
+    const uint32_t rank = S > 1 ? cluster_ctarank() : 0;
+    const int step_n = static_cast<int>(gridDim.x) * kRows;
+    Batch q0, q1;
+    int n0 = static_cast<int>(blockIdx.x) * kRows, turn = 0;
+    rows_from(n0);
+    load(q0, first);
+    for (;; turn ^= 1) {
+        int *sums = sums2[turn];
+        const bool next = step_n < p.N - n0;         // this CTA has another tile
+        clear();
+        since = 0;
+        for (int s = first;; s += 2 * UN) {
+            load(q1, s + UN);
+            multiply(q0, sums);
+            const bool half = s + UN < last, more = s + 2 * UN < last;
+            if (!more && next)
+                rows_from(n0 + step_n);
+            if (more || next)
+                load(q0, more ? s + 2 * UN : first);
+            if (half)
+                multiply(q1, sums);
+            if (!more)
+                break;
         }
-        const float v = __int2float_rn(sum) * __ldg(p.a_s + m) * __ldg(p.b_s + n);
-        if (!in_bounds(m >= 0 && n >= 0, p.status, SITE_BOUNDS_C))
-            continue;
-        const long long at = m * p.ldc + n;
-        if (p.out_kind == OUT_FP32)
-            static_cast<float *>(p.C)[at] = v;
-        else if (p.out_kind == OUT_BF16)
-            static_cast<__nv_bfloat16 *>(p.C)[at] = __float2bfloat16_rn(v);
+        flush(sums);
+        // The CTAs of a cluster hold partial sums of the same tile: each finishes
+        // its share of it, reading the others' through distributed shared memory.
+        if (S > 1)
+            cluster_sync();
         else
-            static_cast<__half *>(p.C)[at] = __float2half_rn(v);
+            __syncthreads();
+        constexpr int kAll = kRows * kTokens;
+        const int hi = kAll * (static_cast<int>(rank) + 1) / S;
+        for (int i = kAll * static_cast<int>(rank) / S + static_cast<int>(threadIdx.x); i < hi;
+             i += 32 * kSmallWarps) {
+            const int m = m0 + i / kRows, n = n0 + i % kRows;
+            int *const at_sum = sums + i / kRows * kPitch + i % kRows;
+            int sum = 0;
+            if (S == 1) {
+                sum = *at_sum;
+                *at_sum = 0;         // for the tile after the next, a barrier away
+            } else {
+                for (int r = 0; r < S; ++r) {
+                    int v;
+                    asm volatile("ld.shared::cluster.s32 %0, [%1];"
+                                 : "=r"(v)
+                                 : "r"(cluster_map(smem_addr(at_sum), static_cast<uint32_t>(r)))
+                                 : "memory");
+                    sum += v;
+                }
+            }
+            if (m >= p.M || n >= p.N)
+                continue;
+            const float v = __int2float_rn(sum) * __ldg(p.a_s + m) * __ldg(p.b_s + n);
+            if (!in_bounds(m >= 0 && n >= 0, p.status, SITE_BOUNDS_C))
+                continue;
+            const long long at = m * p.ldc + n;
+            if (p.out_kind == OUT_FP32)
+                static_cast<float *>(p.C)[at] = v;
+            else if (p.out_kind == OUT_BF16)
+                static_cast<__nv_bfloat16 *>(p.C)[at] = __float2bfloat16_rn(v);
+            else
+                static_cast<__half *>(p.C)[at] = __float2half_rn(v);
+        }
+        if (!next)
+            break;
+        n0 += step_n;
     }
     if (S > 1)
         cluster_sync();              // no CTA leaves while another reads its sums
@@ -315,10 +355,15 @@ cudaError_t launch_small_t(const Int8SmallParams &p, int access, int sm_count, c
     const long long tiles = static_cast<long long>(tiles_n) * tiles_m;
     const int steps = (p.K + 63) / 64;
     int splits = 1;
-    while (splits < 8 && tiles * splits * 2 <= 2ll * sm_count && steps >= 2 * splits * kSmallWarps)
+    while (splits < 8 && tiles * splits * 2 <= static_cast<long long>(kSmallCtas) * sm_count &&
+           steps >= 2 * splits * kSmallWarps)
         splits *= 2;
+    // Without a split a CTA takes several tiles where there are more than stay
+    // resident; a split has one tile a cluster.
+    const int resident = (kSmallCtas * sm_count + tiles_m - 1) / tiles_m;
+    const int each = (tiles_n + resident - 1) / resident;
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(tiles_n, splits, tiles_m);
+    lc.gridDim = dim3(splits > 1 ? tiles_n : (tiles_n + each - 1) / each, splits, tiles_m);
     lc.blockDim = dim3(32 * kSmallWarps, 1, 1);
     lc.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -1039,10 +1084,10 @@ cudaError_t launch_mma(const CUtensorMap &tmA, const CUtensorMap &tmB, const CUt
 cudaError_t launch_int8_small(const Int8SmallParams &p, int access, int sm_count, cudaStream_t stream)
 {
     if (p.M <= 8)
-        return launch_small_t<1, 1, 4>(p, access, sm_count, stream);
+        return launch_small_t<1, 1, 2>(p, access, sm_count, stream);
     if (p.M <= 16)
-        return launch_small_t<2, 1, 4>(p, access, sm_count, stream);
-    return launch_small_t<4, 2, 2>(p, access, sm_count, stream);
+        return launch_small_t<2, 1, 2>(p, access, sm_count, stream);
+    return launch_small_t<4, 2, 1>(p, access, sm_count, stream);
 }
 
 namespace {

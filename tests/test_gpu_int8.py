@@ -60,6 +60,15 @@ def test_forced_kernels(M, N, K, variant):
         assert_same(C, reference(*x, "fp32"), f"{variant} {grid}")
 
 
+@pytest.mark.parametrize("M", [1, 11, 30])
+@pytest.mark.parametrize("N,K", [(4865, 64), (15001, 700), (33000, 1100), (10000, 4096)])
+def test_more_weight_rows_than_ctas(M, N, K):
+    """A CTA of the small-M kernel walks several tiles and starts the next
+    one's loads while it finishes one."""
+    x = make(M, N, K, seed=N + M)
+    assert_same(w8.int8_matmul(*x, "fp32", variant=w8.W8A8_VARIANT_SMALLM), reference(*x, "fp32"))
+
+
 @pytest.mark.parametrize("K", [512, 513, 4096, 20000, w8.W8A8_INT8_MAX_K])
 @pytest.mark.parametrize("M", [2, 40, 130])
 def test_largest_sums_are_exact(M, K):
