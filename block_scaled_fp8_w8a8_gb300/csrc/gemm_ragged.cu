@@ -260,8 +260,9 @@ __global__ void __launch_bounds__(RaggedLayout<BN, STAGES, CPW, EB>::kThreads, 1
 
     if (warp < 4) {
         regs_dealloc<L::kRegsLow>();
-        if (warp == 0 && lane == 0) {
+        if (warp == 0) {
             // ---------------------------------------------------------- TMA producer
+            // The whole warp walks the stages and an elected lane issues.
             int stage = 0;
             uint32_t phase = 0;
             long long issued = 0;
@@ -277,10 +278,10 @@ __global__ void __launch_bounds__(RaggedLayout<BN, STAGES, CPW, EB>::kThreads, 1
                 const int loads = whole ? 1 : (w.rows + kBoxRows - 1) / kBoxRows;
                 const uint32_t a_bytes = (whole ? 128 : loads * kBoxRows) * 128u;
                 for (int g = g0; g < g1; ++g) {
-                    if (!wait_bounded(empty_bar(stage), phase ^ 1u, guard, SITE_TILED_PRODUCER)) {
-                        ok = false;
+                    ok = __all_sync(0xffffffffu, wait_bounded(empty_bar(stage), phase ^ 1u, guard,
+                                                              SITE_TILED_PRODUCER));
+                    if (!ok)
                         break;
-                    }
                     const int arow = w.m0 + ((W8A8_DEBUG_BOUNDS && issued == 0 &&
                                               p.debug_skip_tma == kDebugBadFirstLoad)
                                                  ? (1 << 28)
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(RaggedLayout<BN, STAGES, CPW, EB>::kThreads, 1
                                               SITE_BOUNDS_A) &&
                                     in_bounds(w.nb * BN < p.N && w.e < p.experts, p.status,
                                               SITE_BOUNDS_B);
-                    if (issued != p.debug_skip_tma && in) {
+                    if (issued != p.debug_skip_tma && in && elect_one()) {
                         mbar_arrive_expect_tx(full_bar(stage), a_bytes + L::kBBytes);
                         tma_load_3d(sB + stage * L::kBBytes, &tmB, full_bar(stage), g * 128,
                                     w.nb * BN, w.e);

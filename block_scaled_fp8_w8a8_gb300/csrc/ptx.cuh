@@ -23,6 +23,19 @@ __device__ __forceinline__ uint32_t lane_index() { return threadIdx.x & 31u; }
 // (see mma_f16_elect).
 __device__ __forceinline__ uint32_t warp_uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
+// Whether this is the one lane that a converged warp elects.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "elect.sync _|p, 0xffffffff;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(yes)
+                 :
+                 : "memory");
+    return yes != 0;
+}
+
 // Programmatic dependent launch: wait for the previous grid's memory, and let
 // the next grid start its prologue.  Both are no-ops without the launch attribute.
 __device__ __forceinline__ void grid_dependency_wait()
@@ -526,18 +539,6 @@ __device__ __forceinline__ void mma_f16_elect(uint32_t d_tmem, uint64_t a_desc, 
                      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
                      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
                      : "memory");
-}
-
-// As mma_e4m3, by an elected lane.
-__device__ __forceinline__ void mma_e4m3_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                               uint32_t idesc, uint32_t accumulate)
-{
-    asm volatile("{\n\t.reg .pred p, q;\n\t"
-                 "elect.sync _|q, 0xffffffff;\n\t"
-                 "setp.ne.b32 p, %4, 0;\n\t"
-                 "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-                 : "memory");
 }
 
 // As mma_commit (mma_commit_pair_mc to the CTAs of cta_mask with PAIR), by the
