@@ -21,7 +21,7 @@ LIB_NAME = "libw8a8_gb300.so"
 OUT_DEBUG = os.path.join(HERE, "_build_debug")
 LIB_NAME_DEBUG = "libw8a8_gb300_debug.so"
 UNITS = ["api.cu", "status.cu", "gemm_tiled.cu", "gemm_swapab.cu", "noalloc.cu", "quant.cu", "hostio.cu",
-         "gemm_smallm.cu", "gemm_pair.cu", "gemm_generic.cu", "gemm_ragged.cu", "int8.cu", "norm.cu"]
+         "gemm_smallm.cu", "gemm_pair.cu", "gemm_generic.cu", "gemm_ragged.cu", "gemm_ragged_few.cu", "int8.cu", "norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 HEADERS = ["ptx.cuh", "kernels.cuh", "epilogue.cuh", "promote.cuh", "quant_math.cuh", "dispatch_table.h", "tuning_table.inc"]
 

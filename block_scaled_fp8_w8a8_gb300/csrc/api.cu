@@ -978,11 +978,27 @@ w8a8_status run_ragged(const void *A, const float *a_s, const void *B, const flo
                        int64_t M, int64_t N, int64_t K, int out, cudaStream_t stream,
                        const w8a8_options *o, const Grouping &gr, const DeviceInfo &info)
 {
-    // Row tiles that the routing can make at most; the host does not know it.
-    const int64_t tiles = std::min<int64_t>(gr.experts, M) + M / 128;
+    const int asked = o ? o->split_k : 0, m_tile = o ? o->m_tile : 0;
     int bn = o ? o->block_n_tile : 0;
-    if (bn == 192)
-        return fail(W8A8_ERR_UNSUPPORTED, "the ragged layout takes block_n_tile 128 or 256");
+    if (bn == 192 || (m_tile && m_tile != 32 && m_tile != 128) || (m_tile == 32 && bn == 256))
+        return fail(W8A8_ERR_UNSUPPORTED,
+                    "the ragged layout takes block_n_tile 128 or 256 and m_tile 128, or 128 and 32");
+    const int64_t G = cdiv(K, 128);
+    // Tiles of 32 rows where experts have few rows on average and either K is long
+    // enough for its groups to outweigh the launch, or the items fill the GPU several
+    // times over.  Measured, 32-row / 128-row tiles: 8 rows of 256 experts, 1536 x
+    // 4096, 14.9 / 15.7 us; 512 rows of 256, 186 / 190; 7 rows of 11, 160 x 3376, 6.9 /
+    // 12.4; 128 rows of 8, 1536 x 4096, 14.6 / 15.7; 59 rows of 104, 2320 x 576, 17.5 / 21.3;
+    // but 256 rows of 8, 1536 x 4096, 20.5 / 16.0; 102 rows of 7, 1104 x 880, 7.6 / 6.8.
+    const int64_t most = std::min<int64_t>(gr.experts, M);
+    const bool thin = (G >= 9 && M <= 24 * most) ||
+                      (G >= 5 && M <= 16 * most && (most + M / 32) * cdiv(N, 128) >= 4 * info.sm_count);
+    const bool few = m_tile ? m_tile == 32 : asked > 1 || (!bn && thin);
+    const int rows = few ? 32 : 128;
+    // Row tiles that the routing can make at most; the host does not know it.
+    const int64_t tiles = std::min<int64_t>(gr.experts, M) + M / rows;
+    if (few)
+        bn = 128;
     if (!bn) {
         // The estimated cycles of either width: waves of items, each its K groups
         // and its stores (a group of 128 x 128 / 128 x 256 takes some 700 / 1130
@@ -991,41 +1007,38 @@ w8a8_status run_ragged(const void *A, const float *a_s, const void *B, const flo
         // 2876 rows of 10, 952 x 2368, 19.8 / 16.1; 16384 rows of 64, 4096 x 4096, 397 / 325.
         const double spread = gr.experts * (1.0 - std::exp(-static_cast<double>(M) / gr.experts));
         const int64_t likely = static_cast<int64_t>(spread) + M / 128 + 1;
-        const int64_t G = cdiv(K, 128);
         auto cycles = [&](int64_t width, int64_t group, int64_t store) {
             return cdiv(likely * cdiv(N, width), info.sm_count) * (G * group + store);
         };
         bn = cycles(128, 700, 1500) <= cycles(256, 1130, 2500) ? 128 : 256;
     }
     const int64_t items = tiles * cdiv(N, bn);
-    int64_t grid = std::min<int64_t>(items, info.sm_count);
-    if (o && o->grid_limit)
-        grid = std::min<int64_t>(grid, o->grid_limit);
-    // Clusters that split K, where every item there can be still gets one of its
-    // own, each CTA at least two groups, and the rows are few enough for their
-    // partial sums to cost less than the groups (whole / split: 4 rows of 11
-    // experts, 360 x 3552, 12.8 / 6.6 us; 5 rows of 45, 712 x 1264, 7.7 / 6.6; 8 rows of
-    // 8, 1064 x 528, 6.1 / 6.3; 987 rows of 4, 376 x 1152, 7.6 / 7.9).
-    const int asked = o ? o->split_k : 0, G_all = static_cast<int>(cdiv(K, 128));
-    if (asked > 1 && (asked > 8 || (asked & (asked - 1)) || asked > G_all ||
-                      items > ragged_clusters(asked) || bn != 128))
+    // Clusters split K where every item there can be still gets one of its own and
+    // each CTA at least two groups.
+    int split = asked > 1 ? asked : 1;
+    if (asked > 1 && (!few || asked > 8 || (asked & (asked - 1)) || asked > G ||
+                      items > ragged_few_clusters(asked)))
         return fail(W8A8_ERR_UNSUPPORTED,
-                    "the ragged layout splits K over 2, 4 or 8 CTAs (at most the K groups), on 128-column "
+                    "the ragged layout splits K over 2, 4 or 8 CTAs (at most the K groups), on 32-row "
                     "tiles, where all %lld items find a cluster",
                     static_cast<long long>(items));
-    int split = asked > 1 ? asked : 1;
-    if (!asked && bn == 128 && G_all >= 9 && M <= 32 * tiles && !(o && o->grid_limit))
-        for (int s = 2; s <= 8 && 2 * s <= G_all && items <= ragged_clusters(s); s *= 2)
+    if (few && !asked && !(o && o->grid_limit))
+        for (int s = 2; s <= 8 && 2 * s <= G && items <= ragged_few_clusters(s); s *= 2)
             split = s;
+    int64_t grid = std::min<int64_t>(items, few ? ragged_few_clusters(1) : info.sm_count);
+    if (grid <= 0)
+        return fail(W8A8_ERR_CUDA, "no CTA of the ragged kernel fits on this device");
+    if (o && o->grid_limit)
+        grid = std::min<int64_t>(grid, o->grid_limit);
     if (split > 1)
         grid = items * split;
     w8a8_status st;
-    CUtensorMap mA, mTile, mB, mC;
+    CUtensorMap mA, mTile = {}, mB, mC = {};
     if ((st = encode_u8_map(&mA, A, M, K, 32)) != W8A8_OK ||
-        (st = encode_u8_map(&mTile, A, M, K, 128)) != W8A8_OK ||
         (st = encode_u8_map(&mB, B, N, K, bn, gr.experts)) != W8A8_OK ||
-        (st = encode_out_map(&mC, C, M, N, out, out == W8A8_OUT_FP32 ? 16 : 32, 32,
-                             CU_TENSOR_MAP_SWIZZLE_64B)) != W8A8_OK)
+        (!few && ((st = encode_u8_map(&mTile, A, M, K, 128)) != W8A8_OK ||
+                  (st = encode_out_map(&mC, C, M, N, out, out == W8A8_OUT_FP32 ? 16 : 32, 32,
+                                       CU_TENSOR_MAP_SWIZZLE_64B)) != W8A8_OK)))
         return st;
     RaggedParams p = {};
     p.a_s = a_s;
@@ -1049,7 +1062,8 @@ w8a8_status run_ragged(const void *A, const float *a_s, const void *B, const flo
     LaunchCfg cfg = {};
     cfg.grid = static_cast<int>(grid);
     cfg.stream = stream;
-    const cudaError_t e = launch_ragged(mA, mTile, mB, mC, p, bn, cfg);
+    const cudaError_t e =
+        few ? launch_ragged_few(mA, mB, p, cfg) : launch_ragged(mA, mTile, mB, mC, p, bn, cfg);
     return e == cudaSuccess ? W8A8_OK : cuda_fail(e, "kernel launch");
 }
 

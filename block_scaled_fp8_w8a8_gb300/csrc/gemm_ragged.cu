@@ -8,20 +8,18 @@
 // code waits for a routing.  One persistent CTA per SM turns them into a list
 // of 128-row tiles in shared memory (a prefix sum of the experts' tile counts)
 // and walks the (row tile, BN weight rows) items of it; an item finds its
-// expert by binary search.  Tokens sit on the MMA's M side at every size:
-//  - where experts have many rows this is the tiled kernel's work;
-//  - where they have a few (decode), the weights bound the time: an expert's
-//    block is read once, and only the 32-row boxes of A that hold valid rows
-//    are loaded.  The MMA still runs 128 rows (the others hold whatever the
-//    stage last held: a row of the product depends on its own row of A alone,
-//    and those rows are neither promoted nor stored), which costs nothing:
-//    per 32 KB of weights the MMA takes about a fifth of the SM's share of the
-//    HBM time.  The ring runs across items, so the stream of weights does not
-//    pause between experts.
-// Where even that leaves most SMs without an item (a few rows of a few experts),
-// the CTAs of a cluster share one: each takes a range of its K groups, leaves its
-// fp32 partial rows in shared memory, and they are added in rank order through
-// distributed shared memory.
+// expert by binary search.  Tokens sit on the MMA's M side: where experts have
+// many rows this is the tiled kernel's work.  Of a tile with fewer rows only the
+// 32-row boxes of A that hold valid ones are loaded; the MMA still runs 128 rows
+// (the others hold whatever the stage last held: a row of the product depends on
+// its own row of A alone, and those rows are neither promoted nor stored).  The
+// ring runs across items.  Where experts have a few rows only, k_ragged_few
+// (gemm_ragged_few.cu) takes over.
+// Bound by the promotion out of tensor memory, some 1130 cycles per 128 x 256 group
+// against the MMA's 512, and by the padding of the experts' last tiles: 16384 rows
+// of 64 experts, 4096 x 4096 (a quarter of the tiles' rows padding), 321 us, 1.72
+// PFLOP/s; 128-column tiles take 397.  1013 rows of 16 experts, 520 x 1088: 7.4 us, the
+// latency of launch, offsets and nine groups.
 //
 // Roles per CTA, promotion and scale ring are those of the tiled kernel (see
 // gemm_tiled.cu): warp 0 TMA producer, warps 1 and 3 MMA issuers, warp 2 scale
@@ -30,6 +28,7 @@
 #include "kernels.cuh"
 #include "promote.cuh"
 #include "ptx.cuh"
+#include "ragged.cuh"
 
 namespace w8a8 {
 
@@ -64,92 +63,13 @@ template <int BN, int STAGES, int CPW, int EB> struct RaggedLayout {
     static_assert(kSmem <= 232448, "shared memory per CTA");
 };
 
-// Exclusive prefix over the CTA's threads with Op, in thread order.
-template <int THREADS, typename Op>
-__device__ __forceinline__ int block_prefix(int v, int neutral, volatile int *warp_part, Op op)
-{
-    const int lane = static_cast<int>(lane_index()), w = static_cast<int>(warp_index());
-    int inc = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o)
-            inc = op(inc, u);
-    }
-    if (lane == 31)
-        warp_part[w] = inc;
-    __syncthreads();
-    int base = neutral;
-    for (int i = 0; i < w; ++i)
-        base = op(base, warp_part[i]);
-    const int up = __shfl_up_sync(0xffffffffu, inc, 1);
-    __syncthreads();
-    return lane > 0 ? op(base, up) : base;
-}
-
-// The items of one CTA: blockIdx.x, blockIdx.x + gridDim.x, ... over (row
-// tile, column tile), column tiles innermost, so that the CTAs running at one
-// time share row tiles of A and an expert's weights in L2.  SPLIT: the one item
-// of this CTA's cluster, of which it takes the K groups g0 .. g1-1.
-template <bool SPLIT> __device__ __forceinline__ int first_item(const RaggedParams &p)
-{
-    return static_cast<int>(SPLIT ? blockIdx.x / p.split : blockIdx.x);
-}
-template <bool SPLIT>
-__device__ __forceinline__ void group_range(const RaggedParams &p, int &g0, int &g1)
-{
-    g0 = 0;
-    g1 = p.G;
-    if (SPLIT) {
-        const int r = static_cast<int>(blockIdx.x % p.split);
-        g0 = p.G * r / p.split;
-        g1 = p.G * (r + 1) / p.split;
-    }
-}
-template <bool SPLIT> struct RaggedWalk {
-    const int *row0, *tile0;      // [experts + 1] first row and first tile of each expert
-    int item, items, num_n, experts;
-    int e, m0, rows, nb;          // the current item: expert, first row, valid rows, column tile
-    __device__ RaggedWalk(const RaggedParams &p, const int *r, const int *t)
-        : row0(r), tile0(t), item(first_item<SPLIT>(p)), items(t[p.experts] * p.num_n_tiles),
-          num_n(p.num_n_tiles), experts(p.experts)
-    {
-    }
-    __device__ bool next()
-    {
-        if (item >= items)
-            return false;
-        const int mt = item / num_n;
-        nb = item - mt * num_n;
-        int lo = 0, hi = experts - 1;            // last expert whose first tile is <= mt
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (tile0[mid] <= mt)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
-        e = lo;
-        m0 = row0[lo] + (mt - tile0[lo]) * 128;
-        rows = min(128, row0[lo + 1] - m0);
-        item = SPLIT ? items : item + static_cast<int>(gridDim.x);
-        return true;
-    }
-};
-
-// A partial tile in shared memory: rows of 128 floats, padded so that neighbouring
-// rows start in different banks.
-constexpr int kPartialPitch = 132;
-
-template <int BN, int STAGES, int CPW, int EB, bool SPLIT>
+template <int BN, int STAGES, int CPW, int EB>
 __global__ void __launch_bounds__(RaggedLayout<BN, STAGES, CPW, EB>::kThreads, 1)
     k_ragged(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmTile,
              const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmC,
              const RaggedParams p)
 {
     using L = RaggedLayout<BN, STAGES, CPW, EB>;
-    static_assert(!SPLIT || (BN == 128 && 128 * kPartialPitch * 4 <= L::kStageBytes),
-                  "the partial tile takes the stages' place");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -216,47 +136,7 @@ __global__ void __launch_bounds__(RaggedLayout<BN, STAGES, CPW, EB>::kThreads, 1
     grid_launch_dependents();
     grid_dependency_wait();
 
-    // The tile list.  Offsets that decrease or leave [0, M] are bent into a
-    // non-decreasing sequence in [0, M] (a running maximum), so that nothing
-    // below leaves a buffer whatever they hold.
-    {
-        constexpr int kPerThread = (kRaggedMaxExperts + 1 + L::kThreads - 1) / L::kThreads;
-        const int first = static_cast<int>(threadIdx.x) * kPerThread;
-        auto max_op = [](int a, int b) { return max(a, b); };
-        auto add_op = [](int a, int b) { return a + b; };
-        int o[kPerThread], top = 0;
-#pragma unroll
-        for (int i = 0; i < kPerThread; ++i) {
-            o[i] = first + i <= p.experts ? min(max(__ldg(p.offsets + first + i), 0), p.M) : 0;
-            top = max(top, o[i]);
-        }
-        int run = block_prefix<L::kThreads>(top, 0, warp_part, max_op);
-#pragma unroll
-        for (int i = 0; i < kPerThread; ++i) {
-            run = max(run, o[i]);
-            if (first + i <= p.experts)
-                row0[first + i] = run;
-        }
-        __syncthreads();
-        int tiles[kPerThread], sum = 0;
-#pragma unroll
-        for (int i = 0; i < kPerThread; ++i) {
-            const int e = first + i;
-            tiles[i] = e < p.experts ? (row0[e + 1] - row0[e] + 127) / 128 : 0;
-            sum += tiles[i];
-        }
-        int at = block_prefix<L::kThreads>(sum, 0, warp_part, add_op);
-#pragma unroll
-        for (int i = 0; i < kPerThread; ++i) {
-            if (first + i <= p.experts)
-                tile0[first + i] = at;
-            at += tiles[i];
-        }
-        __syncthreads();
-    }
-
-    int g0, g1;
-    group_range<SPLIT>(p, g0, g1);
+    make_tile_list<L::kThreads, 128>(p, row0, tile0, warp_part);
 
     if (warp < 4) {
         regs_dealloc<L::kRegsLow>();
@@ -267,8 +147,8 @@ __global__ void __launch_bounds__(RaggedLayout<BN, STAGES, CPW, EB>::kThreads, 1
             uint32_t phase = 0;
             long long issued = 0;
             bool ok = true;
-            RaggedWalk<SPLIT> w(p, row0, tile0);
-            while (ok && w.next()) {
+            RaggedWalk<128> w(p, row0, tile0, static_cast<int>(blockIdx.x));
+            while (ok && w.next(static_cast<int>(gridDim.x))) {
                 // All 128 rows at once, or the boxes of 32 that hold valid ones (an
                 // issue takes the producer some hundred cycles: with four boxes for
                 // a whole tile, 128-column tiles took 476 us instead of 412 for
@@ -277,7 +157,7 @@ __global__ void __launch_bounds__(RaggedLayout<BN, STAGES, CPW, EB>::kThreads, 1
                 const CUtensorMap *const map_a = whole ? &tmTile : &tmA;
                 const int loads = whole ? 1 : (w.rows + kBoxRows - 1) / kBoxRows;
                 const uint32_t a_bytes = (whole ? 128 : loads * kBoxRows) * 128u;
-                for (int g = g0; g < g1; ++g) {
+                for (int g = 0; g < p.G; ++g) {
                     ok = __all_sync(0xffffffffu, wait_bounded(empty_bar(stage), phase ^ 1u, guard,
                                                               SITE_TILED_PRODUCER));
                     if (!ok)
@@ -337,9 +217,9 @@ __global__ void __launch_bounds__(RaggedLayout<BN, STAGES, CPW, EB>::kThreads, 1
             uint32_t it = 0;
             bool ok = true;
             const int items = tile0[p.experts] * p.num_n_tiles;
-            for (int item = first_item<SPLIT>(p); ok && item < items;
-                 item = SPLIT ? items : item + static_cast<int>(gridDim.x)) {
-                for (int g = g0; g < g1; ++g) {
+            for (int item = static_cast<int>(blockIdx.x); ok && item < items;
+                 item += static_cast<int>(gridDim.x)) {
+                for (int g = 0; g < p.G; ++g) {
                     if (it % L::kIssuers == me) {
                         const uint32_t buf = it % L::kBufs;
                         const uint32_t bphase = (it / L::kBufs) & 1u;
@@ -377,10 +257,10 @@ __global__ void __launch_bounds__(RaggedLayout<BN, STAGES, CPW, EB>::kThreads, 1
             int slot = 0;
             uint32_t sphase = 0;
             bool ok = true;
-            RaggedWalk<SPLIT> w(p, row0, tile0);
-            while (ok && w.next()) {
+            RaggedWalk<128> w(p, row0, tile0, static_cast<int>(blockIdx.x));
+            while (ok && w.next(static_cast<int>(gridDim.x))) {
                 const size_t b_row0 = static_cast<size_t>(w.e) * p.NB;
-                for (int g = g0; g < g1; ++g) {
+                for (int g = 0; g < p.G; ++g) {
                     ok = __all_sync(0xffffffffu, wait_bounded(sempty_bar(slot), sphase ^ 1u, guard,
                                                               SITE_TILED_SCALES));
                     if (!ok)
@@ -410,11 +290,6 @@ __global__ void __launch_bounds__(RaggedLayout<BN, STAGES, CPW, EB>::kThreads, 1
             // Let every gather land before the CTA can exit.
             asm volatile("cp.async.wait_all;" ::: "memory");
         }
-        __syncwarp();
-        if (SPLIT) {
-            cluster_sync();       // the partial rows are in shared memory
-            cluster_sync();       // and have been read
-        }
     } else {
         // -------------------------------------------------------------- promotion + epilogue
         regs_alloc<L::kRegsHigh>();
@@ -426,8 +301,8 @@ __global__ void __launch_bounds__(RaggedLayout<BN, STAGES, CPW, EB>::kThreads, 1
         uint32_t it = 0;
         int slot = 0;
         uint32_t sphase = 0;
-        RaggedWalk<SPLIT> w(p, row0, tile0);
-        while (w.next()) {
+        RaggedWalk<128> w(p, row0, tile0, static_cast<int>(blockIdx.x));
+        while (w.next(static_cast<int>(gridDim.x))) {
             const int col0 = w.nb * BN + h * CPW;
             const int mine = min(32, w.rows - static_cast<int>(q * 32));   // rows of this warp
             const bool idle = mine <= 0 || col0 >= p.N;
@@ -436,7 +311,7 @@ __global__ void __launch_bounds__(RaggedLayout<BN, STAGES, CPW, EB>::kThreads, 1
             for (int j = 0; j < L::kPairs; ++j)
                 acc[j] = 0ull;
             bool ok = true;
-            for (int g = g0; g < g1; ++g) {
+            for (int g = 0; g < p.G; ++g) {
                 const uint32_t buf = it % L::kBufs;
                 const uint32_t bphase = (it / L::kBufs) & 1u;
                 ok = __all_sync(0xffffffffu,
@@ -471,19 +346,7 @@ __global__ void __launch_bounds__(RaggedLayout<BN, STAGES, CPW, EB>::kThreads, 1
             if (!ok)
                 break;
             const int y = w.m0 + static_cast<int>(q * 32);
-            if (SPLIT) {
-                // Every group's MMA has completed (its partial was read), so the
-                // stages are free.
-                float4 *part = reinterpret_cast<float4 *>(smem) + row * (kPartialPitch / 4) + h * (CPW / 4);
-#pragma unroll
-                for (int j = 0; j < CPW / 4; ++j) {
-                    float4 v;
-                    unpack2f(acc[2 * j], v.x, v.y);
-                    unpack2f(acc[2 * j + 1], v.z, v.w);
-                    if (!idle)
-                        part[j] = v;
-                }
-            } else if (!idle && in_bounds(y >= 0 && y + mine <= p.M, p.status, SITE_BOUNDS_C)) {
+            if (!idle && in_bounds(y >= 0 && y + mine <= p.M, p.status, SITE_BOUNDS_C)) {
                 auto pack = [&](int k, int j) {
                     if (fp32) {
                         const uint64_t a = acc[8 * k + 2 * j], b = acc[8 * k + 2 * j + 1];
@@ -503,44 +366,6 @@ __global__ void __launch_bounds__(RaggedLayout<BN, STAGES, CPW, EB>::kThreads, 1
         }
         if (lane == 0)
             tma_store_wait_read();
-        if (SPLIT) {
-            cluster_sync();
-            // Each CTA finishes its share of the tile's rows: 32 threads to a row,
-            // four columns each.
-            RaggedWalk<SPLIT> last(p, row0, tile0);
-            const int S = p.split, rank = static_cast<int>(blockIdx.x % p.split);
-            if (last.next()) {
-                const int n = last.nb * BN + 4 * static_cast<int>(lane);
-                const uint32_t at = smem_addr(smem) + 16u * lane;
-                const int r1 = last.rows * (rank + 1) / S;
-                for (int r = last.rows * rank / S + static_cast<int>(warp) - 4; r < r1 && n < p.N; r += 8) {
-                    float4 v[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)          // every load before the first addition
-                        if (i < S)
-                            v[i] = ld_cluster_f4(cluster_map(at + 4u * kPartialPitch * r,
-                                                             static_cast<uint32_t>(i)));
-#pragma unroll
-                    for (int i = 1; i < 8; ++i)
-                        if (i < S) {
-                            v[0].x += v[i].x;
-                            v[0].y += v[i].y;
-                            v[0].z += v[i].z;
-                            v[0].w += v[i].w;
-                        }
-                    const size_t to = static_cast<size_t>(last.m0 + r) * p.N + n;
-                    if (!in_bounds(last.m0 + r < p.M && n + 4 <= p.N, p.status, SITE_BOUNDS_C))
-                        continue;
-                    if (fp32)
-                        *reinterpret_cast<float4 *>(static_cast<float *>(p.C) + to) = v[0];
-                    else
-                        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.C) + to) =
-                            bf ? make_uint2(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[0].z, v[0].w))
-                               : make_uint2(pack_f16x2(v[0].x, v[0].y), pack_f16x2(v[0].z, v[0].w));
-                }
-            }
-            cluster_sync();
-        }
     }
 
     tc_fence_before_sync();
@@ -551,65 +376,38 @@ __global__ void __launch_bounds__(RaggedLayout<BN, STAGES, CPW, EB>::kThreads, 1
     }
 }
 
-template <int BN, int STAGES, int CPW, int EB, bool SPLIT>
+template <int BN, int STAGES, int CPW, int EB>
 cudaError_t launch_ragged_t(const CUtensorMap &tmA, const CUtensorMap &tmTile,
                             const CUtensorMap &tmB, const CUtensorMap &tmC, const RaggedParams &p,
-                            const LaunchCfg &cfg, int *clusters = nullptr)
+                            const LaunchCfg &cfg)
 {
     using L = RaggedLayout<BN, STAGES, CPW, EB>;
-    auto kernel = k_ragged<BN, STAGES, CPW, EB, SPLIT>;
+    auto kernel = k_ragged<BN, STAGES, CPW, EB>;
     static volatile int smem_set[kMaxDeviceFlags] = {};
     cudaError_t e = ensure_smem_limit(kernel, smem_set);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(clusters ? p.split : cfg.grid, 1, 1);
+    lc.gridDim = dim3(cfg.grid, 1, 1);
     lc.blockDim = dim3(L::kThreads, 1, 1);
     lc.dynamicSmemBytes = L::kSmem;
     lc.stream = cfg.stream;
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     // the kernel waits for the work before it ahead of its first access
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = clusters ? 0 : 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(SPLIT ? p.split : 1);
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = attr;
-    lc.numAttrs = SPLIT ? 2 : 1;
-    if (clusters)
-        return cudaOccupancyMaxActiveClusters(clusters, kernel, &lc);
+    lc.numAttrs = 1;
     return cudaLaunchKernelEx(&lc, kernel, tmA, tmTile, tmB, tmC, p);
 }
 
 }  // namespace
 
-int ragged_clusters(int split)
-{
-    static volatile int cached[kMaxDeviceFlags][9] = {};
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDeviceFlags)
-        return 0;
-    if (cached[dev][split])
-        return cached[dev][split];
-    const CUtensorMap none = {};
-    RaggedParams p = {};
-    p.split = split;
-    if (launch_ragged_t<128, 6, 64, 1, true>(none, none, none, none, p, LaunchCfg{}, &n) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    cached[dev][split] = n;
-    return n;
-}
-
 cudaError_t launch_ragged(const CUtensorMap &tmA, const CUtensorMap &tmTile, const CUtensorMap &tmB,
                           const CUtensorMap &tmC, const RaggedParams &p, int bn, const LaunchCfg &cfg)
 {
-    if (p.split > 1)
-        return launch_ragged_t<128, 6, 64, 1, true>(tmA, tmTile, tmB, tmC, p, cfg);
-    return bn == 256 ? launch_ragged_t<256, 4, 128, 1, false>(tmA, tmTile, tmB, tmC, p, cfg)
-                     : launch_ragged_t<128, 6, 64, 1, false>(tmA, tmTile, tmB, tmC, p, cfg);
+    return bn == 256 ? launch_ragged_t<256, 4, 128, 1>(tmA, tmTile, tmB, tmC, p, cfg)
+                     : launch_ragged_t<128, 6, 64, 1>(tmA, tmTile, tmB, tmC, p, cfg);
 }
 
 }  // namespace w8a8

@@ -13,10 +13,13 @@
 // every 512 columns of K the accumulator is added to 32-bit integer registers:
 // the INT8 product at the fp16 tensor rate, to the bit.
 //
-// Two launches: k_int8_widen writes both operands as fp16 into the workspace
-// (rows padded with zeros to whole 128-column stages, so that any size, stride
-// and alignment of the INT8 operands is as good as another), k_int8_mma
-// multiplies them.
+// Three forms, by how often a widened value is used:
+//  - up to 32 tokens, k_int8_small widens in registers right after the load;
+//  - some hundred tokens, k_int8_mid widens on the way to shared memory;
+//  - beyond, k_int8_widen writes both operands as fp16 into the workspace (rows
+//    padded with zeros to whole 128-column stages, so that any size, stride and
+//    alignment of the INT8 operands is as good as another) and k_int8_mma
+//    multiplies them.
 #include <algorithm>
 
 #include "epilogue.cuh"
@@ -122,7 +125,8 @@ __device__ __forceinline__ void widen_rows(const uint8_t *src, long long ld, uin
     }
 }
 
-// Both operands in one launch.
+// Both operands in one launch.  HBM- and L2-bound: of 16384 x 4096 and 4096 x 4096 it
+// reads 84 MB and writes 168 in about 36 us (7 TB/s).
 template <int ACCESS>
 __global__ void __launch_bounds__(kWidenThreads) k_int8_widen(const Int8WidenParams p)
 {
@@ -390,7 +394,10 @@ cudaError_t launch_small_t(const Int8SmallParams &p, int access, int sm_count, c
 // added up then, and the cluster's CTAs, which split K, add theirs through
 // distributed shared memory.
 // Bound by shared memory: a step's 24 KB (of 128 + 64 rows) to 48 KB (128 + 256)
-// are written once and read once by the MMA.
+// are written once and read once by the MMA; where CTAs have few steps, by the
+// latency of launch, first loads and the cluster's sum.  256 tokens by 4096 x
+// 4096: 20.7 us (the widening launch and k_int8_mma: 24.6), 512: 41.0 (26.1); 257 by
+// 1537 x 1000, rows off 16-byte boundaries: 8.6.
 constexpr int kMidGroup = 8;
 constexpr int kMidGroups = 2;
 constexpr int kMidWarps = kMidGroup * kMidGroups;
@@ -726,6 +733,8 @@ __device__ __forceinline__ void int8_tile_coords(int t, int num_m, int num_n, in
 // are those of the FP8 kernels (gemm_tiled.cu, gemm_pair.cu) without their
 // per-group scales: warp 0 TMA producer, warp 1 MMA issuer (the odd CTA's:
 // forwarder of its landed stages), warps 4.. integer promotion and epilogue.
+// Bound by the tensor cores under the power cap: 16384 x 4096 x 4096 with the
+// widening launch takes 341 us, without it about 300, 1.83 PFLOP/s (one-CTA tiles: 432).
 template <bool PAIR, int BN, int STAGES, int CPW, int EB>
 __global__ void __launch_bounds__(Int8Layout<PAIR, BN, STAGES, CPW, EB>::kThreads, 1)
     k_int8_mma(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,

@@ -198,19 +198,23 @@ struct RaggedParams {
     int M, N, K, G, NB;
     int experts;
     int num_n_tiles;       // column tiles of BN
-    int split;             // CTAs of a cluster that share an item's K groups (1: none), at
-                           // most G; then bn is 128 and the grid holds split CTAs for
-                           // every item there can be
+    int split;             // launch_ragged_few: CTAs of a cluster that share an item's K
+                           // groups (1: none), at most G and 8; then the grid holds split
+                           // CTAs for every item there can be
     int out_kind;
     int debug_skip_tma;    // test hook: >= 0 makes the producer skip that many-th load
     unsigned *status;
     unsigned long long wait_limit;
 };
-int ragged_clusters(int split);        // clusters of `split` CTAs that run at once
 // tmA, tmTile: A in boxes of 32 and of 128 rows; tmB: 3-D [experts, N, K], boxes of
 // bn rows; tmC as for launch_tiled.  bn: 128 or 256.
 cudaError_t launch_ragged(const CUtensorMap &tmA, const CUtensorMap &tmTile, const CUtensorMap &tmB,
                           const CUtensorMap &tmC, const RaggedParams &p, int bn, const LaunchCfg &cfg);
+
+// Few rows per expert: tiles of 32 rows and 128 columns, tmA and tmB (bn = 128) as above.
+cudaError_t launch_ragged_few(const CUtensorMap &tmA, const CUtensorMap &tmB, const RaggedParams &p,
+                              const LaunchCfg &cfg);
+int ragged_few_clusters(int split);    // its clusters of `split` CTAs that run at once
 
 // INT8 matmul.  Widening: rows_a rows of A and rows_b of B (INT8, K columns) to
 // fp16 rows of Kp columns (a multiple of 128; zeros past K).

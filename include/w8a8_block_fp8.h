@@ -441,13 +441,14 @@ w8a8_status w8a8_block_fp8_grouped_matmul_contiguous(const void *A_dev, const fl
  * decrease or leave [0, M] give unspecified results but never an out-of-bounds
  * access.  E <= W8A8_RAGGED_MAX_EXPERTS; M == 0 is a no-op, E == 0 with rows is
  * W8A8_ERR_INVALID_ARG; other shape rules as for the plain tensor-core call.
- * One kernel for every routing, from one row to full prefill; no workspace.  Its
+ * One launch whatever the routing, from one row to full prefill; no workspace.  The
  * launch may overlap the end of the work before it on the stream, which it waits
  * for on the device, whatever opts->pdl says.
- * opts: variant AUTO or TILED; block_n_tile 128 or 256, grid_limit, split_k (0 =
- * choose; 1 = none; 2, 4 or 8 CTAs of a cluster share an item's K groups, where every
- * item finds a cluster, else W8A8_ERR_UNSUPPORTED; the partial sums are added in a
- * fixed order), wait_limit_cycles and the test hooks apply.
+ * opts: variant AUTO or TILED; m_tile 32 (few rows per expert) or 128, with m_tile
+ * 128 block_n_tile 128 or 256 (0 = choose); grid_limit; split_k (0 = choose; 1 =
+ * none; with m_tile 32, 2, 4 or 8 CTAs of a cluster share an item's K groups, where
+ * every item finds a cluster, else W8A8_ERR_UNSUPPORTED; the partial sums are added
+ * in a fixed order), wait_limit_cycles and the test hooks apply.
  */
 #define W8A8_RAGGED_MAX_EXPERTS 1024
 w8a8_status w8a8_block_fp8_grouped_matmul_ragged(const void *A_dev, const float *a_s_dev,

@@ -82,6 +82,10 @@ def run_all(seed=1):
         C = torch.zeros(230, 264, device="cuda")
         out[f"ragged{bn}"] = w8.grouped_matmul_ragged(A, rn(230, 4).abs(), B, rn(5, 3, 4).abs(), off, "fp32", out=C,
                                                       block_n_tile=bn)
+    for split in (1, 2):
+        C = torch.zeros(230, 264, device="cuda")
+        out[f"ragged_few{split}"] = w8.grouped_matmul_ragged(A, rn(230, 4).abs(), B, rn(5, 3, 4).abs(), off, "fp32",
+                                                             out=C, m_tile=32, split_k=split)
     for name, M, N, K, v in (("small8", 3, 50, 200, 5), ("small32", 29, 130, 333, 5), ("mid", 100, 200, 520, 2),
                              ("tiled", 300, 200, 520, 1), ("pair", 300, 300, 515, 6)):
         out["int8_" + name] = w8.int8_matmul(i8(M, K), rn(M), i8(N, K), rn(N), "fp32", variant=v)

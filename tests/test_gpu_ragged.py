@@ -87,6 +87,42 @@ def test_parity(counts, N, K, opts, out):
     assert_right(C, x, out, f"{len(counts)} experts N={N} K={K} {opts} {out}")
 
 
+FEW = [
+    # counts, N, K: 32-row tiles, whole and split over K
+    ([1], 8, 16),
+    ([0, 31, 32, 33, 0, 64, 65, 1], 264, 528),
+    ([2, 1, 0, 3] * 64, 520, 1040),
+    ([200, 0, 9, 100], 136, 1088),
+    ([1] * 700, 384, 256),
+    ([5, 0, 3], 1000, 4096),
+]
+
+
+@pytest.mark.parametrize("counts,N,K", FEW)
+@pytest.mark.parametrize("out", ["bf16", "fp16", "fp32"])
+def test_tiles_of_32_rows(counts, N, K, out):
+    x = make(counts, N, K, seed=N + K + 1, start=3, tail=5)
+    M = x[0].shape[0]
+    for opts in (dict(), dict(split_k=1), dict(grid_limit=5)):
+        C = torch.full((M, N), 7.0, dtype=OUT[out], device="cuda")
+        w8.grouped_matmul_ragged(*x, out, out=C, m_tile=32, **opts)
+        torch.cuda.synchronize()
+        assert w8.w8a8_get_device_status()[0] == w8.W8A8_OK
+        assert_right(C, x, out, f"{opts}")
+        assert (C[:3] == 7).all() and (C[M - 5:] == 7).all()
+
+
+def test_a_wait_that_runs_out_in_tiles_of_32_rows():
+    x = make([5, 6], 256, 1024, seed=11)
+    for opts in (dict(split_k=1, debug_skip_load=3), dict(split_k=4, debug_skip_load=1)):
+        w8.grouped_matmul_ragged(*x, m_tile=32, wait_limit_cycles=2_000_000, **opts)
+        assert w8.w8a8_get_device_status()[0] == w8.W8A8_ERR_DEVICE_TIMEOUT
+        C = w8.grouped_matmul_ragged(*x, m_tile=32)
+        torch.cuda.synchronize()
+        assert w8.w8a8_get_device_status()[0] == w8.W8A8_OK
+        assert_right(C, x, "bf16")
+
+
 def test_equals_the_plain_matmul_per_expert():
     """Every expert's rows carry the bits of a plain call on them alone."""
     counts = [70, 0, 129, 3]
