@@ -1011,7 +1011,8 @@ struct QuantParams {
 };
 
 // HELD: the row stays in registers; otherwise it is read twice.
-// Bound by the divisions' instructions: 16384 x 4096 in bf16 43.0 us (4.7 TB/s).
+// 16384 x 4096 in bf16: 43.0 us (4.7 TB/s), with 60 % of the issue slots taken, most by
+// the correctly rounded quotients.
 template <int KIND, int VEC, bool HELD>
 __global__ void __launch_bounds__(kMaxThreads) k_quant_int8(const QuantParams p)
 {
