@@ -286,10 +286,11 @@ def quantize_int8_per_token(X, A=None, a_s=None, stream=None):
     """Per-token INT8 quantisation of a CUDA tensor X [M, K] (bf16, fp16 or fp32, unit
     stride along K): returns (A int8 [M, K], a_s float32 [M]), the INT8 matmul's
     activation operand.  ``A`` / ``a_s`` may be preallocated."""
-    import torch
     shape = X.shape
     M, K = shape
     code = _in_codes[X.dtype]
+    if A is None or a_s is None:
+        import torch
     if A is None:
         A = torch.empty(shape, dtype=torch.int8, device=X.device)
     elif A.shape != shape:
@@ -310,6 +311,13 @@ def quantize_int8_per_token(X, A=None, a_s=None, stream=None):
 _NORM_KINDS = {"same": W8A8_NORM_SAME, "fp8": W8A8_NORM_FP8, "int8": W8A8_NORM_INT8}
 
 
+def _norm_weight(t, dtype, D=None):
+    """Why a norm's weight (or gate, without D) is refused."""
+    if t.dtype is not dtype or not t.is_contiguous():
+        raise W8A8Error(W8A8_ERR_UNSUPPORTED, "weights and gate must be contiguous, of h's dtype")
+    _want(t, (D,), "a norm's weight")
+
+
 def sandwich_norm(h, x, w_post=None, w_pre=None, gate=None, gate_rows=None, res_scale=1.0,
                   eps=1e-6, out="same", x_out=None, y_out=None, scales_out=None, stream=None):
     """The norms around a block, fused with its gate and residual, on CUDA tensors:
@@ -321,13 +329,14 @@ def sandwich_norm(h, x, w_post=None, w_pre=None, gate=None, gate_rows=None, res_
     r in x's type; with out="fp8" (E4M3 codes and one scale per 128 columns) or "int8"
     (one scale per row) (r, codes, scales).  x_out may be x itself.  Raises W8A8Error
     on a non-zero status."""
-    import torch
     shape = h.shape
     M, D = shape
     dtype, xtype = h.dtype, x.dtype
     hk, kind = _in_codes[dtype], _NORM_KINDS[out]
     if x.shape != shape:
         _want(x, shape, "x")
+    if x_out is None or y_out is None or scales_out is None and kind:
+        import torch            # not on the way of a call with its outputs (0.1 us)
     if x_out is None:
         x_out = torch.empty(shape, dtype=xtype, device=x.device)
     elif x_out.shape != shape or x_out.dtype is not xtype:
@@ -347,26 +356,34 @@ def sandwich_norm(h, x, w_post=None, w_pre=None, gate=None, gate_rows=None, res_
             _want(scales_out, s_shape, "scales_out")
             _dense(scales_out, "scales_out")
         scales = scales_out.data_ptr()
-    ptrs = [None, None, None]
-    for i, t in enumerate((w_post, w_pre, gate)):
-        if t is not None:
-            if t.dtype is not dtype or not t.is_contiguous():
-                raise W8A8Error(W8A8_ERR_UNSUPPORTED,
-                                "weights and gate must be contiguous, of h's dtype")
-            if i < 2 and t.shape != (D,):
-                _want(t, (D,), "a norm's weight")
-            ptrs[i] = t.data_ptr()
+    width = (D,)
+    post = pre = gates = None
+    if w_post is not None:
+        if w_post.dtype is not dtype or not w_post.is_contiguous() or w_post.shape != width:
+            _norm_weight(w_post, dtype, D)
+        post = w_post.data_ptr()
+    if w_pre is not None:
+        if w_pre.dtype is not dtype or not w_pre.is_contiguous() or w_pre.shape != width:
+            _norm_weight(w_pre, dtype, D)
+        pre = w_pre.data_ptr()
     if gate is not None:
-        R = gate.shape[0] if gate.dim() == 2 else 1
+        if gate.dtype is not dtype or not gate.is_contiguous():
+            _norm_weight(gate, dtype)
+        gates = gate.data_ptr()
+        g_shape = gate.shape
+        R = g_shape[0] if len(g_shape) == 2 else 1
         if gate_rows is None:
             gate_rows = max(1, -(-M // max(R, 1)))
-        if gate.shape[-1] != D or gate_rows < 1 or R * gate_rows < M:
+        if g_shape[-1] != D or gate_rows < 1 or R * gate_rows < M:
             raise W8A8Error(W8A8_ERR_INVALID_ARG,
-                            f"gate of {tuple(gate.shape)} for {M} rows of {D}, {gate_rows} to a gate")
+                            f"gate of {tuple(g_shape)} for {M} rows of {D}, {gate_rows} to a gate")
     st = load_library().w8a8_sandwich_norm(
-        h.data_ptr(), hk, _rows(h), x.data_ptr(), _in_codes[xtype], _rows(x), ptrs[0], ptrs[2],
-        gate_rows or 1, ptrs[1], res_scale, eps, x_out.data_ptr(), _rows(x_out), y_out.data_ptr(),
-        scales, kind, _rows(y_out), M, D, _stream(stream))
+        h.data_ptr(), hk, 0 if h.is_contiguous() else _rows(h),
+        x.data_ptr(), _in_codes[xtype], 0 if x.is_contiguous() else _rows(x),
+        post, gates, gate_rows or 1, pre, res_scale, eps,
+        x_out.data_ptr(), 0 if x_out.is_contiguous() else _rows(x_out),
+        y_out.data_ptr(), scales, kind, 0 if y_out.is_contiguous() else _rows(y_out),
+        M, D, _stream(stream))
     if st:
         check(st)
     return (x_out, y_out) if not kind else (x_out, y_out, scales_out)
