@@ -258,9 +258,15 @@ def int8_matmul(A, a_s, B, b_s, out_dtype="bf16", out=None, stream=None, **opts)
     need unit stride along their last dimension only.  Keyword options map to
     w8a8_options fields.  Raises W8A8Error on a non-zero status."""
     import torch
+    code, lib = out_code(out_dtype), load_library()
+    if out is not None and not opts and lib.int8_tensors is not None:
+        st = lib.int8_tensors(A, a_s, B, b_s, out, code, torch.int8, _stream(stream))
+        if st == 0:
+            return out
+        if st is not None:
+            check(st)
     M, K = A.shape
     N = B.shape[0]
-    code = out_code(out_dtype)
     if A.dtype is not torch.int8 or B.dtype is not torch.int8:
         raise W8A8Error(W8A8_ERR_INVALID_ARG, f"A and B must be int8, not {A.dtype}, {B.dtype}")
     if B.shape != (N, K) or a_s.shape != (M,) or b_s.shape != (N,):
@@ -274,7 +280,7 @@ def int8_matmul(A, a_s, B, b_s, out_dtype="bf16", out=None, stream=None, **opts)
     if not (a_s.is_contiguous() and b_s.is_contiguous()):
         raise W8A8Error(W8A8_ERR_UNSUPPORTED, "scales must be contiguous")
     o = options(**opts) if opts else None
-    st = load_library().w8a8_int8_matmul(
+    st = lib.w8a8_int8_matmul(
         A.data_ptr(), _rows(A), a_s.data_ptr(), B.data_ptr(), _rows(B), b_s.data_ptr(),
         out.data_ptr(), _rows(out), M, N, K, code, _stream(stream), _opts_address(o))
     if st:
@@ -286,6 +292,13 @@ def quantize_int8_per_token(X, A=None, a_s=None, stream=None):
     """Per-token INT8 quantisation of a CUDA tensor X [M, K] (bf16, fp16 or fp32, unit
     stride along K): returns (A int8 [M, K], a_s float32 [M]), the INT8 matmul's
     activation operand.  ``A`` / ``a_s`` may be preallocated."""
+    lib = load_library()
+    if A is not None and a_s is not None and lib.quant_tensors is not None:
+        st = lib.quant_tensors(X, A, a_s, _in_codes, _stream(stream))
+        if st == 0:
+            return A, a_s
+        if st is not None:
+            check(st)
     shape = X.shape
     M, K = shape
     code = _in_codes[X.dtype]
@@ -300,7 +313,7 @@ def quantize_int8_per_token(X, A=None, a_s=None, stream=None):
     elif a_s.shape != (M,) or not a_s.is_contiguous():
         _want(a_s, (M,), "a_s")
         _dense(a_s, "a_s")
-    st = load_library().w8a8_quantize_int8_per_token(
+    st = lib.w8a8_quantize_int8_per_token(
         X.data_ptr(), code, _rows(X), A.data_ptr(), _rows(A), a_s.data_ptr(), M, K,
         _stream(stream))
     if st:
@@ -329,10 +342,18 @@ def sandwich_norm(h, x, w_post=None, w_pre=None, gate=None, gate_rows=None, res_
     r in x's type; with out="fp8" (E4M3 codes and one scale per 128 columns) or "int8"
     (one scale per row) (r, codes, scales).  x_out may be x itself.  Raises W8A8Error
     on a non-zero status."""
+    kind, lib = _NORM_KINDS[out], load_library()
+    if x_out is not None and y_out is not None and lib.norm_tensors is not None:
+        st = lib.norm_tensors(h, x, w_post, w_pre, gate, gate_rows, res_scale, eps, kind, x_out, y_out,
+                              scales_out, _in_codes, _stream(stream))
+        if st == 0:
+            return (x_out, y_out) if not kind else (x_out, y_out, scales_out)
+        if st is not None:
+            check(st)
     shape = h.shape
     M, D = shape
     dtype, xtype = h.dtype, x.dtype
-    hk, kind = _in_codes[dtype], _NORM_KINDS[out]
+    hk = _in_codes[dtype]
     if x.shape != shape:
         _want(x, shape, "x")
     if x_out is None or y_out is None or scales_out is None and kind:
@@ -377,7 +398,7 @@ def sandwich_norm(h, x, w_post=None, w_pre=None, gate=None, gate_rows=None, res_
         if g_shape[-1] != D or gate_rows < 1 or R * gate_rows < M:
             raise W8A8Error(W8A8_ERR_INVALID_ARG,
                             f"gate of {tuple(g_shape)} for {M} rows of {D}, {gate_rows} to a gate")
-    st = load_library().w8a8_sandwich_norm(
+    st = lib.w8a8_sandwich_norm(
         h.data_ptr(), hk, 0 if h.is_contiguous() else _rows(h),
         x.data_ptr(), _in_codes[xtype], 0 if x.is_contiguous() else _rows(x),
         post, gates, gate_rows or 1, pre, res_scale, eps,

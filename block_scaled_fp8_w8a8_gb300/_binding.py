@@ -112,6 +112,7 @@ _PYCALL = ("w8a8_sandwich_norm", "w8a8_block_fp8_grouped_matmul_ragged", "w8a8_i
 def _bind_pycall(lib):
     """Give those functions of the loaded library their entries from the extension
     module where it has been built; they take the same arguments."""
+    lib.norm_tensors = lib.int8_tensors = lib.quant_tensors = None
     path = _build.pycall_path()
     if not os.path.exists(path):
         return
@@ -120,6 +121,9 @@ def _bind_pycall(lib):
     loader.exec_module(mod)
     mod.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _PYCALL))
     for n in _PYCALL:
+        setattr(lib, n, getattr(mod, n))
+    # the plain case of the Python calls, on tensors (see pycall.c)
+    for n in ("norm_tensors", "int8_tensors", "quant_tensors"):
         setattr(lib, n, getattr(mod, n))
 
 

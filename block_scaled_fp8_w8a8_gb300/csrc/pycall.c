@@ -126,6 +126,169 @@ static PyObject *py_quant(PyObject *self, PyObject *const *args, Py_ssize_t n)
     return PyLong_FromLong(st);
 }
 
+/* ---- The calls on tensors.  sandwich_norm's checks read some thirty attributes, which
+ * takes Python code 2 us, as long as the launch, and half as long here.  These entries
+ * only take the plain case: every output given, every tensor dense.  Anything else,
+ * what is to be refused included, is None: the Python code looks at it. */
+typedef struct {
+    void *ptr;
+    int64_t size[2];
+    int dims;
+    PyObject *dtype;       /* borrowed: torch keeps its dtypes */
+} tensor_t;
+
+static PyObject *s_shape, *s_dtype, *s_dense, *s_ptr, *s_bytes;
+
+/* 1 for a dense tensor of one or two dimensions, else 0 (with or without an error set). */
+static int dense(PyObject *t, tensor_t *d)
+{
+    PyObject *o = PyObject_GetAttr(t, s_shape);
+    int ok = o && PyTuple_Check(o) && PyTuple_GET_SIZE(o) >= 1 && PyTuple_GET_SIZE(o) <= 2;
+    if (ok) {
+        d->dims = (int)PyTuple_GET_SIZE(o);
+        for (int i = 0; i < d->dims; ++i)
+            d->size[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(o, i));
+    }
+    Py_XDECREF(o);
+    if (!ok || !(o = PyObject_GetAttr(t, s_dtype)))
+        return 0;
+    d->dtype = o;
+    Py_DECREF(o);
+    if (!(o = PyObject_CallMethodNoArgs(t, s_dense)))
+        return 0;
+    ok = o == Py_True;
+    Py_DECREF(o);
+    if (!ok || !(o = PyObject_CallMethodNoArgs(t, s_ptr)))
+        return 0;
+    d->ptr = (void *)(uintptr_t)PyLong_AsUnsignedLongLong(o);
+    Py_DECREF(o);
+    return !PyErr_Occurred();
+}
+
+static int is(const tensor_t *d, int dims, int64_t a, int64_t b)
+{
+    return d->dims == dims && d->size[0] == a && (dims == 1 || d->size[1] == b);
+}
+
+/* h, x, w_post, w_pre, gate, gate_rows, res_scale, eps, kind, x_out, y_out, scales_out,
+ * the input types' codes by dtype, stream */
+static PyObject *py_norm_tensors(PyObject *self, PyObject *const *args, Py_ssize_t n)
+{
+    (void)self;
+    if (!want(n, 14, f_norm != NULL))
+        return NULL;
+    tensor_t h, x, xo, y, t;
+    void *post = NULL, *pre = NULL, *gate = NULL, *scales = NULL;
+    int64_t gate_rows = 1, M, D;
+    const int kind = I32(8);
+    if (!dense(args[0], &h) || h.dims != 2 || !dense(args[1], &x) || !dense(args[9], &xo) ||
+        !dense(args[10], &y))
+        goto other;
+    M = h.size[0], D = h.size[1];
+    if (!is(&x, 2, M, D) || !is(&xo, 2, M, D) || !is(&y, 2, M, D) || xo.dtype != x.dtype ||
+        (kind == 0 && y.dtype != h.dtype))
+        goto other;
+    if (kind != 0) {
+        PyObject *o = PyObject_CallMethodNoArgs(args[10], s_bytes);
+        const long bytes = o ? PyLong_AsLong(o) : 0;
+        Py_XDECREF(o);
+        if (bytes != 1 || !dense(args[11], &t) ||
+            !(kind == 1 ? is(&t, 2, M, (D + 127) / 128) : is(&t, 1, M, 0)))
+            goto other;
+        scales = t.ptr;
+    }
+    if (args[2] != Py_None) {
+        if (!dense(args[2], &t) || !is(&t, 1, D, 0) || t.dtype != h.dtype)
+            goto other;
+        post = t.ptr;
+    }
+    if (args[3] != Py_None) {
+        if (!dense(args[3], &t) || !is(&t, 1, D, 0) || t.dtype != h.dtype)
+            goto other;
+        pre = t.ptr;
+    }
+    if (args[4] != Py_None) {
+        if (!dense(args[4], &t) || t.size[t.dims - 1] != D || t.dtype != h.dtype)
+            goto other;
+        const int64_t rows = t.dims == 2 ? t.size[0] : 1;
+        if (args[5] != Py_None)
+            gate_rows = I64(5);
+        else if (rows > 0)
+            gate_rows = (M + rows - 1) / rows > 1 ? (M + rows - 1) / rows : 1;
+        if (gate_rows < 1 || rows < (M + gate_rows - 1) / gate_rows)
+            goto other;
+        gate = t.ptr;
+    }
+    PyObject *hk = PyDict_GetItemWithError(args[12], h.dtype);
+    PyObject *xk = PyDict_GetItemWithError(args[12], x.dtype);
+    if (!hk || !xk)
+        goto other;
+    const int h_code = (int)PyLong_AsLong(hk), x_code = (int)PyLong_AsLong(xk);
+    const double rs = PyFloat_AsDouble(args[6]), eps = PyFloat_AsDouble(args[7]);
+    void *s = PTR(13);
+    if (PyErr_Occurred())
+        goto other;
+    int st;
+    Py_BEGIN_ALLOW_THREADS
+    st = f_norm(h.ptr, h_code, 0, x.ptr, x_code, 0, post, gate, gate_rows, pre, (float)rs, (float)eps,
+                xo.ptr, 0, y.ptr, scales, kind, 0, M, D, s);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(st);
+other:
+    PyErr_Clear();
+    Py_RETURN_NONE;
+}
+
+/* A, a_s, B, b_s, out, output code, torch.int8, stream */
+static PyObject *py_int8_tensors(PyObject *self, PyObject *const *args, Py_ssize_t n)
+{
+    (void)self;
+    if (!want(n, 8, f_int8 != NULL))
+        return NULL;
+    tensor_t a, as, b, bs, c;
+    int st;
+    if (dense(args[0], &a) && dense(args[1], &as) && dense(args[2], &b) && dense(args[3], &bs) &&
+        dense(args[4], &c) && a.dtype == args[6] && b.dtype == args[6] && a.dims == 2 && b.dims == 2 &&
+        a.size[1] == b.size[1] && is(&as, 1, a.size[0], 0) && is(&bs, 1, b.size[0], 0) &&
+        is(&c, 2, a.size[0], b.size[0])) {
+        const int out = I32(5);
+        void *s = PTR(7);
+        if (!PyErr_Occurred()) {
+            Py_BEGIN_ALLOW_THREADS
+            st = f_int8(a.ptr, 0, as.ptr, b.ptr, 0, bs.ptr, c.ptr, 0, a.size[0], b.size[0], a.size[1], out,
+                        s, NULL);
+            Py_END_ALLOW_THREADS
+            return PyLong_FromLong(st);
+        }
+    }
+    PyErr_Clear();
+    Py_RETURN_NONE;
+}
+
+/* X, A, a_s, the input types' codes by dtype, stream */
+static PyObject *py_quant_tensors(PyObject *self, PyObject *const *args, Py_ssize_t n)
+{
+    (void)self;
+    if (!want(n, 5, f_quant != NULL))
+        return NULL;
+    tensor_t x, a, as;
+    int st;
+    if (dense(args[0], &x) && dense(args[1], &a) && dense(args[2], &as) && x.dims == 2 &&
+        is(&a, 2, x.size[0], x.size[1]) && is(&as, 1, x.size[0], 0)) {
+        PyObject *code = PyDict_GetItemWithError(args[3], x.dtype);
+        const int kind = code ? (int)PyLong_AsLong(code) : -1;
+        void *s = PTR(4);
+        if (code && !PyErr_Occurred()) {
+            Py_BEGIN_ALLOW_THREADS
+            st = f_quant(x.ptr, kind, 0, a.ptr, 0, as.ptr, x.size[0], x.size[1], s);
+            Py_END_ALLOW_THREADS
+            return PyLong_FromLong(st);
+        }
+    }
+    PyErr_Clear();
+    Py_RETURN_NONE;
+}
+
 /* bind(norm, ragged, int8, quant): addresses in the loaded library */
 static PyObject *py_bind(PyObject *self, PyObject *const *args, Py_ssize_t n)
 {
@@ -136,6 +299,13 @@ static PyObject *py_bind(PyObject *self, PyObject *const *args, Py_ssize_t n)
     f_ragged = (ragged_fn)PTR(1);
     f_int8 = (int8_fn)PTR(2);
     f_quant = (quant_fn)PTR(3);
+    if (!s_shape) {
+        s_shape = PyUnicode_InternFromString("shape");
+        s_dtype = PyUnicode_InternFromString("dtype");
+        s_dense = PyUnicode_InternFromString("is_contiguous");
+        s_ptr = PyUnicode_InternFromString("data_ptr");
+        s_bytes = PyUnicode_InternFromString("element_size");
+    }
     if (PyErr_Occurred())
         return NULL;
     Py_RETURN_NONE;
@@ -145,6 +315,9 @@ static PyObject *py_bind(PyObject *self, PyObject *const *args, Py_ssize_t n)
 static PyMethodDef methods[] = {
     ENTRY("bind", py_bind, "set the library's function addresses"),
     ENTRY("w8a8_sandwich_norm", py_norm, "see the C header"),
+    ENTRY("norm_tensors", py_norm_tensors, "sandwich_norm of dense tensors with every output given"),
+    ENTRY("int8_tensors", py_int8_tensors, "int8_matmul, as norm_tensors"),
+    ENTRY("quant_tensors", py_quant_tensors, "quantize_int8_per_token, as norm_tensors"),
     ENTRY("w8a8_block_fp8_grouped_matmul_ragged", py_ragged, "see the C header"),
     ENTRY("w8a8_int8_matmul", py_int8, "see the C header"),
     ENTRY("w8a8_quantize_int8_per_token", py_quant, "see the C header"),

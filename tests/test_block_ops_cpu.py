@@ -117,3 +117,35 @@ def test_python_wrappers_refuse_shapes_and_types():
     ):
         with pytest.raises(w8.W8A8Error):
             call()
+
+
+def test_sandwich_norm_refuses_the_same_with_its_outputs_given():
+    f, h = torch.zeros, lambda *s: torch.zeros(s, dtype=torch.float16)  # noqa: E731
+    good = dict(h=f(4, 8), x=f(4, 8), x_out=f(4, 8), y_out=f(4, 8))
+    e4, i8 = torch.zeros(4, 8, dtype=torch.float8_e4m3fn), torch.zeros(4, 8, dtype=torch.int8)
+    for bad in (dict(x=f(4, 9)), dict(h=f(5, 8)), dict(x_out=f(4, 9)), dict(y_out=f(3, 8)), dict(x_out=h(4, 8)),
+                dict(y_out=h(4, 8)), dict(w_post=f(9)), dict(w_post=h(8)), dict(w_pre=f(1, 8)), dict(w_pre=h(8)),
+                dict(w_pre=f(16)[::2]), dict(gate=f(1, 8), gate_rows=2), dict(gate=f(2, 9)), dict(gate=h(8)),
+                dict(gate=f(8), gate_rows=3), dict(gate=f(0, 8)), dict(gate=f(4, 8), gate_rows=0),
+                dict(out="fp8", y_out=f(4, 8)), dict(out="fp8", y_out=e4, scales_out=f(4)),
+                dict(out="int8", y_out=i8, scales_out=f(4, 1)), dict(h=f(8, 4).t()), dict(x=f(1, 8).expand(4, 8)),
+                dict(h=torch.zeros(4, 8, dtype=torch.int32))):
+        with pytest.raises(w8.W8A8Error) as e:
+            w8.sandwich_norm(**dict(good, **bad))
+        assert e.value.status in (ARG, UNS), (bad, e.value)
+
+
+def test_int8_calls_refuse_the_same_with_their_outputs_given():
+    e8, f = lambda *s: torch.zeros(s, dtype=torch.int8), torch.zeros  # noqa: E731
+    good = dict(A=e8(4, 16), a_s=f(4), B=e8(8, 16), b_s=f(8), out=f(4, 8))
+    for bad in (dict(A=f(4, 16)), dict(B=f(8, 16)), dict(A=e8(4, 17)), dict(B=e8(8, 15)), dict(a_s=f(5)), dict(b_s=f(7)),
+                dict(a_s=f(8)[::2]), dict(out=f(4, 9)), dict(A=e8(16, 4).t()), dict(a_s=f(4, 1))):
+        with pytest.raises(w8.W8A8Error) as e:
+            w8.int8_matmul(**dict(good, **bad), out_dtype="fp32")
+        assert e.value.status in (ARG, UNS), (bad, e.value)
+    good = dict(X=f(4, 16), A=e8(4, 16), a_s=f(4))
+    for bad in (dict(X=e8(4, 16)), dict(X=f(4, 17)), dict(A=e8(5, 16)), dict(a_s=f(4, 1)), dict(a_s=f(8)[::2]),
+                dict(X=f(16, 4).t())):
+        with pytest.raises(w8.W8A8Error) as e:
+            w8.quantize_int8_per_token(**dict(good, **bad))
+        assert e.value.status in (ARG, UNS), (bad, e.value)

@@ -210,3 +210,16 @@ def test_from_activations():
     s.synchronize()
     q, sc = quant_reference(X)
     assert_same(C, reference(torch.from_numpy(q).cuda(), torch.from_numpy(sc).cuda(), B, b_s, "fp16"))
+
+
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+def test_given_outputs_hold_what_new_ones_would(out):
+    X = torch.randn(9, 200, device="cuda", dtype=torch.float16)
+    B, b_s = make(1, 70, 200, seed=12)[2:]
+    A, a_s = w8.quantize_int8_per_token(X)
+    A2, s2 = torch.empty_like(A), torch.empty_like(a_s)
+    assert all(a is b for a, b in zip(w8.quantize_int8_per_token(X, A=A2, a_s=s2), (A2, s2)))
+    assert torch.equal(A, A2) and torch.equal(a_s, s2)
+    C = torch.empty(9, 70, dtype=OUT[out], device="cuda")
+    assert w8.int8_matmul(A, a_s, B, b_s, out, out=C) is C
+    assert_same(C, w8.int8_matmul(A, a_s, B, b_s, out))

@@ -209,3 +209,22 @@ def test_empty():
     for M, D in ((0, 64), (3, 0)):
         r, y = w8.sandwich_norm(torch.empty(M, D, device="cuda"), torch.empty(M, D, device="cuda"))
         assert r.shape == (M, D) and y.shape == (M, D)
+
+
+@pytest.mark.parametrize("out", ["same", "fp8", "int8"])
+@pytest.mark.parametrize("gate", [None, (1, None), (4, 3), "flat"])
+def test_given_outputs_hold_what_new_ones_would(out, gate):
+    M, D = 10, 304
+    g = torch.Generator(device="cuda").manual_seed(4)
+    rn = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    k = dict(h=rn(M, D), x=rn(M, D).float(), w_post=rn(D), w_pre=rn(D), out=out, res_scale=0.5, eps=EPS)
+    if gate == "flat":
+        k["gate"] = rn(D)
+    elif gate:
+        k.update(gate=rn(gate[0], D), gate_rows=gate[1])
+    want = w8.sandwich_norm(**k)
+    given = [torch.empty_like(t) for t in want]
+    got = w8.sandwich_norm(**k, x_out=given[0], y_out=given[1], scales_out=given[2] if len(given) > 2 else None)
+    assert len(got) == len(want) and all(a is b for a, b in zip(got, given))
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
