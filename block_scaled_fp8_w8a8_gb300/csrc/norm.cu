@@ -843,8 +843,9 @@ __device__ __forceinline__ void store_flat(uint8_t *row, int c0, int D, const fl
 template <int HK, int XK, int THREADS, int PER_SM>
 __global__ void __launch_bounds__(THREADS, PER_SM) k_sandwich_flat(const FlatParams fp)
 {
-    // post [16][kPitch], pre [16][kPitch]; the pitch keeps the columns of a
-    // coalesced load, 16 words of a row apart, in different banks
+    // post [16][kPitch], pre [16][kPitch], thread t's columns at t + 1 (at 0 zeros, for
+    // the elements before a row's first); the pitch keeps the columns of a coalesced
+    // load, 16 words of a row apart, in different banks
     extern __shared__ float weights[];
     constexpr int kPitch = THREADS + 2;
     __shared__ __align__(16) float part[2][2][THREADS < 128 ? 4 : THREADS / 32];
@@ -857,6 +858,8 @@ __global__ void __launch_bounds__(THREADS, PER_SM) k_sandwich_flat(const FlatPar
     const int first = walk.first, step = walk.step, last = walk.last;
     for (int i = tid; i < static_cast<int>(sizeof(part) / 4); i += static_cast<int>(blockDim.x))
         (&part[0][0][0])[i] = 0.f;
+    if (tid < 32)
+        weights[tid * kPitch] = 0.f;
     grid_launch_dependents();
     grid_dependency_wait();
     const bool has_post = p.w_post || p.gate;
@@ -884,7 +887,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) k_sandwich_flat(const FlatPar
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int c = tid + (h + i) * static_cast<int>(blockDim.x);
-            dst[(c & 15) * kPitch + (c >> 4)] = v[i];
+            dst[(c & 15) * kPitch + (c >> 4) + 1] = v[i];
         }
     };
     auto load_post = [&](long long g) {
@@ -915,7 +918,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) k_sandwich_flat(const FlatPar
         }
     __syncthreads();
 
-    const uint32_t w0 = smem_addr(weights) + 4u * tid;
+    const uint32_t w0 = smem_addr(weights) + 4u * (tid + 1);
     int odd = 0;
     for (int m = first; m < last; m += step, odd ^= 1) {
         const long long m0 = static_cast<long long>(m) * D;        // the row's first element
@@ -923,11 +926,19 @@ __global__ void __launch_bounds__(THREADS, PER_SM) k_sandwich_flat(const FlatPar
         const int c0 = 16 * tid - s;                   // column of v[0]
         const bool any = c0 < D, all = c0 >= 0 && c0 + 16 <= D;
         float v[16], x[16];
+        if (all) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const bool in = all || (any && c0 + j >= 0 && c0 + j < D);
-            v[j] = in ? hn[j] : 0.f;
-            x[j] = in ? xn[j] : 0.f;
+            for (int j = 0; j < 16; ++j) {
+                v[j] = hn[j];
+                x[j] = xn[j];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const bool in = c0 + j >= 0 && c0 + j < D;
+                v[j] = in ? hn[j] : 0.f;
+                x[j] = in ? xn[j] : 0.f;
+            }
         }
         if (m + step < last)
             fetch(m + step);
@@ -952,7 +963,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) k_sandwich_flat(const FlatPar
         for (int j = 0; j < 16; ++j) {
             float u = v[j];
             if (has_post)
-                u = u * inv * ((j < 8 && j < s && tid == 0) ? 0.f : weight(j, 0));
+                u = u * inv * weight(j, 0);
             v[j] = fmaf(p.res_scale, x[j], u);
             ss = fmaf(v[j], v[j], ss);
         }
@@ -962,7 +973,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) k_sandwich_flat(const FlatPar
             inv = rsqrtf(fmaf(cta_sum<THREADS>(ss, part[odd][1]), fp.inv_d, p.eps));
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-                v[j] = v[j] * inv * ((j < 8 && j < s && tid == 0) ? 0.f : weight(j, 1));
+                v[j] = v[j] * inv * weight(j, 1);
         }
         if (p.y_kind == W8A8_NORM_SAME) {
             if (any)
