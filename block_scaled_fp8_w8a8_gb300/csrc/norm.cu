@@ -764,18 +764,16 @@ __global__ void __launch_bounds__(THREADS, PER_SM) k_sandwich_ring(const RingPar
 
 // ------------------------------------------------------------------ rows of any width
 
-// Many rows of a width that leaves them off 16-byte boundaries (so not for FP8
-// codes).  All tensors are dense, so row m starts at
-// element m D of each; a thread takes 16 elements from an element index that is
-// a multiple of 8, which every tensor loads and stores in whole 16-byte words
-// (the words at a row's two ends hold elements of its neighbours: masked on the
-// way in, stored one by one on the way out).  Column 16 t + k of a norm's
+// Rows of a width that leaves them off 16-byte boundaries (so not for FP8 codes).
+// All tensors are dense, so row m starts at element m D of each; a thread takes 16
+// elements from an element index that is a multiple of 8, which every tensor loads
+// and stores in whole 16-byte words (the words at a row's two ends hold elements of
+// its neighbours: masked on the way in, stored one by one on the way out).  Column 16 t + k of a norm's
 // weights lies at [k][t] in shared memory, so that a row shifted by s of 8
 // elements reads them without bank conflicts.  The next row's words wait in
 // registers while this one's reductions run.
 // Bound by instruction issue and the two reductions per row: 8192 rows of 1537 in
-// fp16 32.7 us (3.1 TB/s), 16384 of 3943 in bf16 122 us (4.2 TB/s; k_sandwich_norm
-// takes 577).
+// fp16 26.4 us (3.8 TB/s), 16384 of 3943 in bf16 103 us (5.0 TB/s).
 struct FlatParams {
     NormParams n;
     float inv_d;
@@ -1174,6 +1172,8 @@ cudaError_t launch_flat_t(const NormParams &p, const DeviceView &dev, cudaStream
     static volatile int smem_set[kMaxDeviceFlags] = {};
     int id = 0;
     cudaError_t e = cudaGetDevice(&id);
+    if (e == cudaSuccess && (id < 0 || id >= kMaxDeviceFlags))
+        e = cudaErrorInvalidDevice;
     if (e == cudaSuccess && !smem_set[id]) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWeights);
         smem_set[id] = e == cudaSuccess;
@@ -1202,16 +1202,18 @@ cudaError_t launch_flat_t(const NormParams &p, const DeviceView &dev, cudaStream
 template <int HK, int XK>
 cudaError_t launch_norm(const NormParams &p, bool vec, const DeviceView &dev, cudaStream_t stream)
 {
-    // Rows off 16-byte boundaries: the flat kernel where the tensors are dense,
-    // its CTAs get rows enough, and single elements would make narrow accesses
-    // (16384 rows in bf16, flat against direct: of 3943 122 / 577 us, of 513 44 / 84,
-    // of 251 50 / 30; 4096 rows of 513 15.1 / 15.4, 2000 10.6 / 8.5; fp32: 4096 rows
-    // of 7001 98 / 131, of 3943 65 / 60).
+    // Rows off 16-byte boundaries: the flat kernel where the tensors are dense and
+    // single elements would make narrow accesses (flat against direct, bf16: one row
+    // of 1537 3.8 / 4.8 us, 1111 rows 6.6 / 10.4; 1111 of 513 5.3 / 4.9, 16384 26 / 86;
+    // 4096 of 3943 31 / 151, of 301 14.5 / 8.6; 304 of 15001 20 / 37; fp32: 2000 rows of
+    // 8001 60 / 71, 100 6.7 / 5.0; 4096 of 3943 65 / 60, of 2001 45 / 30).
     const int span = p.D + 7;
-    const bool wide = HK == W8A8_IN_FP32 ? p.D > 4096 : p.D >= 1000 || (p.D >= 512 && p.M >= 4096);
-    if (!vec && wide && span <= kRegRow && p.M >= 2 * dev.sm_count && p.ld_h == p.D &&
+    const bool wide = HK == W8A8_IN_FP32 ? p.D > 4096 && p.M >= 2 * dev.sm_count : p.D >= 512;
+    if (!vec && wide && span <= kRegRow && p.ld_h == p.D &&
         p.ld_x == p.D && p.ld_xo == p.D && p.ld_y == p.D && on(p.h, 16) && on(p.x, 16) &&
         on(p.x_out, 16) && on(p.y, p.y_kind == W8A8_NORM_SAME ? 16 : 8)) {
+        if (span <= 16 * 128)
+            return launch_flat_t<HK, XK, 128, 6>(p, dev, stream);
         if (span <= 16 * 256)
             return launch_flat_t<HK, XK, 256, 3>(p, dev, stream);
         if (span <= 16 * 512)
