@@ -768,9 +768,12 @@ int int8_variant(int64_t M, int64_t N, int64_t K, const w8a8_options *o, int sm_
         return W8A8_VARIANT_SMALLM;
     const int m = static_cast<int>(M), n = static_cast<int>(N), k = static_cast<int>(K);
     const float tiled = int8_tiled_cost(m, n, k, sm_count, 0), pair = int8_tiled_cost(m, n, k, sm_count, 1);
-    // (more than some thousand tokens never pay here: the plan is not searched)
-    const float mid = v == W8A8_VARIANT_SWAPAB || M <= 4096 ? int8_mid_plan(m, n, k, sm_count, tile, splits)
-                                                            : -1.f;
+    // (More than some thousand tokens pay only by few output channels, which widen
+    // little twice: 7897 x 128 x 3792 20.4 us, TILED 29.6; 5000 x 64 x 4096 16 / 24; but
+    // 8192 x 512 x 512 15.7 / 11.5, 6000 x 1024 x 4096 117 / 57.  Else the plan is not searched.)
+    const float mid = v == W8A8_VARIANT_SWAPAB || M <= 4096 || N <= 256
+                          ? int8_mid_plan(m, n, k, sm_count, tile, splits)
+                          : -1.f;
     if (v == W8A8_VARIANT_SWAPAB)
         return mid < 0.f ? W8A8_VARIANT_AUTO : v;       // AUTO: K is too long for it
     if (mid >= 0.f && mid <= std::min(tiled, pair))

@@ -52,7 +52,8 @@ VARIANTS = [w8.W8A8_VARIANT_SMALLM, w8.W8A8_VARIANT_SWAPAB, w8.W8A8_VARIANT_TILE
 
 
 @pytest.mark.parametrize("variant", VARIANTS)
-@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 48, 8192), (9, 40, 5000), (20, 100, 2048), (130, 70, 64), (40, 70, 65), (300, 520, 1100), (513, 768, 2048)])
+@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 48, 8192), (9, 40, 5000), (20, 100, 2048), (130, 70, 64), (40, 70, 65), (300, 520, 1100), (513, 768, 2048),
+                                   (5003, 100, 1040)])
 def test_forced_kernels(M, N, K, variant):
     x = make(M, N, K, seed=3)
     for grid in (0, 4):
