@@ -996,7 +996,7 @@ w8a8_status run_ragged(const void *A, const float *a_s, const void *B, const flo
     const int64_t most = std::min<int64_t>(gr.experts, M);
     const bool thin = (G >= 9 && M <= 24 * most) ||
                       (G >= 5 && M <= 16 * most && (most + M / 32) * cdiv(N, 128) >= 4 * info.sm_count);
-    const bool few = m_tile ? m_tile == 32 : asked > 1 || (!bn && thin);
+    const bool few = m_tile ? m_tile == 32 : bn != 256 && (asked > 1 || (!bn && thin));
     const int rows = few ? 32 : 128;
     // Row tiles that the routing can make at most; the host does not know it.
     const int64_t tiles = std::min<int64_t>(gr.experts, M) + M / rows;

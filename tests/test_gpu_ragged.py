@@ -217,3 +217,14 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right():
     torch.cuda.synchronize()
     assert w8.w8a8_get_device_status()[0] == w8.W8A8_OK
     assert_right(C, x, "bf16")
+
+
+def test_options_outside_the_kernels_are_refused():
+    x = make([5, 6], 256, 1024, seed=12)
+    many = make([1] * 200, 512, 1024, seed=13)
+    for args, opts in ((x, dict(m_tile=64)), (x, dict(m_tile=32, block_n_tile=256)), (x, dict(block_n_tile=192)),
+                       (x, dict(m_tile=128, split_k=2)), (x, dict(split_k=3)), (x, dict(split_k=16)),
+                       (many, dict(split_k=8)), (x, dict(block_n_tile=256, split_k=2))):
+        with pytest.raises(w8.W8A8Error) as e:
+            w8.grouped_matmul_ragged(*args, **opts)
+        assert e.value.status == w8.W8A8_ERR_UNSUPPORTED, (opts, e.value)
