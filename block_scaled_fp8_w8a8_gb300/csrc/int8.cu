@@ -150,9 +150,9 @@ __global__ void __launch_bounds__(kWidenThreads) k_int8_widen(const Int8WidenPar
 // The warps of a CTA, and the CTAs of a cluster, split K; whole sums meet in
 // shared memory, where the order of integer additions does not matter.
 // Bound by the latency of a launch and of the loads: two batches of loads a
-// thread, 32 KB a CTA, stay in flight.  One token by 4096 x 4096: 4.2 us (4.0
-// TB/s; with a single batch 5.4), by 8192 x 16384: 28.7 us (4.7 TB/s).
-// Batches of 4 steps give 4.6 and 26.4 us.
+// thread, 32 KB a CTA, stay in flight.  One token by 4096 x 4096: 4.05 us (4.1
+// TB/s; with a single batch 5.4), by 8192 x 16384: 28.6 us (4.7 TB/s).
+// Batches of 4 steps gave 4.6 and 26.4 us where these took 4.25 and 28.7.
 constexpr int kSmallWarps = 8, kSmallCtas = 2;       // CTAs per SM
 
 __device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -178,6 +178,7 @@ __global__ void __launch_bounds__(32 * kSmallWarps, kSmallCtas) k_int8_small(con
     // additions fall into different banks
     constexpr int kPitch = kRows + 4, kSums = kPitch * kTokens;
     __shared__ int sums2[2][kSums];
+    __shared__ float tok_s[kTokens], row_s[2][kRows];    // scales, fetched while the sums form
     const int lane = static_cast<int>(lane_index()), warp = static_cast<int>(warp_index());
     const int g = lane >> 2, t = lane & 3;
     for (int i = static_cast<int>(threadIdx.x); i < 2 * kSums; i += 32 * kSmallWarps)
@@ -186,7 +187,9 @@ __global__ void __launch_bounds__(32 * kSmallWarps, kSmallCtas) k_int8_small(con
     grid_launch_dependents();
     grid_dependency_wait();
 
-    const int m0 = static_cast<int>(blockIdx.z) * kTokens;
+    const int m0 = static_cast<int>(blockIdx.z) * kTokens, tid = static_cast<int>(threadIdx.x);
+    if (tid < kTokens)
+        cp_async_4(smem_addr(tok_s + tid), p.a_s + min(m0 + tid, p.M - 1), 4u);
     // This warp's steps: the cluster's CTAs and their warps take equal shares.
     const int steps = (p.K + 63) / 64, shares = static_cast<int>(gridDim.y) * kSmallWarps;
     const int share = static_cast<int>(blockIdx.y) * kSmallWarps + warp;
@@ -283,6 +286,8 @@ __global__ void __launch_bounds__(32 * kSmallWarps, kSmallCtas) k_int8_small(con
     for (;; turn ^= 1) {
         int *sums = sums2[turn];
         const bool next = step_n < p.N - n0;         // this CTA has another tile
+        if (tid < kRows)
+            cp_async_4(smem_addr(row_s[turn] + tid), p.b_s + min(n0 + tid, p.N - 1), 4u);
         clear();
         since = 0;
         for (int s = first;; s += 2 * UN) {
@@ -299,6 +304,7 @@ __global__ void __launch_bounds__(32 * kSmallWarps, kSmallCtas) k_int8_small(con
                 break;
         }
         flush(sums);
+        cp_async_wait_all();
         // The CTAs of a cluster hold partial sums of the same tile: each finishes
         // its share of it, reading the others' through distributed shared memory.
         if (S > 1)
@@ -327,7 +333,7 @@ __global__ void __launch_bounds__(32 * kSmallWarps, kSmallCtas) k_int8_small(con
             }
             if (m >= p.M || n >= p.N)
                 continue;
-            const float v = __int2float_rn(sum) * __ldg(p.a_s + m) * __ldg(p.b_s + n);
+            const float v = __int2float_rn(sum) * tok_s[i / kRows] * row_s[turn][i % kRows];
             if (!in_bounds(m >= 0 && n >= 0, p.status, SITE_BOUNDS_C))
                 continue;
             const long long at = m * p.ldc + n;

@@ -699,6 +699,12 @@ __device__ __forceinline__ uint64_t mul2_rn(uint64_t a, uint64_t b)
 
 // ------------------------------------------------------------------ cp.async (4-byte gathers)
 
+// This thread's copies have landed.
+__device__ __forceinline__ void cp_async_wait_all()
+{
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // Copy 4 bytes global -> shared; src_bytes = 0 writes zeros and reads nothing.
 __device__ __forceinline__ void cp_async_4(uint32_t dst, const void *src, uint32_t src_bytes)
 {
