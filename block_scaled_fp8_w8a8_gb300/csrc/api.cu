@@ -169,6 +169,56 @@ struct Workspace {
 };
 std::map<std::pair<int, cudaStream_t>, Workspace> g_workspaces;
 
+// A call with a workspace may be several launches that hand it on, and a larger
+// call frees the one it outgrows; so a host thread holds the workspace from taking
+// it to its last launch, and the launches of calls from several threads on one
+// stream do not interleave.  The locks are a fixed table hashed by the workspace's
+// owner (the stream of the library's, the address of a caller's), so that none
+// is ever destroyed while another thread waits for it.
+constexpr int kWorkspaceLocks = 61;
+std::mutex g_workspace_locks[kWorkspaceLocks];
+thread_local bool g_holds_workspace = false;
+
+class WorkspaceHold {
+public:
+    WorkspaceHold() = default;
+    WorkspaceHold(const WorkspaceHold &) = delete;
+    WorkspaceHold &operator=(const WorkspaceHold &) = delete;
+    ~WorkspaceHold()
+    {
+        if (lock_.owns_lock())
+            g_holds_workspace = false;
+    }
+    // (A call made of others holds its workspace for all of them.)
+    void take(const void *owner)
+    {
+        if (g_holds_workspace)
+            return;
+        lock_ = std::unique_lock<std::mutex>(
+            g_workspace_locks[(reinterpret_cast<uintptr_t>(owner) >> 4) % kWorkspaceLocks]);
+        g_holds_workspace = true;
+    }
+
+private:
+    std::unique_lock<std::mutex> lock_;
+};
+
+// Every workspace at rest: no thread is between taking one and its last launch.
+// (Before g_mutex, which a call takes while it holds its workspace.)
+class AllWorkspacesHold {
+public:
+    AllWorkspacesHold()
+    {
+        for (std::mutex &m : g_workspace_locks)
+            m.lock();
+    }
+    ~AllWorkspacesHold()
+    {
+        for (std::mutex &m : g_workspace_locks)
+            m.unlock();
+    }
+};
+
 w8a8_status current_device(int *dev_out, DeviceInfo *info_out)
 {
     int dev = -1;
@@ -636,12 +686,13 @@ w8a8_status library_workspace(int dev, cudaStream_t stream, size_t bytes, void *
     return W8A8_OK;
 }
 
-// The split-K / stream-K workspace of a call: the caller's (checked), else the
-// library's own for this device and stream.
+// The workspace of a call: the caller's (checked), else the library's own for this
+// device and stream.  `hold` lives to the call's last launch.
 w8a8_status acquire_workspace(const w8a8_options *o, int dev, cudaStream_t stream, size_t bytes,
-                              void **out)
+                              void **out, WorkspaceHold &hold)
 {
     void *ws = o ? o->workspace_dev : nullptr;
+    hold.take(ws ? ws : static_cast<const void *>(stream));
     if (ws) {
         if (o->workspace_bytes < bytes || !aligned(ws, 256))
             return fail(W8A8_ERR_WORKSPACE,
@@ -906,7 +957,8 @@ w8a8_status run_int8(const void *A, int64_t lda, const float *a_s, const void *B
     }
     const Int8Plan pl = int8_plan(M, N, K);
     void *ws = nullptr;
-    if ((st = acquire_workspace(o, dev, stream, pl.workspace(), &ws)) != W8A8_OK)
+    WorkspaceHold hold;
+    if ((st = acquire_workspace(o, dev, stream, pl.workspace(), &ws, hold)) != W8A8_OK)
         return st;
     uint8_t *A16 = static_cast<uint8_t *>(ws) + kCounterBytes, *B16 = A16 + pl.a_bytes;
     for (int64_t r0 = 0; r0 < M; r0 += pl.chunk) {
@@ -1245,6 +1297,7 @@ w8a8_status run(const void *A, const float *a_s, const void *B, const float *b_s
     cfg.stream = stream;
 
     cudaError_t e;
+    WorkspaceHold hold;
     if (pl.variant == W8A8_VARIANT_SMALLM) {
         CUtensorMap mB;
         if ((st = encode_u8_map(&mB, B, N, K, 32, 0, sd.ldb)) != W8A8_OK)
@@ -1301,8 +1354,8 @@ w8a8_status run(const void *A, const float *a_s, const void *B, const float *b_s
         }
         if (!pair && pl.splits == 2) {
             void *ws = nullptr;
-            if ((st = acquire_workspace(o, dev, stream, splitk_workspace_bytes(M, N, pl), &ws)) !=
-                W8A8_OK)
+            if ((st = acquire_workspace(o, dev, stream, splitk_workspace_bytes(M, N, pl), &ws,
+                                        hold)) != W8A8_OK)
                 return st;
             p.sk_len = pl.sk_len;
             p.sk_first_tile = pl.sk_first_tile;
@@ -1336,7 +1389,7 @@ w8a8_status run(const void *A, const float *a_s, const void *B, const float *b_s
                 return fail(W8A8_ERR_UNSUPPORTED, "split-K over %lld output tiles (max %zu)",
                             static_cast<long long>(pl.m_tiles) * NB, kCounterWords);
             void *ws = nullptr;
-            if ((st = acquire_workspace(o, dev, stream, ws_bytes, &ws)) != W8A8_OK)
+            if ((st = acquire_workspace(o, dev, stream, ws_bytes, &ws, hold)) != W8A8_OK)
                 return st;
             p.counters = static_cast<unsigned *>(ws);
             p.ws = reinterpret_cast<float *>(static_cast<char *>(ws) + kCounterBytes);
@@ -1572,7 +1625,8 @@ w8a8_status w8a8_block_fp8_quant_matmul(const void *X_dev, w8a8_in_dtype x_dtype
                         static_cast<long long>(M), static_cast<long long>(N),
                         static_cast<long long>(K));
         void *ws = nullptr;
-        if ((st = acquire_workspace(opts, dev, s, total, &ws)) != W8A8_OK)
+        WorkspaceHold hold;
+        if ((st = acquire_workspace(opts, dev, s, total, &ws, hold)) != W8A8_OK)
             return st;
         auto up = [](size_t x) { return (x + 255) / 256 * 256; };
         char *codes = static_cast<char *>(ws) + mm_bytes;
@@ -1954,6 +2008,7 @@ w8a8_status w8a8_get_device_status(unsigned *detail_out)
             return cuda_fail(e, "clearing the status word");
         // A kernel that gave up may have left split-K arrival counters raised:
         // drop the cached workspaces of this device so they start from zero.
+        AllWorkspacesHold rest;
         std::lock_guard<std::mutex> lock(g_mutex);
         for (auto it = g_workspaces.begin(); it != g_workspaces.end();) {
             if (it->first.first == dev) {
@@ -2013,6 +2068,7 @@ w8a8_status w8a8_env_config(int *force_variant, int *deterministic,
 void w8a8_shutdown(void)
 {
     w8a8::noalloc_forget();
+    AllWorkspacesHold rest;
     std::lock_guard<std::mutex> lock(g_mutex);
     int cur = -1;
     cudaGetDevice(&cur);

@@ -44,9 +44,10 @@
  *    w8a8_last_error().  A device-side wait that gives up (a bounded wait that
  *    ran out) is recorded in a per-device status word read by
  *    w8a8_get_device_status(); kernels never trap.
- *  - Thread safety: calls may be made from several host threads.  Concurrent
- *    calls that use the split-K variant on different streams must each pass
- *    their own workspace (see w8a8_options).
+ *  - Thread safety: calls may be made from several host threads, on one stream
+ *    or on several; the launches of one call are not interleaved with those of
+ *    another call on the same workspace.  A caller's workspace (see
+ *    w8a8_options) serves the calls of one stream at a time.
  */
 #ifndef W8A8_BLOCK_FP8_H
 #define W8A8_BLOCK_FP8_H

@@ -70,6 +70,55 @@ def test_threads_on_their_own_streams():
     assert w8.w8a8_get_device_status()[0] == w8.W8A8_OK
 
 
+@pytest.mark.parametrize("grown", [True, False])
+def test_threads_on_one_stream(grown):
+    """Four host threads whose calls share a stream and so the library's workspace, which
+    each of the calls fills by one launch and reads by the next; with the workspace as
+    large as the largest call needs it before the first, and growing between them."""
+    M, N, K = (600, 300, 130, 900), (520, 300, 900, 264), (600, 1040, 300, 2000)
+    stream, errors, start = torch.cuda.Stream(), [], threading.Barrier(4)
+    x = []
+    for i in range(4):
+        g = torch.Generator(device="cuda").manual_seed(i)
+        A, B = (torch.randint(-128, 128, (n, K[i]), generator=g, device="cuda", dtype=torch.int8) for n in (M[i], N[i]))
+        a, b = (torch.rand(n, generator=g, device="cuda") for n in (M[i], N[i]))
+        X = torch.randn(M[i], 512, generator=g, device="cuda")
+        W = (torch.randn(512, 512, generator=g, device="cuda") * 90).clamp_(-448, 448).to(torch.float8_e4m3fn)
+        W_s = torch.rand(4, 4, generator=g, device="cuda")
+        x.append((A, a, B, b, X, W, W_s, (A.double() @ B.double().t()).float() * a[:, None] * b,
+                  w8.matmul(*w8.quantize_fp8_per_token_group(X), W, W_s, "fp32")))
+    torch.cuda.synchronize()
+    if grown:
+        big = torch.ones(3000, 3000, device="cuda", dtype=torch.int8)
+        w8.int8_matmul(big, torch.ones(3000, device="cuda"), big, torch.ones(3000, device="cuda"), stream=stream,
+                       variant=w8.W8A8_VARIANT_TILED)
+
+    def work(i):
+        try:
+            A, a, B, b, X, W, W_s, want, want8 = x[i]
+            got = []
+            start.wait()
+            with torch.cuda.stream(stream):
+                for r in range(30):
+                    v = (w8.W8A8_VARIANT_TILED, w8.W8A8_VARIANT_TILED_PAIR)[r % 2]
+                    got.append((w8.int8_matmul(A, a, B, b, "fp32", variant=v), want))
+                    if r % 3 == 0:      # quantiser and product, the codes in the workspace
+                        got.append((w8.quant_matmul(X, W, W_s, "fp32"), want8))
+            stream.synchronize()
+            for C, ref in got:
+                assert torch.equal(C, ref)
+        except Exception as e:      # noqa: BLE001
+            errors.append((i, repr(e)))
+
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join(timeout=300)
+    assert not any(t.is_alive() for t in ts) and not errors, errors
+    assert w8.w8a8_get_device_status()[0] == w8.W8A8_OK
+
+
 def run_all(seed=1):
     """Every kernel of the three operators once or more, on sizes with ragged ends."""
     g = torch.Generator(device="cuda").manual_seed(seed)
