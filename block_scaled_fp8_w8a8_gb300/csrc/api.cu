@@ -20,6 +20,7 @@
 #include <map>
 #include <mutex>
 #include <utility>
+#include <vector>
 
 #include "../../include/w8a8_block_fp8.h"
 #include "dispatch_table.h"
@@ -161,13 +162,17 @@ std::mutex g_mutex;
 DeviceInfo g_devices[kMaxDevices];
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
-// Per-(device, stream) split-K workspace owned by the library, allocated and
-// grown stream-ordered (cudaMallocAsync / cudaFreeAsync on that stream).
+// Per-(device, stream) workspace owned by the library, allocated and grown
+// stream-ordered (cudaMallocAsync / cudaFreeAsync on that stream).  A stream
+// capture that took it left its address in a graph, which may be replayed at any
+// time later: from then on it is not freed before w8a8_shutdown, outgrown or not.
 struct Workspace {
     void *ptr = nullptr;
     size_t bytes = 0;
+    bool captured = false;
 };
 std::map<std::pair<int, cudaStream_t>, Workspace> g_workspaces;
+std::vector<std::pair<int, void *>> g_outgrown;    // captured ones, by device
 
 // A call with a workspace may be several launches that hand it on, and a larger
 // call frees the one it outgrows; so a host thread holds the workspace from taking
@@ -650,26 +655,29 @@ w8a8_status library_workspace(int dev, cudaStream_t stream, size_t bytes, void *
                                    "by debug_fail_alloc)");
     std::lock_guard<std::mutex> lock(g_mutex);
     Workspace &w = g_workspaces[std::make_pair(dev, stream)];
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    cudaError_t e = w.captured && w.bytes >= bytes ? cudaSuccess : cudaStreamIsCapturing(stream, &cap);
+    if (e != cudaSuccess)
+        return cuda_fail(e, "cudaStreamIsCapturing");
     if (w.bytes >= bytes) {
+        w.captured = w.captured || cap != cudaStreamCaptureStatusNone;
         *out = w.ptr;
         return W8A8_OK;
     }
-    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    cudaError_t e = cudaStreamIsCapturing(stream, &cap);
-    if (e != cudaSuccess)
-        return cuda_fail(e, "cudaStreamIsCapturing");
     if (cap != cudaStreamCaptureStatusNone)
         return fail(W8A8_ERR_WORKSPACE,
                     "split-K workspace would have to grow during stream capture; "
                     "pass w8a8_options.workspace_dev or call once before capturing");
     // Stream-ordered: the old workspace is released after the work already
-    // queued on this stream (the only work that uses it), the new one is
-    // allocated and zeroed in order on the stream; nothing synchronises the
-    // device or the host.
+    // queued on this stream (the only work that uses it, if no capture took it),
+    // the new one is allocated and zeroed in order on the stream; nothing
+    // synchronises the device or the host.
     if (w.ptr) {
-        e = cudaFreeAsync(w.ptr, stream);
-        w.ptr = nullptr;
-        w.bytes = 0;
+        if (w.captured)
+            g_outgrown.push_back({dev, w.ptr});
+        else
+            e = cudaFreeAsync(w.ptr, stream);
+        w = Workspace{};
         if (e != cudaSuccess)
             return cuda_fail(e, "cudaFreeAsync(workspace)");
     }
@@ -2007,17 +2015,27 @@ w8a8_status w8a8_get_device_status(unsigned *detail_out)
         if (e != cudaSuccess)
             return cuda_fail(e, "clearing the status word");
         // A kernel that gave up may have left split-K arrival counters raised:
-        // drop the cached workspaces of this device so they start from zero.
+        // drop the cached workspaces of this device so they start from zero, and
+        // zero the counters of those that a graph's launches hold.
         AllWorkspacesHold rest;
         std::lock_guard<std::mutex> lock(g_mutex);
         for (auto it = g_workspaces.begin(); it != g_workspaces.end();) {
-            if (it->first.first == dev) {
+            if (it->first.first != dev) {
+                ++it;
+            } else if (it->second.captured) {
+                cudaMemset(it->second.ptr, 0, kCounterBytes);
+                ++it;
+            } else {
                 cudaFree(it->second.ptr);
                 it = g_workspaces.erase(it);
-            } else {
-                ++it;
             }
         }
+        for (const auto &old : g_outgrown)
+            if (old.first == dev)
+                cudaMemset(old.second, 0, kCounterBytes);
+        e = cudaDeviceSynchronize();
+        if (e != cudaSuccess)
+            return cuda_fail(e, "clearing the workspaces' counters");
     }
     if (detail_out)
         *detail_out = word;
@@ -2088,6 +2106,11 @@ void w8a8_shutdown(void)
         cudaFree(kv.second.ptr);
     }
     g_workspaces.clear();
+    for (const auto &old : g_outgrown) {
+        cudaSetDevice(old.first);
+        cudaFree(old.second);
+    }
+    g_outgrown.clear();
     if (cur >= 0)
         cudaSetDevice(cur);
 }

@@ -167,7 +167,8 @@ typedef enum {
  *                      (cudaMallocAsync, cudaFreeAsync of the smaller one after
  *                      the work already queued there); not during stream
  *                      capture (W8A8_ERR_WORKSPACE: call once before capturing,
- *                      or pass a workspace).
+ *                      or pass a workspace).  One that a capture took is kept
+ *                      until w8a8_shutdown, for the graph's replays.
  *   wait_limit_cycles  bound of every device-side wait in SM clock cycles
  *                      (0 = the default: W8A8_WAIT_LIMIT_CYCLES from the
  *                      environment, else 2^32 cycles, about 2 s); at least

@@ -149,6 +149,55 @@ def test_callers_workspace_and_capture():
     assert e.value.status == w8.W8A8_ERR_WORKSPACE
 
 
+def test_a_captured_call_keeps_its_workspace():
+    """A graph that holds the library's workspace, replayed after a call on the same
+    stream needed a larger one, and after a timeout made the library drop its
+    workspaces.  (A split-K product of the FP8 matmul, whose counters lie there too,
+    is captured with it.)"""
+    s = torch.cuda.Stream()
+    x, y = make(100, 300, 700, seed=21), make(1500, 1400, 2000, seed=22)
+    A, a_s = w8.quantize_fp8_per_token_group(torch.randn(40, 2048, device="cuda"))
+    B, b_s = torch.randn(512, 2048, device="cuda").to(torch.float8_e4m3fn), torch.rand(4, 16, device="cuda")
+    C, D = torch.zeros(100, 300, device="cuda"), torch.zeros(40, 512, device="cuda")
+    torch.cuda.synchronize()
+
+    def step():
+        w8.int8_matmul(*x, "fp32", out=C, stream=s, variant=w8.W8A8_VARIANT_TILED)
+        w8.matmul(A, a_s, B, b_s, "fp32", out=D, stream=s, variant=w8.W8A8_VARIANT_SPLITK, split_k=4)
+
+    step()
+    s.synchronize()
+    want = D.clone()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        step()
+
+    def replay_is_right(seed):
+        x[0].copy_(make(100, 300, 700, seed=seed)[0])
+        C.zero_(), D.zero_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert w8.w8a8_get_device_status()[0] == w8.W8A8_OK
+        assert_same(C, reference(*x, "fp32"))
+        assert torch.equal(D, want)
+
+    def large():
+        return w8.int8_matmul(*y, "fp32", stream=s, variant=w8.W8A8_VARIANT_TILED)
+
+    E = large()
+    replay_is_right(23)
+    assert_same(E, reference(*y, "fp32"))
+    w8.int8_matmul(*y, stream=s, variant=w8.W8A8_VARIANT_TILED, debug_skip_load=2, wait_limit_cycles=2_000_000)
+    assert w8.w8a8_get_device_status()[0] == w8.W8A8_ERR_DEVICE_TIMEOUT
+    replay_is_right(24)
+    E = large()
+    s.synchronize()
+    assert_same(E, reference(*y, "fp32"))
+    replay_is_right(25)
+
+
 def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right():
     x = make(300, 520, 1100, seed=6)
     for variant in (w8.W8A8_VARIANT_SWAPAB, w8.W8A8_VARIANT_TILED, w8.W8A8_VARIANT_TILED_PAIR):
