@@ -189,6 +189,33 @@ def _dense(t, name):
         raise W8A8Error(W8A8_ERR_UNSUPPORTED, f"{name} must be contiguous")
 
 
+class _Dtypes:
+    """torch's dtypes that the wrappers below compare with (torch is imported late)."""
+
+    def __init__(self):
+        import torch
+        self.f32, self.i32 = torch.float32, torch.int32
+        self.e4m3 = (torch.float8_e4m3fn, torch.uint8)
+        self.out = {W8A8_OUT_BF16: torch.bfloat16, W8A8_OUT_FP16: torch.float16,
+                    W8A8_OUT_FP32: torch.float32}
+
+
+_dtypes = None
+
+
+def _load_dtypes():
+    global _dtypes
+    _dtypes = _Dtypes()
+    return _dtypes
+
+
+def _typed(t, wanted, name):
+    """Refuse a tensor whose elements the kernels would take for another type."""
+    if t.dtype not in wanted:
+        raise W8A8Error(W8A8_ERR_INVALID_ARG,
+                        f"{name} must be {' or '.join(str(w) for w in wanted)}, not {t.dtype}")
+
+
 def _rows(t):
     """Row stride of a 2-D tensor whose rows are contiguous, 0 for a dense one."""
     if t.is_contiguous():
@@ -222,10 +249,11 @@ _in_codes = _Codes()
 
 def grouped_matmul_ragged(A, a_s, B, b_s, offsets, out_dtype="bf16", out=None, stream=None,
                           **opts):
-    """Grouped matmul, ragged layout, on CUDA tensors: A [M, K], a_s [M, ceil(K/128)],
-    B [E, N, K], b_s [E, ceil(N/128), ceil(K/128)], offsets int32 [E + 1] (expert e's
-    rows are offsets[e] .. offsets[e+1]-1; read on the device).  Returns C [M, N];
-    rows of no expert are left as they are in ``out`` (unspecified without it)."""
+    """Grouped matmul, ragged layout, on CUDA tensors: A [M, K] and B [E, N, K] uint8 or
+    float8_e4m3fn, a_s [M, ceil(K/128)] and b_s [E, ceil(N/128), ceil(K/128)] float32,
+    offsets int32 [E + 1] (expert e's rows are offsets[e] .. offsets[e+1]-1; read on
+    the device).  Returns C [M, N]; rows of no expert are left as they are in ``out``
+    (of out_dtype; unspecified without it)."""
     M, K = A.shape
     E, N, Kb = B.shape
     code = out_code(out_dtype)
@@ -243,6 +271,16 @@ def grouped_matmul_ragged(A, a_s, B, b_s, offsets, out_dtype="bf16", out=None, s
     if not (A.is_contiguous() and a_s.is_contiguous() and B.is_contiguous() and
             b_s.is_contiguous() and out.is_contiguous() and offsets.is_contiguous()):
         raise W8A8Error(W8A8_ERR_UNSUPPORTED, "tensors must be contiguous row-major")
+    types = _dtypes or _load_dtypes()
+    if (offsets.dtype is not types.i32 or a_s.dtype is not types.f32 or
+            b_s.dtype is not types.f32 or A.dtype not in types.e4m3 or
+            B.dtype not in types.e4m3 or out.dtype is not types.out[code]):
+        _typed(offsets, (types.i32,), "offsets")
+        _typed(a_s, (types.f32,), "a_s")
+        _typed(b_s, (types.f32,), "b_s")
+        _typed(A, types.e4m3, "A")
+        _typed(B, types.e4m3, "B")
+        _typed(out, (types.out[code],), "out")
     o = options(**opts) if opts else None
     st = load_library().w8a8_block_fp8_grouped_matmul_ragged(
         A.data_ptr(), a_s.data_ptr(), B.data_ptr(), b_s.data_ptr(), out.data_ptr(),

@@ -1,10 +1,12 @@
 """Refusals of the ragged, INT8 and norm entry points: every one comes before any
 CUDA call, so they are checked without a GPU, by status and message."""
+import ctypes
+
 import pytest
 import torch
 
 import block_scaled_fp8_w8a8_gb300 as w8
-from block_scaled_fp8_w8a8_gb300 import build
+from block_scaled_fp8_w8a8_gb300 import _binding, build
 
 OK, ARG, UNS = w8.W8A8_OK, w8.W8A8_ERR_INVALID_ARG, w8.W8A8_ERR_UNSUPPORTED
 
@@ -149,3 +151,54 @@ def test_int8_calls_refuse_the_same_with_their_outputs_given():
         with pytest.raises(w8.W8A8Error) as e:
             w8.quantize_int8_per_token(**dict(good, **bad))
         assert e.value.status in (ARG, UNS), (bad, e.value)
+
+
+@pytest.fixture(params=["python", "extension"])
+def reached(request, monkeypatch):
+    """The calls that reach the library's functions, which are stood in for; with the
+    wrappers' checks in Python alone, and with those of the extension module before them."""
+    hits, real = [], w8.load_library()
+
+    def enter(*args):
+        hits.append(args)
+        return 0
+
+    if request.param == "python":
+        lib = type("Library", (), dict.fromkeys(("norm_tensors", "int8_tensors", "quant_tensors")))()
+        for name in _binding._PYCALL:
+            setattr(lib, name, enter)
+        monkeypatch.setattr(w8, "load_library", lambda: lib)
+        yield hits
+        return
+    if real.norm_tensors is None:
+        pytest.skip("no extension module")
+    entry = ctypes.CFUNCTYPE(ctypes.c_int)(enter)
+    real.norm_tensors.__self__.bind(*[ctypes.cast(entry, ctypes.c_void_p).value] * 4)
+    yield hits
+    _binding._bind_pycall(ctypes.CDLL(w8.library_path()))
+
+
+def refused(call, good, bad, reached):
+    """The call with `bad` in the place of good arguments is refused for what it names
+    (the first of `bad`, or the text that follows it) and does not reach the library."""
+    kw, says = bad if isinstance(bad, tuple) else (bad, next(iter(bad)) + " must be")
+    with pytest.raises(w8.W8A8Error, match=says) as e:
+        call(**dict(good, **kw))
+    assert e.value.status in (ARG, UNS), (bad, e.value)
+    assert not reached, bad
+
+
+def z(*s, dtype=torch.float32):
+    return torch.zeros(s, dtype=dtype)
+
+
+def test_ragged_refuses_elements_of_another_type(reached):
+    u8, i32 = torch.uint8, torch.int32
+    good = dict(A=z(4, 128, dtype=u8), a_s=z(4, 1), B=z(2, 8, 128, dtype=torch.float8_e4m3fn), b_s=z(2, 1, 1),
+                offsets=z(3, dtype=i32), out_dtype="bf16", out=z(4, 8, dtype=torch.bfloat16), stream=0)
+    for bad in (dict(offsets=z(3, dtype=torch.int64)), dict(offsets=z(3)), dict(a_s=z(4, 1, dtype=torch.bfloat16)),
+                dict(b_s=z(2, 1, 1, dtype=torch.float64)), dict(A=z(4, 128, dtype=torch.bfloat16)),
+                dict(A=z(4, 128, dtype=torch.int8)), dict(B=z(2, 8, 128, dtype=torch.float16)),
+                dict(B=z(2, 8, 128, dtype=torch.float8_e5m2)), dict(out=z(4, 8)), dict(out=z(4, 8, dtype=torch.float16)),
+                dict(out=good["out"], out_dtype="fp32"), dict(out=good["out"], out_dtype=torch.float16)):
+        refused(w8.grouped_matmul_ragged, good, bad, reached)
