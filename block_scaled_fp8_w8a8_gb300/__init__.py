@@ -194,10 +194,11 @@ class _Dtypes:
 
     def __init__(self):
         import torch
-        self.f32, self.i32 = torch.float32, torch.int32
+        self.f32, self.i32, self.i8 = torch.float32, torch.int32, torch.int8
         self.e4m3 = (torch.float8_e4m3fn, torch.uint8)
         self.out = {W8A8_OUT_BF16: torch.bfloat16, W8A8_OUT_FP16: torch.float16,
                     W8A8_OUT_FP32: torch.float32}
+        self.fast = (self.i8, self.f32, *(self.out[c] for c in sorted(self.out)))   # see pycall.c
 
 
 _dtypes = None
@@ -293,30 +294,33 @@ def grouped_matmul_ragged(A, a_s, B, b_s, offsets, out_dtype="bf16", out=None, s
 def int8_matmul(A, a_s, B, b_s, out_dtype="bf16", out=None, stream=None, **opts):
     """C[m,n] = a_s[m] b_s[n] sum_k A[m,k] B[n,k] on CUDA tensors: A int8 [M, K], a_s
     float32 [M], B int8 [N, K], b_s float32 [N]; the sum is exact.  A, B and ``out``
-    need unit stride along their last dimension only.  Keyword options map to
-    w8a8_options fields.  Raises W8A8Error on a non-zero status."""
-    import torch
-    code, lib = out_code(out_dtype), load_library()
+    (of out_dtype) need unit stride along their last dimension only.  Keyword options
+    map to w8a8_options fields.  Raises W8A8Error on a non-zero status."""
+    code, lib, types = out_code(out_dtype), load_library(), _dtypes or _load_dtypes()
     if out is not None and not opts and lib.int8_tensors is not None:
-        st = lib.int8_tensors(A, a_s, B, b_s, out, code, torch.int8, _stream(stream))
+        st = lib.int8_tensors(A, a_s, B, b_s, out, code, types.fast, _stream(stream))
         if st == 0:
             return out
         if st is not None:
             check(st)
     M, K = A.shape
     N = B.shape[0]
-    if A.dtype is not torch.int8 or B.dtype is not torch.int8:
-        raise W8A8Error(W8A8_ERR_INVALID_ARG, f"A and B must be int8, not {A.dtype}, {B.dtype}")
+    _typed(A, (types.i8,), "A")
+    _typed(B, (types.i8,), "B")
     if B.shape != (N, K) or a_s.shape != (M,) or b_s.shape != (N,):
         _want(B, (N, K), "B")
         _want(a_s, (M,), "a_s")
         _want(b_s, (N,), "b_s")
     if out is None:
         out = _out_tensor((M, N), code, A.device)
-    elif out.shape != (M, N):
+    elif out.shape != (M, N) or out.dtype is not types.out[code]:
         _want(out, (M, N), "out")
+        _typed(out, (types.out[code],), "out")
     if not (a_s.is_contiguous() and b_s.is_contiguous()):
         raise W8A8Error(W8A8_ERR_UNSUPPORTED, "scales must be contiguous")
+    if a_s.dtype is not types.f32 or b_s.dtype is not types.f32:
+        _typed(a_s, (types.f32,), "a_s")
+        _typed(b_s, (types.f32,), "b_s")
     o = options(**opts) if opts else None
     st = lib.w8a8_int8_matmul(
         A.data_ptr(), _rows(A), a_s.data_ptr(), B.data_ptr(), _rows(B), b_s.data_ptr(),

@@ -239,7 +239,15 @@ other:
     Py_RETURN_NONE;
 }
 
-/* A, a_s, B, b_s, out, output code, torch.int8, stream */
+/* torch's dtypes as the wrappers hand them over: int8, float32, then the output types in
+ * the order of their codes. */
+enum { T_INT8, T_F32, T_OUT };
+static PyObject *type_at(PyObject *types, int i)
+{
+    return PyTuple_Check(types) && i >= 0 && i < PyTuple_GET_SIZE(types) ? PyTuple_GET_ITEM(types, i) : NULL;
+}
+
+/* A, a_s, B, b_s, out, output code, dtypes, stream */
 static PyObject *py_int8_tensors(PyObject *self, PyObject *const *args, Py_ssize_t n)
 {
     (void)self;
@@ -247,11 +255,13 @@ static PyObject *py_int8_tensors(PyObject *self, PyObject *const *args, Py_ssize
         return NULL;
     tensor_t a, as, b, bs, c;
     int st;
+    const int out = I32(5);
+    PyObject *const i8 = type_at(args[6], T_INT8), *const f32 = type_at(args[6], T_F32);
     if (dense(args[0], &a) && dense(args[1], &as) && dense(args[2], &b) && dense(args[3], &bs) &&
-        dense(args[4], &c) && a.dtype == args[6] && b.dtype == args[6] && a.dims == 2 && b.dims == 2 &&
+        dense(args[4], &c) && a.dtype == i8 && b.dtype == i8 && as.dtype == f32 && bs.dtype == f32 &&
+        out >= 0 && c.dtype == type_at(args[6], T_OUT + out) && a.dims == 2 && b.dims == 2 &&
         a.size[1] == b.size[1] && is(&as, 1, a.size[0], 0) && is(&bs, 1, b.size[0], 0) &&
         is(&c, 2, a.size[0], b.size[0])) {
-        const int out = I32(5);
         void *s = PTR(7);
         if (!PyErr_Occurred()) {
             Py_BEGIN_ALLOW_THREADS

@@ -202,3 +202,14 @@ def test_ragged_refuses_elements_of_another_type(reached):
                 dict(B=z(2, 8, 128, dtype=torch.float8_e5m2)), dict(out=z(4, 8)), dict(out=z(4, 8, dtype=torch.float16)),
                 dict(out=good["out"], out_dtype="fp32"), dict(out=good["out"], out_dtype=torch.float16)):
         refused(w8.grouped_matmul_ragged, good, bad, reached)
+
+
+def test_int8_matmul_refuses_elements_of_another_type(reached):
+    i8, bf16 = torch.int8, torch.bfloat16
+    good = dict(A=z(4, 16, dtype=i8), a_s=z(4), B=z(8, 16, dtype=i8), b_s=z(8), out_dtype="fp32", out=z(4, 8), stream=0)
+    for given in (good, dict(good, out=None)):
+        for bad in (dict(a_s=z(4, dtype=bf16)), dict(b_s=z(8, dtype=torch.float64)), dict(A=z(4, 16, dtype=torch.uint8)),
+                    dict(B=z(8, 16, dtype=torch.uint8)), dict(out=z(4, 8, dtype=bf16)),
+                    (dict(out_dtype="bf16", out=good["out"]), "out must be"),
+                    (dict(out_dtype="bf16", out=z(4, 8, dtype=torch.float16)), "out must be")):
+            refused(w8.int8_matmul, given, bad, reached)
