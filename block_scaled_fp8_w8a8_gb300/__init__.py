@@ -334,9 +334,9 @@ def quantize_int8_per_token(X, A=None, a_s=None, stream=None):
     """Per-token INT8 quantisation of a CUDA tensor X [M, K] (bf16, fp16 or fp32, unit
     stride along K): returns (A int8 [M, K], a_s float32 [M]), the INT8 matmul's
     activation operand.  ``A`` / ``a_s`` may be preallocated."""
-    lib = load_library()
+    lib, types = load_library(), _dtypes or _load_dtypes()
     if A is not None and a_s is not None and lib.quant_tensors is not None:
-        st = lib.quant_tensors(X, A, a_s, _in_codes, _stream(stream))
+        st = lib.quant_tensors(X, A, a_s, _in_codes, types.fast, _stream(stream))
         if st == 0:
             return A, a_s
         if st is not None:
@@ -348,12 +348,14 @@ def quantize_int8_per_token(X, A=None, a_s=None, stream=None):
         import torch
     if A is None:
         A = torch.empty(shape, dtype=torch.int8, device=X.device)
-    elif A.shape != shape:
+    elif A.shape != shape or A.dtype is not types.i8:
         _want(A, shape, "A")
+        _typed(A, (types.i8,), "A")
     if a_s is None:
         a_s = torch.empty(M, dtype=torch.float32, device=X.device)
-    elif a_s.shape != (M,) or not a_s.is_contiguous():
+    elif a_s.shape != (M,) or a_s.dtype is not types.f32 or not a_s.is_contiguous():
         _want(a_s, (M,), "a_s")
+        _typed(a_s, (types.f32,), "a_s")
         _dense(a_s, "a_s")
     st = lib.w8a8_quantize_int8_per_token(
         X.data_ptr(), code, _rows(X), A.data_ptr(), _rows(A), a_s.data_ptr(), M, K,

@@ -275,19 +275,20 @@ static PyObject *py_int8_tensors(PyObject *self, PyObject *const *args, Py_ssize
     Py_RETURN_NONE;
 }
 
-/* X, A, a_s, the input types' codes by dtype, stream */
+/* X, A, a_s, the input types' codes by dtype, dtypes, stream */
 static PyObject *py_quant_tensors(PyObject *self, PyObject *const *args, Py_ssize_t n)
 {
     (void)self;
-    if (!want(n, 5, f_quant != NULL))
+    if (!want(n, 6, f_quant != NULL))
         return NULL;
     tensor_t x, a, as;
     int st;
     if (dense(args[0], &x) && dense(args[1], &a) && dense(args[2], &as) && x.dims == 2 &&
+        a.dtype == type_at(args[4], T_INT8) && as.dtype == type_at(args[4], T_F32) &&
         is(&a, 2, x.size[0], x.size[1]) && is(&as, 1, x.size[0], 0)) {
         PyObject *code = PyDict_GetItemWithError(args[3], x.dtype);
         const int kind = code ? (int)PyLong_AsLong(code) : -1;
-        void *s = PTR(4);
+        void *s = PTR(5);
         if (code && !PyErr_Occurred()) {
             Py_BEGIN_ALLOW_THREADS
             st = f_quant(x.ptr, kind, 0, a.ptr, 0, as.ptr, x.size[0], x.size[1], s);

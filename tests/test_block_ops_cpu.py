@@ -213,3 +213,12 @@ def test_int8_matmul_refuses_elements_of_another_type(reached):
                     (dict(out_dtype="bf16", out=good["out"]), "out must be"),
                     (dict(out_dtype="bf16", out=z(4, 8, dtype=torch.float16)), "out must be")):
             refused(w8.int8_matmul, given, bad, reached)
+
+
+def test_quantiser_refuses_outputs_of_another_type(reached):
+    good = dict(X=z(4, 16), A=z(4, 16, dtype=torch.int8), a_s=z(4), stream=0)
+    for bad in (dict(A=z(4, 16, dtype=torch.uint8)), dict(A=z(4, 16)), dict(a_s=z(4, dtype=torch.bfloat16)),
+                dict(a_s=z(4, dtype=torch.float64))):
+        refused(w8.quantize_int8_per_token, good, bad, reached)
+        other = "a_s" if "A" in bad else "A"
+        refused(w8.quantize_int8_per_token, dict(good, **{other: None}), bad, reached)
