@@ -383,13 +383,13 @@ def sandwich_norm(h, x, w_post=None, w_pre=None, gate=None, gate_rows=None, res_
 
     h, x [M, D]; w_post, w_pre [D] (None: no norm); gate [R, D], row m // gate_rows for
     token m (default: R equal runs of tokens), or [D] for all, or None.  Returns (r, y),
-    r in x's type; with out="fp8" (E4M3 codes and one scale per 128 columns) or "int8"
-    (one scale per row) (r, codes, scales).  x_out may be x itself.  Raises W8A8Error
+    r in x's type; with out="fp8" (E4M3 codes and one float32 scale per 128 columns) or
+    "int8" (one scale per row) (r, codes, scales).  x_out may be x itself.  Raises W8A8Error
     on a non-zero status."""
-    kind, lib = _NORM_KINDS[out], load_library()
+    kind, lib, types = _NORM_KINDS[out], load_library(), _dtypes or _load_dtypes()
     if x_out is not None and y_out is not None and lib.norm_tensors is not None:
         st = lib.norm_tensors(h, x, w_post, w_pre, gate, gate_rows, res_scale, eps, kind, x_out, y_out,
-                              scales_out, _in_codes, _stream(stream))
+                              scales_out, _in_codes, types.fast, _stream(stream))
         if st == 0:
             return (x_out, y_out) if not kind else (x_out, y_out, scales_out)
         if st is not None:
@@ -417,8 +417,10 @@ def sandwich_norm(h, x, w_post=None, w_pre=None, gate=None, gate_rows=None, res_
         s_shape = (M, (D + 127) // 128) if kind == W8A8_NORM_FP8 else (M,)
         if scales_out is None:
             scales_out = torch.empty(s_shape, dtype=torch.float32, device=h.device)
-        elif scales_out.shape != s_shape or not scales_out.is_contiguous():
+        elif (scales_out.shape != s_shape or scales_out.dtype is not types.f32 or
+              not scales_out.is_contiguous()):
             _want(scales_out, s_shape, "scales_out")
+            _typed(scales_out, (types.f32,), "scales_out")
             _dense(scales_out, "scales_out")
         scales = scales_out.data_ptr()
     width = (D,)

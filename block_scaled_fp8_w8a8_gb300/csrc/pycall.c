@@ -170,12 +170,20 @@ static int is(const tensor_t *d, int dims, int64_t a, int64_t b)
     return d->dims == dims && d->size[0] == a && (dims == 1 || d->size[1] == b);
 }
 
+/* torch's dtypes as the wrappers hand them over: int8, float32, then the output types in
+ * the order of their codes. */
+enum { T_INT8, T_F32, T_OUT };
+static PyObject *type_at(PyObject *types, int i)
+{
+    return PyTuple_Check(types) && i >= 0 && i < PyTuple_GET_SIZE(types) ? PyTuple_GET_ITEM(types, i) : NULL;
+}
+
 /* h, x, w_post, w_pre, gate, gate_rows, res_scale, eps, kind, x_out, y_out, scales_out,
- * the input types' codes by dtype, stream */
+ * the input types' codes by dtype, dtypes, stream */
 static PyObject *py_norm_tensors(PyObject *self, PyObject *const *args, Py_ssize_t n)
 {
     (void)self;
-    if (!want(n, 14, f_norm != NULL))
+    if (!want(n, 15, f_norm != NULL))
         return NULL;
     tensor_t h, x, xo, y, t;
     void *post = NULL, *pre = NULL, *gate = NULL, *scales = NULL;
@@ -192,7 +200,7 @@ static PyObject *py_norm_tensors(PyObject *self, PyObject *const *args, Py_ssize
         PyObject *o = PyObject_CallMethodNoArgs(args[10], s_bytes);
         const long bytes = o ? PyLong_AsLong(o) : 0;
         Py_XDECREF(o);
-        if (bytes != 1 || !dense(args[11], &t) ||
+        if (bytes != 1 || !dense(args[11], &t) || t.dtype != type_at(args[13], T_F32) ||
             !(kind == 1 ? is(&t, 2, M, (D + 127) / 128) : is(&t, 1, M, 0)))
             goto other;
         scales = t.ptr;
@@ -225,7 +233,7 @@ static PyObject *py_norm_tensors(PyObject *self, PyObject *const *args, Py_ssize
         goto other;
     const int h_code = (int)PyLong_AsLong(hk), x_code = (int)PyLong_AsLong(xk);
     const double rs = PyFloat_AsDouble(args[6]), eps = PyFloat_AsDouble(args[7]);
-    void *s = PTR(13);
+    void *s = PTR(14);
     if (PyErr_Occurred())
         goto other;
     int st;
@@ -237,14 +245,6 @@ static PyObject *py_norm_tensors(PyObject *self, PyObject *const *args, Py_ssize
 other:
     PyErr_Clear();
     Py_RETURN_NONE;
-}
-
-/* torch's dtypes as the wrappers hand them over: int8, float32, then the output types in
- * the order of their codes. */
-enum { T_INT8, T_F32, T_OUT };
-static PyObject *type_at(PyObject *types, int i)
-{
-    return PyTuple_Check(types) && i >= 0 && i < PyTuple_GET_SIZE(types) ? PyTuple_GET_ITEM(types, i) : NULL;
 }
 
 /* A, a_s, B, b_s, out, output code, dtypes, stream */

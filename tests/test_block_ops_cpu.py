@@ -222,3 +222,11 @@ def test_quantiser_refuses_outputs_of_another_type(reached):
         refused(w8.quantize_int8_per_token, good, bad, reached)
         other = "a_s" if "A" in bad else "A"
         refused(w8.quantize_int8_per_token, dict(good, **{other: None}), bad, reached)
+
+
+def test_sandwich_norm_refuses_scales_of_another_type(reached):
+    for out, code, shape in (("fp8", torch.float8_e4m3fn, (4, 2)), ("int8", torch.int8, (4,))):
+        good = dict(h=z(4, 144), x=z(4, 144), x_out=z(4, 144), y_out=z(4, 144, dtype=code), out=out, stream=0)
+        for kw in (good, dict(good, x_out=None)):
+            for dtype in (torch.bfloat16, torch.float64, torch.int32):
+                refused(w8.sandwich_norm, kw, dict(scales_out=z(*shape, dtype=dtype)), reached)
