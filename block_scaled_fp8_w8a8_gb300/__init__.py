@@ -217,6 +217,18 @@ def _typed(t, wanted, name):
                         f"{name} must be {' or '.join(str(w) for w in wanted)}, not {t.dtype}")
 
 
+def _one_gpu(*tensors):
+    """Refuse tensors (None: not given) whose addresses the kernels cannot use together."""
+    device = tensors[0].get_device()
+    wrong = device < 0
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            wrong = True
+    if wrong:
+        raise W8A8Error(W8A8_ERR_INVALID_ARG, "tensors must be on one CUDA device, not on " +
+                        ", ".join(sorted({str(t.device) for t in tensors if t is not None})))
+
+
 def _rows(t):
     """Row stride of a 2-D tensor whose rows are contiguous, 0 for a dense one."""
     if t.is_contiguous():
@@ -282,6 +294,7 @@ def grouped_matmul_ragged(A, a_s, B, b_s, offsets, out_dtype="bf16", out=None, s
         _typed(A, types.e4m3, "A")
         _typed(B, types.e4m3, "B")
         _typed(out, (types.out[code],), "out")
+    _one_gpu(A, a_s, B, b_s, offsets, out)
     o = options(**opts) if opts else None
     st = load_library().w8a8_block_fp8_grouped_matmul_ragged(
         A.data_ptr(), a_s.data_ptr(), B.data_ptr(), b_s.data_ptr(), out.data_ptr(),
@@ -298,7 +311,8 @@ def int8_matmul(A, a_s, B, b_s, out_dtype="bf16", out=None, stream=None, **opts)
     map to w8a8_options fields.  Raises W8A8Error on a non-zero status."""
     code, lib, types = out_code(out_dtype), load_library(), _dtypes or _load_dtypes()
     if out is not None and not opts and lib.int8_tensors is not None:
-        st = lib.int8_tensors(A, a_s, B, b_s, out, code, types.fast, _stream(stream))
+        st = lib.int8_tensors(A, a_s, B, b_s, out, code, types.fast,
+                              stream if stream is None else _stream(stream))
         if st == 0:
             return out
         if st is not None:
@@ -321,10 +335,12 @@ def int8_matmul(A, a_s, B, b_s, out_dtype="bf16", out=None, stream=None, **opts)
     if a_s.dtype is not types.f32 or b_s.dtype is not types.f32:
         _typed(a_s, (types.f32,), "a_s")
         _typed(b_s, (types.f32,), "b_s")
+    ld_a, ld_b, ld_c = _rows(A), _rows(B), _rows(out)
+    _one_gpu(A, a_s, B, b_s, out)
     o = options(**opts) if opts else None
     st = lib.w8a8_int8_matmul(
-        A.data_ptr(), _rows(A), a_s.data_ptr(), B.data_ptr(), _rows(B), b_s.data_ptr(),
-        out.data_ptr(), _rows(out), M, N, K, code, _stream(stream), _opts_address(o))
+        A.data_ptr(), ld_a, a_s.data_ptr(), B.data_ptr(), ld_b, b_s.data_ptr(),
+        out.data_ptr(), ld_c, M, N, K, code, _stream(stream), _opts_address(o))
     if st:
         check(st)
     return out
@@ -336,7 +352,8 @@ def quantize_int8_per_token(X, A=None, a_s=None, stream=None):
     activation operand.  ``A`` / ``a_s`` may be preallocated."""
     lib, types = load_library(), _dtypes or _load_dtypes()
     if A is not None and a_s is not None and lib.quant_tensors is not None:
-        st = lib.quant_tensors(X, A, a_s, _in_codes, types.fast, _stream(stream))
+        st = lib.quant_tensors(X, A, a_s, _in_codes, types.fast,
+                               stream if stream is None else _stream(stream))
         if st == 0:
             return A, a_s
         if st is not None:
@@ -357,9 +374,10 @@ def quantize_int8_per_token(X, A=None, a_s=None, stream=None):
         _want(a_s, (M,), "a_s")
         _typed(a_s, (types.f32,), "a_s")
         _dense(a_s, "a_s")
+    ld_x, ld_a = _rows(X), _rows(A)
+    _one_gpu(X, A, a_s)
     st = lib.w8a8_quantize_int8_per_token(
-        X.data_ptr(), code, _rows(X), A.data_ptr(), _rows(A), a_s.data_ptr(), M, K,
-        _stream(stream))
+        X.data_ptr(), code, ld_x, A.data_ptr(), ld_a, a_s.data_ptr(), M, K, _stream(stream))
     if st:
         check(st)
     return A, a_s
@@ -389,7 +407,8 @@ def sandwich_norm(h, x, w_post=None, w_pre=None, gate=None, gate_rows=None, res_
     kind, lib, types = _NORM_KINDS[out], load_library(), _dtypes or _load_dtypes()
     if x_out is not None and y_out is not None and lib.norm_tensors is not None:
         st = lib.norm_tensors(h, x, w_post, w_pre, gate, gate_rows, res_scale, eps, kind, x_out, y_out,
-                              scales_out, _in_codes, types.fast, _stream(stream))
+                              scales_out, _in_codes, types.fast,
+                              stream if stream is None else _stream(stream))
         if st == 0:
             return (x_out, y_out) if not kind else (x_out, y_out, scales_out)
         if st is not None:
@@ -444,13 +463,12 @@ def sandwich_norm(h, x, w_post=None, w_pre=None, gate=None, gate_rows=None, res_
         if g_shape[-1] != D or gate_rows < 1 or R * gate_rows < M:
             raise W8A8Error(W8A8_ERR_INVALID_ARG,
                             f"gate of {tuple(g_shape)} for {M} rows of {D}, {gate_rows} to a gate")
+    ld_h, ld_x, ld_xo, ld_y = _rows(h), _rows(x), _rows(x_out), _rows(y_out)
+    _one_gpu(h, x, x_out, y_out, w_post, w_pre, gate, scales_out if kind else None)
     st = lib.w8a8_sandwich_norm(
-        h.data_ptr(), hk, 0 if h.is_contiguous() else _rows(h),
-        x.data_ptr(), _in_codes[xtype], 0 if x.is_contiguous() else _rows(x),
-        post, gates, gate_rows or 1, pre, res_scale, eps,
-        x_out.data_ptr(), 0 if x_out.is_contiguous() else _rows(x_out),
-        y_out.data_ptr(), scales, kind, 0 if y_out.is_contiguous() else _rows(y_out),
-        M, D, _stream(stream))
+        h.data_ptr(), hk, ld_h, x.data_ptr(), _in_codes[xtype], ld_x, post, gates,
+        gate_rows or 1, pre, res_scale, eps, x_out.data_ptr(), ld_xo, y_out.data_ptr(), scales,
+        kind, ld_y, M, D, _stream(stream))
     if st:
         check(st)
     return (x_out, y_out) if not kind else (x_out, y_out, scales_out)

@@ -109,9 +109,13 @@ _PYCALL = ("w8a8_sandwich_norm", "w8a8_block_fp8_grouped_matmul_ragged", "w8a8_i
            "w8a8_quantize_int8_per_token")
 
 
+_pycall = None   # the module, once bound
+
+
 def _bind_pycall(lib):
     """Give those functions of the loaded library their entries from the extension
     module where it has been built; they take the same arguments."""
+    global _pycall
     lib.norm_tensors = lib.int8_tensors = lib.quant_tensors = None
     path = _build.pycall_path()
     if not os.path.exists(path):
@@ -122,6 +126,10 @@ def _bind_pycall(lib):
     mod.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _PYCALL))
     for n in _PYCALL:
         setattr(lib, n, getattr(mod, n))
+    _pycall = mod
+    if _current is not None:
+        import torch
+        mod.bind_torch(torch.Tensor, *_current)
     # the plain case of the Python calls, on tensors (see pycall.c)
     for n in ("norm_tensors", "int8_tensors", "quant_tensors"):
         setattr(lib, n, getattr(mod, n))
@@ -229,6 +237,8 @@ def _current_stream():
         # torch.cuda.current_stream().cuda_stream without the Stream object (0.2
         # instead of 2.9 us a call, more than a small kernel's launch)
         _current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        if _pycall is not None:
+            _pycall.bind_torch(torch.Tensor, *_current)
     raw, device = _current
     return raw(device())
 

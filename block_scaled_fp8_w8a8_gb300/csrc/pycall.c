@@ -137,12 +137,34 @@ typedef struct {
     PyObject *dtype;       /* borrowed: torch keeps its dtypes */
 } tensor_t;
 
-static PyObject *s_shape, *s_dtype, *s_dense, *s_ptr, *s_bytes;
+/* The attributes that are read: their names, and what a plain torch.Tensor's type has for
+ * them (a subclass may have others), which saves the search for each. */
+enum { SHAPE, DTYPE, DENSE, PTR_OF, BYTES, GPU_OF, ATTRS };
+static const char *const attr_names[ATTRS] = {"shape", "dtype", "is_contiguous", "data_ptr",
+                                              "element_size", "get_device"};
+static PyObject *names[ATTRS], *own[ATTRS];
+static PyTypeObject *plain;
 
-/* 1 for a dense tensor of one or two dimensions, else 0 (with or without an error set). */
-static int dense(PyObject *t, tensor_t *d)
+static PyObject *get(PyObject *t, int a)
 {
-    PyObject *o = PyObject_GetAttr(t, s_shape);
+    if (Py_TYPE(t) == plain)
+        return Py_TYPE(own[a])->tp_descr_get(own[a], t, (PyObject *)plain);
+    return PyObject_GetAttr(t, names[a]);
+}
+
+static PyObject *call(PyObject *t, int a)
+{
+    if (Py_TYPE(t) == plain)
+        return PyObject_Vectorcall(own[a], &t, 1, NULL);
+    return PyObject_CallMethodNoArgs(t, names[a]);
+}
+
+/* 1 for a dense tensor of one or two dimensions on the GPU *gpu (ANY_GPU: any, which it
+ * becomes), else 0 (with or without an error set). */
+enum { ANY_GPU = -1 };
+static int dense(PyObject *t, tensor_t *d, long *gpu)
+{
+    PyObject *o = get(t, SHAPE);
     int ok = o && PyTuple_Check(o) && PyTuple_GET_SIZE(o) >= 1 && PyTuple_GET_SIZE(o) <= 2;
     if (ok) {
         d->dims = (int)PyTuple_GET_SIZE(o);
@@ -150,19 +172,41 @@ static int dense(PyObject *t, tensor_t *d)
             d->size[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(o, i));
     }
     Py_XDECREF(o);
-    if (!ok || !(o = PyObject_GetAttr(t, s_dtype)))
+    if (!ok || !(o = get(t, DTYPE)))
         return 0;
     d->dtype = o;
     Py_DECREF(o);
-    if (!(o = PyObject_CallMethodNoArgs(t, s_dense)))
+    if (!(o = call(t, GPU_OF)))
         return 0;
+    const long device = PyLong_AsLong(o);            /* -1 for a tensor on no GPU */
+    Py_DECREF(o);
+    if (device < 0 || (*gpu != ANY_GPU && device != *gpu) || !(o = call(t, DENSE)))
+        return 0;
+    *gpu = device;
     ok = o == Py_True;
     Py_DECREF(o);
-    if (!ok || !(o = PyObject_CallMethodNoArgs(t, s_ptr)))
+    if (!ok || !(o = call(t, PTR_OF)))
         return 0;
     d->ptr = (void *)(uintptr_t)PyLong_AsUnsignedLongLong(o);
     Py_DECREF(o);
     return !PyErr_Occurred();
+}
+
+/* The stream argument: an address, or None for torch's current stream, by its functions
+ * that bind_torch got.  Sets an error for anything else. */
+static PyObject *current_raw, *current_device;
+static void *stream_of(PyObject *s)
+{
+    if (s != Py_None)
+        return PyLong_AsVoidPtr(s);
+    PyObject *dev = current_device ? PyObject_CallNoArgs(current_device) : NULL;
+    PyObject *raw = dev ? PyObject_CallOneArg(current_raw, dev) : NULL;
+    void *p = raw ? PyLong_AsVoidPtr(raw) : NULL;
+    if (!raw && !PyErr_Occurred())
+        PyErr_SetString(PyExc_RuntimeError, "bind_torch() first");
+    Py_XDECREF(dev);
+    Py_XDECREF(raw);
+    return p;
 }
 
 static int is(const tensor_t *d, int dims, int64_t a, int64_t b)
@@ -188,35 +232,36 @@ static PyObject *py_norm_tensors(PyObject *self, PyObject *const *args, Py_ssize
     tensor_t h, x, xo, y, t;
     void *post = NULL, *pre = NULL, *gate = NULL, *scales = NULL;
     int64_t gate_rows = 1, M, D;
+    long gpu = ANY_GPU;
     const int kind = I32(8);
-    if (!dense(args[0], &h) || h.dims != 2 || !dense(args[1], &x) || !dense(args[9], &xo) ||
-        !dense(args[10], &y))
+    if (!dense(args[0], &h, &gpu) || h.dims != 2 || !dense(args[1], &x, &gpu) || !dense(args[9], &xo, &gpu) ||
+        !dense(args[10], &y, &gpu))
         goto other;
     M = h.size[0], D = h.size[1];
     if (!is(&x, 2, M, D) || !is(&xo, 2, M, D) || !is(&y, 2, M, D) || xo.dtype != x.dtype ||
         (kind == 0 && y.dtype != h.dtype))
         goto other;
     if (kind != 0) {
-        PyObject *o = PyObject_CallMethodNoArgs(args[10], s_bytes);
+        PyObject *o = call(args[10], BYTES);
         const long bytes = o ? PyLong_AsLong(o) : 0;
         Py_XDECREF(o);
-        if (bytes != 1 || !dense(args[11], &t) || t.dtype != type_at(args[13], T_F32) ||
+        if (bytes != 1 || !dense(args[11], &t, &gpu) || t.dtype != type_at(args[13], T_F32) ||
             !(kind == 1 ? is(&t, 2, M, (D + 127) / 128) : is(&t, 1, M, 0)))
             goto other;
         scales = t.ptr;
     }
     if (args[2] != Py_None) {
-        if (!dense(args[2], &t) || !is(&t, 1, D, 0) || t.dtype != h.dtype)
+        if (!dense(args[2], &t, &gpu) || !is(&t, 1, D, 0) || t.dtype != h.dtype)
             goto other;
         post = t.ptr;
     }
     if (args[3] != Py_None) {
-        if (!dense(args[3], &t) || !is(&t, 1, D, 0) || t.dtype != h.dtype)
+        if (!dense(args[3], &t, &gpu) || !is(&t, 1, D, 0) || t.dtype != h.dtype)
             goto other;
         pre = t.ptr;
     }
     if (args[4] != Py_None) {
-        if (!dense(args[4], &t) || t.size[t.dims - 1] != D || t.dtype != h.dtype)
+        if (!dense(args[4], &t, &gpu) || t.size[t.dims - 1] != D || t.dtype != h.dtype)
             goto other;
         const int64_t rows = t.dims == 2 ? t.size[0] : 1;
         if (args[5] != Py_None)
@@ -233,7 +278,7 @@ static PyObject *py_norm_tensors(PyObject *self, PyObject *const *args, Py_ssize
         goto other;
     const int h_code = (int)PyLong_AsLong(hk), x_code = (int)PyLong_AsLong(xk);
     const double rs = PyFloat_AsDouble(args[6]), eps = PyFloat_AsDouble(args[7]);
-    void *s = PTR(14);
+    void *s = stream_of(args[14]);
     if (PyErr_Occurred())
         goto other;
     int st;
@@ -255,14 +300,15 @@ static PyObject *py_int8_tensors(PyObject *self, PyObject *const *args, Py_ssize
         return NULL;
     tensor_t a, as, b, bs, c;
     int st;
+    long gpu = ANY_GPU;
     const int out = I32(5);
     PyObject *const i8 = type_at(args[6], T_INT8), *const f32 = type_at(args[6], T_F32);
-    if (dense(args[0], &a) && dense(args[1], &as) && dense(args[2], &b) && dense(args[3], &bs) &&
-        dense(args[4], &c) && a.dtype == i8 && b.dtype == i8 && as.dtype == f32 && bs.dtype == f32 &&
+    if (dense(args[0], &a, &gpu) && dense(args[1], &as, &gpu) && dense(args[2], &b, &gpu) && dense(args[3], &bs, &gpu) &&
+        dense(args[4], &c, &gpu) && a.dtype == i8 && b.dtype == i8 && as.dtype == f32 && bs.dtype == f32 &&
         out >= 0 && c.dtype == type_at(args[6], T_OUT + out) && a.dims == 2 && b.dims == 2 &&
         a.size[1] == b.size[1] && is(&as, 1, a.size[0], 0) && is(&bs, 1, b.size[0], 0) &&
         is(&c, 2, a.size[0], b.size[0])) {
-        void *s = PTR(7);
+        void *s = stream_of(args[7]);
         if (!PyErr_Occurred()) {
             Py_BEGIN_ALLOW_THREADS
             st = f_int8(a.ptr, 0, as.ptr, b.ptr, 0, bs.ptr, c.ptr, 0, a.size[0], b.size[0], a.size[1], out,
@@ -283,12 +329,13 @@ static PyObject *py_quant_tensors(PyObject *self, PyObject *const *args, Py_ssiz
         return NULL;
     tensor_t x, a, as;
     int st;
-    if (dense(args[0], &x) && dense(args[1], &a) && dense(args[2], &as) && x.dims == 2 &&
+    long gpu = ANY_GPU;
+    if (dense(args[0], &x, &gpu) && dense(args[1], &a, &gpu) && dense(args[2], &as, &gpu) && x.dims == 2 &&
         a.dtype == type_at(args[4], T_INT8) && as.dtype == type_at(args[4], T_F32) &&
         is(&a, 2, x.size[0], x.size[1]) && is(&as, 1, x.size[0], 0)) {
         PyObject *code = PyDict_GetItemWithError(args[3], x.dtype);
         const int kind = code ? (int)PyLong_AsLong(code) : -1;
-        void *s = PTR(5);
+        void *s = stream_of(args[5]);
         if (code && !PyErr_Occurred()) {
             Py_BEGIN_ALLOW_THREADS
             st = f_quant(x.ptr, kind, 0, a.ptr, 0, as.ptr, x.size[0], x.size[1], s);
@@ -310,21 +357,39 @@ static PyObject *py_bind(PyObject *self, PyObject *const *args, Py_ssize_t n)
     f_ragged = (ragged_fn)PTR(1);
     f_int8 = (int8_fn)PTR(2);
     f_quant = (quant_fn)PTR(3);
-    if (!s_shape) {
-        s_shape = PyUnicode_InternFromString("shape");
-        s_dtype = PyUnicode_InternFromString("dtype");
-        s_dense = PyUnicode_InternFromString("is_contiguous");
-        s_ptr = PyUnicode_InternFromString("data_ptr");
-        s_bytes = PyUnicode_InternFromString("element_size");
-    }
+    for (int i = 0; i < ATTRS && !names[i]; ++i)
+        names[i] = PyUnicode_InternFromString(attr_names[i]);
     if (PyErr_Occurred())
         return NULL;
+    Py_RETURN_NONE;
+}
+
+/* bind_torch(torch.Tensor, current raw stream of a device, current device) */
+static PyObject *py_bind_torch(PyObject *self, PyObject *const *args, Py_ssize_t n)
+{
+    (void)self;
+    if (!want(n, 3, names[0] != NULL))
+        return NULL;
+    if (plain)                       /* torch does not change */
+        Py_RETURN_NONE;
+    for (int i = 0; i < ATTRS; ++i) {
+        if (!(own[i] = PyObject_GetAttr(args[0], names[i])))
+            return NULL;
+        if ((i == SHAPE || i == DTYPE) && !Py_TYPE(own[i])->tp_descr_get) {
+            PyErr_SetString(PyExc_TypeError, "torch.Tensor: shape and dtype are no descriptors");
+            return NULL;
+        }
+    }
+    current_raw = Py_NewRef(args[1]);
+    current_device = Py_NewRef(args[2]);
+    plain = (PyTypeObject *)Py_NewRef(args[0]);
     Py_RETURN_NONE;
 }
 
 #define ENTRY(name, fn, doc) {name, (PyCFunction)(void (*)(void))fn, METH_FASTCALL, doc}
 static PyMethodDef methods[] = {
     ENTRY("bind", py_bind, "set the library's function addresses"),
+    ENTRY("bind_torch", py_bind_torch, "torch's tensor type, and its functions for the current stream"),
     ENTRY("w8a8_sandwich_norm", py_norm, "see the C header"),
     ENTRY("norm_tensors", py_norm_tensors, "sandwich_norm of dense tensors with every output given"),
     ENTRY("int8_tensors", py_int8_tensors, "int8_matmul, as norm_tensors"),

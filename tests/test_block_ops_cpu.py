@@ -230,3 +230,19 @@ def test_sandwich_norm_refuses_scales_of_another_type(reached):
         for kw in (good, dict(good, x_out=None)):
             for dtype in (torch.bfloat16, torch.float64, torch.int32):
                 refused(w8.sandwich_norm, kw, dict(scales_out=z(*shape, dtype=dtype)), reached)
+
+
+def test_tensors_off_the_gpu_do_not_reach_the_library(reached):
+    i8, u8, says = torch.int8, torch.uint8, "one CUDA device, not on cpu"
+    for given in (True, False):
+        for call, good in (
+            (w8.grouped_matmul_ragged, dict(
+                A=z(4, 128, dtype=u8), a_s=z(4, 1), B=z(2, 8, 128, dtype=u8), b_s=z(2, 1, 1),
+                offsets=z(3, dtype=torch.int32), out_dtype="fp32", out=z(4, 8) if given else None)),
+            (w8.int8_matmul, dict(A=z(4, 16, dtype=i8), a_s=z(4), B=z(8, 16, dtype=i8), b_s=z(8), out_dtype="fp32",
+                                  out=z(4, 8) if given else None)),
+            (w8.quantize_int8_per_token, dict(X=z(4, 16), **(dict(A=z(4, 16, dtype=i8), a_s=z(4)) if given else {}))),
+            (w8.sandwich_norm, dict(h=z(4, 16), x=z(4, 16), w_post=z(16), w_pre=z(16), gate=z(16),
+                                    **(dict(x_out=z(4, 16), y_out=z(4, 16)) if given else {}))),
+        ):
+            refused(call, good, (dict(stream=0), says), reached)

@@ -119,6 +119,29 @@ def test_threads_on_one_stream(grown):
     assert w8.w8a8_get_device_status()[0] == w8.W8A8_OK
 
 
+def test_a_tensor_on_the_host_among_others_is_refused():
+    """Each argument in turn, with the outputs given and without."""
+    z = lambda *s, dtype=torch.float32: torch.zeros(s, dtype=dtype, device="cuda")  # noqa: E731
+    i8, u8 = torch.int8, torch.uint8
+    for call, args, outs in (
+        (w8.grouped_matmul_ragged, dict(A=z(4, 128, dtype=u8), a_s=z(4, 1), B=z(2, 8, 128, dtype=u8), b_s=z(2, 1, 1),
+                                        offsets=z(3, dtype=torch.int32)), dict(out=z(4, 8, dtype=torch.bfloat16))),
+        (w8.int8_matmul, dict(A=z(4, 16, dtype=i8), a_s=z(4), B=z(8, 16, dtype=i8), b_s=z(8)),
+         dict(out=z(4, 8, dtype=torch.bfloat16))),
+        (w8.quantize_int8_per_token, dict(X=z(4, 16)), dict(A=z(4, 16, dtype=i8), a_s=z(4))),
+        (w8.sandwich_norm, dict(h=z(4, 16), x=z(4, 16), w_post=z(16), w_pre=z(16), gate=z(16), out="int8"),
+         dict(x_out=z(4, 16), y_out=z(4, 16, dtype=i8), scales_out=z(4))),
+    ):
+        for good in (args, {**args, **outs}):
+            call(**good)
+            for name, t in good.items():
+                if torch.is_tensor(t):
+                    with pytest.raises(w8.W8A8Error, match="one CUDA device") as e:
+                        call(**{**good, name: t.cpu()})
+                    assert e.value.status == w8.W8A8_ERR_INVALID_ARG
+    assert w8.w8a8_get_device_status()[0] == w8.W8A8_OK
+
+
 def run_all(seed=1):
     """Every kernel of the three operators once or more, on sizes with ragged ends."""
     g = torch.Generator(device="cuda").manual_seed(seed)
