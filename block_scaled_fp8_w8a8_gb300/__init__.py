@@ -11,6 +11,7 @@ input generator ``synth`` can be imported without the library.
 """
 from __future__ import annotations
 
+from . import _binding
 from ._binding import (  # noqa: F401
     EXPORTED, W8A8Error, W8A8_OK, W8A8_ERR_INVALID_ARG, W8A8_ERR_UNSUPPORTED, W8A8_ERR_CUDA,
     W8A8_ERR_DEVICE_TIMEOUT, W8A8_ERR_WORKSPACE, W8A8_ERR_NO_DEVICE, W8A8_ERR_DEVICE_BOUNDS,
@@ -219,12 +220,11 @@ def _typed(t, wanted, name):
 
 def _one_gpu(*tensors):
     """Refuse tensors (None: not given) whose addresses the kernels cannot use together."""
-    device = tensors[0].get_device()
-    wrong = device < 0
-    for t in tensors:
-        if t is not None and t.get_device() != device:
-            wrong = True
-    if wrong:
+    ext = _binding._pycall
+    if ext is not None and ext.one_gpu(*tensors):
+        return
+    devices = {t.get_device() for t in tensors if t is not None}
+    if len(devices) > 1 or -1 in devices:
         raise W8A8Error(W8A8_ERR_INVALID_ARG, "tensors must be on one CUDA device, not on " +
                         ", ".join(sorted({str(t.device) for t in tensors if t is not None})))
 

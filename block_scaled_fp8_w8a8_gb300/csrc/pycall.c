@@ -159,9 +159,33 @@ static PyObject *call(PyObject *t, int a)
     return PyObject_CallMethodNoArgs(t, names[a]);
 }
 
-/* 1 for a dense tensor of one or two dimensions on the GPU *gpu (ANY_GPU: any, which it
- * becomes), else 0 (with or without an error set). */
+/* Whether t is on the GPU *gpu (ANY_GPU: on any, which it becomes); an error may be set. */
 enum { ANY_GPU = -1 };
+static int on_gpu(PyObject *t, long *gpu)
+{
+    PyObject *o = call(t, GPU_OF);
+    const long device = o ? PyLong_AsLong(o) : -1;       /* -1 for a tensor on no GPU */
+    Py_XDECREF(o);
+    if (device < 0 || (*gpu != ANY_GPU && device != *gpu))
+        return 0;
+    *gpu = device;
+    return 1;
+}
+
+/* one_gpu(tensors ...): whether those that are not None are on one GPU */
+static PyObject *py_one_gpu(PyObject *self, PyObject *const *args, Py_ssize_t n)
+{
+    (void)self;
+    long gpu = ANY_GPU;
+    int ok = names[0] != NULL;
+    for (Py_ssize_t i = 0; ok && i < n; ++i)
+        ok = args[i] == Py_None || on_gpu(args[i], &gpu);
+    PyErr_Clear();
+    return PyBool_FromLong(ok);
+}
+
+/* 1 for a dense tensor of one or two dimensions on the GPU *gpu (see on_gpu), else 0 (with
+ * or without an error set). */
 static int dense(PyObject *t, tensor_t *d, long *gpu)
 {
     PyObject *o = get(t, SHAPE);
@@ -176,13 +200,8 @@ static int dense(PyObject *t, tensor_t *d, long *gpu)
         return 0;
     d->dtype = o;
     Py_DECREF(o);
-    if (!(o = call(t, GPU_OF)))
+    if (!on_gpu(t, gpu) || !(o = call(t, DENSE)))
         return 0;
-    const long device = PyLong_AsLong(o);            /* -1 for a tensor on no GPU */
-    Py_DECREF(o);
-    if (device < 0 || (*gpu != ANY_GPU && device != *gpu) || !(o = call(t, DENSE)))
-        return 0;
-    *gpu = device;
     ok = o == Py_True;
     Py_DECREF(o);
     if (!ok || !(o = call(t, PTR_OF)))
@@ -390,6 +409,7 @@ static PyObject *py_bind_torch(PyObject *self, PyObject *const *args, Py_ssize_t
 static PyMethodDef methods[] = {
     ENTRY("bind", py_bind, "set the library's function addresses"),
     ENTRY("bind_torch", py_bind_torch, "torch's tensor type, and its functions for the current stream"),
+    ENTRY("one_gpu", py_one_gpu, "whether tensors are on one GPU"),
     ENTRY("w8a8_sandwich_norm", py_norm, "see the C header"),
     ENTRY("norm_tensors", py_norm_tensors, "sandwich_norm of dense tensors with every output given"),
     ENTRY("int8_tensors", py_int8_tensors, "int8_matmul, as norm_tensors"),
