@@ -457,6 +457,9 @@ def sandwich_norm(h, x, w_post=None, w_pre=None, gate=None, gate_rows=None, res_
             _norm_weight(gate, dtype)
         gates = gate.data_ptr()
         g_shape = gate.shape
+        if len(g_shape) not in (1, 2):
+            raise W8A8Error(W8A8_ERR_INVALID_ARG,
+                            f"gate must be [{D}] or [rows, {D}], not {list(g_shape)}")
         R = g_shape[0] if len(g_shape) == 2 else 1
         if gate_rows is None:
             gate_rows = max(1, -(-M // max(R, 1)))

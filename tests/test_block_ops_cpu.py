@@ -246,3 +246,16 @@ def test_tensors_off_the_gpu_do_not_reach_the_library(reached):
                                     **(dict(x_out=z(4, 16), y_out=z(4, 16)) if given else {}))),
         ):
             refused(call, good, (dict(stream=0), says), reached)
+
+
+def test_sandwich_norm_refuses_a_gate_of_other_than_one_or_two_dimensions(reached, monkeypatch):
+    """(A gate [B, 1, D] of an adaptive norm is not one row for all tokens.)"""
+    monkeypatch.setattr(w8, "_one_gpu", lambda *tensors: None)      # these are on the host
+    w8.sandwich_norm(z(12, 16), z(12, 16), gate=z(4, 16), stream=0)
+    assert len(reached) == 1
+    reached.clear()
+    for outs in (dict(x_out=z(12, 16), y_out=z(12, 16)), {}):
+        good = dict(h=z(12, 16), x=z(12, 16), stream=0, **outs)
+        for shape in ((4, 1, 16), (1, 1, 16), (2, 2, 3, 16), ()):
+            for rows in (None, 3, 12):
+                refused(w8.sandwich_norm, good, dict(gate=z(*shape), gate_rows=rows), reached)
