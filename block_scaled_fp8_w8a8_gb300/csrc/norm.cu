@@ -12,6 +12,7 @@
 //
 // INT8 quantiser: a_s[m] = max_k |X[m,k]| / 127 (fp32 quotient; 1 where it is
 // 0), A[m,k] = round_half_even(X[m,k] / a_s[m]) (fp32 quotient), in -127..127.
+// A row with a NaN (an infinity) gets NaN (infinity) for a_s and zeros for A.
 //
 // HBM-bound: every input is read once and every output written once.  A row
 // is held in registers by the threads of one CTA (or one warp, for short
@@ -103,8 +104,28 @@ struct Add {
     static __device__ __forceinline__ float op(float a, float b) { return a + b; }
 };
 struct Max {
-    static __device__ __forceinline__ float op(float a, float b) { return fmaxf(a, b); }
+    // NaN where either is one, so that a row with a NaN gets a NaN for its scale
+    static __device__ __forceinline__ float op(float a, float b)
+    {
+        float m;
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+        return m;
+    }
 };
+// The same of a, |b| and |c| in one instruction.
+__device__ __forceinline__ float max_abs(float a, float b, float c)
+{
+    float m;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
+    return m;
+}
+template <int N> __device__ __forceinline__ float max_abs(float a, const float (&v)[N])
+{
+#pragma unroll
+    for (int j = 0; j + 1 < N; j += 2)
+        a = max_abs(a, v[j], v[j + 1]);
+    return N % 2 ? Max::op(a, fabsf(v[N - 1])) : a;
+}
 template <typename Op>
 __device__ __forceinline__ float row_reduce(float v, float *part, bool warp_rows)
 {
@@ -136,7 +157,8 @@ __device__ __forceinline__ float int8_scale(float amax)
 
 __device__ __forceinline__ uint32_t int8_code(float q)
 {
-    // |q| <= 127 (1 + 2^-23) but where a subnormal scale lost precision
+    // |q| <= 127 (1 + 2^-23) but where a subnormal scale lost precision, or NaN
+    // (a scale that is not finite), which is converted to 0
     return static_cast<uint32_t>(max(-127, min(127, __float2int_rn(q)))) & 0xffu;
 }
 
@@ -358,9 +380,15 @@ __global__ void __launch_bounds__(EARLY ? kEarlyThreads : kMaxThreads)
                 if (p.w_pre)
                     y = y * inv * wp[j];
                 w[j] = y;
-                amax = fmaxf(amax, fabsf(y));
                 if (!HELD && p.y_kind == W8A8_NORM_INT8)
                     held[e + j] = y;
+            }
+            if (p.y_kind == W8A8_NORM_INT8) {
+                amax = max_abs(amax, w);
+            } else {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j)
+                    amax = fmaxf(amax, fabsf(w[j]));
             }
         }
         if (p.y_kind == W8A8_NORM_SAME) {
@@ -739,7 +767,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) k_sandwich_ring(const RingPar
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 unpack2f(v[j], f[2 * j], f[2 * j + 1]);
-                amax = fmaxf(amax, fmaxf(fabsf(f[2 * j]), fabsf(f[2 * j + 1])));
+                amax = max_abs(amax, f[2 * j], f[2 * j + 1]);
             }
             const float s = int8_scale(row_reduce<Max>(amax, part_max[odd], false));
             if (in1)
@@ -977,11 +1005,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) k_sandwich_flat(const FlatPar
             if (any)
                 store_flat<HK>(static_cast<uint8_t *>(p.y) + m0 * kHB, c0, D, v);
         } else {
-            float amax = 0.f;
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                amax = fmaxf(amax, fabsf(v[j]));
-            const float sc = int8_scale(row_reduce<Max>(amax, part_max[odd], false));
+            const float sc = int8_scale(row_reduce<Max>(max_abs(0.f, v), part_max[odd], false));
             uint8_t *row = static_cast<uint8_t *>(p.y) + m0;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -1047,9 +1071,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_quant_int8(const QuantParams p)
         const int e = (i * T + tid) * VEC;
         if (e < p.K) {
             load_vec<KIND, VEC>(row, e, v[HELD ? i : 0]);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j)
-                amax = fmaxf(amax, fabsf(v[HELD ? i : 0][j]));
+            amax = max_abs(amax, v[HELD ? i : 0]);
         }
     }
     const float s = int8_scale(row_reduce<Max>(amax, part, warp_rows));

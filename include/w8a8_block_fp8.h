@@ -504,8 +504,9 @@ size_t w8a8_int8_workspace_size(int64_t M, int64_t N, int64_t K, const w8a8_opti
  *
  *   X_dev [M, ld_x] of x_dtype, A_dev INT8 [M, ld_a]; strides in elements, 0 =
  *   dense (K); any K up to 2^30 and alignments (X to its element size).  M == 0
- *   or K == 0 is a no-op.  X must not overlap A, and must be finite: a row with a
- *   NaN or an infinity gets unspecified codes and scale.
+ *   or K == 0 is a no-op.  X must not overlap A.  A row with a NaN gets the scale
+ *   NaN, one with an infinity the scale infinity, and either zeros for its codes,
+ *   so that its row of a product is NaN.
  */
 w8a8_status w8a8_quantize_int8_per_token(const void *X_dev, w8a8_in_dtype x_dtype, int64_t ld_x,
                                          void *A_dev, int64_t ld_a, float *a_s_dev, int64_t M,
@@ -534,8 +535,8 @@ w8a8_status w8a8_quantize_int8_per_token(const void *X_dev, w8a8_in_dtype x_dtyp
  *     W8A8_NORM_INT8  INT8 codes, scales_dev [M]: as w8a8_quantize_int8_per_token
  * Strides in elements, 0 = dense (D).  D <= W8A8_NORM_MAX_D.  M == 0 or D == 0 is a
  * no-op.  Other overlaps of inputs and outputs are not allowed.  NaN and infinity
- * pass into r and y; with 8-bit codes they leave their row's codes and scales
- * unspecified.  h^2 and r^2 are summed in fp32: they overflow for magnitudes
+ * pass into r and y; a y that is not finite gives INT8 codes as the quantiser does,
+ * and leaves its row's E4M3 codes and scales unspecified.  h^2 and r^2 are summed in fp32: they overflow for magnitudes
  * near 1e19.
  */
 typedef enum { W8A8_NORM_SAME = 0, W8A8_NORM_FP8 = 1, W8A8_NORM_INT8 = 2 } w8a8_norm_out;

@@ -249,6 +249,22 @@ def test_quantiser_extremes_and_strides():
         assert (out[:, :3] == 9).all() and (out[:, 267:] == 9).all()
 
 
+@pytest.mark.parametrize("M,K", [(5, 1), (6, 64), (9, 513), (5, 4096), (4, 16384), (3, 20001), (3, 20000)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_quantiser_of_rows_that_are_not_finite(M, K, dtype):
+    """NaN and infinity show in their row's scale, wherever they stand, and leave the
+    other rows as they are; the row's products are NaN."""
+    for at in {0, K // 2, K - 1}:
+        X = torch.randn(M, K, device="cuda").to(OUT[dtype])
+        want_q, want_s = quant_reference(X)
+        X[0, at], X[1, at] = float("nan"), -float("inf")
+        q, s = w8.quantize_int8_per_token(X)
+        assert torch.isnan(s[0]) and s[1] == float("inf") and (q[:2] == 0).all()
+        assert np.array_equal(s[2:].cpu().numpy(), want_s[2:]) and np.array_equal(q[2:].cpu().numpy(), want_q[2:])
+        C = w8.int8_matmul(q, s, *make(1, 24, K, seed=K)[2:], "fp32")
+        assert torch.isnan(C[:2]).all() and torch.isfinite(C[2:]).all()
+
+
 def test_from_activations():
     """Quantise and multiply, back to back on a side stream."""
     X = torch.randn(77, 1000, device="cuda", dtype=torch.bfloat16)

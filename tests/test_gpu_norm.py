@@ -156,6 +156,28 @@ def test_zero_rows_and_non_finite_values():
     check(sub, r[3:4], y[3:4])
 
 
+@pytest.mark.parametrize("M,D", [(6, 75), (6, 640), (5, 1537), (4, 17000), (4, 17001), (2500, 1024), (700, 4096),
+                                 (2500, 1032), (400, 1537), (350, 12003)])
+@pytest.mark.parametrize("dtype,resid", [("bf16", "fp32"), ("fp32", "fp32")])
+def test_int8_scales_of_rows_that_are_not_finite(M, D, dtype, resid):
+    """One NaN or infinity in a row of y (without norms it stays alone) shows in the
+    row's scale; the rows around it are as they were."""
+    for norms in ((), ("w_post", "w_pre")):
+        k = make(M, D, dtype, resid)
+        for n in ("w_post", "w_pre"):
+            if n not in norms:
+                k[n] = None
+        _, q0, s0 = w8.sandwich_norm(**k, eps=EPS, out="int8")
+        for at in (0, D - 1):
+            h, x = k["h"].clone(), k["x"].clone()
+            h[1, at], x[M - 1, at] = float("nan"), float("inf")
+            _, q, s = w8.sandwich_norm(**dict(k, h=h, x=x), eps=EPS, out="int8")
+            assert torch.isnan(s[1]) and (torch.isnan(s[M - 1]) if norms else s[M - 1] == float("inf"))
+            assert (q[1] == 0).all() and (q[M - 1] == 0).all()
+            rest = [i for i in range(M) if i not in (1, M - 1)]
+            assert torch.equal(q[rest], q0[rest]) and torch.equal(s[rest], s0[rest])
+
+
 def test_many_rows_on_a_side_stream_and_in_a_graph():
     k = make(3000, 264, "bf16", "fp32", gate_rows=7)
     s = torch.cuda.Stream()
