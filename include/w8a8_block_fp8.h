@@ -477,10 +477,14 @@ w8a8_status w8a8_block_fp8_grouped_matmul_ragged(const void *A_dev, const float 
  * Workspace (none for few tokens): w8a8_int8_workspace_size() bytes from
  * opts->workspace_dev, or the library's for this stream, under the rules of the
  * split-K workspace.
- * opts: variant AUTO, SMALLM (few tokens), SWAPAB (some hundred; K within 4096 to
- * 32768 by the token tile, else W8A8_ERR_UNSUPPORTED), TILED (128 x 128 tiles) or
- * TILED_PAIR (CTA pairs, 256 x 256), all with the same bits, the first two without
- * workspace; grid_limit, wait_limit_cycles, workspace and the test hooks apply.  The
+ * opts: variant AUTO, SMALLM (few tokens), SWAPAB (some hundred), TILED (128 x 128
+ * tiles) or TILED_PAIR (CTA pairs, 256 x 256), all with the same bits, the first two
+ * without workspace.  SWAPAB takes m_tile (tokens per tile) and split_k (CTAs of a
+ * cluster that share K, at most 8; 0 = choose), and K up to 512 * split_k times the
+ * number of tiles that 512 columns of tensor memory hold, 512 / (m_tile rounded up
+ * to 32): up to 65536 for M <= 256 where both are left to the call, else
+ * W8A8_ERR_UNSUPPORTED.  grid_limit and workspace apply to the tiled forms,
+ * wait_limit_cycles and the test hooks to all but SMALLM (which waits for nothing).  The
  * launches of a call wait on the device for the work before them on the stream,
  * whatever opts->pdl says.
  */

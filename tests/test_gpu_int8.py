@@ -91,6 +91,21 @@ def test_largest_sums_are_exact(M, K):
         assert_same(C, s.float())
 
 
+@pytest.mark.parametrize("M,opts,most", [(2, {}, 65536), (40, {}, 65536), (130, {}, 65536), (256, {}, 65536),
+                                         (300, dict(m_tile=256), 8192), (100, dict(m_tile=64, split_k=2), 8192),
+                                         (40, dict(m_tile=48, split_k=1), 4096), (40, dict(m_tile=16, split_k=3), 24576)])
+def test_longest_sums_of_the_some_hundred_token_form(M, opts, most):
+    """K up to 512 * split_k * (512 / m_tile rounded up to 32), and no more."""
+    for K in (most - 1, most):
+        x = make(M, 136, K, seed=M)
+        assert_same(w8.int8_matmul(*x, "fp32", variant=w8.W8A8_VARIANT_SWAPAB, **opts), reference(*x, "fp32"))
+    x = make(M, 136, most + 1, seed=M)
+    with pytest.raises(w8.W8A8Error) as e:
+        w8.int8_matmul(*x, variant=w8.W8A8_VARIANT_SWAPAB, **opts)
+    assert e.value.status == w8.W8A8_ERR_UNSUPPORTED
+    assert_same(w8.int8_matmul(*x, "fp32"), reference(*x, "fp32"))
+
+
 def test_every_unit_of_a_large_sum_counts():
     """Sums around 2^23 whose last units differ, read through scales of one."""
     K = 1024
