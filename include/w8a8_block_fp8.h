@@ -476,7 +476,8 @@ w8a8_status w8a8_block_fp8_grouped_matmul_ragged(const void *A_dev, const float 
  * b_s, and cast (each rounded to nearest even).
  * Workspace (none for few tokens): w8a8_int8_workspace_size() bytes from
  * opts->workspace_dev, or the library's for this stream, under the rules of the
- * split-K workspace.
+ * split-K workspace: both operands as fp16, of A at most 512 MB at a time (longer
+ * ones in pieces of rows), of B all N rows (2 N K bytes, K up to whole 128).
  * opts: variant AUTO, SMALLM (few tokens), SWAPAB (some hundred), TILED (128 x 128
  * tiles) or TILED_PAIR (CTA pairs, 256 x 256), all with the same bits, the first two
  * without workspace.  SWAPAB takes m_tile (tokens per tile) and split_k (CTAs of a

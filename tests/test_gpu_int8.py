@@ -142,6 +142,20 @@ def test_no_columns_gives_zeros_and_no_rows_nothing():
     assert w8.int8_matmul(z(0, 8), torch.ones(0, device="cuda"), z(5, 8), torch.ones(5, device="cuda")).shape == (0, 5)
 
 
+@pytest.mark.parametrize("variant", [w8.W8A8_VARIANT_TILED, w8.W8A8_VARIANT_TILED_PAIR])
+def test_more_rows_than_the_workspace_holds(variant):
+    """A's rows go through the workspace in pieces (2048 rows of this K), the last one short."""
+    M, N, K = 4123, 136, 131000
+    A, a_s, B, b_s = make(M, N, K, seed=31)
+    assert w8.w8a8_int8_workspace_size(M, N, K) == w8.w8a8_int8_workspace_size(2 * M, N, K)
+    want = torch.cat([reference(A[i:i + 1000], a_s[i:i + 1000], B, b_s, "fp32") for i in range(0, M, 1000)])
+    for pad in (0, 3):          # rows of C on 16-byte boundaries, and not
+        wide = torch.full((M + 1, N + pad), 7.0, device="cuda")
+        C = w8.int8_matmul(A, a_s, B, b_s, "fp32", out=wide[:M, :N], variant=variant)
+        assert_same(C, want)
+        assert (wide[M] == 7).all() and (wide[:, N:] == 7).all()
+
+
 def test_callers_workspace_and_capture():
     x = make(200, 300, 700, seed=4)
     need = w8.w8a8_int8_workspace_size(200, 300, 700)
