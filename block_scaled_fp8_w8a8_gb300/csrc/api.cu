@@ -807,13 +807,13 @@ w8a8_status run_generic(const void *A, const float *a_s, const void *B, const fl
 // counter block that every workspace starts with, the widened A rows, B.
 constexpr int64_t kInt8ChunkBytes = 512ll << 20;
 // Up to this many tokens AUTO takes the kernel that widens in registers (N = K =
-// 4096: 6.9 against 10.1 us at M = 16, 10.3 against 11.2 at M = 32, 21 against 12.5
+// 4096: 5.6 against 8.7 us at M = 16, 8.8 against 9.3 at M = 32, 13.0 against 10.1
 // at M = 48, for it and for the one that widens on the way to shared memory).
 constexpr int64_t kInt8SmallM = 32;
 
 // The kernel of an INT8 call: by the caller's variant, else by M and, above
-// kInt8SmallM, by the kernels' estimated times (N = K = 4096: SWAPAB 12 / 22 / 43
-// us and TILED 25 / 25 / 26 us at M = 64 / 256 / 512, TILED_PAIR 35 and TILED 40 us
+// kInt8SmallM, by the kernels' estimated times (N = K = 4096: SWAPAB 10.5 / 21 / 41
+// us and TILED 24 / 25 / 26 us at M = 64 / 256 / 512, TILED_PAIR 34 and TILED 40 us
 // at M = 1024).  tile and splits are SWAPAB's.
 int int8_variant(int64_t M, int64_t N, int64_t K, const w8a8_options *o, int sm_count, int *tile,
                  int *splits)
@@ -1050,9 +1050,12 @@ w8a8_status run_ragged(const void *A, const float *a_s, const void *B, const flo
     // Tiles of 32 rows where experts have few rows on average and either K is long
     // enough for its groups to outweigh the launch, or the items fill the GPU several
     // times over.  Measured, 32-row / 128-row tiles: 8 rows of 256 experts, 1536 x
-    // 4096, 14.9 / 15.7 us; 512 rows of 256, 186 / 190; 7 rows of 11, 160 x 3376, 6.9 /
+    // 4096, 15.6 / 15.8 us; 512 rows of 256, 186 / 190; 7 rows of 11, 160 x 3376, 6.9 /
     // 12.4; 128 rows of 8, 1536 x 4096, 14.6 / 15.7; 59 rows of 104, 2320 x 576, 17.5 / 21.3;
     // but 256 rows of 8, 1536 x 4096, 20.5 / 16.0; 102 rows of 7, 1104 x 880, 7.6 / 6.8.
+    // The average misjudges a routing whose rows are mostly one expert's, which the host
+    // does not see: 6000 rows of 256 experts, 1536 x 4096, 254 / 259 us where no expert has
+    // more than 24, but 333 / 266 where one has 4980.
     const int64_t most = std::min<int64_t>(gr.experts, M);
     const bool thin = (G >= 9 && M <= 24 * most) ||
                       (G >= 5 && M <= 16 * most && (most + M / 32) * cdiv(N, 128) >= 4 * info.sm_count);
@@ -1067,7 +1070,7 @@ w8a8_status run_ragged(const void *A, const float *a_s, const void *B, const flo
         // and its stores (a group of 128 x 128 / 128 x 256 takes some 700 / 1130
         // cycles, or what its weights take to arrive).  Measured, 128 / 256: 5 rows
         // of 45 experts, 712 x 1264, 7.8 / 9.9 us; 792 rows of 28, 656 x 784, 10.6 / 9.1;
-        // 2876 rows of 10, 952 x 2368, 19.8 / 16.1; 16384 rows of 64, 4096 x 4096, 397 / 325.
+        // 2876 rows of 10, 952 x 2368, 19.8 / 16.1; 16384 rows of 64, 4096 x 4096, 404 / 328.
         const double spread = gr.experts * (1.0 - std::exp(-static_cast<double>(M) / gr.experts));
         const int64_t likely = static_cast<int64_t>(spread) + M / 128 + 1;
         auto cycles = [&](int64_t width, int64_t group, int64_t store) {
@@ -1537,8 +1540,6 @@ int64_t host_chunk_rows(int64_t M, int64_t N, int64_t K, size_t ob, const w8a8_o
 }  // namespace
 
 namespace w8a8 {
-// Lets other translation units of the library report an error through
-// w8a8_last_error(); returns `st`.
 int device_view(DeviceView *out)
 {
     w8a8_options scratch;
@@ -1555,6 +1556,8 @@ int device_view(DeviceView *out)
     return W8A8_OK;
 }
 
+// Lets other translation units of the library report an error through
+// w8a8_last_error(); returns `st`.
 w8a8_status record_error(w8a8_status st, const char *message)
 {
     return fail(st, "%s", message);

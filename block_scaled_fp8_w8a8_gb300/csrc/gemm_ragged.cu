@@ -17,9 +17,10 @@
 // (gemm_ragged_few.cu) takes over.
 // Bound by the promotion out of tensor memory, some 1130 cycles per 128 x 256 group
 // against the MMA's 512, and by the padding of the experts' last tiles: 16384 rows
-// of 64 experts, 4096 x 4096 (a quarter of the tiles' rows padding), 321 us, 1.72
-// PFLOP/s; 128-column tiles take 397.  1013 rows of 16 experts, 520 x 1088: 7.4 us, the
-// latency of launch, offsets and nine groups.
+// of 64 experts, 4096 x 4096 (a quarter of the tiles' rows padding), 328 us, 1.68
+// PFLOP/s, as captured calls (324 to 334 by the clock that the power cap leaves; 370
+// called in a loop); 128-column tiles take 404.  1013 rows of 16 experts, 520 x 1088:
+// 7.4 us, the latency of launch, offsets and nine groups in series.
 //
 // Roles per CTA, promotion and scale ring are those of the tiled kernel (see
 // gemm_tiled.cu): warp 0 TMA producer, warps 1 and 3 MMA issuers, warp 2 scale

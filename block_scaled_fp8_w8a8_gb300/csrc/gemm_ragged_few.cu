@@ -14,10 +14,10 @@
 // shared memory.
 //
 // Bound by the weights' bytes where the items fill the GPU (512 rows of 256 experts,
-// 1536 x 4096: 186 us, 6.9 TB/s); otherwise by the latency of launch, offsets, first
+// 1536 x 4096: 186 to 190 us, 6.8 TB/s); otherwise by the latency of launch, offsets, first
 // loads and the cluster's sum, some 7 us, and by what a K group takes to pass from
 // load to promotion in one CTA, some 600 cycles (8 rows of 256 experts, 1536 x 4096,
-// split over two CTAs: 14.9 us; unsplit 17.3).
+// split over two CTAs: 14.6 to 15.6 us; unsplit 17.3).
 //
 // Roles: warps 0 and 3 TMA producers, warp 1 MMA issuer, warp 2 scale loader, warps 4..7
 // promotion (a thread owns one weight row, the partial's columns are rows of A).

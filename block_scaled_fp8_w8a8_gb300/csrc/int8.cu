@@ -151,8 +151,11 @@ __global__ void __launch_bounds__(kWidenThreads) k_int8_widen(const Int8WidenPar
 // shared memory, where the order of integer additions does not matter.
 // Bound by the latency of a launch and of the loads: two batches of loads a
 // thread, 32 KB a CTA, stay in flight.  One token by 4096 x 4096: 4.05 us (4.1
-// TB/s; with a single batch 5.4), by 8192 x 16384: 28.6 us (4.7 TB/s).
-// Batches of 4 steps gave 4.6 and 26.4 us where these took 4.25 and 28.7.
+// TB/s; at the lower clock that a long prefill leaves behind it 4.65; with a single
+// batch 5.4), by 8192 x 16384: 28.0 us (4.8 TB/s).
+// Batches of 4 steps gave 4.6 and 26.4 us where these took 4.25 and 28.7.  (The form of
+// 17 to 32 tokens spills some 50 bytes at the 128 registers of two CTAs per SM, and with
+// narrower loads 24 to 172.)
 constexpr int kSmallWarps = 8, kSmallCtas = 2;       // CTAs per SM
 
 __device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -402,7 +405,7 @@ cudaError_t launch_small_t(const Int8SmallParams &p, int access, int sm_count, c
 // Bound by shared memory: a step's 24 KB (of 128 + 64 rows) to 48 KB (128 + 256)
 // are written once and read once by the MMA; where CTAs have few steps, by the
 // latency of launch, first loads and the cluster's sum.  256 tokens by 4096 x
-// 4096: 20.7 us (the widening launch and k_int8_mma: 24.6), 512: 41.0 (26.1); 257 by
+// 4096: 20.7 us (the widening launch and k_int8_mma: 24.7), 512: 41.0 (26.2); 257 by
 // 1537 x 1000, rows off 16-byte boundaries: 8.6.
 constexpr int kMidGroup = 8;
 constexpr int kMidGroups = 2;
@@ -740,7 +743,7 @@ __device__ __forceinline__ void int8_tile_coords(int t, int num_m, int num_n, in
 // per-group scales: warp 0 TMA producer, warp 1 MMA issuer (the odd CTA's:
 // forwarder of its landed stages), warps 4.. integer promotion and epilogue.
 // Bound by the tensor cores under the power cap: 16384 x 4096 x 4096 with the
-// widening launch takes 341 us, without it about 300, 1.83 PFLOP/s (one-CTA tiles: 432).
+// widening launch takes 340 us, without it about 300, 1.83 PFLOP/s (one-CTA tiles: 433).
 template <bool PAIR, int BN, int STAGES, int CPW, int EB>
 __global__ void __launch_bounds__(Int8Layout<PAIR, BN, STAGES, CPW, EB>::kThreads, 1)
     k_int8_mma(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -959,7 +962,7 @@ __global__ void __launch_bounds__(Int8Layout<PAIR, BN, STAGES, CPW, EB>::kThread
     } else {
         // -------------------------------------------------------------- promotion + epilogue
         regs_alloc<L::kRegsHigh>();
-        const uint32_t w = warp_index();       // (not the uniform copy: it costs spills here)
+        const uint32_t w = warp_index();       // (the uniform copy costs more spills; these are 28 bytes)
         const int h = static_cast<int>(w / 4) - 1;
         const uint32_t q = w & 3u;
         const uint32_t epi_buf = sEpi + (w - 4u) * 2048u * EB;

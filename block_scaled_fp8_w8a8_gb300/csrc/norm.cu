@@ -255,7 +255,8 @@ __device__ __forceinline__ void store_fp8(const NormParams &p, long long m, uint
 // at most kEarlyThreads, whose registers also hold the weights and the gate,
 // loaded along with the row.
 // Bound by the latency of the loads and of two reductions over the CTA: one row of
-// 4096 in bf16 2.6 us (back to back), 64 rows to FP8 3.5 us.
+// 4096 in bf16 2.6 us (back to back), 64 rows to FP8 or INT8 3.5 us.  (Beyond 8192
+// columns, at 64 registers a thread, single elements (VEC 1) spill some 320 bytes.)
 constexpr int kEarlyThreads = 512;
 template <int HK, int XK, int VEC, bool HELD, bool EARLY>
 __global__ void __launch_bounds__(EARLY ? kEarlyThreads : kMaxThreads)
@@ -434,8 +435,8 @@ __global__ void __launch_bounds__(EARLY ? kEarlyThreads : kMaxThreads)
 // while the gate's row lasts).  The rows of h and x come through a ring of
 // shared-memory stages filled by bulk copies, so that the next rows' loads are in
 // flight through a row's two reductions.
-// HBM-bound: 16384 x 4096 in bf16 with FP8 codes 79.7 us (5.9 TB/s), with bf16 94.4 us
-// (5.7 TB/s).
+// HBM-bound: 16384 x 4096 in bf16 with FP8 codes 79.7 us (5.9 TB/s), with INT8 codes 84.2
+// us (5.6 TB/s; a third reduction per row), with bf16 94.0 us (5.7 TB/s).
 constexpr int kRingMaxStages = 4;
 constexpr int kRingThreads = 512;
 
@@ -801,7 +802,8 @@ __global__ void __launch_bounds__(THREADS, PER_SM) k_sandwich_ring(const RingPar
 // elements reads them without bank conflicts.  The next row's words wait in
 // registers while this one's reductions run.
 // Bound by instruction issue and the two reductions per row: 8192 rows of 1537 in
-// fp16 26.4 us (3.8 TB/s), 16384 of 3943 in bf16 103 us (5.0 TB/s).
+// fp16 25.5 us (3.9 TB/s), 16384 of 3943 in bf16 104 us (5.0 TB/s).  (1024 threads, at 64
+// registers each, spill 170 to 290 bytes.)
 struct FlatParams {
     NormParams n;
     float inv_d;
@@ -1044,7 +1046,7 @@ struct QuantParams {
 };
 
 // HELD: the row stays in registers; otherwise it is read twice.
-// 16384 x 4096 in bf16: 43.0 us (4.7 TB/s), with 60 % of the issue slots taken, most by
+// 16384 x 4096 in bf16: 43.3 us (4.6 TB/s), with 60 % of the issue slots taken, most by
 // the correctly rounded quotients.
 template <int KIND, int VEC, bool HELD>
 __global__ void __launch_bounds__(kMaxThreads) k_quant_int8(const QuantParams p)
