@@ -29,6 +29,9 @@ from ._binding import (  # noqa: F401
     w8a8_block_fp8_grouped_matmul_ragged, W8A8_RAGGED_MAX_EXPERTS,
     w8a8_int8_matmul, w8a8_int8_workspace_size, W8A8_INT8_MAX_K, w8a8_quantize_int8_per_token,
     w8a8_sandwich_norm, W8A8_NORM_SAME, W8A8_NORM_FP8, W8A8_NORM_INT8, W8A8_NORM_MAX_D,
+    w8a8_route_experts, w8a8_route_workspace_size, W8A8_SCORE_SOFTMAX, W8A8_SCORE_SIGMOID,
+    w8a8_group_rows, w8a8_group_workspace_size, W8A8_GROUPS_MAX, W8A8_ROUTE_MAX_K,
+    W8A8_ROUTE_MAX_GROUPS, w8a8_combine_experts, w8a8_adapter_matmul, W8A8_ADAPTER_MAX_R,
     w8a8_launch_floor_kernel, w8a8_block_fp8_quant_matmul,
     w8a8_block_fp8_quant_matmul_workspace_size,
     w8a8_get_device_status, w8a8_last_error, w8a8_options, w8a8_shutdown, w8a8_status_string,
@@ -199,6 +202,8 @@ class _Dtypes:
         self.e4m3 = (torch.float8_e4m3fn, torch.uint8)
         self.out = {W8A8_OUT_BF16: torch.bfloat16, W8A8_OUT_FP16: torch.float16,
                     W8A8_OUT_FP32: torch.float32}
+        self.u8, self.bool = torch.uint8, torch.bool
+        self.routing = (self.i32, self.f32, self.bool, self.u8)        # see pycall.c
         self.fast = (self.i8, self.f32, *(self.out[c] for c in sorted(self.out)))   # see pycall.c
 
 
@@ -476,3 +481,222 @@ def sandwich_norm(h, x, w_post=None, w_pre=None, gate=None, gate_rows=None, res_
     if st:
         check(st)
     return (x_out, y_out) if not kind else (x_out, y_out, scales_out)
+
+
+def _on_stream(stream):
+    """Where a call's own tensors are allocated: on the stream that uses them, so that
+    their memory is not handed on before it has passed the call."""
+    import contextlib
+
+    import torch
+    if stream is None or not torch.cuda.is_available():
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
+def _here(t, *others):
+    """Refuse tensors that are not all on the current GPU, whose stream the call takes."""
+    _one_gpu(t, *others)
+    if t.get_device() >= 0:
+        import torch
+        if t.get_device() != torch.cuda.current_device():
+            raise W8A8Error(W8A8_ERR_INVALID_ARG, f"tensors on {t.device}, which is not the current device")
+
+
+def _given(t, shape, dtype, name):
+    """Refuse a tensor that is not dense, of this shape and type."""
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
+        _want(t, shape, name)
+        _typed(t, (dtype,), name)
+        _dense(t, name)
+
+
+def _outputs(out, specs, device):
+    """The caller's output tensors, checked, or new ones: specs of (name, shape, dtype)."""
+    if out is None:
+        import torch
+        return tuple(torch.empty(shape, dtype=dtype, device=device) for _, shape, dtype in specs)
+    if len(out) != len(specs):
+        raise W8A8Error(W8A8_ERR_INVALID_ARG, f"out has {len(out)} tensors, want {len(specs)}")
+    for t, (name, shape, dtype) in zip(out, specs):
+        _given(t, shape, dtype, name)
+    return tuple(out)
+
+
+def _workspace(size, device):
+    """(tensor, address) of device scratch; the tensor lives to the end of the call."""
+    if not size:
+        return None, None
+    import torch
+    t = torch.empty(size, dtype=torch.uint8, device=device)
+    return t, t.data_ptr()
+
+
+_SCORES = {"softmax": W8A8_SCORE_SOFTMAX, "sigmoid": W8A8_SCORE_SIGMOID}
+
+
+def route_experts(logits, top_k, scoring="softmax", bias=None, groups=1, top_groups=1, group_top=2,
+                  renormalize=True, scale=1.0, valid=None, out=None, stream=None):
+    """Each token's experts and their weights, and the (token, choice) pairs in the experts'
+    order, on CUDA tensors.
+
+    logits bf16, fp16 or fp32 [T, E]; scores are their softmax or sigmoid, and with bias
+    (float32 [E]) added they rank the experts; of the ``groups`` runs of neighbouring experts
+    the ``top_groups`` with the largest sums of their ``group_top`` (1 or 2) best are open.
+    Weights are scale * the top_k chosen experts' scores (without the bias), divided by
+    their sum with ``renormalize``.  ``valid`` (bool or uint8 [T]): False for padding, whose
+    tokens get no expert.  Returns (ids int32 [T, top_k], weights float32 [T, top_k],
+    order int32 [T * top_k], offsets int32 [E + 1], rows int32 [T, top_k]): grouped_matmul_ragged
+    takes rows order // top_k of the activations by offsets, combine_experts takes rows and
+    weights.  ``out``: those five, preallocated.  Raises W8A8Error on a non-zero status."""
+    lib, types = load_library(), _dtypes or _load_dtypes()
+    code = _SCORES.get(scoring)
+    if code is None:
+        raise W8A8Error(W8A8_ERR_INVALID_ARG, f"scoring {scoring!r}: want 'softmax' or 'sigmoid'")
+    if out is not None and lib.route_tensors is not None:
+        st = lib.route_tensors(logits, top_k, code, bias, groups, top_groups, group_top, renormalize, scale, valid,
+                               out, _in_codes, types.routing, stream if stream is None else _stream(stream))
+        if st == 0:
+            return out
+        if st is not None:
+            check(st)
+    if logits.dim() != 2:
+        raise W8A8Error(W8A8_ERR_INVALID_ARG, f"logits must be [tokens, experts], not {list(logits.shape)}")
+    T, E = logits.shape
+    kind = _in_codes[logits.dtype]
+    if not isinstance(top_k, int) or top_k < 1 or top_k > W8A8_ROUTE_MAX_K:
+        raise W8A8Error(W8A8_ERR_INVALID_ARG, f"top_k of {top_k}: want 1 to {W8A8_ROUTE_MAX_K}")
+    if bias is not None:
+        _given(bias, (E,), types.f32, "bias")
+    if valid is not None:
+        _typed(valid, (types.bool, types.u8), "valid")
+        _given(valid, (T,), valid.dtype, "valid")
+    ld = _rows(logits)
+    with _on_stream(stream):
+        outs = _outputs(out, (("ids", (T, top_k), types.i32), ("weights", (T, top_k), types.f32),
+                              ("order", (T * top_k,), types.i32), ("offsets", (E + 1,), types.i32),
+                              ("rows", (T, top_k), types.i32)), logits.device)
+        _here(logits, bias, valid, *outs)
+        size = lib.w8a8_route_workspace_size(T, E, top_k)
+        keep, scratch = _workspace(size, logits.device)
+    st = lib.w8a8_route_experts(
+        logits.data_ptr(), kind, ld, None if bias is None else bias.data_ptr(),
+        None if valid is None else valid.data_ptr(), T, E, top_k, code, groups, top_groups, group_top,
+        1 if renormalize else 0, scale, *(t.data_ptr() for t in outs), scratch, size, _stream(stream))
+    if st:
+        check(st)
+    return outs
+
+
+def group_rows(ids, groups, out=None, stream=None):
+    """The places of ``ids`` (int32 CUDA tensor of n values, of any dense shape) sorted by
+    value, stable: returns (order int32 [n], offsets int32 [groups + 1]): group g's are
+    order[offsets[g]] .. order[offsets[g + 1] - 1], and those of no group (values outside
+    0 .. groups - 1) come last.  ``out``: both, preallocated."""
+    lib, types = load_library(), _dtypes or _load_dtypes()
+    if out is not None and lib.group_tensors is not None:
+        st = lib.group_tensors(ids, groups, out, types.routing, stream if stream is None else _stream(stream))
+        if st == 0:
+            return out
+        if st is not None:
+            check(st)
+    n = ids.numel()
+    _given(ids, ids.shape, types.i32, "ids")
+    with _on_stream(stream):
+        outs = _outputs(out, (("order", (n,), types.i32), ("offsets", (max(groups, 0) + 1,), types.i32)), ids.device)
+        _here(ids, *outs)
+        size = lib.w8a8_group_workspace_size(n, groups)
+        keep, scratch = _workspace(size, ids.device)
+    st = lib.w8a8_group_rows(ids.data_ptr(), n, groups, outs[0].data_ptr(), outs[1].data_ptr(), None, scratch, size,
+                             _stream(stream))
+    if st:
+        check(st)
+    return outs
+
+
+def combine_experts(Y, rows, weights, add=None, out_dtype=None, out=None, stream=None):
+    """out[t] = add[t] + sum_j weights[t, j] * Y[rows[t, j]] on CUDA tensors: Y [M, D] bf16, fp16
+    or fp32 in the experts' order, rows int32 and weights float32 [T, k] from route_experts;
+    rows outside Y (-1) are left out.  add [T, D] of the output's type, which is Y's or fp32
+    (``out_dtype``, or ``out``'s); ``out`` may be ``add``.  Raises W8A8Error on a non-zero
+    status."""
+    lib, types = load_library(), _dtypes or _load_dtypes()
+    if out is not None and out_dtype is None and lib.combine_tensors is not None:
+        st = lib.combine_tensors(Y, rows, weights, add, out, _in_codes, types.routing,
+                                 stream if stream is None else _stream(stream))
+        if st == 0:
+            return out
+        if st is not None:
+            check(st)
+    if Y.dim() != 2 or rows.dim() != 2:
+        raise W8A8Error(W8A8_ERR_INVALID_ARG, f"Y must be [rows, columns] and rows [tokens, choices], not "
+                                              f"{list(Y.shape)} and {list(rows.shape)}")
+    (M, D), (T, k) = Y.shape, rows.shape
+    kind = _in_codes[Y.dtype]
+    _given(rows, (T, k), types.i32, "rows")
+    _given(weights, (T, k), types.f32, "weights")
+    dtype = types.out[out_code(out_dtype)] if out_dtype is not None else Y.dtype if out is None else out.dtype
+    with _on_stream(stream):
+        if out is None:
+            import torch
+            out = torch.empty((T, D), dtype=dtype, device=Y.device)
+        _want(out, (T, D), "out")
+        _typed(out, (dtype,), "out")
+        if add is not None:
+            _want(add, (T, D), "add")
+            _typed(add, (dtype,), "add")
+        ld_y, ld_out, ld_add = _rows(Y), _rows(out), 0 if add is None else _rows(add)
+        _here(Y, rows, weights, add, out)
+    st = lib.w8a8_combine_experts(Y.data_ptr(), kind, ld_y, M, rows.data_ptr(), weights.data_ptr(),
+                                  None if add is None else add.data_ptr(), ld_add, out.data_ptr(), _in_codes[dtype],
+                                  ld_out, T, k, D, _stream(stream))
+    if st:
+        check(st)
+    return out
+
+
+def adapter_matmul(x, A, B, order, offsets, base, scales=None, out=None, stream=None):
+    """out[t] = base[t] + scales[l] * (x[t] A[l]^T) B[l]^T on CUDA tensors, l the adapter of row
+    t: low-rank adapters of many requests beside the projection that made ``base``.
+
+    x [T, K] bf16 or fp16; A [L, r, K] and B [L, N, r] of its type; order int32 [T] and
+    offsets int32 [L + 1] from group_rows(the rows' adapters, L); base [T, N] of x's type or
+    fp32; scales float32 [L] (None: 1).  Rows without an adapter are base's.  ``out`` may be
+    ``base``, whose rows without an adapter are then not touched.  Raises W8A8Error on a
+    non-zero status."""
+    lib, types = load_library(), _dtypes or _load_dtypes()
+    if out is not None and lib.adapter_tensors is not None:
+        st = lib.adapter_tensors(x, A, B, order, offsets, base, scales, out, _in_codes, types.routing,
+                                 stream if stream is None else _stream(stream))
+        if st == 0:
+            return out
+        if st is not None:
+            check(st)
+    if x.dim() != 2 or A.dim() != 3 or B.dim() != 3:
+        raise W8A8Error(W8A8_ERR_INVALID_ARG, "x must be [rows, K], A [adapters, r, K] and B [adapters, N, r]")
+    T, K = x.shape
+    L, r, _ = A.shape
+    N = B.shape[1]
+    kind = _in_codes[x.dtype]
+    _given(A, (L, r, K), x.dtype, "A")
+    _given(B, (L, N, r), x.dtype, "B")
+    _given(order, (T,), types.i32, "order")
+    _given(offsets, (L + 1,), types.i32, "offsets")
+    if scales is not None:
+        _given(scales, (L,), types.f32, "scales")
+    _want(base, (T, N), "base")
+    with _on_stream(stream):
+        if out is None:
+            import torch
+            out = torch.empty((T, N), dtype=base.dtype, device=base.device)
+        _want(out, (T, N), "out")
+        _typed(out, (base.dtype,), "out")
+        ld_x, ld_base, ld_out = _rows(x), _rows(base), _rows(out)
+        _here(x, A, B, order, offsets, base, scales, out)
+    st = lib.w8a8_adapter_matmul(x.data_ptr(), kind, ld_x, A.data_ptr(), B.data_ptr(), order.data_ptr(),
+                                 offsets.data_ptr(), None if scales is None else scales.data_ptr(), base.data_ptr(),
+                                 ld_base, out.data_ptr(), _in_codes[base.dtype], ld_out, T, L, r, K, N,
+                                 _stream(stream))
+    if st:
+        check(st)
+    return out

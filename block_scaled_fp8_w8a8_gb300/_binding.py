@@ -45,6 +45,12 @@ EXPORTED = (
     "w8a8_int8_workspace_size",
     "w8a8_quantize_int8_per_token",
     "w8a8_sandwich_norm",
+    "w8a8_route_experts",
+    "w8a8_route_workspace_size",
+    "w8a8_group_rows",
+    "w8a8_group_workspace_size",
+    "w8a8_combine_experts",
+    "w8a8_adapter_matmul",
     "w8a8_quantize_fp8_per_token_group",
     "w8a8_launch_floor_kernel",
     "w8a8_block_fp8_quant_matmul",
@@ -109,6 +115,12 @@ _PYCALL = ("w8a8_sandwich_norm", "w8a8_block_fp8_grouped_matmul_ragged", "w8a8_i
            "w8a8_quantize_int8_per_token")
 
 
+# Those that its entries on tensors call beside them, in bind_routing()'s order.
+_PYCALL_ROUTING = ("w8a8_route_experts", "w8a8_route_workspace_size", "w8a8_group_rows",
+                   "w8a8_group_workspace_size", "w8a8_combine_experts", "w8a8_adapter_matmul")
+_ROUTING_TENSORS = ("route_tensors", "group_tensors", "combine_tensors", "adapter_tensors")
+
+
 _pycall = None   # the module, once bound
 
 
@@ -117,6 +129,8 @@ def _bind_pycall(lib):
     module where it has been built; they take the same arguments."""
     global _pycall
     lib.norm_tensors = lib.int8_tensors = lib.quant_tensors = None
+    for n in _ROUTING_TENSORS:
+        setattr(lib, n, None)
     path = _build.pycall_path()
     if not os.path.exists(path):
         return
@@ -124,6 +138,7 @@ def _bind_pycall(lib):
     mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_w8a8_pycall", loader))
     loader.exec_module(mod)
     mod.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _PYCALL))
+    mod.bind_routing(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _PYCALL_ROUTING))
     for n in _PYCALL:
         setattr(lib, n, getattr(mod, n))
     _pycall = mod
@@ -131,7 +146,7 @@ def _bind_pycall(lib):
         import torch
         mod.bind_torch(torch.Tensor, *_current)
     # the plain case of the Python calls, on tensors (see pycall.c)
-    for n in ("norm_tensors", "int8_tensors", "quant_tensors"):
+    for n in ("norm_tensors", "int8_tensors", "quant_tensors", *_ROUTING_TENSORS):
         setattr(lib, n, getattr(mod, n))
 
 
@@ -174,6 +189,20 @@ def load_library():
     f32 = ctypes.c_float
     lib.w8a8_sandwich_norm.argtypes = [vp, i32, i64, vp, i32, i64, vp, vp, i64, vp, f32, f32, vp,
                                        i64, vp, vp, i32, i64, i64, i64, vp]
+    lib.w8a8_route_experts.argtypes = [vp, i32, i64, vp, vp, i64, i64, i32, i32, i32, i32, i32, i32,
+                                       f32, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.w8a8_route_workspace_size.argtypes = [i64, i64, i32]
+    lib.w8a8_group_rows.argtypes = [vp, i64, i64, vp, vp, vp, vp, sz, vp]
+    lib.w8a8_group_workspace_size.argtypes = [i64, i64]
+    lib.w8a8_combine_experts.argtypes = [vp, i32, i64, i64, vp, vp, vp, i64, vp, i32, i64, i64, i64,
+                                         i64, vp]
+    lib.w8a8_adapter_matmul.argtypes = [vp, i32, i64, vp, vp, vp, vp, vp, vp, i64, vp, i32, i64, i64,
+                                        i64, i64, i64, i64, vp]
+    for name in ("w8a8_route_workspace_size", "w8a8_group_workspace_size"):
+        getattr(lib, name).restype = sz
+    for name in ("w8a8_route_experts", "w8a8_group_rows", "w8a8_combine_experts",
+                 "w8a8_adapter_matmul"):
+        getattr(lib, name).restype = ctypes.c_int
     lib.w8a8_block_fp8_quant_matmul.argtypes = [vp, i32, vp, vp, vp, i64, i64, i64, i32, i32, i32,
                                                 vp, opt_p]
     lib.w8a8_block_fp8_quant_matmul.restype = ctypes.c_int
@@ -364,6 +393,51 @@ def w8a8_sandwich_norm(h, h_dtype, ld_h, x, x_dtype, ld_x, w_post, gate, gate_ro
         _ptr(h), h_dtype, ld_h, _ptr(x), x_dtype, ld_x, _ptr(w_post), _ptr(gate), gate_rows,
         _ptr(w_pre), res_scale, eps, _ptr(x_out), ld_xo, _ptr(y), _ptr(scales), y_kind, ld_y, M, D,
         _stream(stream))
+
+
+W8A8_GROUPS_MAX = 1024
+W8A8_ROUTE_MAX_K = 32
+W8A8_ROUTE_MAX_GROUPS = 32
+W8A8_ADAPTER_MAX_R = 256
+W8A8_SCORE_SOFTMAX, W8A8_SCORE_SIGMOID = 0, 1
+
+
+def w8a8_route_experts(logits, dtype, ld, bias, valid, T, E, top_k, scoring, groups, top_groups,
+                       group_top, renormalize, scale, ids, weights, order, offsets, rows,
+                       workspace=None, workspace_bytes=0, stream=None) -> int:
+    return load_library().w8a8_route_experts(
+        _ptr(logits), dtype, ld, _ptr(bias), _ptr(valid), T, E, top_k, scoring, groups, top_groups,
+        group_top, renormalize, scale, _ptr(ids), _ptr(weights), _ptr(order), _ptr(offsets),
+        _ptr(rows), _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def w8a8_route_workspace_size(T, E, top_k) -> int:
+    return load_library().w8a8_route_workspace_size(T, E, top_k)
+
+
+def w8a8_group_rows(ids, n, groups, order, offsets, rows=None, workspace=None, workspace_bytes=0,
+                    stream=None) -> int:
+    return load_library().w8a8_group_rows(_ptr(ids), n, groups, _ptr(order), _ptr(offsets),
+                                          _ptr(rows), _ptr(workspace), workspace_bytes,
+                                          _stream(stream))
+
+
+def w8a8_group_workspace_size(n, groups) -> int:
+    return load_library().w8a8_group_workspace_size(n, groups)
+
+
+def w8a8_combine_experts(Y, y_dtype, ld_y, M, rows, weights, add, ld_add, out, out_dtype, ld_out, T,
+                         k, D, stream=None) -> int:
+    return load_library().w8a8_combine_experts(
+        _ptr(Y), y_dtype, ld_y, M, _ptr(rows), _ptr(weights), _ptr(add), ld_add, _ptr(out),
+        out_dtype, ld_out, T, k, D, _stream(stream))
+
+
+def w8a8_adapter_matmul(x, dtype, ld_x, A, B, order, offsets, scales, base, ld_base, out, out_dtype,
+                        ld_out, T, L, r, K, N, stream=None) -> int:
+    return load_library().w8a8_adapter_matmul(
+        _ptr(x), dtype, ld_x, _ptr(A), _ptr(B), _ptr(order), _ptr(offsets), _ptr(scales),
+        _ptr(base), ld_base, _ptr(out), out_dtype, ld_out, T, L, r, K, N, _stream(stream))
 
 
 def w8a8_launch_floor_kernel(pdl=1, stream=None) -> int:

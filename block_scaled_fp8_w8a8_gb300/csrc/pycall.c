@@ -20,10 +20,30 @@ typedef int (*int8_fn)(const void *, int64_t, const float *, const void *, int64
 typedef int (*quant_fn)(const void *, int, int64_t, void *, int64_t, float *, int64_t, int64_t,
                         stream_t);
 
+typedef int (*route_fn)(const void *, int, int64_t, const float *, const uint8_t *, int64_t, int64_t,
+                        int, int, int, int, int, int, float, int32_t *, float *, int32_t *,
+                        int32_t *, int32_t *, void *, size_t, stream_t);
+typedef size_t (*route_size_fn)(int64_t, int64_t, int);
+typedef int (*group_fn)(const int32_t *, int64_t, int64_t, int32_t *, int32_t *, int32_t *, void *,
+                        size_t, stream_t);
+typedef size_t (*group_size_fn)(int64_t, int64_t);
+typedef int (*combine_fn)(const void *, int, int64_t, int64_t, const int32_t *, const float *,
+                          const void *, int64_t, void *, int, int64_t, int64_t, int64_t, int64_t,
+                          stream_t);
+typedef int (*adapter_fn)(const void *, int, int64_t, const void *, const void *, const int32_t *,
+                          const int32_t *, const float *, const void *, int64_t, void *, int,
+                          int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, stream_t);
+
 static norm_fn f_norm;
 static ragged_fn f_ragged;
 static int8_fn f_int8;
 static quant_fn f_quant;
+static route_fn f_route;
+static route_size_fn f_route_size;
+static group_fn f_group;
+static group_size_fn f_group_size;
+static combine_fn f_combine;
+static adapter_fn f_adapter;
 
 /* Argument i as an integer; None is 0.  Sets an error for anything else. */
 static int64_t num(PyObject *const *args, int i)
@@ -130,9 +150,10 @@ static PyObject *py_quant(PyObject *self, PyObject *const *args, Py_ssize_t n)
  * takes Python code 2 us, as long as the launch, and half as long here.  These entries
  * only take the plain case: every output given, every tensor dense.  Anything else,
  * what is to be refused included, is None: the Python code looks at it. */
+enum { DIMS = 3 };
 typedef struct {
     void *ptr;
-    int64_t size[2];
+    int64_t size[DIMS];
     int dims;
     PyObject *dtype;       /* borrowed: torch keeps its dtypes */
 } tensor_t;
@@ -184,12 +205,12 @@ static PyObject *py_one_gpu(PyObject *self, PyObject *const *args, Py_ssize_t n)
     return PyBool_FromLong(ok);
 }
 
-/* 1 for a dense tensor of one or two dimensions on the GPU *gpu (see on_gpu), else 0 (with
+/* 1 for a dense tensor of one to three dimensions on the GPU *gpu (see on_gpu), else 0 (with
  * or without an error set). */
 static int dense(PyObject *t, tensor_t *d, long *gpu)
 {
     PyObject *o = get(t, SHAPE);
-    int ok = o && PyTuple_Check(o) && PyTuple_GET_SIZE(o) >= 1 && PyTuple_GET_SIZE(o) <= 2;
+    int ok = o && PyTuple_Check(o) && PyTuple_GET_SIZE(o) >= 1 && PyTuple_GET_SIZE(o) <= DIMS;
     if (ok) {
         d->dims = (int)PyTuple_GET_SIZE(o);
         for (int i = 0; i < d->dims; ++i)
@@ -280,7 +301,7 @@ static PyObject *py_norm_tensors(PyObject *self, PyObject *const *args, Py_ssize
         pre = t.ptr;
     }
     if (args[4] != Py_None) {
-        if (!dense(args[4], &t, &gpu) || t.size[t.dims - 1] != D || t.dtype != h.dtype)
+        if (!dense(args[4], &t, &gpu) || t.dims > 2 || t.size[t.dims - 1] != D || t.dtype != h.dtype)
             goto other;
         const int64_t rows = t.dims == 2 ? t.size[0] : 1;
         if (args[5] != Py_None)
@@ -366,6 +387,195 @@ static PyObject *py_quant_tensors(PyObject *self, PyObject *const *args, Py_ssiz
     Py_RETURN_NONE;
 }
 
+static int is3(const tensor_t *d, int64_t a, int64_t b, int64_t c)
+{
+    return d->dims == 3 && d->size[0] == a && d->size[1] == b && d->size[2] == c;
+}
+
+/* Whether the GPU is the current one, by torch's function that bind_torch got. */
+static int is_current(long gpu)
+{
+    PyObject *o = current_device ? PyObject_CallNoArgs(current_device) : NULL;
+    const int ok = o && PyLong_AsLong(o) == gpu;
+    Py_XDECREF(o);
+    return ok;
+}
+
+/* The types of the routing calls: int32, float32, bool, uint8. */
+enum { R_INT32, R_F32, R_BOOL, R_U8 };
+
+/* A dense tensor of `dims` dimensions and of that type */
+static int typed(PyObject *o, tensor_t *t, long *gpu, int dims, PyObject *dtype)
+{
+    return dtype && dense(o, t, gpu) && t->dims == dims && t->dtype == dtype;
+}
+
+static int code_of(PyObject *codes, PyObject *dtype)
+{
+    PyObject *o = PyDict_GetItemWithError(codes, dtype);
+    return o ? (int)PyLong_AsLong(o) : -1;
+}
+
+/* logits, top_k, scoring, bias, groups, top_groups, group_top, renormalize, scale, valid,
+ * outputs, the input types' codes by dtype, dtypes, stream */
+static PyObject *py_route_tensors(PyObject *self, PyObject *const *args, Py_ssize_t n)
+{
+    (void)self;
+    if (!want(n, 14, f_route != NULL))
+        return NULL;
+    tensor_t x, bias = {0}, valid = {0}, o[5];
+    long gpu = ANY_GPU;
+    PyObject *const i32 = type_at(args[12], R_INT32), *const f32 = type_at(args[12], R_F32);
+    if (!PyTuple_Check(args[10]) || PyTuple_GET_SIZE(args[10]) != 5 || !PyLong_Check(args[1]) ||
+        !dense(args[0], &x, &gpu) || x.dims != 2)
+        goto other;
+    const int64_t T = x.size[0], E = x.size[1], k = I64(1);
+    if (k < 1 || k > 32)
+        goto other;
+    if (args[3] != Py_None && (!typed(args[3], &bias, &gpu, 1, f32) || !is(&bias, 1, E, 0)))
+        goto other;
+    if (args[9] != Py_None && (!dense(args[9], &valid, &gpu) || !is(&valid, 1, T, 0) ||
+                               (valid.dtype != type_at(args[12], R_BOOL) && valid.dtype != type_at(args[12], R_U8))))
+        goto other;
+    for (int i = 0; i < 5; ++i) {
+        const int flat = i == 2 || i == 3;
+        if (!typed(PyTuple_GET_ITEM(args[10], i), &o[i], &gpu, flat ? 1 : 2, i == 1 ? f32 : i32) ||
+            !(flat ? is(&o[i], 1, i == 2 ? T * k : E + 1, 0) : is(&o[i], 2, T, k)))
+            goto other;
+    }
+    const int kind = code_of(args[11], x.dtype), renormalize = PyObject_IsTrue(args[7]);
+    const double scale = PyFloat_AsDouble(args[8]);
+    const int scoring = I32(2), groups = I32(4), top_groups = I32(5), group_top = I32(6);
+    if (kind < 0 || renormalize < 0 || !is_current(gpu) || f_route_size(T, E, (int)k))
+        goto other;
+    void *s = stream_of(args[13]);
+    if (PyErr_Occurred())
+        goto other;
+    int st;
+    Py_BEGIN_ALLOW_THREADS
+    st = f_route(x.ptr, kind, 0, bias.ptr, valid.ptr, T, E, (int)k, scoring, groups, top_groups, group_top,
+                 renormalize, (float)scale, o[0].ptr, o[1].ptr, o[2].ptr, o[3].ptr, o[4].ptr, NULL, 0, s);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(st);
+other:
+    PyErr_Clear();
+    Py_RETURN_NONE;
+}
+
+/* ids, groups, outputs, dtypes, stream */
+static PyObject *py_group_tensors(PyObject *self, PyObject *const *args, Py_ssize_t n)
+{
+    (void)self;
+    if (!want(n, 5, f_group != NULL))
+        return NULL;
+    tensor_t ids, order, offsets;
+    long gpu = ANY_GPU;
+    PyObject *const i32 = type_at(args[3], R_INT32);
+    if (!PyTuple_Check(args[2]) || PyTuple_GET_SIZE(args[2]) != 2 || !PyLong_Check(args[1]) ||
+        !typed(args[0], &ids, &gpu, 1, i32) || !typed(PyTuple_GET_ITEM(args[2], 0), &order, &gpu, 1, i32) ||
+        !typed(PyTuple_GET_ITEM(args[2], 1), &offsets, &gpu, 1, i32))
+        goto other;
+    const int64_t count = ids.size[0], groups = I64(1);
+    if (groups < 1 || !is(&order, 1, count, 0) || !is(&offsets, 1, groups + 1, 0) || !is_current(gpu) ||
+        f_group_size(count, groups))
+        goto other;
+    void *s = stream_of(args[4]);
+    if (PyErr_Occurred())
+        goto other;
+    int st;
+    Py_BEGIN_ALLOW_THREADS
+    st = f_group(ids.ptr, count, groups, order.ptr, offsets.ptr, NULL, NULL, 0, s);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(st);
+other:
+    PyErr_Clear();
+    Py_RETURN_NONE;
+}
+
+/* Y, rows, weights, add, out, the input types' codes by dtype, dtypes, stream */
+static PyObject *py_combine_tensors(PyObject *self, PyObject *const *args, Py_ssize_t n)
+{
+    (void)self;
+    if (!want(n, 8, f_combine != NULL))
+        return NULL;
+    tensor_t y, rows, weights, add = {0}, out;
+    long gpu = ANY_GPU;
+    if (!dense(args[0], &y, &gpu) || y.dims != 2 || !typed(args[1], &rows, &gpu, 2, type_at(args[6], R_INT32)) ||
+        !typed(args[2], &weights, &gpu, 2, type_at(args[6], R_F32)) || !dense(args[4], &out, &gpu) ||
+        !is(&weights, 2, rows.size[0], rows.size[1]) || !is(&out, 2, rows.size[0], y.size[1]))
+        goto other;
+    if (args[3] != Py_None && (!typed(args[3], &add, &gpu, 2, out.dtype) || !is(&add, 2, out.size[0], out.size[1])))
+        goto other;
+    const int y_kind = code_of(args[5], y.dtype), out_kind = code_of(args[5], out.dtype);
+    if (y_kind < 0 || out_kind < 0 || !is_current(gpu))
+        goto other;
+    void *s = stream_of(args[7]);
+    if (PyErr_Occurred())
+        goto other;
+    int st;
+    Py_BEGIN_ALLOW_THREADS
+    st = f_combine(y.ptr, y_kind, 0, y.size[0], rows.ptr, weights.ptr, add.ptr, 0, out.ptr, out_kind, 0,
+                   rows.size[0], rows.size[1], y.size[1], s);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(st);
+other:
+    PyErr_Clear();
+    Py_RETURN_NONE;
+}
+
+/* x, A, B, order, offsets, base, scales, out, the input types' codes by dtype, dtypes, stream */
+static PyObject *py_adapter_tensors(PyObject *self, PyObject *const *args, Py_ssize_t n)
+{
+    (void)self;
+    if (!want(n, 11, f_adapter != NULL))
+        return NULL;
+    tensor_t x, a, b, order, offsets, base, scales = {0}, out;
+    long gpu = ANY_GPU;
+    PyObject *const i32 = type_at(args[9], R_INT32);
+    if (!dense(args[0], &x, &gpu) || x.dims != 2 || !typed(args[1], &a, &gpu, 3, x.dtype) ||
+        !typed(args[2], &b, &gpu, 3, x.dtype) || !typed(args[3], &order, &gpu, 1, i32) ||
+        !typed(args[4], &offsets, &gpu, 1, i32) || !dense(args[5], &base, &gpu) || !dense(args[7], &out, &gpu))
+        goto other;
+    const int64_t T = x.size[0], K = x.size[1], L = a.size[0], r = a.size[1], N = b.size[1];
+    if (!is3(&a, L, r, K) || !is3(&b, L, N, r) || !is(&order, 1, T, 0) || !is(&offsets, 1, L + 1, 0) ||
+        !is(&base, 2, T, N) || !is(&out, 2, T, N) || out.dtype != base.dtype)
+        goto other;
+    if (args[6] != Py_None && (!typed(args[6], &scales, &gpu, 1, type_at(args[9], R_F32)) || !is(&scales, 1, L, 0)))
+        goto other;
+    const int kind = code_of(args[8], x.dtype), out_kind = code_of(args[8], out.dtype);
+    if (kind < 0 || out_kind < 0 || !is_current(gpu))
+        goto other;
+    void *s = stream_of(args[10]);
+    if (PyErr_Occurred())
+        goto other;
+    int st;
+    Py_BEGIN_ALLOW_THREADS
+    st = f_adapter(x.ptr, kind, 0, a.ptr, b.ptr, order.ptr, offsets.ptr, scales.ptr, base.ptr, 0, out.ptr, out_kind, 0,
+                   T, L, r, K, N, s);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(st);
+other:
+    PyErr_Clear();
+    Py_RETURN_NONE;
+}
+
+/* bind_routing(route, its workspace size, group, its workspace size, combine, adapter) */
+static PyObject *py_bind_routing(PyObject *self, PyObject *const *args, Py_ssize_t n)
+{
+    (void)self;
+    if (!want(n, 6, 1))
+        return NULL;
+    f_route = (route_fn)PTR(0);
+    f_route_size = (route_size_fn)PTR(1);
+    f_group = (group_fn)PTR(2);
+    f_group_size = (group_size_fn)PTR(3);
+    f_combine = (combine_fn)PTR(4);
+    f_adapter = (adapter_fn)PTR(5);
+    if (PyErr_Occurred())
+        return NULL;
+    Py_RETURN_NONE;
+}
+
 /* bind(norm, ragged, int8, quant): addresses in the loaded library */
 static PyObject *py_bind(PyObject *self, PyObject *const *args, Py_ssize_t n)
 {
@@ -409,6 +619,11 @@ static PyObject *py_bind_torch(PyObject *self, PyObject *const *args, Py_ssize_t
 static PyMethodDef methods[] = {
     ENTRY("bind", py_bind, "set the library's function addresses"),
     ENTRY("bind_torch", py_bind_torch, "torch's tensor type, and its functions for the current stream"),
+    ENTRY("bind_routing", py_bind_routing, "set the addresses of the routing calls"),
+    ENTRY("route_tensors", py_route_tensors, "route_experts, as norm_tensors"),
+    ENTRY("group_tensors", py_group_tensors, "group_rows, as norm_tensors"),
+    ENTRY("combine_tensors", py_combine_tensors, "combine_experts, as norm_tensors"),
+    ENTRY("adapter_tensors", py_adapter_tensors, "adapter_matmul, as norm_tensors"),
     ENTRY("one_gpu", py_one_gpu, "whether tensors are on one GPU"),
     ENTRY("w8a8_sandwich_norm", py_norm, "see the C header"),
     ENTRY("norm_tensors", py_norm_tensors, "sandwich_norm of dense tensors with every output given"),

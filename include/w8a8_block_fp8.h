@@ -554,6 +554,112 @@ w8a8_status w8a8_sandwich_norm(const void *h_dev, w8a8_in_dtype h_dtype, int64_t
                                int64_t ld_y, int64_t M, int64_t D, w8a8_stream_t stream);
 
 /*
+ * Routing of tokens to experts, with the sort that the ragged layout takes.  For
+ * each of T tokens, from its logits l (E of them):
+ *
+ *   s = softmax(l) (W8A8_SCORE_SOFTMAX) or 1 / (1 + exp(-l)) (W8A8_SCORE_SIGMOID)
+ *   c = s + bias  (bias NULL: c = s)
+ *   of the `groups` runs of E / groups neighbouring experts, the top_groups with the
+ *     largest sums of their group_top (1 or 2) largest c keep their experts
+ *   ids = the top_k largest c among those, in descending order
+ *   weights = scale * s[ids], with renormalize divided by the sum of the chosen s (0
+ *     where that sum is 0)
+ *
+ * Ties go to the lower index.  The choice is that of scores in 64 bits (without a bias,
+ * of the logits' own order); weights are made in fp32.  A NaN ranks above every
+ * number; a row with a NaN (with softmax, or an infinity) has NaN weights.  A logit of
+ * -infinity has the score 0, a bias of -infinity ranks last; both are chosen where
+ * too few others are left.
+ *   logits_dev [T, ld] of dtype, the first E of each row used (ld 0 = E); bias_dev fp32
+ *   [E] or NULL; valid_dev [T] bytes or NULL: a token whose byte is 0 gets ids of -1 and
+ *   weights of 0 (the padding of a batch).
+ *   ids_dev int32 and weights_dev fp32 [T, top_k].
+ *   order_dev int32 [T * top_k], offsets_dev int32 [E + 1], rows_dev int32 [T, top_k]: the
+ *   pairs (token, choice), numbered token * top_k + choice, sorted by expert, stable.
+ *   order[i] is the pair in place i, expert e's places are offsets[e] .. offsets[e+1]-1,
+ *   and rows[t, j] is the place of a pair, -1 for a token that is not valid; its pairs
+ *   come after offsets[E].
+ * E <= W8A8_GROUPS_MAX, top_k <= W8A8_ROUTE_MAX_K and at most the experts of top_groups
+ * groups, groups <= W8A8_ROUTE_MAX_GROUPS, T * top_k < 2^31.  T == 0 writes offsets of 0.
+ * workspace_dev: w8a8_route_workspace_size() bytes (0 for few tokens), 4-byte aligned, in
+ * use until the stream has passed the call; its contents do not matter.
+ */
+#define W8A8_GROUPS_MAX 1024
+#define W8A8_ROUTE_MAX_K 32
+#define W8A8_ROUTE_MAX_GROUPS 32
+typedef enum { W8A8_SCORE_SOFTMAX = 0, W8A8_SCORE_SIGMOID = 1 } w8a8_score;
+w8a8_status w8a8_route_experts(const void *logits_dev, w8a8_in_dtype dtype, int64_t ld,
+                               const float *bias_dev, const uint8_t *valid_dev, int64_t T,
+                               int64_t E, int top_k, w8a8_score scoring, int groups,
+                               int top_groups, int group_top, int renormalize, float scale,
+                               int32_t *ids_dev, float *weights_dev, int32_t *order_dev,
+                               int32_t *offsets_dev, int32_t *rows_dev, void *workspace_dev,
+                               size_t workspace_bytes, w8a8_stream_t stream);
+
+/* Workspace bytes of w8a8_route_experts (0 for none, or bad sizes). */
+size_t w8a8_route_workspace_size(int64_t T, int64_t E, int top_k);
+
+/*
+ * The same sort of n rows by a group that is given: ids_dev int32 [n]; an id outside
+ * [0, groups) is in no group.  order_dev int32 [n], offsets_dev int32 [groups + 1] and
+ * rows_dev int32 [n] (NULL: not wanted) as above.  groups <= W8A8_GROUPS_MAX, n < 2^31.
+ * workspace_dev as above, of w8a8_group_workspace_size() bytes.
+ */
+w8a8_status w8a8_group_rows(const int32_t *ids_dev, int64_t n, int64_t groups, int32_t *order_dev,
+                            int32_t *offsets_dev, int32_t *rows_dev, void *workspace_dev,
+                            size_t workspace_bytes, w8a8_stream_t stream);
+size_t w8a8_group_workspace_size(int64_t n, int64_t groups);
+
+/*
+ * The weighted sum of the experts' rows back to tokens:
+ *
+ *   out[t] = add[t] + sum_j weights[t, j] * Y[rows[t, j]]   (add NULL: 0)
+ *
+ *   Y_dev [M, ld_y] of y_dtype (rows in the experts' order); rows_dev int32 and
+ *   weights_dev fp32 [T, k], as w8a8_route_experts makes them: a row outside [0, M) is
+ *   left out, whatever its weight; add_dev [T, ld_add] and out_dev [T, ld_out] of
+ *   out_dtype, which is y_dtype or fp32; out may be add (with its stride), and not
+ *   overlap anything else.
+ * D columns are used; strides in elements, 0 = dense.  Sums in fp32 in the order of j from
+ * add on, one rounding.  T == 0 or D == 0 is a no-op, k == 0 copies add.  D <= 2^24.
+ */
+w8a8_status w8a8_combine_experts(const void *Y_dev, w8a8_in_dtype y_dtype, int64_t ld_y, int64_t M,
+                                 const int32_t *rows_dev, const float *weights_dev,
+                                 const void *add_dev, int64_t ld_add, void *out_dev,
+                                 w8a8_in_dtype out_dtype, int64_t ld_out, int64_t T, int64_t k,
+                                 int64_t D, w8a8_stream_t stream);
+
+/*
+ * Low-rank adapters of many requests at once, beside a projection that they share:
+ *
+ *   out[t] = base[t] + scales[l] * (x[t] A[l]^T) B[l]^T,   l the adapter of row t
+ *
+ *   x_dev [T, ld_x] bf16 or fp16, K columns used; A_dev [L, r, K] and B_dev [L, N, r] of
+ *   x's type, dense; scales_dev fp32 [L] (NULL: 1); base_dev [T, ld_base] and out_dev
+ *   [T, ld_out] of out_dtype (x's type or fp32), N columns used; out may be base (with
+ *   its stride) and not overlap anything else.
+ *   order_dev int32 [T], offsets_dev int32 [L + 1]: the rows sorted by adapter, as
+ *   w8a8_group_rows makes them from each row's adapter: adapter l's are order[offsets[l]]
+ *   .. order[offsets[l+1]-1].  Rows from offsets[L] on have no adapter: out is base there
+ *   (and not written where out is base).
+ * Adapters of lower rank have zeros in their last rows of A and columns of B.  The sums
+ * of x A^T are kept in fp32 between the products.  order and offsets are read on the device;
+ * order must not name a row twice; entries outside [0, T) are skipped, and offsets that
+ * decrease or leave [0, T] give unspecified results but no out-of-bounds access.
+ * L <= W8A8_GROUPS_MAX, r <= W8A8_ADAPTER_MAX_R; any K and N up to 2^24, strides and
+ * alignments (pieces of 16 bytes where K % 8 == 0, r % 4 == 0 and the rows allow).
+ * T == 0 or N == 0 is a no-op.  One launch, no workspace; it waits on the device for the
+ * work before it on the stream.
+ */
+#define W8A8_ADAPTER_MAX_R 256
+w8a8_status w8a8_adapter_matmul(const void *x_dev, w8a8_in_dtype dtype, int64_t ld_x,
+                                const void *A_dev, const void *B_dev, const int32_t *order_dev,
+                                const int32_t *offsets_dev, const float *scales_dev,
+                                const void *base_dev, int64_t ld_base, void *out_dev,
+                                w8a8_out_dtype out_dtype, int64_t ld_out, int64_t T, int64_t L,
+                                int64_t r, int64_t K, int64_t N, w8a8_stream_t stream);
+
+/*
  * Per-token-group FP8 quantiser: makes the matmul's activation operand A and
  * its scales a_s from a higher-precision activation X ("feat: optimize w8a8
  * block fp8 matmul for Hopper", FlagGems-vllm PR #693, Description: the
