@@ -129,14 +129,20 @@ __device__ __forceinline__ void place_pairs(const GroupSmem &s, const GroupOut &
         const int b = threadIdx.x + i * kThreads;
         before[i] = total[i] = 0;
         if (i < per_thread && b < bins) {
-            for (uint32_t r = 0; r < ctas; ++r) {
-                int v;
-                asm volatile("ld.shared::cluster.s32 %0, [%1];"
-                             : "=r"(v)
-                             : "r"(cluster_map(smem_addr(s.tot + b), r))
-                             : "memory");
-                before[i] += r < me ? v : 0;
-                total[i] += v;
+            int v[kMaxCluster];
+#pragma unroll
+            for (uint32_t r = 0; r < kMaxCluster; ++r) {
+                v[r] = 0;
+                if (r < ctas)
+                    asm volatile("ld.shared::cluster.s32 %0, [%1];"
+                                 : "=r"(v[r])
+                                 : "r"(cluster_map(smem_addr(s.tot + b), r))
+                                 : "memory");
+            }
+#pragma unroll
+            for (uint32_t r = 0; r < kMaxCluster; ++r) {
+                before[i] += r < me ? v[r] : 0;
+                total[i] += v[r];
             }
             if (g.hist) {
                 if (me == 0)

@@ -11,14 +11,17 @@
 //
 // One warp per token.  A lane holds ceil(E / 32) neighbouring experts in registers, so
 // runs are whole lanes and the lowest lane with the largest key has the lowest index.
-// Keys are the scores' bits mapped to unsigned numbers in the same order (NaN above
-// all): a round of the selection is one warp maximum, one ballot, one shuffle.
+// A key is a score's bits mapped to an unsigned number in the same order (NaN above
+// all), its lowest bits replaced by the expert's slot in the lane.  Each lane sorts its
+// keys (a network of minima and maxima); a round of the selection is then one warp
+// maximum and one ballot, and the winning lane moves its keys up.
 //
-// Which expert is chosen is decided as the exact scores decide it.  Without a bias
-// the order of the scores is the order of the logits, which are compared themselves.
-// With one, the fp32 scores c carry an error that is bounded below (`Bound`); where two
-// neighbours of the chosen order, or the worst kept and the best dropped run, are
-// nearer than twice that, the token is decided again in fp64 (0.1 to 1 % of tokens).
+// Which expert is chosen is decided as the exact scores decide it.  Keys carry an
+// error: the replaced bits, and where a bias makes the scores themselves be compared
+// (without one their order is the logits', which are compared instead) their rounding,
+// bounded below (`bound`).  Where two neighbours of the chosen order are nearer than
+// that, those that are too near are scored and ranked again in fp64 (refine); where the
+// worst kept and the best dropped run are, the whole token is (choose_exact).
 #include <algorithm>
 #include <cstdio>
 
@@ -141,6 +144,39 @@ __device__ __forceinline__ void load_lane(const RouteParams &p, const void *row,
         l[i] = i < p.per && e0 + i < p.E ? load_logit<KIND>(row, e0 + i) : -INFINITY;
 }
 
+__device__ __forceinline__ float exp2_fast(float x)         // within 2 units of 2^-23
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_fast(float x)          // within 1 unit
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+constexpr float kLog2e = 1.44269504f;
+
+// Descending order by odd-even merging (K. E. Batcher, "Sorting networks and their
+// applications", AFIPS Spring Joint Computer Conference, 1968).
+template <int N> __device__ __forceinline__ void sort_keys(uint32_t (&k)[N])
+{
+#pragma unroll
+    for (int p = 1; p < N; p *= 2)
+#pragma unroll
+        for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+            for (int j = q % p; j + q < N; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q; ++i)
+                    if (j + i + q < N && (j + i) / (2 * p) == (j + i + q) / (2 * p)) {
+                        const uint32_t a = k[j + i], b = k[j + i + q];
+                        k[j + i] = max(a, b);
+                        k[j + i + q] = min(a, b);
+                    }
+}
+
 // The two largest keys of a lane's experts, then of the lanes of its run.
 template <class K> __device__ __forceinline__ void two_best(K &a, K &b, K x)
 {
@@ -239,6 +275,40 @@ template <int KIND> __device__ __noinline__ int choose_exact(const RouteParams &
     return id;
 }
 
+// Ranks `count` (at most 32) experts, lane j's being id, by their scores in fp64: returns
+// the expert of rank `lane`.
+template <int KIND> __device__ __noinline__ int refine(const RouteParams &p, const void *row, int id, int count, float m)
+{
+    const int lane = threadIdx.x & 31;
+    const bool in = lane < count;
+    double s = 0;
+    const double l = in ? static_cast<double>(load_logit<KIND>(row, id)) : 0.;
+    if (p.sigmoid) {
+        s = 1 / (1 + exp(-l));
+    } else {
+        double z = 0;
+#pragma unroll 4
+        for (int e = lane; e < p.E; e += 32)
+            z += exp(static_cast<double>(load_logit<KIND>(row, e)) - m);
+        z = warp_sum(z);
+        s = z == 0 ? 0. : exp(l - m) / z;
+    }
+    // without a bias the logits rank
+    const unsigned long long key = in ? key_of(p.bias ? s + p.bias[id] : l) : 0ull;
+    int above = 0;
+    for (int j = 0; j < count; ++j) {
+        const unsigned long long other = __shfl_sync(kAll, key, j);
+        const int other_id = __shfl_sync(kAll, id, j);
+        above += other > key || (other == key && other_id < id);
+    }
+    int mine = id;
+    for (int j = 0; j < count; ++j) {
+        const int rank = __shfl_sync(kAll, above, j), e = __shfl_sync(kAll, id, j);
+        mine = rank == lane ? e : mine;
+    }
+    return mine;
+}
+
 // One token: lane j < k gets the j-th expert and its weight.
 template <int KIND, int PER>
 __device__ __forceinline__ void route_token(const RouteParams &p, const void *row, const float (&l)[PER],
@@ -249,20 +319,20 @@ __device__ __forceinline__ void route_token(const RouteParams &p, const void *ro
     const bool scored = biased || (p.groups > 1 && p.group_top == 2) || (!p.sigmoid && !p.renormalize);
     float c[PER];
     float m = 0.f, z = 1.f;
-    // An upper bound of the error of an fp32 score.  __expf(x) is within 2 + 1.173 |x|
-    // units of 2^-23 of exp(x) relatively, __fdividef within 2 units.
-    //   sigmoid: s (1 - s) (2 + 1.173 |l|) <= 0.6 units from the exponential, then one
-    //     rounded sum and the quotient: 3.2 units, below 2^-21.
-    //   softmax: at most 2.4 units of the largest term (x e^x peaks at 0.37); the sum of
-    //     terms is within 12 units (|x| averages at most ln E + 1 under the terms as
-    //     weights) and its roundings within 19 (E <= 1024), with the quotient 33 units of
-    //     s, and s <= 1/z: below 2^-17 / z + 2^-21.
+    // An upper bound of the error of an fp32 score, in units of 2^-23.  An exponential of x
+    // is off by 2 units and by its argument's rounding, 0.75 |x|, relatively.
+    //   sigmoid: s (1 - s) (2 + 0.75 |l|) <= 0.6 units, then one rounded sum and the
+    //     quotient: 2.1 units, below 2^-21.
+    //   softmax: with u = -x the terms' errors are at most 2 units of the largest term and,
+    //     in the sum z, 2 + 0.75 u averaged with the terms as weights, where u averages at
+    //     most ln E + 1 < 8; the sum's roundings (PER + 5) / 2 <= 18.5, the quotient 1.5: with
+    //     s <= 1 / z at most 30 units of 1 / z, below 2^-18 / z.
     float bound = 0x1p-21f;
     if (scored) {
         if (p.sigmoid) {
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                c[i] = __fdividef(1.f, 1.f + __expf(-l[i]));
+                c[i] = rcp_fast(1.f + exp2_fast(-kLog2e * l[i]));
         } else {
             m = l[0];
 #pragma unroll
@@ -273,13 +343,13 @@ __device__ __forceinline__ void route_token(const RouteParams &p, const void *ro
             z = 0.f;
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                z += c[i] = __expf(l[i] - m);
+                z += c[i] = exp2_fast(kLog2e * (l[i] - m));
             z = warp_sum(z);
-            const float inv = z == 0.f ? 0.f : __fdividef(1.f, z);
+            const float inv = z == 0.f ? 0.f : rcp_fast(z);
 #pragma unroll
             for (int i = 0; i < PER; ++i)
                 c[i] *= inv;
-            bound += 0x1p-17f * inv;
+            bound = 0x1p-18f * inv;
         }
     }
     if (biased) {
@@ -291,11 +361,10 @@ __device__ __forceinline__ void route_token(const RouteParams &p, const void *ro
 #pragma unroll
     for (int i = 0; i < PER; ++i)
         key[i] = i < p.per && e0 + i < p.E ? key_of(biased ? c[i] : l[i]) : 0u;
-    bool exact = false;             // decide again in fp64
+    bool exact = false;             // decide the whole token again in fp64
     if (p.groups > 1) {
         const int size = p.E / p.groups;
-        uint32_t a = 0, b = 0, keep_bits = 0;
-        bool keep;
+        uint32_t a = 0, b = 0;
         uint32_t kept, dropped;
         const bool sums = p.group_top == 2;
         if (p.group_lanes) {
@@ -307,8 +376,8 @@ __device__ __forceinline__ void route_token(const RouteParams &p, const void *ro
                 two_best(a, b, oa);
                 b = ob > b ? ob : b;
             }
-            keep = rank_groups<uint32_t>(p.groups, p.group_lanes, p.top_groups, lane / p.group_lanes,
-                                         group_value(p.group_top, a, b), &kept, &dropped);
+            const bool keep = rank_groups<uint32_t>(p.groups, p.group_lanes, p.top_groups, lane / p.group_lanes,
+                                                    group_value(p.group_top, a, b), &kept, &dropped);
 #pragma unroll
             for (int i = 0; i < PER; ++i)
                 key[i] = keep ? key[i] : 0u;
@@ -323,58 +392,72 @@ __device__ __forceinline__ void route_token(const RouteParams &p, const void *ro
                 for (int i = 0; i < size; ++i)
                     two_best(a, b, static_cast<uint32_t>(run_keys[lane * size + i]));
             __syncwarp();
-            keep = rank_groups<uint32_t>(p.groups, 1, p.top_groups, lane, group_value(p.group_top, a, b), &kept,
-                                         &dropped);
-            keep_bits = __ballot_sync(kAll, keep);
+            const uint32_t keep = __ballot_sync(kAll, rank_groups<uint32_t>(p.groups, 1, p.top_groups, lane,
+                                                                           group_value(p.group_top, a, b), &kept, &dropped));
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                key[i] = keep_bits >> ((e0 + i) / size & 31) & 1 ? key[i] : 0u;
+                key[i] = keep >> ((e0 + i) / size & 31) & 1 ? key[i] : 0u;
         }
         if ((biased || sums) && p.top_groups < p.groups) {
             const float hi = value_of(kept), lo = value_of(dropped);
             exact = !(hi - lo > 4.f * bound + 0x1p-21f * (fabsf(hi) + fabsf(lo)));
         }
     }
-    // One round more than k where scores are compared: the best that stays behind.
-    const int rounds = biased ? p.k + 1 : p.k;
-    uint32_t best = 0, mine = 0, last = 0;
-    int last_id = 0;
-    id = 0;
+    // The slot takes the place of the key's lowest bits; 16-bit logits have zeros there.
+    constexpr uint32_t kSlots = PER - 1;
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-        best = key[i] > best ? key[i] : best;
-    for (int j = 0; j < rounds; ++j) {
-        const uint32_t top = warp_max(best);
-        const int src = __ffs(__ballot_sync(kAll, best == top)) - 1;
-        int slot = 0;
-#pragma unroll
-        for (int i = PER - 1; i >= 0; --i)
-            slot = key[i] == top ? i : slot;
-        const int e = __shfl_sync(kAll, e0 + slot, src);
+        key[i] = key[i] ? (key[i] & ~kSlots) | (kSlots - i) : 0u;
+    sort_keys(key);
+    const bool whole = !biased && KIND != W8A8_IN_FP32;
+    const float near_by = biased ? 2.f * bound : 0.f, near_at = biased ? 0x1p-22f + PER * 0x1p-23f : 0.f;
+    uint32_t mine = 0, last = 0;        // lane j: the j-th key
+    id = 0;
+    auto round = [&](int j) {
+        // (the lane before the slot: the lower index first)
+        const uint32_t kept_bits = key[0] & ~kSlots;
+        const uint32_t top = warp_max(kept_bits);
+        const int src = __ffs(__ballot_sync(kAll, kept_bits == top)) - 1;
+        const uint32_t slot = kSlots - (__shfl_sync(kAll, key[0], src) & kSlots);
         if (lane == src) {
-            best = 0;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                key[i] = i == slot ? 0u : key[i];
-                best = key[i] > best ? key[i] : best;
-            }
+            for (int i = 0; i + 1 < PER; ++i)
+                key[i] = key[i + 1];
+            key[PER - 1] = 0;
         }
         if (lane == j)
-            mine = top, id = e;
-        last = top, last_id = e;
-    }
-    if (biased && !exact) {
-        uint32_t next = __shfl_down_sync(kAll, mine, 1);
-        int next_id = __shfl_down_sync(kAll, id, 1);
-        if (lane == p.k - 1)
-            next = last, next_id = last_id;
-        const float hi = value_of(mine), lo = value_of(next);
-        bool near = lane < p.k && next != 0 && !(hi - lo > 2.f * bound + 0x1p-22f * (fabsf(hi) + fabsf(lo)));
-        if (__any_sync(kAll, near)) {
-            // equal logits under equal biases are equal scores: their order is by index already
-            if (near)
-                near = !(load_logit<KIND>(row, id) == load_logit<KIND>(row, next_id) && p.bias[id] == p.bias[next_id]);
-            exact = __any_sync(kAll, near);
+            mine = top, id = src * p.per + static_cast<int>(slot);
+        last = top;
+    };
+    for (int j = 0; j < p.k; ++j)
+        round(j);
+    if (!whole && !exact) {
+        // Whether key `a` is surely above key `b`, the next.  (Without a bias that is so where
+        // the kept bits differ.)
+        auto near = [&](uint32_t a, uint32_t b) {
+            const float hi = value_of(a), lo = value_of(b & ~kSlots);
+            return b > kSlots && !(hi - lo > near_by + near_at * (fabsf(hi) + fabsf(lo)));
+        };
+        const uint32_t behind = warp_max(key[0]);
+        const uint32_t below = __shfl_down_sync(kAll, mine, 1);         // (by every lane)
+        const uint32_t next = lane == p.k - 1 ? behind : below;
+        bool unsure = lane < p.k && near(mine, next);
+        if (__any_sync(kAll, unsure)) {
+            // Take on what is too near the last, as many as lanes hold.
+            int count = p.k;
+            while (count < 32 && near(last, warp_max(key[0])))
+                round(count++);
+            const int next_id = __shfl_down_sync(kAll, id, 1);
+            const float own_l = lane < count ? load_logit<KIND>(row, id) : 0.f;
+            const float own_b = biased && lane < count ? p.bias[id] : 0.f;
+            const float next_l = __shfl_down_sync(kAll, own_l, 1), next_b = __shfl_down_sync(kAll, own_b, 1);
+            // equal logits under equal biases are equal scores, in order of their index
+            const uint32_t after = __shfl_down_sync(kAll, mine, 1);
+            unsure = lane + 1 < count && near(mine, after) && !(own_l == next_l && own_b == next_b && id < next_id);
+            if (near(last, warp_max(key[0])))
+                exact = true;               // more than 32
+            else if (__any_sync(kAll, unsure))
+                id = refine<KIND>(p, row, id, count, m);
         }
     }
     if (exact)
@@ -405,7 +488,7 @@ __device__ __forceinline__ void route_token(const RouteParams &p, const void *ro
     weight = s * p.scale;
 }
 
-template <int KIND, int PER> __global__ void __launch_bounds__(kThreads) k_route(const RouteParams p)
+template <int KIND, int PER> __global__ void __launch_bounds__(kThreads, PER <= 8 ? 2 : 1) k_route(const RouteParams p)
 {
     extern __shared__ int smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, bins = p.E + 1, e0 = lane * p.per;
