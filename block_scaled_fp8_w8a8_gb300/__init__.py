@@ -31,7 +31,8 @@ from ._binding import (  # noqa: F401
     w8a8_sandwich_norm, W8A8_NORM_SAME, W8A8_NORM_FP8, W8A8_NORM_INT8, W8A8_NORM_MAX_D,
     w8a8_route_experts, w8a8_route_workspace_size, W8A8_SCORE_SOFTMAX, W8A8_SCORE_SIGMOID,
     w8a8_group_rows, w8a8_group_workspace_size, W8A8_GROUPS_MAX, W8A8_ROUTE_MAX_K,
-    W8A8_ROUTE_MAX_GROUPS, w8a8_combine_experts, w8a8_adapter_matmul, W8A8_ADAPTER_MAX_R,
+    W8A8_ROUTE_MAX_GROUPS, w8a8_combine_experts, w8a8_adapter_matmul,
+    w8a8_adapter_workspace_size, W8A8_ADAPTER_MAX_R,
     w8a8_launch_floor_kernel, w8a8_block_fp8_quant_matmul,
     w8a8_block_fp8_quant_matmul_workspace_size,
     w8a8_get_device_status, w8a8_last_error, w8a8_options, w8a8_shutdown, w8a8_status_string,
@@ -693,9 +694,11 @@ def adapter_matmul(x, A, B, order, offsets, base, scales=None, out=None, stream=
         _typed(out, (base.dtype,), "out")
         ld_x, ld_base, ld_out = _rows(x), _rows(base), _rows(out)
         _here(x, A, B, order, offsets, base, scales, out)
+        size = lib.w8a8_adapter_workspace_size(T, L, r, K)
+        keep, scratch = _workspace(size, x.device)
     st = lib.w8a8_adapter_matmul(x.data_ptr(), kind, ld_x, A.data_ptr(), B.data_ptr(), order.data_ptr(),
                                  offsets.data_ptr(), None if scales is None else scales.data_ptr(), base.data_ptr(),
-                                 ld_base, out.data_ptr(), _in_codes[base.dtype], ld_out, T, L, r, K, N,
+                                 ld_base, out.data_ptr(), _in_codes[base.dtype], ld_out, T, L, r, K, N, scratch, size,
                                  _stream(stream))
     if st:
         check(st)

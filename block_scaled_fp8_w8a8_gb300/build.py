@@ -22,7 +22,7 @@ OUT_DEBUG = os.path.join(HERE, "_build_debug")
 LIB_NAME_DEBUG = "libw8a8_gb300_debug.so"
 UNITS = ["api.cu", "status.cu", "gemm_tiled.cu", "gemm_swapab.cu", "noalloc.cu", "quant.cu", "hostio.cu",
          "gemm_smallm.cu", "gemm_pair.cu", "gemm_generic.cu", "gemm_ragged.cu", "gemm_ragged_few.cu", "int8.cu", "norm.cu",
-         "route.cu", "combine.cu", "adapter.cu"]
+         "route.cu", "combine.cu", "adapter.cu", "adapter_tile.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # What a unit may include: an edit of any of them compiles every unit anew.
 HEADERS = sorted(f for f in os.listdir(SRC) if f.endswith((".cuh", ".h", ".inc")))

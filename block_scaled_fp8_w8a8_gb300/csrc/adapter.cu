@@ -21,6 +21,7 @@
 #include <cstdio>
 
 #include "../../include/w8a8_block_fp8.h"
+#include "adapter.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
 
@@ -29,20 +30,7 @@ w8a8_status record_error(w8a8_status st, const char *message);
 
 namespace {
 
-struct AdapterParams {
-    const uint16_t *x;          // [T, ld_x]
-    const uint16_t *A;          // [L, r, K]
-    const uint16_t *B;          // [L, N, r]
-    const int *order;           // [T]
-    const int *offsets;         // [L + 1]
-    const float *scales;        // [L] or null
-    const void *base;           // [T, ld_base]
-    void *out;                  // [T, ld_out]; may be base
-    long long ld_x, ld_base, ld_out;
-    int T, L, r, K, N;
-    int r_pad;                  // r up to whole 16
-    int vec_k, vec_r;           // 16-byte pieces of x and A, 8-byte pieces of B
-};
+using namespace lora;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
@@ -96,24 +84,6 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// v's leading 16-bit part, removed from v.  An infinity leaves nothing.
-template <bool BF16> __device__ __forceinline__ uint32_t take_part(float &v)
-{
-    float part;
-    uint32_t bits;
-    if constexpr (BF16) {
-        const __nv_bfloat16 h = __float2bfloat16_rn(v);
-        part = __bfloat162float(h);
-        bits = __bfloat16_as_ushort(h);
-    } else {
-        const __half h = __float2half_rn(v);
-        part = __half2float(h);
-        bits = __half_as_ushort(h);
-    }
-    v = fabsf(part) == INFINITY ? 0.f : v - part;
-    return bits;
-}
-
 template <int OUT> __device__ __forceinline__ float load_out(const void *p, long long i)
 {
     if constexpr (OUT == W8A8_OUT_FP32)
@@ -131,50 +101,6 @@ template <int OUT> __device__ __forceinline__ void store_out(void *p, long long 
         static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
     else
         static_cast<__half *>(p)[i] = __float2half_rn(v);
-}
-
-// The item (adapter, first place, rows) of a cluster among tiles of `tile` rows:
-// adapter L is the rows without one.  Every thread of the CTA calls it.
-struct Item {
-    int adapter, first, rows;       // rows 0: none
-};
-__device__ __forceinline__ Item find_item(const AdapterParams &p, int index, int tile, int groups, int *scratch)
-{
-    // scratch: [8] sums of warps, then the item
-    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-    const int q = (groups + kThreads - 1) / kThreads, from = min(t * q, groups), to = min(from + q, groups);
-    auto offset = [&](int g) { return g > p.L ? p.T : min(max(p.offsets[g], 0), p.T); };
-    int sum = 0;
-    for (int g = from; g < to; ++g)
-        sum += (max(offset(g + 1) - offset(g), 0) + tile - 1) / tile;
-    int scan = sum;
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-        const int v = __shfl_up_sync(0xffffffffu, scan, d);
-        scan += lane >= d ? v : 0;
-    }
-    if (lane == 31)
-        scratch[warp] = scan;
-    if (t == 0)
-        scratch[10] = 0;
-    __syncthreads();
-    int run = scan - sum;
-    for (int w = 0; w < warp; ++w)
-        run += scratch[w];
-    if (index >= run && index < run + sum) {
-        for (int g = from; g < to; ++g) {
-            const int first = offset(g), rows = max(offset(g + 1) - first, 0), tiles = (rows + tile - 1) / tile;
-            if (index >= run && index < run + tiles) {
-                const int skip = (index - run) * tile;
-                scratch[8] = g;
-                scratch[9] = first + skip;
-                scratch[10] = min(tile, rows - skip);
-            }
-            run += tiles;
-        }
-    }
-    __syncthreads();
-    return Item{scratch[8], scratch[9], scratch[10]};
 }
 
 // Shared memory: partial sums of the warps (later h's parts as MMA operands), every
@@ -197,7 +123,7 @@ template <bool BF16, int OUT, int NT> __global__ void __launch_bounds__(kThreads
 {
     constexpr int kRows = 8 * NT, kTerms = BF16 && OUT == W8A8_OUT_FP32 ? 3 : 2;
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ int scratch[12];
+    __shared__ int scratch[16];
     __shared__ int rows[kRows];
     __shared__ float factor[kRows];         // what a row's sums are multiplied by (fp16)
     uint32_t ctas, cluster;
@@ -210,7 +136,7 @@ template <bool BF16, int OUT, int NT> __global__ void __launch_bounds__(kThreads
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     grid_dependency_wait();
     grid_launch_dependents();
-    const Item item = find_item(p, static_cast<int>(cluster), kRows, p.out == p.base ? p.L : p.L + 1, scratch);
+    const Item item = find_item<kThreads>(p, static_cast<int>(cluster), kRows, p.out == p.base ? p.L : p.L + 1, scratch);
     if (item.rows == 0)
         return;                             // the whole cluster
     if (threadIdx.x < kRows) {
@@ -317,14 +243,12 @@ template <bool BF16, int OUT, int NT> __global__ void __launch_bounds__(kThreads
 #pragma unroll
             for (int d = 16; d; d /= 2)
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            // top in [2^e, 2^(e+1)); e - 14 is the power taken out, within the normal range
-            const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-            const int power = top == 0.f || e == 128 ? 0 : min(max(e - 14, -126), 126);
-            const float shrink = __uint_as_float(static_cast<uint32_t>(127 - power) << 23);
+            float shrink, back;
+            power_of(top, &shrink, &back);
             for (int i = lane; i < p.r_pad; i += 32)
                 h[i * kRows + t] *= shrink;
             if (lane == 0)
-                factor[t] = __uint_as_float(static_cast<uint32_t>(127 + power) << 23);
+                factor[t] = back;
         }
         __syncthreads();
     }
@@ -379,21 +303,6 @@ template <bool BF16, int OUT, int NT> __global__ void __launch_bounds__(kThreads
 
 bool on(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-// Up to `bytes` of dynamic shared memory for a kernel, set once per device by its own
-// flags.  (The device's most would leave nothing for the kernel's static arrays.)
-template <typename Kernel> cudaError_t allow_smem(Kernel kernel, size_t bytes, volatile int *set)
-{
-    int id = 0;
-    cudaError_t e = cudaGetDevice(&id);
-    if (e == cudaSuccess && (id < 0 || id >= kMaxDeviceFlags))
-        e = cudaErrorInvalidDevice;
-    if (e == cudaSuccess && !set[id]) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-        set[id] = e == cudaSuccess;
-    }
-    return e;
-}
-
 template <bool BF16, int OUT, int NT>
 cudaError_t launch_few(const AdapterParams &p, long long items, const DeviceView &dev, cudaStream_t stream)
 {
@@ -425,13 +334,6 @@ cudaError_t launch_few(const AdapterParams &p, long long items, const DeviceView
     return cudaLaunchKernelEx(&lc, kernel, p);
 }
 
-// Tiles that T rows of `groups` adapters make at most: one unfilled each.
-long long most_items(long long T, long long groups, int tile)
-{
-    const long long g = std::min(T, groups);
-    return (T + g * (tile - 1)) / tile;
-}
-
 template <bool BF16, int OUT> cudaError_t launch_adapter(const AdapterParams &p, const DeviceView &dev, cudaStream_t s)
 {
     const long long groups = p.out == p.base ? p.L : p.L + 1;
@@ -442,14 +344,39 @@ template <bool BF16, int OUT> cudaError_t launch_adapter(const AdapterParams &p,
     return launch_few<BF16, OUT, 2>(p, most_items(p.T, groups, 16), dev, s);
 }
 
+// Whether a problem's sizes are for the tiles of 128 rows (adapter_tile.cu): where adapters
+// have many rows on average.
+bool tiled(const AdapterParams &p) { return p.L > 0 && p.T >= 32 * p.L && p.r >= 8 && p.K >= 64; }
+
+size_t workspace_bytes(const AdapterParams &p)
+{
+    return tiled(p) ? sizeof(float) * tile_splits(p) * p.T * p.r_pad : 0;
+}
+
 }  // namespace
 }  // namespace w8a8
+
+extern "C" size_t w8a8_adapter_workspace_size(int64_t T, int64_t L, int64_t r, int64_t K)
+{
+    using namespace w8a8;
+    if (T <= 0 || L <= 0 || r <= 0 || K <= 0 || L > W8A8_GROUPS_MAX || r > W8A8_ADAPTER_MAX_R || T >= (1ll << 28) ||
+        K > (1ll << 24))
+        return 0;
+    AdapterParams p = {};
+    p.T = static_cast<int>(T);
+    p.L = static_cast<int>(L);
+    p.r = static_cast<int>(r);
+    p.K = static_cast<int>(K);
+    p.r_pad = static_cast<int>((r + 15) / 16 * 16);
+    return workspace_bytes(p);
+}
 
 extern "C" w8a8_status w8a8_adapter_matmul(const void *x_dev, w8a8_in_dtype dtype, int64_t ld_x, const void *A_dev,
                                            const void *B_dev, const int32_t *order_dev, const int32_t *offsets_dev,
                                            const float *scales_dev, const void *base_dev, int64_t ld_base,
                                            void *out_dev, w8a8_out_dtype out_dtype, int64_t ld_out, int64_t T,
-                                           int64_t L, int64_t r, int64_t K, int64_t N, w8a8_stream_t stream)
+                                           int64_t L, int64_t r, int64_t K, int64_t N, void *workspace_dev,
+                                           size_t workspace_bytes, w8a8_stream_t stream)
 {
     using namespace w8a8;
     if (T < 0 || L < 0 || r < 0 || K < 0 || N < 0)
@@ -500,12 +427,22 @@ extern "C" w8a8_status w8a8_adapter_matmul(const void *x_dev, w8a8_in_dtype dtyp
     p.r_pad = static_cast<int>((r + 15) / 16 * 16);
     p.vec_k = K % 8 == 0 && ld_x % 8 == 0 && on(x_dev, 16) && on(A_dev, 16);
     p.vec_r = r % 4 == 0 && on(B_dev, 8);
+    const bool tiles = tiled(p) && tile_takes(p, out_dtype);
+    if (const size_t need = tiles ? w8a8::workspace_bytes(p) : 0;
+        need && (!workspace_dev || workspace_bytes < need || !on(workspace_dev, 16))) {
+        char msg[160];
+        snprintf(msg, sizeof(msg), "workspace of %zu bytes at %p: need %zu bytes, 16-byte aligned", workspace_bytes,
+                 workspace_dev, need);
+        return record_error(W8A8_ERR_WORKSPACE, msg);
+    }
     DeviceView dev;
     if (const int st = device_view(&dev); st != W8A8_OK)
         return static_cast<w8a8_status>(st);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (dtype == W8A8_IN_BF16)
+    if (tiles)
+        e = launch_tile(p, dtype, out_dtype, static_cast<float *>(workspace_dev), dev, s);
+    else if (dtype == W8A8_IN_BF16)
         e = out_dtype == W8A8_OUT_FP32 ? launch_adapter<true, W8A8_OUT_FP32>(p, dev, s)
                                        : launch_adapter<true, W8A8_OUT_BF16>(p, dev, s);
     else

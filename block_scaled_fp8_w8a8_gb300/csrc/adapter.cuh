@@ -1,0 +1,141 @@
+// What the two forms of the adapter product share: the call's parameters, the search for
+// a CTA's rows, the parts of an fp32 number.
+#pragma once
+
+#include <algorithm>
+
+#include "kernels.cuh"
+#include "ptx.cuh"
+
+namespace w8a8 {
+namespace lora {
+
+struct AdapterParams {
+    const uint16_t *x;          // [T, ld_x]
+    const uint16_t *A;          // [L, r, K]
+    const uint16_t *B;          // [L, N, r]
+    const int *order;           // [T]
+    const int *offsets;         // [L + 1]
+    const float *scales;        // [L] or null
+    const void *base;           // [T, ld_base]
+    void *out;                  // [T, ld_out]; may be base
+    long long ld_x, ld_base, ld_out;
+    int T, L, r, K, N;
+    int r_pad;                  // r up to whole 16
+    int vec_k, vec_r;           // 16-byte pieces of x and A, 8-byte pieces of B
+};
+
+// The power of two that brings a row of h, whose largest size is top, near 2^14: the
+// factor that does, and the one that its sums are multiplied by afterwards.
+__device__ __forceinline__ void power_of(float top, float *shrink, float *factor)
+{
+    // top in [2^e, 2^(e+1)); the power stays within the normal numbers
+    const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+    const int power = top == 0.f || e == 128 ? 0 : min(max(e - 14, -126), 126);
+    *shrink = __uint_as_float(static_cast<uint32_t>(127 - power) << 23);
+    *factor = __uint_as_float(static_cast<uint32_t>(127 + power) << 23);
+}
+
+// The item (adapter, first place, rows) of a cluster among tiles of `tile` rows:
+// adapter L is the rows without one.  Every thread of the CTA calls it.
+struct Item {
+    int adapter, first, rows;       // rows 0: none
+};
+template <int THREADS>
+__device__ __forceinline__ Item find_item(const AdapterParams &p, int index, int tile, int groups, int *scratch)
+{
+    // scratch: [12] sums of warps, then the item
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const int q = (groups + THREADS - 1) / THREADS, from = min(t * q, groups), to = min(from + q, groups);
+    auto offset = [&](int g) { return g > p.L ? p.T : min(max(p.offsets[g], 0), p.T); };
+    int sum = 0;
+    for (int g = from; g < to; ++g)
+        sum += (max(offset(g + 1) - offset(g), 0) + tile - 1) / tile;
+    int scan = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int v = __shfl_up_sync(0xffffffffu, scan, d);
+        scan += lane >= d ? v : 0;
+    }
+    if (lane == 31)
+        scratch[warp] = scan;
+    if (t == 0)
+        scratch[14] = 0;
+    __syncthreads();
+    int run = scan - sum;
+    for (int w = 0; w < warp; ++w)
+        run += scratch[w];
+    if (index >= run && index < run + sum) {
+        for (int g = from; g < to; ++g) {
+            const int first = offset(g), rows = max(offset(g + 1) - first, 0), tiles = (rows + tile - 1) / tile;
+            if (index >= run && index < run + tiles) {
+                const int skip = (index - run) * tile;
+                scratch[12] = g;
+                scratch[13] = first + skip;
+                scratch[14] = min(tile, rows - skip);
+            }
+            run += tiles;
+        }
+    }
+    __syncthreads();
+    return Item{scratch[12], scratch[13], scratch[14]};
+}
+
+// v's leading 16-bit part, removed from v.  An infinity leaves nothing.
+template <bool BF16> __device__ __forceinline__ uint32_t take_part(float &v)
+{
+    float part;
+    uint32_t bits;
+    if constexpr (BF16) {
+        const __nv_bfloat16 h = __float2bfloat16_rn(v);
+        part = __bfloat162float(h);
+        bits = __bfloat16_as_ushort(h);
+    } else {
+        const __half h = __float2half_rn(v);
+        part = __half2float(h);
+        bits = __half_as_ushort(h);
+    }
+    v = fabsf(part) == INFINITY ? 0.f : v - part;
+    return bits;
+}
+
+// Up to `bytes` of dynamic shared memory for a kernel, set once per device by its own
+// flags.  (The device's most would leave nothing for the kernel's static arrays.)
+template <typename Kernel> inline cudaError_t allow_smem(Kernel kernel, size_t bytes, volatile int *set)
+{
+    int id = 0;
+    cudaError_t e = cudaGetDevice(&id);
+    if (e == cudaSuccess && (id < 0 || id >= kMaxDeviceFlags))
+        e = cudaErrorInvalidDevice;
+    if (e == cudaSuccess && !set[id]) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+        set[id] = e == cudaSuccess;
+    }
+    return e;
+}
+
+// Tiles that T rows of `groups` adapters make at most: one unfilled each.
+inline long long most_items(long long T, long long groups, int tile)
+{
+    const long long g = std::min(T, groups);
+    return (T + g * (tile - 1)) / tile;
+}
+
+// Many rows: the two launches of adapter_tile.cu.
+struct TileParams {
+    AdapterParams a;
+    float *h;                   // [splits, T, r_pad]: scales[l] x A^T of K's parts, by place
+    int splits;
+    int chunks;                 // CTAs that share a tile's columns
+    unsigned *status;
+    unsigned long long wait_limit;
+};
+// Whether they take a problem (16-byte pieces everywhere, r in bounds), and by how
+// many parts of K.
+bool tile_takes(const AdapterParams &p, int out_kind);
+int tile_splits(const AdapterParams &p);
+cudaError_t launch_tile(const AdapterParams &p, int x_kind, int out_kind, float *h, const DeviceView &dev,
+                        cudaStream_t stream);
+
+}  // namespace lora
+}  // namespace w8a8

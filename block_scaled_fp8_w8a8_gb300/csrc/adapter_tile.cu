@@ -1,0 +1,557 @@
+// Low-rank adapters, many rows: tiles of 128 rows of one adapter on the tcgen05 tensor
+// cores, in two launches with h = scales[l] x A[l]^T between them in fp32:
+//
+//   k_adapter_shrink   h[s] of a tile and the s-th part of K: x's rows (gathered by order)
+//                      and A[l] through a ring of 64-column stages, r columns of TMEM
+//   k_adapter_expand   a tile and some of the columns: the parts of K are added in order,
+//                      h is split into 16-bit parts (adapter.cu says why) that are the MMA's
+//                      A operand for all columns; tiles of B[l] and of base through a
+//                      ring, the sums from TMEM added to base in shared memory, whole
+//                      128-byte pieces of rows out
+//
+// HBM-bound: x, base and out pass once; the products' operands repeat from L2 and are small.
+// Two launches, not one: either product then has as many CTAs as fill the SMs twice,
+// whatever the number of tiles, and while one CTA of an SM fills its pipeline the other streams.
+//
+// Rows lie anywhere, so every 16-byte piece is copied by cp.async, by four warps, eight
+// lanes to a row's 128 bytes, to where the 128-byte swizzle wants it.
+#include "../../include/w8a8_block_fp8.h"
+#include "adapter.cuh"
+
+namespace w8a8 {
+namespace {
+
+using namespace lora;
+
+constexpr uint32_t kTileRows = 128;
+constexpr uint32_t kRowBytes = 128;                 // of an operand tile: 64 16-bit columns
+constexpr uint32_t kTileBytes = kTileRows * kRowBytes;
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, bool in)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Instruction descriptor of kind::f16: idesc_f16_f32 with the operands' format.
+template <bool BF16> __device__ __forceinline__ uint32_t idesc(uint32_t n)
+{
+    return idesc_f16_f32(128, n) | (BF16 ? (1u << 7) | (1u << 10) : 0u);
+}
+
+// Offset of 16-byte piece c of row r in a tile with the 128-byte swizzle.
+__device__ __forceinline__ uint32_t swizzled(uint32_t r, uint32_t c) { return r * kRowBytes + ((c ^ (r & 7u)) << 4); }
+
+// A ring's copies by one of 128 threads: after the copies of step i, those of step
+// i - (STAGES - 1) have landed; they are made visible to the tensor core's proxy and
+// announced.
+template <int STAGES> __device__ __forceinline__ void announce(uint32_t full, int i)
+{
+    cp_async_commit();
+    if (i >= STAGES - 1) {
+        cp_async_wait<STAGES - 1>();
+        fence_async_smem();
+        mbar_arrive(full + 8u * ((i - (STAGES - 1)) % STAGES));
+    }
+}
+template <int STAGES> __device__ __forceinline__ void announce_rest(uint32_t full, int n)
+{
+    cp_async_wait<0>();
+    fence_async_smem();
+    for (int i = n > STAGES - 1 ? n - (STAGES - 1) : 0; i < n; ++i)
+        mbar_arrive(full + 8u * (i % STAGES));
+}
+
+// ------------------------------------------------------------------ x A^T
+
+constexpr int kShrinkStages = 4;
+constexpr int kShrinkThreads = 160;         // warps 0-3 copy and store h, warp 4 issues MMAs
+constexpr int kMaxR = 128;
+
+constexpr size_t shrink_smem(int r_pad) { return 1024 + kShrinkStages * (kTileBytes + static_cast<size_t>(r_pad) * kRowBytes); }
+
+template <bool BF16> __global__ void __launch_bounds__(kShrinkThreads) k_adapter_shrink(const TileParams p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t bars[2 * kShrinkStages + 2];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_word, scratch[16], rows[kTileRows];
+    const uint32_t warp = warp_uniform(warp_index()), lane = lane_index(), t = threadIdx.x;
+    const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    const uint32_t full = smem_addr(bars), empty = full + 8u * kShrinkStages, done = empty + 8u * kShrinkStages,
+                   drain = done + 8u;
+    const uint32_t stage_bytes = kTileBytes + p.a.r_pad * kRowBytes;
+    uint32_t cols = 32;
+    while (cols < static_cast<uint32_t>(p.a.r_pad))
+        cols *= 2;
+    if (t == 0) {
+        for (int s = 0; s < kShrinkStages; ++s) {
+            mbar_init(full + 8u * s, 128);
+            mbar_init(empty + 8u * s, 1);
+        }
+        mbar_init(done, 1);
+        mbar_init(drain, 1);
+        abort_word = 0;
+        mbar_fence_init();
+    }
+    if (warp == 4) {
+        tmem_alloc(smem_addr(&tmem_slot), cols);
+        tmem_relinquish();
+    }
+    grid_dependency_wait();
+    // (only now: the second launch reads base and B before it waits for this one, so what
+    // made those has to be finished when it starts)
+    grid_launch_dependents();
+    const int tile = blockIdx.x / p.splits, split = blockIdx.x % p.splits;
+    const Item item = find_item<kShrinkThreads>(p.a, tile, kTileRows, p.a.L, scratch);
+    if (t < kTileRows) {
+        const int row = static_cast<int>(t) < item.rows ? p.a.order[item.first + t] : -1;
+        rows[t] = static_cast<unsigned>(row) < static_cast<unsigned>(p.a.T) ? row : -1;
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = tmem_slot;
+    const WaitGuard guard{&abort_word, p.status, p.wait_limit};
+    const int blocks = (p.a.K + 63) / 64;
+    const int lo = static_cast<int>(static_cast<long long>(blocks) * split / p.splits);
+    const int steps = item.rows ? static_cast<int>(static_cast<long long>(blocks) * (split + 1) / p.splits) - lo : 0;
+    if (warp < 4 && steps) {
+        const uint32_t c = t & 7u, r0 = t >> 3;
+        const uint16_t *const A = p.a.A + static_cast<long long>(item.adapter) * p.a.r * p.a.K;
+        const uint16_t *x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = rows[r0 + 16 * i];
+            x[i] = row >= 0 ? p.a.x + row * p.a.ld_x : nullptr;
+        }
+        bool ok = true;
+        for (int i = 0; i < steps; ++i) {
+            const int s = i % kShrinkStages;
+            ok = __all_sync(0xffffffffu, wait_bounded(empty + 8u * s, static_cast<uint32_t>(i / kShrinkStages & 1) ^ 1u,
+                                                      guard, SITE_TILED_PRODUCER));
+            if (!ok)
+                break;
+            const uint32_t dst = smem + s * stage_bytes;
+            const int k = (lo + i) * 64 + 8 * static_cast<int>(c);
+            const bool in = k < p.a.K;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                cp_async_16(dst + swizzled(r0 + 16 * j, c), in && x[j] ? x[j] + k : p.a.x, in && x[j]);
+            for (uint32_t r = r0; r < static_cast<uint32_t>(p.a.r_pad); r += 16) {
+                const bool there = in && static_cast<int>(r) < p.a.r;
+                cp_async_16(dst + kTileBytes + swizzled(r, c), there ? A + static_cast<long long>(r) * p.a.K + k : A, there);
+            }
+            announce<kShrinkStages>(full, i);
+        }
+        if (ok)
+            announce_rest<kShrinkStages>(full, steps);
+        else
+            cp_async_wait<0>();
+        // h of this part of K
+        if (ok && __all_sync(0xffffffffu, wait_bounded(done, 0, guard, SITE_TILED_PROMOTE))) {
+            tc_fence_after_sync();
+            const float scale = p.a.scales ? p.a.scales[item.adapter] : 1.f;
+            float *const h = p.h + (static_cast<long long>(split) * p.a.T + item.first + t) * p.a.r_pad;
+            for (int j = 0; j < p.a.r_pad; j += 32) {
+                float v[32];
+                __syncwarp();
+                tmem_load_32cols(tmem + ((warp * 32u) << 16) + j, v);
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                    if (static_cast<int>(t) < item.rows && j + i < p.a.r_pad)
+                        *reinterpret_cast<float4 *>(h + j + i) =
+                            make_float4(v[i] * scale, v[i + 1] * scale, v[i + 2] * scale, v[i + 3] * scale);
+            }
+        }
+    } else if (warp == 4 && steps) {
+        const uint32_t d = idesc<BF16>(p.a.r_pad);
+        bool ok = true;
+        for (int i = 0; i < steps && ok; ++i) {
+            const int s = i % kShrinkStages;
+            ok = __all_sync(0xffffffffu, wait_bounded(full + 8u * s, static_cast<uint32_t>(i / kShrinkStages & 1), guard,
+                                                      SITE_TILED_MMA_FULL));
+            if (!ok)
+                break;
+            tc_fence_after_sync();
+            const uint64_t ad = sw128_kmajor_desc(smem + s * stage_bytes);
+            const uint64_t bd = sw128_kmajor_desc(smem + s * stage_bytes + kTileBytes);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                mma_f16_elect<false>(tmem, ad + 2u * k, bd + 2u * k, d, i + k > 0);
+            mma_commit_elect<false>(empty + 8u * s);
+        }
+        if (ok)
+            mma_commit_elect<false>(done);
+        // no commit arrives on this CTA's shared memory after it exits
+        mma_commit_elect<false>(drain);
+        wait_drain(drain, 0, p.status, p.wait_limit, (SITE_DRAIN << 8) | 4u);
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 4) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, cols);
+    }
+}
+
+// ------------------------------------------------------------------ base + h B^T
+
+constexpr int kExpandThreads = 288;         // warps 0-3 copy, 4-7 epilogue, 8 issues MMAs
+constexpr uint32_t kBasePitch = 144;        // a row's 128 bytes of base; rows 16 bytes apart in banks
+
+template <bool BF16, int OUT> struct Expand {
+    static constexpr int kTerms = BF16 && OUT == W8A8_OUT_FP32 ? 3 : 2;
+    static constexpr int kEach = OUT == W8A8_OUT_FP32 ? 4 : 8;          // elements of 16 bytes
+    static constexpr int kCols = 8 * kEach;                             // of a column tile
+    static constexpr uint32_t kBBytes = kCols * kRowBytes;              // for 64 columns of r
+    static __host__ __device__ constexpr uint32_t stage_bytes(int k_blocks) { return k_blocks * kBBytes + kTileRows * kBasePitch; }
+    static constexpr size_t smem(int k_blocks, int stages)
+    {
+        return 1024 + static_cast<size_t>(kTerms) * k_blocks * kTileBytes + static_cast<size_t>(stages) * stage_bytes(k_blocks);
+    }
+};
+
+template <bool BF16, int OUT, int STAGES>
+__global__ void __launch_bounds__(kExpandThreads) k_adapter_expand(const TileParams p)
+{
+    using X = Expand<BF16, OUT>;
+    constexpr int kCols = X::kCols, kEach = X::kEach, kTerms = X::kTerms, kOut = 16 / kEach;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t bars[2 * STAGES + 6];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_word, scratch[16], rows[kTileRows];
+    const uint32_t warp = warp_uniform(warp_index()), lane = lane_index(), t = threadIdx.x;
+    const uint32_t pad = ((smem_addr(smem_raw) + 1023u) & ~1023u) - smem_addr(smem_raw);
+    const int k_blocks = (p.a.r_pad + 63) / 64;
+    const uint32_t operand = smem_addr(smem_raw) + pad;
+    const uint32_t ring_at = pad + kTerms * k_blocks * kTileBytes, ring = smem_addr(smem_raw) + ring_at;
+    const uint32_t stage_bytes = X::stage_bytes(k_blocks), base_at = k_blocks * X::kBBytes;
+    const uint32_t full = smem_addr(bars), empty = full + 8u * STAGES, h_full = empty + 8u * STAGES, d_full = h_full + 8u,
+                   d_empty = d_full + 16u, drain = d_empty + 16u;
+    if (t == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(full + 8u * s, 128);
+            mbar_init(empty + 8u * s, 5);       // the MMAs' commit and four epilogue warps
+        }
+        mbar_init(h_full, 128);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(d_full + 8u * b, 1);
+            mbar_init(d_empty + 8u * b, 4);
+        }
+        mbar_init(drain, 1);
+        abort_word = 0;
+        mbar_fence_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(smem_addr(&tmem_slot), 2 * kCols);
+        tmem_relinquish();
+    }
+    const int tile = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
+    const Item item = find_item<kExpandThreads>(p.a, tile, kTileRows, p.a.out == p.a.base ? p.a.L : p.a.L + 1, scratch);
+    if (t < kTileRows) {
+        const int row = static_cast<int>(t) < item.rows ? p.a.order[item.first + t] : -1;
+        rows[t] = static_cast<unsigned>(row) < static_cast<unsigned>(p.a.T) ? row : -1;
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = tmem_slot;
+    const WaitGuard guard{&abort_word, p.status, p.wait_limit};
+    const int col_tiles = (p.a.N + kCols - 1) / kCols;
+    const int lo = static_cast<int>(static_cast<long long>(col_tiles) * chunk / p.chunks);
+    const int hi = static_cast<int>(static_cast<long long>(col_tiles) * (chunk + 1) / p.chunks);
+    const int steps = item.rows && item.adapter < p.a.L ? hi - lo : 0;
+    const char *const base = static_cast<const char *>(p.a.base);
+    char *const out = static_cast<char *>(p.a.out);
+    if (warp < 4 && steps) {
+        // (h alone is the first launch's: nothing here waits for it)
+        const uint32_t c = t & 7u, r0 = t >> 3;
+        const uint16_t *const B = p.a.B + static_cast<long long>(item.adapter) * p.a.N * p.a.r;
+        const char *from[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = rows[r0 + 16 * i];
+            from[i] = row >= 0 ? base + row * p.a.ld_base * kOut : nullptr;
+        }
+        bool ok = true;
+        for (int i = 0; i < steps; ++i) {
+            const int s = i % STAGES;
+            ok = __all_sync(0xffffffffu, wait_bounded(empty + 8u * s, static_cast<uint32_t>(i / STAGES & 1) ^ 1u, guard,
+                                                      SITE_TILED_PRODUCER));
+            if (!ok)
+                break;
+            const uint32_t dst = ring + s * stage_bytes;
+            const int n0 = (lo + i) * kCols, col = n0 + static_cast<int>(c) * kEach;
+            const bool in = col < p.a.N;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                cp_async_16(dst + base_at + (r0 + 16 * j) * kBasePitch + 16 * c,
+                            in && from[j] ? from[j] + static_cast<long long>(col) * kOut : base, in && from[j]);
+            for (int q = 0; q < k_blocks; ++q) {
+                const int k = 64 * q + 8 * static_cast<int>(c);
+                if (k < p.a.r_pad)
+#pragma unroll
+                    for (int j = 0; j < kCols / 16; ++j) {
+                        const int n = n0 + static_cast<int>(r0) + 16 * j;
+                        const bool there = n < p.a.N && k < p.a.r;
+                        cp_async_16(dst + q * X::kBBytes + swizzled(r0 + 16 * j, c),
+                                    there ? B + static_cast<long long>(n) * p.a.r + k : B, there);
+                    }
+            }
+            announce<STAGES>(full, i);
+        }
+        if (ok)
+            announce_rest<STAGES>(full, steps);
+        else
+            cp_async_wait<0>();
+    }
+    grid_dependency_wait();
+    grid_launch_dependents();
+    if (warp >= 4 && warp < 8 && steps) {
+        // ---------------------------------------------------- h's parts, then the epilogue
+        const uint32_t e = warp - 4, row = e * 32 + lane;
+        const float *const h = p.h + (static_cast<long long>(item.first) + row) * p.a.r_pad;
+        const bool mine = static_cast<int>(row) < item.rows;
+        const long long plane = static_cast<long long>(p.a.T) * p.a.r_pad;
+        auto load = [&](int k, float (&v)[8]) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = 0.f;
+            if (!mine || k >= p.a.r_pad)
+                return;
+            for (int s = 0; s < p.splits; ++s) {
+                const float4 a = *reinterpret_cast<const float4 *>(h + s * plane + k);
+                const float4 b = *reinterpret_cast<const float4 *>(h + s * plane + k + 4);
+                v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+                v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+            }
+        };
+        float factor = 1.f, shrink = 1.f;
+        if constexpr (!BF16) {
+            float top = 0.f;
+            for (int k = 0; k < p.a.r_pad; k += 8) {
+                float v[8];
+                load(k, v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    top = fmaxf(top, fabsf(v[i]));
+            }
+            power_of(top, &shrink, &factor);
+        }
+        for (int k = 0; k < p.a.r_pad; k += 8) {
+            float v[8];
+            load(k, v);
+            if constexpr (!BF16) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[i] *= shrink;
+            }
+#pragma unroll
+            for (int q = 0; q < kTerms; ++q) {
+                uint32_t w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    w[i] = take_part<BF16>(v[i]);
+                const uint32_t at = operand + (q * k_blocks + k / 64) * kTileBytes + swizzled(row, (k & 63) / 8);
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[1] << 16 | w[0]),
+                             "r"(w[3] << 16 | w[2]), "r"(w[5] << 16 | w[4]), "r"(w[7] << 16 | w[6])
+                             : "memory");
+            }
+        }
+        fence_async_smem();
+        mbar_arrive(h_full);
+        bool ok = true;
+        for (int i = 0; i < steps; ++i) {
+            const int s = i % STAGES, b = i & 1;
+            ok = __all_sync(0xffffffffu,
+                            wait_bounded(full + 8u * s, static_cast<uint32_t>(i / STAGES & 1), guard, SITE_TILED_PROMOTE) &&
+                                wait_bounded(d_full + 8u * b, static_cast<uint32_t>(i / 2 & 1), guard, SITE_TILED_PROMOTE));
+            if (!ok)
+                break;
+            tc_fence_after_sync();
+            const uint32_t tile_at = ring_at + s * stage_bytes + base_at;
+            uint8_t *const own = smem_raw + tile_at + row * kBasePitch;
+#pragma unroll
+            for (int j = 0; j < kCols; j += 32) {
+                float v[32];
+                tmem_load_32cols(tmem + ((e * 32u) << 16) + b * kCols + j, v);
+                if (j + 32 == kCols) {
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(d_empty + 8u * b);
+                }
+#pragma unroll
+                for (int q = 0; q < 32; q += kEach) {
+                    uint4 *const piece = reinterpret_cast<uint4 *>(own + (j + q) * kOut);
+                    const uint4 u = *piece;
+                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                    uint32_t o[4];
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        if constexpr (OUT == W8A8_OUT_FP32) {
+                            o[z] = __float_as_uint(fmaf(v[q + z], factor, __uint_as_float(w[z])));
+                        } else if constexpr (BF16) {
+                            o[z] = pack_bf16x2(v[q + 2 * z] + __uint_as_float(w[z] << 16),
+                                               v[q + 2 * z + 1] + __uint_as_float(w[z] & 0xffff0000u));
+                        } else {
+                            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[z]));
+                            o[z] = pack_f16x2(fmaf(v[q + 2 * z], factor, f.x), fmaf(v[q + 2 * z + 1], factor, f.y));
+                        }
+                    }
+                    *piece = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+            }
+            __syncwarp();
+            // out: eight lanes to a row's 128 bytes
+            const uint32_t c = lane & 7u;
+            const int col = (lo + i) * kCols + static_cast<int>(c) * kEach;
+            if (col < p.a.N)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t r = e * 32 + (lane >> 3) + 4 * j;
+                    const int to = rows[r];
+                    if (to >= 0)
+                        *reinterpret_cast<uint4 *>(out + (to * p.a.ld_out + col) * kOut) =
+                            *reinterpret_cast<const uint4 *>(smem_raw + tile_at + r * kBasePitch + 16 * c);
+                }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(empty + 8u * s);
+        }
+    } else if (warp == 8 && steps) {
+        // ---------------------------------------------------- MMAs
+        const uint32_t d = idesc<BF16>(kCols);
+        bool ok = __all_sync(0xffffffffu, wait_bounded(h_full, 0, guard, SITE_TILED_MMA_FULL));
+        for (int i = 0; i < steps && ok; ++i) {
+            const int s = i % STAGES, b = i & 1;
+            ok = __all_sync(0xffffffffu, wait_bounded(d_empty + 8u * b, static_cast<uint32_t>(i / 2 & 1) ^ 1u, guard,
+                                                      SITE_TILED_MMA_TMEM) &&
+                                             wait_bounded(full + 8u * s, static_cast<uint32_t>(i / STAGES & 1), guard,
+                                                          SITE_TILED_MMA_FULL));
+            if (!ok)
+                break;
+            tc_fence_after_sync();
+            uint32_t more = 0;
+            for (int q = 0; q < k_blocks; ++q) {
+                const uint64_t bd = sw128_kmajor_desc(ring + s * stage_bytes + q * X::kBBytes);
+                const int ks = min(4, (p.a.r_pad - 64 * q) / 16);
+                for (int z = 0; z < kTerms; ++z) {
+                    const uint64_t ad = sw128_kmajor_desc(operand + (z * k_blocks + q) * kTileBytes);
+                    for (int k = 0; k < ks; ++k) {
+                        mma_f16_elect<false>(tmem + b * kCols, ad + 2u * k, bd + 2u * k, d, more);
+                        more = 1;
+                    }
+                }
+            }
+            mma_commit_elect<false>(empty + 8u * s);
+            mma_commit_elect<false>(d_full + 8u * b);
+        }
+        // no commit arrives on this CTA's shared memory, and none reads it, after it exits
+        mma_commit_elect<false>(drain);
+        wait_drain(drain, 0, p.status, p.wait_limit, (SITE_DRAIN << 8) | 4u);
+    }
+    if (item.rows && item.adapter == p.a.L) {
+        // rows without an adapter
+        const int from = lo * kCols, to = min(hi * kCols, p.a.N);
+        for (int i = warp; i < item.rows; i += kExpandThreads / 32)
+            if (const int row = rows[i]; row >= 0)
+                for (int n = from + static_cast<int>(lane) * kEach; n < to; n += 32 * kEach)
+                    *reinterpret_cast<uint4 *>(out + (row * p.a.ld_out + n) * kOut) =
+                        *reinterpret_cast<const uint4 *>(base + (row * p.a.ld_base + n) * kOut);
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, 2 * kCols);
+    }
+}
+
+template <class Kernel> cudaError_t launch(Kernel kernel, const TileParams &p, long long ctas, int threads, size_t smem,
+                                           volatile int *flags, cudaStream_t stream)
+{
+    if (const cudaError_t e = allow_smem(kernel, 224 * 1024, flags); e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+    lc.blockDim = dim3(threads, 1, 1);
+    lc.dynamicSmemBytes = smem;
+    lc.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelEx(&lc, kernel, p);
+}
+
+template <bool BF16, int OUT, int STAGES> cudaError_t launch_expand(const TileParams &p, long long ctas, cudaStream_t s)
+{
+    static volatile int flags[kMaxDeviceFlags] = {};
+    return launch(k_adapter_expand<BF16, OUT, STAGES>, p, ctas, kExpandThreads,
+                  Expand<BF16, OUT>::smem((p.a.r_pad + 63) / 64, STAGES), flags, s);
+}
+
+template <bool BF16, int OUT> cudaError_t launch_both(TileParams p, const DeviceView &dev, cudaStream_t stream)
+{
+    const long long tiles = most_items(p.a.T, p.a.L, kTileRows);
+    static volatile int flags[kMaxDeviceFlags] = {};
+    cudaError_t e = launch(k_adapter_shrink<BF16>, p, tiles * p.splits, kShrinkThreads, shrink_smem(p.a.r_pad), flags, stream);
+    if (e != cudaSuccess)
+        return e;
+    const long long all = most_items(p.a.T, p.a.out == p.a.base ? p.a.L : p.a.L + 1, kTileRows);
+    const int col_tiles = (p.a.N + Expand<BF16, OUT>::kCols - 1) / Expand<BF16, OUT>::kCols;
+    // As many CTAs as fill the SMs twice, with at least four column tiles each.
+    p.chunks = static_cast<int>(std::max(1ll, std::min<long long>((2ll * dev.sm_count + all - 1) / all, col_tiles / 4)));
+    constexpr size_t kHalf = 113 * 1024;        // two CTAs to an SM
+    const int k_blocks = (p.a.r_pad + 63) / 64;
+    using X = Expand<BF16, OUT>;
+    if (X::smem(k_blocks, 3) + 2048 <= kHalf)
+        return launch_expand<BF16, OUT, 3>(p, all * p.chunks, stream);
+    if (X::smem(k_blocks, 2) + 2048 <= kHalf)
+        return launch_expand<BF16, OUT, 2>(p, all * p.chunks, stream);
+    return launch_expand<BF16, OUT, 4>(p, all * p.chunks, stream);
+}
+
+bool on(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+}  // namespace
+
+namespace lora {
+
+bool tile_takes(const AdapterParams &p, int out_kind)
+{
+    const int each = out_kind == W8A8_OUT_FP32 ? 4 : 8;
+    return p.r >= 8 && p.r <= kMaxR && p.r % 8 == 0 && p.K >= 64 && p.vec_k && on(p.B, 16) && p.N % each == 0 &&
+           p.ld_base % each == 0 && p.ld_out % each == 0 && on(p.base, 16) && on(p.out, 16);
+}
+
+// (The workspace's size goes by it: a GB300's SMs, so that no device is asked.)
+constexpr int kSms = 152;
+int tile_splits(const AdapterParams &p)
+{
+    // CTAs that fill the SMs twice, with at least four steps of 64 columns each
+    const long long tiles = most_items(p.T, p.L, kTileRows);
+    return static_cast<int>(std::max(1ll, std::min<long long>({(2ll * kSms + tiles - 1) / tiles, p.K / 256, 8})));
+}
+
+cudaError_t launch_tile(const AdapterParams &a, int x_kind, int out_kind, float *h, const DeviceView &dev, cudaStream_t stream)
+{
+    TileParams p = {};
+    p.a = a;
+    p.h = h;
+    p.splits = tile_splits(a);
+    p.status = dev.status;
+    p.wait_limit = dev.wait_limit;
+    if (x_kind == W8A8_IN_BF16)
+        return out_kind == W8A8_OUT_FP32 ? launch_both<true, W8A8_OUT_FP32>(p, dev, stream)
+                                         : launch_both<true, W8A8_OUT_BF16>(p, dev, stream);
+    return out_kind == W8A8_OUT_FP32 ? launch_both<false, W8A8_OUT_FP32>(p, dev, stream)
+                                     : launch_both<false, W8A8_OUT_FP16>(p, dev, stream);
+}
+
+}  // namespace lora
+}  // namespace w8a8

@@ -32,7 +32,9 @@ typedef int (*combine_fn)(const void *, int, int64_t, int64_t, const int32_t *, 
                           stream_t);
 typedef int (*adapter_fn)(const void *, int, int64_t, const void *, const void *, const int32_t *,
                           const int32_t *, const float *, const void *, int64_t, void *, int,
-                          int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, stream_t);
+                          int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, void *, size_t,
+                          stream_t);
+typedef size_t (*adapter_size_fn)(int64_t, int64_t, int64_t, int64_t);
 
 static norm_fn f_norm;
 static ragged_fn f_ragged;
@@ -44,6 +46,7 @@ static group_fn f_group;
 static group_size_fn f_group_size;
 static combine_fn f_combine;
 static adapter_fn f_adapter;
+static adapter_size_fn f_adapter_size;
 
 /* Argument i as an integer; None is 0.  Sets an error for anything else. */
 static int64_t num(PyObject *const *args, int i)
@@ -401,6 +404,35 @@ static int is_current(long gpu)
     return ok;
 }
 
+/* Device scratch of `bytes`: a tensor of t's device on the current stream, a new
+ * reference, and its address; NULL and no address for 0.  0 on an error. */
+static int scratch_of(PyObject *t, size_t bytes, PyObject *u8, PyObject **keep, void **ptr)
+{
+    static PyObject *new_empty, *kw;
+    *keep = NULL;
+    *ptr = NULL;
+    if (!bytes)
+        return 1;
+    if (!new_empty && !(new_empty = PyUnicode_InternFromString("new_empty")))
+        return 0;
+    if (!kw && !(kw = Py_BuildValue("(s)", "dtype")))
+        return 0;
+    PyObject *n = PyLong_FromSize_t(bytes);
+    PyObject *shape = n ? PyTuple_Pack(1, n) : NULL;
+    PyObject *call_args[3] = {t, shape, u8};
+    *keep = shape && u8 ? PyObject_VectorcallMethod(new_empty, call_args, 2, kw) : NULL;
+    Py_XDECREF(n);
+    Py_XDECREF(shape);
+    PyObject *o = *keep ? call(*keep, PTR_OF) : NULL;
+    if (o)
+        *ptr = (void *)(uintptr_t)PyLong_AsUnsignedLongLong(o);
+    Py_XDECREF(o);
+    if (o && !PyErr_Occurred())
+        return 1;
+    Py_CLEAR(*keep);
+    return 0;
+}
+
 /* The types of the routing calls: int32, float32, bool, uint8. */
 enum { R_INT32, R_F32, R_BOOL, R_U8 };
 
@@ -446,16 +478,19 @@ static PyObject *py_route_tensors(PyObject *self, PyObject *const *args, Py_ssiz
     const int kind = code_of(args[11], x.dtype), renormalize = PyObject_IsTrue(args[7]);
     const double scale = PyFloat_AsDouble(args[8]);
     const int scoring = I32(2), groups = I32(4), top_groups = I32(5), group_top = I32(6);
-    if (kind < 0 || renormalize < 0 || !is_current(gpu) || f_route_size(T, E, (int)k))
+    const size_t size = f_route_size(T, E, (int)k);
+    if (kind < 0 || renormalize < 0 || !is_current(gpu) || (size && args[13] != Py_None))
         goto other;
-    void *s = stream_of(args[13]);
-    if (PyErr_Occurred())
+    void *s = stream_of(args[13]), *scratch;
+    PyObject *keep;
+    if (PyErr_Occurred() || !scratch_of(args[0], size, type_at(args[12], R_U8), &keep, &scratch))
         goto other;
     int st;
     Py_BEGIN_ALLOW_THREADS
     st = f_route(x.ptr, kind, 0, bias.ptr, valid.ptr, T, E, (int)k, scoring, groups, top_groups, group_top,
-                 renormalize, (float)scale, o[0].ptr, o[1].ptr, o[2].ptr, o[3].ptr, o[4].ptr, NULL, 0, s);
+                 renormalize, (float)scale, o[0].ptr, o[1].ptr, o[2].ptr, o[3].ptr, o[4].ptr, scratch, size, s);
     Py_END_ALLOW_THREADS
+    Py_XDECREF(keep);
     return PyLong_FromLong(st);
 other:
     PyErr_Clear();
@@ -476,16 +511,19 @@ static PyObject *py_group_tensors(PyObject *self, PyObject *const *args, Py_ssiz
         !typed(PyTuple_GET_ITEM(args[2], 1), &offsets, &gpu, 1, i32))
         goto other;
     const int64_t count = ids.size[0], groups = I64(1);
+    const size_t size = f_group_size(count, groups);
     if (groups < 1 || !is(&order, 1, count, 0) || !is(&offsets, 1, groups + 1, 0) || !is_current(gpu) ||
-        f_group_size(count, groups))
+        (size && args[4] != Py_None))
         goto other;
-    void *s = stream_of(args[4]);
-    if (PyErr_Occurred())
+    void *s = stream_of(args[4]), *scratch;
+    PyObject *keep;
+    if (PyErr_Occurred() || !scratch_of(args[0], size, type_at(args[3], R_U8), &keep, &scratch))
         goto other;
     int st;
     Py_BEGIN_ALLOW_THREADS
-    st = f_group(ids.ptr, count, groups, order.ptr, offsets.ptr, NULL, NULL, 0, s);
+    st = f_group(ids.ptr, count, groups, order.ptr, offsets.ptr, NULL, scratch, size, s);
     Py_END_ALLOW_THREADS
+    Py_XDECREF(keep);
     return PyLong_FromLong(st);
 other:
     PyErr_Clear();
@@ -543,27 +581,31 @@ static PyObject *py_adapter_tensors(PyObject *self, PyObject *const *args, Py_ss
     if (args[6] != Py_None && (!typed(args[6], &scales, &gpu, 1, type_at(args[9], R_F32)) || !is(&scales, 1, L, 0)))
         goto other;
     const int kind = code_of(args[8], x.dtype), out_kind = code_of(args[8], out.dtype);
-    if (kind < 0 || out_kind < 0 || !is_current(gpu))
+    const size_t size = f_adapter_size(T, L, r, K);
+    if (kind < 0 || out_kind < 0 || !is_current(gpu) || (size && args[10] != Py_None))
         goto other;
-    void *s = stream_of(args[10]);
-    if (PyErr_Occurred())
+    void *s = stream_of(args[10]), *scratch;
+    PyObject *keep;
+    if (PyErr_Occurred() || !scratch_of(args[0], size, type_at(args[9], R_U8), &keep, &scratch))
         goto other;
     int st;
     Py_BEGIN_ALLOW_THREADS
     st = f_adapter(x.ptr, kind, 0, a.ptr, b.ptr, order.ptr, offsets.ptr, scales.ptr, base.ptr, 0, out.ptr, out_kind, 0,
-                   T, L, r, K, N, s);
+                   T, L, r, K, N, scratch, size, s);
     Py_END_ALLOW_THREADS
+    Py_XDECREF(keep);
     return PyLong_FromLong(st);
 other:
     PyErr_Clear();
     Py_RETURN_NONE;
 }
 
-/* bind_routing(route, its workspace size, group, its workspace size, combine, adapter) */
+/* bind_routing(route, its workspace size, group, its workspace size, combine, adapter, its
+ * workspace size) */
 static PyObject *py_bind_routing(PyObject *self, PyObject *const *args, Py_ssize_t n)
 {
     (void)self;
-    if (!want(n, 6, 1))
+    if (!want(n, 7, 1))
         return NULL;
     f_route = (route_fn)PTR(0);
     f_route_size = (route_size_fn)PTR(1);
@@ -571,6 +613,7 @@ static PyObject *py_bind_routing(PyObject *self, PyObject *const *args, Py_ssize
     f_group_size = (group_size_fn)PTR(3);
     f_combine = (combine_fn)PTR(4);
     f_adapter = (adapter_fn)PTR(5);
+    f_adapter_size = (adapter_size_fn)PTR(6);
     if (PyErr_Occurred())
         return NULL;
     Py_RETURN_NONE;

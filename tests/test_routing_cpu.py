@@ -50,6 +50,13 @@ def test_workspace_sizes():
     assert size(-1, 4) == size(1 << 20, 0) == size(1 << 31, 4) == size(1 << 20, w8.W8A8_GROUPS_MAX + 1) == 0
 
 
+    size = w8.w8a8_adapter_workspace_size
+    assert size(64, 32, 16, 4096) == 0 and size(16384, 16, 64, 4096) >= 16384 * 64 * 4
+    for bad in ((0, 1, 16, 64), (4096, 0, 16, 64), (4096, 1, 0, 64), (4096, 1, 16, 0), (1 << 28, 1, 16, 64),
+                (4096, 1, w8.W8A8_ADAPTER_MAX_R + 1, 64), (4096, w8.W8A8_GROUPS_MAX + 1, 16, 64)):
+        assert size(*bad) == 0
+
+
 def group(n=8, groups=4, **ptr):
     p = dict(ids=256, order=256, off=256, rows=0, ws=0, size=0)
     p.update(ptr)
@@ -84,10 +91,10 @@ def test_combine(kw, status):
 
 
 def adapters(T=4, L=2, r=16, K=64, N=32, dtype=0, out_dtype=0, ld_x=0, ld_base=0, ld_out=0, **ptr):
-    p = dict(x=256, A=256, B=256, order=256, off=256, scales=0, base=256, out=512)
+    p = dict(x=256, A=256, B=256, order=256, off=256, scales=0, base=256, out=512, ws=0, size=0)
     p.update(ptr)
     return w8.w8a8_adapter_matmul(p["x"], dtype, ld_x, p["A"], p["B"], p["order"], p["off"], p["scales"], p["base"], ld_base,
-                                  p["out"], out_dtype, ld_out, T, L, r, K, N, 0)
+                                  p["out"], out_dtype, ld_out, T, L, r, K, N, p["ws"], p["size"], 0)
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -97,7 +104,8 @@ def adapters(T=4, L=2, r=16, K=64, N=32, dtype=0, out_dtype=0, ld_x=0, ld_base=0
     (dict(out=256, ld_out=40), ARG), (dict(T=0), OK), (dict(N=0), OK), (dict(x=0), ARG), (dict(A=0), ARG), (dict(B=0), ARG),
     (dict(order=0), ARG), (dict(off=0), ARG), (dict(base=0), ARG), (dict(out=0), ARG), (dict(L=w8.W8A8_GROUPS_MAX + 1), UNS),
     (dict(r=w8.W8A8_ADAPTER_MAX_R + 1), UNS), (dict(T=1 << 28), UNS), (dict(K=(1 << 24) + 1), UNS), (dict(x=257), UNS),
-    (dict(base=258, out_dtype=2), UNS), (dict(scales=258), UNS), (dict(order=257), UNS),
+    (dict(base=258, out_dtype=2), UNS), (dict(scales=258), UNS), (dict(order=257), UNS), (dict(T=4096), WS),
+    (dict(T=4096, ws=256, size=4096), WS), (dict(T=4096, ws=264, size=1 << 30), WS),
 ])
 def test_adapters(kw, status):
     assert adapters(**kw) == status
@@ -126,7 +134,7 @@ def reached(request, monkeypatch):
     if real.route_tensors is None:
         pytest.skip("no extension module")
     entry = ctypes.CFUNCTYPE(ctypes.c_int)(enter)
-    real.route_tensors.__self__.bind_routing(*[ctypes.cast(entry, ctypes.c_void_p).value] * 6)
+    real.route_tensors.__self__.bind_routing(*[ctypes.cast(entry, ctypes.c_void_p).value] * 7)
     yield hits
     _binding._bind_pycall(ctypes.CDLL(w8.library_path()))
 
