@@ -148,11 +148,14 @@ template <bool BF16, int OUT, int NT> __global__ void __launch_bounds__(kThreads
     const int tile_lo = static_cast<int>(static_cast<long long>(n_tiles) * me / ctas);
     const int tile_hi = static_cast<int>(static_cast<long long>(n_tiles) * (me + 1) / ctas);
     if (item.adapter == p.L) {
-        const int lo = tile_lo * 16, hi = min(tile_hi * 16, p.N);
-        for (int i = warp; i < item.rows; i += kWarps)
-            if (const int row = rows[i]; row >= 0)
-                for (int n = lo + lane; n < hi; n += 32)
-                    store_out<OUT>(p.out, row * p.ld_out + n, load_out<OUT>(p.base, row * p.ld_base + n));
+        const int from = tile_lo * 16, to = min(tile_hi * 16, p.N);
+        constexpr int kElement = OUT == W8A8_OUT_FP32 ? 4 : 2;
+        if (p.vec_n)
+            copy_rows<uint4, kThreads>(p, rows, item.rows, from, to, kElement);
+        else if constexpr (kElement == 4)
+            copy_rows<uint32_t, kThreads>(p, rows, item.rows, from, to, kElement);
+        else
+            copy_rows<uint16_t, kThreads>(p, rows, item.rows, from, to, kElement);
         return;
     }
     const uint16_t *const A = p.A + static_cast<long long>(item.adapter) * p.r * p.K;
@@ -427,7 +430,9 @@ extern "C" w8a8_status w8a8_adapter_matmul(const void *x_dev, w8a8_in_dtype dtyp
     p.r_pad = static_cast<int>((r + 15) / 16 * 16);
     p.vec_k = K % 8 == 0 && ld_x % 8 == 0 && on(x_dev, 16) && on(A_dev, 16);
     p.vec_r = r % 4 == 0 && on(B_dev, 8);
-    const bool tiles = tiled(p) && tile_takes(p, out_dtype);
+    const int each = 16 / ob;
+    p.vec_n = N % each == 0 && ld_base % each == 0 && ld_out % each == 0 && on(base_dev, 16) && on(out_dev, 16);
+    const bool tiles = tiled(p) && tile_takes(p);
     if (const size_t need = tiles ? w8a8::workspace_bytes(p) : 0;
         need && (!workspace_dev || workspace_bytes < need || !on(workspace_dev, 16))) {
         char msg[160];

@@ -23,6 +23,7 @@ struct AdapterParams {
     int T, L, r, K, N;
     int r_pad;                  // r up to whole 16
     int vec_k, vec_r;           // 16-byte pieces of x and A, 8-byte pieces of B
+    int vec_n;                  // 16-byte pieces of base and out
 };
 
 // The power of two that brings a row of h, whose largest size is top, near 2^14: the
@@ -99,6 +100,37 @@ template <bool BF16> __device__ __forceinline__ uint32_t take_part(float &v)
     return bits;
 }
 
+// Copies columns [from, to) of rows[0 .. count-1] (-1: none) of base to out, by all threads
+// of the CTA; WORD is the piece that is copied at once.  Eight pieces of a thread are in
+// flight: with one, 128 rows of 8 KB took a CTA 100 us.
+template <typename WORD, int THREADS>
+__device__ __forceinline__ void copy_rows(const AdapterParams &p, const int *rows, int count, int from, int to, int element)
+{
+    constexpr int kFlight = 8;
+    const int each = static_cast<int>(sizeof(WORD)) / element, pieces = (to - from) / each;
+    const long long all = static_cast<long long>(pieces) * count;
+    for (long long i0 = threadIdx.x; i0 < all; i0 += THREADS * kFlight) {
+        WORD v[kFlight];
+        long long at[kFlight];
+#pragma unroll
+        for (int j = 0; j < kFlight; ++j) {
+            const long long i = i0 + j * THREADS;
+            at[j] = -1;
+            if (i < all) {
+                const int r = static_cast<int>(i / pieces), n = from + static_cast<int>(i - static_cast<long long>(r) * pieces) * each;
+                if (const int row = rows[r]; row >= 0) {
+                    at[j] = (row * p.ld_out + n) * element;
+                    v[j] = *reinterpret_cast<const WORD *>(static_cast<const char *>(p.base) + (row * p.ld_base + n) * element);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kFlight; ++j)
+            if (at[j] >= 0)
+                *reinterpret_cast<WORD *>(static_cast<char *>(p.out) + at[j]) = v[j];
+    }
+}
+
 // Up to `bytes` of dynamic shared memory for a kernel, set once per device by its own
 // flags.  (The device's most would leave nothing for the kernel's static arrays.)
 template <typename Kernel> inline cudaError_t allow_smem(Kernel kernel, size_t bytes, volatile int *set)
@@ -132,7 +164,7 @@ struct TileParams {
 };
 // Whether they take a problem (16-byte pieces everywhere, r in bounds), and by how
 // many parts of K.
-bool tile_takes(const AdapterParams &p, int out_kind);
+bool tile_takes(const AdapterParams &p);
 int tile_splits(const AdapterParams &p);
 cudaError_t launch_tile(const AdapterParams &p, int x_kind, int out_kind, float *h, const DeviceView &dev,
                         cudaStream_t stream);

@@ -14,7 +14,8 @@
 // whatever the number of tiles, and while one CTA of an SM fills its pipeline the other streams.
 //
 // Rows lie anywhere, so every 16-byte piece is copied by cp.async, by four warps, eight
-// lanes to a row's 128 bytes, to where the 128-byte swizzle wants it.
+// lanes to a row's 128 bytes, to where the 128-byte swizzle wants it; a stage's barrier
+// completes when all of its copies have landed.
 #include "../../include/w8a8_block_fp8.h"
 #include "adapter.cuh"
 
@@ -31,8 +32,12 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, bool 
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// The same from rows that are read on in the next steps: L2 fetches 256 bytes at a time.
+__device__ __forceinline__ void cp_async_16_ahead(uint32_t dst, const void *src, bool in)
+{
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0)
+                 : "memory");
+}
 
 // Instruction descriptor of kind::f16: idesc_f16_f32 with the operands' format.
 template <bool BF16> __device__ __forceinline__ uint32_t idesc(uint32_t n)
@@ -42,26 +47,6 @@ template <bool BF16> __device__ __forceinline__ uint32_t idesc(uint32_t n)
 
 // Offset of 16-byte piece c of row r in a tile with the 128-byte swizzle.
 __device__ __forceinline__ uint32_t swizzled(uint32_t r, uint32_t c) { return r * kRowBytes + ((c ^ (r & 7u)) << 4); }
-
-// A ring's copies by one of 128 threads: after the copies of step i, those of step
-// i - (STAGES - 1) have landed; they are made visible to the tensor core's proxy and
-// announced.
-template <int STAGES> __device__ __forceinline__ void announce(uint32_t full, int i)
-{
-    cp_async_commit();
-    if (i >= STAGES - 1) {
-        cp_async_wait<STAGES - 1>();
-        fence_async_smem();
-        mbar_arrive(full + 8u * ((i - (STAGES - 1)) % STAGES));
-    }
-}
-template <int STAGES> __device__ __forceinline__ void announce_rest(uint32_t full, int n)
-{
-    cp_async_wait<0>();
-    fence_async_smem();
-    for (int i = n > STAGES - 1 ? n - (STAGES - 1) : 0; i < n; ++i)
-        mbar_arrive(full + 8u * (i % STAGES));
-}
 
 // ------------------------------------------------------------------ x A^T
 
@@ -138,17 +123,14 @@ template <bool BF16> __global__ void __launch_bounds__(kShrinkThreads) k_adapter
             const bool in = k < p.a.K;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                cp_async_16(dst + swizzled(r0 + 16 * j, c), in && x[j] ? x[j] + k : p.a.x, in && x[j]);
+                cp_async_16_ahead(dst + swizzled(r0 + 16 * j, c), in && x[j] ? x[j] + k : p.a.x, in && x[j]);
             for (uint32_t r = r0; r < static_cast<uint32_t>(p.a.r_pad); r += 16) {
                 const bool there = in && static_cast<int>(r) < p.a.r;
                 cp_async_16(dst + kTileBytes + swizzled(r, c), there ? A + static_cast<long long>(r) * p.a.K + k : A, there);
             }
-            announce<kShrinkStages>(full, i);
+            cp_async_arrive(full + 8u * s);
         }
-        if (ok)
-            announce_rest<kShrinkStages>(full, steps);
-        else
-            cp_async_wait<0>();
+        cp_async_wait_all();
         // h of this part of K
         if (ok && __all_sync(0xffffffffu, wait_bounded(done, 0, guard, SITE_TILED_PROMOTE))) {
             tc_fence_after_sync();
@@ -174,6 +156,7 @@ template <bool BF16> __global__ void __launch_bounds__(kShrinkThreads) k_adapter
                                                       SITE_TILED_MMA_FULL));
             if (!ok)
                 break;
+            fence_async_smem();         // the copies, which this warp has seen land, for the MMAs
             tc_fence_after_sync();
             const uint64_t ad = sw128_kmajor_desc(smem + s * stage_bytes);
             const uint64_t bd = sw128_kmajor_desc(smem + s * stage_bytes + kTileBytes);
@@ -287,7 +270,7 @@ __global__ void __launch_bounds__(kExpandThreads) k_adapter_expand(const TilePar
             const bool in = col < p.a.N;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                cp_async_16(dst + base_at + (r0 + 16 * j) * kBasePitch + 16 * c,
+                cp_async_16_ahead(dst + base_at + (r0 + 16 * j) * kBasePitch + 16 * c,
                             in && from[j] ? from[j] + static_cast<long long>(col) * kOut : base, in && from[j]);
             for (int q = 0; q < k_blocks; ++q) {
                 const int k = 64 * q + 8 * static_cast<int>(c);
@@ -300,12 +283,9 @@ __global__ void __launch_bounds__(kExpandThreads) k_adapter_expand(const TilePar
                                     there ? B + static_cast<long long>(n) * p.a.r + k : B, there);
                     }
             }
-            announce<STAGES>(full, i);
+            cp_async_arrive(full + 8u * s);
         }
-        if (ok)
-            announce_rest<STAGES>(full, steps);
-        else
-            cp_async_wait<0>();
+        cp_async_wait_all();
     }
     grid_dependency_wait();
     grid_launch_dependents();
@@ -433,6 +413,7 @@ __global__ void __launch_bounds__(kExpandThreads) k_adapter_expand(const TilePar
                                                           SITE_TILED_MMA_FULL));
             if (!ok)
                 break;
+            fence_async_smem();         // the copies, which this warp has seen land, for the MMAs
             tc_fence_after_sync();
             uint32_t more = 0;
             for (int q = 0; q < k_blocks; ++q) {
@@ -455,12 +436,7 @@ __global__ void __launch_bounds__(kExpandThreads) k_adapter_expand(const TilePar
     }
     if (item.rows && item.adapter == p.a.L) {
         // rows without an adapter
-        const int from = lo * kCols, to = min(hi * kCols, p.a.N);
-        for (int i = warp; i < item.rows; i += kExpandThreads / 32)
-            if (const int row = rows[i]; row >= 0)
-                for (int n = from + static_cast<int>(lane) * kEach; n < to; n += 32 * kEach)
-                    *reinterpret_cast<uint4 *>(out + (row * p.a.ld_out + n) * kOut) =
-                        *reinterpret_cast<const uint4 *>(base + (row * p.a.ld_base + n) * kOut);
+        copy_rows<uint4, kExpandThreads>(p.a, rows, item.rows, lo * kCols, min(hi * kCols, p.a.N), kOut);
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -469,6 +445,10 @@ __global__ void __launch_bounds__(kExpandThreads) k_adapter_expand(const TilePar
         tmem_dealloc(tmem, 2 * kCols);
     }
 }
+
+// Tiles of a problem where half of the adapters' last ones are full (the most there can be are
+// launched; those without rows leave at once).
+long long likely_tiles(const AdapterParams &p) { return p.T / kTileRows + std::min(p.T, p.L) / 2 + 1; }
 
 template <class Kernel> cudaError_t launch(Kernel kernel, const TileParams &p, long long ctas, int threads, size_t smem,
                                            volatile int *flags, cudaStream_t stream)
@@ -505,7 +485,7 @@ template <bool BF16, int OUT> cudaError_t launch_both(TileParams p, const Device
     const long long all = most_items(p.a.T, p.a.out == p.a.base ? p.a.L : p.a.L + 1, kTileRows);
     const int col_tiles = (p.a.N + Expand<BF16, OUT>::kCols - 1) / Expand<BF16, OUT>::kCols;
     // As many CTAs as fill the SMs twice, with at least four column tiles each.
-    p.chunks = static_cast<int>(std::max(1ll, std::min<long long>((2ll * dev.sm_count + all - 1) / all, col_tiles / 4)));
+    p.chunks = static_cast<int>(std::max(1ll, std::min<long long>(2ll * dev.sm_count / likely_tiles(p.a), col_tiles / 4)));
     constexpr size_t kHalf = 113 * 1024;        // two CTAs to an SM
     const int k_blocks = (p.a.r_pad + 63) / 64;
     using X = Expand<BF16, OUT>;
@@ -522,11 +502,9 @@ bool on(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a 
 
 namespace lora {
 
-bool tile_takes(const AdapterParams &p, int out_kind)
+bool tile_takes(const AdapterParams &p)
 {
-    const int each = out_kind == W8A8_OUT_FP32 ? 4 : 8;
-    return p.r >= 8 && p.r <= kMaxR && p.r % 8 == 0 && p.K >= 64 && p.vec_k && on(p.B, 16) && p.N % each == 0 &&
-           p.ld_base % each == 0 && p.ld_out % each == 0 && on(p.base, 16) && on(p.out, 16);
+    return p.r >= 8 && p.r <= kMaxR && p.r % 8 == 0 && p.K >= 64 && p.vec_k && p.vec_n && on(p.B, 16);
 }
 
 // (The workspace's size goes by it: a GB300's SMs, so that no device is asked.)
@@ -534,8 +512,7 @@ constexpr int kSms = 152;
 int tile_splits(const AdapterParams &p)
 {
     // CTAs that fill the SMs twice, with at least four steps of 64 columns each
-    const long long tiles = most_items(p.T, p.L, kTileRows);
-    return static_cast<int>(std::max(1ll, std::min<long long>({(2ll * kSms + tiles - 1) / tiles, p.K / 256, 8})));
+    return static_cast<int>(std::max(1ll, std::min<long long>({2ll * kSms / likely_tiles(p), p.K / 256, 8})));
 }
 
 cudaError_t launch_tile(const AdapterParams &a, int x_kind, int out_kind, float *h, const DeviceView &dev, cudaStream_t stream)
