@@ -13,9 +13,8 @@
 // Two launches, not one: either product then has as many CTAs as fill the SMs twice,
 // whatever the number of tiles, and while one CTA of an SM fills its pipeline the other streams.
 //
-// Rows lie anywhere, so every 16-byte piece is copied by cp.async, by four warps, eight
-// lanes to a row's 128 bytes, to where the 128-byte swizzle wants it; a stage's barrier
-// completes when all of its copies have landed.
+// Rows lie anywhere, but mostly one after the other (a request's tokens): 32 rows of a tile
+// that do are one TMA box, others are gathered four at a time.
 #include "../../include/w8a8_block_fp8.h"
 #include "adapter.cuh"
 
@@ -28,17 +27,6 @@ constexpr uint32_t kTileRows = 128;
 constexpr uint32_t kRowBytes = 128;                 // of an operand tile: 64 16-bit columns
 constexpr uint32_t kTileBytes = kTileRows * kRowBytes;
 
-__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, bool in)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
-}
-// The same from rows that are read on in the next steps: L2 fetches 256 bytes at a time.
-__device__ __forceinline__ void cp_async_16_ahead(uint32_t dst, const void *src, bool in)
-{
-    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0)
-                 : "memory");
-}
-
 // Instruction descriptor of kind::f16: idesc_f16_f32 with the operands' format.
 template <bool BF16> __device__ __forceinline__ uint32_t idesc(uint32_t n)
 {
@@ -48,37 +36,88 @@ template <bool BF16> __device__ __forceinline__ uint32_t idesc(uint32_t n)
 // Offset of 16-byte piece c of row r in a tile with the 128-byte swizzle.
 __device__ __forceinline__ uint32_t swizzled(uint32_t r, uint32_t c) { return r * kRowBytes + ((c ^ (r & 7u)) << 4); }
 
+// Rows of a tile as a producer warp loads them: lane 8 i for the 32 rows of part i, if
+// they follow one another (rows behind the item's last are then some others', whose sums go
+// nowhere), else each of the part's lanes four of them, -1 as the row past the last: zeros.
+// (All by four: 16384 rows in order, rank 64, 97 us; by boxes see k_adapter_expand.)
+struct RowLoads {
+    int row[4];
+    uint32_t lane;
+    bool box, any;
+    __device__ __forceinline__ RowLoads(const int *list, int count, int T) : lane(lane_index())
+    {
+        const int first = list[lane / 8 * 32];
+        bool follow = first >= 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int at = 4 * lane + i, r = list[at];
+            follow = follow && (at >= count || r == first + (at & 31));
+            row[i] = r >= 0 ? r : T;
+        }
+        const uint32_t yes = __ballot_sync(0xffffffffu, follow);
+        box = (yes >> (lane & 24u) & 0xffu) == 0xffu;
+        any = !box || (lane & 7u) == 0;
+        if (box)
+            row[0] = first;
+    }
+    __device__ __forceinline__ void operator()(uint32_t dst, const CUtensorMap *one, const CUtensorMap *boxes, uint32_t bar,
+                                               int x) const
+    {
+        if (box && any)
+            tma_load_2d(dst + lane * 4 * kRowBytes, boxes, bar, x, row[0]);
+        else if (any)
+            tma_gather4(dst + lane * 4 * kRowBytes, one, bar, x, row[0], row[1], row[2], row[3]);
+    }
+};
+
+// After an abort: the loads still landing, the last into each stage of `issued` steps.
+template <int STAGES> __device__ __forceinline__ void drain_loads(uint32_t full, int issued, unsigned *status,
+                                                                  unsigned long long limit)
+{
+    for (int i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
+        wait_drain(full + 8u * (i % STAGES), static_cast<uint32_t>(i / STAGES & 1), status, limit, (SITE_DRAIN << 8) | 4u);
+}
+
 // ------------------------------------------------------------------ x A^T
 
-constexpr int kShrinkStages = 4;
-constexpr int kShrinkThreads = 160;         // warps 0-3 copy and store h, warp 4 issues MMAs
+constexpr int kShrinkThreads = 192;         // warps 0-3 store h, 4 issues MMAs, 5 loads
 constexpr int kMaxR = 128;
 
-constexpr size_t shrink_smem(int r_pad) { return 1024 + kShrinkStages * (kTileBytes + static_cast<size_t>(r_pad) * kRowBytes); }
+constexpr size_t shrink_smem(int r_pad, int stages)
+{
+    return 1024 + stages * (kTileBytes + static_cast<size_t>(r_pad) * kRowBytes);
+}
 
-template <bool BF16> __global__ void __launch_bounds__(kShrinkThreads) k_adapter_shrink(const TileParams p)
+template <bool BF16, int STAGES> __global__ void __launch_bounds__(kShrinkThreads) k_adapter_shrink(
+    const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_x32,
+    const __grid_constant__ CUtensorMap map_a, const TileParams p)
 {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t bars[2 * kShrinkStages + 2];
+    __shared__ uint64_t bars[2 * STAGES + 2];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_word, scratch[16], rows[kTileRows];
     const uint32_t warp = warp_uniform(warp_index()), lane = lane_index(), t = threadIdx.x;
     const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
-    const uint32_t full = smem_addr(bars), empty = full + 8u * kShrinkStages, done = empty + 8u * kShrinkStages,
+    const uint32_t full = smem_addr(bars), empty = full + 8u * STAGES, done = empty + 8u * STAGES,
                    drain = done + 8u;
     const uint32_t stage_bytes = kTileBytes + p.a.r_pad * kRowBytes;
     uint32_t cols = 32;
     while (cols < static_cast<uint32_t>(p.a.r_pad))
         cols *= 2;
     if (t == 0) {
-        for (int s = 0; s < kShrinkStages; ++s) {
-            mbar_init(full + 8u * s, 128);
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(full + 8u * s, 1);
             mbar_init(empty + 8u * s, 1);
         }
         mbar_init(done, 1);
         mbar_init(drain, 1);
         abort_word = 0;
         mbar_fence_init();
+    }
+    if (warp == 5 && lane == 0) {
+        tma_prefetch_map(&map_x);
+        tma_prefetch_map(&map_x32);
+        tma_prefetch_map(&map_a);
     }
     if (warp == 4) {
         tmem_alloc(smem_addr(&tmem_slot), cols);
@@ -103,36 +142,8 @@ template <bool BF16> __global__ void __launch_bounds__(kShrinkThreads) k_adapter
     const int lo = static_cast<int>(static_cast<long long>(blocks) * split / p.splits);
     const int steps = item.rows ? static_cast<int>(static_cast<long long>(blocks) * (split + 1) / p.splits) - lo : 0;
     if (warp < 4 && steps) {
-        const uint32_t c = t & 7u, r0 = t >> 3;
-        const uint16_t *const A = p.a.A + static_cast<long long>(item.adapter) * p.a.r * p.a.K;
-        const uint16_t *x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int row = rows[r0 + 16 * i];
-            x[i] = row >= 0 ? p.a.x + row * p.a.ld_x : nullptr;
-        }
-        bool ok = true;
-        for (int i = 0; i < steps; ++i) {
-            const int s = i % kShrinkStages;
-            ok = __all_sync(0xffffffffu, wait_bounded(empty + 8u * s, static_cast<uint32_t>(i / kShrinkStages & 1) ^ 1u,
-                                                      guard, SITE_TILED_PRODUCER));
-            if (!ok)
-                break;
-            const uint32_t dst = smem + s * stage_bytes;
-            const int k = (lo + i) * 64 + 8 * static_cast<int>(c);
-            const bool in = k < p.a.K;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                cp_async_16_ahead(dst + swizzled(r0 + 16 * j, c), in && x[j] ? x[j] + k : p.a.x, in && x[j]);
-            for (uint32_t r = r0; r < static_cast<uint32_t>(p.a.r_pad); r += 16) {
-                const bool there = in && static_cast<int>(r) < p.a.r;
-                cp_async_16(dst + kTileBytes + swizzled(r, c), there ? A + static_cast<long long>(r) * p.a.K + k : A, there);
-            }
-            cp_async_arrive(full + 8u * s);
-        }
-        cp_async_wait_all();
         // h of this part of K
-        if (ok && __all_sync(0xffffffffu, wait_bounded(done, 0, guard, SITE_TILED_PROMOTE))) {
+        if (__all_sync(0xffffffffu, wait_bounded(done, 0, guard, SITE_TILED_PROMOTE))) {
             tc_fence_after_sync();
             const float scale = p.a.scales ? p.a.scales[item.adapter] : 1.f;
             float *const h = p.h + (static_cast<long long>(split) * p.a.T + item.first + t) * p.a.r_pad;
@@ -151,12 +162,11 @@ template <bool BF16> __global__ void __launch_bounds__(kShrinkThreads) k_adapter
         const uint32_t d = idesc<BF16>(p.a.r_pad);
         bool ok = true;
         for (int i = 0; i < steps && ok; ++i) {
-            const int s = i % kShrinkStages;
-            ok = __all_sync(0xffffffffu, wait_bounded(full + 8u * s, static_cast<uint32_t>(i / kShrinkStages & 1), guard,
+            const int s = i % STAGES;
+            ok = __all_sync(0xffffffffu, wait_bounded(full + 8u * s, static_cast<uint32_t>(i / STAGES & 1), guard,
                                                       SITE_TILED_MMA_FULL));
             if (!ok)
                 break;
-            fence_async_smem();         // the copies, which this warp has seen land, for the MMAs
             tc_fence_after_sync();
             const uint64_t ad = sw128_kmajor_desc(smem + s * stage_bytes);
             const uint64_t bd = sw128_kmajor_desc(smem + s * stage_bytes + kTileBytes);
@@ -170,6 +180,25 @@ template <bool BF16> __global__ void __launch_bounds__(kShrinkThreads) k_adapter
         // no commit arrives on this CTA's shared memory after it exits
         mma_commit_elect<false>(drain);
         wait_drain(drain, 0, p.status, p.wait_limit, (SITE_DRAIN << 8) | 4u);
+    } else if (warp == 5 && steps) {
+        const RowLoads load(rows, item.rows, p.a.T);
+        int i = 0;
+        for (; i < steps; ++i) {
+            const int s = i % STAGES;
+            if (!__all_sync(0xffffffffu, wait_bounded(empty + 8u * s, static_cast<uint32_t>(i / STAGES & 1) ^ 1u,
+                                                      guard, SITE_TILED_PRODUCER)))
+                break;
+            const uint32_t dst = smem + s * stage_bytes, bar = full + 8u * s;
+            const int k = (lo + i) * 64;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar, stage_bytes);
+                tma_load_3d(dst + kTileBytes, &map_a, bar, k, 0, item.adapter);
+            }
+            __syncwarp();
+            load(dst, &map_x, &map_x32, bar, k);
+        }
+        if (i < steps)
+            drain_loads<STAGES>(full, i, p.status, p.wait_limit);
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -181,15 +210,14 @@ template <bool BF16> __global__ void __launch_bounds__(kShrinkThreads) k_adapter
 
 // ------------------------------------------------------------------ base + h B^T
 
-constexpr int kExpandThreads = 288;         // warps 0-3 copy, 4-7 epilogue, 8 issues MMAs
-constexpr uint32_t kBasePitch = 144;        // a row's 128 bytes of base; rows 16 bytes apart in banks
+constexpr int kExpandThreads = 192;         // warps 0-3 epilogue, 4 issues MMAs, 5 loads
 
 template <bool BF16, int OUT> struct Expand {
     static constexpr int kTerms = BF16 && OUT == W8A8_OUT_FP32 ? 3 : 2;
     static constexpr int kEach = OUT == W8A8_OUT_FP32 ? 4 : 8;          // elements of 16 bytes
     static constexpr int kCols = 8 * kEach;                             // of a column tile
     static constexpr uint32_t kBBytes = kCols * kRowBytes;              // for 64 columns of r
-    static __host__ __device__ constexpr uint32_t stage_bytes(int k_blocks) { return k_blocks * kBBytes + kTileRows * kBasePitch; }
+    static __host__ __device__ constexpr uint32_t stage_bytes(int k_blocks) { return k_blocks * kBBytes + kTileBytes; }
     static constexpr size_t smem(int k_blocks, int stages)
     {
         return 1024 + static_cast<size_t>(kTerms) * k_blocks * kTileBytes + static_cast<size_t>(stages) * stage_bytes(k_blocks);
@@ -197,7 +225,9 @@ template <bool BF16, int OUT> struct Expand {
 };
 
 template <bool BF16, int OUT, int STAGES>
-__global__ void __launch_bounds__(kExpandThreads) k_adapter_expand(const TileParams p)
+__global__ void __launch_bounds__(kExpandThreads) k_adapter_expand(
+    const __grid_constant__ CUtensorMap map_base, const __grid_constant__ CUtensorMap map_base32,
+    const __grid_constant__ CUtensorMap map_b, const TileParams p)
 {
     using X = Expand<BF16, OUT>;
     constexpr int kCols = X::kCols, kEach = X::kEach, kTerms = X::kTerms, kOut = 16 / kEach;
@@ -215,7 +245,7 @@ __global__ void __launch_bounds__(kExpandThreads) k_adapter_expand(const TilePar
                    d_empty = d_full + 16u, drain = d_empty + 16u;
     if (t == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(full + 8u * s, 128);
+            mbar_init(full + 8u * s, 1);
             mbar_init(empty + 8u * s, 5);       // the MMAs' commit and four epilogue warps
         }
         mbar_init(h_full, 128);
@@ -227,7 +257,12 @@ __global__ void __launch_bounds__(kExpandThreads) k_adapter_expand(const TilePar
         abort_word = 0;
         mbar_fence_init();
     }
-    if (warp == 8) {
+    if (warp == 5 && lane == 0) {
+        tma_prefetch_map(&map_base);
+        tma_prefetch_map(&map_base32);
+        tma_prefetch_map(&map_b);
+    }
+    if (warp == 4) {
         tmem_alloc(smem_addr(&tmem_slot), 2 * kCols);
         tmem_relinquish();
     }
@@ -246,98 +281,89 @@ __global__ void __launch_bounds__(kExpandThreads) k_adapter_expand(const TilePar
     const int lo = static_cast<int>(static_cast<long long>(col_tiles) * chunk / p.chunks);
     const int hi = static_cast<int>(static_cast<long long>(col_tiles) * (chunk + 1) / p.chunks);
     const int steps = item.rows && item.adapter < p.a.L ? hi - lo : 0;
-    const char *const base = static_cast<const char *>(p.a.base);
     char *const out = static_cast<char *>(p.a.out);
-    if (warp < 4 && steps) {
+    if (warp == 5 && steps) {
         // (h alone is the first launch's: nothing here waits for it)
-        const uint32_t c = t & 7u, r0 = t >> 3;
-        const uint16_t *const B = p.a.B + static_cast<long long>(item.adapter) * p.a.N * p.a.r;
-        const char *from[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int row = rows[r0 + 16 * i];
-            from[i] = row >= 0 ? base + row * p.a.ld_base * kOut : nullptr;
-        }
-        bool ok = true;
-        for (int i = 0; i < steps; ++i) {
+        const RowLoads load(rows, item.rows, p.a.T);
+        int i = 0;
+        for (; i < steps; ++i) {
             const int s = i % STAGES;
-            ok = __all_sync(0xffffffffu, wait_bounded(empty + 8u * s, static_cast<uint32_t>(i / STAGES & 1) ^ 1u, guard,
-                                                      SITE_TILED_PRODUCER));
-            if (!ok)
+            if (!__all_sync(0xffffffffu, wait_bounded(empty + 8u * s, static_cast<uint32_t>(i / STAGES & 1) ^ 1u, guard,
+                                                      SITE_TILED_PRODUCER)))
                 break;
-            const uint32_t dst = ring + s * stage_bytes;
-            const int n0 = (lo + i) * kCols, col = n0 + static_cast<int>(c) * kEach;
-            const bool in = col < p.a.N;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                cp_async_16_ahead(dst + base_at + (r0 + 16 * j) * kBasePitch + 16 * c,
-                            in && from[j] ? from[j] + static_cast<long long>(col) * kOut : base, in && from[j]);
-            for (int q = 0; q < k_blocks; ++q) {
-                const int k = 64 * q + 8 * static_cast<int>(c);
-                if (k < p.a.r_pad)
-#pragma unroll
-                    for (int j = 0; j < kCols / 16; ++j) {
-                        const int n = n0 + static_cast<int>(r0) + 16 * j;
-                        const bool there = n < p.a.N && k < p.a.r;
-                        cp_async_16(dst + q * X::kBBytes + swizzled(r0 + 16 * j, c),
-                                    there ? B + static_cast<long long>(n) * p.a.r + k : B, there);
-                    }
+            const uint32_t dst = ring + s * stage_bytes, bar = full + 8u * s;
+            const int n0 = (lo + i) * kCols;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar, stage_bytes);
+                for (int q = 0; q < k_blocks; ++q)
+                    tma_load_3d(dst + q * X::kBBytes, &map_b, bar, 64 * q, n0, item.adapter);
             }
-            cp_async_arrive(full + 8u * s);
+            __syncwarp();
+            load(dst + base_at, &map_base, &map_base32, bar, n0);
         }
-        cp_async_wait_all();
+        if (i < steps)
+            drain_loads<STAGES>(full, i, p.status, p.wait_limit);
     }
     grid_dependency_wait();
     grid_launch_dependents();
-    if (warp >= 4 && warp < 8 && steps) {
+    if (warp < 4 && steps) {
         // ---------------------------------------------------- h's parts, then the epilogue
-        const uint32_t e = warp - 4, row = e * 32 + lane;
+        const uint32_t e = warp, row = e * 32 + lane;
         const float *const h = p.h + (static_cast<long long>(item.first) + row) * p.a.r_pad;
         const bool mine = static_cast<int>(row) < item.rows;
         const long long plane = static_cast<long long>(p.a.T) * p.a.r_pad;
-        auto load = [&](int k, float (&v)[8]) {
+        // 32 columns at a time, the loads of a part of K together (r_pad is a multiple of 16)
+        auto load = [&](int k, float (&v)[32]) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 32; ++i)
                 v[i] = 0.f;
-            if (!mine || k >= p.a.r_pad)
+            if (!mine)
                 return;
             for (int s = 0; s < p.splits; ++s) {
-                const float4 a = *reinterpret_cast<const float4 *>(h + s * plane + k);
-                const float4 b = *reinterpret_cast<const float4 *>(h + s * plane + k + 4);
-                v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
-                v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+                float4 a[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    a[i] = i < 4 || k + 16 < p.a.r_pad ? *reinterpret_cast<const float4 *>(h + s * plane + k + 4 * i)
+                                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[4 * i] += a[i].x, v[4 * i + 1] += a[i].y, v[4 * i + 2] += a[i].z, v[4 * i + 3] += a[i].w;
             }
         };
         float factor = 1.f, shrink = 1.f;
         if constexpr (!BF16) {
             float top = 0.f;
-            for (int k = 0; k < p.a.r_pad; k += 8) {
-                float v[8];
+            for (int k = 0; k < p.a.r_pad; k += 32) {
+                float v[32];
                 load(k, v);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
+                for (int i = 0; i < 32; ++i)
                     top = fmaxf(top, fabsf(v[i]));
             }
             power_of(top, &shrink, &factor);
         }
-        for (int k = 0; k < p.a.r_pad; k += 8) {
-            float v[8];
+#pragma unroll 2
+        for (int k = 0; k < p.a.r_pad; k += 32) {
+            float v[32];
             load(k, v);
-            if constexpr (!BF16) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    v[i] *= shrink;
-            }
+            for (int c = 0; c < 4; ++c) {
+                if (k + 8 * c >= p.a.r_pad)
+                    continue;
 #pragma unroll
-            for (int q = 0; q < kTerms; ++q) {
-                uint32_t w[8];
+                for (int q = 0; q < kTerms; ++q) {
+                    uint32_t w[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    w[i] = take_part<BF16>(v[i]);
-                const uint32_t at = operand + (q * k_blocks + k / 64) * kTileBytes + swizzled(row, (k & 63) / 8);
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[1] << 16 | w[0]),
-                             "r"(w[3] << 16 | w[2]), "r"(w[5] << 16 | w[4]), "r"(w[7] << 16 | w[6])
-                             : "memory");
+                    for (int i = 0; i < 8; ++i) {
+                        if (!BF16 && q == 0)
+                            v[8 * c + i] *= shrink;
+                        w[i] = take_part<BF16>(v[8 * c + i]);
+                    }
+                    const uint32_t at = operand + (q * k_blocks + k / 64) * kTileBytes + swizzled(row, (k & 63) / 8 + c);
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[1] << 16 | w[0]),
+                                 "r"(w[3] << 16 | w[2]), "r"(w[5] << 16 | w[4]), "r"(w[7] << 16 | w[6])
+                                 : "memory");
+                }
             }
         }
         fence_async_smem();
@@ -352,7 +378,7 @@ __global__ void __launch_bounds__(kExpandThreads) k_adapter_expand(const TilePar
                 break;
             tc_fence_after_sync();
             const uint32_t tile_at = ring_at + s * stage_bytes + base_at;
-            uint8_t *const own = smem_raw + tile_at + row * kBasePitch;
+            uint8_t *const tile_rows = smem_raw + tile_at;
 #pragma unroll
             for (int j = 0; j < kCols; j += 32) {
                 float v[32];
@@ -365,7 +391,7 @@ __global__ void __launch_bounds__(kExpandThreads) k_adapter_expand(const TilePar
                 }
 #pragma unroll
                 for (int q = 0; q < 32; q += kEach) {
-                    uint4 *const piece = reinterpret_cast<uint4 *>(own + (j + q) * kOut);
+                    uint4 *const piece = reinterpret_cast<uint4 *>(tile_rows + swizzled(row, (j + q) / kEach));
                     const uint4 u = *piece;
                     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
                     uint32_t o[4];
@@ -395,13 +421,14 @@ __global__ void __launch_bounds__(kExpandThreads) k_adapter_expand(const TilePar
                     const int to = rows[r];
                     if (to >= 0)
                         *reinterpret_cast<uint4 *>(out + (to * p.a.ld_out + col) * kOut) =
-                            *reinterpret_cast<const uint4 *>(smem_raw + tile_at + r * kBasePitch + 16 * c);
+                            *reinterpret_cast<const uint4 *>(tile_rows + swizzled(r, c));
                 }
+            fence_async_smem();         // these accesses before the next load's
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(empty + 8u * s);
         }
-    } else if (warp == 8 && steps) {
+    } else if (warp == 4 && steps) {
         // ---------------------------------------------------- MMAs
         const uint32_t d = idesc<BF16>(kCols);
         bool ok = __all_sync(0xffffffffu, wait_bounded(h_full, 0, guard, SITE_TILED_MMA_FULL));
@@ -413,7 +440,6 @@ __global__ void __launch_bounds__(kExpandThreads) k_adapter_expand(const TilePar
                                                           SITE_TILED_MMA_FULL));
             if (!ok)
                 break;
-            fence_async_smem();         // the copies, which this warp has seen land, for the MMAs
             tc_fence_after_sync();
             uint32_t more = 0;
             for (int q = 0; q < k_blocks; ++q) {
@@ -440,7 +466,7 @@ __global__ void __launch_bounds__(kExpandThreads) k_adapter_expand(const TilePar
     }
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == 4) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, 2 * kCols);
     }
@@ -450,8 +476,9 @@ __global__ void __launch_bounds__(kExpandThreads) k_adapter_expand(const TilePar
 // launched; those without rows leave at once).
 long long likely_tiles(const AdapterParams &p) { return p.T / kTileRows + std::min(p.T, p.L) / 2 + 1; }
 
-template <class Kernel> cudaError_t launch(Kernel kernel, const TileParams &p, long long ctas, int threads, size_t smem,
-                                           volatile int *flags, cudaStream_t stream)
+template <class Kernel>
+cudaError_t launch(Kernel kernel, const CUtensorMap (&rows)[2], const CUtensorMap &weights, const TileParams &p,
+                   long long ctas, int threads, size_t smem, volatile int *flags, cudaStream_t stream)
 {
     if (const cudaError_t e = allow_smem(kernel, 224 * 1024, flags); e != cudaSuccess)
         return e;
@@ -465,38 +492,78 @@ template <class Kernel> cudaError_t launch(Kernel kernel, const TileParams &p, l
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = attr;
     lc.numAttrs = 1;
-    return cudaLaunchKernelEx(&lc, kernel, p);
+    return cudaLaunchKernelEx(&lc, kernel, rows[0], rows[1], weights, p);
 }
 
-template <bool BF16, int OUT, int STAGES> cudaError_t launch_expand(const TileParams &p, long long ctas, cudaStream_t s)
+template <bool BF16, int OUT, int STAGES>
+cudaError_t launch_expand(const CUtensorMap (&rows)[2], const CUtensorMap &weights, const TileParams &p, long long ctas,
+                          cudaStream_t s)
 {
     static volatile int flags[kMaxDeviceFlags] = {};
-    return launch(k_adapter_expand<BF16, OUT, STAGES>, p, ctas, kExpandThreads,
+    return launch(k_adapter_expand<BF16, OUT, STAGES>, rows, weights, p, ctas, kExpandThreads,
                   Expand<BF16, OUT>::smem((p.a.r_pad + 63) / 64, STAGES), flags, s);
+}
+
+template <bool BF16, int STAGES>
+cudaError_t launch_shrink(const CUtensorMap (&rows)[2], const CUtensorMap &weights, const TileParams &p, long long ctas,
+                          cudaStream_t s)
+{
+    static volatile int flags[kMaxDeviceFlags] = {};
+    return launch(k_adapter_shrink<BF16, STAGES>, rows, weights, p, ctas, kShrinkThreads, shrink_smem(p.a.r_pad, STAGES), flags,
+                  s);
+}
+
+// Rows of 128 bytes: boxes of one row, which are gathered, and of 32.
+cudaError_t rows_maps(CUtensorMap (&map)[2], int kind, const void *base, int64_t rows, int64_t cols, int64_t ld)
+{
+    const int element = kind == W8A8_OUT_FP32 ? 4 : 2;
+    const uint64_t sizes[2] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows)},
+                   strides[1] = {static_cast<uint64_t>(ld) * element};
+    const uint32_t one[2] = {kRowBytes / element, 1}, boxes[2] = {kRowBytes / element, 32};
+    const cudaError_t e = encode_rows_map(&map[0], kind, 2, base, sizes, strides, one);
+    return e == cudaSuccess ? encode_rows_map(&map[1], kind, 2, base, sizes, strides, boxes) : e;
+}
+
+// The adapters' weights [L, rows, cols]: boxes of 64 columns of `high` rows.
+cudaError_t weights_map(CUtensorMap *map, int kind, const void *base, int64_t L, int64_t rows, int64_t cols, int high)
+{
+    const uint64_t sizes[3] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows), static_cast<uint64_t>(L)},
+                   strides[2] = {static_cast<uint64_t>(cols) * 2, static_cast<uint64_t>(cols) * rows * 2};
+    const uint32_t box[3] = {64, static_cast<uint32_t>(high), 1};
+    return encode_rows_map(map, kind, 3, base, sizes, strides, box);
 }
 
 template <bool BF16, int OUT> cudaError_t launch_both(TileParams p, const DeviceView &dev, cudaStream_t stream)
 {
+    using X = Expand<BF16, OUT>;
+    constexpr int kKind = BF16 ? W8A8_OUT_BF16 : W8A8_OUT_FP16;
+    CUtensorMap map_x[2], map_base[2], map_a, map_b;
+    cudaError_t e = rows_maps(map_x, kKind, p.a.x, p.a.T, p.a.K, p.a.ld_x);
+    if (e == cudaSuccess)
+        e = weights_map(&map_a, kKind, p.a.A, p.a.L, p.a.r, p.a.K, p.a.r_pad);
+    if (e == cudaSuccess)
+        e = rows_maps(map_base, OUT, p.a.base, p.a.T, p.a.N, p.a.ld_base);
+    if (e == cudaSuccess)
+        e = weights_map(&map_b, kKind, p.a.B, p.a.L, p.a.N, p.a.r, X::kCols);
+    if (e != cudaSuccess)
+        return e;
     const long long tiles = most_items(p.a.T, p.a.L, kTileRows);
-    static volatile int flags[kMaxDeviceFlags] = {};
-    cudaError_t e = launch(k_adapter_shrink<BF16>, p, tiles * p.splits, kShrinkThreads, shrink_smem(p.a.r_pad), flags, stream);
+    // stages that leave room for two CTAs on an SM
+    e = p.a.r_pad <= 64 ? launch_shrink<BF16, 4>(map_x, map_a, p, tiles * p.splits, stream)
+                        : launch_shrink<BF16, 3>(map_x, map_a, p, tiles * p.splits, stream);
     if (e != cudaSuccess)
         return e;
     const long long all = most_items(p.a.T, p.a.out == p.a.base ? p.a.L : p.a.L + 1, kTileRows);
-    const int col_tiles = (p.a.N + Expand<BF16, OUT>::kCols - 1) / Expand<BF16, OUT>::kCols;
-    // As many CTAs as fill the SMs twice, with at least four column tiles each.
-    p.chunks = static_cast<int>(std::max(1ll, std::min<long long>(2ll * dev.sm_count / likely_tiles(p.a), col_tiles / 4)));
-    constexpr size_t kHalf = 113 * 1024;        // two CTAs to an SM
+    const int col_tiles = (p.a.N + X::kCols - 1) / X::kCols;
     const int k_blocks = (p.a.r_pad + 63) / 64;
-    using X = Expand<BF16, OUT>;
-    if (X::smem(k_blocks, 3) + 2048 <= kHalf)
-        return launch_expand<BF16, OUT, 3>(p, all * p.chunks, stream);
-    if (X::smem(k_blocks, 2) + 2048 <= kHalf)
-        return launch_expand<BF16, OUT, 2>(p, all * p.chunks, stream);
-    return launch_expand<BF16, OUT, 4>(p, all * p.chunks, stream);
+    // Two CTAs to an SM where three stages leave room for them; as many CTAs as fill the
+    // SMs, with at least four column tiles each.
+    const bool two = X::smem(k_blocks, 3) + 2048 <= 113 * 1024;
+    p.chunks = static_cast<int>(
+        std::max(1ll, std::min<long long>((two ? 2ll : 1ll) * dev.sm_count / likely_tiles(p.a), col_tiles / 4)));
+    return two ? launch_expand<BF16, OUT, 3>(map_base, map_b, p, all * p.chunks, stream)
+               : launch_expand<BF16, OUT, 4>(map_base, map_b, p, all * p.chunks, stream);
 }
-
-bool on(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 }  // namespace
 
@@ -504,7 +571,8 @@ namespace lora {
 
 bool tile_takes(const AdapterParams &p)
 {
-    return p.r >= 8 && p.r <= kMaxR && p.r % 8 == 0 && p.K >= 64 && p.vec_k && p.vec_n && on(p.B, 16);
+    return p.r >= 8 && p.r <= kMaxR && p.r % 8 == 0 && p.K >= 64 && p.vec_k && p.vec_n &&
+           reinterpret_cast<uintptr_t>(p.B) % 16 == 0;
 }
 
 // (The workspace's size goes by it: a GB300's SMs, so that no device is asked.)

@@ -1556,6 +1556,26 @@ int device_view(DeviceView *out)
     return W8A8_OK;
 }
 
+cudaError_t encode_rows_map(CUtensorMap *map, int kind, int rank, const void *base, const uint64_t *sizes,
+                            const uint64_t *strides, const uint32_t *box)
+{
+    const CUtensorMapDataType dt = kind == W8A8_OUT_FP32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : kind == W8A8_OUT_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                           : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    cuuint64_t d[3] = {}, st[2] = {};
+    cuuint32_t b[3] = {};
+    for (int i = 0; i < rank; ++i) {
+        d[i] = sizes[i];
+        b[i] = box[i];
+        if (i + 1 < rank)
+            st[i] = strides[i];
+    }
+    return encode_cached(map, dt, rank, const_cast<void *>(base), d, st, b, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
 // Lets other translation units of the library report an error through
 // w8a8_last_error(); returns `st`.
 w8a8_status record_error(w8a8_status st, const char *message)

@@ -339,4 +339,10 @@ struct DeviceView {
 };
 int device_view(DeviceView *out);      // a w8a8_status
 
+// Tensor map of rows in a type by its W8A8_OUT_* code, 128-byte swizzle, zeros out of
+// range: sizes and box from the innermost on, strides of the outer ones in bytes
+// (multiples of 16).  After a device_view().
+cudaError_t encode_rows_map(CUtensorMap *map, int kind, int rank, const void *base, const uint64_t *sizes,
+                            const uint64_t *strides, const uint32_t *box);
+
 }  // namespace w8a8

@@ -226,6 +226,17 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 
 // 2-D tiled store of a dense row-major shared-memory box to (x, y); elements
 // outside the tensor are not written.  Tracked by the bulk async-group.
+// Four rows at any places: the pieces of rows y0 .. y3 that begin at x, one after the other
+// (the map's box is one row high); a row out of range is read as zeros.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map, uint32_t bar,
+                                            int32_t x, int32_t y0, int32_t y1, int32_t y2, int32_t y3)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3)
+                 : "memory");
+}
+
 // 3-D form (x innermost; z selects the expert slab of a grouped operand).
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar,
                                             int32_t x, int32_t y, int32_t z)
