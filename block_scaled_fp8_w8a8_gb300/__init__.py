@@ -595,10 +595,10 @@ def group_rows(ids, groups, out=None, stream=None):
     order[offsets[g]] .. order[offsets[g + 1] - 1], and those of no group (values outside
     0 .. groups - 1) come last.  ``out``: both, preallocated."""
     lib, types = load_library(), _dtypes or _load_dtypes()
-    if out is not None and lib.group_tensors is not None:
+    if lib.group_tensors is not None:
         st = lib.group_tensors(ids, groups, out, types.routing, stream if stream is None else _stream(stream))
-        if st == 0:
-            return out
+        if st == 0 or type(st) is tuple:
+            return st or out
         if st is not None:
             check(st)
     n = ids.numel()
@@ -656,17 +656,18 @@ def combine_experts(Y, rows, weights, add=None, out_dtype=None, out=None, stream
     return out
 
 
-def adapter_matmul(x, A, B, order, offsets, base, scales=None, out=None, stream=None):
+def adapter_matmul(x, A, B, order, offsets, base, scales=None, out=None, stream=None,
+                   variant=W8A8_VARIANT_AUTO):
     """out[t] = base[t] + scales[l] * (x[t] A[l]^T) B[l]^T on CUDA tensors, l the adapter of row
     t: low-rank adapters of many requests beside the projection that made ``base``.
 
     x [T, K] bf16 or fp16; A [L, r, K] and B [L, N, r] of its type; order int32 [T] and
     offsets int32 [L + 1] from group_rows(the rows' adapters, L); base [T, N] of x's type or
     fp32; scales float32 [L] (None: 1).  Rows without an adapter are base's.  ``out`` may be
-    ``base``, whose rows without an adapter are then not touched.  Raises W8A8Error on a
-    non-zero status."""
+    ``base``, whose rows without an adapter are then not touched.  variant: W8A8_VARIANT_AUTO,
+    _SMALLM or _TILED (see the header).  Raises W8A8Error on a non-zero status."""
     lib, types = load_library(), _dtypes or _load_dtypes()
-    if out is not None and lib.adapter_tensors is not None:
+    if out is not None and not variant and lib.adapter_tensors is not None:
         st = lib.adapter_tensors(x, A, B, order, offsets, base, scales, out, _in_codes, types.routing,
                                  stream if stream is None else _stream(stream))
         if st == 0:
@@ -694,12 +695,12 @@ def adapter_matmul(x, A, B, order, offsets, base, scales=None, out=None, stream=
         _typed(out, (base.dtype,), "out")
         ld_x, ld_base, ld_out = _rows(x), _rows(base), _rows(out)
         _here(x, A, B, order, offsets, base, scales, out)
-        size = lib.w8a8_adapter_workspace_size(T, L, r, K)
+        size = lib.w8a8_adapter_workspace_size(T, L, r, K, variant)
         keep, scratch = _workspace(size, x.device)
     st = lib.w8a8_adapter_matmul(x.data_ptr(), kind, ld_x, A.data_ptr(), B.data_ptr(), order.data_ptr(),
                                  offsets.data_ptr(), None if scales is None else scales.data_ptr(), base.data_ptr(),
-                                 ld_base, out.data_ptr(), _in_codes[base.dtype], ld_out, T, L, r, K, N, scratch, size,
-                                 _stream(stream))
+                                 ld_base, out.data_ptr(), _in_codes[base.dtype], ld_out, T, L, r, K, N, variant,
+                                 scratch, size, _stream(stream))
     if st:
         check(st)
     return out

@@ -199,8 +199,8 @@ def load_library():
     lib.w8a8_combine_experts.argtypes = [vp, i32, i64, i64, vp, vp, vp, i64, vp, i32, i64, i64, i64,
                                          i64, vp]
     lib.w8a8_adapter_matmul.argtypes = [vp, i32, i64, vp, vp, vp, vp, vp, vp, i64, vp, i32, i64, i64,
-                                        i64, i64, i64, i64, vp, sz, vp]
-    lib.w8a8_adapter_workspace_size.argtypes = [i64, i64, i64, i64]
+                                        i64, i64, i64, i64, i32, vp, sz, vp]
+    lib.w8a8_adapter_workspace_size.argtypes = [i64, i64, i64, i64, i32]
     for name in ("w8a8_route_workspace_size", "w8a8_group_workspace_size",
                  "w8a8_adapter_workspace_size"):
         getattr(lib, name).restype = sz
@@ -438,15 +438,16 @@ def w8a8_combine_experts(Y, y_dtype, ld_y, M, rows, weights, add, ld_add, out, o
 
 
 def w8a8_adapter_matmul(x, dtype, ld_x, A, B, order, offsets, scales, base, ld_base, out, out_dtype,
-                        ld_out, T, L, r, K, N, workspace=None, workspace_bytes=0, stream=None) -> int:
+                        ld_out, T, L, r, K, N, variant=W8A8_VARIANT_AUTO, workspace=None, workspace_bytes=0,
+                        stream=None) -> int:
     return load_library().w8a8_adapter_matmul(
         _ptr(x), dtype, ld_x, _ptr(A), _ptr(B), _ptr(order), _ptr(offsets), _ptr(scales),
-        _ptr(base), ld_base, _ptr(out), out_dtype, ld_out, T, L, r, K, N, _ptr(workspace),
-        workspace_bytes, _stream(stream))
+        _ptr(base), ld_base, _ptr(out), out_dtype, ld_out, T, L, r, K, N, variant,
+        _ptr(workspace), workspace_bytes, _stream(stream))
 
 
-def w8a8_adapter_workspace_size(T, L, r, K) -> int:
-    return load_library().w8a8_adapter_workspace_size(T, L, r, K)
+def w8a8_adapter_workspace_size(T, L, r, K, variant=W8A8_VARIANT_AUTO) -> int:
+    return load_library().w8a8_adapter_workspace_size(T, L, r, K, variant)
 
 
 def w8a8_launch_floor_kernel(pdl=1, stream=None) -> int:

@@ -5,12 +5,14 @@
 // with rows sorted by adapter (group_rows): adapter l's are order[offsets[l]] ..
 // order[offsets[l+1] - 1]; rows behind offsets[L] have none and are base's.
 //
-// A cluster of CTAs takes up to 8 NT rows of one adapter.  First each CTA multiplies
-// its share of K: h^T = A[l] x^T by mma.sync, A's rows on the M side, tokens on the
-// N side, operands straight from global memory in 16-byte pieces (a permutation of K
-// that both operands share).  Partial h go to every CTA of the cluster through
-// distributed shared memory and are added in rank order, so that all have the same
-// bits.  Then each CTA takes its share of N: out^T = base^T + B[l] h^T.
+// A cluster of CTAs takes up to 16 rows of one adapter.  First each CTA multiplies
+// its share of K: h = x A[l]^T by mma.sync, tokens on the M side, A's rows on the N side,
+// operands straight from global memory in 16-byte pieces (a permutation of K that both
+// operands share).  Partial h go to every CTA of the cluster through distributed shared
+// memory and are added in rank order, so that all have the same bits.  Then each CTA takes
+// its share of N: out = base + h B[l]^T, by warps of 32 columns, whose order in the MMAs is
+// such that a lane ends with eight neighbouring ones.  B's and base's share are fetched into
+// L2 while x A^T is computed.
 //
 // h is kept to fp32: an MMA takes 16-bit operands, so h is split into a sum of two or
 // three of them, each the rounding of what the ones before leave.  bf16: two leave an
@@ -35,7 +37,8 @@ using namespace lora;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kChunk = 64;          // rows of A whose sums a warp holds at once
-constexpr int kMaxCluster = 8;
+constexpr int kRows = 16;           // of an item
+constexpr int kMaxCluster = 16;     // CTAs (more than 8 where that is allowed, see launch_few)
 
 // Eight elements of a row at k, zeros past its end (row null: zeros).
 __device__ __forceinline__ uint4 load8(const uint16_t *row, int k, int K, bool vec)
@@ -52,21 +55,6 @@ __device__ __forceinline__ uint4 load8(const uint16_t *row, int k, int K, bool v
         w[i] = hi << 16 | lo;
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-__device__ __forceinline__ uint2 load4(const uint16_t *row, int k, int K, bool vec)
-{
-    if (!row || k >= K)
-        return make_uint2(0, 0);
-    if (vec)
-        return *reinterpret_cast<const uint2 *>(row + k);
-    uint32_t w[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t lo = k + 2 * i < K ? row[k + 2 * i] : 0, hi = k + 2 * i + 1 < K ? row[k + 2 * i + 1] : 0;
-        w[i] = hi << 16 | lo;
-    }
-    return make_uint2(w[0], w[1]);
 }
 
 // D (16 x 8) += A (16 x 16) B (16 x 8), fp32 sums.
@@ -103,25 +91,72 @@ template <int OUT> __device__ __forceinline__ void store_out(void *p, long long 
         static_cast<__half *>(p)[i] = __float2half_rn(v);
 }
 
-// Shared memory: partial sums of the warps (later h's parts as MMA operands), every
+// Shared memory of floats: the warps' partial sums (later h's parts as MMA operands), every
 // CTA's partial h, h itself.
-template <int NT> struct FewSmem {
-    static constexpr int kRows = 8 * NT;
-    static __host__ __device__ size_t part(int terms, int r_pad)
+template <int TERMS> struct FewSmem {
+    static constexpr int kPitch = kChunk + 4;           // of a row of partial sums: spreads banks
+    static __host__ __device__ int padded(int r_pad) { return (r_pad + 31) / 32 * 32; }
+    static __host__ __device__ size_t part(int r_pad)
     {
-        const size_t sums = sizeof(float) * kWarps * kChunk * kRows, frags = sizeof(uint2) * 32 * (r_pad / 16) * NT * terms;
+        const size_t sums = sizeof(float) * kWarps * kRows * kPitch;
+        const size_t frags = sizeof(uint4) * 32 * (padded(r_pad) / 16) * TERMS;
         return sums > frags ? sums : frags;
     }
     static __host__ __device__ size_t received(int r_pad, int cluster) { return sizeof(float) * r_pad * kRows * cluster; }
-    static __host__ __device__ size_t bytes(int terms, int r_pad, int cluster)
+    static __host__ __device__ size_t bytes(int r_pad, int cluster)
     {
-        return part(terms, r_pad) + received(r_pad, cluster) + sizeof(float) * r_pad * kRows;
+        return part(r_pad) + received(r_pad, cluster) + sizeof(float) * padded(r_pad) * kRows;
     }
 };
 
-template <bool BF16, int OUT, int NT> __global__ void __launch_bounds__(kThreads) k_adapter_few(const AdapterParams p)
+// Starts fetching into L2 (16-byte boundaries; of long ranges the first megabyte).
+__device__ __forceinline__ void prefetch_l2(const void *p, size_t bytes)
 {
-    constexpr int kRows = 8 * NT, kTerms = BF16 && OUT == W8A8_OUT_FP32 ? 3 : 2;
+    const uint32_t n = static_cast<uint32_t>(min(bytes, static_cast<size_t>(1) << 20));
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(n) : "memory");
+}
+
+// Eight neighbouring elements of a row of base or out, as fp32; `in` of them.
+template <int OUT> struct Eight {
+    uint4 w[OUT == W8A8_OUT_FP32 ? 2 : 1];
+    __device__ __forceinline__ void load(const void *base, long long i)
+    {
+        const uint4 *const p = reinterpret_cast<const uint4 *>(static_cast<const char *>(base) + i * (OUT == W8A8_OUT_FP32 ? 4 : 2));
+#pragma unroll
+        for (int j = 0; j < static_cast<int>(sizeof(w) / 16); ++j)
+            w[j] = p[j];
+    }
+    __device__ __forceinline__ float at(int i) const
+    {
+        const uint32_t *const u = reinterpret_cast<const uint32_t *>(w);
+        if constexpr (OUT == W8A8_OUT_FP32)
+            return __uint_as_float(u[i]);
+        else if constexpr (OUT == W8A8_OUT_BF16)
+            return __uint_as_float(i & 1 ? u[i >> 1] & 0xffff0000u : u[i >> 1] << 16);
+        else
+            return __half2float(__ushort_as_half(static_cast<unsigned short>(i & 1 ? u[i >> 1] >> 16 : u[i >> 1])));
+    }
+    __device__ __forceinline__ void store(void *out, long long i, const float (&v)[8])
+    {
+        uint32_t u[sizeof(w) / 4];
+#pragma unroll
+        for (int j = 0; j < static_cast<int>(sizeof(w) / 4); ++j)
+            u[j] = OUT == W8A8_OUT_FP32   ? __float_as_uint(v[j])
+                   : OUT == W8A8_OUT_BF16 ? pack_bf16x2(v[2 * j % 8], v[(2 * j + 1) % 8])
+                                          : pack_f16x2(v[2 * j % 8], v[(2 * j + 1) % 8]);
+        uint4 *const p = reinterpret_cast<uint4 *>(static_cast<char *>(out) + i * (OUT == W8A8_OUT_FP32 ? 4 : 2));
+#pragma unroll
+        for (int j = 0; j < static_cast<int>(sizeof(w) / 16); ++j)
+            p[j] = make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
+    }
+};
+
+template <bool BF16, int OUT>
+__global__ void __launch_bounds__(kThreads, 2) k_adapter_few(const AdapterParams p)
+{
+    constexpr int kTerms = BF16 && OUT == W8A8_OUT_FP32 ? 3 : 2;
+    using S = FewSmem<kTerms>;
+    constexpr int kElement = OUT == W8A8_OUT_FP32 ? 4 : 2;
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ int scratch[16];
     __shared__ int rows[kRows];
@@ -131,97 +166,108 @@ template <bool BF16, int OUT, int NT> __global__ void __launch_bounds__(kThreads
     asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(cluster));
     const uint32_t me = cluster_ctarank();
     float *const part = reinterpret_cast<float *>(smem);
-    float *const received = reinterpret_cast<float *>(smem + FewSmem<NT>::part(kTerms, p.r_pad));
+    float *const received = reinterpret_cast<float *>(smem + S::part(p.r_pad));
     float *const h = received + p.r_pad * kRows * ctas;
+    const int r32 = S::padded(p.r_pad);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     grid_dependency_wait();
     grid_launch_dependents();
     const Item item = find_item<kThreads>(p, static_cast<int>(cluster), kRows, p.out == p.base ? p.L : p.L + 1, scratch);
     if (item.rows == 0)
         return;                             // the whole cluster
-    if (threadIdx.x < kRows) {
-        int row = threadIdx.x < item.rows ? p.order[item.first + threadIdx.x] : -1;
-        rows[threadIdx.x] = static_cast<unsigned>(row) < static_cast<unsigned>(p.T) ? row : -1;
-    }
-    __syncthreads();
-    const int n_tiles = (p.N + 15) / 16;
-    const int tile_lo = static_cast<int>(static_cast<long long>(n_tiles) * me / ctas);
-    const int tile_hi = static_cast<int>(static_cast<long long>(n_tiles) * (me + 1) / ctas);
+    auto row_at = [&](int i) {
+        const int row = i < item.rows ? p.order[item.first + i] : -1;
+        return static_cast<unsigned>(row) < static_cast<unsigned>(p.T) ? row : -1;
+    };
+    const int n_blocks = (p.N + 31) / 32;
+    const int block_lo = static_cast<int>(static_cast<long long>(n_blocks) * me / ctas);
+    const int block_hi = static_cast<int>(static_cast<long long>(n_blocks) * (me + 1) / ctas);
+    const int n_lo = block_lo * 32, n_hi = min(block_hi * 32, p.N);
+    // (the last warp has the least to do at first)
+    const int slot = static_cast<int>(threadIdx.x) - (kThreads - 32);
+    if (slot >= 0 && slot < kRows)
+        rows[slot] = row_at(slot);
     if (item.adapter == p.L) {
-        const int from = tile_lo * 16, to = min(tile_hi * 16, p.N);
-        constexpr int kElement = OUT == W8A8_OUT_FP32 ? 4 : 2;
+        __syncthreads();
         if (p.vec_n)
-            copy_rows<uint4, kThreads>(p, rows, item.rows, from, to, kElement);
+            copy_rows<uint4, kThreads>(p, rows, item.rows, n_lo, n_hi, kElement);
         else if constexpr (kElement == 4)
-            copy_rows<uint32_t, kThreads>(p, rows, item.rows, from, to, kElement);
+            copy_rows<uint32_t, kThreads>(p, rows, item.rows, n_lo, n_hi, kElement);
         else
-            copy_rows<uint16_t, kThreads>(p, rows, item.rows, from, to, kElement);
+            copy_rows<uint16_t, kThreads>(p, rows, item.rows, n_lo, n_hi, kElement);
         return;
     }
-    const uint16_t *const A = p.A + static_cast<long long>(item.adapter) * p.r * p.K;
-    const uint16_t *const B = p.B + static_cast<long long>(item.adapter) * p.N * p.r;
-
+    __syncwarp();
     if (ctas > 1)                           // peers write here once every CTA has started
         asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    const uint16_t *const A = p.A + static_cast<long long>(item.adapter) * p.r * p.K;
+    const uint16_t *const B = p.B + static_cast<long long>(item.adapter) * p.N * p.r;
+    if (slot == kRows && p.vec_r && n_hi > n_lo && p.r)
+        prefetch_l2(B + static_cast<long long>(n_lo) * p.r, static_cast<size_t>(n_hi - n_lo) * p.r * 2);
+    if (slot >= 0 && slot < kRows && p.vec_n && n_hi > n_lo)
+        if (const int row = rows[slot]; row >= 0)
+            prefetch_l2(static_cast<const char *>(p.base) + (row * p.ld_base + n_lo) * kElement,
+                        static_cast<size_t>(n_hi - n_lo) * kElement);
+    __syncwarp();
 
-    // h^T, this CTA's share of K
+    // h, this CTA's share of K
     const int blocks = (p.K + 63) / 64;
     const int lo = static_cast<int>(static_cast<long long>(blocks) * me / ctas);
     const int hi = static_cast<int>(static_cast<long long>(blocks) * (me + 1) / ctas);
-    const uint16_t *token[NT];
+    const uint16_t *token[2];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const int row = rows[8 * t + g];
-        token[t] = row >= 0 ? p.x + row * p.ld_x : nullptr;
+    for (int i = 0; i < 2; ++i) {
+        const int row = row_at(8 * i + g);
+        token[i] = row >= 0 ? p.x + row * p.ld_x : nullptr;
     }
     for (int r0 = 0; r0 < p.r_pad; r0 += kChunk) {
-        float acc[4][NT][4] = {};
-        const int m_tiles = min(4, (p.r_pad - r0) / 16);
+        float acc[8][4] = {};
+        const int tiles = min(8, (p.r_pad - r0) / 8);
         for (int b = lo + warp; b < hi; b += kWarps) {
-            const int k = b * 64 + 8 * c;
-            uint4 xv[NT][2];
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+            for (int s = 0; s < 2; ++s) {
+                const int k = b * 64 + 32 * s + 8 * c;
+                uint4 a[8], xv[2];
 #pragma unroll
-                for (int s = 0; s < 2; ++s)
-                    xv[t][s] = load8(token[t], k + 32 * s, p.K, p.vec_k);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                if (m >= m_tiles)
-                    continue;
-                const int r_lo = r0 + 16 * m + g, r_hi = r_lo + 8;
-                const uint16_t *const a_lo = r_lo < p.r ? A + static_cast<long long>(r_lo) * p.K : nullptr;
-                const uint16_t *const a_hi = r_hi < p.r ? A + static_cast<long long>(r_hi) * p.K : nullptr;
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const uint4 u = load8(a_lo, k + 32 * s, p.K, p.vec_k), v = load8(a_hi, k + 32 * s, p.K, p.vec_k);
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        mma<BF16>(acc[m][t], u.x, v.x, u.y, v.y, xv[t][s].x, xv[t][s].y);
-                        mma<BF16>(acc[m][t], u.z, v.z, u.w, v.w, xv[t][s].z, xv[t][s].w);
-                    }
+                for (int j = 0; j < 8; ++j) {
+                    const int r = r0 + 8 * j + g;
+                    if (j < tiles)
+                        a[j] = load8(r < p.r ? A + static_cast<long long>(r) * p.K : nullptr, k, p.K, p.vec_k);
                 }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    xv[i] = load8(token[i], k, p.K, p.vec_k);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (j < tiles) {
+                        mma<BF16>(acc[j], xv[0].x, xv[1].x, xv[0].y, xv[1].y, a[j].x, a[j].y);
+                        mma<BF16>(acc[j], xv[0].z, xv[1].z, xv[0].w, xv[1].w, a[j].z, a[j].w);
+                    }
             }
         }
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
+        for (int j = 0; j < 8; ++j)
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    *reinterpret_cast<float2 *>(part + ((warp * kChunk + 16 * m + g + 8 * i) * kRows + 8 * t + 2 * c)) =
-                        make_float2(acc[m][t][2 * i], acc[m][t][2 * i + 1]);
+            for (int i = 0; i < 2; ++i)
+                if (j < tiles)
+                    *reinterpret_cast<float2 *>(part + ((warp * kRows + g + 8 * i) * S::kPitch + 8 * j + 2 * c)) =
+                        make_float2(acc[j][2 * i], acc[j][2 * i + 1]);
         __syncthreads();
         if (ctas > 1 && r0 == 0)
             asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-        for (int i = threadIdx.x; i < 16 * m_tiles * kRows; i += kThreads) {
-            float sum = 0.f;
+        for (int i = threadIdx.x; i < item.rows * 2 * tiles; i += kThreads) {
+            const int row = i / (2 * tiles), r = (i - row * 2 * tiles) * 4;
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w)
-                sum += part[w * kChunk * kRows + i];
-            const uint32_t at = smem_addr(received + me * p.r_pad * kRows + r0 * kRows + i);
+            for (int w = 0; w < kWarps; ++w) {
+                const float4 v = *reinterpret_cast<const float4 *>(part + (w * kRows + row) * S::kPitch + r);
+                sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+            }
+            const uint32_t at = smem_addr(received + (me * kRows + row) * p.r_pad + r0 + r);
             for (uint32_t q = 0; q < ctas; ++q)
-                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_map(at, q)), "f"(sum) : "memory");
+                asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_map(at, q)), "f"(sum.x),
+                             "f"(sum.y), "f"(sum.z), "f"(sum.w)
+                             : "memory");
         }
         __syncthreads();
     }
@@ -231,95 +277,148 @@ template <bool BF16, int OUT, int NT> __global__ void __launch_bounds__(kThreads
         cluster_sync();
     }
     const float scale = p.scales ? p.scales[item.adapter] : 1.f;
-    for (int i = threadIdx.x; i < p.r_pad * kRows; i += kThreads) {
-        float sum = 0.f;
-        for (uint32_t q = 0; q < ctas; ++q)
-            sum += received[q * p.r_pad * kRows + i];
-        h[i] = sum * scale;
+    for (int i = threadIdx.x; i < item.rows * (r32 / 4); i += kThreads) {
+        const int row = i / (r32 / 4), r = (i - row * (r32 / 4)) * 4;
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < p.r_pad)
+#pragma unroll 8
+            for (uint32_t q = 0; q < ctas; ++q) {
+                const float4 v = *reinterpret_cast<const float4 *>(received + (q * kRows + row) * p.r_pad + r);
+                sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+            }
+        *reinterpret_cast<float4 *>(h + row * r32 + r) =
+            make_float4(sum.x * scale, sum.y * scale, sum.z * scale, sum.w * scale);
     }
     __syncthreads();
     if constexpr (!BF16) {
-        for (int t = warp; t < kRows; t += kWarps) {
+        for (int t = warp; t < item.rows; t += kWarps) {
             float top = 0.f;
             for (int i = lane; i < p.r_pad; i += 32)
-                top = fmaxf(top, fabsf(h[i * kRows + t]));
+                top = fmaxf(top, fabsf(h[t * r32 + i]));
 #pragma unroll
             for (int d = 16; d; d /= 2)
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
             float shrink, back;
             power_of(top, &shrink, &back);
             for (int i = lane; i < p.r_pad; i += 32)
-                h[i * kRows + t] *= shrink;
+                h[t * r32 + i] *= shrink;
             if (lane == 0)
                 factor[t] = back;
         }
         __syncthreads();
     }
-    // h's parts as B operands: lane (g, c) of step s has elements 16 s + 4 c .. + 3 of token g
-    const int steps = p.r_pad / 16;
-    uint2 *const frags = reinterpret_cast<uint2 *>(part);
-    for (int i = threadIdx.x; i < steps * NT * 32; i += kThreads) {
-        const int ln = i & 31, t = (i >> 5) % NT, s = (i >> 5) / NT;
-        float v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            v[j] = h[(16 * s + 4 * (ln & 3) + j) * kRows + 8 * t + (ln >> 2)];
+    // h's parts as A operands: for step s of 16 columns lane (g, c) has the elements
+    // 32 (s / 2) + 8 c + 4 (s % 2) .. + 3 of rows g and g + 8 (what lies past the item's
+    // rows stays in its own rows of the product)
+    const int steps = r32 / 16;
+    uint4 *const frags = reinterpret_cast<uint4 *>(part);
+    for (int i = threadIdx.x; i < steps * 32; i += kThreads) {
+        const int ln = i & 31, s = i >> 5;
+        const int k = 32 * (s / 2) + 8 * (ln & 3) + 4 * (s & 1), row = ln >> 2;
+        const float4 u = *reinterpret_cast<const float4 *>(h + row * r32 + k);
+        const float4 w = *reinterpret_cast<const float4 *>(h + (row + 8) * r32 + k);
+        float a[4] = {u.x, u.y, u.z, u.w}, b[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int q = 0; q < kTerms; ++q) {
-            uint32_t w[4];
+            uint32_t x[4], y[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                w[j] = take_part<BF16>(v[j]);
-            frags[((s * NT + t) * kTerms + q) * 32 + ln] = make_uint2(w[1] << 16 | w[0], w[3] << 16 | w[2]);
+            for (int j = 0; j < 4; ++j) {
+                x[j] = take_part<BF16>(a[j]);
+                y[j] = take_part<BF16>(b[j]);
+            }
+            frags[(s * kTerms + q) * 32 + ln] =
+                make_uint4(x[1] << 16 | x[0], y[1] << 16 | y[0], x[3] << 16 | x[2], y[3] << 16 | y[2]);
         }
     }
     __syncthreads();
-    // out^T, this CTA's share of N
-    for (int tile = tile_lo + warp; tile < tile_hi; tile += kWarps) {
-        const int n_lo = tile * 16 + g, n_hi = n_lo + 8;
-        const uint16_t *const b_lo = n_lo < p.N ? B + static_cast<long long>(n_lo) * p.r : nullptr;
-        const uint16_t *const b_hi = n_hi < p.N ? B + static_cast<long long>(n_hi) * p.r : nullptr;
-        float acc[NT][4] = {};
-#pragma unroll 4
-        for (int s = 0; s < steps; ++s) {
-            const uint2 u = load4(b_lo, 16 * s + 4 * c, p.r, p.vec_r), v = load4(b_hi, 16 * s + 4 * c, p.r, p.vec_r);
+    // out, this CTA's share of N: in tile j of 8, the MMA's column i is column
+    // 8 (i / 2) + 2 j + i % 2 of the block (a lane's 2 c and 2 c + 1 of four tiles are 8 c ..
+    // 8 c + 7), or 8 j + i where rows of base or out do not lie on 16 bytes
+    for (int block = block_lo + warp; block < block_hi; block += kWarps) {
+        const int n0 = block * 32;
+        int to[2];
+        Eight<OUT> old[2];
+        const bool whole = p.vec_n && n0 + 8 * c < p.N;         // (vec_n: eight columns are in or out of N)
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+        for (int i = 0; i < 2; ++i) {
+            to[i] = rows[8 * i + g];
+            if (whole && to[i] >= 0)
+                old[i].load(p.base, to[i] * p.ld_base + n0 + 8 * c);
+        }
+        const uint16_t *b_row[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int n = n0 + (p.vec_n ? 8 * (g >> 1) + 2 * j + (g & 1) : 8 * j + g);
+            b_row[j] = n < p.N ? B + static_cast<long long>(n) * p.r : nullptr;
+        }
+        float acc[4][4] = {};
+#pragma unroll 2
+        for (int s = 0; s < steps; s += 2) {
+            uint4 b[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                b[j] = load8(b_row[j], 16 * s + 8 * c, p.r, p.vec_r);
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
 #pragma unroll
                 for (int q = 0; q < kTerms; ++q) {
-                    const uint2 f = frags[((s * NT + t) * kTerms + q) * 32 + lane];
-                    mma<BF16>(acc[t], u.x, v.x, u.y, v.y, f.x, f.y);
+                    const uint4 f = frags[((s + half) * kTerms + q) * 32 + lane];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        mma<BF16>(acc[j], f.x, f.y, f.z, f.w, half ? b[j].z : b[j].x, half ? b[j].w : b[j].y);
                 }
         }
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int i = 0; i < 2; ++i) {
+            if (to[i] < 0)
+                continue;
+            const float f = BF16 ? 1.f : factor[8 * i + g];
+            const long long at_out = to[i] * p.ld_out + n0, at_base = to[i] * p.ld_base + n0;
+            if (p.vec_n) {
+                if (!whole)
+                    continue;
+                float v[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int n = i < 2 ? n_lo : n_hi, slot = 8 * t + 2 * c + (i & 1), row = rows[slot];
-                if (n < p.N && row >= 0) {
-                    const float f = BF16 ? 1.f : factor[slot];
-                    store_out<OUT>(p.out, row * p.ld_out + n, fmaf(acc[t][i], f, load_out<OUT>(p.base, row * p.ld_base + n)));
+                for (int j = 0; j < 8; ++j)
+                    v[j] = fmaf(acc[j >> 1][2 * i + (j & 1)], f, old[i].at(j));
+                old[i].store(p.out, at_out + 8 * c, v);
+            } else {
+                float v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int n = 8 * (j >> 1) + 2 * c + (j & 1);
+                    v[j] = n0 + n < p.N ? load_out<OUT>(p.base, at_base + n) : 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int n = 8 * (j >> 1) + 2 * c + (j & 1);
+                    if (n0 + n < p.N)
+                        store_out<OUT>(p.out, at_out + n, fmaf(acc[j >> 1][2 * i + (j & 1)], f, v[j]));
                 }
             }
+        }
     }
 }
 
 bool on(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-template <bool BF16, int OUT, int NT>
+template <bool BF16, int OUT>
 cudaError_t launch_few(const AdapterParams &p, long long items, const DeviceView &dev, cudaStream_t stream)
 {
     constexpr int kTerms = BF16 && OUT == W8A8_OUT_FP32 ? 3 : 2;
+    using S = FewSmem<kTerms>;
     constexpr size_t kRoom = 200 * 1024;
-    auto kernel = k_adapter_few<BF16, OUT, NT>;
-    // As many CTAs share an item as fill the SMs twice, with 128 columns of K for each.
+    auto kernel = k_adapter_few<BF16, OUT>;
+    // As many CTAs share an item as fill the SMs twice, 16 as fill them once, with 128
+    // columns of K for each (one row, rank 16, 4096x4096: 4 CTAs 8.9 us, 8 6.7, 16 6.2; 64
+    // rows of 32 adapters of rank 64: 2 23 us, 4 14.7, 8 11.4).
     int cluster = 1;
-    while (cluster < kMaxCluster && items * cluster * 2 <= 2ll * dev.sm_count && cluster * 2 * 128 <= p.K &&
-           FewSmem<NT>::bytes(kTerms, p.r_pad, cluster * 2) <= kRoom)
+    while (cluster < kMaxCluster && items * cluster * 2 <= (cluster < 8 ? 2ll : 1ll) * dev.sm_count &&
+           cluster * 2 * 128 <= p.K && S::bytes(p.r_pad, cluster * 2) <= kRoom)
         cluster *= 2;
-    const size_t smem = FewSmem<NT>::bytes(kTerms, p.r_pad, cluster);
+    const size_t smem = S::bytes(p.r_pad, cluster);
     static volatile int flags[kMaxDeviceFlags] = {};
-    if (const cudaError_t e = allow_smem(kernel, kRoom, flags); e != cudaSuccess)
+    if (const cudaError_t e = allow_smem(kernel, kRoom, flags, true); e != cudaSuccess)
         return e;
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3(static_cast<unsigned>(items * cluster), 1, 1);
@@ -342,24 +441,29 @@ template <bool BF16, int OUT> cudaError_t launch_adapter(const AdapterParams &p,
     const long long groups = p.out == p.base ? p.L : p.L + 1;
     if (groups == 0)
         return cudaSuccess;
-    if (p.T <= 4 * p.L)
-        return launch_few<BF16, OUT, 1>(p, most_items(p.T, groups, 8), dev, s);
-    return launch_few<BF16, OUT, 2>(p, most_items(p.T, groups, 16), dev, s);
+    return launch_few<BF16, OUT>(p, most_items(p.T, groups, kRows), dev, s);
 }
 
-// Whether a problem's sizes are for the tiles of 128 rows (adapter_tile.cu): where adapters
-// have many rows on average.
-bool tiled(const AdapterParams &p) { return p.L > 0 && p.T >= 32 * p.L && p.r >= 8 && p.K >= 64; }
-
-size_t workspace_bytes(const AdapterParams &p)
+// Whether a problem's sizes are for the tiles of 128 rows (adapter_tile.cu), which take two
+// launches and some 20 us for them, then stream: where rows are many, and many to an adapter
+// (16 rows a cluster against tiles, rank 64, 4096x4096: 2048 rows of 32 adapters 47 / 67 us, 4096
+// of 16 53 / 45, 8192 103 / 53; 1024x8192 from rank 32 into bf16: 2048 rows 30.0 / 26.7, 4096
+// 55 / 41; of rank 128 into fp32: 2048 73 / 90, 4096 138 / 148).
+bool tiled(const AdapterParams &p)
 {
-    return tiled(p) ? sizeof(float) * tile_splits(p) * p.T * p.r_pad : 0;
+    return p.L > 0 && p.T >= (p.r <= 64 ? 2560 : 5120) && p.T / 64 >= p.L && p.r >= 8 && p.K >= 64;
+}
+
+size_t workspace_bytes(const AdapterParams &p, int variant)
+{
+    const bool tiles = variant == W8A8_VARIANT_TILED || (variant == W8A8_VARIANT_AUTO && tiled(p));
+    return tiles ? sizeof(float) * tile_splits(p) * p.T * p.r_pad : 0;
 }
 
 }  // namespace
 }  // namespace w8a8
 
-extern "C" size_t w8a8_adapter_workspace_size(int64_t T, int64_t L, int64_t r, int64_t K)
+extern "C" size_t w8a8_adapter_workspace_size(int64_t T, int64_t L, int64_t r, int64_t K, int variant)
 {
     using namespace w8a8;
     if (T <= 0 || L <= 0 || r <= 0 || K <= 0 || L > W8A8_GROUPS_MAX || r > W8A8_ADAPTER_MAX_R || T >= (1ll << 28) ||
@@ -371,21 +475,25 @@ extern "C" size_t w8a8_adapter_workspace_size(int64_t T, int64_t L, int64_t r, i
     p.r = static_cast<int>(r);
     p.K = static_cast<int>(K);
     p.r_pad = static_cast<int>((r + 15) / 16 * 16);
-    return workspace_bytes(p);
+    return workspace_bytes(p, variant);
 }
 
 extern "C" w8a8_status w8a8_adapter_matmul(const void *x_dev, w8a8_in_dtype dtype, int64_t ld_x, const void *A_dev,
                                            const void *B_dev, const int32_t *order_dev, const int32_t *offsets_dev,
                                            const float *scales_dev, const void *base_dev, int64_t ld_base,
                                            void *out_dev, w8a8_out_dtype out_dtype, int64_t ld_out, int64_t T,
-                                           int64_t L, int64_t r, int64_t K, int64_t N, void *workspace_dev,
-                                           size_t workspace_bytes, w8a8_stream_t stream)
+                                           int64_t L, int64_t r, int64_t K, int64_t N, int variant,
+                                           void *workspace_dev, size_t workspace_bytes, w8a8_stream_t stream)
 {
     using namespace w8a8;
     if (T < 0 || L < 0 || r < 0 || K < 0 || N < 0)
         return record_error(W8A8_ERR_INVALID_ARG, "negative size");
     if (dtype < W8A8_IN_BF16 || dtype > W8A8_IN_FP32 || out_dtype < W8A8_OUT_BF16 || out_dtype > W8A8_OUT_FP32)
         return record_error(W8A8_ERR_INVALID_ARG, "unknown dtype");
+    if (variant < W8A8_VARIANT_AUTO || variant > W8A8_VARIANT_GENERIC)
+        return record_error(W8A8_ERR_INVALID_ARG, "unknown variant");
+    if (variant != W8A8_VARIANT_AUTO && variant != W8A8_VARIANT_SMALLM && variant != W8A8_VARIANT_TILED)
+        return record_error(W8A8_ERR_UNSUPPORTED, "variant must be AUTO, SMALLM or TILED");
     if (dtype == W8A8_IN_FP32)
         return record_error(W8A8_ERR_UNSUPPORTED, "x, A and B must be bf16 or fp16");
     if (out_dtype != W8A8_OUT_FP32 && static_cast<int>(out_dtype) != static_cast<int>(dtype))
@@ -429,11 +537,15 @@ extern "C" w8a8_status w8a8_adapter_matmul(const void *x_dev, w8a8_in_dtype dtyp
     p.N = static_cast<int>(N);
     p.r_pad = static_cast<int>((r + 15) / 16 * 16);
     p.vec_k = K % 8 == 0 && ld_x % 8 == 0 && on(x_dev, 16) && on(A_dev, 16);
-    p.vec_r = r % 4 == 0 && on(B_dev, 8);
+    p.vec_r = r % 8 == 0 && on(B_dev, 16);
     const int each = 16 / ob;
-    p.vec_n = N % each == 0 && ld_base % each == 0 && ld_out % each == 0 && on(base_dev, 16) && on(out_dev, 16);
-    const bool tiles = tiled(p) && tile_takes(p);
-    if (const size_t need = tiles ? w8a8::workspace_bytes(p) : 0;
+    p.vec_n = N % 8 == 0 && ld_base % each == 0 && ld_out % each == 0 && on(base_dev, 16) && on(out_dev, 16);
+    const bool fits = L > 0 && tile_takes(p);
+    if (variant == W8A8_VARIANT_TILED && !fits)
+        return record_error(W8A8_ERR_UNSUPPORTED, "TILED needs an adapter, r % 8 == 0 from 8 to 128, K % 8 == 0 from 64 on, "
+                                                  "N % 8 == 0 and rows on 16-byte boundaries");
+    const bool tiles = fits && (variant == W8A8_VARIANT_TILED || (variant == W8A8_VARIANT_AUTO && tiled(p)));
+    if (const size_t need = tiles ? w8a8::workspace_bytes(p, variant) : 0;
         need && (!workspace_dev || workspace_bytes < need || !on(workspace_dev, 16))) {
         char msg[160];
         snprintf(msg, sizeof(msg), "workspace of %zu bytes at %p: need %zu bytes, 16-byte aligned", workspace_bytes,
@@ -443,6 +555,8 @@ extern "C" w8a8_status w8a8_adapter_matmul(const void *x_dev, w8a8_in_dtype dtyp
     DeviceView dev;
     if (const int st = device_view(&dev); st != W8A8_OK)
         return static_cast<w8a8_status>(st);
+    p.status = dev.status;
+    p.wait_limit = dev.wait_limit;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (tiles)

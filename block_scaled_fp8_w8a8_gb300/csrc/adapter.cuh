@@ -22,8 +22,10 @@ struct AdapterParams {
     long long ld_x, ld_base, ld_out;
     int T, L, r, K, N;
     int r_pad;                  // r up to whole 16
-    int vec_k, vec_r;           // 16-byte pieces of x and A, 8-byte pieces of B
-    int vec_n;                  // 16-byte pieces of base and out
+    int vec_k, vec_r;           // 16-byte pieces of x and A, of B
+    unsigned *status;
+    unsigned long long wait_limit;
+    int vec_n;                  // eight columns of base and out at a time, by 16 bytes
 };
 
 // The power of two that brings a row of h, whose largest size is top, near 2^14: the
@@ -131,9 +133,10 @@ __device__ __forceinline__ void copy_rows(const AdapterParams &p, const int *row
     }
 }
 
-// Up to `bytes` of dynamic shared memory for a kernel, set once per device by its own
-// flags.  (The device's most would leave nothing for the kernel's static arrays.)
-template <typename Kernel> inline cudaError_t allow_smem(Kernel kernel, size_t bytes, volatile int *set)
+// Up to `bytes` of dynamic shared memory for a kernel, and clusters of up to 16 CTAs,
+// set once per device by its own flags.  (The device's most would leave nothing for the kernel's static arrays.)
+template <typename Kernel>
+inline cudaError_t allow_smem(Kernel kernel, size_t bytes, volatile int *set, bool large_clusters = false)
 {
     int id = 0;
     cudaError_t e = cudaGetDevice(&id);
@@ -141,6 +144,8 @@ template <typename Kernel> inline cudaError_t allow_smem(Kernel kernel, size_t b
         e = cudaErrorInvalidDevice;
     if (e == cudaSuccess && !set[id]) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+        if (e == cudaSuccess && large_clusters)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         set[id] = e == cudaSuccess;
     }
     return e;
@@ -159,8 +164,6 @@ struct TileParams {
     float *h;                   // [splits, T, r_pad]: scales[l] x A^T of K's parts, by place
     int splits;
     int chunks;                 // CTAs that share a tile's columns
-    unsigned *status;
-    unsigned long long wait_limit;
 };
 // Whether they take a problem (16-byte pieces everywhere, r in bounds), and by how
 // many parts of K.

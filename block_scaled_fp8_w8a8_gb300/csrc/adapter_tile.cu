@@ -137,7 +137,7 @@ template <bool BF16, int STAGES> __global__ void __launch_bounds__(kShrinkThread
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = tmem_slot;
-    const WaitGuard guard{&abort_word, p.status, p.wait_limit};
+    const WaitGuard guard{&abort_word, p.a.status, p.a.wait_limit};
     const int blocks = (p.a.K + 63) / 64;
     const int lo = static_cast<int>(static_cast<long long>(blocks) * split / p.splits);
     const int steps = item.rows ? static_cast<int>(static_cast<long long>(blocks) * (split + 1) / p.splits) - lo : 0;
@@ -179,7 +179,7 @@ template <bool BF16, int STAGES> __global__ void __launch_bounds__(kShrinkThread
             mma_commit_elect<false>(done);
         // no commit arrives on this CTA's shared memory after it exits
         mma_commit_elect<false>(drain);
-        wait_drain(drain, 0, p.status, p.wait_limit, (SITE_DRAIN << 8) | 4u);
+        wait_drain(drain, 0, p.a.status, p.a.wait_limit, (SITE_DRAIN << 8) | 4u);
     } else if (warp == 5 && steps) {
         const RowLoads load(rows, item.rows, p.a.T);
         int i = 0;
@@ -198,7 +198,7 @@ template <bool BF16, int STAGES> __global__ void __launch_bounds__(kShrinkThread
             load(dst, &map_x, &map_x32, bar, k);
         }
         if (i < steps)
-            drain_loads<STAGES>(full, i, p.status, p.wait_limit);
+            drain_loads<STAGES>(full, i, p.a.status, p.a.wait_limit);
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kExpandThreads) k_adapter_expand(
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = tmem_slot;
-    const WaitGuard guard{&abort_word, p.status, p.wait_limit};
+    const WaitGuard guard{&abort_word, p.a.status, p.a.wait_limit};
     const int col_tiles = (p.a.N + kCols - 1) / kCols;
     const int lo = static_cast<int>(static_cast<long long>(col_tiles) * chunk / p.chunks);
     const int hi = static_cast<int>(static_cast<long long>(col_tiles) * (chunk + 1) / p.chunks);
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kExpandThreads) k_adapter_expand(
             load(dst + base_at, &map_base, &map_base32, bar, n0);
         }
         if (i < steps)
-            drain_loads<STAGES>(full, i, p.status, p.wait_limit);
+            drain_loads<STAGES>(full, i, p.a.status, p.a.wait_limit);
     }
     grid_dependency_wait();
     grid_launch_dependents();
@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kExpandThreads) k_adapter_expand(
         }
         // no commit arrives on this CTA's shared memory, and none reads it, after it exits
         mma_commit_elect<false>(drain);
-        wait_drain(drain, 0, p.status, p.wait_limit, (SITE_DRAIN << 8) | 4u);
+        wait_drain(drain, 0, p.a.status, p.a.wait_limit, (SITE_DRAIN << 8) | 4u);
     }
     if (item.rows && item.adapter == p.a.L) {
         // rows without an adapter
@@ -589,8 +589,6 @@ cudaError_t launch_tile(const AdapterParams &a, int x_kind, int out_kind, float 
     p.a = a;
     p.h = h;
     p.splits = tile_splits(a);
-    p.status = dev.status;
-    p.wait_limit = dev.wait_limit;
     if (x_kind == W8A8_IN_BF16)
         return out_kind == W8A8_OUT_FP32 ? launch_both<true, W8A8_OUT_FP32>(p, dev, stream)
                                          : launch_both<true, W8A8_OUT_BF16>(p, dev, stream);

@@ -32,9 +32,9 @@ typedef int (*combine_fn)(const void *, int, int64_t, int64_t, const int32_t *, 
                           stream_t);
 typedef int (*adapter_fn)(const void *, int, int64_t, const void *, const void *, const int32_t *,
                           const int32_t *, const float *, const void *, int64_t, void *, int,
-                          int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, void *, size_t,
-                          stream_t);
-typedef size_t (*adapter_size_fn)(int64_t, int64_t, int64_t, int64_t);
+                          int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int, void *,
+                          size_t, stream_t);
+typedef size_t (*adapter_size_fn)(int64_t, int64_t, int64_t, int64_t, int);
 
 static norm_fn f_norm;
 static ragged_fn f_ragged;
@@ -404,33 +404,37 @@ static int is_current(long gpu)
     return ok;
 }
 
-/* Device scratch of `bytes`: a tensor of t's device on the current stream, a new
- * reference, and its address; NULL and no address for 0.  0 on an error. */
-static int scratch_of(PyObject *t, size_t bytes, PyObject *u8, PyObject **keep, void **ptr)
+/* A new tensor [n] on t's device and the current stream, of dtype or (NULL) t's; a new
+ * reference and its address, or NULL with an error set. */
+static PyObject *new_tensor(PyObject *t, int64_t n, PyObject *dtype, void **ptr)
 {
     static PyObject *new_empty, *kw;
-    *keep = NULL;
-    *ptr = NULL;
-    if (!bytes)
-        return 1;
     if (!new_empty && !(new_empty = PyUnicode_InternFromString("new_empty")))
-        return 0;
+        return NULL;
     if (!kw && !(kw = Py_BuildValue("(s)", "dtype")))
-        return 0;
-    PyObject *n = PyLong_FromSize_t(bytes);
-    PyObject *shape = n ? PyTuple_Pack(1, n) : NULL;
-    PyObject *call_args[3] = {t, shape, u8};
-    *keep = shape && u8 ? PyObject_VectorcallMethod(new_empty, call_args, 2, kw) : NULL;
-    Py_XDECREF(n);
+        return NULL;
+    PyObject *count = PyLong_FromLongLong(n);
+    PyObject *shape = count ? PyTuple_Pack(1, count) : NULL;
+    PyObject *call_args[3] = {t, shape, dtype};
+    PyObject *made = shape ? PyObject_VectorcallMethod(new_empty, call_args, 2, dtype ? kw : NULL) : NULL;
+    Py_XDECREF(count);
     Py_XDECREF(shape);
-    PyObject *o = *keep ? call(*keep, PTR_OF) : NULL;
+    PyObject *o = made ? call(made, PTR_OF) : NULL;
     if (o)
         *ptr = (void *)(uintptr_t)PyLong_AsUnsignedLongLong(o);
     Py_XDECREF(o);
     if (o && !PyErr_Occurred())
-        return 1;
-    Py_CLEAR(*keep);
-    return 0;
+        return made;
+    Py_XDECREF(made);
+    return NULL;
+}
+
+/* Device scratch of `bytes`: NULL and no address for 0.  0 on an error. */
+static int scratch_of(PyObject *t, size_t bytes, PyObject *u8, PyObject **keep, void **ptr)
+{
+    *keep = NULL;
+    *ptr = NULL;
+    return !bytes || (u8 && (*keep = new_tensor(t, (int64_t)bytes, u8, ptr)) != NULL);
 }
 
 /* The types of the routing calls: int32, float32, bool, uint8. */
@@ -497,36 +501,50 @@ other:
     Py_RETURN_NONE;
 }
 
-/* ids, groups, outputs, dtypes, stream */
+/* ids, groups, outputs, dtypes, stream.  Without outputs (None) the result is a tuple of new
+ * ones, or a status other than 0. */
 static PyObject *py_group_tensors(PyObject *self, PyObject *const *args, Py_ssize_t n)
 {
     (void)self;
     if (!want(n, 5, f_group != NULL))
         return NULL;
     tensor_t ids, order, offsets;
+    PyObject *made[2] = {NULL, NULL}, *keep = NULL;
     long gpu = ANY_GPU;
     PyObject *const i32 = type_at(args[3], R_INT32);
-    if (!PyTuple_Check(args[2]) || PyTuple_GET_SIZE(args[2]) != 2 || !PyLong_Check(args[1]) ||
-        !typed(args[0], &ids, &gpu, 1, i32) || !typed(PyTuple_GET_ITEM(args[2], 0), &order, &gpu, 1, i32) ||
-        !typed(PyTuple_GET_ITEM(args[2], 1), &offsets, &gpu, 1, i32))
+    if (!PyLong_Check(args[1]) || !typed(args[0], &ids, &gpu, 1, i32))
         goto other;
     const int64_t count = ids.size[0], groups = I64(1);
-    const size_t size = f_group_size(count, groups);
-    if (groups < 1 || !is(&order, 1, count, 0) || !is(&offsets, 1, groups + 1, 0) || !is_current(gpu) ||
-        (size && args[4] != Py_None))
+    if (groups < 1 || groups > 1024 || !is_current(gpu))
         goto other;
+    const size_t size = f_group_size(count, groups);
+    if ((size || args[2] == Py_None) && args[4] != Py_None)
+        goto other;
+    if (args[2] == Py_None) {
+        if (!(made[0] = new_tensor(args[0], count, NULL, &order.ptr)) ||
+            !(made[1] = new_tensor(args[0], groups + 1, NULL, &offsets.ptr)))
+            goto other;
+    } else if (!PyTuple_Check(args[2]) || PyTuple_GET_SIZE(args[2]) != 2 ||
+               !typed(PyTuple_GET_ITEM(args[2], 0), &order, &gpu, 1, i32) || !is(&order, 1, count, 0) ||
+               !typed(PyTuple_GET_ITEM(args[2], 1), &offsets, &gpu, 1, i32) || !is(&offsets, 1, groups + 1, 0)) {
+        goto other;
+    }
     void *s = stream_of(args[4]), *scratch;
-    PyObject *keep;
     if (PyErr_Occurred() || !scratch_of(args[0], size, type_at(args[3], R_U8), &keep, &scratch))
         goto other;
     int st;
     Py_BEGIN_ALLOW_THREADS
     st = f_group(ids.ptr, count, groups, order.ptr, offsets.ptr, NULL, scratch, size, s);
     Py_END_ALLOW_THREADS
+    PyObject *result = made[0] && !st ? PyTuple_Pack(2, made[0], made[1]) : PyLong_FromLong(st);
     Py_XDECREF(keep);
-    return PyLong_FromLong(st);
+    Py_XDECREF(made[0]);
+    Py_XDECREF(made[1]);
+    return result;
 other:
     PyErr_Clear();
+    Py_XDECREF(made[0]);
+    Py_XDECREF(made[1]);
     Py_RETURN_NONE;
 }
 
@@ -581,7 +599,7 @@ static PyObject *py_adapter_tensors(PyObject *self, PyObject *const *args, Py_ss
     if (args[6] != Py_None && (!typed(args[6], &scales, &gpu, 1, type_at(args[9], R_F32)) || !is(&scales, 1, L, 0)))
         goto other;
     const int kind = code_of(args[8], x.dtype), out_kind = code_of(args[8], out.dtype);
-    const size_t size = f_adapter_size(T, L, r, K);
+    const size_t size = f_adapter_size(T, L, r, K, 0);
     if (kind < 0 || out_kind < 0 || !is_current(gpu) || (size && args[10] != Py_None))
         goto other;
     void *s = stream_of(args[10]), *scratch;
@@ -591,7 +609,7 @@ static PyObject *py_adapter_tensors(PyObject *self, PyObject *const *args, Py_ss
     int st;
     Py_BEGIN_ALLOW_THREADS
     st = f_adapter(x.ptr, kind, 0, a.ptr, b.ptr, order.ptr, offsets.ptr, scales.ptr, base.ptr, 0, out.ptr, out_kind, 0,
-                   T, L, r, K, N, scratch, size, s);
+                   T, L, r, K, N, 0, scratch, size, s);
     Py_END_ALLOW_THREADS
     Py_XDECREF(keep);
     return PyLong_FromLong(st);

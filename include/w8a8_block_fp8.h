@@ -648,8 +648,10 @@ w8a8_status w8a8_combine_experts(const void *Y_dev, w8a8_in_dtype y_dtype, int64
  * decrease or leave [0, T] give unspecified results but no out-of-bounds access.
  * L <= W8A8_GROUPS_MAX, r <= W8A8_ADAPTER_MAX_R; any K and N up to 2^24, strides and
  * alignments (pieces of 16 bytes where K % 8 == 0, r % 4 == 0 and the rows allow).
- * T == 0 or N == 0 is a no-op.  The launches (one, or two for many rows) wait on the
- * device for the work before them on the stream.
+ * T == 0 or N == 0 is a no-op.  variant (w8a8_variant): AUTO; SMALLM, one launch of
+ * clusters on 16 rows each; TILED, two launches of 128-row tiles on the tensor cores' tcgen05
+ * path (r % 8 == 0 from 8 to 128, K % 8 == 0 from 64 on, N % 8 == 0, rows on 16-byte
+ * boundaries, L > 0).  The launches wait on the device for the work before them on the stream.
  * workspace_dev: w8a8_adapter_workspace_size() bytes (0 for few rows), 16-byte aligned, in
  * use until the stream has passed the call; its contents do not matter.
  */
@@ -659,11 +661,12 @@ w8a8_status w8a8_adapter_matmul(const void *x_dev, w8a8_in_dtype dtype, int64_t 
                                 const int32_t *offsets_dev, const float *scales_dev,
                                 const void *base_dev, int64_t ld_base, void *out_dev,
                                 w8a8_out_dtype out_dtype, int64_t ld_out, int64_t T, int64_t L,
-                                int64_t r, int64_t K, int64_t N, void *workspace_dev,
-                                size_t workspace_bytes, w8a8_stream_t stream);
+                                int64_t r, int64_t K, int64_t N, int variant,
+                                void *workspace_dev, size_t workspace_bytes,
+                                w8a8_stream_t stream);
 
 /* Workspace bytes that w8a8_adapter_matmul takes at most (0 for none, or bad sizes). */
-size_t w8a8_adapter_workspace_size(int64_t T, int64_t L, int64_t r, int64_t K);
+size_t w8a8_adapter_workspace_size(int64_t T, int64_t L, int64_t r, int64_t K, int variant);
 
 /*
  * Per-token-group FP8 quantiser: makes the matmul's activation operand A and

@@ -405,7 +405,8 @@ def check_adapters(c, **kw):
     assert torch.equal(got[c["ids"] < 0], before[c["ids"] < 0])
     # the same bits again, in place too
     again = c["base"].clone()
-    assert w8.adapter_matmul(c["x"], c["A"], c["B"], order, offsets, again, scales=c["scales"], out=again) is again
+    assert w8.adapter_matmul(c["x"], c["A"], c["B"], order, offsets, again, scales=c["scales"], out=again,
+                             variant=kw.get("variant", 0)) is again
     assert torch.equal(again, got)
     ok()
     return got
@@ -426,7 +427,10 @@ def test_adapters(T, L, K, N, r, dtype, out):
     check_adapters(c)
 
 
-# Many rows per adapter: tiles of 128 rows (T >= 32 L, 16-byte rows).
+SMALL, TILED = w8.W8A8_VARIANT_SMALLM, w8.W8A8_VARIANT_TILED
+
+
+# The tiles of 128 rows.
 @pytest.mark.parametrize("T,L,K,N,r", [
     (32, 1, 64, 8, 8), (128, 1, 128, 64, 16), (129, 1, 72, 72, 24), (255, 2, 4096, 256, 64), (1000, 3, 1000, 1032, 40),
     (640, 20, 256, 200, 56), (5000, 4, 512, 264, 48), (300, 2, 328, 4096, 128), (257, 1, 64, 136, 72), (400, 3, 2048, 64, 104),
@@ -434,27 +438,40 @@ def test_adapters(T, L, K, N, r, dtype, out):
 ])
 @pytest.mark.parametrize("dtype,out", [("bf16", None), ("fp16", None), ("bf16", "fp32"), ("fp16", "fp32")])
 def test_adapters_many_rows(T, L, K, N, r, dtype, out):
-    assert w8.w8a8_adapter_workspace_size(T, L, r, K) > 0
     c = adapter_case(T, L, K, N, r, dtype, out)
-    check_adapters(c)
+    check_adapters(c, variant=TILED)
     c["scales"] = None
     c["ids"] = torch.sort(c["ids"], descending=True).values.clone()
-    check_adapters(c)
+    check_adapters(c, variant=TILED)
+
+
+def test_adapters_forms_chosen_by_themselves():
+    """Either form at sizes that are its own, and TILED refused where it does not fit."""
+    for T, L in ((100, 4), (6000, 4)):
+        c = adapter_case(T, L, 256, 264, 16, "bf16", None)
+        order, offsets = w8.group_rows(c["ids"], L)
+        call = lambda **kw: w8.adapter_matmul(c["x"], c["A"], c["B"], order, offsets, c["base"], **kw)  # noqa: E731
+        assert torch.equal(call(), call(variant=SMALL if T == 100 else TILED))
+        check_adapters(c)
+    with pytest.raises(w8.W8A8Error) as e:
+        w8.adapter_matmul(c["x"], c["A"], c["B"], order, offsets, c["base"][:, :259].contiguous()[:, :0], variant=TILED)
+    assert e.value.status in (w8.W8A8_ERR_INVALID_ARG, w8.W8A8_ERR_UNSUPPORTED)
 
 
 def test_adapters_many_rows_bad_order_and_offsets_stay_in_bounds():
     c = adapter_case(400, 3, 128, 64, 8, "bf16", None, none=0.0)
     order, offsets = w8.group_rows(c["ids"], 3)
-    good = w8.adapter_matmul(c["x"], c["A"], c["B"], order, offsets, c["base"])
+    good = w8.adapter_matmul(c["x"], c["A"], c["B"], order, offsets, c["base"], variant=TILED)
     bad = order.clone()
     bad[3], bad[200] = -5, 2 ** 30
     out = torch.full_like(c["base"], 7.0)
-    w8.adapter_matmul(c["x"], c["A"], c["B"], bad, offsets, c["base"], out=out)
+    w8.adapter_matmul(c["x"], c["A"], c["B"], bad, offsets, c["base"], out=out, variant=TILED)
     skipped = order[[3, 200]].long().tolist()
     rest = [i for i in range(400) if i not in skipped]
     assert (out[skipped] == 7.0).all() and torch.equal(out[rest], good[rest])
     for wrong in ([0, 999, -4, 400], [300, 200, 100, 0], [-1, 2 ** 31 - 1, -2 ** 31, 5]):
-        w8.adapter_matmul(c["x"], c["A"], c["B"], order, torch.tensor(wrong, dtype=torch.int32, device="cuda"), c["base"])
+        w8.adapter_matmul(c["x"], c["A"], c["B"], order, torch.tensor(wrong, dtype=torch.int32, device="cuda"), c["base"],
+                          variant=TILED)
     ok()
 
 
@@ -462,19 +479,19 @@ def test_adapters_many_rows_strides_not_finite_rows_and_large_fp16_sums():
     for dtype in ("bf16", "fp16"):
         c = adapter_case(500, 2, 200, 96, 16, dtype, "fp32", none=0.1)
         order, offsets = w8.group_rows(c["ids"], 2)
-        clean = check_adapters(c)
+        clean = check_adapters(c, variant=TILED)
         x, base = torch.zeros(500, 264, device="cuda", dtype=c["x"].dtype), torch.zeros(500, 100, device="cuda")
         x[:, 8:208], base[:, :96] = c["x"], c["base"]
-        assert torch.equal(check_adapters(dict(c, x=x[:, 8:208], base=base[:, :96])), clean)
+        assert torch.equal(check_adapters(dict(c, x=x[:, 8:208], base=base[:, :96]), variant=TILED), clean)
         t = (c["ids"] >= 0).nonzero()[:, 0][[5, 90]].tolist()
         c["x"][t[0], 17], c["x"][t[1], 3] = math.nan, math.inf
-        got = w8.adapter_matmul(c["x"], c["A"], c["B"], order, offsets, c["base"], scales=c["scales"])
+        got = w8.adapter_matmul(c["x"], c["A"], c["B"], order, offsets, c["base"], scales=c["scales"], variant=TILED)
         assert got[t[0]].isnan().all() and not got[t[1]].isfinite().any()
         others = [i for i in range(500) if i not in t]
         assert torch.equal(got[others], clean[others])
     c = adapter_case(200, 2, 1024, 136, 40, "fp16", "fp32", sizes=200.0)
     c["A"] = (c["A"].float() * 256).half()
-    check_adapters(c)
+    check_adapters(c, variant=TILED)
 
 
 def test_adapters_many_rows_captured_twice_and_replayed_at_once():
@@ -482,10 +499,10 @@ def test_adapters_many_rows_captured_twice_and_replayed_at_once():
     for i in range(2):
         c = adapter_case(1500, 4, 512, 264, 32, "bf16", None, seed=i)
         order, offsets = w8.group_rows(c["ids"], 4)
-        w8.adapter_matmul(c["x"], c["A"], c["B"], order, offsets, c["base"], scales=c["scales"])
+        w8.adapter_matmul(c["x"], c["A"], c["B"], order, offsets, c["base"], scales=c["scales"], variant=TILED)
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
-            outs.append(w8.adapter_matmul(c["x"], c["A"], c["B"], order, offsets, c["base"], scales=c["scales"]))
+            outs.append(w8.adapter_matmul(c["x"], c["A"], c["B"], order, offsets, c["base"], scales=c["scales"], variant=TILED))
         graphs.append(graph), cases.append(c), kept.append((order, offsets))      # the graph reads them
     streams = [torch.cuda.Stream() for _ in range(2)]
     for _ in range(5):

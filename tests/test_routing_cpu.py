@@ -52,6 +52,7 @@ def test_workspace_sizes():
 
     size = w8.w8a8_adapter_workspace_size
     assert size(64, 32, 16, 4096) == 0 and size(16384, 16, 64, 4096) >= 16384 * 64 * 4
+    assert size(64, 32, 16, 4096, w8.W8A8_VARIANT_TILED) > 0 and size(16384, 16, 64, 4096, w8.W8A8_VARIANT_SMALLM) == 0
     for bad in ((0, 1, 16, 64), (4096, 0, 16, 64), (4096, 1, 0, 64), (4096, 1, 16, 0), (1 << 28, 1, 16, 64),
                 (4096, 1, w8.W8A8_ADAPTER_MAX_R + 1, 64), (4096, w8.W8A8_GROUPS_MAX + 1, 16, 64)):
         assert size(*bad) == 0
@@ -90,11 +91,11 @@ def test_combine(kw, status):
     assert combine(**kw) == status
 
 
-def adapters(T=4, L=2, r=16, K=64, N=32, dtype=0, out_dtype=0, ld_x=0, ld_base=0, ld_out=0, **ptr):
+def adapters(T=4, L=2, r=16, K=64, N=32, dtype=0, out_dtype=0, ld_x=0, ld_base=0, ld_out=0, variant=0, **ptr):
     p = dict(x=256, A=256, B=256, order=256, off=256, scales=0, base=256, out=512, ws=0, size=0)
     p.update(ptr)
     return w8.w8a8_adapter_matmul(p["x"], dtype, ld_x, p["A"], p["B"], p["order"], p["off"], p["scales"], p["base"], ld_base,
-                                  p["out"], out_dtype, ld_out, T, L, r, K, N, p["ws"], p["size"], 0)
+                                  p["out"], out_dtype, ld_out, T, L, r, K, N, variant, p["ws"], p["size"], 0)
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -106,6 +107,12 @@ def adapters(T=4, L=2, r=16, K=64, N=32, dtype=0, out_dtype=0, ld_x=0, ld_base=0
     (dict(r=w8.W8A8_ADAPTER_MAX_R + 1), UNS), (dict(T=1 << 28), UNS), (dict(K=(1 << 24) + 1), UNS), (dict(x=257), UNS),
     (dict(base=258, out_dtype=2), UNS), (dict(scales=258), UNS), (dict(order=257), UNS), (dict(T=4096), WS),
     (dict(T=4096, ws=256, size=4096), WS), (dict(T=4096, ws=264, size=1 << 30), WS),
+    (dict(variant=-1), ARG), (dict(variant=8), ARG), (dict(variant=w8.W8A8_VARIANT_SWAPAB), UNS),
+    (dict(variant=w8.W8A8_VARIANT_TILED), WS), (dict(variant=w8.W8A8_VARIANT_TILED, r=12), UNS),
+    (dict(variant=w8.W8A8_VARIANT_TILED, r=136), UNS), (dict(variant=w8.W8A8_VARIANT_TILED, K=66), UNS),
+    (dict(variant=w8.W8A8_VARIANT_TILED, K=56), UNS), (dict(variant=w8.W8A8_VARIANT_TILED, N=36), UNS),
+    (dict(variant=w8.W8A8_VARIANT_TILED, x=264), UNS), (dict(variant=w8.W8A8_VARIANT_TILED, ld_x=65), UNS),
+    (dict(variant=w8.W8A8_VARIANT_TILED, L=0), UNS),
 ])
 def test_adapters(kw, status):
     assert adapters(**kw) == status
