@@ -32,15 +32,11 @@ struct GroupOut {
     long long n;
 };
 
-// Exclusive sums of a[0 .. n-1] in shared memory by all threads of the block;
-// returns the total.  `part` holds one int per warp.
-__device__ __forceinline__ int block_scan(int *a, int n, int *part)
+// Exclusive scan over the block's threads of one number each; part holds one int per
+// warp.  All threads call it, with a barrier between the writes and reads of part.
+template <int THREADS> __device__ __forceinline__ int thread_scan(int sum, int *part)
 {
-    const int threads = blockDim.x, t = threadIdx.x, warp = t >> 5, lane = t & 31;
-    const int q = (n + threads - 1) / threads, from = min(t * q, n), to = min(from + q, n);
-    int sum = 0;
-    for (int i = from; i < to; ++i)
-        sum += a[i];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int scan = sum;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
@@ -50,20 +46,20 @@ __device__ __forceinline__ int block_scan(int *a, int n, int *part)
     if (lane == 31)
         part[warp] = scan;
     __syncthreads();
-    int before = 0, total = 0;
-    for (int w = 0; w < threads / 32; ++w) {
-        const int v = part[w];
-        before += w < warp ? v : 0;
-        total += v;
+    int before = lane < THREADS / 32 ? part[lane] : 0;
+#pragma unroll
+    for (int d = 1; d < THREADS / 32; d *= 2) {
+        const int v = __shfl_up_sync(0xffffffffu, before, d);
+        before += lane >= d ? v : 0;
     }
-    int run = before + scan - sum;
-    for (int i = from; i < to; ++i) {
-        const int v = a[i];
-        a[i] = run;
-        run += v;
-    }
-    __syncthreads();
-    return total;
+    const int earlier = __shfl_sync(0xffffffffu, before, warp > 0 ? warp - 1 : 0);
+    return scan - sum + (warp > 0 ? earlier : 0);
+}
+
+// Where unit `i` of n pieces of `units` begins.
+__host__ __device__ __forceinline__ long long piece(long long units, int n, int i)
+{
+    return units * i / n;
 }
 
 // Shared memory of a sorting CTA.
@@ -72,11 +68,11 @@ struct GroupSmem {
     int *tot;               // [bins] of this CTA, read by the cluster
     int *first;             // [bins] places before this CTA's
     int *part;              // [32]
-    uint32_t *pairs;        // [kWarps, per_warp]: bin << 16 | rank within the warp
+    uint32_t *pairs;        // [numbers of the CTA]: bin << 16 | rank within the warp
 };
-__host__ __device__ constexpr size_t group_smem_bytes(int bins, int per_warp)
+__host__ __device__ constexpr size_t group_smem_bytes(int bins, int numbers)
 {
-    return sizeof(int) * (static_cast<size_t>(kWarps + 2) * bins + 32 + static_cast<size_t>(kWarps) * per_warp);
+    return sizeof(int) * ((static_cast<size_t>(kWarps + 2) * bins + 3) / 4 * 4 + 32 + numbers);
 }
 __device__ __forceinline__ GroupSmem carve(int *base, int bins)
 {
@@ -84,7 +80,7 @@ __device__ __forceinline__ GroupSmem carve(int *base, int bins)
     s.hist = base;
     s.tot = s.hist + kWarps * bins;
     s.first = s.tot + bins;
-    s.part = s.first + bins;
+    s.part = base + ((kWarps + 2) * bins + 3) / 4 * 4;          // 16-byte boundary
     s.pairs = reinterpret_cast<uint32_t *>(s.part + 32);
     return s;
 }
@@ -96,39 +92,46 @@ __device__ __forceinline__ void clear_hist(const GroupSmem &s, int bins)
     __syncthreads();
 }
 
-// After every warp has counted its numbers [first_number, first_number + count):
-// places of the CTA's numbers.  Called by all threads of all CTAs of the cluster.
-__device__ __forceinline__ void place_pairs(const GroupSmem &s, const GroupOut &g, long long first_number,
-                                            int count, int per_warp)
+// After every warp has counted its numbers, [lo, hi) of those that begin with
+// first_number in the CTA: their places.  Called by all threads of all CTAs of the
+// cluster.  A thread takes up to three neighbouring bins.
+__device__ __forceinline__ void place_pairs(const GroupSmem &s, const GroupOut &g, long long first_number, int lo, int hi)
 {
+    constexpr int kMost = 3;
     const int bins = g.groups + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t ctas, cluster;
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
     asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(cluster));
     const uint32_t me = cluster_ctarank();
+    const int q = bins <= kThreads ? 1 : bins <= 2 * kThreads ? 2 : kMost, b0 = threadIdx.x * q;
     __syncthreads();
-    for (int b = threadIdx.x; b < bins; b += kThreads) {
+    int total[kMost], before[kMost];
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+        total[i] = before[i] = 0;
+        const int b = b0 + i;
+        if (i >= q || b >= bins)
+            continue;
+        int v[kWarps];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+            v[w] = s.hist[w * bins + b];
         int run = 0;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const int v = s.hist[w * bins + b];
             s.hist[w * bins + b] = run;
-            run += v;
+            run += v[w];
         }
+        total[i] = run;
         s.tot[b] = run;
     }
-    if (ctas > 1)
+    if (ctas > 1) {
         cluster_sync();
-    else
-        __syncthreads();
-    // first[b]: what the cluster's earlier CTAs hold; and the cluster's total
-    const int per_thread = (bins + kThreads - 1) / kThreads;       // at most 3
-    int before[3], total[3];
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        const int b = threadIdx.x + i * kThreads;
-        before[i] = total[i] = 0;
-        if (i < per_thread && b < bins) {
+        for (int i = 0; i < kMost; ++i) {
+            const int b = b0 + i;
+            if (i >= q || b >= bins)
+                continue;
             int v[kMaxCluster];
 #pragma unroll
             for (uint32_t r = 0; r < kMaxCluster; ++r) {
@@ -139,36 +142,34 @@ __device__ __forceinline__ void place_pairs(const GroupSmem &s, const GroupOut &
                                  : "r"(cluster_map(smem_addr(s.tot + b), r))
                                  : "memory");
             }
+            total[i] = 0;
 #pragma unroll
             for (uint32_t r = 0; r < kMaxCluster; ++r) {
                 before[i] += r < me ? v[r] : 0;
                 total[i] += v[r];
             }
-            if (g.hist) {
-                if (me == 0)
-                    g.hist[static_cast<long long>(cluster) * bins + b] = total[i];
-                s.first[b] = before[i];
-            } else {
-                s.first[b] = total[i];
-            }
         }
+    }
+    if (g.hist) {
+#pragma unroll
+        for (int i = 0; i < kMost; ++i)
+            if (i < q && b0 + i < bins) {
+                if (me == 0)
+                    g.hist[static_cast<long long>(cluster) * bins + b0 + i] = total[i];
+                s.first[b0 + i] = before[i];
+            }
+    } else {
+        int run = thread_scan<kThreads>(total[0] + total[1] + total[2], s.part);
+#pragma unroll
+        for (int i = 0; i < kMost; ++i)
+            if (i < q && b0 + i < bins) {
+                if (me == 0)
+                    g.offsets[b0 + i] = run;
+                s.first[b0 + i] = run + before[i];
+                run += total[i];
+            }
     }
     __syncthreads();
-    if (!g.hist) {
-        block_scan(s.first, bins, s.part);
-        if (me == 0)
-            for (int b = threadIdx.x; b < bins; b += kThreads)
-                g.offsets[b] = s.first[b];
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            const int b = threadIdx.x + i * kThreads;
-            if (i < per_thread && b < bins)
-                s.first[b] += before[i];
-        }
-        __syncthreads();
-    }
-    const int lo = warp * per_warp, hi = min(lo + per_warp, count);
     for (int i = lo + lane; i < hi; i += 32) {
         const uint32_t v = s.pairs[i];
         const int b = v >> 16;

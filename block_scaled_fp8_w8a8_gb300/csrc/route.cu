@@ -28,6 +28,7 @@
 #include "../../include/w8a8_block_fp8.h"
 #include "group.cuh"
 #include "kernels.cuh"
+#include "pair32.cuh"
 #include "ptx.cuh"
 
 namespace w8a8 {
@@ -48,21 +49,24 @@ struct RouteParams {
     int per;                    // experts of a lane
     int groups, top_groups, group_top;
     int group_lanes;            // lanes of a run where runs are whole lanes, a power of two; else 0
+    int group_shift;            // its logarithm
     int sigmoid, renormalize;
     int vec;                    // a lane's logits can be loaded by 16 bytes
     float scale;
-    int per_warp;               // tokens of a warp
+    int most;                   // tokens of a CTA at most
     GroupOut out;
 };
 
 constexpr uint32_t kAll = 0xffffffffu;
 
-// Order-preserving maps; key 0 belongs to no number.
-__device__ __forceinline__ uint32_t key_of(float f)
+// Order-preserving maps; key 0 belongs to no number.  The addition makes -0 +0 and any NaN the
+// canonical one, whose sign is plus: it ranks above infinity.
+__device__ __forceinline__ uint32_t key_of_sum(float f)     // of a number that is a sum already
 {
-    const uint32_t u = __float_as_uint(f + 0.f);        // -0 -> +0
-    return f != f ? 0xffffffffu : u ^ (static_cast<uint32_t>(static_cast<int>(u) >> 31) | 0x80000000u);
+    const uint32_t u = __float_as_uint(f);
+    return u ^ (static_cast<uint32_t>(static_cast<int>(u) >> 31) | 0x80000000u);
 }
+__device__ __forceinline__ uint32_t key_of(float f) { return key_of_sum(f + 0.f); }
 __device__ __forceinline__ float value_of(uint32_t k)
 {
     return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
@@ -75,6 +79,15 @@ __device__ __forceinline__ unsigned long long key_of(double f)
 __device__ __forceinline__ double value_of(unsigned long long k)
 {
     return __longlong_as_double(k >> 63 ? k ^ (1ull << 63) : ~k);
+}
+// (A pair's lower part decides among equal upper ones.)
+__device__ __forceinline__ unsigned long long key_of(Pair32 v)
+{
+    return static_cast<unsigned long long>(key_of(v.h)) << 32 | key_of(v.h == v.h ? v.l : 0.f);
+}
+__device__ __forceinline__ Pair32 pair_of(unsigned long long k)
+{
+    return {value_of(static_cast<uint32_t>(k >> 32)), value_of(static_cast<uint32_t>(k))};
 }
 __device__ __forceinline__ uint32_t warp_max(uint32_t k) { return __reduce_max_sync(kAll, k); }
 __device__ __forceinline__ unsigned long long warp_max(unsigned long long k)
@@ -96,6 +109,66 @@ __device__ __forceinline__ double warp_sum(double v)
     for (int d = 16; d; d /= 2)
         v += __shfl_xor_sync(kAll, v, d);
     return v;
+}
+
+__device__ __forceinline__ float exp2_fast(float x)         // within 2 units of 2^-23
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_fast(float x)          // within 1 unit
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+constexpr float kLog2e = 1.44269504f;
+
+// 0! .. 12!, inverted
+__constant__ double kInverseFactorial[13] = {1.,           1.,            1. / 2.,       1. / 6.,       1. / 24.,
+                                             1. / 120.,    1. / 720.,     1. / 5040.,    1. / 40320.,   1. / 362880.,
+                                             1. / 3628800., 1. / 39916800., 1. / 479001600.};
+
+// exp of four numbers in fp64, to a few units of 2^-53, zero below -708: reduced by
+// multiples of ln 2 in two parts (W. J. Cody and W. Waite, "Software Manual for the
+// Elementary Functions", 1980), then the power series up to f^13 / 13!, whose next term is
+// below 2^-57.  Short and four at a time, because what decides a near tie once in
+// thousands of tokens is never in the instruction cache, and fp64's latency is long: with
+// the library's function unrolled over a lane's experts such a token took its warp 20 us.
+constexpr int kQuad = 4;
+__device__ __forceinline__ void exp64(double (&x)[kQuad])
+{
+    const double kMagic = 6755399441055744.;            // 1.5 2^52: the sum's low bits are the rounded quotient
+    double f[kQuad], s[kQuad];
+    int n[kQuad];
+#pragma unroll
+    for (int i = 0; i < kQuad; ++i) {
+        const double in = fmin(fmax(x[i], -708.), 709.);                // (a NaN is put back below)
+        const double t = fma(in, 1.4426950408889634, kMagic), q = t - kMagic;
+        f[i] = fma(q, -1.90821492927058770002e-10, fma(q, -6.93147180369123816490e-01, in));
+        n[i] = __double2loint(t);
+        s[i] = 1. / 6227020800.;
+    }
+#pragma unroll 1
+    for (int k = 12; k >= 0; --k) {
+        const double c = kInverseFactorial[k];
+#pragma unroll
+        for (int i = 0; i < kQuad; ++i)
+            s[i] = fma(s[i], f[i], c);
+    }
+#pragma unroll
+    for (int i = 0; i < kQuad; ++i) {
+        const double v = __longlong_as_double(__double_as_longlong(s[i]) + (static_cast<long long>(n[i]) << 52));
+        x[i] = x[i] != x[i] ? x[i] : x[i] < -708. ? 0. : x[i] > 709. ? INFINITY : v;
+    }
+}
+// 1 / d for d from 1 to 2^20: two steps of Newton's method from fp32
+__device__ __forceinline__ double inverse64(double d)
+{
+    double r = static_cast<double>(rcp_fast(static_cast<float>(d)));
+    r = fma(r, fma(-d, r, 1.), r);
+    return fma(r, fma(-d, r, 1.), r);
 }
 
 template <int KIND> __device__ __forceinline__ float load_logit(const void *row, int e)
@@ -144,20 +217,6 @@ __device__ __forceinline__ void load_lane(const RouteParams &p, const void *row,
         l[i] = i < p.per && e0 + i < p.E ? load_logit<KIND>(row, e0 + i) : -INFINITY;
 }
 
-__device__ __forceinline__ float exp2_fast(float x)         // within 2 units of 2^-23
-{
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ float rcp_fast(float x)          // within 1 unit
-{
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-constexpr float kLog2e = 1.44269504f;
-
 // Descending order by odd-even merging (K. E. Batcher, "Sorting networks and their
 // applications", AFIPS Spring Joint Computer Conference, 1968).
 template <int N> __device__ __forceinline__ void sort_keys(uint32_t (&k)[N])
@@ -185,16 +244,21 @@ template <class K> __device__ __forceinline__ void two_best(K &a, K &b, K x)
     b = lo < b ? b : lo;
 }
 
-// Whether this lane's run is kept, from its value (the same in all of its lanes), and
-// the values at the border.
+// Whether this lane's run g is kept, from its value (the same in all of its group_lanes
+// lanes, a power of two), and the values at the border.  Each lane compares with its share
+// of the runs.
 template <class K>
 __device__ __forceinline__ bool rank_groups(int groups, int group_lanes, int top, int g, K value, K *kept, K *dropped)
 {
+    const int share = (groups + group_lanes - 1) / group_lanes, from = (threadIdx.x & (group_lanes - 1)) * share;
     int above = 0;
-    for (int j = 0; j < groups; ++j) {
-        const K v = __shfl_sync(kAll, value, j * group_lanes);
-        above += v > value || (v == value && j < g);
+    for (int i = 0; i < share; ++i) {
+        const int j = from + i;
+        const K v = __shfl_sync(kAll, value, min(j, groups - 1) * group_lanes);
+        above += j < groups && (v > value || (v == value && j < g));
     }
+    for (int d = 1; d < group_lanes; d *= 2)
+        above += __shfl_xor_sync(kAll, above, d);
     const bool keep = g < groups && above < top;
     *kept = ~warp_max(keep ? ~value : K(0));
     *dropped = warp_max(keep || g >= groups ? K(0) : value);
@@ -204,6 +268,71 @@ __device__ __forceinline__ bool rank_groups(int groups, int group_lanes, int top
 template <class K> __device__ __forceinline__ K group_value(int group_top, K a, K b)
 {
     return group_top == 2 ? key_of(value_of(a) + value_of(b)) : a;
+}
+
+// A softmax's sum in fp64 (1 for a sigmoid).
+template <int KIND> __device__ __forceinline__ double softmax_sum(const RouteParams &p, const void *row, float m)
+{
+    if (p.sigmoid)
+        return 1.;
+    double z = 0;
+#pragma unroll 1
+    for (int e = threadIdx.x & 31; e < p.E; e += 32 * kQuad) {
+        double x[kQuad];
+#pragma unroll
+        for (int i = 0; i < kQuad; ++i)
+            x[i] = e + 32 * i < p.E ? static_cast<double>(load_logit<KIND>(row, e + 32 * i)) - m : -1000.;
+        exp64(x);
+#pragma unroll
+        for (int i = 0; i < kQuad; ++i)
+            z += x[i];
+    }
+    return warp_sum(z);
+}
+// Scores of four logits, in their place.
+__device__ __forceinline__ void score64(const RouteParams &p, double (&l)[kQuad], float m, double z)
+{
+    double e[kQuad];
+#pragma unroll
+    for (int i = 0; i < kQuad; ++i)
+        e[i] = p.sigmoid ? -fabs(l[i]) : l[i] - m;
+    exp64(e);
+    const double inv = p.sigmoid || z == 0 ? 0. : inverse64(z);
+#pragma unroll
+    for (int i = 0; i < kQuad; ++i) {
+        if (p.sigmoid) {
+            const double q = inverse64(1. + e[i]);
+            l[i] = l[i] != l[i] ? l[i] : l[i] >= 0 ? q : e[i] * q;
+        } else {
+            l[i] = z == 0 ? 0. : e[i] * inv;
+        }
+    }
+}
+
+// The same as pairs of fp32.  Their scores are off by less than 2^-42, and sums with
+// a bias by 2^-46 of their sizes: below kPairError (1 + the size).
+constexpr float kPairError = 0x1p-40f;
+template <int KIND> __device__ __forceinline__ Pair32 softmax_sum_pair(const RouteParams &p, const void *row, float m)
+{
+    Pair32 z = {0.f, 0.f};
+    if (p.sigmoid)
+        return z;
+#pragma unroll 2
+    for (int e = threadIdx.x & 31; e < p.E; e += 32)
+        z = z + exp_pair(two_sum(load_logit<KIND>(row, e), -m));
+#pragma unroll
+    for (int d = 16; d; d /= 2) {
+        const float h = __shfl_xor_sync(kAll, z.h, d), l = __shfl_xor_sync(kAll, z.l, d);
+        // (the same in every lane: the lower lane's part first)
+        z = threadIdx.x & d ? Pair32{h, l} + z : z + Pair32{h, l};
+    }
+    return z;
+}
+__device__ __forceinline__ Pair32 score_pair(const RouteParams &p, float l, float m, Pair32 z)
+{
+    if (p.sigmoid)
+        return sigmoid(l);
+    return z.h == 0.f ? z : exp_pair(two_sum(l, -m)) * inverse(z);
 }
 
 // The choice in fp64: lane j < k gets the j-th expert.  Rare, so one version for every
@@ -218,21 +347,16 @@ template <int KIND> __device__ __noinline__ int choose_exact(const RouteParams &
         m = fmaxf(m, load_logit<KIND>(row, e0 + i));
     m = value_of(warp_max(key_of(m)));
     m = m == -INFINITY ? 0.f : m;
-    double z = 0;
-    if (!p.sigmoid) {
-        for (int i = 0; i < n; ++i)
-            z += exp(static_cast<double>(load_logit<KIND>(row, e0 + i)) - m);
-        z = warp_sum(z);
-    }
-    for (int i = 0; i < n; ++i) {
-        const float l = load_logit<KIND>(row, e0 + i);
-        double s;
-        if (p.sigmoid)
-            s = 1 / (1 + exp(-static_cast<double>(l)));
-        else
-            s = z == 0 ? 0. : exp(static_cast<double>(l) - m) / z;
-        ck[i] = key_of(p.bias ? s + p.bias[e0 + i] : s);
-        key[i] = p.bias ? ck[i] : key_of(static_cast<double>(l));
+    const double z = softmax_sum<KIND>(p, row, m);
+    for (int i = 0; i < n; i += kQuad) {
+        double x[kQuad], l[kQuad];
+        for (int j = 0; j < kQuad; ++j)
+            x[j] = l[j] = load_logit<KIND>(row, e0 + min(i + j, n - 1));
+        score64(p, x, m, z);
+        for (int j = 0; j < kQuad && i + j < n; ++j) {
+            ck[i + j] = key_of(p.bias ? x[j] + p.bias[e0 + i + j] : x[j]);
+            key[i + j] = p.bias ? ck[i + j] : key_of(l[j]);
+        }
     }
     if (p.groups > 1) {
         const int size = p.E / p.groups;
@@ -275,59 +399,213 @@ template <int KIND> __device__ __noinline__ int choose_exact(const RouteParams &
     return id;
 }
 
-// Ranks `count` (at most 32) experts, lane j's being id, by their scores in fp64: returns
-// the expert of rank `lane`.
-template <int KIND> __device__ __noinline__ int refine(const RouteParams &p, const void *row, int id, int count, float m)
+// The runs that are kept, as bits, from scores in fp64.
+template <int KIND> __device__ __noinline__ uint32_t exact_groups(const RouteParams &p, const void *row, float m)
+{
+    using K = unsigned long long;
+    const int lane = threadIdx.x & 31, e0 = lane * p.per, n = max(0, min(p.per, p.E - e0)), size = p.E / p.groups;
+    const double z = softmax_sum<KIND>(p, row, m);
+    K ck[32];
+#pragma unroll 1
+    for (int i = 0; i < n; i += kQuad) {
+        double x[kQuad];
+#pragma unroll
+        for (int j = 0; j < kQuad; ++j)
+            x[j] = load_logit<KIND>(row, e0 + min(i + j, n - 1));
+        if (p.bias || p.group_top == 2)
+            score64(p, x, m, z);
+#pragma unroll
+        for (int j = 0; j < kQuad; ++j)
+            if (i + j < n)
+                ck[i + j] = key_of(p.bias ? x[j] + p.bias[e0 + i + j] : x[j]);
+    }
+    K value = 0;
+    if (p.group_lanes) {
+        K a = 0, b = 0;
+        for (int i = 0; i < n; ++i)
+            two_best(a, b, ck[i]);
+        for (int d = 1; d < p.group_lanes; d *= 2) {
+            const K oa = __shfl_xor_sync(kAll, a, d), ob = __shfl_xor_sync(kAll, b, d);
+            two_best(a, b, oa);
+            b = ob > b ? ob : b;
+        }
+        const K mine = group_value(p.group_top, a, b);
+        value = __shfl_sync(kAll, mine, min(lane, p.groups - 1) * p.group_lanes);
+    } else {
+        for (int g = 0; g < p.groups; ++g) {
+            K a = 0, b = 0;
+            for (int i = 0; i < n; ++i)
+                if ((e0 + i) / size == g)
+                    two_best(a, b, ck[i]);
+            const K top = warp_max(a);
+            const uint32_t who = __ballot_sync(kAll, a == top);
+            const K second = warp_max(lane == __ffs(who) - 1 ? b : a);
+            const K v = group_value(p.group_top, top, second);
+            value = lane == g ? v : value;
+        }
+    }
+    K kept, dropped;
+    const bool keep = rank_groups<K>(p.groups, 1, p.top_groups, lane, value, &kept, &dropped);
+    return __ballot_sync(kAll, keep);
+}
+
+// The same from pairs of fp32; *sure: whether they tell.
+template <int KIND>
+__device__ __noinline__ uint32_t near_groups(const RouteParams &p, const void *row, float m, bool *sure)
+{
+    using K = unsigned long long;
+    const int lane = threadIdx.x & 31, e0 = lane * p.per, n = max(0, min(p.per, p.E - e0)), size = p.E / p.groups;
+    const Pair32 z = softmax_sum_pair<KIND>(p, row, m);
+    K value = 0, a = 0, b = 0;
+    auto key = [&](int e) {
+        const float l = load_logit<KIND>(row, e);
+        if (!p.bias && p.group_top == 1)
+            return key_of(Pair32{l, 0.f});
+        const Pair32 s = score_pair(p, l, m, z);
+        return key_of(p.bias ? s + Pair32{p.bias[e], 0.f} : s);
+    };
+    auto value_of_run = [&](K first, K second) {
+        return p.group_top == 2 ? key_of(pair_of(first) + pair_of(second)) : first;
+    };
+    float most = 0.f;
+    if (p.group_lanes) {
+#pragma unroll 2
+        for (int i = 0; i < n; ++i)
+            two_best(a, b, key(e0 + i));
+        for (int d = 1; d < p.group_lanes; d *= 2) {
+            const K oa = __shfl_xor_sync(kAll, a, d), ob = __shfl_xor_sync(kAll, b, d);
+            two_best(a, b, oa);
+            b = ob > b ? ob : b;
+        }
+        most = n ? fabsf(pair_of(a).h) + (p.group_top == 2 ? fabsf(pair_of(b).h) : 0.f) : 0.f;
+        const K mine = value_of_run(a, b);
+        value = __shfl_sync(kAll, mine, min(lane, p.groups - 1) * p.group_lanes);
+    } else if (lane < p.groups) {
+        for (int i = 0; i < size; ++i)
+            two_best(a, b, key(lane * size + i));
+        most = fabsf(pair_of(a).h) + (p.group_top == 2 ? fabsf(pair_of(b).h) : 0.f);
+        value = value_of_run(a, b);
+    }
+    __syncwarp();
+    K kept, dropped;
+    const bool keep = rank_groups<K>(p.groups, 1, p.top_groups, lane, value, &kept, &dropped);
+    most = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(most)));
+    const Pair32 hi = pair_of(kept), lo = pair_of(dropped);
+    *sure = (hi.h - lo.h) + (hi.l - lo.l) > 4.f * kPairError * (1.f + most);
+    return __ballot_sync(kAll, keep);
+}
+
+// Ranks `count` (at most 32) experts, lane j's being id, by their scores: returns the expert
+// of rank `lane`.  In pairs of fp32 first; where neighbours are nearer than those tell, in fp64.
+template <class K> __device__ __forceinline__ int by_rank(K key, int id, int count, K *sorted)
 {
     const int lane = threadIdx.x & 31;
-    const bool in = lane < count;
-    double s = 0;
-    const double l = in ? static_cast<double>(load_logit<KIND>(row, id)) : 0.;
-    if (p.sigmoid) {
-        s = 1 / (1 + exp(-l));
-    } else {
-        double z = 0;
-#pragma unroll 4
-        for (int e = lane; e < p.E; e += 32)
-            z += exp(static_cast<double>(load_logit<KIND>(row, e)) - m);
-        z = warp_sum(z);
-        s = z == 0 ? 0. : exp(l - m) / z;
-    }
-    // without a bias the logits rank
-    const unsigned long long key = in ? key_of(p.bias ? s + p.bias[id] : l) : 0ull;
     int above = 0;
+#pragma unroll 1
     for (int j = 0; j < count; ++j) {
-        const unsigned long long other = __shfl_sync(kAll, key, j);
+        const K other = __shfl_sync(kAll, key, j);
         const int other_id = __shfl_sync(kAll, id, j);
         above += other > key || (other == key && other_id < id);
     }
     int mine = id;
+    K its = key;
+#pragma unroll 1
     for (int j = 0; j < count; ++j) {
         const int rank = __shfl_sync(kAll, above, j), e = __shfl_sync(kAll, id, j);
+        const K k = __shfl_sync(kAll, key, j);
         mine = rank == lane ? e : mine;
+        its = rank == lane ? k : its;
     }
+    *sorted = its;
     return mine;
 }
-
-// One token: lane j < k gets the j-th expert and its weight.
-template <int KIND, int PER>
-__device__ __forceinline__ void route_token(const RouteParams &p, const void *row, const float (&l)[PER],
-                                            const float *bias, int *run_keys, int &id, float &weight)
+template <int KIND> __device__ __noinline__ int refine(const RouteParams &p, const void *row, int id, int count, float m)
 {
+    using K = unsigned long long;
+    const int lane = threadIdx.x & 31;
+    const bool in = lane < count;
+    const float l = in ? load_logit<KIND>(row, id) : 0.f;
+    K sorted;
+    if (!p.bias)        // the logits rank
+        return by_rank<K>(in ? key_of(Pair32{l, 0.f}) : 0ull, id, count, &sorted);
+    const float b = in ? p.bias[id] : 0.f;
+    const Pair32 z = softmax_sum_pair<KIND>(p, row, m);
+    const int ranked = by_rank<K>(in ? key_of(score_pair(p, l, m, z) + Pair32{b, 0.f}) : 0ull, id, count, &sorted);
+    const K next = __shfl_down_sync(kAll, sorted, 1);
+    const int next_id = __shfl_down_sync(kAll, ranked, 1);
+    bool near = false;
+    if (lane + 1 < count) {
+        const Pair32 x = pair_of(sorted), y = pair_of(next);
+        near = !((x.h - y.h) + (x.l - y.l) > 2.f * kPairError * (1.f + fabsf(x.h)));
+        // equal logits under equal biases are equal scores, in order of their index
+        near = near && !(load_logit<KIND>(row, ranked) == load_logit<KIND>(row, next_id) && p.bias[ranked] == p.bias[next_id]);
+    }
+    if (!__any_sync(kAll, near))
+        return ranked;
+    double x[kQuad] = {l, l, l, l};         // (one of them is wanted)
+    score64(p, x, m, softmax_sum<KIND>(p, row, m));
+    return by_rank<K>(in ? key_of(x[0] + b) : 0ull, id, count, &sorted);
+}
+
+// Shared memory of k_route beside the sort's.
+struct RouteSmem {
+    uint2 *won;                 // of a warp [batch, k + 1]: the choices' keys and experts, then what is behind
+    uint2 *spare;               // of a warp [32]
+    float4 *row;                // of a warp [batch]: a softmax's m and z, a score's bound, the key behind all
+    float *bias;                // [32 per]
+    int *run_keys;              // of a warp [E], where runs are not whole lanes
+    static constexpr int kWon = 64;                     // 32 / k (k + 1) at most
+    static __host__ __device__ size_t bytes(const RouteParams &p)
+    {
+        return kWarps * (sizeof(float4) * 32 + sizeof(uint2) * (kWon + 32)) + sizeof(float) * 32 * p.per +
+               (p.groups > 1 && !p.group_lanes ? sizeof(int) * kWarps * p.E : 0);
+    }
+    __device__ __forceinline__ RouteSmem(const RouteParams &p, const GroupSmem &s, int warp)
+    {
+        float4 *const rows = reinterpret_cast<float4 *>(s.pairs + (p.most * p.k + 3) / 4 * 4);
+        uint2 *const keys = reinterpret_cast<uint2 *>(rows + 32 * kWarps);
+        row = rows + 32 * warp;
+        won = keys + (kWon + 32) * warp;
+        spare = won + kWon;
+        bias = reinterpret_cast<float *>(keys + (kWon + 32) * kWarps);
+        run_keys = reinterpret_cast<int *>(bias + 32 * p.per) + warp * p.E;
+    }
+};
+
+// A score as make_keys makes it.
+__device__ __forceinline__ float score32(const RouteParams &p, float l, float m, float z)
+{
+    return p.sigmoid ? rcp_fast(1.f + exp2_fast(-kLog2e * l))
+                     : exp2_fast(kLog2e * (l - m)) * (z == 0.f ? 0.f : rcp_fast(z));
+}
+
+// A token's scores as a lane's keys: sorted, of the open runs, and what the weights need.
+template <int PER> struct Keys {
+    static constexpr uint32_t kSlots = PER - 1;
+    uint32_t key[PER];
+    float m, z;                 // softmax: the largest logit (0 for -infinity) and the sum
+    float bound;                // of a score's error
+};
+
+template <int KIND, int PER>
+__device__ __forceinline__ void make_keys(const RouteParams &p, const void *row, const float (&l)[PER], const float *bias,
+                                          int *run_keys, Keys<PER> &out)
+{
+    constexpr uint32_t kSlots = Keys<PER>::kSlots;
     const int lane = threadIdx.x & 31, e0 = lane * p.per;
-    const bool biased = p.bias != nullptr;
-    const bool scored = biased || (p.groups > 1 && p.group_top == 2) || (!p.sigmoid && !p.renormalize);
+    const bool biased = p.bias != nullptr, sums = p.groups > 1 && p.group_top == 2;
+    const bool scored = biased || sums || (!p.sigmoid && !p.renormalize);
     float c[PER];
     float m = 0.f, z = 1.f;
     // An upper bound of the error of an fp32 score, in units of 2^-23.  An exponential of x
     // is off by 2 units and by its argument's rounding, 0.75 |x|, relatively.
     //   sigmoid: s (1 - s) (2 + 0.75 |l|) <= 0.6 units, then one rounded sum and the
-    //     quotient: 2.1 units, below 2^-21.
+    //     quotient: 2.1 units, below 17/16 2^-22.
     //   softmax: with u = -x the terms' errors are at most 2 units of the largest term and,
     //     in the sum z, 2 + 0.75 u averaged with the terms as weights, where u averages at
     //     most ln E + 1 < 8; the sum's roundings (PER + 5) / 2 <= 18.5, the quotient 1.5: with
     //     s <= 1 / z at most 30 units of 1 / z, below 2^-18 / z.
-    float bound = 0x1p-21f;
+    float bound = 0x1.1p-22f;
     if (scored) {
         if (p.sigmoid) {
 #pragma unroll
@@ -352,140 +630,159 @@ __device__ __forceinline__ void route_token(const RouteParams &p, const void *ro
             bound = 0x1p-18f * inv;
         }
     }
+    uint32_t (&key)[PER] = out.key;
+    const int mine = min(p.per, p.E - e0);      // experts of this lane
     if (biased) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
-            c[i] += PER <= 8 ? bias[i] : i < p.per && e0 + i < p.E ? p.bias[e0 + i] : 0.f;
-    }
-    uint32_t key[PER];
+        for (int i = 0; i < PER; ++i) {
+            c[i] += i < p.per ? bias[i] : 0.f;
+            key[i] = i < mine ? key_of_sum(c[i]) : 0u;
+        }
+    } else {
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-        key[i] = i < p.per && e0 + i < p.E ? key_of(biased ? c[i] : l[i]) : 0u;
-    bool exact = false;             // decide the whole token again in fp64
+        for (int i = 0; i < PER; ++i)
+            key[i] = i < mine ? key_of(l[i]) : 0u;
+    }
     if (p.groups > 1) {
         const int size = p.E / p.groups;
-        uint32_t a = 0, b = 0;
-        uint32_t kept, dropped;
-        const bool sums = p.group_top == 2;
+        uint32_t a = 0, b = 0, kept, dropped;
+        const bool by_score = sums && !biased;          // (keys are the logits')
+        bool keep;
         if (p.group_lanes) {
+            if (by_score) {
 #pragma unroll
-            for (int i = 0; i < PER; ++i)
-                two_best(a, b, sums && !biased ? (key[i] ? key_of(c[i]) : 0u) : key[i]);
+                for (int i = 0; i < PER; ++i)
+                    two_best(a, b, i < mine ? key_of_sum(c[i]) : 0u);
+            } else {
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                    two_best(a, b, key[i]);
+            }
             for (int d = 1; d < p.group_lanes; d *= 2) {
                 const uint32_t oa = __shfl_xor_sync(kAll, a, d), ob = __shfl_xor_sync(kAll, b, d);
                 two_best(a, b, oa);
                 b = ob > b ? ob : b;
             }
-            const bool keep = rank_groups<uint32_t>(p.groups, p.group_lanes, p.top_groups, lane / p.group_lanes,
-                                                    group_value(p.group_top, a, b), &kept, &dropped);
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                key[i] = keep ? key[i] : 0u;
+            keep = rank_groups<uint32_t>(p.groups, p.group_lanes, p.top_groups, lane >> p.group_shift,
+                                         group_value(p.group_top, a, b), &kept, &dropped);
         } else {
             // runs that do not begin with a lane: through shared memory, lane g takes run g
 #pragma unroll
             for (int i = 0; i < PER; ++i)
                 if (key[i])
-                    run_keys[e0 + i] = static_cast<int>(sums && !biased ? key_of(c[i]) : key[i]);
+                    run_keys[e0 + i] = static_cast<int>(by_score ? key_of_sum(c[i]) : key[i]);
             __syncwarp();
             if (lane < p.groups)
                 for (int i = 0; i < size; ++i)
                     two_best(a, b, static_cast<uint32_t>(run_keys[lane * size + i]));
             __syncwarp();
-            const uint32_t keep = __ballot_sync(kAll, rank_groups<uint32_t>(p.groups, 1, p.top_groups, lane,
-                                                                           group_value(p.group_top, a, b), &kept, &dropped));
+            keep = rank_groups<uint32_t>(p.groups, 1, p.top_groups, lane, group_value(p.group_top, a, b), &kept, &dropped);
+        }
+        bool near_group = false;        // which runs are open is nearer than the scores' errors
+        if ((biased || sums) && p.top_groups < p.groups) {
+            // Each value is off by two scores' errors, their sums' with the biases and the sum of
+            // both: 2 bound + 2^-23 of the scores' sizes, taken as the largest run's.
+            const float sizes = p.group_lanes || lane < p.groups ? fabsf(value_of(a)) + (sums ? fabsf(value_of(b)) : 0.f) : 0.f;
+            const float most = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(sizes)));
+            near_group = !(value_of(kept) - value_of(dropped) > 4.f * bound + 0x1p-22f * most);
+        }
+        uint32_t open = 0;
+        if (near_group) {
+            bool sure;
+            open = near_groups<KIND>(p, row, m, &sure);
+            if (!sure)
+                open = exact_groups<KIND>(p, row, m);
+        }
+        if (p.group_lanes) {
+            if (near_group)
+                keep = open >> (lane >> p.group_shift) & 1;
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                key[i] = keep >> ((e0 + i) / size & 31) & 1 ? key[i] : 0u;
-        }
-        if ((biased || sums) && p.top_groups < p.groups) {
-            const float hi = value_of(kept), lo = value_of(dropped);
-            exact = !(hi - lo > 4.f * bound + 0x1p-21f * (fabsf(hi) + fabsf(lo)));
+                key[i] = keep ? key[i] : 0u;
+        } else {
+            const uint32_t lanes = __ballot_sync(kAll, keep);
+            if (!near_group)
+                open = lanes;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                key[i] = open >> ((e0 + i) / size & 31) & 1 ? key[i] : 0u;
         }
     }
     // The slot takes the place of the key's lowest bits; 16-bit logits have zeros there.
-    constexpr uint32_t kSlots = PER - 1;
 #pragma unroll
     for (int i = 0; i < PER; ++i)
         key[i] = key[i] ? (key[i] & ~kSlots) | (kSlots - i) : 0u;
     sort_keys(key);
-    const bool whole = !biased && KIND != W8A8_IN_FP32;
-    const float near_by = biased ? 2.f * bound : 0.f, near_at = biased ? 0x1p-22f + PER * 0x1p-23f : 0.f;
-    uint32_t mine = 0, last = 0;        // lane j: the j-th key
-    id = 0;
-    auto round = [&](int j) {
-        // (the lane before the slot: the lower index first)
-        const uint32_t kept_bits = key[0] & ~kSlots;
-        const uint32_t top = warp_max(kept_bits);
-        const int src = __ffs(__ballot_sync(kAll, kept_bits == top)) - 1;
-        const uint32_t slot = kSlots - (__shfl_sync(kAll, key[0], src) & kSlots);
-        if (lane == src) {
+    out.m = m;
+    out.z = z;
+    out.bound = bound;
+}
+
+__device__ __forceinline__ uint32_t lanes_below()
+{
+    uint32_t m;
+    asm("mov.u32 %0, %%lanemask_lt;" : "=r"(m));
+    return m;
+}
+
+// The best key that is left goes to *won with its expert, and from its lane; returns it.
+template <int PER> __device__ __forceinline__ uint32_t take_best(uint32_t (&key)[PER], int e0, uint2 *won)
+{
+    constexpr uint32_t kSlots = PER - 1;
+    // (the lane before the slot: the lower index first)
+    const uint32_t bits = key[0] & ~kSlots, top = warp_max(bits);
+    const uint32_t best = __ballot_sync(kAll, bits == top);
+    if (bits == top && (best & lanes_below()) == 0) {
+        *won = make_uint2(top, e0 + kSlots - (key[0] & kSlots));
 #pragma unroll
-            for (int i = 0; i + 1 < PER; ++i)
-                key[i] = key[i + 1];
-            key[PER - 1] = 0;
-        }
-        if (lane == j)
-            mine = top, id = src * p.per + static_cast<int>(slot);
-        last = top;
-    };
-    for (int j = 0; j < p.k; ++j)
-        round(j);
-    if (!whole && !exact) {
-        // Whether key `a` is surely above key `b`, the next.  (Without a bias that is so where
-        // the kept bits differ.)
-        auto near = [&](uint32_t a, uint32_t b) {
-            const float hi = value_of(a), lo = value_of(b & ~kSlots);
-            return b > kSlots && !(hi - lo > near_by + near_at * (fabsf(hi) + fabsf(lo)));
-        };
-        const uint32_t behind = warp_max(key[0]);
-        const uint32_t below = __shfl_down_sync(kAll, mine, 1);         // (by every lane)
-        const uint32_t next = lane == p.k - 1 ? behind : below;
-        bool unsure = lane < p.k && near(mine, next);
-        if (__any_sync(kAll, unsure)) {
-            // Take on what is too near the last, as many as lanes hold.
-            int count = p.k;
-            while (count < 32 && near(last, warp_max(key[0])))
-                round(count++);
-            const int next_id = __shfl_down_sync(kAll, id, 1);
-            const float own_l = lane < count ? load_logit<KIND>(row, id) : 0.f;
-            const float own_b = biased && lane < count ? p.bias[id] : 0.f;
-            const float next_l = __shfl_down_sync(kAll, own_l, 1), next_b = __shfl_down_sync(kAll, own_b, 1);
-            // equal logits under equal biases are equal scores, in order of their index
-            const uint32_t after = __shfl_down_sync(kAll, mine, 1);
-            unsure = lane + 1 < count && near(mine, after) && !(own_l == next_l && own_b == next_b && id < next_id);
-            if (near(last, warp_max(key[0])))
-                exact = true;               // more than 32
-            else if (__any_sync(kAll, unsure))
-                id = refine<KIND>(p, row, id, count, m);
-        }
+        for (int i = 0; i + 1 < PER; ++i)
+            key[i] = key[i + 1];
+        key[PER - 1] = 0;
     }
-    if (exact)
-        id = choose_exact<KIND>(p, row);
-    // The weights from the chosen logits, in full fp32.
-    const bool chosen = lane < p.k;
-    const float x = chosen ? load_logit<KIND>(row, id) : -INFINITY;
-    float s;
-    if (p.renormalize) {
-        // relative to the largest of them, so that small scores keep their ratios
-        float r = value_of(warp_max(key_of(x != x ? -INFINITY : x)));
-        if (p.sigmoid) {
-            r = fminf(r, 0.f);
-            s = x > 0.f ? 1.f / (1.f + expf(-x)) : expf(x - r) / (1.f + expf(x));
-        } else {
-            s = expf(x - r);
-        }
-        if (r == -INFINITY && x == -INFINITY)
-            s = 0.f;            // (-infinity) - (-infinity)
-        s = chosen ? s : 0.f;
-        const float sum = warp_sum(s);
-        s = sum == 0.f ? 0.f : s / sum;
-        if (!p.sigmoid && z != z)
-            s = z;              // a NaN or an infinity in the row that was not chosen
-    } else {
-        s = p.sigmoid ? 1.f / (1.f + expf(-x)) : z == 0.f ? 0.f : expf(x - m) / z;
+    return top;
+}
+
+// Whether key a is not surely above key b: they differ by no more than `by` and `at` times
+// their sizes.  (Without a bias, by and at 0: sure where the kept bits differ.)
+template <int PER> struct Near {
+    float by, at;
+    __device__ __forceinline__ Near(bool biased, float bound)
+        : by(biased ? 2.f * bound : 0.f), at(biased ? 0x1p-22f + PER * 0x1p-23f : 0.f)
+    {
     }
-    weight = s * p.scale;
+    __device__ __forceinline__ bool operator()(uint32_t a, uint32_t b) const
+    {
+        constexpr uint32_t kSlots = PER - 1;
+        const float hi = value_of(a & ~kSlots), lo = value_of(b & ~kSlots);
+        return b > kSlots && !(hi - lo > by + at * (fabsf(hi) + fabsf(lo)));
+    }
+};
+
+// A token whose choice fp32 does not tell: once more, with what is near decided in fp64.
+// Lane j < k gets the j-th expert.  won holds 32 places.
+template <int KIND, int PER>
+__device__ __noinline__ int choose_near(const RouteParams &p, const void *row, const float *bias, int *run_keys, uint2 *won)
+{
+    const int lane = threadIdx.x & 31, e0 = lane * p.per;
+    const bool biased = p.bias != nullptr;
+    float l[PER];
+    load_lane<KIND, PER>(p, row, e0, l);
+    Keys<PER> t;
+    make_keys<KIND, PER>(p, row, l, bias, run_keys, t);
+    const Near<PER> near(biased, t.bound);
+    __syncwarp();
+    uint32_t last = 0;
+    int count = 0;
+    for (; count < p.k; ++count)
+        last = take_best(t.key, e0, won + count);
+    // what is too near the last, as many as lanes hold
+    for (; count < 32 && near(last, warp_max(t.key[0])); ++count)
+        last = take_best(t.key, e0, won + count);
+    const bool more = near(last, warp_max(t.key[0]));
+    __syncwarp();
+    const int id = lane < count ? static_cast<int>(won[lane].y) : 0;
+    __syncwarp();
+    return more ? choose_exact<KIND>(p, row) : refine<KIND>(p, row, id, count, t.m);
 }
 
 template <int KIND, int PER> __global__ void __launch_bounds__(kThreads, PER <= 8 ? 2 : 1) k_route(const RouteParams p)
@@ -493,52 +790,161 @@ template <int KIND, int PER> __global__ void __launch_bounds__(kThreads, PER <= 
     extern __shared__ int smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, bins = p.E + 1, e0 = lane * p.per;
     const GroupSmem s = carve(smem, bins);
-    const int pairs = p.per_warp * p.k;
-    int *const run_keys = reinterpret_cast<int *>(s.pairs + kWarps * pairs) + warp * p.E;
+    RouteSmem r(p, s, warp);
+    const float *const bias = r.bias + e0;
     clear_hist(s, bins);
     grid_dependency_wait();
     grid_launch_dependents();
-    float bias[PER <= 8 ? PER : 1];
-    if constexpr (PER <= 8) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            bias[i] = p.bias && i < p.per && e0 + i < p.E ? p.bias[e0 + i] : 0.f;
+    if (p.bias) {
+        for (int e = threadIdx.x; e < 32 * p.per; e += kThreads)
+            r.bias[e] = e < p.E ? p.bias[e] : 0.f;
+        __syncthreads();
     }
-    const long long cta_first = static_cast<long long>(blockIdx.x) * kWarps * p.per_warp;
-    const long long first = cta_first + static_cast<long long>(warp) * p.per_warp;
-    const int tokens = static_cast<int>(max(0ll, min(static_cast<long long>(p.per_warp), p.T - first)));
+    // the CTA's tokens, and this warp's of them
+    const int ctas = gridDim.x, cta = blockIdx.x;
+    const long long cta_first = piece(p.T, ctas, cta);
+    const int tokens = static_cast<int>(piece(p.T, ctas, cta + 1) - cta_first);
+    const int lo = tokens * warp / kWarps, hi = tokens * (warp + 1) / kWarps;
     constexpr int kBytes = KIND == W8A8_IN_FP32 ? 4 : 2;
-    for (int i = 0; i < tokens; ++i) {
-        const long long t = first + i;
-        const void *row = static_cast<const char *>(p.logits) + t * p.ld * kBytes;
-        int id = p.E, rank;
-        float weight = 0.f;
-        const bool valid = !p.valid || p.valid[t] != 0;
-        if (valid) {
+    const long long pitch = p.ld * kBytes;
+    const char *const rows = static_cast<const char *>(p.logits) + cta_first * pitch;
+    constexpr bool kAhead = PER <= 8;           // the next token's logits, while registers last
+    float next[kAhead ? PER : 1];
+    if constexpr (kAhead)
+        if (lo < hi)
+            load_lane<KIND, PER>(p, rows + lo * pitch, e0, next);
+    // As many tokens at a time as have 32 choices: the choices one after the other, then
+    // their check, the weights and the counts with a lane to each.
+    const bool checked = p.bias || KIND == W8A8_IN_FP32;
+    const int batch = 32 / p.k, in_batch = lane / p.k, choice = lane - in_batch * p.k;
+    for (int i0 = lo; i0 < hi; i0 += batch) {
+        const int here = min(batch, hi - i0);
+        uint32_t near_tokens = 0;
+        for (int i = 0; i < here; ++i) {
             float l[PER];
-            load_lane<KIND, PER>(p, row, e0, l);
-            route_token<KIND, PER>(p, row, l, bias, run_keys, id, weight);
-        }
-        int *const h = s.hist + warp * bins;
-        if (lane < p.k) {
-            p.ids[t * p.k + lane] = valid ? id : -1;
-            p.weights[t * p.k + lane] = weight;
-            rank = h[id] + (valid ? 0 : lane);          // a token's experts differ
-            s.pairs[warp * pairs + i * p.k + lane] = static_cast<uint32_t>(id) << 16 | rank;
+            const char *const row = rows + (i0 + i) * pitch;
+            if constexpr (kAhead) {
+#pragma unroll
+                for (int j = 0; j < PER; ++j)
+                    l[j] = next[j];
+                if (i0 + i + 1 < hi)
+                    load_lane<KIND, PER>(p, row + pitch, e0, next);
+            } else {
+                load_lane<KIND, PER>(p, row, e0, l);
+            }
+            if (p.valid && !p.valid[cta_first + i0 + i])
+                continue;
+            Keys<PER> t;
+            make_keys<KIND, PER>(p, row, l, bias, r.run_keys, t);
+            uint2 *const won = r.won + i * (p.k + 1);
+            // (one more where the choice is checked: the best that stays behind; and the key after it)
+            for (int j = 0; j < (checked ? p.k + 1 : p.k); ++j)
+                take_best(t.key, e0, won + j);
+            const uint32_t after = checked ? warp_max(t.key[0]) : 0u;
+            if (lane == 0)
+                r.row[i] = make_float4(t.m, t.z, t.bound, __uint_as_float(after));
         }
         __syncwarp();
-        if (valid ? lane < p.k : lane == 0)
-            h[id] += valid ? 1 : p.k;
+        const int token = i0 + in_batch;
+        const bool in = in_batch < here, valid = in && !(p.valid && !p.valid[cta_first + token]);
+        const char *const row = rows + token * pitch;
+        int id = p.E;
+        float x = 0.f;
+        if (valid) {
+            const uint2 got = r.won[in_batch * (p.k + 1) + choice];
+            id = static_cast<int>(got.y);
+            x = load_logit<KIND>(row, id);
+            if (checked) {
+                const uint2 below = r.won[in_batch * (p.k + 1) + choice + 1];
+                const float4 of = r.row[in_batch];
+                const int other = static_cast<int>(below.y);
+                bool near = below.x != 0;
+                if (near && p.bias) {
+                    // the fp32 scores anew, which the keys hold cut off: each off by the bound, and by half
+                    // a unit for the sum with the bias
+                    const float y = load_logit<KIND>(row, other);
+                    const float hi = score32(p, x, of.x, of.y) + r.bias[id], lo = score32(p, y, of.x, of.y) + r.bias[other];
+                    near = !(hi - lo > 2.f * of.z + 0x1p-23f * (fabsf(hi) + fabsf(lo)));
+                    // equal logits under equal biases are equal scores, in order of their index
+                    near = near && !(x == y && r.bias[id] == r.bias[other] && id < other && choice + 1 < p.k);
+                } else if (near) {
+                    near = got.x == below.x;            // (the kept bits)
+                    near = near && !(x == load_logit<KIND>(row, other) && id < other && choice + 1 < p.k);
+                }
+                near_tokens = near ? 1u << in_batch : 0u;
+            }
+        }
+        near_tokens = __reduce_or_sync(kAll, near_tokens);
+        while (near_tokens) {
+            const int i = __ffs(near_tokens) - 1;
+            near_tokens &= near_tokens - 1;
+            const float4 of = r.row[i];
+            const uint2 *const won = r.won + i * (p.k + 1);
+            const char *const its = rows + (i0 + i) * pitch;
+            // among the choices and the best behind them, where nothing is near that one
+            const uint32_t behind = won[p.k].x;
+            const int count = behind ? p.k + 1 : p.k;
+            int chosen;
+            if (count <= 32 && !Near<PER>(p.bias != nullptr, of.z)(behind, __float_as_uint(of.w)))
+                chosen = refine<KIND>(p, its, lane < count ? static_cast<int>(won[lane].y) : 0, count, of.x);
+            else
+                chosen = choose_near<KIND, PER>(p, its, bias, r.run_keys, r.spare);
+            const int again = __shfl_sync(kAll, chosen, choice);
+            if (in_batch == i && valid) {
+                id = again;
+                x = load_logit<KIND>(row, id);
+            }
+        }
+        // The weights from the chosen logits, in full fp32.
+        const float4 about = in ? r.row[in_batch] : make_float4(0.f, 1.f, 0.f, 0.f);
+        float w;
+        if (p.renormalize) {
+            // relative to the largest of them, so that small scores keep their ratios
+            const int first = in_batch * p.k;
+            float top = -INFINITY;
+            for (int j = 0; j < p.k; ++j)
+                top = fmaxf(top, __shfl_sync(kAll, x, first + j));      // (leaves NaN aside)
+            if (p.sigmoid) {
+                top = fminf(top, 0.f);
+                const float e = expf(-fabsf(x));        // 1 / (1 + exp(-x)) over exp(top)
+                w = (x > 0.f ? 1.f : top == 0.f ? e : expf(x - top)) / (1.f + e);
+                w = x != x ? x : w;
+            } else {
+                w = expf(x - top);
+            }
+            if (top == -INFINITY && x == -INFINITY)
+                w = 0.f;            // (-infinity) - (-infinity)
+            float sum = 0.f;
+            for (int j = 0; j < p.k; ++j)
+                sum += __shfl_sync(kAll, w, first + j);
+            w = sum == 0.f ? 0.f : w / sum;
+            if (!p.sigmoid && about.y != about.y)
+                w = about.y;        // a NaN or an infinity in the row that was not chosen
+        } else {
+            w = p.sigmoid ? 1.f / (1.f + expf(-x)) : about.y == 0.f ? 0.f : expf(x - about.x) / about.y;
+        }
+        const bool writes = in && lane < batch * p.k;
+        const long long pair = (cta_first + i0) * p.k + lane;
+        if (writes) {
+            p.ids[pair] = valid ? id : -1;
+            p.weights[pair] = valid ? w * p.scale : 0.f;
+        }
+        // its rank among the warp's choices of the same expert
+        int *const h = s.hist + warp * bins;
+        const int bin = writes ? id : bins;
+        const uint32_t same = __match_any_sync(kAll, bin), before = same & ((1u << lane) - 1u);
+        if (writes)
+            s.pairs[i0 * p.k + lane] = static_cast<uint32_t>(bin) << 16 | (h[bin] + __popc(before));
+        __syncwarp();
+        if (writes && !before)
+            h[bin] += __popc(same);
         __syncwarp();
     }
-    const long long left = max(0ll, p.T - cta_first);
-    place_pairs(s, p.out, cta_first * p.k,
-                static_cast<int>(min(left, static_cast<long long>(kWarps) * p.per_warp)) * p.k, pairs);
+    place_pairs(s, p.out, cta_first * p.k, lo * p.k, hi * p.k);
 }
 
 struct GroupParams {
     const int *ids;             // [n]
-    int per_warp;               // numbers of a warp, a multiple of 32
     GroupOut out;
 };
 
@@ -550,35 +956,36 @@ __global__ void __launch_bounds__(kThreads) k_group(const GroupParams p)
     clear_hist(s, bins);
     grid_dependency_wait();
     grid_launch_dependents();
-    const long long cta_first = static_cast<long long>(blockIdx.x) * kWarps * p.per_warp;
-    const long long first = cta_first + static_cast<long long>(warp) * p.per_warp;
-    const int count = static_cast<int>(max(0ll, min(static_cast<long long>(p.per_warp), p.out.n - first)));
+    // in units of 32 numbers
+    const long long units = (p.out.n + 31) / 32;
+    const long long cta_first = piece(units, gridDim.x, blockIdx.x) * 32;
+    const int cta_units = static_cast<int>(piece(units, gridDim.x, blockIdx.x + 1) - cta_first / 32);
+    const int count = static_cast<int>(min(p.out.n - cta_first, cta_units * 32ll));
+    const int lo = min(cta_units * warp / kWarps * 32, count), hi = min(cta_units * (warp + 1) / kWarps * 32, count);
     int *const h = s.hist + warp * bins;
-    for (int i = 0; i < count; i += 32) {
-        const bool in = i + lane < count;
-        const int id = in ? p.ids[first + i + lane] : 0;
+    for (int i = lo; i < hi; i += 32) {
+        const bool in = i + lane < hi;
+        const int id = in ? p.ids[cta_first + i + lane] : 0;
         const int bin = !in ? bins : static_cast<uint32_t>(id) < static_cast<uint32_t>(groups) ? id : groups;
         const uint32_t same = __match_any_sync(kAll, bin);
         const uint32_t before = same & ((1u << lane) - 1u);
         if (in)
-            s.pairs[warp * p.per_warp + i + lane] = static_cast<uint32_t>(bin) << 16 | (h[bin] + __popc(before));
+            s.pairs[i + lane] = static_cast<uint32_t>(bin) << 16 | (h[bin] + __popc(before));
         __syncwarp();
         if (in && !before)
             h[bin] += __popc(same);
         __syncwarp();
     }
-    const long long left = max(0ll, p.out.n - cta_first);
-    place_pairs(s, p.out, cta_first, static_cast<int>(min(left, static_cast<long long>(kWarps) * p.per_warp)),
-                p.per_warp);
+    place_pairs(s, p.out, cta_first, lo, hi);
 }
 
 // The second launch of a sort over several clusters: places within a cluster, plus
-// what earlier clusters hold.  `span` numbers belong to a cluster, gridDim.x / clusters
-// CTAs to each.
+// what earlier clusters hold.  Every cluster's numbers are shared by p.ctas CTAs.
 struct PlaceParams {
     const int *ids;
-    int clusters, ctas;             // CTAs of a cluster's span
-    long long span;
+    int clusters, ctas;
+    long long units;            // of the first launch
+    int per_unit, first_ctas;   // its numbers of a unit, and its CTAs
     GroupOut out;
 };
 
@@ -613,14 +1020,26 @@ __global__ void __launch_bounds__(kPlaceThreads) k_place(const PlaceParams p)
         }
     }
     __syncthreads();
-    block_scan(total, bins, part);
-    if (blockIdx.x == 0)
-        for (int b = threadIdx.x; b < bins; b += kPlaceThreads)
-            p.out.offsets[b] = total[b];
-    for (int b = threadIdx.x; b < bins; b += kPlaceThreads)
-        before[b] += total[b];
+    // a thread takes up to two neighbouring bins
+    const int q = bins <= kPlaceThreads ? 1 : 2, b0 = threadIdx.x * q;
+    int t[2] = {}, sum = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (i < q && b0 + i < bins)
+            sum += t[i] = total[b0 + i];
+    int run = thread_scan<kPlaceThreads>(sum, part);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (i < q && b0 + i < bins) {
+            if (blockIdx.x == 0)
+                p.out.offsets[b0 + i] = run;
+            before[b0 + i] += run;
+            run += t[i];
+        }
     __syncthreads();
-    const long long first = cluster * p.span, last = min(p.out.n, first + p.span);
+    const int ctas = kMaxCluster;
+    const long long first = piece(p.units, p.first_ctas, cluster * ctas) * p.per_unit;
+    const long long last = min(p.out.n, piece(p.units, p.first_ctas, (cluster + 1) * ctas) * p.per_unit);
     for (long long i = first + slice * kPlaceThreads + threadIdx.x; i < last; i += p.ctas * kPlaceThreads) {
         const int id = p.ids[i];
         const int bin = static_cast<uint32_t>(id) < static_cast<uint32_t>(groups) ? id : groups;
@@ -640,41 +1059,40 @@ w8a8_status cuda_error(const char *what, cudaError_t e)
     return record_error(W8A8_ERR_CUDA, msg);
 }
 
-// How a sort is cut.  `units` of work (tokens, or 32 numbers) go to warps in runs of
-// per_warp: up to one cluster of eight CTAs while a warp's run is at most `deep` units
-// (one launch), else runs that give two CTAs to every SM.
+// How a sort is cut.  `units` of work (tokens, or 32 numbers) are dealt to CTAs, and to
+// their warps, in equal runs: up to one cluster of eight CTAs while a warp's run is at
+// most `deep` units (one launch), else to as many clusters as a GB300 holds at once (four of
+// 8 CTAs, two to an SM, in each of eight parts; 38, which fill its 152 SMs in number, ran in
+// two waves: 16384 tokens 56 us), or more where a CTA's run would not fit its shared memory.
 struct Cut {
-    int per_warp;
     int ctas;           // of the first launch
     int cluster;        // CTAs of a cluster
     int clusters;       // 1: one launch
+    int most;           // units of a CTA at most
 };
-constexpr int kMaxPerWarp = 64;
-Cut cut(long long units, int deep, int sm_count)
+constexpr int kAtOnce = 32;
+Cut cut(long long units, int deep, int per_warp)
 {
     Cut c;
-    const long long warps = kMaxCluster * kWarps;
-    if (units <= warps * deep) {
-        c.per_warp = static_cast<int>(std::max(1ll, (units + warps - 1) / warps));
-        c.ctas = static_cast<int>(std::max(1ll, (units + kWarps * c.per_warp - 1) / (kWarps * c.per_warp)));
+    if (units <= static_cast<long long>(kMaxCluster) * kWarps * deep) {
         c.cluster = 1;
-        while (c.cluster < c.ctas)
+        while (c.cluster < kMaxCluster && c.cluster * kWarps < units)
             c.cluster *= 2;
         c.ctas = c.cluster;
         c.clusters = 1;
-        return c;
+    } else {
+        const long long most = static_cast<long long>(kMaxCluster) * kWarps * per_warp;
+        c.cluster = kMaxCluster;
+        c.clusters = static_cast<int>(std::max<long long>(kAtOnce, (units + most - 1) / most));
+        c.ctas = c.clusters * kMaxCluster;
     }
-    const long long want = 2ll * sm_count * kWarps;
-    c.per_warp = static_cast<int>(std::min<long long>(kMaxPerWarp, (units + want - 1) / want));
-    const long long span = static_cast<long long>(kMaxCluster) * kWarps * c.per_warp;
-    c.cluster = kMaxCluster;
-    c.clusters = static_cast<int>((units + span - 1) / span);
-    c.ctas = c.clusters * kMaxCluster;
+    c.most = static_cast<int>((units + c.ctas - 1) / c.ctas);
     return c;
 }
 constexpr int kRouteDeep = 4, kGroupDeep = 16;
-Cut route_cut(long long T, int sm_count) { return cut(T, kRouteDeep, sm_count); }
-Cut group_cut(long long n, int sm_count) { return cut((n + 31) / 32, kGroupDeep, sm_count); }
+// (A CTA's numbers take at most 64 and 128 KB.)
+Cut route_cut(long long T, int k) { return cut(T, kRouteDeep, 1024 / k); }
+Cut group_cut(long long n) { return cut((n + 31) / 32, kGroupDeep, 64); }
 
 size_t workspace_bytes(const Cut &c, long long n, int64_t groups, bool ranks)
 {
@@ -706,12 +1124,16 @@ cudaError_t launch(void (*kernel)(Params), const Params &p, int ctas, int cluste
     return cudaLaunchKernelEx(&lc, kernel, p);
 }
 
-cudaError_t launch_place(const GroupOut &out, const int *ids, const Cut &c, long long span, cudaStream_t stream)
+cudaError_t launch_place(const GroupOut &out, const int *ids, const Cut &c, long long units, int per_unit,
+                         cudaStream_t stream)
 {
     PlaceParams p = {};
     p.ids = ids;
     p.clusters = c.clusters;
-    p.span = span;
+    p.units = units;
+    p.per_unit = per_unit;
+    p.first_ctas = c.ctas;
+    const long long span = static_cast<long long>(c.most) * c.cluster * per_unit;
     p.ctas = static_cast<int>(std::max(1ll, std::min(8ll, (span + kPlaceThreads - 1) / kPlaceThreads)));
     p.out = out;
     static volatile int flags[kMaxDeviceFlags] = {};
@@ -723,9 +1145,7 @@ template <int KIND, int PER>
 cudaError_t launch_route(const RouteParams &p, const Cut &c, cudaStream_t stream)
 {
     static volatile int flags[kMaxDeviceFlags] = {};
-    size_t smem = group_smem_bytes(p.E + 1, p.per_warp * p.k);
-    if (p.groups > 1 && !p.group_lanes)
-        smem += sizeof(int) * kWarps * p.E;
+    const size_t smem = group_smem_bytes(p.E + 1, (p.most * p.k + 3) / 4 * 4) + RouteSmem::bytes(p);
     return launch(k_route<KIND, PER>, p, c.ctas, c.cluster, kThreads, smem, flags, stream);
 }
 
@@ -763,9 +1183,6 @@ w8a8_status take_workspace(GroupOut &out, const Cut &c, void *workspace, size_t 
     return W8A8_OK;
 }
 
-// The SMs that cuts go by: a GB300's, so that a workspace's size asks no device.
-constexpr int kCutSms = 152;
-
 }  // namespace
 }  // namespace w8a8
 
@@ -774,7 +1191,7 @@ extern "C" size_t w8a8_route_workspace_size(int64_t T, int64_t E, int top_k)
     using namespace w8a8;
     if (T < 0 || E < 1 || E > W8A8_GROUPS_MAX || top_k < 1 || T > ((1ll << 31) - 1) / top_k)
         return 0;
-    return workspace_bytes(route_cut(T, kCutSms), T * top_k, E, false);
+    return workspace_bytes(route_cut(T, top_k), T * top_k, E, false);
 }
 
 extern "C" size_t w8a8_group_workspace_size(int64_t n, int64_t groups)
@@ -782,7 +1199,7 @@ extern "C" size_t w8a8_group_workspace_size(int64_t n, int64_t groups)
     using namespace w8a8;
     if (n < 0 || groups < 1 || groups > W8A8_GROUPS_MAX || n > (1ll << 31) - 1)
         return 0;
-    return workspace_bytes(group_cut(n, kCutSms), n, groups, true);
+    return workspace_bytes(group_cut(n), n, groups, true);
 }
 
 extern "C" w8a8_status w8a8_route_experts(const void *logits_dev, w8a8_in_dtype dtype, int64_t ld,
@@ -834,6 +1251,8 @@ extern "C" w8a8_status w8a8_route_experts(const void *logits_dev, w8a8_in_dtype 
     p.group_top = group_top;
     const int size = p.E / groups, lanes = size % p.per == 0 ? size / p.per : 0;
     p.group_lanes = (lanes & (lanes - 1)) == 0 ? lanes : 0;
+    while (p.group_lanes >> p.group_shift > 1)
+        ++p.group_shift;
     p.sigmoid = scoring == W8A8_SCORE_SIGMOID;
     p.renormalize = renormalize != 0;
     p.scale = scale;
@@ -844,8 +1263,8 @@ extern "C" w8a8_status w8a8_route_experts(const void *logits_dev, w8a8_in_dtype 
     p.out.rows = rows_dev;
     p.out.groups = p.E;
     p.out.n = T * top_k;
-    const Cut c = route_cut(T, kCutSms);
-    p.per_warp = c.per_warp;
+    const Cut c = route_cut(T, top_k);
+    p.most = c.most;
     if (const w8a8_status st = take_workspace(p.out, c, workspace_dev, workspace_bytes); st != W8A8_OK)
         return st;
     DeviceView dev;
@@ -856,7 +1275,7 @@ extern "C" w8a8_status w8a8_route_experts(const void *logits_dev, w8a8_in_dtype 
                     : dtype == W8A8_IN_BF16 ? launch_route<W8A8_IN_BF16>(p, c, s)
                                             : launch_route<W8A8_IN_FP16>(p, c, s);
     if (e == cudaSuccess && p.out.hist)
-        e = launch_place(p.out, ids_dev, c, static_cast<long long>(c.cluster) * grp::kWarps * c.per_warp * top_k, s);
+        e = launch_place(p.out, ids_dev, c, T, top_k, s);
     return e == cudaSuccess ? W8A8_OK : cuda_error("kernel launch", e);
 }
 
@@ -880,8 +1299,7 @@ extern "C" w8a8_status w8a8_group_rows(const int32_t *ids_dev, int64_t n, int64_
     p.out.rows = rows_dev;
     p.out.groups = static_cast<int>(groups);
     p.out.n = n;
-    const Cut c = group_cut(n, kCutSms);
-    p.per_warp = c.per_warp * 32;
+    const Cut c = group_cut(n);
     if (const w8a8_status st = take_workspace(p.out, c, workspace_dev, workspace_bytes); st != W8A8_OK)
         return st;
     DeviceView dev;
@@ -890,8 +1308,8 @@ extern "C" w8a8_status w8a8_group_rows(const int32_t *ids_dev, int64_t n, int64_
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     static volatile int flags[kMaxDeviceFlags] = {};
     cudaError_t e = launch(k_group, p, c.ctas, c.cluster, grp::kThreads,
-                           group_smem_bytes(p.out.groups + 1, p.per_warp), flags, s);
+                           group_smem_bytes(p.out.groups + 1, c.most * 32), flags, s);
     if (e == cudaSuccess && p.out.hist)
-        e = launch_place(p.out, ids_dev, c, static_cast<long long>(c.cluster) * grp::kWarps * p.per_warp, s);
+        e = launch_place(p.out, ids_dev, c, (n + 31) / 32, 32, s);
     return e == cudaSuccess ? W8A8_OK : cuda_error("kernel launch", e);
 }
