@@ -317,7 +317,7 @@ template <int KIND> __device__ __forceinline__ Pair32 softmax_sum_pair(const Rou
     Pair32 z = {0.f, 0.f};
     if (p.sigmoid)
         return z;
-#pragma unroll 2
+#pragma unroll 1
     for (int e = threadIdx.x & 31; e < p.E; e += 32)
         z = z + exp_pair(two_sum(load_logit<KIND>(row, e), -m));
 #pragma unroll
@@ -399,59 +399,9 @@ template <int KIND> __device__ __noinline__ int choose_exact(const RouteParams &
     return id;
 }
 
-// The runs that are kept, as bits, from scores in fp64.
-template <int KIND> __device__ __noinline__ uint32_t exact_groups(const RouteParams &p, const void *row, float m)
-{
-    using K = unsigned long long;
-    const int lane = threadIdx.x & 31, e0 = lane * p.per, n = max(0, min(p.per, p.E - e0)), size = p.E / p.groups;
-    const double z = softmax_sum<KIND>(p, row, m);
-    K ck[32];
-#pragma unroll 1
-    for (int i = 0; i < n; i += kQuad) {
-        double x[kQuad];
-#pragma unroll
-        for (int j = 0; j < kQuad; ++j)
-            x[j] = load_logit<KIND>(row, e0 + min(i + j, n - 1));
-        if (p.bias || p.group_top == 2)
-            score64(p, x, m, z);
-#pragma unroll
-        for (int j = 0; j < kQuad; ++j)
-            if (i + j < n)
-                ck[i + j] = key_of(p.bias ? x[j] + p.bias[e0 + i + j] : x[j]);
-    }
-    K value = 0;
-    if (p.group_lanes) {
-        K a = 0, b = 0;
-        for (int i = 0; i < n; ++i)
-            two_best(a, b, ck[i]);
-        for (int d = 1; d < p.group_lanes; d *= 2) {
-            const K oa = __shfl_xor_sync(kAll, a, d), ob = __shfl_xor_sync(kAll, b, d);
-            two_best(a, b, oa);
-            b = ob > b ? ob : b;
-        }
-        const K mine = group_value(p.group_top, a, b);
-        value = __shfl_sync(kAll, mine, min(lane, p.groups - 1) * p.group_lanes);
-    } else {
-        for (int g = 0; g < p.groups; ++g) {
-            K a = 0, b = 0;
-            for (int i = 0; i < n; ++i)
-                if ((e0 + i) / size == g)
-                    two_best(a, b, ck[i]);
-            const K top = warp_max(a);
-            const uint32_t who = __ballot_sync(kAll, a == top);
-            const K second = warp_max(lane == __ffs(who) - 1 ? b : a);
-            const K v = group_value(p.group_top, top, second);
-            value = lane == g ? v : value;
-        }
-    }
-    K kept, dropped;
-    const bool keep = rank_groups<K>(p.groups, 1, p.top_groups, lane, value, &kept, &dropped);
-    return __ballot_sync(kAll, keep);
-}
-
-// The same from pairs of fp32; *sure: whether they tell.
+// The runs that are kept, as bits, from scores in pairs of fp32; *sure: whether they tell.
 template <int KIND>
-__device__ __noinline__ uint32_t near_groups(const RouteParams &p, const void *row, float m, bool *sure)
+__device__ __forceinline__ uint32_t near_groups(const RouteParams &p, const void *row, float m, bool *sure)
 {
     using K = unsigned long long;
     const int lane = threadIdx.x & 31, e0 = lane * p.per, n = max(0, min(p.per, p.E - e0)), size = p.E / p.groups;
@@ -469,7 +419,7 @@ __device__ __noinline__ uint32_t near_groups(const RouteParams &p, const void *r
     };
     float most = 0.f;
     if (p.group_lanes) {
-#pragma unroll 2
+#pragma unroll 1
         for (int i = 0; i < n; ++i)
             two_best(a, b, key(e0 + i));
         for (int d = 1; d < p.group_lanes; d *= 2) {
@@ -496,7 +446,7 @@ __device__ __noinline__ uint32_t near_groups(const RouteParams &p, const void *r
 }
 
 // Ranks `count` (at most 32) experts, lane j's being id, by their scores: returns the expert
-// of rank `lane`.  In pairs of fp32 first; where neighbours are nearer than those tell, in fp64.
+// of rank `lane`.  *sure: whether pairs of fp32 tell neighbours apart.
 template <class K> __device__ __forceinline__ int by_rank(K key, int id, int count, K *sorted)
 {
     const int lane = threadIdx.x & 31;
@@ -519,45 +469,44 @@ template <class K> __device__ __forceinline__ int by_rank(K key, int id, int cou
     *sorted = its;
     return mine;
 }
-template <int KIND> __device__ __noinline__ int refine(const RouteParams &p, const void *row, int id, int count, float m)
+template <int KIND>
+__device__ __forceinline__ int refine(const RouteParams &p, const void *row, int id, int count, float m, bool *sure)
 {
     using K = unsigned long long;
     const int lane = threadIdx.x & 31;
     const bool in = lane < count;
     const float l = in ? load_logit<KIND>(row, id) : 0.f;
+    Pair32 c = {l, 0.f};                    // without a bias the logits rank
+    if (p.bias) {
+        const Pair32 z = softmax_sum_pair<KIND>(p, row, m);
+        c = score_pair(p, l, m, z) + Pair32{in ? p.bias[id] : 0.f, 0.f};
+    }
     K sorted;
-    if (!p.bias)        // the logits rank
-        return by_rank<K>(in ? key_of(Pair32{l, 0.f}) : 0ull, id, count, &sorted);
-    const float b = in ? p.bias[id] : 0.f;
-    const Pair32 z = softmax_sum_pair<KIND>(p, row, m);
-    const int ranked = by_rank<K>(in ? key_of(score_pair(p, l, m, z) + Pair32{b, 0.f}) : 0ull, id, count, &sorted);
+    const int ranked = by_rank<K>(in ? key_of(c) : 0ull, id, count, &sorted);
     const K next = __shfl_down_sync(kAll, sorted, 1);
     const int next_id = __shfl_down_sync(kAll, ranked, 1);
     bool near = false;
-    if (lane + 1 < count) {
+    if (p.bias && lane + 1 < count) {
         const Pair32 x = pair_of(sorted), y = pair_of(next);
         near = !((x.h - y.h) + (x.l - y.l) > 2.f * kPairError * (1.f + fabsf(x.h)));
         // equal logits under equal biases are equal scores, in order of their index
         near = near && !(load_logit<KIND>(row, ranked) == load_logit<KIND>(row, next_id) && p.bias[ranked] == p.bias[next_id]);
     }
-    if (!__any_sync(kAll, near))
-        return ranked;
-    double x[kQuad] = {l, l, l, l};         // (one of them is wanted)
-    score64(p, x, m, softmax_sum<KIND>(p, row, m));
-    return by_rank<K>(in ? key_of(x[0] + b) : 0ull, id, count, &sorted);
+    *sure = !__any_sync(kAll, near);
+    return ranked;
 }
 
 // Shared memory of k_route beside the sort's.
 struct RouteSmem {
     uint2 *won;                 // of a warp [batch, k + 1]: the choices' keys and experts, then what is behind
-    uint2 *spare;               // of a warp [32]
+    uint32_t *hard;             // of a warp [32]: bits of its tokens that are left to fp64
     float4 *row;                // of a warp [batch]: a softmax's m and z, a score's bound, the key behind all
     float *bias;                // [32 per]
     int *run_keys;              // of a warp [E], where runs are not whole lanes
     static constexpr int kWon = 64;                     // 32 / k (k + 1) at most
     static __host__ __device__ size_t bytes(const RouteParams &p)
     {
-        return kWarps * (sizeof(float4) * 32 + sizeof(uint2) * (kWon + 32)) + sizeof(float) * 32 * p.per +
+        return kWarps * (sizeof(float4) * 32 + sizeof(uint2) * kWon + sizeof(uint32_t) * 32) + sizeof(float) * 32 * p.per +
                (p.groups > 1 && !p.group_lanes ? sizeof(int) * kWarps * p.E : 0);
     }
     __device__ __forceinline__ RouteSmem(const RouteParams &p, const GroupSmem &s, int warp)
@@ -565,9 +514,10 @@ struct RouteSmem {
         float4 *const rows = reinterpret_cast<float4 *>(s.pairs + (p.most * p.k + 3) / 4 * 4);
         uint2 *const keys = reinterpret_cast<uint2 *>(rows + 32 * kWarps);
         row = rows + 32 * warp;
-        won = keys + (kWon + 32) * warp;
-        spare = won + kWon;
-        bias = reinterpret_cast<float *>(keys + (kWon + 32) * kWarps);
+        won = keys + kWon * warp;
+        uint32_t *const bits = reinterpret_cast<uint32_t *>(keys + kWon * kWarps);
+        hard = bits + 32 * warp;
+        bias = reinterpret_cast<float *>(bits + 32 * kWarps);
         run_keys = reinterpret_cast<int *>(bias + 32 * p.per) + warp * p.E;
     }
 };
@@ -585,6 +535,7 @@ template <int PER> struct Keys {
     uint32_t key[PER];
     float m, z;                 // softmax: the largest logit (0 for -infinity) and the sum
     float bound;                // of a score's error
+    bool hard;                  // which runs are open is left to fp64
 };
 
 template <int KIND, int PER>
@@ -631,6 +582,7 @@ __device__ __forceinline__ void make_keys(const RouteParams &p, const void *row,
         }
     }
     uint32_t (&key)[PER] = out.key;
+    out.hard = false;
     const int mine = min(p.per, p.E - e0);      // experts of this lane
     if (biased) {
 #pragma unroll
@@ -690,8 +642,7 @@ __device__ __forceinline__ void make_keys(const RouteParams &p, const void *row,
         if (near_group) {
             bool sure;
             open = near_groups<KIND>(p, row, m, &sure);
-            if (!sure)
-                open = exact_groups<KIND>(p, row, m);
+            out.hard = !sure;
         }
         if (p.group_lanes) {
             if (near_group)
@@ -758,31 +709,36 @@ template <int PER> struct Near {
     }
 };
 
-// A token whose choice fp32 does not tell: once more, with what is near decided in fp64.
-// Lane j < k gets the j-th expert.  won holds 32 places.
-template <int KIND, int PER>
-__device__ __noinline__ int choose_near(const RouteParams &p, const void *row, const float *bias, int *run_keys, uint2 *won)
+// The weight of a lane's choice, of k lanes from `first` on, from its logit, in full fp32; m
+// and z are a softmax's.
+__device__ __forceinline__ float weigh(const RouteParams &p, float x, int first, float m, float z)
 {
-    const int lane = threadIdx.x & 31, e0 = lane * p.per;
-    const bool biased = p.bias != nullptr;
-    float l[PER];
-    load_lane<KIND, PER>(p, row, e0, l);
-    Keys<PER> t;
-    make_keys<KIND, PER>(p, row, l, bias, run_keys, t);
-    const Near<PER> near(biased, t.bound);
-    __syncwarp();
-    uint32_t last = 0;
-    int count = 0;
-    for (; count < p.k; ++count)
-        last = take_best(t.key, e0, won + count);
-    // what is too near the last, as many as lanes hold
-    for (; count < 32 && near(last, warp_max(t.key[0])); ++count)
-        last = take_best(t.key, e0, won + count);
-    const bool more = near(last, warp_max(t.key[0]));
-    __syncwarp();
-    const int id = lane < count ? static_cast<int>(won[lane].y) : 0;
-    __syncwarp();
-    return more ? choose_exact<KIND>(p, row) : refine<KIND>(p, row, id, count, t.m);
+    float w;
+    if (p.renormalize) {
+        // relative to the largest of them, so that small scores keep their ratios
+        float top = -INFINITY;
+        for (int j = 0; j < p.k; ++j)
+            top = fmaxf(top, __shfl_sync(kAll, x, first + j));      // (leaves NaN aside)
+        if (p.sigmoid) {
+            top = fminf(top, 0.f);
+            const float e = expf(-fabsf(x));        // 1 / (1 + exp(-x)) over exp(top)
+            w = (x > 0.f ? 1.f : top == 0.f ? e : expf(x - top)) / (1.f + e);
+            w = x != x ? x : w;
+        } else {
+            w = expf(x - top);
+        }
+        if (top == -INFINITY && x == -INFINITY)
+            w = 0.f;            // (-infinity) - (-infinity)
+        float sum = 0.f;
+        for (int j = 0; j < p.k; ++j)
+            sum += __shfl_sync(kAll, w, first + j);
+        w = sum == 0.f ? 0.f : w / sum;
+        if (!p.sigmoid && z != z)
+            w = z;              // a NaN or an infinity in the row that was not chosen
+    } else {
+        w = p.sigmoid ? 1.f / (1.f + expf(-x)) : z == 0.f ? 0.f : expf(x - m) / z;
+    }
+    return w * p.scale;
 }
 
 template <int KIND, int PER> __global__ void __launch_bounds__(kThreads, PER <= 8 ? 2 : 1) k_route(const RouteParams p)
@@ -817,9 +773,11 @@ template <int KIND, int PER> __global__ void __launch_bounds__(kThreads, PER <= 
     // their check, the weights and the counts with a lane to each.
     const bool checked = p.bias || KIND == W8A8_IN_FP32;
     const int batch = 32 / p.k, in_batch = lane / p.k, choice = lane - in_batch * p.k;
+    bool any_hard = false;
+    r.hard[lane] = 0;
     for (int i0 = lo; i0 < hi; i0 += batch) {
         const int here = min(batch, hi - i0);
-        uint32_t near_tokens = 0;
+        uint32_t near_tokens = 0, hard_tokens = 0;
         for (int i = 0; i < here; ++i) {
             float l[PER];
             const char *const row = rows + (i0 + i) * pitch;
@@ -836,6 +794,7 @@ template <int KIND, int PER> __global__ void __launch_bounds__(kThreads, PER <= 
                 continue;
             Keys<PER> t;
             make_keys<KIND, PER>(p, row, l, bias, r.run_keys, t);
+            hard_tokens |= t.hard ? 1u << i : 0u;
             uint2 *const won = r.won + i * (p.k + 1);
             // (one more where the choice is checked: the best that stays behind; and the key after it)
             for (int j = 0; j < (checked ? p.k + 1 : p.k); ++j)
@@ -884,59 +843,74 @@ template <int KIND, int PER> __global__ void __launch_bounds__(kThreads, PER <= 
             // among the choices and the best behind them, where nothing is near that one
             const uint32_t behind = won[p.k].x;
             const int count = behind ? p.k + 1 : p.k;
-            int chosen;
+            bool sure = false;
+            int chosen = 0;
             if (count <= 32 && !Near<PER>(p.bias != nullptr, of.z)(behind, __float_as_uint(of.w)))
-                chosen = refine<KIND>(p, its, lane < count ? static_cast<int>(won[lane].y) : 0, count, of.x);
-            else
-                chosen = choose_near<KIND, PER>(p, its, bias, r.run_keys, r.spare);
+                chosen = refine<KIND>(p, its, lane < count ? static_cast<int>(won[lane].y) : 0, count, of.x, &sure);
+            if (!sure) {
+                hard_tokens |= 1u << i;
+                continue;
+            }
             const int again = __shfl_sync(kAll, chosen, choice);
             if (in_batch == i && valid) {
                 id = again;
                 x = load_logit<KIND>(row, id);
             }
         }
-        // The weights from the chosen logits, in full fp32.
-        const float4 about = in ? r.row[in_batch] : make_float4(0.f, 1.f, 0.f, 0.f);
-        float w;
-        if (p.renormalize) {
-            // relative to the largest of them, so that small scores keep their ratios
-            const int first = in_batch * p.k;
-            float top = -INFINITY;
-            for (int j = 0; j < p.k; ++j)
-                top = fmaxf(top, __shfl_sync(kAll, x, first + j));      // (leaves NaN aside)
-            if (p.sigmoid) {
-                top = fminf(top, 0.f);
-                const float e = expf(-fabsf(x));        // 1 / (1 + exp(-x)) over exp(top)
-                w = (x > 0.f ? 1.f : top == 0.f ? e : expf(x - top)) / (1.f + e);
-                w = x != x ? x : w;
-            } else {
-                w = expf(x - top);
-            }
-            if (top == -INFINITY && x == -INFINITY)
-                w = 0.f;            // (-infinity) - (-infinity)
-            float sum = 0.f;
-            for (int j = 0; j < p.k; ++j)
-                sum += __shfl_sync(kAll, w, first + j);
-            w = sum == 0.f ? 0.f : w / sum;
-            if (!p.sigmoid && about.y != about.y)
-                w = about.y;        // a NaN or an infinity in the row that was not chosen
-        } else {
-            w = p.sigmoid ? 1.f / (1.f + expf(-x)) : about.y == 0.f ? 0.f : expf(x - about.x) / about.y;
+        if (hard_tokens) {
+            any_hard = true;
+            if (lane < here && hard_tokens >> lane & 1)
+                atomicOr(r.hard + (i0 - lo + lane) / 32, 1u << ((i0 - lo + lane) & 31));
         }
+        const float4 about = in ? r.row[in_batch] : make_float4(0.f, 1.f, 0.f, 0.f);
+        const float w = weigh(p, x, in_batch * p.k, about.x, about.y);
         const bool writes = in && lane < batch * p.k;
         const long long pair = (cta_first + i0) * p.k + lane;
         if (writes) {
             p.ids[pair] = valid ? id : -1;
-            p.weights[pair] = valid ? w * p.scale : 0.f;
+            p.weights[pair] = valid ? w : 0.f;
         }
-        // its rank among the warp's choices of the same expert
-        int *const h = s.hist + warp * bins;
-        const int bin = writes ? id : bins;
-        const uint32_t same = __match_any_sync(kAll, bin), before = same & ((1u << lane) - 1u);
         if (writes)
-            s.pairs[i0 * p.k + lane] = static_cast<uint32_t>(bin) << 16 | (h[bin] + __popc(before));
+            s.pairs[i0 * p.k + lane] = id;
         __syncwarp();
-        if (writes && !before)
+    }
+    // What pairs of fp32 do not tell either.
+    if (any_hard) {
+        __syncwarp();
+        for (int i = lo; i < hi; ++i) {
+            if (!(r.hard[(i - lo) / 32] >> ((i - lo) & 31) & 1))
+                continue;
+            const char *const row = rows + i * pitch;
+            const int id = choose_exact<KIND>(p, row);
+            float m = -INFINITY, z = 0.f;
+            for (int e = lane; e < p.E; e += 32)
+                m = fmaxf(m, load_logit<KIND>(row, e));
+            m = value_of(warp_max(key_of(m)));
+            m = m == -INFINITY ? 0.f : m;
+            for (int e = lane; e < p.E; e += 32)
+                z += expf(load_logit<KIND>(row, e) - m);
+            z = warp_sum(z);
+            const float w = weigh(p, lane < p.k ? load_logit<KIND>(row, id) : 0.f, 0, m, z);
+            if (lane < p.k) {
+                const long long pair = (cta_first + i) * p.k + lane;
+                p.ids[pair] = id;
+                p.weights[pair] = w;
+                s.pairs[i * p.k + lane] = id;
+            }
+            __syncwarp();
+        }
+    }
+    // each choice's rank among the warp's of the same expert
+    int *const h = s.hist + warp * bins;
+    for (int i0 = lo * p.k; i0 < hi * p.k; i0 += 32) {
+        const int i = i0 + lane;
+        const bool in = i < hi * p.k;
+        const int bin = in ? static_cast<int>(s.pairs[i]) : bins;
+        const uint32_t same = __match_any_sync(kAll, bin), before = same & lanes_below();
+        if (in)
+            s.pairs[i] = static_cast<uint32_t>(bin) << 16 | (h[bin] + __popc(before));
+        __syncwarp();
+        if (in && !before)
             h[bin] += __popc(same);
         __syncwarp();
     }
