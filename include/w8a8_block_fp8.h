@@ -613,15 +613,15 @@ size_t w8a8_group_workspace_size(int64_t n, int64_t groups);
 /*
  * The weighted sum of the experts' rows back to tokens:
  *
- *   out[t] = add[t] + sum_j weights[t, j] * Y[rows[t, j]]   (add NULL: 0)
+ *   out[t] = sum_j weights[t, j] * Y[rows[t, j]] + add[t]   (add NULL: 0)
  *
  *   Y_dev [M, ld_y] of y_dtype (rows in the experts' order); rows_dev int32 and
  *   weights_dev fp32 [T, k], as w8a8_route_experts makes them: a row outside [0, M) is
  *   left out, whatever its weight; add_dev [T, ld_add] and out_dev [T, ld_out] of
  *   out_dtype, which is y_dtype or fp32; out may be add (with its stride), and not
  *   overlap anything else.
- * D columns are used; strides in elements, 0 = dense.  Sums in fp32 in the order of j from
- * add on, one rounding.  T == 0 or D == 0 is a no-op, k == 0 copies add.  D <= 2^24.
+ * D columns are used; strides in elements, 0 = dense.  Sums in fp32 in the order of j,
+ * then add, one rounding.  T == 0 or D == 0 is a no-op, k == 0 copies add.  D <= 2^24.
  */
 w8a8_status w8a8_combine_experts(const void *Y_dev, w8a8_in_dtype y_dtype, int64_t ld_y, int64_t M,
                                  const int32_t *rows_dev, const float *weights_dev,
