@@ -173,7 +173,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_adapter_few(const AdapterParams
     grid_dependency_wait();
     grid_launch_dependents();
     const Item item = find_item<kThreads>(p, static_cast<int>(cluster), kRows, p.out == p.base ? p.L : p.L + 1, scratch);
-    if (item.rows == 0)
+    if (item.rows == 0 || !in_bounds(item.first >= 0 && item.first + item.rows <= p.T && item.adapter <= p.L, p.status,
+                                     SITE_BOUNDS_A))
         return;                             // the whole cluster
     auto row_at = [&](int i) {
         const int row = i < item.rows ? p.order[item.first + i] : -1;

@@ -125,8 +125,10 @@ template <bool BF16, int STAGES> __global__ void __launch_bounds__(kShrinkThread
     }
     grid_dependency_wait();
     // (only now: the second launch reads base and B before it waits for this one, so what
-    // made those has to be finished when it starts)
-    grid_launch_dependents();
+    // made those has to be finished when it starts; and only when this CTA has its TMEM,
+    // which the second launch's CTAs hold while they wait)
+    if (warp == 4)
+        grid_launch_dependents();
     const int tile = blockIdx.x / p.splits, split = blockIdx.x % p.splits;
     const Item item = find_item<kShrinkThreads>(p.a, tile, kTileRows, p.a.L, scratch);
     if (t < kTileRows) {
@@ -140,7 +142,9 @@ template <bool BF16, int STAGES> __global__ void __launch_bounds__(kShrinkThread
     const WaitGuard guard{&abort_word, p.a.status, p.a.wait_limit};
     const int blocks = (p.a.K + 63) / 64;
     const int lo = static_cast<int>(static_cast<long long>(blocks) * split / p.splits);
-    const int steps = item.rows ? static_cast<int>(static_cast<long long>(blocks) * (split + 1) / p.splits) - lo : 0;
+    const bool some = item.rows && in_bounds(item.first >= 0 && item.first + item.rows <= p.a.T && item.adapter < p.a.L,
+                                             p.a.status, SITE_BOUNDS_A);
+    const int steps = some ? static_cast<int>(static_cast<long long>(blocks) * (split + 1) / p.splits) - lo : 0;
     if (warp < 4 && steps) {
         // h of this part of K
         if (__all_sync(0xffffffffu, wait_bounded(done, 0, guard, SITE_TILED_PROMOTE))) {
@@ -280,7 +284,9 @@ __global__ void __launch_bounds__(kExpandThreads) k_adapter_expand(
     const int col_tiles = (p.a.N + kCols - 1) / kCols;
     const int lo = static_cast<int>(static_cast<long long>(col_tiles) * chunk / p.chunks);
     const int hi = static_cast<int>(static_cast<long long>(col_tiles) * (chunk + 1) / p.chunks);
-    const int steps = item.rows && item.adapter < p.a.L ? hi - lo : 0;
+    const bool some = item.rows && item.adapter < p.a.L &&
+                      in_bounds(item.first >= 0 && item.first + item.rows <= p.a.T, p.a.status, SITE_BOUNDS_B);
+    const int steps = some ? hi - lo : 0;
     char *const out = static_cast<char *>(p.a.out);
     if (warp == 5 && steps) {
         // (h alone is the first launch's: nothing here waits for it)
