@@ -28,12 +28,44 @@ struct CombineParams {
     void *out;                  // [T, ld_out]
     long long M, ld_y, ld_add, ld_out;
     int k, D;
-    int chunks;                 // CTAs of a token
+    int chunks;                 // pieces of a token's row
+    long long pieces;           // of all
 };
 
 constexpr int kThreads = 128;
-constexpr int kFlight = 8;
-constexpr int kVec = 8;             // columns a thread, on 16-byte boundaries
+constexpr int kVec = 8;                     // columns of a thread
+
+// A CTA, or for narrow rows each of its warps, takes UNITS pieces of a token, of kVec columns a
+// thread, one after the other whatever the tokens that they lie in: with few rows to a token as
+// many loads are in flight as with many (4767 of one row of 1936 in bf16 and an addend 23.0 us by
+// one piece, 14.4), and narrow rows leave few threads idle (15012 tokens of 6 rows of 160 in
+// fp16 18.0 us by a CTA's pieces, 12.9 by a warp's).  Wide rows are a CTA's: tokens that
+// come from the block's number alone cost less (16384 tokens of 8 rows of 4096 by a warp's pieces 222
+// us, not 208).
+struct Piece {
+    long long t;
+    int col;                    // the thread's or warp's first
+    bool in;
+};
+template <bool WARPS, int UNITS> __device__ __forceinline__ void find_pieces(const CombineParams &p, Piece (&at)[UNITS])
+{
+    constexpr int kWarps = kThreads / 32, columns = (WARPS ? 32 : kThreads) * kVec;
+    const long long first =
+        UNITS * (WARPS ? static_cast<long long>(blockIdx.x) * kWarps + warp_uniform(warp_index()) : static_cast<long long>(blockIdx.x));
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) {
+        const long long n = first + u;
+        at[u].in = n < p.pieces;
+        if (n >> 32) {
+            at[u].t = n / p.chunks;
+            at[u].col = static_cast<int>(n - at[u].t * p.chunks) * columns;
+        } else {
+            const uint32_t t = static_cast<uint32_t>(n) / static_cast<uint32_t>(p.chunks);
+            at[u].t = t;
+            at[u].col = static_cast<int>(static_cast<uint32_t>(n) - t * p.chunks) * columns;
+        }
+    }
+}
 
 template <int KIND> struct Raw {
     static constexpr int kPieces = KIND == W8A8_IN_FP32 ? 2 : 1;
@@ -71,85 +103,137 @@ template <int KIND> struct Raw {
     }
 };
 
-template <int KIND, int OUT> __global__ void __launch_bounds__(kThreads) k_combine(const CombineParams p)
+template <int KIND, int OUT, bool WARPS, int UNITS>
+__global__ void __launch_bounds__(kThreads) k_combine(const CombineParams p)
 {
-    const long long t = blockIdx.x / p.chunks;
-    const int col = (static_cast<int>(blockIdx.x % p.chunks) * kThreads + threadIdx.x) * kVec;
+    constexpr int kDeep = 8 / UNITS;
+    Piece at[UNITS];
+    find_pieces<WARPS>(p, at);
+    bool mine[UNITS];
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) {
+        at[u].col += static_cast<int>(WARPS ? lane_index() : threadIdx.x) * kVec;
+        mine[u] = at[u].in && at[u].col < p.D;
+    }
     grid_dependency_wait();
     grid_launch_dependents();
-    if (col >= p.D)
+    if (UNITS == 1 && !mine[0])
         return;
-    float acc[kVec] = {};
-    Raw<OUT> plus;
-    if (p.add)
-        plus.load(p.add, t * p.ld_add + col);
-    const int *rows = p.rows + t * p.k;
-    const float *weights = p.weights + t * p.k;
-    for (int j0 = 0; j0 < p.k; j0 += kFlight) {
-        Raw<KIND> y[kFlight];
-        float w[kFlight];
-        bool in[kFlight];
+    float acc[UNITS][kVec] = {};
+    Raw<OUT> plus[UNITS];
 #pragma unroll
-        for (int j = 0; j < kFlight; ++j) {
-            const long long row = j0 + j < p.k ? rows[j0 + j] : -1;
-            in[j] = row >= 0 && row < p.M;
-            w[j] = in[j] ? weights[j0 + j] : 0.f;
-            if (in[j])
-                y[j].load(p.Y, row * p.ld_y + col);
+    for (int u = 0; u < UNITS; ++u)
+        if (p.add && mine[u])
+            plus[u].load(p.add, at[u].t * p.ld_add + at[u].col);
+    for (int j0 = 0; j0 < p.k; j0 += kDeep) {
+        Raw<KIND> y[UNITS][kDeep];
+        float w[UNITS][kDeep];
+        bool in[UNITS][kDeep];
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+            const int *const rows = p.rows + at[u].t * p.k + j0;
+            const float *const weights = p.weights + at[u].t * p.k + j0;
+#pragma unroll
+            for (int j = 0; j < kDeep; ++j) {
+                const long long row = mine[u] && j0 + j < p.k ? rows[j] : -1;
+                in[u][j] = row >= 0 && row < p.M;
+                w[u][j] = in[u][j] ? weights[j] : 0.f;
+                if (in[u][j])
+                    y[u][j].load(p.Y, row * p.ld_y + at[u].col);
+            }
         }
 #pragma unroll
-        for (int j = 0; j < kFlight; ++j)
-            if (in[j]) {
+        for (int u = 0; u < UNITS; ++u)
 #pragma unroll
-                for (int i = 0; i < kVec; ++i)
-                    acc[i] = fmaf(w[j], y[j].at(i), acc[i]);
-            }
-    }
-    if (p.add) {
+            for (int j = 0; j < kDeep; ++j)
+                if (in[u][j]) {
 #pragma unroll
-        for (int i = 0; i < kVec; ++i)
-            acc[i] += plus.at(i);
+                    for (int i = 0; i < kVec; ++i)
+                        acc[u][i] = fmaf(w[u][j], y[u][j].at(i), acc[u][i]);
+                }
     }
-    Raw<OUT> o;
-    o.set(acc);
-    o.store(p.out, t * p.ld_out + col);
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) {
+        if (!mine[u])
+            continue;
+        if (p.add) {
+#pragma unroll
+            for (int i = 0; i < kVec; ++i)
+                acc[u][i] += plus[u].at(i);
+        }
+        Raw<OUT> o;
+        o.set(acc[u]);
+        o.store(p.out, at[u].t * p.ld_out + at[u].col);
+    }
 }
 
-// Rows off 16-byte boundaries.  A thread takes the columns of 16 bytes of a row; of each row
-// it loads the two aligned pieces that hold them and shifts them into place (the same shift for
-// the whole row), without a branch before the loads (but where a piece would not lie wholly in
-// Y).  Results go through shared memory, so
-// that neighbouring threads store neighbouring elements: 1013 tokens of 6 rows of 1537 in fp16
-// 10.7 us (an element at a time 15.4).  What remains over the bytes' 3.7 us is the picking of
-// elements: the same rows of 1536 columns, on boundaries, take 5.1.
-constexpr int kShiftThreads = 64, kShiftFlight = 4;         // as many CTAs on an SM as registers allow
-
-template <int KIND> struct Shifted {        // of bf16 or fp16
-    static constexpr int kBytes = 2, kEach = 8;
-    uint4 w0, w1;
-    // acc += weight * the elements from p on (shift: p's place in its piece)
-    __device__ __forceinline__ void add_to(float (&acc)[kEach], float weight, int shift) const
+// Rows off 16-byte boundaries, by words of 4 bytes: neighbouring threads have neighbouring words.
+// A row of 16-bit elements that begins within a word is one element off: then a thread
+// also loads the word after its own and takes the halves that it needs from the two, which is
+// one instruction; the first and last row of Y, whose outer words may not lie wholly in Y, are
+// loaded by elements.  Instructions and latency bound it: 1013 tokens of 6 rows of 1537 in fp16
+// 6.8 us, with columns in whole pieces (1536) 4.8 as above (by elements 15.4; by aligned pieces
+// of 16 bytes shifted into place 10.7, of 200 instructions a piece and row).  The CTAs that an
+// SM holds hide more than rows in flight do: 16384 tokens 96 us with eight CTAs of four rows,
+// 104 with seven, 146 with three or four of eight rows (in fp32, 1013 tokens, 10.4 with seven, 11.3
+// with eight).
+template <int KIND> struct Words {
+    static constexpr bool kFp32 = KIND == W8A8_IN_FP32;
+    static constexpr int kEach = kFp32 ? 8 : 4;         // a thread's words
+    // a thread's i-th column in its warp's piece
+    static __device__ __forceinline__ int column(int i)
     {
-        uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+        const int lane = static_cast<int>(lane_index());
+        return kFp32 ? 32 * i + lane : 64 * (i / 2) + 2 * lane + i % 2;
+    }
+    uint32_t w[kEach], next[kFp32 ? 1 : kEach];
+    uint32_t shift;                                     // in bits
+    // columns from p on, of which `left` are in the row (FULL: all); whole: words may be loaded
+    // that reach an element out of it
+    template <bool FULL> __device__ __forceinline__ void load(const char *p, int left, bool whole)
+    {
+        shift = 0;
+        if constexpr (kFp32) {
 #pragma unroll
-        for (int i = 0; i < 6; ++i)
-            w[i] = shift & 8 ? w[i + 2] : w[i];
+            for (int i = 0; i < kEach; ++i)
+                if (FULL || column(i) < left)
+                    w[i] = *reinterpret_cast<const uint32_t *>(p + 128 * i + 4 * lane_index());
+        } else if (whole) {
+            shift = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 2) * 8;
+            const uint32_t *const word = reinterpret_cast<const uint32_t *>(p - shift / 8) + lane_index();
 #pragma unroll
-        for (int i = 0; i < 5; ++i)
-            w[i] = shift & 4 ? w[i + 1] : w[i];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t u = __funnelshift_r(w[i], w[i + 1], 8 * (shift & 2));
-            float lo, hi;
-            if constexpr (KIND == W8A8_IN_BF16) {
-                lo = __uint_as_float(u << 16), hi = __uint_as_float(u & 0xffff0000u);
-            } else {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u));
-                lo = f.x, hi = f.y;
+            for (int i = 0; i < kEach; ++i) {
+                if (FULL || column(2 * i) < left)
+                    w[i] = word[32 * i];
+                if (shift && (FULL || column(2 * i + 1) < left))
+                    next[i] = word[32 * i + 1];
             }
-            acc[2 * i] = fmaf(weight, lo, acc[2 * i]);
-            acc[2 * i + 1] = fmaf(weight, hi, acc[2 * i + 1]);
+        } else {
+            const uint16_t *const half = reinterpret_cast<const uint16_t *>(p);
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                w[i] = FULL || column(2 * i) < left ? half[column(2 * i)] : 0;
+                if (FULL || column(2 * i + 1) < left)
+                    w[i] |= static_cast<uint32_t>(half[column(2 * i + 1)]) << 16;
+            }
         }
+    }
+    __device__ __forceinline__ void add_to(float (&acc)[kVec], float weight) const
+    {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            if constexpr (kFp32) {
+                acc[i] = fmaf(weight, __uint_as_float(w[i]), acc[i]);
+            } else {
+                const uint32_t u = __funnelshift_r(w[i], next[i], shift);
+                float2 f;
+                if constexpr (KIND == W8A8_IN_BF16)
+                    f = make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+                else
+                    f = __half22float2(*reinterpret_cast<const __half2 *>(&u));
+                acc[2 * i] = fmaf(weight, f.x, acc[2 * i]);
+                acc[2 * i + 1] = fmaf(weight, f.y, acc[2 * i + 1]);
+            }
     }
 };
 
@@ -163,151 +247,87 @@ template <int OUT> __device__ __forceinline__ float element(const void *p, long 
         return __half2float(static_cast<const __half *>(p)[i]);
 }
 
-template <int KIND, int OUT> __global__ void __launch_bounds__(kShiftThreads, 14) k_combine_shift(const CombineParams p)
+template <bool FULL, int KIND, int OUT, int UNITS>
+__device__ __forceinline__ void sum_words(const CombineParams &p, const Piece (&at)[UNITS])
 {
-    using In = Shifted<KIND>;
-    constexpr int kEach = In::kEach;
-    __shared__ float sums[kShiftThreads * kEach];
-    const long long t = blockIdx.x / p.chunks;
-    // an even share of the row's pieces
-    const int pieces = (p.D + kEach - 1) / kEach, part = static_cast<int>(blockIdx.x % p.chunks);
-    const int first = static_cast<int>(static_cast<long long>(pieces) * part / p.chunks) * kEach;
-    const int last = min(p.D, static_cast<int>(static_cast<long long>(pieces) * (part + 1) / p.chunks) * kEach);
-    const int col = first + static_cast<int>(threadIdx.x) * kEach;
-    grid_dependency_wait();
-    grid_launch_dependents();
-    // what is added, as it is stored: neighbouring elements by neighbouring threads
-    float plus[kEach];
+    using In = Words<KIND>;
+    constexpr int kDeep = 4 / UNITS, kBytes = In::kFp32 ? 4 : 2;
+    float acc[UNITS][kVec] = {}, plus[UNITS][kVec];
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-        const int c = first + static_cast<int>(threadIdx.x) + i * kShiftThreads;
-        plus[i] = p.add && c < last ? element<OUT>(p.add, t * p.ld_add + c) : 0.f;
-    }
-    const char *const begin = static_cast<const char *>(p.Y);
-    const char *const end = begin + ((p.M - 1) * p.ld_y + p.D) * In::kBytes;
-    const int need = min(kEach, last - col) * In::kBytes;
-    const int *rows = p.rows + t * p.k;
-    const float *weights = p.weights + t * p.k;
-    float acc[kEach] = {};
-    if (need > 0)
-        for (int j0 = 0; j0 < p.k; j0 += kShiftFlight) {
-            const char *at[kShiftFlight];
-            float w[kShiftFlight];
-            bool edge = false;          // a piece is not wholly within Y
+    for (int u = 0; u < UNITS; ++u)
 #pragma unroll
-            for (int j = 0; j < kShiftFlight; ++j) {
-                const long long row = j0 + j < p.k ? rows[j0 + j] : -1;
-                const bool in = row >= 0 && row < p.M;
-                at[j] = in ? begin + (row * p.ld_y + col) * In::kBytes : nullptr;
-                w[j] = in ? weights[j0 + j] : 0.f;
-                const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(at[j]) & 15);
-                edge = edge || (in && (at[j] - shift < begin || at[j] - shift + (shift + need > 16 ? 32 : 16) > end));
-            }
-            if (!edge) {
-                In y[kShiftFlight];
+        for (int i = 0; i < kVec; ++i) {
+            const int col = at[u].col + In::column(i);
+            plus[u][i] = p.add && (FULL || (at[u].in && col < p.D)) ? element<OUT>(p.add, at[u].t * p.ld_add + col) : 0.f;
+        }
+    for (int j0 = 0; j0 < p.k; j0 += kDeep) {
+        In y[UNITS][kDeep];
+        float w[UNITS][kDeep];
+        bool in[UNITS][kDeep];
 #pragma unroll
-                for (int j = 0; j < kShiftFlight; ++j) {
-                    y[j].w0 = y[j].w1 = make_uint4(0, 0, 0, 0);
-                    const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(at[j]) & 15);
-                    const uint4 *const piece = reinterpret_cast<const uint4 *>(at[j] - shift);
-                    if (at[j])
-                        y[j].w0 = piece[0];
-                    if (at[j] && shift + need > 16)
-                        y[j].w1 = piece[1];
-                }
+        for (int u = 0; u < UNITS; ++u) {
+            const int *const rows = p.rows + at[u].t * p.k + j0;
+            const float *const weights = p.weights + at[u].t * p.k + j0;
 #pragma unroll
-                for (int j = 0; j < kShiftFlight; ++j)
-                    if (at[j])
-                        y[j].add_to(acc, w[j], static_cast<int>(reinterpret_cast<uintptr_t>(at[j]) & 15));
-            } else {
-#pragma unroll 1
-                for (int j = j0; j < min(p.k, j0 + kShiftFlight); ++j) {
-                    const long long row = rows[j];
-                    if (row < 0 || row >= p.M)
-                        continue;
-                    const float weight = weights[j];
-#pragma unroll
-                    for (int i = 0; i < kEach; ++i)
-                        if (col + i < p.D)
-                            acc[i] = fmaf(weight, element<KIND>(p.Y, row * p.ld_y + col + i), acc[i]);
-                }
+            for (int j = 0; j < kDeep; ++j) {
+                const long long row = (FULL || at[u].in) && j0 + j < p.k ? rows[j] : -1;
+                in[u][j] = row >= 0 && row < p.M;
+                w[u][j] = in[u][j] ? weights[j] : 0.f;
+                if (in[u][j])
+                    y[u][j].template load<FULL>(static_cast<const char *>(p.Y) + (row * p.ld_y + at[u].col) * kBytes, p.D - at[u].col,
+                                 row > 0 && row < p.M - 1);
             }
         }
-    // [element of a thread][thread]: no two lanes of a warp in one bank
 #pragma unroll
-    for (int i = 0; i < kEach; ++i)
-        sums[i * kShiftThreads + threadIdx.x] = acc[i];
-    __syncthreads();
+        for (int u = 0; u < UNITS; ++u)
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-        const int n = static_cast<int>(threadIdx.x) + i * kShiftThreads;
-        if (first + n >= last)
-            continue;
-        const float v = sums[(n % kEach) * kShiftThreads + n / kEach] + plus[i];
-        const long long at = t * p.ld_out + first + n;
-        if constexpr (OUT == W8A8_IN_FP32)
-            static_cast<float *>(p.out)[at] = v;
-        else if constexpr (OUT == W8A8_IN_BF16)
-            static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(v);
-        else
-            static_cast<__half *>(p.out)[at] = __float2half_rn(v);
+            for (int j = 0; j < kDeep; ++j)
+                if (in[u][j])
+                    y[u][j].add_to(acc[u], w[u][j]);
     }
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u)
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            const int col = at[u].col + In::column(i);
+            if (!FULL && (!at[u].in || col >= p.D))
+                continue;
+            const long long n = at[u].t * p.ld_out + col;
+            const float v = acc[u][i] + plus[u][i];
+            if constexpr (OUT == W8A8_IN_FP32)
+                static_cast<float *>(p.out)[n] = v;
+            else if constexpr (OUT == W8A8_IN_BF16)
+                static_cast<__nv_bfloat16 *>(p.out)[n] = __float2bfloat16_rn(v);
+            else
+                static_cast<__half *>(p.out)[n] = __float2half_rn(v);
+        }
 }
 
-// fp32 rows off 16-byte boundaries: whole elements, eight columns a thread, 64 apart, so that the
-// rows' places and weights are loaded once for eight: 1013 tokens of 6 rows of 1537 10.8 us (one
-// column a thread 23, shifted as above 17.7).
-__global__ void __launch_bounds__(kShiftThreads, 14) k_combine_columns(const CombineParams p)
+template <int KIND, int OUT, int UNITS>
+__global__ void __launch_bounds__(kThreads, UNITS == 4 ? 3 : UNITS == 2 ? 5 : Words<KIND>::kFp32 ? 7 : 8)
+k_combine_words(const CombineParams p)
 {
-    constexpr int kEach = 8;
-    const long long t = blockIdx.x / p.chunks;
-    const int first = static_cast<int>(static_cast<long long>(p.D) * (blockIdx.x % p.chunks) / p.chunks);
-    const int last = static_cast<int>(static_cast<long long>(p.D) * (blockIdx.x % p.chunks + 1) / p.chunks);
-    const int col = first + static_cast<int>(threadIdx.x);
+    Piece at[UNITS];
+    find_pieces<true>(p, at);
+    bool full = true;
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u)
+        full = full && at[u].in && at[u].col + 32 * kVec <= p.D;
     grid_dependency_wait();
     grid_launch_dependents();
-    const float *const Y = static_cast<const float *>(p.Y), *const add = static_cast<const float *>(p.add);
-    const int *rows = p.rows + t * p.k;
-    const float *weights = p.weights + t * p.k;
-    float acc[kEach] = {}, plus[kEach];
-#pragma unroll
-    for (int i = 0; i < kEach; ++i)
-        plus[i] = add && col + i * kShiftThreads < last ? add[t * p.ld_add + col + i * kShiftThreads] : 0.f;
-    for (int j0 = 0; j0 < p.k; j0 += kShiftFlight) {
-        float y[kShiftFlight][kEach], w[kShiftFlight];
-        bool in[kShiftFlight];
-#pragma unroll
-        for (int j = 0; j < kShiftFlight; ++j) {
-            const long long row = j0 + j < p.k ? rows[j0 + j] : -1;
-            in[j] = row >= 0 && row < p.M;
-            w[j] = in[j] ? weights[j0 + j] : 0.f;
-#pragma unroll
-            for (int i = 0; i < kEach; ++i)
-                if (in[j] && col + i * kShiftThreads < last)
-                    y[j][i] = Y[row * p.ld_y + col + i * kShiftThreads];
-        }
-#pragma unroll
-        for (int j = 0; j < kShiftFlight; ++j)
-            if (in[j]) {
-#pragma unroll
-                for (int i = 0; i < kEach; ++i)
-                    acc[i] = fmaf(w[j], y[j][i], acc[i]);
-            }
-    }
-#pragma unroll
-    for (int i = 0; i < kEach; ++i)
-        if (col + i * kShiftThreads < last)
-            static_cast<float *>(p.out)[t * p.ld_out + col + i * kShiftThreads] = acc[i] + plus[i];
+    if (full)
+        sum_words<true, KIND, OUT>(p, at);
+    else
+        sum_words<false, KIND, OUT>(p, at);
 }
 
 bool on(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-cudaError_t launch_chunks(void (*kernel)(CombineParams), const CombineParams &p, long long T, int threads,
-                          cudaStream_t stream)
+cudaError_t launch_pieces(void (*kernel)(CombineParams), const CombineParams &p, long long each, cudaStream_t stream)
 {
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(static_cast<unsigned>(T * p.chunks), 1, 1);
-    lc.blockDim = dim3(threads, 1, 1);
+    lc.gridDim = dim3(static_cast<unsigned>((p.pieces + each - 1) / each), 1, 1);
+    lc.blockDim = dim3(kThreads, 1, 1);
     lc.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -317,22 +337,29 @@ cudaError_t launch_chunks(void (*kernel)(CombineParams), const CombineParams &p,
     return cudaLaunchKernelEx(&lc, kernel, p);
 }
 
-template <int KIND, int OUT> cudaError_t launch(const CombineParams &p, long long T, cudaStream_t stream)
+template <int KIND, int OUT> cudaError_t launch(CombineParams p, long long T, int sms, cudaStream_t stream)
 {
-    // Eight columns a thread where every row of every tensor allows it.
     constexpr int kY = KIND == W8A8_IN_FP32 ? 4 : 2, kO = OUT == W8A8_IN_FP32 ? 4 : 2;
-    if (p.D % 8 == 0 && on(p.Y, 16) && on(p.add, 16) && on(p.out, 16) && p.ld_y * kY % 16 == 0 &&
-        (!p.add || p.ld_add * kO % 16 == 0) && p.ld_out * kO % 16 == 0) {
-        CombineParams q = p;
-        q.chunks = (p.D + kThreads * kVec - 1) / (kThreads * kVec);
-        return launch_chunks(k_combine<KIND, OUT>, q, T, kThreads, stream);
-    }
-    CombineParams q = p;
-    q.chunks = (p.D + kShiftThreads * 8 - 1) / (kShiftThreads * 8);
-    if constexpr (KIND == W8A8_IN_FP32)
-        return launch_chunks(k_combine_columns, q, T, kShiftThreads, stream);
-    else
-        return launch_chunks(k_combine_shift<KIND, OUT>, q, T, kShiftThreads, stream);
+    const bool wide = p.D % 8 == 0 && on(p.Y, 16) && on(p.add, 16) && on(p.out, 16) && p.ld_y * kY % 16 == 0 &&
+                      (!p.add || p.ld_add * kO % 16 == 0) && p.ld_out * kO % 16 == 0;
+    // pieces of a CTA where they leave at most an eighth of its threads idle
+    constexpr int kWarps = kThreads / 32;
+    auto chunks = [&](int threads) { return (p.D + threads * kVec - 1) / (threads * kVec); };
+    const bool warps = !wide || static_cast<long long>(chunks(kThreads)) * kThreads * kVec - p.D > p.D / 8;
+    p.chunks = chunks(warps ? 32 : kThreads);
+    p.pieces = T * p.chunks;
+    // more of them with few rows to a token, where that leaves every SM 16 warps
+    const int flight = wide ? 8 : 4;
+    int units = p.k <= flight / 4 ? 4 : p.k <= flight / 2 ? 2 : 1;
+    while (units > 1 && p.pieces * (warps ? 1 : kWarps) < 16ll * sms * units)
+        units /= 2;
+    const int each = units * (warps ? kWarps : 1);
+    auto pick = [&](auto one, auto two, auto four) { return launch_pieces(units == 4 ? four : units == 2 ? two : one, p, each, stream); };
+    if (wide && !warps)
+        return pick(k_combine<KIND, OUT, false, 1>, k_combine<KIND, OUT, false, 2>, k_combine<KIND, OUT, false, 4>);
+    if (wide)
+        return pick(k_combine<KIND, OUT, true, 1>, k_combine<KIND, OUT, true, 2>, k_combine<KIND, OUT, true, 4>);
+    return pick(k_combine_words<KIND, OUT, 1>, k_combine_words<KIND, OUT, 2>, k_combine_words<KIND, OUT, 4>);
 }
 
 }  // namespace
@@ -359,7 +386,7 @@ extern "C" w8a8_status w8a8_combine_experts(const void *Y_dev, w8a8_in_dtype y_d
         return W8A8_OK;
     if (!out_dev || (k > 0 && (!rows_dev || !weights_dev)) || (k > 0 && M > 0 && !Y_dev))
         return record_error(W8A8_ERR_INVALID_ARG, "null pointer argument");
-    if (D > (1ll << 24) || k > (1ll << 20) || T > ((1ll << 31) - 1) / ((D + kThreads - 1) / kThreads))
+    if (D > (1ll << 24) || k > (1ll << 20) || T > ((1ll << 31) - 1) / ((D + 127) / 128))
         return record_error(W8A8_ERR_UNSUPPORTED, "D above 2^24, k above 2^20, or T * ceil(D / 128) of 2^31 or more");
     const int yb = y_dtype == W8A8_IN_FP32 ? 4 : 2, ob = out_dtype == W8A8_IN_FP32 ? 4 : 2;
     if (!on(Y_dev, yb) || !on(rows_dev, 4) || !on(weights_dev, 4) || !on(add_dev, ob) || !on(out_dev, ob))
@@ -382,13 +409,13 @@ extern "C" w8a8_status w8a8_combine_experts(const void *Y_dev, w8a8_in_dtype y_d
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (y_dtype == W8A8_IN_FP32)
-        e = launch<W8A8_IN_FP32, W8A8_IN_FP32>(p, T, s);
+        e = launch<W8A8_IN_FP32, W8A8_IN_FP32>(p, T, dev.sm_count, s);
     else if (y_dtype == W8A8_IN_BF16)
-        e = out_dtype == W8A8_IN_FP32 ? launch<W8A8_IN_BF16, W8A8_IN_FP32>(p, T, s)
-                                      : launch<W8A8_IN_BF16, W8A8_IN_BF16>(p, T, s);
+        e = out_dtype == W8A8_IN_FP32 ? launch<W8A8_IN_BF16, W8A8_IN_FP32>(p, T, dev.sm_count, s)
+                                      : launch<W8A8_IN_BF16, W8A8_IN_BF16>(p, T, dev.sm_count, s);
     else
-        e = out_dtype == W8A8_IN_FP32 ? launch<W8A8_IN_FP16, W8A8_IN_FP32>(p, T, s)
-                                      : launch<W8A8_IN_FP16, W8A8_IN_FP16>(p, T, s);
+        e = out_dtype == W8A8_IN_FP32 ? launch<W8A8_IN_FP16, W8A8_IN_FP32>(p, T, dev.sm_count, s)
+                                      : launch<W8A8_IN_FP16, W8A8_IN_FP16>(p, T, dev.sm_count, s);
     if (e == cudaSuccess)
         return W8A8_OK;
     char msg[256];

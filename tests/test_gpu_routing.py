@@ -349,6 +349,33 @@ def test_combine_strides_and_alignments():
             assert torch.equal(out._base[:, shift + D:], before[:, shift + D:])
 
 
+@pytest.mark.parametrize("T,k,D", [(6000, 1, 1936), (9001, 1, 486), (20000, 2, 40), (7000, 3, 1000), (12001, 4, 73),
+                                   (20011, 1, 8), (5003, 2, 257), (9000, 0, 136), (9000, 2, 1)])
+@pytest.mark.parametrize("dtype,out", [("bf16", None), ("fp16", "fp32"), ("fp32", None)])
+def test_combine_many_tokens_of_few_rows(T, k, D, dtype, out):
+    g = gen(T + D)
+    Y = torch.randn(997, D, generator=g, device="cuda").to(DT[dtype])
+    rows = torch.randint(-1, 997, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    weights = torch.rand(T, k, generator=g, device="cuda")
+    add = torch.randn(T, D, generator=g, device="cuda").to(DT[out or dtype])
+    check_combine(Y, rows, weights, out_dtype=out)
+    check_combine(Y, rows, weights, add=add, out_dtype=out)
+
+
+@pytest.mark.parametrize("M", [1, 2, 5])
+@pytest.mark.parametrize("D", [1, 2, 63, 255, 256, 257, 769])
+@pytest.mark.parametrize("shift", [1, 2, 3])
+@pytest.mark.parametrize("dtype", list(DT))
+def test_combine_sees_only_its_own_columns(M, D, shift, dtype):
+    """What lies before, between and after the rows is NaN."""
+    g = gen(M + D + shift)
+    flat = torch.full((shift + M * (D + 3) + 5,), math.nan, device="cuda").to(DT[dtype])
+    Y = torch.as_strided(flat, (M, D), (D + 3, 1), shift)
+    Y.copy_(torch.randn(M, D, generator=g, device="cuda"))
+    rows = torch.randint(0, M, (70, 5), generator=g, device="cuda", dtype=torch.int32)
+    assert torch.isfinite(check_combine(Y, rows, torch.rand(70, 5, generator=g, device="cuda"))).all()
+
+
 def test_combine_rows_past_2_31_elements():
     D = 4096
     M = (1 << 31) // D + 40
