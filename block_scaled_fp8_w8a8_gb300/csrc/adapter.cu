@@ -415,7 +415,7 @@ cudaError_t launch_few(const AdapterParams &p, long long items, const DeviceView
     // rows of 32 adapters of rank 64: 2 23 us, 4 14.7, 8 11.4).
     int cluster = 1;
     while (cluster < kMaxCluster && items * cluster * 2 <= (cluster < 8 ? 2ll : 1ll) * dev.sm_count &&
-           cluster * 2 * 128 <= p.K && S::bytes(p.r_pad, cluster * 2) <= kRoom)
+           cluster * 2 * 128 <= std::max(p.K, p.N) && S::bytes(p.r_pad, cluster * 2) <= kRoom)
         cluster *= 2;
     const size_t smem = S::bytes(p.r_pad, cluster);
     static volatile int flags[kMaxDeviceFlags] = {};
