@@ -554,9 +554,11 @@ def route_experts(logits, top_k, scoring="softmax", bias=None, groups=1, top_gro
     code = _SCORES.get(scoring)
     if code is None:
         raise W8A8Error(W8A8_ERR_INVALID_ARG, f"scoring {scoring!r}: want 'softmax' or 'sigmoid'")
-    if out is not None and lib.route_tensors is not None:
+    if lib.route_tensors is not None:
         st = lib.route_tensors(logits, top_k, code, bias, groups, top_groups, group_top, renormalize, scale, valid,
                                out, _in_codes, types.routing, stream if stream is None else _stream(stream))
+        if type(st) is tuple:
+            return st
         if st == 0:
             return out
         if st is not None:
@@ -597,8 +599,10 @@ def group_rows(ids, groups, out=None, stream=None):
     lib, types = load_library(), _dtypes or _load_dtypes()
     if lib.group_tensors is not None:
         st = lib.group_tensors(ids, groups, out, types.routing, stream if stream is None else _stream(stream))
-        if st == 0 or type(st) is tuple:
-            return st or out
+        if type(st) is tuple:
+            return st
+        if st == 0:
+            return out
         if st is not None:
             check(st)
     n = ids.numel()
@@ -622,13 +626,16 @@ def combine_experts(Y, rows, weights, add=None, out_dtype=None, out=None, stream
     (``out_dtype``, or ``out``'s); ``out`` may be ``add``.  Raises W8A8Error on a non-zero
     status."""
     lib, types = load_library(), _dtypes or _load_dtypes()
-    if out is not None and out_dtype is None and lib.combine_tensors is not None:
-        st = lib.combine_tensors(Y, rows, weights, add, out, _in_codes, types.routing,
-                                 stream if stream is None else _stream(stream))
-        if st == 0:
-            return out
-        if st is not None:
+    if lib.combine_tensors is not None and (out is None or out_dtype is None):
+        st = lib.combine_tensors(Y, rows, weights, add,
+                                 out if out_dtype is None else types.out[out_code(out_dtype)], _in_codes,
+                                 types.routing, stream if stream is None else _stream(stream))
+        if type(st) is int:
+            if st == 0:
+                return out
             check(st)
+        elif st is not None:
+            return st
     if Y.dim() != 2 or rows.dim() != 2:
         raise W8A8Error(W8A8_ERR_INVALID_ARG, f"Y must be [rows, columns] and rows [tokens, choices], not "
                                               f"{list(Y.shape)} and {list(rows.shape)}")
@@ -667,13 +674,15 @@ def adapter_matmul(x, A, B, order, offsets, base, scales=None, out=None, stream=
     ``base``, whose rows without an adapter are then not touched.  variant: W8A8_VARIANT_AUTO,
     _SMALLM or _TILED (see the header).  Raises W8A8Error on a non-zero status."""
     lib, types = load_library(), _dtypes or _load_dtypes()
-    if out is not None and not variant and lib.adapter_tensors is not None:
+    if not variant and lib.adapter_tensors is not None:
         st = lib.adapter_tensors(x, A, B, order, offsets, base, scales, out, _in_codes, types.routing,
                                  stream if stream is None else _stream(stream))
-        if st == 0:
-            return out
-        if st is not None:
+        if type(st) is int:
+            if st == 0:
+                return out
             check(st)
+        elif st is not None:
+            return st
     if x.dim() != 2 or A.dim() != 3 or B.dim() != 3:
         raise W8A8Error(W8A8_ERR_INVALID_ARG, "x must be [rows, K], A [adapters, r, K] and B [adapters, N, r]")
     T, K = x.shape

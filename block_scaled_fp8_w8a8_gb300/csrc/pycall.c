@@ -404,21 +404,26 @@ static int is_current(long gpu)
     return ok;
 }
 
-/* A new tensor [n] on t's device and the current stream, of dtype or (NULL) t's; a new
- * reference and its address, or NULL with an error set. */
-static PyObject *new_tensor(PyObject *t, int64_t n, PyObject *dtype, void **ptr)
+/* A new tensor [a], or with b >= 0 [a, b], of dtype on t's device and the current stream; a
+ * new reference and its address, or NULL with an error set.  (Between launches a tensor
+ * costs some 2.5 us on the host, by this or another of torch's calls: loops give outputs.) */
+static PyObject *new_tensor(PyObject *t, int64_t a, int64_t b, PyObject *dtype, void **ptr)
 {
     static PyObject *new_empty, *kw;
     if (!new_empty && !(new_empty = PyUnicode_InternFromString("new_empty")))
         return NULL;
     if (!kw && !(kw = Py_BuildValue("(s)", "dtype")))
         return NULL;
-    PyObject *count = PyLong_FromLongLong(n);
-    PyObject *shape = count ? PyTuple_Pack(1, count) : NULL;
-    PyObject *call_args[3] = {t, shape, dtype};
-    PyObject *made = shape ? PyObject_VectorcallMethod(new_empty, call_args, 2, dtype ? kw : NULL) : NULL;
-    Py_XDECREF(count);
-    Py_XDECREF(shape);
+    PyObject *call_args[4] = {t, PyLong_FromLongLong(a)};
+    int n = 2;
+    if (b >= 0)
+        call_args[n++] = PyLong_FromLongLong(b);
+    call_args[n] = dtype;
+    PyObject *made = NULL;
+    if (call_args[1] && call_args[n - 1])
+        made = PyObject_VectorcallMethod(new_empty, call_args, n, kw);
+    for (int i = 1; i < n; ++i)
+        Py_XDECREF(call_args[i]);
     PyObject *o = made ? call(made, PTR_OF) : NULL;
     if (o)
         *ptr = (void *)(uintptr_t)PyLong_AsUnsignedLongLong(o);
@@ -434,7 +439,7 @@ static int scratch_of(PyObject *t, size_t bytes, PyObject *u8, PyObject **keep, 
 {
     *keep = NULL;
     *ptr = NULL;
-    return !bytes || (u8 && (*keep = new_tensor(t, (int64_t)bytes, u8, ptr)) != NULL);
+    return !bytes || (u8 && (*keep = new_tensor(t, (int64_t)bytes, -1, u8, ptr)) != NULL);
 }
 
 /* The types of the routing calls: int32, float32, bool, uint8. */
@@ -446,6 +451,15 @@ static int typed(PyObject *o, tensor_t *t, long *gpu, int dims, PyObject *dtype)
     return dtype && dense(o, t, gpu) && t->dims == dims && t->dtype == dtype;
 }
 
+/* What a call returns that made its outputs (takes the reference), or was given them (NULL). */
+static PyObject *result_of(PyObject *made, int st)
+{
+    if (made && !st)
+        return made;
+    Py_XDECREF(made);
+    return PyLong_FromLong(st);
+}
+
 static int code_of(PyObject *codes, PyObject *dtype)
 {
     PyObject *o = PyDict_GetItemWithError(codes, dtype);
@@ -453,7 +467,8 @@ static int code_of(PyObject *codes, PyObject *dtype)
 }
 
 /* logits, top_k, scoring, bias, groups, top_groups, group_top, renormalize, scale, valid,
- * outputs, the input types' codes by dtype, dtypes, stream */
+ * outputs, the input types' codes by dtype, dtypes, stream.  Without outputs (None), here and
+ * below, the result is a tuple of new ones (one: the tensor), or a status other than 0. */
 static PyObject *py_route_tensors(PyObject *self, PyObject *const *args, Py_ssize_t n)
 {
     (void)self;
@@ -461,8 +476,10 @@ static PyObject *py_route_tensors(PyObject *self, PyObject *const *args, Py_ssiz
         return NULL;
     tensor_t x, bias = {0}, valid = {0}, o[5];
     long gpu = ANY_GPU;
+    const int make = args[10] == Py_None;
+    PyObject *made = NULL, *keep = NULL;
     PyObject *const i32 = type_at(args[12], R_INT32), *const f32 = type_at(args[12], R_F32);
-    if (!PyTuple_Check(args[10]) || PyTuple_GET_SIZE(args[10]) != 5 || !PyLong_Check(args[1]) ||
+    if ((!make && (!PyTuple_Check(args[10]) || PyTuple_GET_SIZE(args[10]) != 5)) || !PyLong_Check(args[1]) ||
         !dense(args[0], &x, &gpu) || x.dims != 2)
         goto other;
     const int64_t T = x.size[0], E = x.size[1], k = I64(1);
@@ -473,7 +490,7 @@ static PyObject *py_route_tensors(PyObject *self, PyObject *const *args, Py_ssiz
     if (args[9] != Py_None && (!dense(args[9], &valid, &gpu) || !is(&valid, 1, T, 0) ||
                                (valid.dtype != type_at(args[12], R_BOOL) && valid.dtype != type_at(args[12], R_U8))))
         goto other;
-    for (int i = 0; i < 5; ++i) {
+    for (int i = 0; i < 5 && !make; ++i) {
         const int flat = i == 2 || i == 3;
         if (!typed(PyTuple_GET_ITEM(args[10], i), &o[i], &gpu, flat ? 1 : 2, i == 1 ? f32 : i32) ||
             !(flat ? is(&o[i], 1, i == 2 ? T * k : E + 1, 0) : is(&o[i], 2, T, k)))
@@ -483,10 +500,22 @@ static PyObject *py_route_tensors(PyObject *self, PyObject *const *args, Py_ssiz
     const double scale = PyFloat_AsDouble(args[8]);
     const int scoring = I32(2), groups = I32(4), top_groups = I32(5), group_top = I32(6);
     const size_t size = f_route_size(T, E, (int)k);
-    if (kind < 0 || renormalize < 0 || !is_current(gpu) || (size && args[13] != Py_None))
+    if (kind < 0 || renormalize < 0 || !is_current(gpu) || ((size || make) && args[13] != Py_None) ||
+        PyErr_Occurred())
         goto other;
+    if (make) {
+        if (!i32 || !f32 || !(made = PyTuple_New(5)))
+            goto other;
+        for (int i = 0; i < 5; ++i) {
+            const int flat = i == 2 || i == 3;
+            PyObject *const t = new_tensor(args[0], !flat ? T : i == 2 ? T * k : E + 1, flat ? -1 : k,
+                                           i == 1 ? f32 : i32, &o[i].ptr);
+            if (!t)
+                goto other;
+            PyTuple_SET_ITEM(made, i, t);
+        }
+    }
     void *s = stream_of(args[13]), *scratch;
-    PyObject *keep;
     if (PyErr_Occurred() || !scratch_of(args[0], size, type_at(args[12], R_U8), &keep, &scratch))
         goto other;
     int st;
@@ -495,14 +524,14 @@ static PyObject *py_route_tensors(PyObject *self, PyObject *const *args, Py_ssiz
                  renormalize, (float)scale, o[0].ptr, o[1].ptr, o[2].ptr, o[3].ptr, o[4].ptr, scratch, size, s);
     Py_END_ALLOW_THREADS
     Py_XDECREF(keep);
-    return PyLong_FromLong(st);
+    return result_of(made, st);
 other:
     PyErr_Clear();
+    Py_XDECREF(made);
     Py_RETURN_NONE;
 }
 
-/* ids, groups, outputs, dtypes, stream.  Without outputs (None) the result is a tuple of new
- * ones, or a status other than 0. */
+/* ids, groups, outputs, dtypes, stream */
 static PyObject *py_group_tensors(PyObject *self, PyObject *const *args, Py_ssize_t n)
 {
     (void)self;
@@ -521,8 +550,8 @@ static PyObject *py_group_tensors(PyObject *self, PyObject *const *args, Py_ssiz
     if ((size || args[2] == Py_None) && args[4] != Py_None)
         goto other;
     if (args[2] == Py_None) {
-        if (!(made[0] = new_tensor(args[0], count, NULL, &order.ptr)) ||
-            !(made[1] = new_tensor(args[0], groups + 1, NULL, &offsets.ptr)))
+        if (!(made[0] = new_tensor(args[0], count, -1, i32, &order.ptr)) ||
+            !(made[1] = new_tensor(args[0], groups + 1, -1, i32, &offsets.ptr)))
             goto other;
     } else if (!PyTuple_Check(args[2]) || PyTuple_GET_SIZE(args[2]) != 2 ||
                !typed(PyTuple_GET_ITEM(args[2], 0), &order, &gpu, 1, i32) || !is(&order, 1, count, 0) ||
@@ -548,7 +577,8 @@ other:
     Py_RETURN_NONE;
 }
 
-/* Y, rows, weights, add, out, the input types' codes by dtype, dtypes, stream */
+/* Y, rows, weights, add, out (or a new one's dtype, None: Y's), the input types' codes by dtype,
+ * dtypes, stream */
 static PyObject *py_combine_tensors(PyObject *self, PyObject *const *args, Py_ssize_t n)
 {
     (void)self;
@@ -556,14 +586,28 @@ static PyObject *py_combine_tensors(PyObject *self, PyObject *const *args, Py_ss
         return NULL;
     tensor_t y, rows, weights, add = {0}, out;
     long gpu = ANY_GPU;
+    const int make = Py_TYPE(args[4]) != plain;
+    PyObject *made = NULL;
     if (!dense(args[0], &y, &gpu) || y.dims != 2 || !typed(args[1], &rows, &gpu, 2, type_at(args[6], R_INT32)) ||
-        !typed(args[2], &weights, &gpu, 2, type_at(args[6], R_F32)) || !dense(args[4], &out, &gpu) ||
-        !is(&weights, 2, rows.size[0], rows.size[1]) || !is(&out, 2, rows.size[0], y.size[1]))
+        !typed(args[2], &weights, &gpu, 2, type_at(args[6], R_F32)) ||
+        !is(&weights, 2, rows.size[0], rows.size[1]))
         goto other;
+    if (make) {
+        if (args[7] != Py_None || !is_current(gpu) || (args[4] != Py_None && code_of(args[5], args[4]) < 0))
+            goto other;
+        out.dtype = args[4] == Py_None ? y.dtype : args[4];
+        out.dims = 2;
+        out.size[0] = rows.size[0];
+        out.size[1] = y.size[1];
+    } else if (!dense(args[4], &out, &gpu) || !is(&out, 2, rows.size[0], y.size[1])) {
+        goto other;
+    }
     if (args[3] != Py_None && (!typed(args[3], &add, &gpu, 2, out.dtype) || !is(&add, 2, out.size[0], out.size[1])))
         goto other;
     const int y_kind = code_of(args[5], y.dtype), out_kind = code_of(args[5], out.dtype);
     if (y_kind < 0 || out_kind < 0 || !is_current(gpu))
+        goto other;
+    if (make && !(made = new_tensor(args[0], out.size[0], out.size[1], out.dtype, &out.ptr)))
         goto other;
     void *s = stream_of(args[7]);
     if (PyErr_Occurred())
@@ -573,9 +617,10 @@ static PyObject *py_combine_tensors(PyObject *self, PyObject *const *args, Py_ss
     st = f_combine(y.ptr, y_kind, 0, y.size[0], rows.ptr, weights.ptr, add.ptr, 0, out.ptr, out_kind, 0,
                    rows.size[0], rows.size[1], y.size[1], s);
     Py_END_ALLOW_THREADS
-    return PyLong_FromLong(st);
+    return result_of(made, st);
 other:
     PyErr_Clear();
+    Py_XDECREF(made);
     Py_RETURN_NONE;
 }
 
@@ -587,23 +632,27 @@ static PyObject *py_adapter_tensors(PyObject *self, PyObject *const *args, Py_ss
         return NULL;
     tensor_t x, a, b, order, offsets, base, scales = {0}, out;
     long gpu = ANY_GPU;
+    const int make = args[7] == Py_None;
+    PyObject *made = NULL, *keep = NULL;
     PyObject *const i32 = type_at(args[9], R_INT32);
     if (!dense(args[0], &x, &gpu) || x.dims != 2 || !typed(args[1], &a, &gpu, 3, x.dtype) ||
         !typed(args[2], &b, &gpu, 3, x.dtype) || !typed(args[3], &order, &gpu, 1, i32) ||
-        !typed(args[4], &offsets, &gpu, 1, i32) || !dense(args[5], &base, &gpu) || !dense(args[7], &out, &gpu))
+        !typed(args[4], &offsets, &gpu, 1, i32) || !dense(args[5], &base, &gpu) ||
+        (!make && !dense(args[7], &out, &gpu)))
         goto other;
     const int64_t T = x.size[0], K = x.size[1], L = a.size[0], r = a.size[1], N = b.size[1];
     if (!is3(&a, L, r, K) || !is3(&b, L, N, r) || !is(&order, 1, T, 0) || !is(&offsets, 1, L + 1, 0) ||
-        !is(&base, 2, T, N) || !is(&out, 2, T, N) || out.dtype != base.dtype)
+        !is(&base, 2, T, N) || (!make && (!is(&out, 2, T, N) || out.dtype != base.dtype)))
         goto other;
     if (args[6] != Py_None && (!typed(args[6], &scales, &gpu, 1, type_at(args[9], R_F32)) || !is(&scales, 1, L, 0)))
         goto other;
-    const int kind = code_of(args[8], x.dtype), out_kind = code_of(args[8], out.dtype);
+    const int kind = code_of(args[8], x.dtype), out_kind = code_of(args[8], base.dtype);
     const size_t size = f_adapter_size(T, L, r, K, 0);
-    if (kind < 0 || out_kind < 0 || !is_current(gpu) || (size && args[10] != Py_None))
+    if (kind < 0 || out_kind < 0 || !is_current(gpu) || ((size || make) && args[10] != Py_None))
+        goto other;
+    if (make && !(made = new_tensor(args[5], T, N, base.dtype, &out.ptr)))
         goto other;
     void *s = stream_of(args[10]), *scratch;
-    PyObject *keep;
     if (PyErr_Occurred() || !scratch_of(args[0], size, type_at(args[9], R_U8), &keep, &scratch))
         goto other;
     int st;
@@ -612,9 +661,10 @@ static PyObject *py_adapter_tensors(PyObject *self, PyObject *const *args, Py_ss
                    T, L, r, K, N, 0, scratch, size, s);
     Py_END_ALLOW_THREADS
     Py_XDECREF(keep);
-    return PyLong_FromLong(st);
+    return result_of(made, st);
 other:
     PyErr_Clear();
+    Py_XDECREF(made);
     Py_RETURN_NONE;
 }
 
