@@ -446,18 +446,26 @@ template <bool BF16, int OUT> cudaError_t launch_adapter(const AdapterParams &p,
 }
 
 // Whether a problem's sizes are for the tiles of 128 rows (adapter_tile.cu), which take two
-// launches and some 20 us for them, then stream: where rows are many, and many to an adapter
-// (16 rows a cluster against tiles, rank 64, 4096x4096: 2048 rows of 32 adapters 47 / 67 us, 4096
-// of 16 53 / 45, 8192 103 / 53; 1024x8192 from rank 32 into bf16: 2048 rows 30.0 / 26.7, 4096
-// 55 / 41; of rank 128 into fp32: 2048 73 / 90, 4096 138 / 148).
+// launches and some 10 to 20 us for them, then stream: where there is much to read, and many rows
+// to an adapter.  The clusters of 16 rows take a time that grows with T (K + N + 640), the tiles
+// one that hardly depends on r.  Clusters / tiles in us, T of L adapters, KxN, bf16 into
+// bf16:
+//   r 16   1600 of 24 1024x1024 9.4 / 13.6, 2048 of 4 4096x4096 25.2 / 20.5, 4096 of 8 1024x1024
+//          13.5 / 12.4, 16384 256x256 23 / 11.6; 1536 256x4096 into fp32 20.7 / 19.3
+//   r 64   4096 of 8 2048x2048 34 / 39, 8192 of 8 1024x1024 38 / 29, 16384 512x512 44 / 24; 2048
+//          of 16 4096x4096 35 / 43; r 32 1024x8192 30.7 / 27.0, into fp32 40.6 / 41.9
+//   r 128  3200 of 8 4096x4096 103 / 68, 16384 512x512 68 / 36; 4096 of 16 1024x8192 into fp32 138 / 148
+bool many_rows(const AdapterParams &p) { return p.L > 0 && p.T >= 1536 && p.T / 64 >= p.L && p.r >= 8 && p.K >= 64; }
 bool tiled(const AdapterParams &p)
 {
-    return p.L > 0 && p.T >= (p.r <= 64 ? 2560 : 5120) && p.T / 64 >= p.L && p.r >= 8 && p.K >= 64;
+    const long long work = static_cast<long long>(p.T) * (static_cast<long long>(p.K) + p.N + 640);
+    return many_rows(p) && work >= (p.r <= 16 ? 6500000 : p.r <= 64 ? 21000000 : 25000000);
 }
 
+// Asked for wherever some N makes tiles of the rows.
 size_t workspace_bytes(const AdapterParams &p, int variant)
 {
-    const bool tiles = variant == W8A8_VARIANT_TILED || (variant == W8A8_VARIANT_AUTO && tiled(p));
+    const bool tiles = variant == W8A8_VARIANT_TILED || (variant == W8A8_VARIANT_AUTO && many_rows(p));
     return tiles ? sizeof(float) * tile_splits(p) * p.T * p.r_pad : 0;
 }
 
@@ -546,7 +554,7 @@ extern "C" w8a8_status w8a8_adapter_matmul(const void *x_dev, w8a8_in_dtype dtyp
         return record_error(W8A8_ERR_UNSUPPORTED, "TILED needs an adapter, r % 8 == 0 from 8 to 128, K % 8 == 0 from 64 on, "
                                                   "N % 8 == 0 and rows on 16-byte boundaries");
     const bool tiles = fits && (variant == W8A8_VARIANT_TILED || (variant == W8A8_VARIANT_AUTO && tiled(p)));
-    if (const size_t need = tiles ? w8a8::workspace_bytes(p, variant) : 0;
+    if (const size_t need = fits ? w8a8::workspace_bytes(p, variant) : 0;
         need && (!workspace_dev || workspace_bytes < need || !on(workspace_dev, 16))) {
         char msg[160];
         snprintf(msg, sizeof(msg), "workspace of %zu bytes at %p: need %zu bytes, 16-byte aligned", workspace_bytes,

@@ -647,7 +647,7 @@ w8a8_status w8a8_combine_experts(const void *Y_dev, w8a8_in_dtype y_dtype, int64
  * order must not name a row twice; entries outside [0, T) are skipped, and offsets that
  * decrease or leave [0, T] give unspecified results but no out-of-bounds access.
  * L <= W8A8_GROUPS_MAX, r <= W8A8_ADAPTER_MAX_R; any K and N up to 2^24, strides and
- * alignments (pieces of 16 bytes where K % 8 == 0, r % 4 == 0 and the rows allow).
+ * alignments (pieces of 16 bytes where K % 8 == 0, r % 8 == 0 and the rows allow).
  * T == 0 or N == 0 is a no-op.  variant (w8a8_variant): AUTO; SMALLM, one launch of
  * clusters on 16 rows each; TILED, two launches of 128-row tiles on the tensor cores' tcgen05
  * path (r % 8 == 0 from 8 to 128, K % 8 == 0 from 64 on, N % 8 == 0, rows on 16-byte
