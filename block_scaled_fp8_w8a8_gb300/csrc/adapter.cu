@@ -15,10 +15,16 @@
 // L2 while x A^T is computed.
 //
 // h is kept to fp32: an MMA takes 16-bit operands, so h is split into a sum of two or
-// three of them, each the rounding of what the ones before leave.  bf16: two leave an
-// error of 2^-18 (16-bit output, whose rounding is 2^-9), three one of 2^-27 (fp32
-// output).  fp16: two leave 2^-24; h is first scaled by a power of two per row so that
-// its largest element is near 2^14, because fp16's range is narrow.
+// three of them, each the rounding of what the ones before leave (a rounding of p bits
+// leaves at most 2^-p, and what it leaves begins one bit lower).  bf16: two leave an error of
+// 2^-17 (16-bit output, whose rounding is 2^-8), three one of 2^-26 (fp32 output).  fp16:
+// two leave 2^-23, a step of fp32; h is first scaled by a power of two per row so that its
+// largest element is near 2^14, because fp16's range is narrow.
+//
+// Latency bounds it (the SMs hold 16 warps each by registers): one row of rank 16, 4096x4096, 6.5
+// us; 64 rows of 32 adapters of rank 64 12.5 us, of which the weights' 24 MB are 3.6; 257 rows of
+// rank 24, 1000x1537 in fp16, 11.5 us (9.0 with 1536 columns, on 16-byte boundaries); 2048 rows of 16
+// adapters of rank 32, 1024x8192 into fp32, 40.6 us, 3.5 TB/s.
 #include <algorithm>
 #include <cstdio>
 

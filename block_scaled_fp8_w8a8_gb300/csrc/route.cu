@@ -20,8 +20,13 @@
 // error: the replaced bits, and where a bias makes the scores themselves be compared
 // (without one their order is the logits', which are compared instead) their rounding,
 // bounded below (`bound`).  Where two neighbours of the chosen order are nearer than
-// that, those that are too near are scored and ranked again in fp64 (refine); where the
-// worst kept and the best dropped run are, the whole token is (choose_exact).
+// that, those that are too near are scored and ranked again as pairs of fp32 (refine), and so
+// are the runs where the worst kept and the best dropped one are (near_groups); what pairs do
+// not tell is chosen in fp64 after all tokens (choose_exact).
+//
+// Instructions and latency bound it: 16384 tokens of 256 experts in fp32, 8 of 8 runs' 4, sigmoid and
+// bias, 33 us, of which the placing of the pairs in a second launch is 5; 1000 instructions a
+// token, 53 % of the issue slots.  One token 5.4 us, 64 6.3, 1013 of 160 experts 16.3.
 #include <algorithm>
 #include <cstdio>
 
