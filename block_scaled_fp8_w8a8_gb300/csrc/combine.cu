@@ -382,6 +382,8 @@ extern "C" w8a8_status w8a8_combine_experts(const void *Y_dev, w8a8_in_dtype y_d
     ld_out = ld_out ? ld_out : D;
     if (ld_y < D || ld_add < D || ld_out < D)
         return record_error(W8A8_ERR_INVALID_ARG, "a row stride is shorter than its row");
+    if (add_dev && add_dev == out_dev && ld_add != ld_out && T > 1)
+        return record_error(W8A8_ERR_INVALID_ARG, "out in add's place with another row stride");
     if (T == 0 || D == 0)
         return W8A8_OK;
     if (!out_dev || (k > 0 && (!rows_dev || !weights_dev)) || (k > 0 && M > 0 && !Y_dev))

@@ -167,6 +167,25 @@ def test_route(T, E, k, groups, top_groups, group_top, scoring, biased):
                     renormalize=renormalize, scale=1.5, valid=valid)
 
 
+@pytest.mark.parametrize("T,E,k,groups", [(131073, 1023, 32, 31), (140000, 1024, 32, 1), (1 << 20, 3, 1, 3), (300000, 33, 7, 1)])
+def test_route_as_many_as_its_shared_memory_holds(T, E, k, groups):
+    """Without a bias the scores' order is the logits', compared here as numbers (those of one
+    value may stand in any order in torch.topk)."""
+    g = gen(E)
+    logits = torch.randn(T, E, generator=g, device="cuda")
+    ids, weights, order, offsets, rows = w8.route_experts(logits, k, "sigmoid", groups=groups, top_groups=groups, group_top=1)
+    top = logits.topk(k, 1).values
+    assert torch.equal(logits.gather(1, ids.long()), top)
+    s = top.double().sigmoid()
+    # 4 roundings of a score, k of the sum, one quotient
+    assert ((weights - s / s.sum(1, keepdim=True)).abs() <= (k + 8) * 2.0 ** -24).all()
+    pairs = torch.sort(ids.flatten(), stable=True)
+    assert torch.equal(order, pairs.indices.int())
+    assert torch.equal(offsets[1:].long(), torch.bincount(ids.flatten(), minlength=E).cumsum(0)) and offsets[0] == 0
+    assert torch.equal(rows.flatten()[order.long()], torch.arange(T * k, device="cuda", dtype=torch.int32))
+    ok()
+
+
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("bias", ["none", "zero", "levels"])
 def test_route_ties_go_to_the_lower_index(scoring, bias):
@@ -645,6 +664,31 @@ def test_adapters_captured_and_replayed_over_new_rows():
         graph.replay()
         want, bound = adapter_reference(**c)
         assert ((out.double() - want).abs() <= bound).all()
+    ok()
+
+
+@pytest.mark.parametrize("variant", [SMALL, TILED])
+def test_adapters_rows_past_2_31_elements(variant):
+    c = adapter_case(40, 3, 256, 264, 16, "bf16", None)
+    order, offsets = w8.group_rows(c["ids"], 3)
+    want = w8.adapter_matmul(c["x"], c["A"], c["B"], order, offsets, c["base"], variant=variant)
+    ld = (1 << 26) + 8
+    far = torch.zeros(40 * ld, dtype=torch.bfloat16, device="cuda")
+    x, base, out = (torch.as_strided(far, (40, n), (ld, 1), at) for n, at in ((256, 0), (264, 1024), (264, 4096)))
+    x.copy_(c["x"]), base.copy_(c["base"])
+    w8.adapter_matmul(x, c["A"], c["B"], order, offsets, base, out=out, variant=variant)
+    assert torch.equal(out, want)
+    ok()
+
+
+def test_route_rows_past_2_31_elements():
+    g = gen(8)
+    logits = torch.randn(40, 64, generator=g, device="cuda").half()
+    far = torch.zeros(40 * ((1 << 26) + 3), dtype=torch.float16, device="cuda")
+    strided = torch.as_strided(far, (40, 64), ((1 << 26) + 3, 1))
+    strided.copy_(logits)
+    for a, b in zip(w8.route_experts(logits, 4), w8.route_experts(strided, 4)):
+        assert torch.equal(a, b)
     ok()
 
 

@@ -91,6 +91,11 @@ def test_combine(kw, status):
     assert combine(**kw) == status
 
 
+def test_combine_in_place_of_an_addend_of_another_stride():
+    assert combine(add=256, ld_add=64, ld_out=40) == ARG
+    assert "add's place" in w8.w8a8_last_error()
+
+
 def adapters(T=4, L=2, r=16, K=64, N=32, dtype=0, out_dtype=0, ld_x=0, ld_base=0, ld_out=0, variant=0, **ptr):
     p = dict(x=256, A=256, B=256, order=256, off=256, scales=0, base=256, out=512, ws=0, size=0)
     p.update(ptr)
