@@ -17,7 +17,8 @@ namespace grp {
 
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxCluster = 8;
+constexpr int kCluster = 8;             // CTAs of each cluster of many
+constexpr int kMaxCluster = 16;         // and of one by itself at most
 constexpr int kPlaceThreads = 1024;
 
 // Where a sort's results go.  Bin `groups` holds what belongs to no group: it is
@@ -132,16 +133,17 @@ __device__ __forceinline__ void place_pairs(const GroupSmem &s, const GroupOut &
             const int b = b0 + i;
             if (i >= q || b >= bins)
                 continue;
-            int v[kMaxCluster];
+            int v[kMaxCluster] = {};
 #pragma unroll
-            for (uint32_t r = 0; r < kMaxCluster; ++r) {
-                v[r] = 0;
-                if (r < ctas)
-                    asm volatile("ld.shared::cluster.s32 %0, [%1];"
-                                 : "=r"(v[r])
-                                 : "r"(cluster_map(smem_addr(s.tot + b), r))
-                                 : "memory");
-            }
+            for (uint32_t half = 0; half < kMaxCluster; half += kCluster)
+                if (half < ctas)
+#pragma unroll
+                    for (uint32_t r = half; r < half + kCluster; ++r)
+                        if (r < ctas)
+                            asm volatile("ld.shared::cluster.s32 %0, [%1];"
+                                         : "=r"(v[r])
+                                         : "r"(cluster_map(smem_addr(s.tot + b), r))
+                                         : "memory");
             total[i] = 0;
 #pragma unroll
             for (uint32_t r = 0; r < kMaxCluster; ++r) {

@@ -1016,7 +1016,7 @@ __global__ void __launch_bounds__(kPlaceThreads) k_place(const PlaceParams p)
             run += t[i];
         }
     __syncthreads();
-    const int ctas = kMaxCluster;
+    const int ctas = kCluster;
     const long long first = piece(p.units, p.first_ctas, cluster * ctas) * p.per_unit;
     const long long last = min(p.out.n, piece(p.units, p.first_ctas, (cluster + 1) * ctas) * p.per_unit);
     for (long long i = first + slice * kPlaceThreads + threadIdx.x; i < last; i += p.ctas * kPlaceThreads) {
@@ -1039,8 +1039,9 @@ w8a8_status cuda_error(const char *what, cudaError_t e)
 }
 
 // How a sort is cut.  `units` of work (tokens, or 32 numbers) are dealt to CTAs, and to
-// their warps, in equal runs: up to one cluster of eight CTAs while a warp's run is at
-// most `deep` units (one launch), else to as many clusters as a GB300 holds at once (four of
+// their warps, in equal runs: up to one cluster of sixteen CTAs while a warp's run is at
+// most `deep` units (one launch; 512 tokens of 256 experts 12.0 us with sixteen, 16.6 with
+// eight of twice the run; 768 in one launch of longer runs 14.6, in two 13.2), else to as many clusters as a GB300 holds at once (four of
 // 8 CTAs, two to an SM, in each of eight parts; 38, which fill its 152 SMs in number, ran in
 // two waves: 16384 tokens 56 us), or more where a CTA's run would not fit its shared memory.
 struct Cut {
@@ -1060,15 +1061,15 @@ Cut cut(long long units, int deep, int per_warp)
         c.ctas = c.cluster;
         c.clusters = 1;
     } else {
-        const long long most = static_cast<long long>(kMaxCluster) * kWarps * per_warp;
-        c.cluster = kMaxCluster;
+        const long long most = static_cast<long long>(kCluster) * kWarps * per_warp;
+        c.cluster = kCluster;
         c.clusters = static_cast<int>(std::max<long long>(kAtOnce, (units + most - 1) / most));
-        c.ctas = c.clusters * kMaxCluster;
+        c.ctas = c.clusters * kCluster;
     }
     c.most = static_cast<int>((units + c.ctas - 1) / c.ctas);
     return c;
 }
-constexpr int kRouteDeep = 4, kGroupDeep = 16;
+constexpr int kRouteDeep = 2, kGroupDeep = 8;
 // (A CTA's numbers take at most 64 and 128 KB.)
 Cut route_cut(long long T, int k) { return cut(T, kRouteDeep, 1024 / k); }
 Cut group_cut(long long n) { return cut((n + 31) / 32, kGroupDeep, 64); }
@@ -1086,6 +1087,10 @@ cudaError_t launch(void (*kernel)(Params), const Params &p, int ctas, int cluste
 {
     if (smem > 48 * 1024)
         if (const cudaError_t e = ensure_smem_limit(kernel, smem_set); e != cudaSuccess)
+            return e;
+    if (cluster > 8)                // more than every device has
+        if (const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            e != cudaSuccess)
             return e;
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3(ctas, 1, 1);
