@@ -979,6 +979,12 @@ __global__ void __launch_bounds__(kPlaceThreads) k_place(const PlaceParams p)
     __syncthreads();
     grid_dependency_wait();
     grid_launch_dependents();
+    // the first number, fetched while the counts are
+    const long long first = piece(p.units, p.first_ctas, cluster * kCluster) * p.per_unit + slice * kPlaceThreads + threadIdx.x;
+    const long long last = min(p.out.n, piece(p.units, p.first_ctas, (cluster + 1) * kCluster) * p.per_unit);
+    int id = 0, rank = 0;
+    if (first < last)
+        id = p.ids[first], rank = p.out.rank[first];
     // Bins side by side in a warp, the clusters dealt to slices of the block.
     const int width = (bins + 31) / 32 * 32, slices = max(1, kPlaceThreads / width);
     const int mine = threadIdx.x / width;
@@ -1016,13 +1022,11 @@ __global__ void __launch_bounds__(kPlaceThreads) k_place(const PlaceParams p)
             run += t[i];
         }
     __syncthreads();
-    const int ctas = kCluster;
-    const long long first = piece(p.units, p.first_ctas, cluster * ctas) * p.per_unit;
-    const long long last = min(p.out.n, piece(p.units, p.first_ctas, (cluster + 1) * ctas) * p.per_unit);
-    for (long long i = first + slice * kPlaceThreads + threadIdx.x; i < last; i += p.ctas * kPlaceThreads) {
-        const int id = p.ids[i];
+    for (long long i = first; i < last; i += p.ctas * kPlaceThreads) {
+        if (i > first)
+            id = p.ids[i], rank = p.out.rank[i];
         const int bin = static_cast<uint32_t>(id) < static_cast<uint32_t>(groups) ? id : groups;
-        const int place = p.out.rank[i] + before[bin];
+        const int place = rank + before[bin];
         p.out.order[place] = static_cast<int>(i);
         if (p.out.rows)
             p.out.rows[i] = bin < groups ? place : -1;
