@@ -133,22 +133,25 @@ __device__ __forceinline__ void place_pairs(const GroupSmem &s, const GroupOut &
             const int b = b0 + i;
             if (i >= q || b >= bins)
                 continue;
-            int v[kMaxCluster] = {};
-#pragma unroll
-            for (uint32_t half = 0; half < kMaxCluster; half += kCluster)
-                if (half < ctas)
-#pragma unroll
-                    for (uint32_t r = half; r < half + kCluster; ++r)
-                        if (r < ctas)
-                            asm volatile("ld.shared::cluster.s32 %0, [%1];"
-                                         : "=r"(v[r])
-                                         : "r"(cluster_map(smem_addr(s.tot + b), r))
-                                         : "memory");
             total[i] = 0;
+            // (eight at a time: all sixteen at once 64 tokens 6.4 us, not 6.3, and 256 9.4, not 9.5)
+#pragma unroll 1
+            for (uint32_t r0 = 0; r0 < ctas; r0 += kCluster) {
+                int v[kCluster];
 #pragma unroll
-            for (uint32_t r = 0; r < kMaxCluster; ++r) {
-                before[i] += r < me ? v[r] : 0;
-                total[i] += v[r];
+                for (uint32_t r = 0; r < kCluster; ++r) {
+                    v[r] = 0;
+                    if (r0 + r < ctas)
+                        asm volatile("ld.shared::cluster.s32 %0, [%1];"
+                                     : "=r"(v[r])
+                                     : "r"(cluster_map(smem_addr(s.tot + b), r0 + r))
+                                     : "memory");
+                }
+#pragma unroll
+                for (uint32_t r = 0; r < kCluster; ++r) {
+                    before[i] += r0 + r < me ? v[r] : 0;
+                    total[i] += v[r];
+                }
             }
         }
     }
