@@ -6,8 +6,8 @@
 // Sums over the warps of a CTA, then (through distributed shared memory) over the
 // CTAs of the cluster turn these ranks into places.  Where one cluster holds all
 // numbers, that is the whole sort, in one launch; else each cluster's counts go to a
-// workspace and a second launch adds what the earlier clusters hold.  No atomics:
-// the result is the same on every run.
+// workspace and a second launch adds what the earlier clusters hold.  No atomics but
+// of whole numbers: the result is the same on every run.
 #pragma once
 
 #include "ptx.cuh"

@@ -26,7 +26,7 @@
 //
 // Instructions and latency bound it: 16384 tokens of 256 experts in fp32, 8 of 8 runs' 4, sigmoid and
 // bias, 33 us, of which the placing of the pairs in a second launch is 5; 1000 instructions a
-// token, 53 % of the issue slots.  One token 5.5 us, 64 6.3, 1013 of 160 experts 13.7.
+// token, 53 % of the issue slots.  One token 5.7 us, 64 6.3, 1013 of 160 experts 13.8.
 #include <algorithm>
 #include <cstdio>
 
