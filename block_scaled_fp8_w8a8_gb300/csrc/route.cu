@@ -20,9 +20,12 @@
 // error: the replaced bits, and where a bias makes the scores themselves be compared
 // (without one their order is the logits', which are compared instead) their rounding,
 // bounded below (`bound`).  Where two neighbours of the chosen order are nearer than
-// that, those that are too near are scored and ranked again as pairs of fp32 (refine), and so
-// are the runs where the worst kept and the best dropped one are (near_groups); what pairs do
-// not tell is chosen in fp64 after all tokens (choose_exact).
+// that, the last choice and the best expert that stays behind among them, the choices and that
+// expert are scored and ranked again as pairs of fp32 (refine), and so are the runs where the worst
+// kept and the best dropped one are (near_groups).  Experts whose keys agree stand in any order, so the
+// last choice is also compared with the key behind that expert, which bounds all the others;
+// where that is as near, or pairs do not tell, the token is chosen in fp64 after all tokens
+// (choose_exact).
 //
 // Instructions and latency bound it: 16384 tokens of 256 experts in fp32, 8 of 8 runs' 4, sigmoid and
 // bias, 33 us, of which the placing of the pairs in a second launch is 5; 1000 instructions a
@@ -698,8 +701,9 @@ template <int PER> __device__ __forceinline__ uint32_t take_best(uint32_t (&key)
     return top;
 }
 
-// Whether key a is not surely above key b: they differ by no more than `by` and `at` times
-// their sizes.  (Without a bias, by and at 0: sure where the kept bits differ.)
+// Whether key a is not surely above key b, and so above whatever has b's kept bits or less: they
+// differ by no more than `by` and `at` times their sizes, which is the errors of both scores and the bits
+// that the keys lack.  (Without a bias, by and at 0: sure where the kept bits differ.)
 template <int PER> struct Near {
     float by, at;
     __device__ __forceinline__ Near(bool biased, float bound)
@@ -831,6 +835,9 @@ template <int KIND, int PER> __global__ void __launch_bounds__(kThreads, PER <= 
                     near = !(hi - lo > 2.f * of.z + 0x1p-23f * (fabsf(hi) + fabsf(lo)));
                     // equal logits under equal biases are equal scores, in order of their index
                     near = near && !(x == y && r.bias[id] == r.bias[other] && id < other && choice + 1 < p.k);
+                    // what is behind that one has a key that is no larger, but may have a larger score: the
+                    // last choice has to be surely above it too
+                    near = near || (choice + 1 == p.k && Near<PER>(true, of.z)(got.x, __float_as_uint(of.w)));
                 } else if (near) {
                     near = got.x == below.x;            // (the kept bits)
                     near = near && !(x == load_logit<KIND>(row, other) && id < other && choice + 1 < p.k);
