@@ -524,7 +524,8 @@ extern "C" w8a8_status w8a8_adapter_matmul(const void *x_dev, w8a8_in_dtype dtyp
         return W8A8_OK;
     if (!base_dev || !out_dev || !order_dev || !offsets_dev)
         return record_error(W8A8_ERR_INVALID_ARG, "null pointer argument");
-    if (L > 0 && r > 0 && K > 0 && (!x_dev || !A_dev || !B_dev))
+    // (B does not depend on K, and is read where x and A have no columns too)
+    if (L > 0 && r > 0 && (!B_dev || (K > 0 && (!x_dev || !A_dev))))
         return record_error(W8A8_ERR_INVALID_ARG, "null pointer argument");
     if (L > W8A8_GROUPS_MAX || r > W8A8_ADAPTER_MAX_R || T >= (1ll << 28) || K > (1ll << 24) || N > (1ll << 24))
         return record_error(W8A8_ERR_UNSUPPORTED, "L above W8A8_GROUPS_MAX, r above W8A8_ADAPTER_MAX_R, T of 2^28 or "

@@ -648,7 +648,8 @@ w8a8_status w8a8_combine_experts(const void *Y_dev, w8a8_in_dtype y_dtype, int64
  * decrease or leave [0, T] give unspecified results but no out-of-bounds access.
  * L <= W8A8_GROUPS_MAX, r <= W8A8_ADAPTER_MAX_R; any K and N up to 2^24, strides and
  * alignments (pieces of 16 bytes where K % 8 == 0, r % 8 == 0 and the rows allow).
- * T == 0 or N == 0 is a no-op.  variant (w8a8_variant): AUTO; SMALLM, one launch of
+ * T == 0 or N == 0 is a no-op; without adapters (L or r 0) x, A and B may be NULL, with
+ * K == 0 x and A.  variant (w8a8_variant): AUTO; SMALLM, one launch of
  * clusters on 16 rows each; TILED, two launches of 128-row tiles on the tensor cores' tcgen05
  * path (r % 8 == 0 from 8 to 128, K % 8 == 0 from 64 on, N % 8 == 0, rows on 16-byte
  * boundaries, L > 0).  The launches wait on the device for the work before them on the stream.

@@ -220,3 +220,14 @@ def test_tensors_off_the_gpu_do_not_reach_the_library(name, reached):
         with pytest.raises(w8.W8A8Error, match="one CUDA device, not on cpu"):
             getattr(w8, name)(**given)
         assert not [h for h in reached if len(h) > 3]
+
+
+# ---------------------------------------------------------------- operands of sizes that are zero
+
+
+@pytest.mark.parametrize("kw", [dict(K=0, B=0), dict(K=0, B=0, x=0, A=0), dict(K=0, B=0, N=1), dict(K=0, B=0, out_dtype=2),
+                                dict(K=0, B=0, T=5000, r=64)])
+def test_adapters_without_columns_of_x_still_read_b(kw):
+    """B [L, N, r] does not depend on K: it is read where there are adapters of some rank."""
+    assert adapters(**kw) == ARG
+    assert "null pointer" in w8.w8a8_last_error()
