@@ -46,11 +46,13 @@ constexpr int kChunk = 64;          // rows of A whose sums a warp holds at once
 constexpr int kRows = 16;           // of an item
 constexpr int kMaxCluster = 16;     // CTAs (more than 8 where that is allowed, see launch_few)
 
-// Eight elements of a row at k, zeros past its end (row null: zeros).
-__device__ __forceinline__ uint4 load8(const uint16_t *row, int k, int K, bool vec)
+// Eight elements of a row of `of` at k, zeros past its end (row null: zeros).
+__device__ __forceinline__ uint4 load8(const Buffer &of, const uint16_t *row, int k, int K, bool vec)
 {
     uint4 v = make_uint4(0, 0, 0, 0);
     if (!row || k >= K)
+        return v;
+    if (!of.holds(row + k, 2 * (vec ? 8 : min(8, K - k))))
         return v;
     if (vec)
         return *reinterpret_cast<const uint4 *>(row + k);
@@ -116,13 +118,14 @@ template <int TERMS> struct FewSmem {
 };
 
 // Starts fetching into L2 (16-byte boundaries; of long ranges the first megabyte).
-__device__ __forceinline__ void prefetch_l2(const void *p, size_t bytes)
+__device__ __forceinline__ void prefetch_l2(const Buffer &of, const void *p, size_t bytes)
 {
     const uint32_t n = static_cast<uint32_t>(min(bytes, static_cast<size_t>(1) << 20));
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(n) : "memory");
+    if (of.holds(p, bytes))
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(n) : "memory");
 }
 
-// Eight neighbouring elements of a row of base or out, as fp32; `in` of them.
+// Eight neighbouring elements of a row of base or out, as fp32.
 template <int OUT> struct Eight {
     uint4 w[OUT == W8A8_OUT_FP32 ? 2 : 1];
     __device__ __forceinline__ void load(const void *base, long long i)
@@ -182,10 +185,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_adapter_few(const AdapterParams
     if (item.rows == 0 || !in_bounds(item.first >= 0 && item.first + item.rows <= p.T && item.adapter <= p.L, p.status,
                                      SITE_BOUNDS_A))
         return;                             // the whole cluster
-    auto row_at = [&](int i) {
-        const int row = i < item.rows ? p.order[item.first + i] : -1;
-        return static_cast<unsigned>(row) < static_cast<unsigned>(p.T) ? row : -1;
-    };
+    auto row_at = [&](int i) { return i < item.rows ? row_in_place(p, item.first + i) : -1; };
+    const Buffer x_all = x_of(p), a_all = a_of(p), b_all = b_of(p), base_all = base_of(p, kElement), out_all = out_of(p, kElement);
     const int n_blocks = (p.N + 31) / 32;
     const int block_lo = static_cast<int>(static_cast<long long>(n_blocks) * me / ctas);
     const int block_hi = static_cast<int>(static_cast<long long>(n_blocks) * (me + 1) / ctas);
@@ -210,10 +211,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_adapter_few(const AdapterParams
     const uint16_t *const A = p.A + static_cast<long long>(item.adapter) * p.r * p.K;
     const uint16_t *const B = p.B + static_cast<long long>(item.adapter) * p.N * p.r;
     if (slot == kRows && p.vec_r && n_hi > n_lo && p.r)
-        prefetch_l2(B + static_cast<long long>(n_lo) * p.r, static_cast<size_t>(n_hi - n_lo) * p.r * 2);
+        prefetch_l2(b_all, B + static_cast<long long>(n_lo) * p.r, static_cast<size_t>(n_hi - n_lo) * p.r * 2);
     if (slot >= 0 && slot < kRows && p.vec_n && n_hi > n_lo)
         if (const int row = rows[slot]; row >= 0)
-            prefetch_l2(static_cast<const char *>(p.base) + (row * p.ld_base + n_lo) * kElement,
+            prefetch_l2(base_all, static_cast<const char *>(p.base) + (row * p.ld_base + n_lo) * kElement,
                         static_cast<size_t>(n_hi - n_lo) * kElement);
     __syncwarp();
 
@@ -239,11 +240,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_adapter_few(const AdapterParams
                 for (int j = 0; j < 8; ++j) {
                     const int r = r0 + 8 * j + g;
                     if (j < tiles)
-                        a[j] = load8(r < p.r ? A + static_cast<long long>(r) * p.K : nullptr, k, p.K, p.vec_k);
+                        a[j] = load8(a_all, r < p.r ? A + static_cast<long long>(r) * p.K : nullptr, k, p.K, p.vec_k);
                 }
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                    xv[i] = load8(token[i], k, p.K, p.vec_k);
+                    xv[i] = load8(x_all, token[i], k, p.K, p.vec_k);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     if (j < tiles) {
@@ -283,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_adapter_few(const AdapterParams
             asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
         cluster_sync();
     }
-    const float scale = p.scales ? p.scales[item.adapter] : 1.f;
+    const float scale = scale_of(p, item.adapter);
     for (int i = threadIdx.x; i < item.rows * (r32 / 4); i += kThreads) {
         const int row = i / (r32 / 4), r = (i - row * (r32 / 4)) * 4;
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -349,7 +350,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_adapter_few(const AdapterParams
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             to[i] = rows[8 * i + g];
-            if (whole && to[i] >= 0)
+            if (whole && to[i] >= 0 &&
+                base_all.holds(static_cast<const char *>(p.base) + (to[i] * p.ld_base + n0 + 8 * c) * kElement, 8 * kElement))
                 old[i].load(p.base, to[i] * p.ld_base + n0 + 8 * c);
         }
         const uint16_t *b_row[4];
@@ -364,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_adapter_few(const AdapterParams
             uint4 b[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                b[j] = load8(b_row[j], 16 * s + 8 * c, p.r, p.vec_r);
+                b[j] = load8(b_all, b_row[j], 16 * s + 8 * c, p.r, p.vec_r);
 #pragma unroll
             for (int half = 0; half < 2; ++half)
 #pragma unroll
@@ -388,18 +390,21 @@ __global__ void __launch_bounds__(kThreads, 2) k_adapter_few(const AdapterParams
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     v[j] = fmaf(acc[j >> 1][2 * i + (j & 1)], f, old[i].at(j));
-                old[i].store(p.out, at_out + 8 * c, v);
+                if (out_all.holds(static_cast<const char *>(p.out) + (at_out + 8 * c) * kElement, 8 * kElement))
+                    old[i].store(p.out, at_out + 8 * c, v);
             } else {
                 float v[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int n = 8 * (j >> 1) + 2 * c + (j & 1);
-                    v[j] = n0 + n < p.N ? load_out<OUT>(p.base, at_base + n) : 0.f;
+                    const bool in = n0 + n < p.N &&
+                                    base_all.holds(static_cast<const char *>(p.base) + (at_base + n) * kElement, kElement);
+                    v[j] = in ? load_out<OUT>(p.base, at_base + n) : 0.f;
                 }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int n = 8 * (j >> 1) + 2 * c + (j & 1);
-                    if (n0 + n < p.N)
+                    if (n0 + n < p.N && out_all.holds(static_cast<const char *>(p.out) + (at_out + n) * kElement, kElement))
                         store_out<OUT>(p.out, at_out + n, fmaf(acc[j >> 1][2 * i + (j & 1)], f, v[j]));
                 }
             }

@@ -28,6 +28,48 @@ struct AdapterParams {
     int vec_n;                  // eight columns of base and out at a time, by 16 bytes
 };
 
+// (debug-bounds build: whether an access lies in its buffer)
+struct Buffer {
+    const void *base;
+    size_t size;
+    unsigned *status;
+    uint32_t site;
+    __device__ __forceinline__ bool holds(const void *at, size_t bytes) const
+    {
+        return in_bounds(inside(at, bytes, base, size), status, site);
+    }
+};
+__device__ __forceinline__ Buffer x_of(const AdapterParams &p)
+{
+    return {p.x, span(p.T, p.ld_x, p.K, 2), p.status, SITE_BOUNDS_A};
+}
+__device__ __forceinline__ Buffer a_of(const AdapterParams &p)
+{
+    return {p.A, span(static_cast<long long>(p.L) * p.r, p.K, p.K, 2), p.status, SITE_BOUNDS_B};
+}
+__device__ __forceinline__ Buffer b_of(const AdapterParams &p)
+{
+    return {p.B, span(static_cast<long long>(p.L) * p.N, p.r, p.r, 2), p.status, SITE_BOUNDS_B};
+}
+__device__ __forceinline__ Buffer base_of(const AdapterParams &p, int element)
+{
+    return {p.base, span(p.T, p.ld_base, p.N, element), p.status, SITE_BOUNDS_C};
+}
+__device__ __forceinline__ Buffer out_of(const AdapterParams &p, int element)
+{
+    return {p.out, span(p.T, p.ld_out, p.N, element), p.status, SITE_BOUNDS_C};
+}
+// The row in a place of the sort, -1 for one that is none.
+__device__ __forceinline__ int row_in_place(const AdapterParams &p, int place)
+{
+    const int row = in_bounds(place >= 0 && place < p.T, p.status, SITE_BOUNDS_A) ? p.order[place] : -1;
+    return static_cast<unsigned>(row) < static_cast<unsigned>(p.T) ? row : -1;
+}
+__device__ __forceinline__ float scale_of(const AdapterParams &p, int adapter)
+{
+    return p.scales && in_bounds(adapter >= 0 && adapter < p.L, p.status, SITE_BOUNDS_SCALES) ? p.scales[adapter] : 1.f;
+}
+
 // The power of two that brings a row of h, whose largest size is top, near 2^14: the
 // factor that does, and the one that its sums are multiplied by afterwards.
 __device__ __forceinline__ void power_of(float top, float *shrink, float *factor)
@@ -50,7 +92,9 @@ __device__ __forceinline__ Item find_item(const AdapterParams &p, int index, int
     // scratch: [12] sums of warps, then the item
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const int q = (groups + THREADS - 1) / THREADS, from = min(t * q, groups), to = min(from + q, groups);
-    auto offset = [&](int g) { return g > p.L ? p.T : min(max(p.offsets[g], 0), p.T); };
+    auto offset = [&](int g) {
+        return g > p.L || !in_bounds(g >= 0, p.status, SITE_BOUNDS_B) ? p.T : min(max(p.offsets[g], 0), p.T);
+    };
     int sum = 0;
     for (int g = from; g < to; ++g)
         sum += (max(offset(g + 1) - offset(g), 0) + tile - 1) / tile;
@@ -121,14 +165,17 @@ __device__ __forceinline__ void copy_rows(const AdapterParams &p, const int *row
             if (i < all) {
                 const int r = static_cast<int>(i / pieces), n = from + static_cast<int>(i - static_cast<long long>(r) * pieces) * each;
                 if (const int row = rows[r]; row >= 0) {
+                    const char *const from_at = static_cast<const char *>(p.base) + (row * p.ld_base + n) * element;
+                    if (!base_of(p, element).holds(from_at, sizeof(WORD)))
+                        continue;
                     at[j] = (row * p.ld_out + n) * element;
-                    v[j] = *reinterpret_cast<const WORD *>(static_cast<const char *>(p.base) + (row * p.ld_base + n) * element);
+                    v[j] = *reinterpret_cast<const WORD *>(from_at);
                 }
             }
         }
 #pragma unroll
         for (int j = 0; j < kFlight; ++j)
-            if (at[j] >= 0)
+            if (at[j] >= 0 && out_of(p, element).holds(static_cast<char *>(p.out) + at[j], sizeof(WORD)))
                 *reinterpret_cast<WORD *>(static_cast<char *>(p.out) + at[j]) = v[j];
     }
 }

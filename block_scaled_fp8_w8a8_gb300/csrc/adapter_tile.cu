@@ -36,6 +36,12 @@ template <bool BF16> __device__ __forceinline__ uint32_t idesc(uint32_t n)
     return idesc_f16_f32(128, n) | (BF16 ? (1u << 7) | (1u << 10) : 0u);
 }
 
+// (debug-bounds build)
+__device__ __forceinline__ Buffer h_of(const TileParams &p)
+{
+    return {p.h, span(static_cast<long long>(p.splits) * p.a.T, p.a.r_pad, p.a.r_pad, 4), p.a.status, SITE_BOUNDS_WORKSPACE};
+}
+
 // Offset of 16-byte piece c of row r in a tile with the 128-byte swizzle.
 __device__ __forceinline__ uint32_t swizzled(uint32_t r, uint32_t c) { return r * kRowBytes + ((c ^ (r & 7u)) << 4); }
 
@@ -64,8 +70,13 @@ struct RowLoads {
             row[0] = first;
     }
     __device__ __forceinline__ void operator()(uint32_t dst, const CUtensorMap *one, const CUtensorMap *boxes, uint32_t bar,
-                                               int x) const
+                                               int x, int cols, int T, unsigned *status, uint32_t site) const
     {
+        const bool rows_in = box ? row[0] >= 0 && row[0] < T
+                                 : min(min(row[0], row[1]), min(row[2], row[3])) >= 0 &&
+                                       max(max(row[0], row[1]), max(row[2], row[3])) <= T;
+        if (any && !in_bounds(rows_in && x >= 0 && x < cols, status, site))
+            return;
         if (box && any)
             tma_load_2d(dst + lane * 4 * kRowBytes, boxes, bar, x, row[0]);
         else if (any)
@@ -135,8 +146,7 @@ template <bool BF16, int STAGES> __global__ void __launch_bounds__(kShrinkThread
     const int tile = blockIdx.x / p.splits, split = blockIdx.x % p.splits;
     const Item item = find_item<kShrinkThreads>(p.a, tile, kTileRows, p.a.L, scratch);
     if (t < kTileRows) {
-        const int row = static_cast<int>(t) < item.rows ? p.a.order[item.first + t] : -1;
-        rows[t] = static_cast<unsigned>(row) < static_cast<unsigned>(p.a.T) ? row : -1;
+        rows[t] = static_cast<int>(t) < item.rows ? row_in_place(p.a, item.first + static_cast<int>(t)) : -1;
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -152,7 +162,7 @@ template <bool BF16, int STAGES> __global__ void __launch_bounds__(kShrinkThread
         // h of this part of K
         if (__all_sync(0xffffffffu, wait_bounded(done, 0, guard, SITE_TILED_PROMOTE))) {
             tc_fence_after_sync();
-            const float scale = p.a.scales ? p.a.scales[item.adapter] : 1.f;
+            const float scale = scale_of(p.a, item.adapter);
             float *const h = p.h + (static_cast<long long>(split) * p.a.T + item.first + t) * p.a.r_pad;
             for (int j = 0; j < p.a.r_pad; j += 32) {
                 float v[32];
@@ -160,7 +170,7 @@ template <bool BF16, int STAGES> __global__ void __launch_bounds__(kShrinkThread
                 tmem_load_32cols(tmem + ((warp * 32u) << 16) + j, v);
 #pragma unroll
                 for (int i = 0; i < 32; i += 4)
-                    if (static_cast<int>(t) < item.rows && j + i < p.a.r_pad)
+                    if (static_cast<int>(t) < item.rows && j + i < p.a.r_pad && h_of(p).holds(h + j + i, 16))
                         *reinterpret_cast<float4 *>(h + j + i) =
                             make_float4(v[i] * scale, v[i + 1] * scale, v[i + 2] * scale, v[i + 3] * scale);
             }
@@ -199,10 +209,11 @@ template <bool BF16, int STAGES> __global__ void __launch_bounds__(kShrinkThread
             const int k = (lo + i) * 64;
             if (lane == 0) {
                 mbar_arrive_expect_tx(bar, stage_bytes);
-                tma_load_3d(dst + kTileBytes, &map_a, bar, k, 0, item.adapter);
+                if (in_bounds(k >= 0 && k < p.a.K && item.adapter >= 0 && item.adapter < p.a.L, p.a.status, SITE_BOUNDS_B))
+                    tma_load_3d(dst + kTileBytes, &map_a, bar, k, 0, item.adapter);
             }
             __syncwarp();
-            load(dst, &map_x, &map_x32, bar, k);
+            load(dst, &map_x, &map_x32, bar, k, p.a.K, p.a.T, p.a.status, SITE_BOUNDS_A);
         }
         if (i < steps)
             drain_loads<STAGES>(full, i, p.a.status, p.a.wait_limit);
@@ -276,8 +287,7 @@ __global__ void __launch_bounds__(kExpandThreads) k_adapter_expand(
     const int tile = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
     const Item item = find_item<kExpandThreads>(p.a, tile, kTileRows, p.a.out == p.a.base ? p.a.L : p.a.L + 1, scratch);
     if (t < kTileRows) {
-        const int row = static_cast<int>(t) < item.rows ? p.a.order[item.first + t] : -1;
-        rows[t] = static_cast<unsigned>(row) < static_cast<unsigned>(p.a.T) ? row : -1;
+        rows[t] = static_cast<int>(t) < item.rows ? row_in_place(p.a, item.first + static_cast<int>(t)) : -1;
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -305,10 +315,12 @@ __global__ void __launch_bounds__(kExpandThreads) k_adapter_expand(
             if (lane == 0) {
                 mbar_arrive_expect_tx(bar, stage_bytes);
                 for (int q = 0; q < k_blocks; ++q)
-                    tma_load_3d(dst + q * X::kBBytes, &map_b, bar, 64 * q, n0, item.adapter);
+                    if (in_bounds(n0 >= 0 && n0 < p.a.N && 64 * q < p.a.r && item.adapter >= 0 && item.adapter < p.a.L,
+                                  p.a.status, SITE_BOUNDS_B))
+                        tma_load_3d(dst + q * X::kBBytes, &map_b, bar, 64 * q, n0, item.adapter);
             }
             __syncwarp();
-            load(dst + base_at, &map_base, &map_base32, bar, n0);
+            load(dst + base_at, &map_base, &map_base32, bar, n0, p.a.N, p.a.T, p.a.status, SITE_BOUNDS_C);
         }
         if (i < steps)
             drain_loads<STAGES>(full, i, p.a.status, p.a.wait_limit);
@@ -332,8 +344,9 @@ __global__ void __launch_bounds__(kExpandThreads) k_adapter_expand(
                 float4 a[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    a[i] = i < 4 || k + 16 < p.a.r_pad ? *reinterpret_cast<const float4 *>(h + s * plane + k + 4 * i)
-                                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+                    a[i] = (i < 4 || k + 16 < p.a.r_pad) && h_of(p).holds(h + s * plane + k + 4 * i, 16)
+                               ? *reinterpret_cast<const float4 *>(h + s * plane + k + 4 * i)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     v[4 * i] += a[i].x, v[4 * i + 1] += a[i].y, v[4 * i + 2] += a[i].z, v[4 * i + 3] += a[i].w;
@@ -428,7 +441,7 @@ __global__ void __launch_bounds__(kExpandThreads) k_adapter_expand(
                 for (int j = 0; j < 8; ++j) {
                     const uint32_t r = e * 32 + (lane >> 3) + 4 * j;
                     const int to = rows[r];
-                    if (to >= 0)
+                    if (to >= 0 && out_of(p.a, kOut).holds(out + (to * p.a.ld_out + col) * kOut, 16))
                         *reinterpret_cast<uint4 *>(out + (to * p.a.ld_out + col) * kOut) =
                             *reinterpret_cast<const uint4 *>(tile_rows + swizzled(r, c));
                 }

@@ -30,7 +30,31 @@ struct CombineParams {
     int k, D;
     int chunks;                 // pieces of a token's row
     long long pieces;           // of all
+    long long T;
+    unsigned *status;
 };
+
+// (debug-bounds build: whether an access lies in its buffer)
+__device__ __forceinline__ bool is_choice(const CombineParams &p, long long t, int j)
+{
+    return in_bounds(t >= 0 && t < p.T && j >= 0 && j < p.k, p.status, SITE_BOUNDS_SCALES);
+}
+template <int KIND> __device__ __forceinline__ bool is_y(const CombineParams &p, const void *at, int bytes)
+{
+    return in_bounds(inside(at, bytes, p.Y, span(p.M, p.ld_y, p.D, KIND == W8A8_IN_FP32 ? 4 : 2)), p.status, SITE_BOUNDS_A);
+}
+template <int OUT> __device__ __forceinline__ bool is_add(const CombineParams &p, long long element, int count)
+{
+    constexpr int kBytes = OUT == W8A8_IN_FP32 ? 4 : 2;
+    return in_bounds(inside(static_cast<const char *>(p.add) + element * kBytes, count * kBytes, p.add,
+                            span(p.T, p.ld_add, p.D, kBytes)), p.status, SITE_BOUNDS_B);
+}
+template <int OUT> __device__ __forceinline__ bool is_out(const CombineParams &p, long long element, int count)
+{
+    constexpr int kBytes = OUT == W8A8_IN_FP32 ? 4 : 2;
+    return in_bounds(inside(static_cast<const char *>(p.out) + element * kBytes, count * kBytes, p.out,
+                            span(p.T, p.ld_out, p.D, kBytes)), p.status, SITE_BOUNDS_C);
+}
 
 constexpr int kThreads = 128;
 constexpr int kVec = 8;                     // columns of a thread
@@ -106,7 +130,7 @@ template <int KIND> struct Raw {
 template <int KIND, int OUT, bool WARPS, int UNITS>
 __global__ void __launch_bounds__(kThreads) k_combine(const CombineParams p)
 {
-    constexpr int kDeep = 8 / UNITS;
+    constexpr int kDeep = 8 / UNITS, kBytes = KIND == W8A8_IN_FP32 ? 4 : 2;
     Piece at[UNITS];
     find_pieces<WARPS>(p, at);
     bool mine[UNITS];
@@ -123,7 +147,7 @@ __global__ void __launch_bounds__(kThreads) k_combine(const CombineParams p)
     Raw<OUT> plus[UNITS];
 #pragma unroll
     for (int u = 0; u < UNITS; ++u)
-        if (p.add && mine[u])
+        if (p.add && mine[u] && is_add<OUT>(p, at[u].t * p.ld_add + at[u].col, kVec))
             plus[u].load(p.add, at[u].t * p.ld_add + at[u].col);
     for (int j0 = 0; j0 < p.k; j0 += kDeep) {
         Raw<KIND> y[UNITS][kDeep];
@@ -135,8 +159,9 @@ __global__ void __launch_bounds__(kThreads) k_combine(const CombineParams p)
             const float *const weights = p.weights + at[u].t * p.k + j0;
 #pragma unroll
             for (int j = 0; j < kDeep; ++j) {
-                const long long row = mine[u] && j0 + j < p.k ? rows[j] : -1;
-                in[u][j] = row >= 0 && row < p.M;
+                const long long row = mine[u] && j0 + j < p.k && is_choice(p, at[u].t, j0 + j) ? rows[j] : -1;
+                in[u][j] = row >= 0 && row < p.M &&
+                           is_y<KIND>(p, static_cast<const char *>(p.Y) + (row * p.ld_y + at[u].col) * kBytes, kVec * kBytes);
                 w[u][j] = in[u][j] ? weights[j] : 0.f;
                 if (in[u][j])
                     y[u][j].load(p.Y, row * p.ld_y + at[u].col);
@@ -163,7 +188,8 @@ __global__ void __launch_bounds__(kThreads) k_combine(const CombineParams p)
         }
         Raw<OUT> o;
         o.set(acc[u]);
-        o.store(p.out, at[u].t * p.ld_out + at[u].col);
+        if (is_out<OUT>(p, at[u].t * p.ld_out + at[u].col, kVec))
+            o.store(p.out, at[u].t * p.ld_out + at[u].col);
     }
 }
 
@@ -190,30 +216,30 @@ template <int KIND> struct Words {
     uint32_t shift;                                     // in bits
     // columns from p on, of which `left` are in the row (FULL: all); whole: words may be loaded
     // that reach an element out of it
-    template <bool FULL> __device__ __forceinline__ void load(const char *p, int left, bool whole)
+    template <bool FULL> __device__ __forceinline__ void load(const CombineParams &c, const char *p, int left, bool whole)
     {
         shift = 0;
         if constexpr (kFp32) {
 #pragma unroll
             for (int i = 0; i < kEach; ++i)
-                if (FULL || column(i) < left)
+                if ((FULL || column(i) < left) && is_y<KIND>(c, p + 128 * i + 4 * lane_index(), 4))
                     w[i] = *reinterpret_cast<const uint32_t *>(p + 128 * i + 4 * lane_index());
         } else if (whole) {
             shift = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 2) * 8;
             const uint32_t *const word = reinterpret_cast<const uint32_t *>(p - shift / 8) + lane_index();
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
-                if (FULL || column(2 * i) < left)
+                if ((FULL || column(2 * i) < left) && is_y<KIND>(c, word + 32 * i, 4))
                     w[i] = word[32 * i];
-                if (shift && (FULL || column(2 * i + 1) < left))
+                if (shift && (FULL || column(2 * i + 1) < left) && is_y<KIND>(c, word + 32 * i + 1, 4))
                     next[i] = word[32 * i + 1];
             }
         } else {
             const uint16_t *const half = reinterpret_cast<const uint16_t *>(p);
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
-                w[i] = FULL || column(2 * i) < left ? half[column(2 * i)] : 0;
-                if (FULL || column(2 * i + 1) < left)
+                w[i] = (FULL || column(2 * i) < left) && is_y<KIND>(c, half + column(2 * i), 2) ? half[column(2 * i)] : 0;
+                if ((FULL || column(2 * i + 1) < left) && is_y<KIND>(c, half + column(2 * i + 1), 2))
                     w[i] |= static_cast<uint32_t>(half[column(2 * i + 1)]) << 16;
             }
         }
@@ -258,7 +284,8 @@ __device__ __forceinline__ void sum_words(const CombineParams &p, const Piece (&
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
             const int col = at[u].col + In::column(i);
-            plus[u][i] = p.add && (FULL || (at[u].in && col < p.D)) ? element<OUT>(p.add, at[u].t * p.ld_add + col) : 0.f;
+            plus[u][i] = p.add && (FULL || (at[u].in && col < p.D)) && is_add<OUT>(p, at[u].t * p.ld_add + col, 1)
+                             ? element<OUT>(p.add, at[u].t * p.ld_add + col) : 0.f;
         }
     for (int j0 = 0; j0 < p.k; j0 += kDeep) {
         In y[UNITS][kDeep];
@@ -270,11 +297,11 @@ __device__ __forceinline__ void sum_words(const CombineParams &p, const Piece (&
             const float *const weights = p.weights + at[u].t * p.k + j0;
 #pragma unroll
             for (int j = 0; j < kDeep; ++j) {
-                const long long row = (FULL || at[u].in) && j0 + j < p.k ? rows[j] : -1;
+                const long long row = (FULL || at[u].in) && j0 + j < p.k && is_choice(p, at[u].t, j0 + j) ? rows[j] : -1;
                 in[u][j] = row >= 0 && row < p.M;
                 w[u][j] = in[u][j] ? weights[j] : 0.f;
                 if (in[u][j])
-                    y[u][j].template load<FULL>(static_cast<const char *>(p.Y) + (row * p.ld_y + at[u].col) * kBytes, p.D - at[u].col,
+                    y[u][j].template load<FULL>(p, static_cast<const char *>(p.Y) + (row * p.ld_y + at[u].col) * kBytes, p.D - at[u].col,
                                  row > 0 && row < p.M - 1);
             }
         }
@@ -294,6 +321,8 @@ __device__ __forceinline__ void sum_words(const CombineParams &p, const Piece (&
                 continue;
             const long long n = at[u].t * p.ld_out + col;
             const float v = acc[u][i] + plus[u][i];
+            if (!is_out<OUT>(p, n, 1))
+                continue;
             if constexpr (OUT == W8A8_IN_FP32)
                 static_cast<float *>(p.out)[n] = v;
             else if constexpr (OUT == W8A8_IN_BF16)
@@ -403,11 +432,13 @@ extern "C" w8a8_status w8a8_combine_experts(const void *Y_dev, w8a8_in_dtype y_d
     p.ld_y = ld_y;
     p.ld_add = ld_add;
     p.ld_out = ld_out;
+    p.T = T;
     p.k = static_cast<int>(k);
     p.D = static_cast<int>(D);
     DeviceView dev;
     if (const int st = device_view(&dev); st != W8A8_OK)
         return static_cast<w8a8_status>(st);
+    p.status = dev.status;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (y_dtype == W8A8_IN_FP32)

@@ -10,6 +10,7 @@
 // of whole numbers: the result is the same on every run.
 #pragma once
 
+#include "kernels.cuh"
 #include "ptx.cuh"
 
 namespace w8a8 {
@@ -31,7 +32,23 @@ struct GroupOut {
     int *hist;              // [clusters, groups + 1] counts; null: one cluster, one launch
     int groups;
     long long n;
+    long long hist_size;    // of hist, in counts
+    unsigned *status;
 };
+
+// (debug-bounds build)
+__device__ __forceinline__ bool is_number(const GroupOut &g, long long i, uint32_t site)
+{
+    return in_bounds(i >= 0 && i < g.n, g.status, site);
+}
+__device__ __forceinline__ bool is_count(const GroupOut &g, long long i)
+{
+    return in_bounds(i >= 0 && i < g.hist_size, g.status, SITE_BOUNDS_WORKSPACE);
+}
+__device__ __forceinline__ bool is_offset(const GroupOut &g, int b)
+{
+    return in_bounds(b >= 0 && b <= g.groups, g.status, SITE_BOUNDS_C);
+}
 
 // Exclusive scan over the block's threads of one number each; part holds one int per
 // warp.  All threads call it, with a barrier between the writes and reads of part.
@@ -159,7 +176,7 @@ __device__ __forceinline__ void place_pairs(const GroupSmem &s, const GroupOut &
 #pragma unroll
         for (int i = 0; i < kMost; ++i)
             if (i < q && b0 + i < bins) {
-                if (me == 0)
+                if (me == 0 && is_count(g, static_cast<long long>(cluster) * bins + b0 + i))
                     g.hist[static_cast<long long>(cluster) * bins + b0 + i] = total[i];
                 s.first[b0 + i] = before[i];
             }
@@ -168,7 +185,7 @@ __device__ __forceinline__ void place_pairs(const GroupSmem &s, const GroupOut &
 #pragma unroll
         for (int i = 0; i < kMost; ++i)
             if (i < q && b0 + i < bins) {
-                if (me == 0)
+                if (me == 0 && is_offset(g, b0 + i))
                     g.offsets[b0 + i] = run;
                 s.first[b0 + i] = run + before[i];
                 run += total[i];
@@ -181,8 +198,9 @@ __device__ __forceinline__ void place_pairs(const GroupSmem &s, const GroupOut &
         const int place = s.first[b] + s.hist[warp * bins + b] + static_cast<int>(v & 0xffffu);
         const long long p = first_number + i;
         if (g.hist) {
-            g.rank[p] = place;
-        } else {
+            if (is_number(g, p, SITE_BOUNDS_WORKSPACE))
+                g.rank[p] = place;
+        } else if (is_number(g, p, SITE_BOUNDS_C) && is_number(g, place, SITE_BOUNDS_C)) {
             g.order[place] = static_cast<int>(p);
             if (g.rows)
                 g.rows[p] = b < g.groups ? place : -1;

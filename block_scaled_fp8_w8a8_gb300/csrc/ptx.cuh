@@ -102,6 +102,18 @@ __device__ __forceinline__ bool in_bounds(bool ok, unsigned *status, uint32_t si
 #endif
 }
 
+// What a check compares: whether the `bytes` at `at` lie in the `size` bytes from `base` on, and
+// the size of a buffer of rows.
+__device__ __forceinline__ bool inside(const void *at, size_t bytes, const void *base, size_t size)
+{
+    const size_t before = reinterpret_cast<uintptr_t>(at) - reinterpret_cast<uintptr_t>(base);
+    return reinterpret_cast<uintptr_t>(at) >= reinterpret_cast<uintptr_t>(base) && before <= size && bytes <= size - before;
+}
+__device__ __forceinline__ size_t span(long long rows, long long ld, long long cols, int element)
+{
+    return rows > 0 ? static_cast<size_t>((rows - 1) * ld + cols) * element : 0;
+}
+
 // ------------------------------------------------------------------ mbarrier
 
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)

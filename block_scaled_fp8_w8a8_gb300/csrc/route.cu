@@ -179,8 +179,32 @@ __device__ __forceinline__ double inverse64(double d)
     return fma(r, fma(-d, r, 1.), r);
 }
 
-template <int KIND> __device__ __forceinline__ float load_logit(const void *row, int e)
+// (debug-bounds build: whether an access lies in its buffer)
+template <int KIND> __device__ __forceinline__ bool is_logit(const RouteParams &p, const void *at, int bytes)
 {
+    return in_bounds(inside(at, bytes, p.logits, span(p.T, p.ld, p.E, KIND == W8A8_IN_FP32 ? 4 : 2)), p.out.status,
+                     SITE_BOUNDS_A);
+}
+__device__ __forceinline__ bool is_expert(const RouteParams &p, int e)
+{
+    return in_bounds(e >= 0 && e < p.E, p.out.status, SITE_BOUNDS_B);
+}
+__device__ __forceinline__ float bias_of(const RouteParams &p, int e) { return is_expert(p, e) ? p.bias[e] : 0.f; }
+__device__ __forceinline__ bool is_valid(const RouteParams &p, long long token)
+{
+    return !p.valid || (in_bounds(token >= 0 && token < p.T, p.out.status, SITE_BOUNDS_B) && p.valid[token]);
+}
+// (of the numbers that a CTA keeps)
+__device__ __forceinline__ bool is_kept(const RouteParams &p, int i)
+{
+    return in_bounds(i >= 0 && i < p.most * p.k, p.out.status, SITE_BOUNDS_SMEM);
+}
+
+template <int KIND> __device__ __forceinline__ float load_logit(const RouteParams &p, const void *row, int e)
+{
+    constexpr int kBytes = KIND == W8A8_IN_FP32 ? 4 : 2;
+    if (!is_logit<KIND>(p, static_cast<const char *>(row) + e * static_cast<long long>(kBytes), kBytes))
+        return 0.f;
     if constexpr (KIND == W8A8_IN_FP32)
         return static_cast<const float *>(row)[e];
     else if constexpr (KIND == W8A8_IN_BF16)
@@ -200,7 +224,7 @@ __device__ __forceinline__ void load_lane(const RouteParams &p, const void *row,
             for (int i = 0; i < PER; i += kEach) {
                 uint4 w = make_uint4(0, 0, 0, 0);
                 const bool in = e0 + i < p.E;
-                if (in)
+                if (in && is_logit<KIND>(p, static_cast<const char *>(row) + (e0 + i) * (16 / kEach), 16))
                     w = *reinterpret_cast<const uint4 *>(static_cast<const char *>(row) + (e0 + i) * (16 / kEach));
                 const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -222,7 +246,7 @@ __device__ __forceinline__ void load_lane(const RouteParams &p, const void *row,
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-        l[i] = i < p.per && e0 + i < p.E ? load_logit<KIND>(row, e0 + i) : -INFINITY;
+        l[i] = i < p.per && e0 + i < p.E ? load_logit<KIND>(p, row, e0 + i) : -INFINITY;
 }
 
 // Descending order by odd-even merging (K. E. Batcher, "Sorting networks and their
@@ -289,7 +313,7 @@ template <int KIND> __device__ __forceinline__ double softmax_sum(const RoutePar
         double x[kQuad];
 #pragma unroll
         for (int i = 0; i < kQuad; ++i)
-            x[i] = e + 32 * i < p.E ? static_cast<double>(load_logit<KIND>(row, e + 32 * i)) - m : -1000.;
+            x[i] = e + 32 * i < p.E ? static_cast<double>(load_logit<KIND>(p, row, e + 32 * i)) - m : -1000.;
         exp64(x);
 #pragma unroll
         for (int i = 0; i < kQuad; ++i)
@@ -327,7 +351,7 @@ template <int KIND> __device__ __forceinline__ Pair32 softmax_sum_pair(const Rou
         return z;
 #pragma unroll 1
     for (int e = threadIdx.x & 31; e < p.E; e += 32)
-        z = z + exp_pair(two_sum(load_logit<KIND>(row, e), -m));
+        z = z + exp_pair(two_sum(load_logit<KIND>(p, row, e), -m));
 #pragma unroll
     for (int d = 16; d; d /= 2) {
         const float h = __shfl_xor_sync(kAll, z.h, d), l = __shfl_xor_sync(kAll, z.l, d);
@@ -352,17 +376,17 @@ template <int KIND> __device__ __noinline__ int choose_exact(const RouteParams &
     K key[32], ck[32];
     float m = -INFINITY;
     for (int i = 0; i < n; ++i)
-        m = fmaxf(m, load_logit<KIND>(row, e0 + i));
+        m = fmaxf(m, load_logit<KIND>(p, row, e0 + i));
     m = value_of(warp_max(key_of(m)));
     m = m == -INFINITY ? 0.f : m;
     const double z = softmax_sum<KIND>(p, row, m);
     for (int i = 0; i < n; i += kQuad) {
         double x[kQuad], l[kQuad];
         for (int j = 0; j < kQuad; ++j)
-            x[j] = l[j] = load_logit<KIND>(row, e0 + min(i + j, n - 1));
+            x[j] = l[j] = load_logit<KIND>(p, row, e0 + min(i + j, n - 1));
         score64(p, x, m, z);
         for (int j = 0; j < kQuad && i + j < n; ++j) {
-            ck[i + j] = key_of(p.bias ? x[j] + p.bias[e0 + i + j] : x[j]);
+            ck[i + j] = key_of(p.bias ? x[j] + bias_of(p, e0 + i + j) : x[j]);
             key[i + j] = p.bias ? ck[i + j] : key_of(l[j]);
         }
     }
@@ -416,11 +440,11 @@ __device__ __forceinline__ uint32_t near_groups(const RouteParams &p, const void
     const Pair32 z = softmax_sum_pair<KIND>(p, row, m);
     K value = 0, a = 0, b = 0;
     auto key = [&](int e) {
-        const float l = load_logit<KIND>(row, e);
+        const float l = load_logit<KIND>(p, row, e);
         if (!p.bias && p.group_top == 1)
             return key_of(Pair32{l, 0.f});
         const Pair32 s = score_pair(p, l, m, z);
-        return key_of(p.bias ? s + Pair32{p.bias[e], 0.f} : s);
+        return key_of(p.bias ? s + Pair32{bias_of(p, e), 0.f} : s);
     };
     auto value_of_run = [&](K first, K second) {
         return p.group_top == 2 ? key_of(pair_of(first) + pair_of(second)) : first;
@@ -483,11 +507,11 @@ __device__ __forceinline__ int refine(const RouteParams &p, const void *row, int
     using K = unsigned long long;
     const int lane = threadIdx.x & 31;
     const bool in = lane < count;
-    const float l = in ? load_logit<KIND>(row, id) : 0.f;
+    const float l = in ? load_logit<KIND>(p, row, id) : 0.f;
     Pair32 c = {l, 0.f};                    // without a bias the logits rank
     if (p.bias) {
         const Pair32 z = softmax_sum_pair<KIND>(p, row, m);
-        c = score_pair(p, l, m, z) + Pair32{in ? p.bias[id] : 0.f, 0.f};
+        c = score_pair(p, l, m, z) + Pair32{in ? bias_of(p, id) : 0.f, 0.f};
     }
     K sorted;
     const int ranked = by_rank<K>(in ? key_of(c) : 0ull, id, count, &sorted);
@@ -498,7 +522,7 @@ __device__ __forceinline__ int refine(const RouteParams &p, const void *row, int
         const Pair32 x = pair_of(sorted), y = pair_of(next);
         near = !((x.h - y.h) + (x.l - y.l) > 2.f * kPairError * (1.f + fabsf(x.h)));
         // equal logits under equal biases are equal scores, in order of their index
-        near = near && !(load_logit<KIND>(row, ranked) == load_logit<KIND>(row, next_id) && p.bias[ranked] == p.bias[next_id]);
+        near = near && !(load_logit<KIND>(p, row, ranked) == load_logit<KIND>(p, row, next_id) && bias_of(p, ranked) == bias_of(p, next_id));
     }
     *sure = !__any_sync(kAll, near);
     return ranked;
@@ -762,7 +786,7 @@ template <int KIND, int PER> __global__ void __launch_bounds__(kThreads, PER <= 
     grid_launch_dependents();
     if (p.bias) {
         for (int e = threadIdx.x; e < 32 * p.per; e += kThreads)
-            r.bias[e] = e < p.E ? p.bias[e] : 0.f;
+            r.bias[e] = e < p.E ? bias_of(p, e) : 0.f;
         __syncthreads();
     }
     // the CTA's tokens, and this warp's of them
@@ -799,7 +823,7 @@ template <int KIND, int PER> __global__ void __launch_bounds__(kThreads, PER <= 
             } else {
                 load_lane<KIND, PER>(p, row, e0, l);
             }
-            if (p.valid && !p.valid[cta_first + i0 + i])
+            if (!is_valid(p, cta_first + i0 + i))
                 continue;
             Keys<PER> t;
             make_keys<KIND, PER>(p, row, l, bias, r.run_keys, t);
@@ -814,14 +838,14 @@ template <int KIND, int PER> __global__ void __launch_bounds__(kThreads, PER <= 
         }
         __syncwarp();
         const int token = i0 + in_batch;
-        const bool in = in_batch < here, valid = in && !(p.valid && !p.valid[cta_first + token]);
+        const bool in = in_batch < here, valid = in && is_valid(p, cta_first + token);
         const char *const row = rows + token * pitch;
         int id = p.E;
         float x = 0.f;
         if (valid) {
             const uint2 got = r.won[in_batch * (p.k + 1) + choice];
             id = static_cast<int>(got.y);
-            x = load_logit<KIND>(row, id);
+            x = load_logit<KIND>(p, row, id);
             if (checked) {
                 const uint2 below = r.won[in_batch * (p.k + 1) + choice + 1];
                 const float4 of = r.row[in_batch];
@@ -830,7 +854,7 @@ template <int KIND, int PER> __global__ void __launch_bounds__(kThreads, PER <= 
                 if (near && p.bias) {
                     // the fp32 scores anew, which the keys hold cut off: each off by the bound, and by half
                     // a unit for the sum with the bias
-                    const float y = load_logit<KIND>(row, other);
+                    const float y = load_logit<KIND>(p, row, other);
                     const float hi = score32(p, x, of.x, of.y) + r.bias[id], lo = score32(p, y, of.x, of.y) + r.bias[other];
                     near = !(hi - lo > 2.f * of.z + 0x1p-23f * (fabsf(hi) + fabsf(lo)));
                     // equal logits under equal biases are equal scores, in order of their index
@@ -840,7 +864,7 @@ template <int KIND, int PER> __global__ void __launch_bounds__(kThreads, PER <= 
                     near = near || (choice + 1 == p.k && Near<PER>(true, of.z)(got.x, __float_as_uint(of.w)));
                 } else if (near) {
                     near = got.x == below.x;            // (the kept bits)
-                    near = near && !(x == load_logit<KIND>(row, other) && id < other && choice + 1 < p.k);
+                    near = near && !(x == load_logit<KIND>(p, row, other) && id < other && choice + 1 < p.k);
                 }
                 near_tokens = near ? 1u << in_batch : 0u;
             }
@@ -866,7 +890,7 @@ template <int KIND, int PER> __global__ void __launch_bounds__(kThreads, PER <= 
             const int again = __shfl_sync(kAll, chosen, choice);
             if (in_batch == i && valid) {
                 id = again;
-                x = load_logit<KIND>(row, id);
+                x = load_logit<KIND>(p, row, id);
             }
         }
         if (hard_tokens) {
@@ -878,11 +902,11 @@ template <int KIND, int PER> __global__ void __launch_bounds__(kThreads, PER <= 
         const float w = weigh(p, x, in_batch * p.k, about.x, about.y);
         const bool writes = in && lane < batch * p.k;
         const long long pair = (cta_first + i0) * p.k + lane;
-        if (writes) {
+        if (writes && is_number(p.out, pair, SITE_BOUNDS_C)) {
             p.ids[pair] = valid ? id : -1;
             p.weights[pair] = valid ? w : 0.f;
         }
-        if (writes)
+        if (writes && is_kept(p, i0 * p.k + lane))
             s.pairs[i0 * p.k + lane] = id;
         __syncwarp();
     }
@@ -896,15 +920,15 @@ template <int KIND, int PER> __global__ void __launch_bounds__(kThreads, PER <= 
             const int id = choose_exact<KIND>(p, row);
             float m = -INFINITY, z = 0.f;
             for (int e = lane; e < p.E; e += 32)
-                m = fmaxf(m, load_logit<KIND>(row, e));
+                m = fmaxf(m, load_logit<KIND>(p, row, e));
             m = value_of(warp_max(key_of(m)));
             m = m == -INFINITY ? 0.f : m;
             for (int e = lane; e < p.E; e += 32)
-                z += expf(load_logit<KIND>(row, e) - m);
+                z += expf(load_logit<KIND>(p, row, e) - m);
             z = warp_sum(z);
-            const float w = weigh(p, lane < p.k ? load_logit<KIND>(row, id) : 0.f, 0, m, z);
-            if (lane < p.k) {
-                const long long pair = (cta_first + i) * p.k + lane;
+            const float w = weigh(p, lane < p.k ? load_logit<KIND>(p, row, id) : 0.f, 0, m, z);
+            const long long pair = (cta_first + i) * p.k + lane;
+            if (lane < p.k && is_number(p.out, pair, SITE_BOUNDS_C) && is_kept(p, i * p.k + lane)) {
                 p.ids[pair] = id;
                 p.weights[pair] = w;
                 s.pairs[i * p.k + lane] = id;
@@ -951,7 +975,7 @@ __global__ void __launch_bounds__(kThreads) k_group(const GroupParams p)
     int *const h = s.hist + warp * bins;
     for (int i = lo; i < hi; i += 32) {
         const bool in = i + lane < hi;
-        const int id = in ? p.ids[cta_first + i + lane] : 0;
+        const int id = in && is_number(p.out, cta_first + i + lane, SITE_BOUNDS_A) ? p.ids[cta_first + i + lane] : 0;
         const int bin = !in ? bins : static_cast<uint32_t>(id) < static_cast<uint32_t>(groups) ? id : groups;
         const uint32_t same = __match_any_sync(kAll, bin);
         const uint32_t before = same & ((1u << lane) - 1u);
@@ -990,7 +1014,7 @@ __global__ void __launch_bounds__(kPlaceThreads) k_place(const PlaceParams p)
     const long long first = piece(p.units, p.first_ctas, cluster * kCluster) * p.per_unit + slice * kPlaceThreads + threadIdx.x;
     const long long last = min(p.out.n, piece(p.units, p.first_ctas, (cluster + 1) * kCluster) * p.per_unit);
     int id = 0, rank = 0;
-    if (first < last)
+    if (first < last && is_number(p.out, first, SITE_BOUNDS_A))
         id = p.ids[first], rank = p.out.rank[first];
     // Bins side by side in a warp, the clusters dealt to slices of the block.
     const int width = (bins + 31) / 32 * 32, slices = max(1, kPlaceThreads / width);
@@ -999,7 +1023,8 @@ __global__ void __launch_bounds__(kPlaceThreads) k_place(const PlaceParams p)
         int all = 0, early = 0;
 #pragma unroll 8
         for (int c = mine; c < p.clusters; c += slices) {
-            const int v = p.out.hist[static_cast<long long>(c) * bins + b];
+            const long long at = static_cast<long long>(c) * bins + b;
+            const int v = is_count(p.out, at) ? p.out.hist[at] : 0;
             all += v;
             early += c < cluster ? v : 0;
         }
@@ -1023,17 +1048,19 @@ __global__ void __launch_bounds__(kPlaceThreads) k_place(const PlaceParams p)
 #pragma unroll
     for (int i = 0; i < 2; ++i)
         if (i < q && b0 + i < bins) {
-            if (blockIdx.x == 0)
+            if (blockIdx.x == 0 && is_offset(p.out, b0 + i))
                 p.out.offsets[b0 + i] = run;
             before[b0 + i] += run;
             run += t[i];
         }
     __syncthreads();
     for (long long i = first; i < last; i += p.ctas * kPlaceThreads) {
-        if (i > first)
+        if (i > first && is_number(p.out, i, SITE_BOUNDS_A))
             id = p.ids[i], rank = p.out.rank[i];
         const int bin = static_cast<uint32_t>(id) < static_cast<uint32_t>(groups) ? id : groups;
         const int place = rank + before[bin];
+        if (!is_number(p.out, i, SITE_BOUNDS_C) || !is_number(p.out, place, SITE_BOUNDS_C))
+            continue;
         p.out.order[place] = static_cast<int>(i);
         if (p.out.rows)
             p.out.rows[i] = bin < groups ? place : -1;
@@ -1175,8 +1202,9 @@ w8a8_status take_workspace(GroupOut &out, const Cut &c, void *workspace, size_t 
         return record_error(W8A8_ERR_WORKSPACE, msg);
     }
     out.hist = static_cast<int *>(workspace);
+    out.hist_size = static_cast<long long>(c.clusters) * (out.groups + 1);
     if (!out.rank)
-        out.rank = out.hist + static_cast<size_t>(c.clusters) * (out.groups + 1);
+        out.rank = out.hist + out.hist_size;
     return W8A8_OK;
 }
 
@@ -1267,6 +1295,7 @@ extern "C" w8a8_status w8a8_route_experts(const void *logits_dev, w8a8_in_dtype 
     DeviceView dev;
     if (const int st = device_view(&dev); st != W8A8_OK)
         return static_cast<w8a8_status>(st);
+    p.out.status = dev.status;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = dtype == W8A8_IN_FP32   ? launch_route<W8A8_IN_FP32>(p, c, s)
                     : dtype == W8A8_IN_BF16 ? launch_route<W8A8_IN_BF16>(p, c, s)
@@ -1302,6 +1331,7 @@ extern "C" w8a8_status w8a8_group_rows(const int32_t *ids_dev, int64_t n, int64_
     DeviceView dev;
     if (const int st = device_view(&dev); st != W8A8_OK)
         return static_cast<w8a8_status>(st);
+    p.out.status = dev.status;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     static volatile int flags[kMaxDeviceFlags] = {};
     cudaError_t e = launch(k_group, p, c.ctas, c.cluster, grp::kThreads,
