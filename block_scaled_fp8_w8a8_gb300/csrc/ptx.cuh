@@ -236,10 +236,9 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
-// 2-D tiled store of a dense row-major shared-memory box to (x, y); elements
-// outside the tensor are not written.  Tracked by the bulk async-group.
 // Four rows at any places: the pieces of rows y0 .. y3 that begin at x, one after the other
-// (the map's box is one row high); a row out of range is read as zeros.
+// (the map's box is one row high); a row out of range is read as zeros.  Completion as transaction
+// bytes on `bar`.
 __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map, uint32_t bar,
                                             int32_t x, int32_t y0, int32_t y1, int32_t y2, int32_t y3)
 {
@@ -259,6 +258,8 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
                  : "memory");
 }
 
+// Tiled stores of a dense row-major shared-memory box to (x, y), in 3-D (x, y, z); elements
+// outside the tensor are not written.  Tracked by the bulk async-group.
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, uint32_t src, int32_t x,
                                              int32_t y, int32_t z)
 {
