@@ -138,8 +138,12 @@ __constant__ double kInverseFactorial[13] = {1.,           1.,            1. / 2
                                              1. / 120.,    1. / 720.,     1. / 5040.,    1. / 40320.,   1. / 362880.,
                                              1. / 3628800., 1. / 39916800., 1. / 479001600.};
 
+// ln 2 as its first 40 bits, whose products with a quotient of up to 11 bits are exact, and the
+// number nearest to the rest, which leaves 2^-102.
+constexpr double kLn2High = 0x1.62e42fefa2p-1, kLn2Low = 0x1.9ef35793c7673p-41;
+
 // exp of four numbers in fp64, to a few units of 2^-53, zero below -708: reduced by
-// multiples of ln 2 in two parts (W. J. Cody and W. Waite, "Software Manual for the
+// multiples of ln 2 in two parts (after W. J. Cody and W. Waite, "Software Manual for the
 // Elementary Functions", 1980), then the power series up to f^13 / 13!, whose next term is
 // below 2^-57.  Short and four at a time, because what decides a near tie once in
 // thousands of tokens is never in the instruction cache, and fp64's latency is long: with
@@ -154,7 +158,7 @@ __device__ __forceinline__ void exp64(double (&x)[kQuad])
     for (int i = 0; i < kQuad; ++i) {
         const double in = fmin(fmax(x[i], -708.), 709.);                // (a NaN is put back below)
         const double t = fma(in, 1.4426950408889634, kMagic), q = t - kMagic;
-        f[i] = fma(q, -1.90821492927058770002e-10, fma(q, -6.93147180369123816490e-01, in));
+        f[i] = fma(q, -kLn2Low, fma(q, -kLn2High, in));
         n[i] = __double2loint(t);
         s[i] = 1. / 6227020800.;
     }
