@@ -458,14 +458,21 @@ template <bool BF16, int OUT> cudaError_t launch_adapter(const AdapterParams &p,
 
 // Whether a problem's sizes are for the tiles of 128 rows (adapter_tile.cu), which take two
 // launches and some 10 to 20 us for them, then stream: where there is much to read, and many rows
-// to an adapter.  The clusters of 16 rows take a time that grows with T (K + N + 640), the tiles
-// one that hardly depends on r.  Clusters / tiles in us, T of L adapters, KxN, bf16 into
+// to an adapter.  The clusters of 16 rows take a time that grows with T (K + N + 640) and with r,
+// the tiles one that hardly depends on r.  Clusters / tiles in us, T of L adapters, KxN, bf16 into
 // bf16:
-//   r 16   1600 of 24 1024x1024 9.4 / 13.6, 2048 of 4 4096x4096 25.2 / 20.5, 4096 of 8 1024x1024
+//   r 16   1600 of 24 1024x1024 9.4 / 13.6, 2048 of 4 4096x4096 21.1 / 16.5, 4096 of 8 1024x1024
 //          13.5 / 12.4, 16384 256x256 23 / 11.6; 1536 256x4096 into fp32 20.7 / 19.3
-//   r 64   4096 of 8 2048x2048 34 / 39, 8192 of 8 1024x1024 38 / 29, 16384 512x512 44 / 24; 2048
-//          of 16 4096x4096 35 / 43; r 32 1024x8192 30.7 / 27.0, into fp32 40.6 / 41.9
+//   r 32   2200 of 8 4096x4096 24.0 / 35.3, 4200 of 8 2048x2048 22.9 / 36.6, into fp32 29.0 / 46.2
+//   r 64   4096 of 8 2048x2048 31.3 / 36.7, 8192 of 8 1024x1024 35.5 / 27.2, 16384 512x512 42.7 / 22.2;
+//          2048 of 16 4096x4096 33.2 / 38.8, into fp32 40.6 / 51.5
 //   r 128  3200 of 8 4096x4096 103 / 68, 16384 512x512 68 / 36; 4096 of 16 1024x8192 into fp32 138 / 148
+// One line for every output type and every shape of the widths: over 760 problems of the range that it
+// decides (1 to 64 adapters, K and N 64 to 8192, r 8 to 128, runs of 1 to 2000 rows; 304 of them into fp32,
+// 456 into bf16) it takes 4.8 % longer than the faster form of each on average, more than 10 % longer
+// for 121, 1.9 times at worst.  It is too high for many rows of narrow layers (r 64: 12000 of 4 512x512
+// 32.3 / 21.2, 7400 of 8 1024x1024 35.3 / 26.7) and for a narrow K beside a wide N (r 32, 2048 of 16
+// 1024x8192 27.5 / 24.2, into fp32 39.6 / 38.8), too low for rank 8 and 16 (4500 of 4 512x512 9.1 / 13.6).
 bool many_rows(const AdapterParams &p) { return p.L > 0 && p.T >= 1536 && p.T / 64 >= p.L && p.r >= 8 && p.K >= 64; }
 bool tiled(const AdapterParams &p)
 {
