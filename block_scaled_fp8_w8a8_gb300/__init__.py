@@ -533,6 +533,18 @@ def _workspace(size, device):
     return t, t.data_ptr()
 
 
+def _number(v, name, low=1, high=2 ** 31 - 1):
+    """v as a whole number, refused out of range: the C calls take it in 32 bits."""
+    import operator
+    try:
+        v = operator.index(v)
+    except TypeError:
+        v = None
+    if v is None or not low <= v <= high:
+        raise W8A8Error(W8A8_ERR_INVALID_ARG, f"{name}: want a whole number from {low} to {high}")
+    return v
+
+
 _SCORES = {"softmax": W8A8_SCORE_SOFTMAX, "sigmoid": W8A8_SCORE_SIGMOID}
 
 
@@ -569,6 +581,8 @@ def route_experts(logits, top_k, scoring="softmax", bias=None, groups=1, top_gro
     kind = _in_codes[logits.dtype]
     if not isinstance(top_k, int) or top_k < 1 or top_k > W8A8_ROUTE_MAX_K:
         raise W8A8Error(W8A8_ERR_INVALID_ARG, f"top_k of {top_k}: want 1 to {W8A8_ROUTE_MAX_K}")
+    groups, top_groups = _number(groups, "groups"), _number(top_groups, "top_groups")
+    group_top = _number(group_top, "group_top")
     if bias is not None:
         _given(bias, (E,), types.f32, "bias")
     if valid is not None:
@@ -607,8 +621,11 @@ def group_rows(ids, groups, out=None, stream=None):
             check(st)
     n = ids.numel()
     _given(ids, ids.shape, types.i32, "ids")
+    groups = _number(groups, "groups")
+    if groups > W8A8_GROUPS_MAX:        # (before offsets of that size are made)
+        raise W8A8Error(W8A8_ERR_UNSUPPORTED, f"{groups} groups: at most {W8A8_GROUPS_MAX}")
     with _on_stream(stream):
-        outs = _outputs(out, (("order", (n,), types.i32), ("offsets", (max(groups, 0) + 1,), types.i32)), ids.device)
+        outs = _outputs(out, (("order", (n,), types.i32), ("offsets", (groups + 1,), types.i32)), ids.device)
         _here(ids, *outs)
         size = lib.w8a8_group_workspace_size(n, groups)
         keep, scratch = _workspace(size, ids.device)
@@ -683,6 +700,7 @@ def adapter_matmul(x, A, B, order, offsets, base, scales=None, out=None, stream=
             check(st)
         elif st is not None:
             return st
+    variant = _number(variant, "variant", 0) if variant else W8A8_VARIANT_AUTO
     if x.dim() != 2 or A.dim() != 3 or B.dim() != 3:
         raise W8A8Error(W8A8_ERR_INVALID_ARG, "x must be [rows, K], A [adapters, r, K] and B [adapters, N, r]")
     T, K = x.shape

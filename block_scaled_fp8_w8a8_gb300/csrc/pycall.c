@@ -466,6 +466,9 @@ static int code_of(PyObject *codes, PyObject *dtype)
     return o ? (int)PyLong_AsLong(o) : -1;
 }
 
+/* Whether a positive number stays what it is in the C call's 32 bits. */
+static int fits32(int64_t v) { return v >= 1 && v <= INT32_MAX; }
+
 /* logits, top_k, scoring, bias, groups, top_groups, group_top, renormalize, scale, valid,
  * outputs, the input types' codes by dtype, dtypes, stream.  Without outputs (None), here and
  * below, the result is a tuple of new ones (one: the tensor), or a status other than 0. */
@@ -498,9 +501,10 @@ static PyObject *py_route_tensors(PyObject *self, PyObject *const *args, Py_ssiz
     }
     const int kind = code_of(args[11], x.dtype), renormalize = PyObject_IsTrue(args[7]);
     const double scale = PyFloat_AsDouble(args[8]);
-    const int scoring = I32(2), groups = I32(4), top_groups = I32(5), group_top = I32(6);
+    const int64_t groups = I64(4), top_groups = I64(5), group_top = I64(6);
+    const int scoring = I32(2);
     const size_t size = f_route_size(T, E, (int)k);
-    if (kind < 0 || renormalize < 0 || !is_current(gpu) || ((size || make) && args[13] != Py_None) ||
+    if (!fits32(groups) || !fits32(top_groups) || !fits32(group_top) || kind < 0 || renormalize < 0 || !is_current(gpu) || ((size || make) && args[13] != Py_None) ||
         PyErr_Occurred())
         goto other;
     if (make) {
@@ -520,8 +524,8 @@ static PyObject *py_route_tensors(PyObject *self, PyObject *const *args, Py_ssiz
         goto other;
     int st;
     Py_BEGIN_ALLOW_THREADS
-    st = f_route(x.ptr, kind, 0, bias.ptr, valid.ptr, T, E, (int)k, scoring, groups, top_groups, group_top,
-                 renormalize, (float)scale, o[0].ptr, o[1].ptr, o[2].ptr, o[3].ptr, o[4].ptr, scratch, size, s);
+    st = f_route(x.ptr, kind, 0, bias.ptr, valid.ptr, T, E, (int)k, scoring, (int)groups, (int)top_groups,
+                 (int)group_top, renormalize, (float)scale, o[0].ptr, o[1].ptr, o[2].ptr, o[3].ptr, o[4].ptr, scratch, size, s);
     Py_END_ALLOW_THREADS
     Py_XDECREF(keep);
     return result_of(made, st);

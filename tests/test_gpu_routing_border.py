@@ -93,3 +93,14 @@ def test_many_rows_of_spread_logits_and_biases_of_one_level(E, groups, top_group
             worst = torch.where(rows_[:, None], best - mine, 0.0)
             assert (worst <= unit).all(), (k, spread, (worst > unit).any(1).sum().item(), worst.max().item())
     ok()
+
+
+@pytest.mark.parametrize("kw", [dict(groups=2 ** 32 + 1), dict(groups=2, top_groups=2 ** 32 + 2), dict(groups=2, group_top=2 ** 32 + 1)])
+def test_numbers_of_groups_that_32_bits_do_not_hold_are_refused(kw):
+    x = torch.randn(4, 8, device="cuda")
+    out = w8.route_experts(x, 2)
+    for given in (None, out):
+        with pytest.raises(w8.W8A8Error) as e:
+            w8.route_experts(x, 2, out=given, **kw)
+        assert e.value.status == w8.W8A8_ERR_INVALID_ARG
+    ok()

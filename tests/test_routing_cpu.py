@@ -231,3 +231,30 @@ def test_adapters_without_columns_of_x_still_read_b(kw):
     """B [L, N, r] does not depend on K: it is read where there are adapters of some rank."""
     assert adapters(**kw) == ARG
     assert "null pointer" in w8.w8a8_last_error()
+
+
+# ---------------------------------------------------------------- numbers that the C calls take in 32 bits
+
+
+@pytest.mark.parametrize("kw", [dict(groups=2 ** 32 + 1), dict(groups=2 ** 31), dict(groups=-2 ** 32), dict(groups=0), dict(groups=1.0),
+                                dict(groups=4, top_groups=2 ** 32 + 2), dict(groups=4, top_groups=2 ** 40), dict(groups=2, group_top=2 ** 32 + 1),
+                                dict(groups=2, group_top=0), dict(groups=2, group_top=None)])
+def test_routing_refuses_numbers_of_groups_out_of_range(kw, reached):
+    """They would be cut to 32 bits on their way to the library: 2^32 + 1 groups to one."""
+    with pytest.raises(w8.W8A8Error, match=list(kw)[-1]) as e:
+        w8.route_experts(z(4, 8), 2, **kw)
+    assert e.value.status == ARG and not [h for h in reached if len(h) > 3]
+
+
+@pytest.mark.parametrize("variant", [2 ** 32, 2 ** 32 + w8.W8A8_VARIANT_SMALLM, -1, 2 ** 31, 1.5, "tiled"])
+def test_adapters_refuse_a_variant_out_of_range(variant, reached):
+    with pytest.raises(w8.W8A8Error, match="variant") as e:
+        w8.adapter_matmul(**dict(GOOD["adapter_matmul"][0], variant=variant))
+    assert e.value.status == ARG and not [h for h in reached if len(h) > 3]
+
+
+@pytest.mark.parametrize("groups", [2 ** 32 + 3, 2 ** 63, 0, -1, 1025, 3.0])
+def test_grouping_refuses_numbers_of_groups_out_of_range(groups, reached):
+    with pytest.raises(w8.W8A8Error, match="groups"):
+        w8.group_rows(z(6, dtype=I32), groups)
+    assert not [h for h in reached if len(h) > 3]
