@@ -14,10 +14,12 @@
 // such that a lane ends with eight neighbouring ones.  B's and base's share are fetched into
 // L2 while x A^T is computed.
 //
-// h is kept to fp32: an MMA takes 16-bit operands, so h is split into a sum of two or
+// h is made in fp32: an MMA takes 16-bit operands, so h is split into a sum of two or
 // three of them, each the rounding of what the ones before leave (a rounding of p bits
 // leaves at most 2^-p, and what it leaves begins one bit lower).  bf16: two leave an error of
-// 2^-17 (16-bit output, whose rounding is 2^-8), three one of 2^-26 (fp32 output).  fp16:
+// 2^-17 (16-bit output, whose rounding is 2^-8: 0.2 % of 16384 x 4096 outputs fall to the other side of
+// one than with all of h, and the error against 64 bits is the same), three one of 2^-26 (fp32
+// output; three for both would cost the tiles their second CTA on an SM).  fp16:
 // two leave 2^-23, a step of fp32; h is first scaled by a power of two per row so that its
 // largest element is near 2^14, because fp16's range is narrow.
 //
